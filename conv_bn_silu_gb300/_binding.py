@@ -28,6 +28,7 @@ CBS_VARIANT_STEM = 4
 CBS_VARIANT_TC_TF32X3 = 5
 CBS_ACT_SILU, CBS_ACT_IDENTITY = 0, 1
 CBS_LAUNCH_PDL = 1
+CBS_ATTN_ROWS = 0
 
 EXPORTED = (
     "cbs_plan", "cbs_fold_bn", "cbs_pack_input", "cbs_conv_bn_silu_f32", "cbs_conv_bn_silu_i8",
@@ -35,7 +36,8 @@ EXPORTED = (
     "cbs_last_error", "cbs_abi_version", "cbs_conv_bn_silu_f32_noalloc", "cbs_conv_bn_act",
     "cbs_conv_bn_act_cat", "cbs_set_launch_options", "cbs_launch_options", "cbs_maxpool2d",
     "cbs_conv_bn_silu_i8_cat", "cbs_selftest_wait_timeout", "cbs_sppf_pool", "cbs_dequantize_i8",
-    "cbs_quantize_i8",
+    "cbs_quantize_i8", "cbs_cache_write", "cbs_cache_read", "cbs_attn_plan", "cbs_paged_attention", "cbs_rmsnorm",
+    "cbs_dequantize_rows", "cbs_linear_w4", "cbs_quantize_w4",
 )
 
 
@@ -57,6 +59,28 @@ class cbs_plan_t(ctypes.Structure):
         [(n, ctypes.c_size_t) for n in (
             "x_bytes", "y_bytes", "w_packed_bytes", "bias_bytes", "workspace_bytes", "x_b_bytes")] + \
         [("desc", cbs_layer_desc)]
+
+
+class cbs_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+        [(n, ctypes.c_int) for n in ("prec", "num_pages", "page_size", "kv_heads", "head_dim")]
+
+
+class cbs_sequences(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("new_start", "seq_lens", "page_table")] + \
+        [(n, ctypes.c_int) for n in ("batch", "max_pages", "total")]
+
+
+class cbs_attn_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "max_new", "max_len", "heads", "kv_heads", "head_dim", "cache_prec", "causal", "window", "num_sms",
+        "force_kernel", "force_split")]
+
+
+class cbs_attn_plan_t(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("abi_version", ctypes.c_uint32)] + \
+        [(n, ctypes.c_int) for n in ("kernel", "row_tile", "row_tiles", "split", "grid_ctas", "threads")] + \
+        [("workspace_bytes", ctypes.c_size_t), ("desc", cbs_attn_desc)]
 
 
 class CbsError(RuntimeError):
@@ -89,6 +113,15 @@ def lib():
         L.cbs_dequantize_i8.argtypes = [P, P, Z, F, I, I, P]
         L.cbs_quantize_i8.argtypes = [P, I, P, Z, F, I, P]
         L.cbs_conv_bn_silu_f32_noalloc.argtypes = [ctypes.POINTER(cbs_plan_t), P, P, P, P, P]
+        LL, CP, SP = ctypes.c_longlong, ctypes.POINTER(cbs_cache), ctypes.POINTER(cbs_sequences)
+        L.cbs_cache_write.argtypes = [CP, SP, P, LL, P, LL, I, P]
+        L.cbs_cache_read.argtypes = [CP, SP, I, P, P, I, P]
+        L.cbs_attn_plan.argtypes = [ctypes.POINTER(cbs_attn_desc), ctypes.POINTER(cbs_attn_plan_t)]
+        L.cbs_paged_attention.argtypes = [ctypes.POINTER(cbs_attn_plan_t), CP, SP, P, LL, F, P, LL, P, Z, P]
+        L.cbs_rmsnorm.argtypes = [P, P, P, P, P, P, I, I, F, I, I, P]
+        L.cbs_dequantize_rows.argtypes = [P, P, P, I, I, I, P]
+        L.cbs_linear_w4.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, P]
+        L.cbs_quantize_w4.argtypes = [P, I, I, I, P, P, P]
         L.cbs_workspace_init.argtypes = [P, Z, P]
         L.cbs_read_device_status.argtypes = [ctypes.POINTER(I), I, P]
         L.cbs_selftest_wait_timeout.argtypes = [I, P]
@@ -236,3 +269,40 @@ def cbs_selftest_wait_timeout(limit_us: int, stream):
     """Enqueue the diagnostic kernel whose bounded wait runs out after
     limit_us microseconds and records a timeout in the status word."""
     _check(lib().cbs_selftest_wait_timeout(int(limit_us), stream), "cbs_selftest_wait_timeout")
+
+
+def cbs_cache_write(cache, seqs, k, k_stride, v, v_stride, in_prec, stream):
+    _check(lib().cbs_cache_write(cache, seqs, _p(k), k_stride, _p(v), v_stride, in_prec, stream), "cbs_cache_write")
+
+
+def cbs_cache_read(cache, seqs, max_len, k_out, v_out, out_prec, stream):
+    _check(lib().cbs_cache_read(cache, seqs, max_len, _p(k_out), _p(v_out), out_prec, stream), "cbs_cache_read")
+
+
+def cbs_attn_plan(desc: cbs_attn_desc) -> cbs_attn_plan_t:
+    plan = cbs_attn_plan_t()
+    _check(lib().cbs_attn_plan(ctypes.byref(desc), ctypes.byref(plan)), "cbs_attn_plan")
+    return plan
+
+
+def cbs_paged_attention(plan, cache, seqs, q, q_stride, scale, out, out_stride, workspace, workspace_bytes, stream):
+    _check(lib().cbs_paged_attention(plan, cache, seqs, _p(q), q_stride, scale, _p(out), out_stride, _p(workspace),
+                                     workspace_bytes, stream), "cbs_paged_attention")
+
+
+def cbs_rmsnorm(x, residual, weight, h_out, y, scale, rows, cols, eps, in_prec, out_prec, stream):
+    _check(lib().cbs_rmsnorm(_p(x), _p(residual), _p(weight), _p(h_out), _p(y), _p(scale), rows, cols, eps, in_prec,
+                             out_prec, stream), "cbs_rmsnorm")
+
+
+def cbs_dequantize_rows(q, scale, out, rows, cols, out_prec, stream):
+    _check(lib().cbs_dequantize_rows(_p(q), _p(scale), _p(out), rows, cols, out_prec, stream), "cbs_dequantize_rows")
+
+
+def cbs_linear_w4(x, x_prec, x_scale, w, scales, zeros, bias, y, out_prec, rows, n, k, group, activation, stream):
+    _check(lib().cbs_linear_w4(_p(x), x_prec, _p(x_scale), _p(w), _p(scales), _p(zeros), _p(bias), _p(y), out_prec,
+                               rows, n, k, group, activation, stream), "cbs_linear_w4")
+
+
+def cbs_quantize_w4(w, n, k, group, packed, scales, stream):
+    _check(lib().cbs_quantize_w4(_p(w), n, k, group, _p(packed), _p(scales), stream), "cbs_quantize_w4")

@@ -689,7 +689,7 @@ __global__ void wait_selftest_kernel(unsigned long long limit_ns, unsigned int *
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    if (threadIdx.x == 0 && !ptx::mbar_wait_bounded(b, 0, limit_ns)) atomicOr(status, 1u);
+    if (threadIdx.x == 0 && !ptx::mbar_wait_bounded(b, 0, limit_ns)) atomicOr(status, kStatusTimeout);
 }
 
 }  // namespace
@@ -901,7 +901,7 @@ cbs_status read_and_reset_status(int *status_out, int reset, cudaStream_t s) {
         st = cuda_check(cudaMemcpyToSymbol(g_cbs_status_word, &zero, sizeof(zero)), "reset status word");
         if (st != CBS_OK) return st;
     }
-    *status_out = v ? (int)CBS_ERR_TIMEOUT : (int)CBS_OK;
+    *status_out = (int)((v & kStatusTimeout) ? CBS_ERR_TIMEOUT : v ? CBS_ERR_INVALID_ARG : CBS_OK);
     return CBS_OK;
 }
 

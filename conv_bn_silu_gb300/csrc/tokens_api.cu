@@ -1,0 +1,289 @@
+// tokens_api.cu -- the token operators' C entry points (include/cbs.h):
+// argument checks, the attention's planning and dispatch to the kernels.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "tokens.cuh"
+
+namespace cbs {
+namespace {
+
+cbs_status need(const void *p, const char *what) {
+    if (!p) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", what);
+    if (!aligned16(p)) return fail(CBS_ERR_MISALIGNED, "%s is not 16-byte aligned", what);
+    return CBS_OK;
+}
+
+cbs_status may(const void *p, const char *what) { return p ? need(p, what) : CBS_OK; }
+
+cbs_status float_type(int prec, const char *what) {
+    if (prec != CBS_FP32 && prec != CBS_BF16) return fail(CBS_ERR_INVALID_ARG, "%s must be FP32 or BF16", what);
+    return CBS_OK;
+}
+
+cbs_status head_shape(int kv_heads, int head_dim) {
+    if (kv_heads < 1 || head_dim < 1) return fail(CBS_ERR_INVALID_ARG, "bad heads (%d of %d)", kv_heads, head_dim);
+    if (head_dim != 64 && head_dim != 128) return fail(CBS_ERR_UNSUPPORTED, "head_dim %d: 64 or 128", head_dim);
+    return CBS_OK;
+}
+
+// Checks a cache and a call's sequences and lays them out for the kernels.
+cbs_status cache_args(const cbs_cache *c, const cbs_sequences *s, bool starts, CacheArgs *a) {
+    if (!c || !s) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", c ? "sequences" : "cache");
+    if (c->prec != CBS_BF16 && c->prec != CBS_INT8) return fail(CBS_ERR_INVALID_ARG, "a cache is BF16 or INT8");
+    CBS_TRY(head_shape(c->kv_heads, c->head_dim));
+    if (c->num_pages < 1) return fail(CBS_ERR_INVALID_ARG, "a cache needs a page");
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+        return fail(CBS_ERR_UNSUPPORTED, "page_size %d: 16, 32, 64, 128 or 256", c->page_size);
+    if ((long long)c->num_pages * c->kv_heads > INT_MAX / c->page_size)
+        return fail(CBS_ERR_UNSUPPORTED, "cache of over 2^31 rows");
+    CBS_TRY(need(c->k, "k"));
+    CBS_TRY(need(c->v, "v"));
+    if (c->prec == CBS_INT8) {
+        CBS_TRY(need(c->k_scale, "k_scale"));
+        CBS_TRY(need(c->v_scale, "v_scale"));
+    } else if (c->k_scale || c->v_scale) {
+        return fail(CBS_ERR_INVALID_ARG, "scales given for a BF16 cache");
+    }
+    if (s->batch < 0 || s->max_pages < 0 || s->total < 0 || s->max_pages > INT_MAX / c->page_size)
+        return fail(CBS_ERR_INVALID_ARG, "bad sequences (batch=%d max_pages=%d total=%d)", s->batch, s->max_pages, s->total);
+    if (s->batch > 0) {
+        if (starts && !s->new_start) return fail(CBS_ERR_INVALID_ARG, "new_start is NULL");
+        if (!s->seq_lens) return fail(CBS_ERR_INVALID_ARG, "seq_lens is NULL");
+        if (s->max_pages > 0 && !s->page_table) return fail(CBS_ERR_INVALID_ARG, "page_table is NULL");
+        for (const void *p : {(const void *)s->new_start, (const void *)s->seq_lens, (const void *)s->page_table})
+            if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(CBS_ERR_MISALIGNED, "an int32 array is not 4-byte aligned");
+    }
+    a->k = c->k; a->v = c->v; a->k_scale = c->k_scale; a->v_scale = c->v_scale;
+    a->int8 = c->prec == CBS_INT8;
+    a->num_pages = c->num_pages;
+    a->page_shift = 0;
+    while ((1 << a->page_shift) < c->page_size) ++a->page_shift;
+    a->kv_heads = c->kv_heads; a->head_dim = c->head_dim;
+    a->new_start = s->new_start; a->seq_lens = s->seq_lens; a->page_table = s->page_table;
+    a->batch = s->batch; a->max_pages = s->max_pages; a->total = s->total;
+    a->status = nullptr;
+    return CBS_OK;
+}
+
+cbs_status status_word(CacheArgs *a) {
+    a->status = device_status_word();
+    if (!a->status) return fail(CBS_ERR_CUDA, "cannot resolve the device status word");
+    return CBS_OK;
+}
+
+cbs_status token_stride(long long stride, long long least, const char *what) {
+    if (stride < least) return fail(CBS_ERR_INVALID_ARG, "%s %lld < %lld elements of a token", what, stride, least);
+    if (stride % 8) return fail(CBS_ERR_MISALIGNED, "%s %lld is not a multiple of 8", what, stride);
+    return CBS_OK;
+}
+
+constexpr int kGridMax = 65535;
+
+size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
+    return ((size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * 4 + 255) / 256 * 256;
+}
+size_t attn_stat_rows(const cbs_attn_plan_t &p) {
+    return (size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * p.split * p.row_tile;
+}
+
+}  // namespace
+}  // namespace cbs
+
+using namespace cbs;
+
+extern "C" {
+
+cbs_status cbs_cache_write(const cbs_cache *c, const cbs_sequences *s, const void *k, long long k_stride,
+                           const void *v, long long v_stride, int in_prec, void *stream) {
+    CacheArgs a;
+    CBS_TRY(cache_args(c, s, true, &a));
+    CBS_TRY(float_type(in_prec, "keys and values"));
+    CBS_TRY(token_stride(k_stride, (long long)c->kv_heads * c->head_dim, "k_stride"));
+    CBS_TRY(token_stride(v_stride, (long long)c->kv_heads * c->head_dim, "v_stride"));
+    if (s->batch == 0 || s->total == 0) return CBS_OK;
+    CBS_TRY(need(k, "k"));
+    CBS_TRY(need(v, "v"));
+    CBS_TRY(status_word(&a));
+    return cuda_check(launch_cache_write(a, k, k_stride, v, v_stride, in_prec == CBS_BF16, (cudaStream_t)stream),
+                      "cache write launch");
+}
+
+cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_len, void *k_out, void *v_out,
+                          int out_prec, void *stream) {
+    CacheArgs a;
+    CBS_TRY(cache_args(c, s, false, &a));
+    CBS_TRY(float_type(out_prec, "output"));
+    if (max_len < 0) return fail(CBS_ERR_INVALID_ARG, "max_len %d", max_len);
+    if (s->batch == 0 || max_len == 0) return CBS_OK;
+    CBS_TRY(need(k_out, "k_out"));
+    CBS_TRY(need(v_out, "v_out"));
+    CBS_TRY(status_word(&a));
+    return cuda_check(launch_cache_read(a, max_len, k_out, v_out, out_prec == CBS_BF16, (cudaStream_t)stream),
+                      "cache read launch");
+}
+
+cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
+    if (!d || !out) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", d ? "out" : "desc");
+    if (d->batch < 0 || d->max_new < 0 || d->max_len < 0 || d->heads < 1 || d->window < 0 || d->force_split < 0 ||
+        d->num_sms < 0)
+        return fail(CBS_ERR_INVALID_ARG, "bad attention shape (batch=%d max_new=%d max_len=%d heads=%d window=%d)",
+                    d->batch, d->max_new, d->max_len, d->heads, d->window);
+    CBS_TRY(head_shape(d->kv_heads, d->head_dim));
+    if (d->heads % d->kv_heads)
+        return fail(CBS_ERR_INVALID_ARG, "%d heads do not share %d key heads evenly", d->heads, d->kv_heads);
+    if (d->cache_prec != CBS_BF16 && d->cache_prec != CBS_INT8)
+        return fail(CBS_ERR_INVALID_ARG, "a cache is BF16 or INT8");
+    if (d->force_kernel < -1 || d->force_kernel > CBS_ATTN_ROWS)
+        return fail(CBS_ERR_INVALID_ARG, "unknown attention kernel %d", d->force_kernel);
+    cbs_attn_plan_t p;
+    std::memset(&p, 0, sizeof(p));
+    p.size = sizeof(p);
+    p.abi_version = CBS_ABI_VERSION;
+    p.desc = *d;
+    const long long rows = (long long)d->max_new * (d->heads / d->kv_heads);
+    p.kernel = CBS_ATTN_ROWS;
+    p.row_tile = rows <= 8 ? 8 : 16;
+    const long long tiles = (rows + p.row_tile - 1) / p.row_tile;
+    if (tiles * d->kv_heads > kGridMax || d->batch > kGridMax)
+        return fail(CBS_ERR_UNSUPPORTED, "%lld row tiles of %d heads, %d sequences: at most %d", tiles, d->kv_heads,
+                    d->batch, kGridMax);
+    p.row_tiles = (int)std::max(tiles, 1ll);
+    const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
+    const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
+    const int keys = d->window > 0 ? std::min(d->max_len, d->window + d->max_new) : d->max_len;
+    const long long want = ((long long)sms * 4 + base - 1) / base;
+    p.split = d->force_split ? d->force_split
+                             : (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
+    p.threads = 128;
+    const long long ctas = base * p.split;
+    if (ctas > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld CTAs", ctas);
+    p.grid_ctas = (int)ctas;
+    if (p.split > 1) {
+        const size_t rows_all = attn_stat_rows(p);
+        p.workspace_bytes = attn_counter_bytes(p) + (rows_all * 8 + 255) / 256 * 256 + rows_all * d->head_dim * 4;
+    }
+    *out = p;
+    return CBS_OK;
+}
+
+cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, const cbs_sequences *s, const void *q,
+                               long long q_stride, float scale, void *out, long long out_stride, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    if (!p) return fail(CBS_ERR_INVALID_ARG, "plan is NULL");
+    if (p->size != sizeof(cbs_attn_plan_t) || p->abi_version != CBS_ABI_VERSION)
+        return fail(CBS_ERR_PLAN_MISMATCH, "plan of another library version");
+    const cbs_attn_desc &d = p->desc;
+    AttnLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    CBS_TRY(cache_args(c, s, true, &L.c));
+    if (c->prec != d.cache_prec || c->kv_heads != d.kv_heads || c->head_dim != d.head_dim || s->batch != d.batch)
+        return fail(CBS_ERR_PLAN_MISMATCH, "the plan is for another cache or batch");
+    const long long width = (long long)d.heads * d.head_dim;
+    CBS_TRY(token_stride(q_stride, width, "q_stride"));
+    CBS_TRY(token_stride(out_stride, width, "out_stride"));
+    if (!std::isfinite(scale)) return fail(CBS_ERR_INVALID_ARG, "scale is not finite");
+    if (s->batch == 0 || s->total == 0) return CBS_OK;
+    if (d.max_new == 0) return fail(CBS_ERR_INVALID_ARG, "%d new tokens for a plan of none", s->total);
+    CBS_TRY(need(q, "q"));
+    CBS_TRY(need(out, "out"));
+    if (p->workspace_bytes > 0) {
+        if (!workspace || workspace_bytes < p->workspace_bytes)
+            return fail(CBS_ERR_WORKSPACE, "workspace of %zu bytes, %zu required", workspace ? workspace_bytes : (size_t)0,
+                        p->workspace_bytes);
+        CBS_TRY(need(workspace, "workspace"));
+    }
+    CBS_TRY(status_word(&L.c));
+    L.q = q; L.out = out; L.q_stride = q_stride; L.out_stride = out_stride;
+    L.scale_log2 = scale * 1.44269504088896340736f;
+    L.heads = d.heads; L.causal = d.causal != 0; L.window = d.window; L.max_new = d.max_new;
+    L.split = p->split; L.row_tiles = p->row_tiles;
+    if (p->split > 1) {
+        char *w = static_cast<char *>(workspace);
+        L.counters = reinterpret_cast<unsigned int *>(w);
+        L.stats = reinterpret_cast<float2 *>(w + attn_counter_bytes(*p));
+        L.partial = reinterpret_cast<float *>(w + attn_counter_bytes(*p) + (attn_stat_rows(*p) * 8 + 255) / 256 * 256);
+    }
+    return cuda_check(launch_attn_rows(L, p->row_tile, (cudaStream_t)stream), "attention launch");
+}
+
+cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight, void *h_out, void *y, float *scale,
+                       int rows, int cols, float eps, int in_prec, int out_prec, void *stream) {
+    CBS_TRY(float_type(in_prec, "input"));
+    if (out_prec != in_prec && out_prec != CBS_INT8)
+        return fail(CBS_ERR_INVALID_ARG, "output must be of the input's type or INT8");
+    if (rows < 0 || cols < 1) return fail(CBS_ERR_INVALID_ARG, "bad norm shape (%d x %d)", rows, cols);
+    if (cols > kNormMaxCols) return fail(CBS_ERR_UNSUPPORTED, "%d columns: at most %d", cols, kNormMaxCols);
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(CBS_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (h_out && !residual) return fail(CBS_ERR_INVALID_ARG, "h_out without a residual is x itself");
+    if (rows == 0) return CBS_OK;
+    CBS_TRY(need(x, "x"));
+    CBS_TRY(may(residual, "residual"));
+    CBS_TRY(need(weight, "weight"));
+    CBS_TRY(may(h_out, "h_out"));
+    CBS_TRY(need(y, "y"));
+    if (out_prec == CBS_INT8) CBS_TRY(need(scale, "scale"));
+    NormLaunch L;
+    L.x = x; L.residual = residual; L.weight = weight; L.h = h_out; L.y = y; L.scale = scale;
+    L.eps = eps; L.rows = rows; L.cols = cols; L.in_bf16 = in_prec == CBS_BF16; L.out_int8 = out_prec == CBS_INT8;
+    return cuda_check(launch_rmsnorm(L, (cudaStream_t)stream), "norm launch");
+}
+
+cbs_status cbs_dequantize_rows(const int8_t *q, const float *scale, void *out, int rows, int cols, int out_prec,
+                               void *stream) {
+    CBS_TRY(float_type(out_prec, "output"));
+    if (rows < 0 || cols < 1) return fail(CBS_ERR_INVALID_ARG, "bad shape (%d x %d)", rows, cols);
+    if (rows == 0) return CBS_OK;
+    CBS_TRY(need(q, "q"));
+    CBS_TRY(need(scale, "scale"));
+    CBS_TRY(need(out, "out"));
+    return cuda_check(launch_dequantize_rows(q, scale, out, rows, cols, out_prec == CBS_BF16, (cudaStream_t)stream),
+                      "dequantise launch");
+}
+
+static cbs_status w4_shape(int n, int k, int group) {
+    if (n < 1 || k < 1) return fail(CBS_ERR_INVALID_ARG, "bad weight shape (%d x %d)", n, k);
+    if (group != 32 && group != 64 && group != 128) return fail(CBS_ERR_UNSUPPORTED, "group %d: 32, 64 or 128", group);
+    if (k % group) return fail(CBS_ERR_UNSUPPORTED, "k = %d is not a multiple of the group (%d)", k, group);
+    return CBS_OK;
+}
+
+cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const void *w, const void *scales,
+                         const void *zeros, const float *bias, void *y, int out_prec, int rows, int n, int k, int group,
+                         int activation, void *stream) {
+    if (x_prec != CBS_BF16 && x_prec != CBS_INT8) return fail(CBS_ERR_INVALID_ARG, "x must be BF16 or INT8");
+    CBS_TRY(float_type(out_prec, "output"));
+    CBS_TRY(w4_shape(n, k, group));
+    if (activation != CBS_ACT_SILU && activation != CBS_ACT_IDENTITY)
+        return fail(CBS_ERR_INVALID_ARG, "unknown activation %d", activation);
+    if (rows < 0) return fail(CBS_ERR_INVALID_ARG, "%d rows", rows);
+    if (rows > 8 * kGridMax) return fail(CBS_ERR_UNSUPPORTED, "%d rows: at most %d", rows, 8 * kGridMax);
+    if (x_prec == CBS_BF16 && x_scale) return fail(CBS_ERR_INVALID_ARG, "x_scale given for BF16 inputs");
+    if (rows == 0) return CBS_OK;
+    CBS_TRY(need(x, "x"));
+    if (x_prec == CBS_INT8) CBS_TRY(need(x_scale, "x_scale"));
+    CBS_TRY(need(w, "w"));
+    CBS_TRY(need(scales, "scales"));
+    CBS_TRY(may(zeros, "zeros"));
+    CBS_TRY(may(bias, "bias"));
+    CBS_TRY(need(y, "y"));
+    W4Launch L;
+    L.x = x; L.x_scale = x_scale; L.w = static_cast<const uint8_t *>(w); L.scales = scales;
+    L.zeros = static_cast<const uint8_t *>(zeros); L.bias = bias; L.y = y;
+    L.rows = rows; L.n = n; L.k = k; L.group = group; L.x_int8 = x_prec == CBS_INT8; L.out_bf16 = out_prec == CBS_BF16;
+    L.act = activation;
+    return cuda_check(launch_w4(L, (cudaStream_t)stream), "4-bit product launch");
+}
+
+cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed, void *scales, void *stream) {
+    CBS_TRY(w4_shape(n, k, group));
+    CBS_TRY(need(w, "w"));
+    CBS_TRY(need(packed, "packed"));
+    CBS_TRY(need(scales, "scales"));
+    return cuda_check(launch_quantize_w4(w, n, k, group, static_cast<uint8_t *>(packed), scales, (cudaStream_t)stream),
+                      "4-bit quantiser launch");
+}
+
+}  // extern "C"

@@ -437,14 +437,164 @@ CBS_API cbs_status cbs_conv_bn_silu_f32_noalloc(const cbs_plan_t *p, const float
 CBS_API cbs_status cbs_set_launch_options(int flags);
 CBS_API int cbs_launch_options(void);
 
+/* ------------------------------------------------------------------------
+ * Token operators: one quantised step of a model that answers in tokens about
+ * what the layers above saw -- RMS norm to 8 bits, products with 4-bit
+ * weights, a paged key/value cache in 8 bits, attention over it.  No passage
+ * of the pages has a counterpart; the 8-bit scheme is the library's own
+ * (codes q with r = s q, IEEE division, round to nearest even), with one
+ * scale a row instead of one a tensor.  The conventions at the head of this
+ * file hold.  Arrays that name places in other arrays (page tables, lengths,
+ * starts) are checked on the device: a value out of range makes the kernel
+ * skip what it would have named and cbs_read_device_status report
+ * CBS_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache.  A page holds page_size consecutive positions of one
+ * sequence, for every head: k, v [num_pages][kv_heads][page_size][head_dim].
+ * prec CBS_BF16: bfloat16, no scales.  CBS_INT8: codes, and a float scale for
+ * each page, head and position ([num_pages][kv_heads][page_size]).
+ * page_size: 16, 32, 64, 128 or 256.  head_dim: 64 or 128. */
+typedef struct cbs_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;   /* NULL for CBS_BF16 */
+    int prec, num_pages, page_size, kv_heads, head_dim;
+} cbs_cache;
+
+/* The sequences of a call (device arrays; this struct itself is on the host).
+ * Sequence b holds seq_lens[b] positions, the last
+ * new_start[b + 1] - new_start[b] of them new in this call; its position p is
+ * slot p % page_size of page page_table[b * max_pages + p / page_size].  The
+ * new tokens of all sequences lie one after another: sequence b's are
+ * new_start[b] .. new_start[b + 1] - 1 of the call's `total`.  A sequence may
+ * have none, and may be empty. */
+typedef struct cbs_sequences {
+    const int32_t *new_start;    /* [batch + 1], from 0, not decreasing, at most total */
+    const int32_t *seq_lens;     /* [batch] */
+    const int32_t *page_table;   /* [batch][max_pages]; entries past a sequence's length are not read */
+    int batch, max_pages, total;
+} cbs_sequences;
+
+/*
+ * cbs_cache_write -- the new tokens' keys and values into their pages.
+ *   CBS_INT8: s = max|x| / 127 over the token's head_dim values of one head,
+ *   code = clamp(rne(x / s), -127, 127); a row of zeros has scale 0; a row
+ *   that holds a NaN or an infinity gets the scale NaN (it reads back as NaN).
+ *   CBS_BF16: round to nearest even.
+ * k, v: [total][kv_heads][head_dim], in_prec CBS_FP32 or CBS_BF16, with
+ * k_stride and v_stride elements between tokens (multiples of 8, at least
+ * kv_heads * head_dim), so that slices of a fused product can be given.
+ */
+CBS_API cbs_status cbs_cache_write(const cbs_cache *c, const cbs_sequences *s, const void *k, long long k_stride,
+                                   const void *v, long long v_stride, int in_prec, void *stream);
+
+/*
+ * cbs_cache_read -- the sequences' keys and values in order:
+ *   k_out, v_out [batch][max_len][kv_heads][head_dim] (out_prec CBS_FP32 or
+ *   CBS_BF16), positions past a sequence's length zero, positions past
+ *   max_len left out.  new_start is not read and may be NULL.
+ */
+CBS_API cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_len, void *k_out, void *v_out,
+                                  int out_prec, void *stream);
+
+/* One kind of attention call. */
+typedef struct cbs_attn_desc {
+    int batch;         /* sequences */
+    int max_new;       /* most new tokens of one sequence */
+    int max_len;       /* longest length expected; longer ones are computed too, with a less even split */
+    int heads, kv_heads, head_dim;   /* heads a multiple of kv_heads: query head h reads key head h / (heads / kv_heads) */
+    int cache_prec;    /* CBS_BF16 or CBS_INT8 */
+    int causal;        /* 1: a token sees positions up to its own; 0: the whole sequence */
+    int window;        /* > 0: and only the last `window` positions up to its own; 0: no limit */
+    int num_sms;       /* 0 = 152 */
+    int force_kernel;  /* -1: choose; else a cbs_attn_kernel */
+    int force_split;   /* 0: choose; else how many ranges of keys are computed side by side */
+} cbs_attn_desc;
+
+typedef enum cbs_attn_kernel {
+    CBS_ATTN_ROWS = 0   /* few query rows: tiles of 8 or 16 (token, head) rows, keys straight to registers */
+} cbs_attn_kernel;
+
+typedef struct cbs_attn_plan_t {
+    uint32_t size, abi_version;
+    int kernel;             /* cbs_attn_kernel */
+    int row_tile;           /* (token, query head of one key head) rows of a CTA */
+    int row_tiles;          /* tiles of the longest chunk */
+    int split;              /* ranges of keys computed side by side, joined in order */
+    int grid_ctas, threads;
+    size_t workspace_bytes;
+    cbs_attn_desc desc;
+} cbs_attn_plan_t;
+
+/* cbs_attn_plan -- kernel, tile and split for a kind of call.  Host only.
+ * Errors: CBS_ERR_INVALID_ARG, CBS_ERR_UNSUPPORTED (head_dim not 64 or 128). */
+CBS_API cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out);
+
+/*
+ * cbs_paged_attention -- attention of the new tokens over the cache, which
+ * already holds their own keys and values:
+ *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[t, h].k_j - max)
+ * over the positions j that token t sees: j < length; with causal j <= pos(t),
+ * pos(t) = length - new + t; with a window j > pos(t) - window.  A token that
+ * sees nothing gets zeros.  Positions that a token does not see cannot reach
+ * it, whatever they hold (a NaN or infinity included).
+ * q, out: bfloat16 [total][heads][head_dim] with q_stride, out_stride elements
+ * between tokens (multiples of 8).  scale: finite.  workspace: zeroed once
+ * with cbs_workspace_init; not shared by calls that may run at the same time.
+ */
+CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, const cbs_sequences *s,
+                                       const void *q, long long q_stride, float scale, void *out, long long out_stride,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * cbs_rmsnorm -- RMS normalisation with the residual's addition:
+ *   h = x + residual,   y = h * weight / sqrt(mean(h^2) + eps)   per row
+ * x, residual (NULL: h = x), h_out: [rows][cols] of in_prec (CBS_FP32 or
+ * CBS_BF16; h rounded once, the norm computed from the sum in 32 bits);
+ * h_out may be NULL, x or residual.  weight: float[cols].  out_prec = in_prec:
+ * y in that type, scale unused.  out_prec CBS_INT8: with u = h * weight,
+ *   s = max|u| / 127,  y = clamp(rne(u / s), -127, 127),  scale[row] = s / sqrt(..)
+ * so the codes do not depend on the order in which the squares are summed.  A
+ * row that holds a NaN or an infinity gets the scale NaN.  cols: 1 .. 32768.
+ */
+CBS_API cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight, void *h_out, void *y,
+                               float *scale, int rows, int cols, float eps, int in_prec, int out_prec, void *stream);
+
+/* cbs_dequantize_rows -- out[r][c] = q[r][c] * scale[r], CBS_FP32 or CBS_BF16:
+ * the seam behind an operator that scales each row by itself. */
+CBS_API cbs_status cbs_dequantize_rows(const int8_t *q, const float *scale, void *out, int rows, int cols,
+                                       int out_prec, void *stream);
+
+/*
+ * cbs_linear_w4 -- product with 4-bit weights in groups along k:
+ *   y[m,n] = act( xs[m] * sum_g s[g,n] * sum_{k in g} x[m,k] (q[n,k] - z[g,n]) + bias[n] )
+ * x: [rows][k], x_prec CBS_BF16 (x_scale NULL, xs = 1) or CBS_INT8 codes with
+ * x_scale float[rows] (the group sums are then exact whole numbers).
+ * w: [n][k/2] bytes; each 32-bit word (little-endian) holds eight weights of
+ * one output, weights 2i and 2i + 1 in nibbles i and 4 + i.  scales: bfloat16
+ * [k/group][n].  zeros: uint8 [k/group][n] in 0..15, or NULL for 8.  bias:
+ * float[n] or NULL.  y: [rows][n], out_prec CBS_FP32 or CBS_BF16.  activation:
+ * cbs_activation.  group: 32, 64 or 128; k a multiple of it.  Sums in 32 bits.
+ * Made for few rows (every 32 rows read the weights again).
+ */
+CBS_API cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const void *w, const void *scales,
+                                 const void *zeros, const float *bias, void *y, int out_prec, int rows, int n, int k,
+                                 int group, int activation, void *stream);
+
+/* cbs_quantize_w4 -- one-time weight transform for cbs_linear_w4: w float
+ * [n][k] -> packed codes and scales, symmetric (zero point 8):
+ * s = bf16(max|w| / 7) over a group, q = 8 + clamp(rne(w / s), -7, 7). */
+CBS_API cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed, void *scales, void *stream);
+
 /* Zero a workspace before its first use (cudaMemsetAsync on `stream`). */
 CBS_API cbs_status cbs_workspace_init(void *workspace, size_t bytes, void *stream);
 
 /*
  * cbs_read_device_status -- synchronise `stream`, then report whether any
  * kernel of this library on the current device gave up a bounded wait since
- * the last reset: *status_out (host) receives CBS_OK or CBS_ERR_TIMEOUT.
- * reset != 0 clears the flag.
+ * the last reset: *status_out (host) receives CBS_OK or CBS_ERR_TIMEOUT; or,
+ * with no such wait, CBS_ERR_INVALID_ARG if a token operator met a value out
+ * of range in a page table, a length or a start.  reset != 0 clears both.
  */
 CBS_API cbs_status cbs_read_device_status(int *status_out, int reset, void *stream);
 
