@@ -23,9 +23,6 @@ int current_device_sms();
 // A device reset, or a primary context released and made again, gives a new
 // ID: addresses of the library's device globals are cached per ID.
 cbs_status current_context_id(unsigned long long *id);
-// Status-word bits (cbs_read_device_status): a bounded wait ran out; a device
-// array of a call (page table, lengths, starts) held a value out of range.
-constexpr unsigned int kStatusTimeout = 1u, kStatusBadIndex = 2u;
 // Device address of the status word that bounded waits report into.
 unsigned int *device_status_word();
 // One CTA whose bounded wait on a barrier nothing arrives at runs out after

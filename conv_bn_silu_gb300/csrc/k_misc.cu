@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "cbs_internal.cuh"
+#include "status.cuh"
 #include "tc_ptx.cuh"
 
 namespace cbs {

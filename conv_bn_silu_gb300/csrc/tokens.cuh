@@ -4,6 +4,7 @@
 #pragma once
 
 #include "cbs_internal.cuh"
+#include "status.cuh"
 
 namespace cbs {
 
