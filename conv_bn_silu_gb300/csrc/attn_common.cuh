@@ -1,0 +1,157 @@
+// attn_common.cuh -- what the attention kernels share: which keys a row sees,
+// where its query and output lie, the slow path for values that are not
+// finite, and the joining of ranges of keys.
+#pragma once
+
+#include "mma_frag.cuh"
+#include "tokens.cuh"
+
+namespace cbs {
+
+// The running maximum is raised only when a score passes it by more than this
+// (base 2): p stays below 2^8, far inside float and bf16, and most blocks need
+// neither an exchange between lanes nor a rescaling of the output.
+constexpr float kLazy = 8.0f;
+
+// Keys [lo, hi) are what a row at `place` sees of a sequence.
+struct Seen { int lo, hi; };
+__device__ __forceinline__ Seen seen_by(int place, int len, int causal, int window) {
+    Seen s;
+    s.hi = causal ? min(len, place + 1) : len;
+    s.lo = window ? max(0, place - window + 1) : 0;
+    return s;
+}
+
+// One sequence's rows of one key/value head: row r is token r / G of the
+// chunk, query head head * G + r % G.
+struct Rows {
+    int start, fresh, G, R, len, base, head;   // first new token, how many, heads a key head, rows; length, first place
+    __device__ __forceinline__ Seen seen(const AttnLaunch &L, int r) const {
+        return seen_by(base + r / G, len, L.causal, L.window);
+    }
+    __device__ __forceinline__ const __nv_bfloat16 *query(const AttnLaunch &L, int r, int D) const {
+        return static_cast<const __nv_bfloat16 *>(L.q) + (size_t)(start + r / G) * L.q_stride + (size_t)(head * G + r % G) * D;
+    }
+    __device__ __forceinline__ __nv_bfloat16 *out(const AttnLaunch &L, int r, int D) const {
+        return static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + r / G) * L.out_stride + (size_t)(head * G + r % G) * D;
+    }
+};
+
+// The rows of sequence b, its starts within the call's tokens and its chunk
+// within the plan's (the status bit otherwise).
+__device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head) {
+    const CacheArgs &c = L.c;
+    Rows s;
+    const int s0 = c.new_start[b], s1 = c.new_start[b + 1];
+    s.start = max(0, min(s0, c.total));
+    const int end = max(s.start, min(s1, c.total));
+    s.fresh = end - s.start;
+    if (s.start != s0 || end != s1 || s.fresh > L.max_new) {
+        if (threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
+        s.fresh = min(s.fresh, L.max_new);
+    }
+    s.G = L.heads / c.kv_heads;
+    s.R = s.fresh * s.G;
+    s.head = head;
+    s.len = seq_len(c, b);
+    s.base = s.len - s.fresh;
+    return s;
+}
+
+// A share of a row's softmax: (maximum, sum) and the unnormalised output.  A
+// share without a visible key has maximum -inf and sum zero, and adds nothing
+// (its output may hold anything); a NaN score leaves the sum NaN, which stays.
+__device__ __forceinline__ float share_factor(float m, float l, float top) {
+    if (m == -INFINITY) return l == 0.0f ? 0.0f : 1.0f;
+    return frag::ex2(m - top);
+}
+
+// Four dimensions of a row's output: acc / sum, zeros for a row that sees nothing.
+__device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, int r, int D, int dim, float4 acc, float sum) {
+    const Seen z = s.seen(L, r);
+    uint2 w = make_uint2(0u, 0u);
+    if (z.hi > z.lo) {
+        const float inv = __fdiv_rn(1.0f, sum);
+        w.x = frag::pack_bf16(acc.x * inv, acc.y * inv);
+        w.y = frag::pack_bf16(acc.z * inv, acc.w * inv);
+    }
+    *reinterpret_cast<uint2 *>(s.out(L, r, D) + dim) = w;
+}
+
+// A bf16 cache's row by itself over keys [k0, k1): what the kernels fall back
+// to when a block that some rows must not see in full holds a value that is not
+// finite (0 x inf would reach them).  A warp; lane holds D / 32 dimensions.
+template <int D>
+__device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b, int r, int k0, int k1, int lane,
+                                      float (&acc)[D / 32], float &mm, float &ll) {
+    constexpr int kE = D / 32;
+    const CacheArgs &c = L.c;
+    const __nv_bfloat16 *qp = s.query(L, r, D) + lane * kE;
+    const Seen z = s.seen(L, r);
+    float qv[kE];
+    mm = -INFINITY;
+    ll = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        qv[e] = __bfloat162float(qp[e]);
+        acc[e] = 0.0f;
+    }
+    for (int key = max(z.lo, k0); key < min(z.hi, k1); ++key) {
+        const int p = page_of(c, b, key);
+        if (p < 0) continue;
+        const size_t at = ((((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1))) * D + lane * kE;
+        const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(c.k) + at, *vp = static_cast<const __nv_bfloat16 *>(c.v) + at;
+        float dot = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) dot = fmaf(qv[e], __bfloat162float(kp[e]), dot);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(~0u, dot, x);
+        dot *= L.scale_log2;
+        const float nm = fmaxf(mm, dot);
+        const float use = nm == -INFINITY ? 0.0f : nm;
+        const float fac = mm == -INFINITY ? 0.0f : frag::ex2(mm - use), pr = frag::ex2(dot - use);
+        ll = ll * fac + pr;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = acc[e] * fac + pr * __bfloat162float(vp[e]);
+        mm = nm;
+    }
+}
+
+// After a CTA has written its range's share of a tile (L.partial, L.stats):
+// the CTA that comes last joins the ranges, in their order, so that the result
+// does not depend on which one that is.  `flag`: a word of shared memory.
+template <int D, int kRows, int kThreads>
+__device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, int tile, int r0, int active, int tid, int *flag) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const unsigned before = atomicAdd(L.counters + tile, 1u);
+        *flag = before == (unsigned)active - 1u;
+        if (*flag) L.counters[tile] = 0u;   // ready for the next call
+    }
+    __syncthreads();
+    if (!*flag) return;
+    __threadfence();
+    constexpr int kU = D / 4;   // units of four dimensions
+    for (int i = tid; i < kRows * kU; i += kThreads) {
+        const int r = i / kU, u = i % kU;
+        if (r0 + r >= s.R) break;
+        const size_t at = (size_t)tile * L.split * kRows + r;
+        float top = -INFINITY;
+        for (int x = 0; x < active; ++x) top = fmaxf(top, __ldcg(&L.stats[at + (size_t)x * kRows]).x);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+        for (int x = 0; x < active; ++x) {
+            const float2 st = __ldcg(&L.stats[at + (size_t)x * kRows]);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(L.partial + (at + (size_t)x * kRows) * D + 4 * u));
+            const float fac = share_factor(st.x, st.y, top);
+            if (st.x == -INFINITY && fac == 0.0f) continue;
+            acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
+            acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
+            sum = fmaf(st.y, fac, sum);
+        }
+        store_out4(L, s, r0 + r, D, 4 * u, acc, sum);
+    }
+}
+
+}  // namespace cbs

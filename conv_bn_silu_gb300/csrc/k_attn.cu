@@ -18,6 +18,7 @@
 // Ranges of keys are joined by the range's CTA that finishes last (a counter
 // per row tile), in the order of the ranges: the result does not depend on
 // which CTA that is.
+#include "attn_common.cuh"
 #include "mma_frag.cuh"
 #include "tc_ptx.cuh"
 #include "tokens.cuh"
@@ -27,10 +28,6 @@ namespace cbs {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kBlock = 16;   // keys a warp takes at a time
-// The running maximum is raised only when a score passes it by more than this
-// (base 2): p stays below 2^8, far inside float and bf16, and most blocks need
-// no exchange between lanes.
-constexpr float kLazy = 8.0f;
 
 __device__ __forceinline__ bool not_finite_pair(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -85,15 +82,6 @@ struct KvFrag {
     }
 };
 
-// One row's positions: keys [lo, hi) are what the row sees.
-struct Seen { int lo, hi; };
-__device__ __forceinline__ Seen seen_by(int place, int len, int causal, int window) {
-    Seen s;
-    s.hi = causal ? min(len, place + 1) : len;
-    s.lo = window ? max(0, place - window + 1) : 0;
-    return s;
-}
-
 template <int D, bool I8, int NR>
 __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L) {
     constexpr int kRows = 8 * NR;
@@ -108,16 +96,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads, rt = blockIdx.y / c.kv_heads;
-    const int G = L.heads / c.kv_heads;
-    const int start = max(0, min(c.new_start[b], c.total)), end = max(start, min(c.new_start[b + 1], c.total));
-    int fresh = end - start;
-    if (start != c.new_start[b] || end != c.new_start[b + 1] || fresh > L.max_new) {
-        if (tid == 0) atomicOr(c.status, kStatusBadIndex);
-        fresh = min(fresh, L.max_new);
-    }
-    const int R = fresh * G, r0 = rt * kRows;
+    const Rows rs = rows_of(L, b, head);
+    const int R = rs.R, G = rs.G, r0 = rt * kRows, len = rs.len, base = rs.base;
     if (r0 >= R) return;
-    const int len = seq_len(c, b), base = len - fresh;
     const int t_lo = r0 / G, t_hi = (min(R, r0 + kRows) - 1) / G;
     // Keys that some row of the tile sees, in blocks of 16 from a multiple of 16.
     const int lo = seen_by(base + t_lo, len, L.causal, L.window).lo;
@@ -142,8 +123,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int r = r0 + n * 8 + g;
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(L.q) +
-                                 (size_t)(start + r / G) * L.q_stride + (size_t)(head * G + r % G) * D;
+        const __nv_bfloat16 *p = rs.query(L, r, D);
 #pragma unroll
         for (int u = 0; u < D / 32; ++u) {   // 16-byte units of this lane
             const int dim = I8 ? (u >> 1) * 64 + j * 16 + (u & 1) * 8 : u * 32 + j * 8;
@@ -151,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
             q[n][4 * u] = w.x; q[n][4 * u + 1] = w.y; q[n][4 * u + 2] = w.z; q[n][4 * u + 3] = w.w;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) seen[n][i] = seen_by(base + (r0 + n * 8 + 2 * j + i) / G, len, L.causal, L.window);
+        for (int i = 0; i < 2; ++i) seen[n][i] = rs.seen(L, r0 + n * 8 + 2 * j + i);
     }
 
     float o[NR][kMT][4], m[NR][2], l[NR][2];
@@ -349,36 +329,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
         // finite.  Each row by itself, over the keys it sees.
         constexpr int kE = D / 32;   // dimensions a lane
         for (int r = warp; r < kRows && r0 + r < R; r += kWarps) {
-            const int row_id = r0 + r;
-            const Seen z = seen_by(base + row_id / G, len, L.causal, L.window);
-            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(L.q) + (size_t)(start + row_id / G) * L.q_stride +
-                                      (size_t)(head * G + row_id % G) * D + lane * kE;
-            float qv[kE], acc[kE], mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                qv[e] = __bfloat162float(qp[e]);
-                acc[e] = 0.0f;
-            }
-            const int k0 = max(z.lo, lo16 + b0 * kBlock), k1 = min(z.hi, lo16 + b1 * kBlock);
-            for (int key = k0; key < k1; ++key) {
-                const int p = page_of(c, b, key);
-                if (p < 0) continue;
-                const size_t at = ((((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1))) * D + lane * kE;
-                const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(c.k) + at, *vp = static_cast<const __nv_bfloat16 *>(c.v) + at;
-                float dot = 0.0f;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) dot = fmaf(qv[e], __bfloat162float(kp[e]), dot);
-#pragma unroll
-                for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(~0u, dot, x);
-                dot *= L.scale_log2;
-                const float nm = fmaxf(mm, dot);
-                const float use = nm == -INFINITY ? 0.0f : nm;
-                const float fac = mm == -INFINITY ? 0.0f : frag::ex2(mm - use), pr = frag::ex2(dot - use);
-                ll = ll * fac + pr;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) acc[e] = acc[e] * fac + pr * __bfloat162float(vp[e]);
-                mm = nm;
-            }
+            float acc[kE], mm, ll;
+            slow_row<D>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
 #pragma unroll
             for (int e = 0; e < kE; ++e) s_o[0][r][lane * kE + e] = acc[e];
             if (lane < kWarps) {
@@ -401,72 +353,22 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            // A warp without a visible key adds nothing (its l is zero, or NaN
-            // where a score was NaN, which stays).
-            const float mw = s_m[w][r];
-            const float fac = mw == -INFINITY ? (s_l[w][r] == 0.0f ? 0.0f : 1.0f) : frag::ex2(mw - top);
-            if (fac == 0.0f && mw == -INFINITY) continue;
+            const float fac = share_factor(s_m[w][r], s_l[w][r], top);
+            if (s_m[w][r] == -INFINITY && fac == 0.0f) continue;
             const float4 v = *reinterpret_cast<const float4 *>(&s_o[w][r][4 * u]);
             acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
             acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
             sum = fmaf(s_l[w][r], fac, sum);
         }
         if (active == 1) {
-            const int row_id = r0 + r;
-            const Seen z = seen_by(base + row_id / G, len, L.causal, L.window);
-            const float inv = z.hi > z.lo ? __fdiv_rn(1.0f, sum) : 0.0f;
-            uint2 w;
-            w.x = z.hi > z.lo ? frag::pack_bf16(acc.x * inv, acc.y * inv) : 0u;
-            w.y = z.hi > z.lo ? frag::pack_bf16(acc.z * inv, acc.w * inv) : 0u;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + row_id / G) * L.out_stride +
-                                 (size_t)(head * G + row_id % G) * D + 4 * u;
-            *reinterpret_cast<uint2 *>(out) = w;
+            store_out4(L, rs, r0 + r, D, 4 * u, acc, sum);
         } else {
             const size_t at = ((size_t)tile * L.split + sp) * kRows + r;
             *reinterpret_cast<float4 *>(L.partial + at * D + 4 * u) = acc;
             if (u == 0) L.stats[at] = make_float2(top, sum);
         }
     }
-    if (active == 1) return;
-
-    // ---- the last range's CTA to get here joins them all
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        const unsigned seen_before = atomicAdd(L.counters + tile, 1u);
-        s_flag = seen_before == (unsigned)active - 1u;
-        if (s_flag) L.counters[tile] = 0u;   // ready for the next call
-    }
-    __syncthreads();
-    if (!s_flag) return;
-    __threadfence();
-    for (int i = tid; i < kRows * kU; i += kThreads) {
-        const int r = i / kU, u = i % kU;
-        if (r0 + r >= R) break;
-        const size_t at = (size_t)tile * L.split * kRows + r;
-        float top = -INFINITY;
-        for (int x = 0; x < active; ++x) top = fmaxf(top, __ldcg(&L.stats[at + (size_t)x * kRows]).x);
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-        for (int x = 0; x < active; ++x) {
-            const float2 st = __ldcg(&L.stats[at + (size_t)x * kRows]);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(L.partial + (at + (size_t)x * kRows) * D + 4 * u));
-            const float fac = st.x == -INFINITY ? (st.y == 0.0f ? 0.0f : 1.0f) : frag::ex2(st.x - top);
-            if (fac == 0.0f && st.x == -INFINITY) continue;
-            acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
-            acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
-            sum = fmaf(st.y, fac, sum);
-        }
-        const int row_id = r0 + r;
-        const Seen z = seen_by(base + row_id / G, len, L.causal, L.window);
-        const float inv = z.hi > z.lo ? __fdiv_rn(1.0f, sum) : 0.0f;
-        uint2 w;
-        w.x = z.hi > z.lo ? frag::pack_bf16(acc.x * inv, acc.y * inv) : 0u;
-        w.y = z.hi > z.lo ? frag::pack_bf16(acc.z * inv, acc.w * inv) : 0u;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + row_id / G) * L.out_stride +
-                             (size_t)(head * G + row_id % G) * D + 4 * u;
-        *reinterpret_cast<uint2 *>(out) = w;
-    }
+    if (active > 1) join_ranges<D, kRows, kThreads>(L, rs, tile, r0, active, tid, &s_flag);
 }
 
 template <int D, bool I8>

@@ -87,5 +87,8 @@ struct AttnLaunch {
     unsigned int *counters;     // [batch][kv_heads][row_tiles]
 };
 cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
+// Tensor-core kernel: tiles of kAttnChunkRows rows.
+cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);
+constexpr int kAttnChunkRows = 256, kAttnChunkKeys = 128;
 
 }  // namespace cbs

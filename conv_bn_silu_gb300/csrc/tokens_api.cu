@@ -82,6 +82,9 @@ cbs_status token_stride(long long stride, long long least, const char *what) {
 
 constexpr int kGridMax = 65535;
 
+// Most rows of a key head for the few-row kernel.
+constexpr int kAttnRowsMost = 64;
+
 size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
     return ((size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * 4 + 255) / 256 * 256;
 }
@@ -136,7 +139,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         return fail(CBS_ERR_INVALID_ARG, "%d heads do not share %d key heads evenly", d->heads, d->kv_heads);
     if (d->cache_prec != CBS_BF16 && d->cache_prec != CBS_INT8)
         return fail(CBS_ERR_INVALID_ARG, "a cache is BF16 or INT8");
-    if (d->force_kernel < -1 || d->force_kernel > CBS_ATTN_ROWS)
+    if (d->force_kernel < -1 || d->force_kernel > CBS_ATTN_CHUNK)
         return fail(CBS_ERR_INVALID_ARG, "unknown attention kernel %d", d->force_kernel);
     cbs_attn_plan_t p;
     std::memset(&p, 0, sizeof(p));
@@ -144,8 +147,9 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     p.abi_version = CBS_ABI_VERSION;
     p.desc = *d;
     const long long rows = (long long)d->max_new * (d->heads / d->kv_heads);
-    p.kernel = CBS_ATTN_ROWS;
-    p.row_tile = rows <= 8 ? 8 : 16;
+    p.kernel = d->force_kernel >= 0 ? d->force_kernel : rows > kAttnRowsMost ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
+    const bool chunk = p.kernel == CBS_ATTN_CHUNK;
+    p.row_tile = chunk ? kAttnChunkRows : rows <= 8 ? 8 : 16;
     const long long tiles = (rows + p.row_tile - 1) / p.row_tile;
     if (tiles * d->kv_heads > kGridMax || d->batch > kGridMax)
         return fail(CBS_ERR_UNSUPPORTED, "%lld row tiles of %d heads, %d sequences: at most %d", tiles, d->kv_heads,
@@ -154,10 +158,24 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
     const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
     const int keys = d->window > 0 ? std::min(d->max_len, d->window + d->max_new) : d->max_len;
-    const long long want = ((long long)sms * 4 + base - 1) / base;
-    p.split = d->force_split ? d->force_split
-                             : (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
-    p.threads = 128;
+    if (d->force_split) {
+        p.split = d->force_split;
+    } else if (chunk) {
+        // One CTA an SM: the split with the least rounds of CTAs times key tiles
+        // of a range, where each range costs about two tiles more (filling the
+        // pipeline, and writing and joining its share).
+        const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
+        long long best = LLONG_MAX;
+        for (int x = 1; x <= std::min(key_tiles, 32); ++x) {
+            const long long rounds = (base * x + sms - 1) / sms;
+            const long long cost = rounds * ((key_tiles + x - 1) / x + (x > 1 ? 3 : 1));
+            if (cost < best) best = cost, p.split = x;
+        }
+    } else {
+        const long long want = ((long long)sms * 4 + base - 1) / base;
+        p.split = (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
+    }
+    p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 512 : 384) : 128;
     const long long ctas = base * p.split;
     if (ctas > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld CTAs", ctas);
     p.grid_ctas = (int)ctas;
@@ -206,6 +224,7 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
         L.stats = reinterpret_cast<float2 *>(w + attn_counter_bytes(*p));
         L.partial = reinterpret_cast<float *>(w + attn_counter_bytes(*p) + (attn_stat_rows(*p) * 8 + 255) / 256 * 256);
     }
+    if (p->kernel == CBS_ATTN_CHUNK) return launch_attn_chunk(L, (cudaStream_t)stream);
     return cuda_check(launch_attn_rows(L, p->row_tile, (cudaStream_t)stream), "attention launch");
 }
 

@@ -512,7 +512,8 @@ typedef struct cbs_attn_desc {
 } cbs_attn_desc;
 
 typedef enum cbs_attn_kernel {
-    CBS_ATTN_ROWS = 0   /* few query rows: tiles of 8 or 16 (token, head) rows, keys straight to registers */
+    CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 or 16 (token, head) rows, keys straight to registers */
+    CBS_ATTN_CHUNK = 1  /* many: tiles of 256 rows on tcgen05, scores and output in tensor memory */
 } cbs_attn_kernel;
 
 typedef struct cbs_attn_plan_t {

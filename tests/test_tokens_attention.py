@@ -72,6 +72,34 @@ def test_chunks(cuda_lib, lens, new, causal, int8):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", [B.CBS_ATTN_ROWS, B.CBS_ATTN_CHUNK])
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 256), (128, 32), (128, 128)])
+def test_both_kernels(cuda_lib, d, page, kernel, int8):
+    """The kernels hold over the same calls, whichever the plan would take."""
+    kw = dict(d=d, page=page, int8=int8, kernel=kernel)
+    run_case([1], [1], 2, 1, **kw)
+    run_case([127, 128, 129, 0], [1, 128, 50, 0], 4, 2, **kw)
+    run_case([640], [129], 6, 2, **kw)
+    run_case([640], [129], 6, 2, causal=False, split=3, **kw)
+    run_case([1300, 700], [70, 300], 8, 2, window=200, split=2, **kw)
+    run_case([3, 0, 5], [6, 2, 1], 4, 2, **kw)
+    run_case([900], [64], 35, 5, split=5, scale=0.3, **kw)
+
+
+@pytest.mark.parametrize("kernel", [B.CBS_ATTN_ROWS, B.CBS_ATTN_CHUNK])
+def test_scores_that_grow_along_the_keys(cuda_lib, kernel):
+    """The running maximum moves at every tile, by much."""
+    n, d, page, new = 700, 64, 16, 40
+    paged = refs.make_paged([n], 1, d, page, False, 6)
+    grow = torch.linspace(-8, 8, n)
+    for pos in range(n):
+        paged["k"][paged["table"][0, pos // page], 0, pos % page] = (grow[pos] * torch.ones(d)).to(torch.bfloat16)
+    q = (torch.ones((new, 4, d)) * torch.linspace(-4, 4, new)[:, None, None]).to(torch.bfloat16)
+    for split in (1, 3):
+        run_case([n], [new], 4, 1, d, page, False, q=q, paged=paged, split=split, kernel=kernel)
+
+
+@pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("window", [1, 2, 16, 100, 5000])
 def test_windows(cuda_lib, window, int8):
     run_case([400, 77], [150, 1], 8, 2, 64, 32, int8, window=window)
