@@ -13,10 +13,27 @@ namespace {
 // Code of x in a row of scale s: clamp(rne(x / s)), IEEE division as in the
 // library's other quantisers.  A zero scale (a row of zeros, or one so small
 // that max / 127 is zero) gives code 0, and so does a NaN.
-__device__ __forceinline__ int code_of(float x, float s) {
-    if (!(s > 0.0f)) return 0;
-    const float q = rintf(__fdiv_rn(x, s));
-    return q != q ? 0 : (int)fminf(fmaxf(q, -127.0f), 127.0f);
+//
+// x times the rounded reciprocal is within 2^-15 of the quotient (|q| <= 127,
+// three roundings), so away from the halves between whole numbers both round
+// to the same code; only a product that close to a half (or a scale whose
+// reciprocal overflows) pays for the division.  Adding 1.5 * 2^23 rounds to
+// the nearest even whole number and leaves it in the sum's low byte.
+struct RowScale {
+    float s, inv;
+    static __device__ __forceinline__ RowScale of(float scale) { return RowScale{scale, __fdiv_rn(1.0f, scale)}; }
+    __device__ uint32_t code(float x) const {   // in the low byte
+        const float y = __fmul_rn(x, inv);
+        const float t = __fadd_rn(y, 12582912.0f);
+        if (fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) < 0.5f - 6.2e-5f) return __float_as_uint(t);
+        if (!(s > 0.0f)) return 0u;
+        const float q = rintf(__fdiv_rn(x, s));
+        return q != q ? 0u : (uint32_t)(int)fminf(fmaxf(q, -127.0f), 127.0f);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 template <typename T>
@@ -84,7 +101,35 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // element by element.
 constexpr int kNormMaxThreads = 1024;
 
-template <typename T, int VPT, bool I8, bool RES>
+// Eight weights from column c (a multiple of eight in rows that are).  Rows of
+// other widths start anywhere in a unit: three 16-byte loads around the eight,
+// shifted by c mod 4, which is the same for the whole row.
+template <bool WHOLE>
+__device__ __forceinline__ void weights8(const float *w, long long c, int cols, float (&f)[8]) {
+    if constexpr (WHOLE) {
+        Vec8<float> v;
+        v.load(w + c);
+        v.get(f);
+    } else {
+        const int at = (int)c, sh = at & 3, lo = at - sh;
+        if (at >= 0 && lo + 12 <= cols) {
+            float g[12];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(w + lo) + i);
+                g[4 * i] = v.x; g[4 * i + 1] = v.y; g[4 * i + 2] = v.z; g[4 * i + 3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = sh < 2 ? (sh ? g[i + 1] : g[i]) : (sh == 2 ? g[i + 2] : g[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = at + i >= 0 && at + i < cols ? __ldg(w + at + i) : 0.0f;
+        }
+    }
+}
+
+// WHOLE: cols is a multiple of eight, so every unit lies in one row.
+template <typename T, int VPT, bool I8, bool RES, bool WHOLE>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaunch L) {
     __shared__ float red[2][32];
     ptx::griddep_wait();
@@ -94,54 +139,64 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
     const long long u0 = e0 >> 3;                                     // its first unit
     const T *x = static_cast<const T *>(L.x), *r = static_cast<const T *>(L.residual);
     T *ho = static_cast<T *>(L.h);
+    const auto unit = [&](int v) { return (u0 + tid + (long long)v * nt) * 8; };
+    const auto whole = [&](long long e) { return (WHOLE || e >= e0) && e + 8 <= e1; };
+    const auto any = [&](long long e) { return !WHOLE && e < e1; };   // an edge's elements, one by one
 
     float h[VPT][8];
-    float sum = 0.0f, top = 0.0f;
+    {
+        Vec8<T> a[VPT], b[RES ? VPT : 1];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const long long e = (u0 + tid + (long long)v * nt) * 8;
-        if (e >= e0 && e + 8 <= e1) {
-            Vec8<T> a;
-            a.load(x + e);
-            a.get(h[v]);
-            if (RES) {
-                Vec8<T> b;
-                float f[8];
-                b.load(r + e);
-                b.get(f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[v][i] = __fadd_rn(h[v][i], f[i]);
+        for (int v = 0; v < VPT; ++v)
+            if (whole(unit(v))) {
+                a[v].load(x + unit(v));
+                if constexpr (RES) b[v].load(r + unit(v));
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = e + i >= e0 && e + i < e1;
-                h[v][i] = in ? to_float(x[e + i]) : 0.0f;
-                if (RES && in) h[v][i] = __fadd_rn(h[v][i], to_float(r[e + i]));
+        for (int v = 0; v < VPT; ++v) {
+            const long long e = unit(v);
+            if (whole(e)) {
+                a[v].get(h[v]);
+                if constexpr (RES) {
+                    float f[8];
+                    b[v].get(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[v][i] = __fadd_rn(h[v][i], f[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = any(e) && e + i >= e0 && e + i < e1;
+                    h[v][i] = in ? to_float(x[e + i]) : 0.0f;
+                    if (RES && in) h[v][i] = __fadd_rn(h[v][i], to_float(r[e + i]));
+                }
             }
         }
     }
+    float sum = 0.0f, top = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const long long e = (u0 + tid + (long long)v * nt) * 8;
+        const long long e = unit(v);
         if (RES && ho) {
-            if (e >= e0 && e + 8 <= e1) {
+            if (whole(e)) {
                 Vec8<T> a;
                 a.set(h[v]);
                 a.store(ho + e);
-            } else {
+            } else if (any(e)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (e + i >= e0 && e + i < e1) put(ho + e + i, h[v][i]);
             }
         }
+        if (whole(e) || any(e)) {
+            float w[8];
+            weights8<WHOLE>(L.weight, e - e0, L.cols, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sum = fmaf(h[v][i], h[v][i], sum);
-            const long long c = e + i - e0;
-            const float w = c >= 0 && c < L.cols ? __ldg(L.weight + c) : 0.0f;
-            h[v][i] = __fmul_rn(h[v][i], w);
-            if (I8) top = fmaxf(top, fabsf(h[v][i]));
+            for (int i = 0; i < 8; ++i) {
+                sum = fmaf(h[v][i], h[v][i], sum);
+                h[v][i] = __fmul_rn(h[v][i], w[i]);
+                if (I8) top = fmaxf(top, fabsf(h[v][i]));
+            }
         }
     }
     // The two reductions of the block in one exchange.
@@ -164,18 +219,19 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
         if (I8) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     }
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)L.cols), L.eps)));
-    const float s = __fdiv_rn(top, 127.0f);
-    if (I8 && tid == 0) L.scale[row] = __fmul_rn(s, rstd);
+    const RowScale s = RowScale::of(__fdiv_rn(top, 127.0f));
+    if (I8 && tid == 0) L.scale[row] = __fmul_rn(s.s, rstd);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const long long e = (u0 + tid + (long long)v * nt) * 8;
-        const bool whole = e >= e0 && e + 8 <= e1;
-        if (I8) {
+        const long long e = unit(v);
+        if (!whole(e) && !any(e)) continue;
+        if constexpr (I8) {
             int8_t *y = static_cast<int8_t *>(L.y);
-            uint32_t w[2] = {0u, 0u};
+            uint32_t w[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(uint8_t)code_of(h[v][i], s) << (8 * (i & 3));
-            if (whole) {
+            for (int i = 0; i < 2; ++i)
+                w[i] = pack4(s.code(h[v][4 * i]), s.code(h[v][4 * i + 1]), s.code(h[v][4 * i + 2]), s.code(h[v][4 * i + 3]));
+            if (whole(e)) {
                 *reinterpret_cast<uint2 *>(y + e) = make_uint2(w[0], w[1]);
             } else {
 #pragma unroll
@@ -186,7 +242,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
             T *y = static_cast<T *>(L.y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[v][i] = __fmul_rn(h[v][i], rstd);
-            if (whole) {
+            if (whole(e)) {
                 Vec8<T> a;
                 a.set(h[v]);
                 a.store(y + e);
@@ -199,25 +255,31 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
     }
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool WHOLE>
 cudaError_t launch_norm_vpt(const NormLaunch &L, int units, cudaStream_t s) {
     const int threads = ((units + VPT - 1) / VPT + 31) / 32 * 32;
     const bool res = L.residual != nullptr;
     if (L.out_int8) {
-        if (res) return launch_kernel(rmsnorm_kernel<T, VPT, true, true>, L.rows, threads, 0, s, L);
-        return launch_kernel(rmsnorm_kernel<T, VPT, true, false>, L.rows, threads, 0, s, L);
+        if (res) return launch_kernel(rmsnorm_kernel<T, VPT, true, true, WHOLE>, L.rows, threads, 0, s, L);
+        return launch_kernel(rmsnorm_kernel<T, VPT, true, false, WHOLE>, L.rows, threads, 0, s, L);
     }
-    if (res) return launch_kernel(rmsnorm_kernel<T, VPT, false, true>, L.rows, threads, 0, s, L);
-    return launch_kernel(rmsnorm_kernel<T, VPT, false, false>, L.rows, threads, 0, s, L);
+    if (res) return launch_kernel(rmsnorm_kernel<T, VPT, false, true, WHOLE>, L.rows, threads, 0, s, L);
+    return launch_kernel(rmsnorm_kernel<T, VPT, false, false, WHOLE>, L.rows, threads, 0, s, L);
 }
 
 template <typename T>
 cudaError_t launch_norm_typed(const NormLaunch &L, cudaStream_t s) {
     // Units of eight elements a row can touch: one more where rows start off a unit's edge.
-    const int units = (L.cols + 7) / 8 + (L.cols % 8 ? 1 : 0);
-    if (units <= 256) return launch_norm_vpt<T, 1>(L, units, s);
-    if (units <= 1024) return launch_norm_vpt<T, 2>(L, units, s);
-    return launch_norm_vpt<T, 5>(L, units, s);   // kNormMaxCols and an odd start: 4097 units
+    if (L.cols % 8 == 0) {
+        const int units = L.cols / 8;
+        if (units <= 256) return launch_norm_vpt<T, 1, true>(L, units, s);
+        if (units <= 1024) return launch_norm_vpt<T, 2, true>(L, units, s);
+        return launch_norm_vpt<T, 4, true>(L, units, s);
+    }
+    const int units = (L.cols + 7) / 8 + 1;
+    if (units <= 256) return launch_norm_vpt<T, 1, false>(L, units, s);
+    if (units <= 1024) return launch_norm_vpt<T, 2, false>(L, units, s);
+    return launch_norm_vpt<T, 5, false>(L, units, s);   // kNormMaxCols and an odd start: 4097 units
 }
 
 // ------------------------------------------------------- rows in 8 bits -> float
@@ -230,9 +292,10 @@ __global__ void dequantize_rows_kernel(const int8_t *__restrict__ q, const float
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const size_t units = (count + 15) / 16;
+    const bool narrow = count >> 32 == 0;   // a 64-bit division costs more than the unit's sixteen products
     for (size_t g = blockIdx.x * (size_t)blockDim.x + threadIdx.x; g < units; g += (size_t)gridDim.x * blockDim.x) {
         const size_t e = g * 16;
-        const size_t row = e / cols;
+        const size_t row = narrow ? (uint32_t)e / (uint32_t)cols : e / cols;
         const int c = (int)(e - row * cols);
         if (e + 16 <= count && c + 16 <= cols) {
             const uint4 w = *reinterpret_cast<const uint4 *>(q + e);
@@ -279,115 +342,144 @@ __device__ __forceinline__ int sequence_of(const CacheArgs &a, int i) {
     return a.new_start[lo] <= i && i < a.new_start[lo + 1] ? lo : -1;
 }
 
-// New tokens into their pages.  D / 4 lanes take one row (a token's key or
-// value of one head), four elements each; a row's largest magnitude comes from
-// a butterfly over its lanes.
+// Where a token's rows go: its page's first row of head 0 and its slot, or -1.
+struct Place { int page, slot; };
+__device__ __forceinline__ Place place_of(const CacheArgs &a, int i) {
+    const int b = sequence_of(a, i);
+    const int pos = b < 0 ? -1 : seq_len(a, b) - (a.new_start[b + 1] - i);
+    if (pos < 0) {
+        atomicOr(a.status, kStatusBadIndex);
+        return Place{-1, 0};
+    }
+    return Place{page_of(a, b, pos), pos & ((1 << a.page_shift) - 1)};
+}
+
+// New tokens into their pages.  A row is a token's key or value of one head;
+// D / 4 lanes take it, four elements each, and its largest magnitude comes from
+// a butterfly over them.  A warp takes kRowsWarp rows of one token (rows 2 head +
+// side), so the token's place is looked up once for all of them and their loads
+// are in flight together.
+constexpr int kRowsWarp = 4;
+
 template <typename T, int D>
 __global__ void cache_write_kernel(const CacheArgs a, const T *__restrict__ k, long long k_stride,
                                    const T *__restrict__ v, long long v_stride) {
-    constexpr int kLanes = D / 4;
+    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes, kSteps = kRowsWarp / kAtOnce;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const long long rows = (long long)a.total * a.kv_heads * 2;
-    const int lane = threadIdx.x % kLanes;
-    const long long step = (long long)gridDim.x * (blockDim.x / kLanes);
-    // Whole warps go round together: the butterfly needs every lane.
-    const long long first = (long long)blockIdx.x * (blockDim.x / kLanes) + threadIdx.x / kLanes;
-    const long long rounds = (rows + step - 1) / step;
-    for (long long it = 0; it < rounds; ++it) {
-        const long long row = first + it * step;
-        bool live = row < rows;
-        const int side = (int)(row & 1);   // 0: key, 1: value
-        const int head = live ? (int)((row >> 1) % a.kv_heads) : 0;
-        const int i = live ? (int)((row >> 1) / a.kv_heads) : 0;
-        size_t at = 0;
-        if (live) {
-            const int b = sequence_of(a, i);
-            const int n = b < 0 ? 0 : seq_len(a, b);
-            const int pos = b < 0 ? -1 : n - (a.new_start[b + 1] - i);
-            const int p = pos < 0 ? -1 : page_of(a, b, pos);
-            if (pos < 0) atomicOr(a.status, kStatusBadIndex);
-            live = p >= 0;
-            if (live)
-                at = (((size_t)p * a.kv_heads + head) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-        }
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (live) {
-            const T *src = (side ? v + (size_t)i * v_stride : k + (size_t)i * k_stride) + head * D + lane * 4;
+    const int rows = 2 * a.kv_heads, parts = (rows + kRowsWarp - 1) / kRowsWarp;
+    const long long tasks = (long long)a.total * parts;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, at4 = (lane % kLanes) * 4;
+    const long long step = (long long)gridDim.x * (blockDim.x >> 5);
+    for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < tasks; task += step) {
+        const int i = (int)(task / parts), part = (int)(task - (long long)i * parts);
+        const Place place = place_of(a, i);
+        if (place.page < 0) continue;
+        float f[kSteps][4];
+#pragma unroll
+        for (int x = 0; x < kSteps; ++x) {
+            const int row = part * kRowsWarp + x * kAtOnce + sub, head = row >> 1;
+            f[x][0] = f[x][1] = f[x][2] = f[x][3] = 0.0f;
+            if (row >= rows) continue;
+            const T *src = (row & 1 ? v + (size_t)i * v_stride : k + (size_t)i * k_stride) + head * D + at4;
             if constexpr (sizeof(T) == 2) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                f[0] = __uint_as_float(w.x << 16);
-                f[1] = __uint_as_float(w.x & 0xffff0000u);
-                f[2] = __uint_as_float(w.y << 16);
-                f[3] = __uint_as_float(w.y & 0xffff0000u);
+                f[x][0] = __uint_as_float(w.x << 16);
+                f[x][1] = __uint_as_float(w.x & 0xffff0000u);
+                f[x][2] = __uint_as_float(w.y << 16);
+                f[x][3] = __uint_as_float(w.y & 0xffff0000u);
             } else {
                 const float4 w = *reinterpret_cast<const float4 *>(src);
-                f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
+                f[x][0] = w.x; f[x][1] = w.y; f[x][2] = w.z; f[x][3] = w.w;
             }
         }
-        if (a.int8) {
-            float top = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
-            bool nan = f[0] != f[0] || f[1] != f[1] || f[2] != f[2] || f[3] != f[3];
 #pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) {
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                nan |= __shfl_xor_sync(~0u, (int)nan, o) != 0;
+        for (int x = 0; x < kSteps; ++x) {
+            const int row = part * kRowsWarp + x * kAtOnce + sub, head = row >> 1;
+            const size_t at = (((size_t)place.page * a.kv_heads + head) << a.page_shift) + place.slot;
+            if (a.int8) {
+                float top = fmaxf(fmaxf(fabsf(f[x][0]), fabsf(f[x][1])), fmaxf(fabsf(f[x][2]), fabsf(f[x][3])));
+                // NaN where a value is not finite (0 x inf, 0 x NaN), else zero
+                float odd = 0.0f * f[x][0] + 0.0f * f[x][1] + 0.0f * f[x][2] + 0.0f * f[x][3];
+#pragma unroll
+                for (int o = kLanes / 2; o; o >>= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                    odd += __shfl_xor_sync(~0u, odd, o);
+                }
+                if (row >= rows) continue;
+                // A row that holds a NaN or an infinity reads back as NaN.
+                const RowScale s = RowScale::of(odd == 0.0f ? __fdiv_rn(top, 127.0f) : __int_as_float(0x7fc00000));
+                *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(row & 1 ? a.v : a.k) + at * D + at4) =
+                    pack4(s.code(f[x][0]), s.code(f[x][1]), s.code(f[x][2]), s.code(f[x][3]));
+                if (at4 == 0) (row & 1 ? a.v_scale : a.k_scale)[at] = s.s;
+            } else if (row < rows) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(f[x][0], f[x][1]), hi = __floats2bfloat162_rn(f[x][2], f[x][3]);
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(row & 1 ? a.v : a.k) + at * D + at4) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             }
-            if (!live) continue;
-            // A row that holds a NaN or an infinity reads back as NaN.
-            const float s = nan || top > 3.402823466e38f ? __int_as_float(0x7fc00000) : __fdiv_rn(top, 127.0f);
-            uint32_t w = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w |= (uint32_t)(uint8_t)code_of(f[e], s) << (8 * e);
-            int8_t *dst = static_cast<int8_t *>(side ? a.v : a.k) + at * D + lane * 4;
-            *reinterpret_cast<uint32_t *>(dst) = w;
-            if (lane == 0) (side ? a.v_scale : a.k_scale)[at] = s;
-        } else if (live) {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(side ? a.v : a.k) + at * D + lane * 4;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                                                         *reinterpret_cast<const uint32_t *>(&hi));
         }
     }
 }
 
-// The sequences' rows in order: out[b][pos][head][:], zero past a length.
-// Eight elements a thread.
+// The sequences' rows in order: out[b][pos][head][:], zero past a length.  A
+// CTA takes consecutive positions of one sequence and some of its heads
+// (blockIdx.z and every gridDim.z after it); a thread 16 bytes of the cache a
+// row, of K and V, so the pages' rows are read as they lie and every index but
+// the page is a shift.
+constexpr int kReadThreads = 256;
+template <int D, bool I8>
+constexpr int read_positions() { return kReadThreads / (D * (I8 ? 1 : 2) / 16); }
+
 template <typename T, int D, bool I8>
-__global__ void cache_read_kernel(const CacheArgs a, int max_len, T *__restrict__ k_out, T *__restrict__ v_out) {
-    constexpr int kUnits = D / 8;
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CacheArgs a, int max_len, T *__restrict__ k_out,
+                                                                  T *__restrict__ v_out) {
+    constexpr int kE = I8 ? 16 : 8, kUnits = D / kE;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const size_t units = (size_t)a.batch * max_len * a.kv_heads * kUnits;
-    for (size_t g = blockIdx.x * (size_t)blockDim.x + threadIdx.x; g < units; g += (size_t)gridDim.x * blockDim.x) {
-        const int u = (int)(g % kUnits);
-        const size_t row = g / kUnits;
-        const int head = (int)(row % a.kv_heads);
-        const size_t bp = row / a.kv_heads;
-        const int b = (int)(bp / max_len), pos = (int)(bp % max_len);
-        const int p = pos < seq_len(a, b) ? page_of(a, b, pos) : -1;
-        const size_t at = (((size_t)(p < 0 ? 0 : p) * a.kv_heads + head) << a.page_shift) +
-                          (pos & ((1 << a.page_shift) - 1));
+    const int u = threadIdx.x % kUnits, b = blockIdx.y;
+    const int pos = blockIdx.x * read_positions<D, I8>() + threadIdx.x / kUnits;
+    if (pos >= max_len) return;
+    const int p = pos < seq_len(a, b) ? page_of(a, b, pos) : -1;
+    const size_t from = (((size_t)(p < 0 ? 0 : p) * a.kv_heads) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    const size_t to = ((size_t)b * max_len + pos) * a.kv_heads;
+#pragma unroll 2
+    for (int head = blockIdx.z; head < a.kv_heads; head += gridDim.z) {
+        const size_t at = from + ((size_t)head << a.page_shift);
+        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        float s[2] = {0.0f, 0.0f};
+        if (p >= 0) {
+            w[0] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.k) + at * (D * (I8 ? 1 : 2))) + u);
+            w[1] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.v) + at * (D * (I8 ? 1 : 2))) + u);
+            if (I8) {
+                s[0] = a.k_scale[at];
+                s[1] = a.v_scale[at];
+            }
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (p >= 0) {
-                if (I8) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(
-                        static_cast<const int8_t *>(side ? a.v : a.k) + at * D + u * 8);
-                    const float s = (side ? a.v_scale : a.k_scale)[at];
+            T *out = (side ? v_out : k_out) + (to + head) * D + u * kE;
+            if constexpr (I8) {
+                const uint32_t c[4] = {w[side].x, w[side].y, w[side].z, w[side].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        f[i] = __fmul_rn((float)(int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3))), s);
-                } else {
-                    Vec8<__nv_bfloat16> w;
-                    w.load(static_cast<const __nv_bfloat16 *>(side ? a.v : a.k) + at * D + u * 8);
-                    w.get(f);
+                for (int q = 0; q < 2; ++q) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = __fmul_rn((float)(int8_t)(c[2 * q + (i >> 2)] >> (8 * (i & 3))), s[side]);
+                    Vec8<T> o;
+                    o.set(f);
+                    o.store(out + 8 * q);
                 }
+            } else if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4 *>(out) = w[side];
+            } else {
+                Vec8<__nv_bfloat16> in;
+                in.w = w[side];
+                float f[8];
+                in.get(f);
+                Vec8<T> o;
+                o.set(f);
+                o.store(out);
             }
-            Vec8<T> o;
-            o.set(f);
-            o.store((side ? v_out : k_out) + g * 8);
         }
     }
 }
@@ -409,9 +501,9 @@ cudaError_t launch_dequantize_rows(const int8_t *q, const float *scale, void *ou
 
 cudaError_t launch_cache_write(const CacheArgs &a, const void *k, long long k_stride, const void *v,
                                long long v_stride, int in_bf16, cudaStream_t s) {
-    const size_t threads = (size_t)a.total * a.kv_heads * 2 * (a.head_dim / 4);
-    const int g = grid_for_units(threads, 256, 8);
-    auto run = [&](auto kern, auto *kp, auto *vp) { return launch_kernel(kern, g, 256, 0, s, a, kp, k_stride, vp, v_stride); };
+    const size_t threads = (size_t)a.total * ((2 * a.kv_heads + kRowsWarp - 1) / kRowsWarp) * 32;
+    const int g = grid_for_units(threads, 128, 32);
+    auto run = [&](auto kern, auto *kp, auto *vp) { return launch_kernel(kern, g, 128, 0, s, a, kp, k_stride, vp, v_stride); };
     if (in_bf16) {
         auto *kp = static_cast<const __nv_bfloat16 *>(k), *vp = static_cast<const __nv_bfloat16 *>(v);
         if (a.head_dim == 64) return run(cache_write_kernel<__nv_bfloat16, 64>, kp, vp);
@@ -423,9 +515,12 @@ cudaError_t launch_cache_write(const CacheArgs &a, const void *k, long long k_st
 }
 
 cudaError_t launch_cache_read(const CacheArgs &a, int max_len, void *k_out, void *v_out, int out_bf16, cudaStream_t s) {
-    const size_t units = (size_t)a.batch * max_len * a.kv_heads * (a.head_dim / 8);
-    const int g = grid_for_units(units, 256, 16);
-    auto run = [&](auto kern, auto *ko, auto *vo) { return launch_kernel(kern, g, 256, 0, s, a, max_len, ko, vo); };
+    const int positions = kReadThreads / (a.head_dim * (a.int8 ? 1 : 2) / 16);
+    const long long ctas = (long long)((max_len + positions - 1) / positions) * a.batch;
+    // Heads side by side until each SM has eight CTAs.
+    const long long want = (current_device_sms() * 8 + ctas - 1) / ctas;
+    const dim3 grid((max_len + positions - 1) / positions, a.batch, (unsigned)(want < a.kv_heads ? want : a.kv_heads));
+    auto run = [&](auto kern, auto *ko, auto *vo) { return launch_kernel(kern, grid, kReadThreads, 0, s, a, max_len, ko, vo); };
     auto dims = [&](auto *ko, auto *vo) {
         using T = std::remove_pointer_t<decltype(ko)>;
         if (a.head_dim == 64)

@@ -14,6 +14,8 @@
 // Each lane copies the words it will use itself into a ring of its own in
 // shared memory (cp.async), several stages ahead, so no thread waits for
 // another's copy and the bytes in flight cost no registers.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "mma_frag.cuh"
@@ -31,12 +33,21 @@ constexpr int kStages = 4;
 __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
 
 // GROUP: weights a scale covers (32, 64 or 128).  NT: tiles of eight input
-// rows.  RB: tiles of sixteen outputs a warp.
-template <int GROUP, int NT, int RB, bool XI8>
-__global__ void __launch_bounds__(kThreads) w4_kernel(const W4Launch L, int wk) {
+// rows.  RB: tiles of sixteen outputs a warp.  FULL: k is a multiple of the
+// stage's 128, so no stage ends early.
+//
+// What the loop costs is instructions (a weight is half a byte: at HBM's rate an
+// SM has a dozen issue slots for a warp's 64 weights), so rows past the ends
+// are clamped instead of masked, pointers advance, and for 8-bit inputs the zero
+// point comes off the group's whole-number sum (sum x (128 + q) - (128 + z)
+// sum x, exact below 2^24) instead of every weight.
+template <int GROUP, int NT, int RB, bool XI8, bool FULL>
+__global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) w4_kernel(const W4Launch L, int wk) {
     constexpr int V = GROUP / 32;            // words a lane, row and group
     constexpr int kGroups = kStageK / GROUP; // groups in a stage
     constexpr int kRowBytes = 16;            // a lane's bytes of one row in a stage
+    constexpr int kXB = XI8 ? 1 : 2;         // bytes of an input
+    constexpr bool kEarlyX = NT * kXB <= 2;  // X one stage ahead: 8 NT kXB registers
     extern __shared__ __align__(16) unsigned char smem[];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -47,39 +58,45 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Launch L, int wk) 
     const int m0 = blockIdx.y * 8 * NT;
     const int stages = (L.k + kStageK - 1) / kStageK;
     const int st0 = (int)((long long)stages * part / wk), st1 = (int)((long long)stages * (part + 1) / wk);
-    const size_t row_bytes = (size_t)L.k / 2;
+    const int left = L.k - st0 * kStageK;         // weights from this share's start to the row's end
 
-    // This lane's rows: g and g + 8 of each tile (rows past n read the last one).
-    const uint8_t *wrow[2 * RB];
+    // This lane's rows: g and g + 8 of each tile (rows past n repeat the last one),
+    // at its bytes of the first group; X's row g of each tile (likewise).
+    const uint8_t *wp[2 * RB];
     int nrow[2 * RB];
 #pragma unroll
     for (int i = 0; i < 2 * RB; ++i) {
         nrow[i] = min(n0 + (i >> 1) * 16 + (i & 1) * 8 + g, L.n - 1);
-        wrow[i] = L.w + (size_t)nrow[i] * row_bytes;
+        wp[i] = L.w + (size_t)nrow[i] * (L.k / 2) + st0 * (kStageK / 2) + j * 4 * V;
     }
-    unsigned char *ring = smem + (size_t)tid * kRowBytes;   // [stage][row][thread], 16 bytes each
-    auto slot = [&](int st, int i) { return ring + (size_t)((st % kStages) * 2 * RB + i) * kThreads * kRowBytes; };
-    auto copy = [&](int st) {
+    const char *xp[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        xp[t] = static_cast<const char *>(L.x) + ((size_t)min(m0 + t * 8 + g, L.rows - 1) * L.k + st0 * kStageK + j * 8 * V) * kXB;
+
+    unsigned char *const ring = smem + (size_t)tid * kRowBytes;   // [stage][row][thread], 16 bytes each
+    const uint32_t ring32 = ptx::smem_u32(ring);
+    const auto copy = [&](int st, int s) {   // stage st into place s of the ring
         if (st < st1) {
 #pragma unroll
             for (int i = 0; i < 2 * RB; ++i) {
-                const uint32_t dst = ptx::smem_u32(slot(st, i));
+                const uint32_t dst = ring32 + (s * 2 * RB + i) * kThreads * kRowBytes;
 #pragma unroll
                 for (int gi = 0; gi < kGroups; ++gi) {
-                    const int k = st * kStageK + gi * GROUP;
-                    // bytes [k / 2 + j * 4 V, + 4 V) of the row, in order of groups in the ring
-                    const uint8_t *src = wrow[i] + (size_t)(k < L.k ? k : 0) / 2 + j * 4 * V;
-                    const uint32_t bytes = k < L.k ? 4 * V : 0;
+                    const bool in = FULL || (st - st0) * kStageK + gi * GROUP < left;
+                    const uint8_t *src = in ? wp[i] + gi * (GROUP / 2) : L.w;
+                    const uint32_t bytes = in ? 4 * V : 0;
                     if constexpr (V == 4) ptx::cp_async_16(dst, src, bytes);
                     else if constexpr (V == 2) ptx::cp_async_8(dst + gi * 8, src, bytes);
                     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + gi * 4), "l"(src), "r"(bytes) : "memory");
                 }
+                wp[i] += kStageK / 2;
             }
         }
         ptx::cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) copy(st0 + s);
+    for (int s = 0; s < kStages - 1; ++s) copy(st0 + s, s);
 
     float total[RB][NT][4];
 #pragma unroll
@@ -89,81 +106,141 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Launch L, int wk) 
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[r][t][i] = 0.0f;
 
-    const __nv_bfloat16 *scales = static_cast<const __nv_bfloat16 *>(L.scales);
-    for (int st = st0; st < st1; ++st) {
-        copy(st + kStages - 1);
-        float sc[kGroups][2 * RB];
-        uint32_t zp[kGroups][2 * RB];
-#pragma unroll
-        for (int gi = 0; gi < kGroups; ++gi) {
-            const int k = st * kStageK + gi * GROUP;
-            const size_t at = (size_t)(k < L.k ? k / GROUP : 0) * L.n;
-#pragma unroll
-            for (int i = 0; i < 2 * RB; ++i) {
-                sc[gi][i] = k < L.k ? __bfloat162float(scales[at + nrow[i]]) : 0.0f;
-                zp[gi][i] = 0x43004300u | (L.zeros ? (L.zeros[at + nrow[i]] & 15u) * 0x00010001u : 0x00080008u);
-            }
-        }
-        ptx::cp_async_wait<kStages - 1>();
-        uint32_t wv[2 * RB][4];
+    // The groups' scales and zero points: lane j of a row's four holds those of
+    // the stage's group j, some stages ahead and as they were loaded (arithmetic
+    // on them here would wait for the loads), and the row's lanes get a group's by
+    // a shuffle.
+    constexpr int kAhead = RB == 1 ? 4 : 2;
+    static_assert(kStages % kAhead == 0, "the rings turn together");
+    struct Scale { uint16_t s; uint8_t z; };
+    Scale sz[kAhead][2 * RB];
+    const uint16_t *sp = static_cast<const uint16_t *>(L.scales);
+    const uint8_t *zpt = L.zeros;
+    const int groups = L.k / GROUP;
+    const auto load_scales = [&](int st, Scale (&to)[2 * RB]) {
+        if (st >= st1) return;
+        const int gr = st * kGroups + j % kGroups;
+        const size_t at = (size_t)(FULL || gr < groups ? gr : groups - 1) * L.n;
 #pragma unroll
         for (int i = 0; i < 2 * RB; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(slot(st, i));
-            wv[i][0] = w.x; wv[i][1] = w.y; wv[i][2] = w.z; wv[i][3] = w.w;
+            to[i].s = __ldg(sp + at + nrow[i]);
+            if (zpt) to[i].z = __ldg(zpt + at + nrow[i]);
         }
+    };
 #pragma unroll
-        for (int gi = 0; gi < kGroups; ++gi) {
-            const int k = st * kStageK + gi * GROUP;
-            if (k >= L.k) break;
-            float acc[RB][NT][4];
+    for (int s = 0; s < kAhead; ++s) load_scales(st0 + s, sz[s]);
+
+    using XWord = typename std::conditional<XI8, uint2, uint4>::type;   // eight consecutive inputs
+    XWord xs[kEarlyX ? NT : 1][4];
+    const auto load_x = [&](int t, int gi, int v) -> XWord {   // word v of group gi of xp's stage
+        return __ldg(reinterpret_cast<const XWord *>(xp[t] + (gi * GROUP + v * 8) * kXB));
+    };
+    if constexpr (kEarlyX) {
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
+        for (int gi = 0; gi < kGroups; ++gi)
+            if (st0 < st1 && (FULL || gi * GROUP < left)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                // X: eight consecutive inputs of row g of each tile
-                uint32_t x[NT][4];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int m = m0 + t * 8 + g;
-                    const size_t at = (size_t)m * L.k + k + j * 8 * V + v * 8;
-                    if constexpr (XI8) {
-                        const uint2 w = m < L.rows ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const int8_t *>(L.x) + at)) : make_uint2(0, 0);
-                        x[t][0] = frag::i8_pair(__byte_perm(w.x, 0, 0x4140));
-                        x[t][1] = frag::i8_pair(__byte_perm(w.x, 0, 0x4342));
-                        x[t][2] = frag::i8_pair(__byte_perm(w.y, 0, 0x4140));
-                        x[t][3] = frag::i8_pair(__byte_perm(w.y, 0, 0x4342));
-                    } else {
-                        const uint4 w = m < L.rows ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(L.x) + at)) : make_uint4(0, 0, 0, 0);
-                        x[t][0] = w.x; x[t][1] = w.y; x[t][2] = w.z; x[t][3] = w.w;
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < RB; ++r) {
-                    uint32_t a[2][4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w = wv[2 * r + i][gi * V + v];
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            a[i][p] = frag::sub_bf16x2(((w >> (4 * p)) & 0x000f000fu) | 0x43004300u, zp[gi][2 * r + i]);
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        frag::mma(acc[r][t], a[0][0], a[1][0], a[0][1], a[1][1], x[t][0], x[t][1]);
-                        frag::mma(acc[r][t], a[0][2], a[1][2], a[0][3], a[1][3], x[t][2], x[t][3]);
-                    }
-                }
+                    for (int v = 0; v < V; ++v) xs[t][gi * V + v] = load_x(t, gi, v);
             }
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
+        for (int t = 0; t < NT; ++t) xp[t] += kStageK * kXB;
+    }
+    for (int sb = st0; sb < st1; sb += kStages) {
+#pragma unroll
+        for (int su = 0; su < kStages; ++su) {
+            const int st = sb + su;
+            if (st >= st1) break;
+            copy(st + kStages - 1, (su + kStages - 1) % kStages);
+            ptx::cp_async_wait<kStages - 1>();
+            uint32_t wv[2 * RB][4];
+#pragma unroll
+            for (int i = 0; i < 2 * RB; ++i) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(ring + (su * 2 * RB + i) * kThreads * kRowBytes);
+                wv[i][0] = w.x; wv[i][1] = w.y; wv[i][2] = w.z; wv[i][3] = w.w;
+            }
+            const int past = (st - st0) * kStageK;   // weights of the share before this stage
+#pragma unroll
+            for (int gi = 0; gi < kGroups; ++gi) {
+                if (!FULL && past + gi * GROUP >= left) break;
+                float acc[RB][NT][4], sx[NT][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) total[r][t][i] = fmaf(acc[r][t][i], sc[gi][2 * r + (i >> 1)], total[r][t][i]);
+                    for (int i = 0; i < 4; ++i) {
+                        sx[t][i] = 0.0f;
+#pragma unroll
+                        for (int r = 0; r < RB; ++r) acc[r][t][i] = 0.0f;
+                    }
+                uint32_t zp[2 * RB];   // 128 + z, a pair of bf16
+                float sc[2 * RB];
+#pragma unroll
+                for (int i = 0; i < 2 * RB; ++i) {
+                    const Scale &o = sz[su % kAhead][i];
+                    const uint32_t mine = (uint32_t)o.s << 16 | (zpt ? o.z & 15u : 8u);
+                    const uint32_t w = kGroups == 1 ? mine : __shfl_sync(~0u, mine, (lane & ~3) | gi);
+                    zp[i] = __byte_perm(w, 0x43u, 0x4040);
+                    sc[i] = __uint_as_float(w & 0xffff0000u);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    uint32_t x[NT][4];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        XWord w;
+                        if constexpr (kEarlyX) {
+                            w = xs[t][gi * V + v];
+                            if (st + 1 < st1 && (FULL || past + kStageK + gi * GROUP < left)) xs[t][gi * V + v] = load_x(t, gi, v);
+                        } else {
+                            w = load_x(t, gi, v);
+                        }
+                        if constexpr (XI8) {
+                            x[t][0] = frag::i8_pair(__byte_perm(w.x, 0, 0x4140));
+                            x[t][1] = frag::i8_pair(__byte_perm(w.x, 0, 0x4342));
+                            x[t][2] = frag::i8_pair(__byte_perm(w.y, 0, 0x4140));
+                            x[t][3] = frag::i8_pair(__byte_perm(w.y, 0, 0x4342));
+                            // a row of ones: the group's sum of x in every output's place
+                            constexpr uint32_t kOnes = 0x3f803f80u;
+                            frag::mma(sx[t], kOnes, kOnes, kOnes, kOnes, x[t][0], x[t][1]);
+                            frag::mma(sx[t], kOnes, kOnes, kOnes, kOnes, x[t][2], x[t][3]);
+                        } else {
+                            x[t][0] = w.x; x[t][1] = w.y; x[t][2] = w.z; x[t][3] = w.w;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t w = wv[2 * r + i][gi * V + v];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                a[i][p] = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+                                if constexpr (!XI8) a[i][p] = frag::sub_bf16x2(a[i][p], zp[2 * r + i]);
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            frag::mma(acc[r][t], a[0][0], a[1][0], a[0][1], a[1][1], x[t][0], x[t][1]);
+                            frag::mma(acc[r][t], a[0][2], a[1][2], a[0][3], a[1][3], x[t][2], x[t][3]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (XI8)
+                                acc[r][t][i] = fmaf(-__uint_as_float(zp[2 * r + (i >> 1)] & 0xffff0000u), sx[t][i], acc[r][t][i]);
+                            total[r][t][i] = fmaf(acc[r][t][i], sc[2 * r + (i >> 1)], total[r][t][i]);
+                        }
+            }
+            load_scales(st + kAhead, sz[su % kAhead]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xp[t] += kStageK * kXB;
         }
     }
     ptx::cp_async_wait<0>();
@@ -196,18 +273,20 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Launch L, int wk) 
     }
 }
 
-template <int GROUP, int NT, int RB, bool XI8>
+template <int GROUP, int NT, int RB, bool XI8, bool FULL>
 cudaError_t launch_w4_one(const W4Launch &L, cudaStream_t s) {
     const int ring = kStages * 2 * RB * kThreads * 16;
     const int join = kWarps * 8 * NT * (16 * RB + 1) * 4;
     const int smem = ring > join ? ring : join;
-    // Warps along k until the outputs' tiles times that give each SM 16 warps.
+    // Warps side by side along k: as few as give every SM one and a half CTAs,
+    // since a CTA's warps along n share X (its bytes are 4 rows / (outputs of the
+    // CTA) of the weights').
     const int tiles = (L.n + 16 * RB - 1) / (16 * RB), stages = (L.k + kStageK - 1) / kStageK;
     int wk = 1;
-    while (wk < kWarps && tiles * wk < current_device_sms() * 16 && wk * 2 <= stages) wk *= 2;
+    while (wk < kWarps && tiles * wk < current_device_sms() * 12 && wk * 2 <= stages) wk *= 2;
     const int per = kWarps / wk;
     const dim3 grid((tiles + per - 1) / per, (L.rows + 8 * NT - 1) / (8 * NT));
-    auto kern = w4_kernel<GROUP, NT, RB, XI8>;
+    auto kern = w4_kernel<GROUP, NT, RB, XI8, FULL>;
     cudaError_t e = set_max_dyn_smem(kern, smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(kern, grid, kThreads, smem, s, L, wk);
@@ -215,9 +294,14 @@ cudaError_t launch_w4_one(const W4Launch &L, cudaStream_t s) {
 
 template <int GROUP, bool XI8>
 cudaError_t launch_w4_rows(const W4Launch &L, cudaStream_t s) {
-    if (L.rows <= 8) return launch_w4_one<GROUP, 1, 1, XI8>(L, s);
-    if (L.rows <= 16) return launch_w4_one<GROUP, 2, 2, XI8>(L, s);
-    return launch_w4_one<GROUP, 4, 2, XI8>(L, s);
+    const bool full = L.k % kStageK == 0;
+    const auto run = [&](auto nt, auto rb) {
+        return full ? launch_w4_one<GROUP, nt, rb, XI8, true>(L, s) : launch_w4_one<GROUP, nt, rb, XI8, false>(L, s);
+    };
+    using std::integral_constant;
+    if (L.rows <= 8) return run(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (L.rows <= 16) return run(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    return run(integral_constant<int, 4>{}, integral_constant<int, 2>{});
 }
 
 // One-time weight transform: symmetric codes q in 1..15 (zero point 8) with

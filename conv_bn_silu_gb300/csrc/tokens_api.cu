@@ -120,6 +120,8 @@ cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_le
     CBS_TRY(cache_args(c, s, false, &a));
     CBS_TRY(float_type(out_prec, "output"));
     if (max_len < 0) return fail(CBS_ERR_INVALID_ARG, "max_len %d", max_len);
+    if (s->batch > kGridMax || c->kv_heads > kGridMax)
+        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
     if (s->batch == 0 || max_len == 0) return CBS_OK;
     CBS_TRY(need(k_out, "k_out"));
     CBS_TRY(need(v_out, "v_out"));
