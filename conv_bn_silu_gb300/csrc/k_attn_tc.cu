@@ -29,32 +29,77 @@ namespace {
 
 constexpr int kHalf = 128, kRows = kAttnChunkRows, kTile = kAttnChunkKeys;   // rows of a half and of a CTA; keys of a tile
 static_assert(kRows == 2 * kHalf, "two halves");
-constexpr int kStages = 2;
+constexpr int kCols = kTile / 2;              // keys of a tile a softmax thread takes
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 template <int D, bool I8>
 struct Chunk {
-    // Warps 0-3: MMA issue, TMA, and two that check values; 4-11: softmax of
-    // the halves; 12-15 (int8): converters.
-    static constexpr int kThreads = I8 ? 512 : 384;
+    // Warp 0: MMA issue; 1-3: TMA and two that check values (bf16), or
+    // converters (int8); 4-19: softmax, eight warps a half (two threads a row, 64
+    // keys of the tile each).
+    static constexpr int kThreads = 640;
+    static constexpr int kConverters = 3;
     static constexpr int kPanel = kTile * 128;                 // 64 dimensions of 128 rows
     static constexpr int kOperand = (D / 64) * kPanel;         // one Q half, K tile or V tile
-    static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + kStages * kOperand;
-    static constexpr int kScale = kV + kStages * kOperand;     // [K, V][stage][128] floats
-    static constexpr int kBars = kScale + (I8 ? 2 * kStages * kTile * 4 : 0);
-    // q_full[2], k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2],
-    // s_full[2], p_ready[2], pv_done[2], drain; then the TMEM address and flags.
-    static constexpr int kNumBars = 19;
-    static constexpr int kSmem = kBars + kNumBars * 8 + 16 + 1024;   // 1 KB to align the operands
+    // A ring of K and V tiles in turn (K of tile i is its item 2 i, V 2 i + 1): as
+    // deep as shared memory allows, since a tile takes about a microsecond to
+    // arrive and as long to use.
+    static constexpr int kSlots = D == 64 ? 8 : I8 ? 4 : 5;
+    static constexpr int kQ = 0, kRing = 2 * kOperand;
+    // int8: the scales of four tiles' keys, [K, V][tile % 4][128] floats.  Tile i's
+    // are written once its V tile's slot is free, when V of tile i - kSlots / 2 (at
+    // least i - 4) has been used, and so have that tile's scales.
+    static constexpr int kScaleTiles = 4;
+    static constexpr int kScale = kRing + kSlots * kOperand;
+    static constexpr int kShare = kScale + (I8 ? 2 * kScaleTiles * kTile * 4 : 0);   // a row's threads exchange here
+    static constexpr int kBars = kShare + 2 * kRows * 4;
+    // V tiles checked but not yet waited for: while the MMAs of tile i wait, items
+    // up to 2 i + kSlots have had their slots, V of tile i + (kSlots - 1) / 2 the last.
+    static constexpr int kReady = 4;
+    static_assert((kSlots - 1) / 2 < kReady, "a check's turn comes after the last one's was seen");
+    // q_full[2], s_full[2], p_ready[2], pv_done[2], drain, ready[], full[], empty[];
+    // then the TMEM address and flags.
+    static constexpr int kNumBars = 9 + kReady + 2 * kSlots;
+    static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+    static_assert(kSmem <= kMaxDynSmem, "ring");
+    static_assert(!I8 || (kSlots % 2 == 0 && kSlots / 2 <= kScaleTiles), "scales are free when V's slot is");
 };
 
-// D[tmem] (+)= A[tmem] B[smem desc], bf16 operands.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// An item's slot in the ring, and the parity of its turn there.
+template <int kSlots>
+struct Turn {
+    int slot;
+    uint32_t parity;
+    __device__ __forceinline__ explicit Turn(int item) : slot(item % kSlots), parity((item / kSlots) & 1) {}
+};
+
+// The MMA warp's instructions.  All its lanes run the loop around them, so that
+// addresses and descriptors stay warp-uniform values, and one (`lead`) issues.
+// D[tmem] (+)= A[smem] B[smem] and D[tmem] (+)= A[tmem] B[smem], bf16 operands.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
@@ -91,13 +136,91 @@ __device__ __forceinline__ Span span_of(const AttnLaunch &L, const Rows &s, int 
     return Span{a.lo, b.hi, b.lo, a.hi};
 }
 
+// Pairs of floats in one register pair (two lanes of one instruction).
+struct F2 { unsigned long long v; };
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+
+// A thread's pass over its kCols of a row's scores: t = s * scale - ref (ks: a scale a key,
+// for 8-bit keys), p = 2^t (times vs, for 8-bit values) as bf16 pairs, the
+// largest t and the sum of 2^t.  MASK: columns outside [first, end) are not
+// seen.  Rounding p to bf16 moves each term by at most 2^-8 of itself, either
+// way, as the output's own rounding does.
+template <bool I8, bool MASK>
+__device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref, const float *ks, const float *vs, int first,
+                                          int end, uint32_t (&p)[kCols / 2], float &top, float &sum) {
+    const F2 scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+    F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+    float tops[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int q = 0; q < kCols / 32; ++q) {
+        uint32_t v[32];
+        tmem_ld32(taddr + 32 * q, v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            F2 k2[2] = {scale2, scale2}, w2[2];
+            if constexpr (I8) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + e), v4 = *reinterpret_cast<const float4 *>(vs + 32 * q + e);
+                k2[0] = pair(k4.x, k4.y); k2[1] = pair(k4.z, k4.w);
+                w2[0] = pair(v4.x, v4.y); w2[1] = pair(v4.z, v4.w);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float2 t = split(fma2(pair(__uint_as_float(v[e + 2 * x]), __uint_as_float(v[e + 2 * x + 1])), k2[x], ref2));
+                if constexpr (MASK) {
+                    const int col = 32 * q + e + 2 * x;
+                    if (col < first || col >= end) t.x = -INFINITY;
+                    if (col + 1 < first || col + 1 >= end) t.y = -INFINITY;
+                }
+                tops[x] = fmaxf(tops[x], fmaxf(t.x, t.y));
+                F2 pr = pair(frag::ex2(t.x), frag::ex2(t.y));
+                acc[x] = add2(acc[x], pr);
+                if constexpr (I8) pr = mul2(pr, w2[x]);
+                float2 y = split(pr);
+                if constexpr (I8 && MASK) {   // a hidden key's scale may be anything
+                    if (t.x == -INFINITY) y.x = 0.0f;
+                    if (t.y == -INFINITY) y.y = 0.0f;
+                }
+                p[16 * q + (e >> 1) + x] = frag::pack_bf16(y.x, y.y);
+            }
+        }
+    }
+    top = fmaxf(tops[0], tops[1]);
+    const float2 a = split(add2(acc[0], acc[1]));
+    sum = a.x + a.y;
+}
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(Chunk<D, I8>::kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnLaunch L) {
     using C = Chunk<D, I8>;
-    extern __shared__ unsigned char smem_raw[];
-    const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-    unsigned char *const sgen = smem_raw + (sbase - ptx::smem_u32(smem_raw));
+    using T = Turn<C::kSlots>;
+    extern __shared__ __align__(1024) unsigned char sgen[];   // the only shared memory: it starts at a multiple of 1 KB
+    const uint32_t sbase = ptx::smem_u32(sgen);
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -120,29 +243,30 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
     const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
     const auto q_full = [&](int h) { return bar(h); };
-    const auto k_full = [&](int s) { return bar(2 + s); };
-    const auto k_empty = [&](int s) { return bar(4 + s); };
-    const auto v_full = [&](int s) { return bar(6 + s); };
-    const auto v_ready = [&](int s) { return bar(8 + s); };
-    const auto v_empty = [&](int s) { return bar(10 + s); };
-    const auto s_full = [&](int h) { return bar(12 + h); };
-    const auto p_ready = [&](int h) { return bar(14 + h); };
-    const auto pv_done = [&](int h) { return bar(16 + h); };
-    const uint32_t drain = bar(18);
+    const auto s_full = [&](int h) { return bar(2 + h); };
+    const auto p_ready = [&](int h) { return bar(4 + h); };
+    const auto pv_done = [&](int h) { return bar(6 + h); };
+    const uint32_t drain = bar(8);
+    // bf16: tile i's V has been checked.  Its own turns, by tile: a slot of the
+    // ring holds K and V alternately, so the ring's parities do not count V's.
+    const auto ready = [&](int i) { return bar(9 + i % C::kReady); };
+    const auto full = [&](int s) { return bar(9 + C::kReady + s); };                // an item has arrived
+    const auto empty = [&](int s) { return bar(9 + C::kReady + C::kSlots + s); };   // and been used
+    const auto slot_at = [&](int s) { return C::kRing + s * C::kOperand; };
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(sgen + C::kBars + 8 * C::kNumBars);
     // words[0]: TMEM address; [1]: a wait ran out; [2]: a value is not finite; [3]: the join's flag
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(q_full(i), 4);
-            ptx::mbar_init(k_full(i), I8 ? 4 : 1);
-            ptx::mbar_init(k_empty(i), 1);
-            ptx::mbar_init(v_full(i), I8 ? 4 : 1);
-            ptx::mbar_init(v_ready(i), 2);
-            ptx::mbar_init(v_empty(i), 1);
+            ptx::mbar_init(q_full(i), 8);
             ptx::mbar_init(s_full(i), 1);
-            ptx::mbar_init(p_ready(i), 4);
+            ptx::mbar_init(p_ready(i), 8);
             ptx::mbar_init(pv_done(i), 1);
+        }
+        for (int i = 0; i < C::kReady; ++i) ptx::mbar_init(ready(i), 2);
+        for (int s = 0; s < C::kSlots; ++s) {
+            ptx::mbar_init(full(s), I8 ? C::kConverters : 1);
+            ptx::mbar_init(empty(s), 1);
         }
         ptx::mbar_init(drain, 1);
         ptx::fence_mbar_init();
@@ -171,221 +295,274 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
     if (warp == 0) {
         // ------------------------------------------------------- MMA issue
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((kHalf >> 4) << 24);
             constexpr uint32_t idesc_s = idesc0 | ((kTile >> 3) << 17);
             constexpr uint32_t idesc_o = idesc0 | ((D >> 3) << 17) | (1u << 16);   // V: dimensions contiguous
-            const auto scores = [&](int h, int st) {
+            const uint32_t lead = elect_one();
+            // Operand descriptors: everything but the slot and the step along k.
+            const uint64_t d_q = ptx::smem_desc(sbase + C::kQ, 16, 1024, 2), d_k = ptx::smem_desc(sbase + C::kRing, 16, 1024, 2);
+            const uint64_t d_v = ptx::smem_desc(sbase + C::kRing, C::kPanel, 1024, 2);
+            constexpr uint32_t kStep = C::kOperand >> 4;   // descriptors count 16 bytes
+            const auto scores = [&](int h, int slot) {
+                const uint64_t q = d_q + h * kStep, k = d_k + (uint32_t)slot * kStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * C::kPanel + (k & 3) * 32;
-                    ptx::mma_f16(t_s(h), ptx::smem_desc(sbase + C::kQ + h * C::kOperand + off, 16, 1024, 2),
-                                 ptx::smem_desc(sbase + C::kK + st * C::kOperand + off, 16, 1024, 2), idesc_s, k > 0);
+                for (int x = 0; x < D / 16; ++x) {
+                    constexpr uint32_t kPanelStep = C::kPanel >> 4;
+                    const uint32_t off = (x >> 2) * kPanelStep + (x & 3) * 2;
+                    mma_ss(lead, t_s(h), q + off, k + off, idesc_s, x > 0);
                 }
-                ptx::mma_commit(s_full(h));
+                mma_commit(lead, s_full(h));
             };
-            const auto output = [&](int h, int st, bool more) {
+            const auto output = [&](int h, int slot, bool more) {
+                const uint64_t v = d_v + (uint32_t)slot * kStep;
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_f16_ta(t_o(h), t_s(h) + 8 * k,
-                               ptx::smem_desc(sbase + C::kV + st * C::kOperand + k * 2048, C::kPanel, 1024, 2), idesc_o,
-                               more || k > 0);
-                ptx::mma_commit(pv_done(h));
+                for (int x = 0; x < kTile / 16; ++x) mma_ts(lead, t_o(h), t_s(h) + 8 * x, v + 128u * x, idesc_o, more || x > 0);
+                mma_commit(lead, pv_done(h));
             };
-            bool ok = wait(k_full(0), 0);
+            bool ok = wait(full(0), 0);
             for (int h = 0; ok && h < halves; ++h) {
                 ok = wait(q_full(h), 0);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 scores(h, 0);
             }
-            if (ok) ptx::mma_commit(k_empty(0));
-            for (int i = 0; ok && i < n && !lost(); ++i) {
-                const int st = i & 1, nx = (i + 1) & 1;
-                ok = wait(I8 ? v_full(st) : v_ready(st), (i >> 1) & 1);
+            if (ok) mma_commit(lead, empty(0));
+            int v_slot = 1, k_slot = 2 % C::kSlots;
+            uint32_t v_par = 0, k_par = 0;   // items 2 i + 1 and 2 i + 2
+            const auto advance = [](int &slot, uint32_t &par) {
+                slot += 2;
+                if (slot >= C::kSlots) slot -= C::kSlots, par ^= 1;
+            };
+            for (int i = 0; ok && i < n; ++i) {
+                ok = (I8 ? wait(full(v_slot), v_par) : wait(ready(i), (i / C::kReady) & 1)) && !lost();
+                ok = __all_sync(~0u, ok);
                 for (int h = 0; ok && h < halves; ++h) {
                     ok = wait(p_ready(h), i & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    output(h, st, i > 0);
-                    if (h == halves - 1) ptx::mma_commit(v_empty(st));
+                    output(h, v_slot, i > 0);
+                    if (h == halves - 1) mma_commit(lead, empty(v_slot));
                     if (i + 1 < n) {
-                        if (h == 0) ok = wait(k_full(nx), ((i + 1) >> 1) & 1);
+                        if (h == 0) ok = wait(full(k_slot), k_par);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        scores(h, nx);
-                        if (h == halves - 1) ptx::mma_commit(k_empty(nx));
+                        scores(h, k_slot);
+                        if (h == halves - 1) mma_commit(lead, empty(k_slot));
                     }
                 }
+                advance(v_slot, v_par);
+                advance(k_slot, k_par);
             }
-            ptx::mma_commit(drain);   // nothing leaves while an MMA reads shared memory
+            __syncwarp();
+            mma_commit(lead, drain);   // nothing leaves while an MMA reads shared memory
             if (!ptx::mbar_wait_bounded(drain, 0, kWaitNs)) atomicOr(c.status, kStatusTimeout);
         }
     } else if (warp == 1 && !I8) {
         // ------------------------------------------------------- TMA
         const int page = 1 << c.page_shift, box = min(page, kTile), boxes = kTile / box;
         const int none = c.num_pages * c.kv_heads << c.page_shift;   // a row past the pool: reads as zeros
-        const int pages = (rs.len + page - 1) >> c.page_shift;
-        int done = 0;
+        // Lane x < boxes: the page of tile i's position x * box as loaded (two
+        // tiles ahead), and from it the pool's row.
+        const auto needed = [&](int i) { return i < n && lane < boxes && key0 + i * kTile + lane * box < rs.len; };
+        const auto page_entry = [&](int i) -> int {
+            return needed(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + lane * box) >> c.page_shift)) : 0;
+        };
+        int entry = page_entry(0), entry_next = page_entry(1), done = 0;
         for (int i = 0; i < n; ++i) {
-            const int st = i & 1;
             int row = none;
-            const int pos = key0 + i * kTile + lane * box;
-            if (lane < boxes && (pos >> c.page_shift) < pages) {
-                const int p = page_of(c, b, pos);
-                if (p >= 0) row = ((p * c.kv_heads + head) << c.page_shift) + (pos & (page - 1));
+            if (needed(i)) {
+                if ((unsigned)entry < (unsigned)c.num_pages)
+                    row = ((entry * c.kv_heads + head) << c.page_shift) + ((key0 + i * kTile + lane * box) & (page - 1));
+                else
+                    atomicOr(c.status, kStatusBadIndex);
             }
+            entry = entry_next;
+            entry_next = page_entry(i + 2);
             bool ok = true;
 #pragma unroll
             for (int side = 0; side < 2 && ok; ++side) {
+                const T x(2 * i + side);
                 if (lane == 0) {
-                    ok = wait(side ? v_empty(st) : k_empty(st), ((i >> 1) & 1) ^ 1) && !lost();
-                    if (ok) ptx::mbar_arrive_expect_tx(side ? v_full(st) : k_full(st), C::kOperand);
+                    ok = wait(empty(x.slot), x.parity ^ 1) && !lost();
+                    if (ok) ptx::mbar_arrive_expect_tx(full(x.slot), C::kOperand);
                 }
                 ok = __shfl_sync(~0u, (int)ok, 0) != 0;
                 if (ok && lane < boxes) {
-                    const uint32_t dst = sbase + (side ? C::kV : C::kK) + st * C::kOperand + lane * box * 128;
+                    const uint32_t dst = sbase + slot_at(x.slot) + lane * box * 128;
 #pragma unroll
                     for (int p = 0; p < D / 64; ++p)
-                        ptx::tma_load_2d(dst + p * C::kPanel, side ? &tm_v : &tm_k, side ? v_full(st) : k_full(st), p * 64, row);
+                        ptx::tma_load_2d(dst + p * C::kPanel, side ? &tm_v : &tm_k, full(x.slot), p * 64, row);
                 }
                 if (ok) ++done;
             }
             if (!ok) break;
         }
         if (lane == 0 && lost()) {   // the copies in flight land before the CTA leaves
-            for (int x = max(0, done - 4); x < done; ++x) {
-                const int i = x >> 1;
-                ptx::mbar_wait_bounded((x & 1) ? v_full(i & 1) : k_full(i & 1), (i >> 1) & 1, kWaitNs);
-            }
+            for (int x = max(0, done - C::kSlots); x < done; ++x) ptx::mbar_wait_bounded(full(T(x).slot), T(x).parity, kWaitNs);
         }
-    } else if (warp == 2 || (warp == 3 && !I8)) {
+    } else if (!I8 && warp < 4) {
         // ------------------------- values some row must not see (bf16 cache)
-        if (!I8) {
-            for (int i = 0; i < n; ++i) {
-                const int st = i & 1, pos = key0 + i * kTile;
-                if (!wait(v_full(st), (i >> 1) & 1)) break;
-                if (pos < all.all_lo || pos + kTile > all.all_hi) {
-                    // Rows that nobody sees become zeros (a page's slots past the
-                    // length may hold anything, and 0 x NaN is NaN); a value that is
-                    // not finite among the others sends the CTA down the slow path.
-                    unsigned char *v = sgen + C::kV + st * C::kOperand;
-                    bool bad = false;
-                    for (int u = (warp - 2) * 32 + lane; u < C::kOperand / 16; u += 64) {
-                        const int key = pos + ((u >> 3) & (kTile - 1));
-                        uint4 *p = reinterpret_cast<uint4 *>(v + u * 16);
-                        if (key < all.lo || key >= all.hi) {
-                            *p = make_uint4(0, 0, 0, 0);
-                        } else {
-                            const uint4 w = *p;
-                            const auto odd = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
-                            bad |= odd(w.x) || odd(w.y) || odd(w.z) || odd(w.w);
-                        }
+        for (int i = 0; i < n; ++i) {
+            const T x(2 * i + 1);
+            const int pos = key0 + i * kTile;
+            if (!wait(full(x.slot), x.parity)) break;
+            if (pos < all.all_lo || pos + kTile > all.all_hi) {
+                // Rows that nobody sees become zeros (a page's slots past the
+                // length may hold anything, and 0 x NaN is NaN); a value that is
+                // not finite among the others sends the CTA down the slow path.
+                unsigned char *v = sgen + slot_at(x.slot);
+                bool bad = false;
+                for (int u = (warp - 2) * 32 + lane; u < C::kOperand / 16; u += 64) {
+                    const int key = pos + ((u >> 3) & (kTile - 1));
+                    uint4 *p = reinterpret_cast<uint4 *>(v + u * 16);
+                    if (key < all.lo || key >= all.hi) {
+                        *p = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint4 w = *p;
+                        const auto odd = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+                        bad |= odd(w.x) || odd(w.y) || odd(w.z) || odd(w.w);
                     }
-                    if (bad) words[2] = 1;
-                    ptx::fence_proxy_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(v_ready(st));
+                if (bad) words[2] = 1;
+                ptx::fence_proxy_async_smem();
             }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ready(i));
         }
-    } else if (I8 && warp >= 12) {
+    } else if (I8 && warp < 4) {
         // ------------------------------------------------------- converters
         if constexpr (I8) {
-            constexpr int kU = D / 16;                  // 16-code units of a row
-            constexpr int kPer = kTile * kU / 128;      // units a thread
-            const int ct = tid - 384;
+            // A tile is four pieces: 64 keys' rows of K, the other 64, then V's.
+            // Codes are loaded two pieces ahead.
+            constexpr int kU = D / 16;                       // 16-code units of a row
+            constexpr int kRowsOnce = 32 / kU;               // rows a warp takes at once (of one page: 4 or 8)
+            constexpr int kPiece = kTile / 2, kPer = (kPiece / kRowsOnce + C::kConverters - 1) / C::kConverters;
+            const int cw = warp - 1, u = lane % kU, sub = lane / kU;
             uint4 raw[2][kPer];
-            float sc[2];
-            // Tile i's codes and scales (zeros for positions nobody sees).
-            const auto load = [&](int i, int side) {
+            float sc[2][2] = {};
+            // Lane x < 8: the page of tile i's position 16 x as loaded, and from it
+            // the pool's row of that position (-1: no such page).
+            const auto needed = [&](int i) { return i < n && lane < kTile / 16 && key0 + i * kTile + lane * 16 < rs.len; };
+            const auto page_entry = [&](int i) -> int {
+                return needed(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + lane * 16) >> c.page_shift)) : 0;
+            };
+            const auto first_row = [&](int i, int p) -> int {
+                if (!needed(i)) return -1;
+                if ((unsigned)p >= (unsigned)c.num_pages) {
+                    atomicOr(c.status, kStatusBadIndex);
+                    return -1;
+                }
+                return ((p * c.kv_heads + head) << c.page_shift) + ((key0 + i * kTile + lane * 16) & ((1 << c.page_shift) - 1));
+            };
+            // A piece's codes; zeros for positions nobody sees.
+            const auto load = [&](int i, int side, int half, int rows) {
                 const int pos = key0 + i * kTile;
-                const int8_t *pool = static_cast<const int8_t *>(side ? c.v : c.k);
+                const char *pool = static_cast<const char *>(side ? c.v : c.k) + u * 16;
 #pragma unroll
                 for (int x = 0; x < kPer; ++x) {
-                    const int unit = x * 128 + ct, key = pos + unit / kU;
-                    raw[side][x] = make_uint4(0, 0, 0, 0);
-                    if (i < n && key >= all.lo && key < all.hi) {
-                        const int p = page_of(c, b, key);
-                        if (p >= 0) {
-                            const size_t at = (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-                            raw[side][x] = __ldg(reinterpret_cast<const uint4 *>(pool + at * D + (unit % kU) * 16));
-                        }
-                    }
+                    const int q = (x * C::kConverters + cw) * kRowsOnce + sub, r = half * kPiece + q;
+                    const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
+                    raw[half][x] = make_uint4(0, 0, 0, 0);
+                    if (q < kPiece && base >= 0 && pos + r >= all.lo && pos + r < all.hi)
+                        raw[half][x] = __ldg(reinterpret_cast<const uint4 *>(pool + (size_t)(base + (r & 15)) * D));
                 }
-                if (side) {
-                    sc[0] = sc[1] = 0.0f;
-                    const int key = pos + ct;
-                    const int p = i < n && key >= all.lo && key < all.hi ? page_of(c, b, key) : -1;
-                    if (p >= 0) {
-                        const size_t at = (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-                        sc[0] = c.k_scale[at];
-                        sc[1] = c.v_scale[at];
+            };
+            const auto load_scales = [&](int i, int rows) {
+                const int pos = key0 + i * kTile;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int r = (x * C::kConverters + cw) * 32 + lane;
+                    const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
+                    sc[0][x] = sc[1][x] = 0.0f;
+                    if (r < kTile && base >= 0 && pos + r >= all.lo && pos + r < all.hi) {
+                        sc[0][x] = __ldg(c.k_scale + base + (r & 15));
+                        sc[1][x] = __ldg(c.v_scale + base + (r & 15));
                     }
                 }
             };
-            const auto store = [&](int st, int side) {
+            const auto store = [&](int slot, int half) {
 #pragma unroll
                 for (int x = 0; x < kPer; ++x) {
-                    const int unit = x * 128 + ct, row = unit / kU, u = unit % kU;
-                    const uint32_t w[4] = {raw[side][x].x, raw[side][x].y, raw[side][x].z, raw[side][x].w};
+                    const int q = (x * C::kConverters + cw) * kRowsOnce + sub, r = half * kPiece + q;
+                    if (q >= kPiece) break;
+                    const uint32_t w[4] = {raw[half][x].x, raw[half][x].y, raw[half][x].z, raw[half][x].w};
                     uint32_t o[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         o[2 * e] = frag::i8_pair(__byte_perm(w[e], 0, 0x4140));
                         o[2 * e + 1] = frag::i8_pair(__byte_perm(w[e], 0, 0x4342));
                     }
-                    unsigned char *base = sgen + (side ? C::kV : C::kK) + st * C::kOperand + (u >> 2) * C::kPanel + row * 128;
+                    unsigned char *base = sgen + slot_at(slot) + (u >> 2) * C::kPanel + r * 128;
                     const int ch = (u & 3) * 2;
-                    *reinterpret_cast<uint4 *>(base + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(base + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-                if (side) {
-                    // Both sides' scales go with the values: the softmax warps read
-                    // them until the tile's last product, which is what v_empty waits for.
-                    float *at = reinterpret_cast<float *>(sgen + C::kScale) + st * kTile + ct;
-                    at[0] = sc[0] * L.scale_log2;
-                    at[kStages * kTile] = sc[1];
+                    *reinterpret_cast<uint4 *>(base + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(base + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
             };
-            load(0, 0);
-            load(0, 1);
+            int rows = first_row(0, page_entry(0)), entry = page_entry(1);
+            load(0, 0, 0, rows);
+            load(0, 0, 1, rows);
             for (int i = 0; i < n; ++i) {
-                const int st = i & 1;
                 bool ok = true;
+                const int rows_next = first_row(i + 1, entry);
+                entry = page_entry(i + 2);
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    if (ok) ok = wait(side ? v_empty(st) : k_empty(st), ((i >> 1) & 1) ^ 1) && !lost();
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    store(st, side);
+                    const T item(2 * i + side);
+                    ok = wait(empty(item.slot), item.parity ^ 1) && !lost();
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (side == 0) load_scales(i, rows);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        store(item.slot, half);
+                        if (side == 0) load(i, 1, half, rows);
+                        else load(i + 1, 0, half, rows_next);
+                    }
+                    if (side) {
+                        // both sides' scales go with the values
+                        float *at = reinterpret_cast<float *>(sgen + C::kScale) + (i % C::kScaleTiles) * kTile;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int r = (x * C::kConverters + cw) * 32 + lane;
+                            if (r >= kTile) break;
+                            at[r] = sc[0][x] * L.scale_log2;
+                            at[C::kScaleTiles * kTile + r] = sc[1][x];
+                        }
+                    }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(side ? v_full(st) : k_full(st));
-                    load(i + 1, side);
+                    if (lane == 0) ptx::mbar_arrive(full(item.slot));
                 }
                 if (!ok) break;
+                rows = rows_next;
             }
         }
     }
-
     __syncwarp();
 
     float m = -INFINITY, l = 0.0f;
-    const int h = (warp - 4) >> 2;                       // this softmax warp's half
-    const int r = r0 + h * kHalf + (warp & 3) * 32 + lane;   // and its thread's row
+    // A softmax warp's half, its part of each tile's keys (and of O's
+    // dimensions), and its thread's row.
+    const int h = ((warp - 4) >> 2) & 1, part = (warp - 4) >> 3;
+    const int hr = (warp & 3) * 32 + lane, r = r0 + h * kHalf + hr;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-    const bool softmax = warp >= 4 && warp < 12 && h < halves;
+    const bool softmax = warp >= 4 && h < halves;
+    constexpr int kDims = D / 2;                      // of O a thread rescales and writes
+    float *const share = reinterpret_cast<float *>(sgen + C::kShare);
+    const int pair_bar = 1 + h * 4 + (warp & 3);      // the two warps of 32 rows
     if (softmax) {
         // ------------------------------------------------------- softmax
-        {   // this thread's row of Q, in the operand's swizzled rows
-            const int qr = r - r0 - h * kHalf;
-            unsigned char *base = sgen + C::kQ + h * C::kOperand + qr * 128;
+        {   // half of this thread's row of Q, in the operand's swizzled rows
+            unsigned char *base = sgen + C::kQ + h * C::kOperand + hr * 128;
             const __nv_bfloat16 *p = rs.query(L, r, D);
 #pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
+            for (int x = 0; x < D / 16; ++x) {
+                const int u = part * (D / 16) + x;
                 const uint4 w = r < rs.R ? __ldg(reinterpret_cast<const uint4 *>(p + u * 8)) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(base + (u >> 3) * C::kPanel + (((u & 7) ^ (qr & 7)) << 4)) = w;
+                *reinterpret_cast<uint4 *>(base + (u >> 3) * C::kPanel + (((u & 7) ^ (hr & 7)) << 4)) = w;
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -394,79 +571,74 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int last = min(r1, r0 + (h + 1) * kHalf);
         const Span mine = span_of(L, rs, r0 + h * kHalf, last);
         const Seen z = rs.seen(L, min(r, rs.R - 1));
+        const uint32_t t_mine = t_s(h) + lanes;
+        bool ok = true;
         for (int i = 0; i < n; ++i) {
-            if (!__all_sync(~0u, wait(s_full(h), i & 1) && !lost())) break;
+            ok = wait(s_full(h), i & 1) && !lost();
+            if (I8 && ok) ok = wait(full(T(2 * i + 1).slot), T(2 * i + 1).parity);   // the tile's scales
+            __syncwarp();
+            // The two warps leave together, whatever ran out.
+            if (ptx::bar_red_or(pair_bar, 64, !ok)) break;
             ptx::tc_fence_after();
             const int pos = key0 + i * kTile;
             const bool partial = pos < mine.all_lo || pos + kTile > mine.all_hi;
-            const float *ks = reinterpret_cast<const float *>(sgen + C::kScale) + (i & 1) * kTile;
-            const float *vs = ks + kStages * kTile;
-            const int first = z.lo - pos, end = z.hi - pos;   // columns [first, end) are seen
-            if (I8 && !__all_sync(~0u, wait(v_full(i & 1), (i >> 1) & 1))) break;   // the tile's scales
-            uint32_t p[kTile / 2];
+            const int col0 = part * kCols;
+            const float *ks = reinterpret_cast<const float *>(sgen + C::kScale) + (i % C::kScaleTiles) * kTile + col0;
+            const float *vs = ks + C::kScaleTiles * kTile;
+            const int first = z.lo - pos - col0, end = z.hi - pos - col0;   // of my columns, [first, end) are seen
+            uint32_t p[kCols / 2];
             while (true) {
+                // Scores in base 2 above the reference maximum, their largest, the
+                // probabilities and their sum.
                 const float ref = m == -INFINITY ? 0.0f : m;
-                float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t v[32];
-                    tmem_ld32(t_s(h) + lanes + 32 * q, v);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float t = __uint_as_float(v[e]) * (I8 ? ks[32 * q + e] : L.scale_log2);
-                        if (partial && (32 * q + e < first || 32 * q + e >= end)) t = -INFINITY;
-                        top = fmaxf(top, t);
-                        float x = frag::ex2(t - ref);
-                        sum += x;
-                        if (I8) x = partial && t == -INFINITY ? 0.0f : x * vs[32 * q + e];
-                        v[e] = __float_as_uint(x);
-                    }
-                    // Rounded to bf16 for the second product: at most 2^-8 of
-                    // each term, of either sign, as small as the output's own rounding.
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        p[16 * q + e] = frag::pack_bf16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-                }
+                float top, sum;
+                if (partial) tile_pass<I8, true>(t_mine + col0, L.scale_log2, ref, ks, vs, first, end, p, top, sum);
+                else tile_pass<I8, false>(t_mine + col0, L.scale_log2, ref, ks, vs, first, end, p, top, sum);
+                top += ref;
                 const bool grow = top > m + kLazy;   // also from m = -inf
-                if (!__any_sync(~0u, grow)) {
+                // Both warps have read their scores here: P may replace them.
+                if (!ptx::bar_red_or(pair_bar, 64, grow)) {
                     l += sum;
                     break;
                 }
-                // Raise the maxima and read the scores again.
-                const float nm = fmaxf(m, top);
+                // Raise the maxima to what both threads of a row saw, and read
+                // the scores again.
+                share[part * kRows + h * kHalf + hr] = top;
+                ptx::bar_red_or(pair_bar, 64, false);
+                const float nm = fmaxf(m, fmaxf(top, share[(part ^ 1) * kRows + h * kHalf + hr]));
                 const float fac = nm == -INFINITY ? 1.0f : frag::ex2(m - nm);
                 if (i > 0) {
-                    if (!__all_sync(~0u, wait(pv_done(h), (i - 1) & 1))) break;
+                    ok = wait(pv_done(h), (i - 1) & 1);
+                    __syncwarp();
                     ptx::tc_fence_after();
+                    if (__all_sync(~0u, ok)) {
 #pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t v[32];
-                        tmem_ld32(t_o(h) + lanes + 32 * q, v);
-                        ptx::tmem_ld_wait();
+                        for (int q = 0; q < kDims / 32; ++q) {
+                            uint32_t v[32];
+                            const uint32_t at = t_o(h) + lanes + part * kDims + 32 * q;
+                            tmem_ld32(at, v);
+                            ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fac);
-                        tmem_st32(t_o(h) + lanes + 32 * q, v);
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fac);
+                            tmem_st32(at, v);
+                        }
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
                 }
                 l *= fac;
                 m = nm;
+                ptx::bar_red_or(pair_bar, 64, false);   // `share` may be written again
             }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = p[32 * q + e];
-                tmem_st32(t_s(h) + lanes + 32 * q, v);
-            }
+            tmem_st32(t_mine + part * (kCols / 2), p);
             tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(p_ready(h));
         }
-        if (n > 0) wait(pv_done(h), (n - 1) & 1);
+        if (n > 0 && ok) wait(pv_done(h), (n - 1) & 1);
+        __syncwarp();
         ptx::tc_fence_after();
+        share[part * kRows + h * kHalf + hr] = l;
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -478,7 +650,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const size_t at = ((size_t)tile * L.split + sp) * kRows + (r - r0);
         if (!I8 && words[2]) {
             constexpr int kE = D / 32;
-            for (int x = 0; x < 32; ++x) {
+            for (int x = part; x < 32; x += 2) {
                 const int row = r - lane + x;
                 if (row >= rs.R) break;
                 float acc[kE], mm, ll;
@@ -497,17 +669,18 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
         } else {
             const Seen z = rs.seen(L, min(r, rs.R - 1));
+            l += share[(part ^ 1) * kRows + h * kHalf + hr];
             const float inv = __fdiv_rn(1.0f, l);
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
+            for (int q = 0; q < kDims / 32; ++q) {
                 uint32_t v[32];
                 if (n > 0) {
-                    tmem_ld32(t_o(h) + lanes + 32 * q, v);
+                    tmem_ld32(t_o(h) + lanes + part * kDims + 32 * q, v);
                     ptx::tmem_ld_wait();
                 }
                 if (r < rs.R && active == 1) {
                     const bool any = z.hi > z.lo && n > 0;
-                    uint4 *dst = reinterpret_cast<uint4 *>(rs.out(L, r, D) + 32 * q);
+                    uint4 *dst = reinterpret_cast<uint4 *>(rs.out(L, r, D) + part * kDims + 32 * q);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
@@ -519,10 +692,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else if (r < rs.R) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(L.partial + at * D + 32 * q);
+                    uint4 *dst = reinterpret_cast<uint4 *>(L.partial + at * D + part * kDims + 32 * q);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    if (q == 0) L.stats[at] = make_float2(m, l);
+                    if (q == 0 && part == 0) L.stats[at] = make_float2(m, l);
                 }
                 __syncwarp();
             }
