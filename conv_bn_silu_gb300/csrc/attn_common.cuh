@@ -25,15 +25,20 @@ __device__ __forceinline__ Seen seen_by(int place, int len, int causal, int wind
 // One sequence's rows of one key/value head: row r is token r / G of the
 // chunk, query head head * G + r % G.
 struct Rows {
-    int start, fresh, G, R, len, base, head;   // first new token, how many, heads a key head, rows; length, first place
+    int start, fresh, R, len, base, head;   // first new token, how many, rows; length, first place
+    static __device__ __forceinline__ int token(const AttnLaunch &L, int r) {
+        return L.group > 1 ? (int)__umulhi((unsigned)r, L.group_magic) : r;
+    }
     __device__ __forceinline__ Seen seen(const AttnLaunch &L, int r) const {
-        return seen_by(base + r / G, len, L.causal, L.window);
+        return seen_by(base + token(L, r), len, L.causal, L.window);
     }
     __device__ __forceinline__ const __nv_bfloat16 *query(const AttnLaunch &L, int r, int D) const {
-        return static_cast<const __nv_bfloat16 *>(L.q) + (size_t)(start + r / G) * L.q_stride + (size_t)(head * G + r % G) * D;
+        const int t = token(L, r);
+        return static_cast<const __nv_bfloat16 *>(L.q) + (size_t)(start + t) * L.q_stride + (size_t)(head * L.group + r - t * L.group) * D;
     }
     __device__ __forceinline__ __nv_bfloat16 *out(const AttnLaunch &L, int r, int D) const {
-        return static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + r / G) * L.out_stride + (size_t)(head * G + r % G) * D;
+        const int t = token(L, r);
+        return static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + t) * L.out_stride + (size_t)(head * L.group + r - t * L.group) * D;
     }
 };
 
@@ -43,6 +48,7 @@ __device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head) {
     const CacheArgs &c = L.c;
     Rows s;
     const int s0 = c.new_start[b], s1 = c.new_start[b + 1];
+    s.len = seq_len(c, b);
     s.start = max(0, min(s0, c.total));
     const int end = max(s.start, min(s1, c.total));
     s.fresh = end - s.start;
@@ -50,10 +56,8 @@ __device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head) {
         if (threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
         s.fresh = min(s.fresh, L.max_new);
     }
-    s.G = L.heads / c.kv_heads;
-    s.R = s.fresh * s.G;
+    s.R = s.fresh * L.group;
     s.head = head;
-    s.len = seq_len(c, b);
     s.base = s.len - s.fresh;
     return s;
 }

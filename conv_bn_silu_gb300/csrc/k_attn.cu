@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch L)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads, rt = blockIdx.y / c.kv_heads;
     const Rows rs = rows_of(L, b, head);
-    const int R = rs.R, G = rs.G, r0 = rt * kRows, len = rs.len, base = rs.base;
+    const int R = rs.R, r0 = rt * kRows, len = rs.len, base = rs.base;
     if (r0 >= R) return;
-    const int t_lo = r0 / G, t_hi = (min(R, r0 + kRows) - 1) / G;
+    const int t_lo = Rows::token(L, r0), t_hi = Rows::token(L, min(R, r0 + kRows) - 1);
     // Keys that some row of the tile sees, in blocks of 16 from a multiple of 16.
     const int lo = seen_by(base + t_lo, len, L.causal, L.window).lo;
     const int hi = seen_by(base + t_hi, len, L.causal, L.window).hi;

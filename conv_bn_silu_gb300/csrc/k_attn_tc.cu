@@ -214,6 +214,25 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
     sum = a.x + a.y;
 }
 
+// The largest of a thread's scores, in base 2.
+template <bool I8, bool MASK>
+__device__ __forceinline__ float tile_top(uint32_t taddr, float scale, const float *ks, int first, int end) {
+    float tops[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int q = 0; q < kCols / 32; ++q) {
+        uint32_t v[32];
+        tmem_ld32(taddr + 32 * q, v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            float t = __uint_as_float(v[e]) * (I8 ? ks[32 * q + e] : scale);
+            if (MASK && (32 * q + e < first || 32 * q + e >= end)) t = -INFINITY;
+            tops[e & 1] = fmaxf(tops[e & 1], t);
+        }
+    }
+    return fmaxf(tops[0], tops[1]);
+}
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(Chunk<D, I8>::kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnLaunch L) {
@@ -224,6 +243,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    if (!I8 && warp == 1 && lane < 2) ptx::prefetch_tmap(lane ? &tm_v : &tm_k);
     ptx::griddep_wait();
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads;
     const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
@@ -555,14 +575,15 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int pair_bar = 1 + h * 4 + (warp & 3);      // the two warps of 32 rows
     if (softmax) {
         // ------------------------------------------------------- softmax
-        {   // half of this thread's row of Q, in the operand's swizzled rows
-            unsigned char *base = sgen + C::kQ + h * C::kOperand + hr * 128;
-            const __nv_bfloat16 *p = rs.query(L, r, D);
+        {   // the half's rows of Q, in the operand's swizzled rows: consecutive lanes
+            // take consecutive 16 bytes of a row
+            const int at = part * 128 + hr;
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
-                const int u = part * (D / 16) + x;
-                const uint4 w = r < rs.R ? __ldg(reinterpret_cast<const uint4 *>(p + u * 8)) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(base + (u >> 3) * C::kPanel + (((u & 7) ^ (hr & 7)) << 4)) = w;
+                const int unit = x * 256 + at, row = unit / (D / 8), u = unit % (D / 8);
+                const int qr = r0 + h * kHalf + row;
+                const uint4 w = qr < rs.R ? __ldg(reinterpret_cast<const uint4 *>(rs.query(L, qr, D)) + u) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(sgen + C::kQ + h * C::kOperand + (u >> 3) * C::kPanel + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -587,6 +608,16 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const float *vs = ks + C::kScaleTiles * kTile;
             const int first = z.lo - pos - col0, end = z.hi - pos - col0;   // of my columns, [first, end) are seen
             uint32_t p[kCols / 2];
+            if (i == 0) {
+                // The first tile's largest score is the first reference.
+                float top;
+                if (partial) top = tile_top<I8, true>(t_mine + col0, L.scale_log2, ks, first, end);
+                else top = tile_top<I8, false>(t_mine + col0, L.scale_log2, ks, first, end);
+                share[part * kRows + h * kHalf + hr] = top;
+                ptx::bar_red_or(pair_bar, 64, false);
+                m = fmaxf(top, share[(part ^ 1) * kRows + h * kHalf + hr]);
+                ptx::bar_red_or(pair_bar, 64, false);   // `share` may be written again
+            }
             while (true) {
                 // Scores in base 2 above the reference maximum, their largest, the
                 // probabilities and their sum.
@@ -668,9 +699,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
             }
         } else {
+            // Through shared memory (the ring, and Q, are free), so that stores
+            // are of whole rows: bf16 rows in Q's place, or float rows in the ring's.
             const Seen z = rs.seen(L, min(r, rs.R - 1));
             l += share[(part ^ 1) * kRows + h * kHalf + hr];
+            const bool any = z.hi > z.lo && n > 0;
             const float inv = __fdiv_rn(1.0f, l);
+            unsigned char *const f_rows = sgen + C::kRing + h * (kHalf * D * 4);
+            unsigned char *const b_rows = sgen + C::kQ + h * C::kOperand;
 #pragma unroll
             for (int q = 0; q < kDims / 32; ++q) {
                 uint32_t v[32];
@@ -678,9 +714,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     tmem_ld32(t_o(h) + lanes + part * kDims + 32 * q, v);
                     ptx::tmem_ld_wait();
                 }
-                if (r < rs.R && active == 1) {
-                    const bool any = z.hi > z.lo && n > 0;
-                    uint4 *dst = reinterpret_cast<uint4 *>(rs.out(L, r, D) + part * kDims + 32 * q);
+                const int dim = part * kDims + 32 * q;
+                if (active == 1) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
@@ -689,15 +724,39 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             w[y] = any ? frag::pack_bf16(__uint_as_float(v[8 * e + 2 * y]) * inv,
                                                          __uint_as_float(v[8 * e + 2 * y + 1]) * inv)
                                        : 0u;
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        const int u = dim / 8 + e;
+                        *reinterpret_cast<uint4 *>(b_rows + hr * (D * 2) + ((u ^ (hr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else if (r < rs.R) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(L.partial + at * D + part * kDims + 32 * q);
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    if (q == 0 && part == 0) L.stats[at] = make_float2(m, l);
+                    for (int e = 0; e < 8; ++e) {
+                        const int u = dim / 4 + e;
+                        *reinterpret_cast<uint4 *>(f_rows + hr * (D * 4) + ((u ^ (hr & 7)) << 4)) =
+                            make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
                 }
-                __syncwarp();
+            }
+            if (active > 1 && part == 0 && r < rs.R) L.stats[at] = make_float2(m, l);
+            ptx::bar_red_or(9 + h, 256, false);   // the half's rows are in place
+            const int mine = part * 128 + hr;
+            if (active == 1) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const int unit = x * 256 + mine, row = unit / (D / 8), u = unit % (D / 8);
+                    const int qr = r0 + h * kHalf + row;
+                    if (qr < rs.R)
+                        reinterpret_cast<uint4 *>(rs.out(L, qr, D))[u] =
+                            *reinterpret_cast<const uint4 *>(b_rows + row * (D * 2) + ((u ^ (row & 7)) << 4));
+                }
+            } else {
+                float *dst = L.partial + (((size_t)tile * L.split + sp) * kRows + h * kHalf) * D;
+#pragma unroll 4
+                for (int x = 0; x < D / 8; ++x) {
+                    const int unit = x * 256 + mine, row = unit / (D / 4), u = unit % (D / 4);
+                    if (r0 + h * kHalf + row < rs.R)
+                        reinterpret_cast<uint4 *>(dst)[unit] =
+                            *reinterpret_cast<const uint4 *>(f_rows + row * (D * 4) + ((u ^ (row & 7)) << 4));
+                }
             }
         }
     }

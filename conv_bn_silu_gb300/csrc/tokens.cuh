@@ -80,6 +80,8 @@ struct AttnLaunch {
     void *out;
     long long q_stride, out_stride;
     float scale_log2;           // softmax scale * log2(e)
+    int group;                  // query heads of a key head
+    unsigned int group_magic;   // ceil(2^32 / group): r / group for r group < 2^32 (group > 1)
     int heads, causal, window, max_new;
     int split, row_tiles;
     float *partial;             // [batch][kv_heads][row_tiles][split][rows][head_dim], then (max, sum) of each row

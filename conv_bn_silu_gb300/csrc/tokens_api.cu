@@ -156,6 +156,8 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     if (tiles * d->kv_heads > kGridMax || d->batch > kGridMax)
         return fail(CBS_ERR_UNSUPPORTED, "%lld row tiles of %d heads, %d sequences: at most %d", tiles, d->kv_heads,
                     d->batch, kGridMax);
+    if (rows * (d->heads / d->kv_heads) >= 1ll << 32)
+        return fail(CBS_ERR_UNSUPPORTED, "%d new tokens of %d heads", d->max_new, d->heads);
     p.row_tiles = (int)std::max(tiles, 1ll);
     const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
     const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
@@ -218,6 +220,8 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
     CBS_TRY(status_word(&L.c));
     L.q = q; L.out = out; L.q_stride = q_stride; L.out_stride = out_stride;
     L.scale_log2 = scale * 1.44269504088896340736f;
+    L.group = d.heads / d.kv_heads;
+    L.group_magic = L.group > 1 ? (unsigned)(((1ull << 32) + L.group - 1) / L.group) : 0u;
     L.heads = d.heads; L.causal = d.causal != 0; L.window = d.window; L.max_new = d.max_new;
     L.split = p->split; L.row_tiles = p->row_tiles;
     if (p->split > 1) {
