@@ -35,10 +35,10 @@ constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 template <int D, bool I8>
 struct Chunk {
     // Warp 0: MMA issue; 1-3: TMA and two that check values (bf16), or
-    // converters (int8); 4-19: softmax, eight warps a half (two threads a row, 64
-    // keys of the tile each).
-    static constexpr int kThreads = 640;
-    static constexpr int kConverters = 3;
+    // converters (int8, with 20-23); 4-19: softmax, eight warps a half (two
+    // threads a row, 64 keys of the tile each).
+    static constexpr int kThreads = I8 ? 768 : 640;
+    static constexpr int kConverters = 7;
     static constexpr int kPanel = kTile * 128;                 // 64 dimensions of 128 rows
     static constexpr int kOperand = (D / 64) * kPanel;         // one Q half, K tile or V tile
     // A ring of K and V tiles in turn (K of tile i is its item 2 i, V 2 i + 1): as
@@ -450,7 +450,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ready(i));
         }
-    } else if (I8 && warp < 4) {
+    } else if (I8 && (warp < 4 || warp >= 20)) {
         // ------------------------------------------------------- converters
         if constexpr (I8) {
             // A tile is four pieces: 64 keys' rows of K, the other 64, then V's.
@@ -458,9 +458,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             constexpr int kU = D / 16;                       // 16-code units of a row
             constexpr int kRowsOnce = 32 / kU;               // rows a warp takes at once (of one page: 4 or 8)
             constexpr int kPiece = kTile / 2, kPer = (kPiece / kRowsOnce + C::kConverters - 1) / C::kConverters;
-            const int cw = warp - 1, u = lane % kU, sub = lane / kU;
+            const int cw = warp < 4 ? warp - 1 : warp - 17, u = lane % kU, sub = lane / kU;
             uint4 raw[2][kPer];
-            float sc[2][2] = {};
+            float sc[2] = {};
             // Lane x < 8: the page of tile i's position 16 x as loaded, and from it
             // the pool's row of that position (-1: no such page).
             const auto needed = [&](int i) { return i < n && lane < kTile / 16 && key0 + i * kTile + lane * 16 < rs.len; };
@@ -488,17 +488,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         raw[half][x] = __ldg(reinterpret_cast<const uint4 *>(pool + (size_t)(base + (r & 15)) * D));
                 }
             };
+            static_assert(C::kConverters >= kTile / 32, "a key's scales a lane");
             const auto load_scales = [&](int i, int rows) {
-                const int pos = key0 + i * kTile;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int r = (x * C::kConverters + cw) * 32 + lane;
-                    const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
-                    sc[0][x] = sc[1][x] = 0.0f;
-                    if (r < kTile && base >= 0 && pos + r >= all.lo && pos + r < all.hi) {
-                        sc[0][x] = __ldg(c.k_scale + base + (r & 15));
-                        sc[1][x] = __ldg(c.v_scale + base + (r & 15));
-                    }
+                const int pos = key0 + i * kTile, r = cw * 32 + lane;
+                const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
+                sc[0] = sc[1] = 0.0f;
+                if (r < kTile && base >= 0 && pos + r >= all.lo && pos + r < all.hi) {
+                    sc[0] = __ldg(c.k_scale + base + (r & 15));
+                    sc[1] = __ldg(c.v_scale + base + (r & 15));
                 }
             };
             const auto store = [&](int slot, int half) {
@@ -544,12 +541,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (side) {
                         // both sides' scales go with the values
                         float *at = reinterpret_cast<float *>(sgen + C::kScale) + (i % C::kScaleTiles) * kTile;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int r = (x * C::kConverters + cw) * 32 + lane;
-                            if (r >= kTile) break;
-                            at[r] = sc[0][x] * L.scale_log2;
-                            at[C::kScaleTiles * kTile + r] = sc[1][x];
+                        if (cw * 32 + lane < kTile) {
+                            at[cw * 32 + lane] = sc[0] * L.scale_log2;
+                            at[C::kScaleTiles * kTile + cw * 32 + lane] = sc[1];
                         }
                     }
                     ptx::fence_proxy_async_smem();
@@ -569,7 +563,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int h = ((warp - 4) >> 2) & 1, part = (warp - 4) >> 3;
     const int hr = (warp & 3) * 32 + lane, r = r0 + h * kHalf + hr;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-    const bool softmax = warp >= 4 && h < halves;
+    const bool softmax = warp >= 4 && warp < 20 && h < halves;
     constexpr int kDims = D / 2;                      // of O a thread rescales and writes
     float *const share = reinterpret_cast<float *>(sgen + C::kShare);
     const int pair_bar = 1 + h * 4 + (warp & 3);      // the two warps of 32 rows

@@ -179,7 +179,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         const long long want = ((long long)sms * 4 + base - 1) / base;
         p.split = (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
     }
-    p.threads = chunk ? 640 : 128;
+    p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 768 : 640) : 128;
     const long long ctas = base * p.split;
     if (ctas > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld CTAs", ctas);
     p.grid_ctas = (int)ctas;
