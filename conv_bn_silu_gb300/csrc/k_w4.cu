@@ -3,267 +3,352 @@
 //   y[m, n] = act( xs[m] * sum_g s[g, n] * sum_{k in g} x[m, k] (q[n, k] - z[g, n]) + bias[n] )
 //
 // The weights are read once: half a byte each, so HBM (L2, for small layers)
-// bounds the call.  Y^T = W X^T: sixteen outputs fill the rows of an m16n8k16
-// MMA and the few input rows its columns.  A packed word holds eight weights
-// of one output with weights 2i and 2i + 1 in nibbles i and i + 4, so a shift
-// and a mask give a pair in the two halves of a register; 0x4300 | q is the
-// bf16 value 128 + q, and taking 128 + z away leaves q - z exactly.  Group
-// sums stay apart (exact whole numbers for 8-bit inputs), are scaled in 32
-// bits and added to the running total in 32 bits.
+// bounds the call, and after it the instructions that turn nibbles into
+// operands.  Y^T = W X^T on tcgen05: 128 outputs are the rows of the product (the
+// lanes of tensor memory) and the input rows its 16, 32 or 64 columns.  A thread
+// owns an output: it takes 64 of its weights from shared memory, turns them into
+// bf16 and stores them to tensor memory as the MMA's A operand; X comes by TMA as
+// B (8-bit X is widened by the threads).  A piece's sums come back through tensor
+// memory, are scaled in 32 bits and added to the thread's running totals, so
+// every weight costs about two instructions and the MMA none of the threads'.
+// (On mma.sync the same product spent as many again on fragments of X and on
+// the MMAs: 38 us for 16 rows of 8192 x 16384.)
 //
-// Each lane copies the words it will use itself into a ring of its own in
-// shared memory (cp.async), several stages ahead, so no thread waits for
-// another's copy and the bytes in flight cost no registers.
+// A packed word holds eight weights of one output with weights 2i and 2i + 1 in
+// nibbles i and i + 4, so a shift and a mask-and-or give a pair in the two halves
+// of a register: 0x4300 | q is the bf16 value 128 + q, and taking 128 + z away
+// leaves q - z exactly.  Products of bf16 pairs are exact in 32 bits, and sums of
+// 8-bit inputs are whole numbers below 2^24.
+//
+// Two warpgroups take alternate pieces, each with two operand and two result
+// buffers: while the MMA of one piece runs, the group dequantises its next and
+// drains its last.  Shares of k are CTAs of a cluster, which add their sums in
+// order through distributed shared memory.
 #include <type_traits>
 
 #include <cuda_bf16.h>
 
 #include "mma_frag.cuh"
 #include "tc_ptx.cuh"
+#include "tc_warp.cuh"
 #include "tokens.cuh"
 
 namespace cbs {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStageK = 128;    // weights along k in one stage of the ring
-constexpr int kStages = 4;
+constexpr int kOut = 128;                    // outputs of a CTA: tensor memory's lanes
+constexpr int kStageK = 256, kPiece = 64;    // weights along k in a stage (128 bytes a row) and in a piece
+constexpr int kPieces = kStageK / kPiece;    // of a stage; each group of warps takes two
+constexpr int kWorkers = 256, kThreads = kWorkers + 64;   // two warpgroups, an MMA warp, a TMA warp
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 
 __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
 
-// GROUP: weights a scale covers (32, 64 or 128).  NT: tiles of eight input
-// rows.  RB: tiles of sixteen outputs a warp.  FULL: k is a multiple of the
-// stage's 128, so no stage ends early.
-//
-// What the loop costs is instructions (a weight is half a byte: at HBM's rate an
-// SM has a dozen issue slots for a warp's 64 weights), so rows past the ends
-// are clamped instead of masked, pointers advance, and for 8-bit inputs the zero
-// point comes off the group's whole-number sum (sum x (128 + q) - (128 + z)
-// sum x, exact below 2^24) instead of every weight.
-template <int GROUP, int NT, int RB, bool XI8, bool FULL>
-__global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) w4_kernel(const W4Launch L, int wk) {
-    constexpr int V = GROUP / 32;            // words a lane, row and group
-    constexpr int kGroups = kStageK / GROUP; // groups in a stage
-    constexpr int kRowBytes = 16;            // a lane's bytes of one row in a stage
-    constexpr int kXB = XI8 ? 1 : 2;         // bytes of an input
-    constexpr bool kEarlyX = NT * kXB <= 2;  // X one stage ahead: 8 NT kXB registers
-    extern __shared__ __align__(16) unsigned char smem[];
+// GROUP: weights a scale covers.  kN: input rows of a CTA.
+template <int GROUP, int kN>
+struct W4Tile {
+    static constexpr int kSubs = GROUP < kPiece ? kPiece / GROUP : 1;   // groups in a piece
+    static constexpr int kW = kOut * 128, kX = kPieces * kN * 128;      // a stage's weights; inputs, 64 a panel
+    static constexpr int kSlot = kW + kX;
+    static constexpr int kStages = kN == 16 ? 4 : kN == 32 ? 3 : 2;
+    // full[], x_ready[], empty[], a_ready[2][2], d_ready[2][2], drain; TMEM address, flag
+    static constexpr int kBars = kStages * kSlot, kNumBars = 3 * kStages + 9;
+    static constexpr int kSmem = kBars + kNumBars * 8 + 16;
+    // tensor memory: A [group][buffer][32], then the results [group][buffer][sub][kN]
+    static constexpr int kACols = 4 * (kPiece / 2), kDCols = 4 * kSubs * kN;
+    static constexpr int kTmem = kACols + kDCols <= 256 ? 256 : 512;
+    static_assert(kACols + kDCols <= 512, "tensor memory");
+    // at the end: each group's sums [2][kN][kOut + 1]
+    static_assert(2 * kN * (kOut + 1) * 4 <= kBars, "sums fit where the stages were");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A float of another CTA's shared memory (this CTA's address, that CTA's rank).
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int GROUP, int kN, bool XI8>
+__global__ void __launch_bounds__(kThreads, W4Tile<GROUP, kN>::kTmem == 256 ? 2 : 1)
+w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const W4Launch L, int split) {
+    using C = W4Tile<GROUP, kN>;
+    extern __shared__ __align__(1024) unsigned char smem[];   // the only shared memory: starts at a multiple of 1 KB
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+    const int n0 = (blockIdx.x / split) * kOut, m0 = blockIdx.y * kN;
+    const int stages = (L.k + kStageK - 1) / kStageK;
+    const int st0 = (int)((long long)stages * rank / split), ns = (int)((long long)stages * (rank + 1) / split) - st0;
+    const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+    const auto full = [&](int s) { return bar(s); };                          // a stage has arrived
+    const auto x_ready = [&](int s) { return bar(C::kStages + s); };          // its 8-bit inputs are widened
+    const auto empty = [&](int s) { return bar(2 * C::kStages + s); };        // and it has been used
+    const auto a_ready = [&](int w, int b) { return bar(3 * C::kStages + 2 * w + b); };       // a piece's operand is stored
+    const auto d_ready = [&](int w, int b) { return bar(3 * C::kStages + 4 + 2 * w + b); };   // and its sums are there
+    const uint32_t drain = bar(3 * C::kStages + 8);
+    volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kBars + 8 * C::kNumBars);
+    // words[0]: TMEM address; [1]: a wait ran out
+
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(x_ready(s), kWorkers / 32);
+            ptx::mbar_init(empty(s), kWorkers / 32 + 1);   // every worker warp, and the MMAs
+        }
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(a_ready(i >> 1, i & 1), 4);
+            ptx::mbar_init(d_ready(i >> 1, i & 1), 1);
+        }
+        ptx::mbar_init(drain, 1);
+        ptx::fence_mbar_init();
+        words[1] = 0;
+    }
+    if (warp == 8) {
+        ptx::tmem_alloc(sbase + C::kBars + 8 * C::kNumBars, C::kTmem);
+        ptx::tmem_relinquish();
+    }
+    if (warp == 9 && lane < 2) ptx::prefetch_tmap(lane ? &tm_x : &tm_w);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    const uint32_t tmem = words[0];
+    const auto t_a = [&](int w, int b) { return tmem + (uint32_t)(2 * w + b) * (kPiece / 2); };
+    const auto t_d = [&](int w, int b, int sub) { return tmem + C::kACols + (uint32_t)((2 * w + b) * C::kSubs + sub) * kN; };
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int wr = warp / wk, part = warp % wk;   // which outputs, which share of k
-    const int n0 = (blockIdx.x * (kWarps / wk) + wr) * 16 * RB;
-    const int m0 = blockIdx.y * 8 * NT;
-    const int stages = (L.k + kStageK - 1) / kStageK;
-    const int st0 = (int)((long long)stages * part / wk), st1 = (int)((long long)stages * (part + 1) / wk);
-    const int left = L.k - st0 * kStageK;         // weights from this share's start to the row's end
+    const auto wait = [&](uint32_t bar_, uint32_t parity) -> bool {
+        if (ptx::mbar_wait_bounded(bar_, parity, kWaitNs)) return true;
+        words[1] = 1;
+        atomicOr(L.status, kStatusTimeout);
+        return false;
+    };
+    const auto lost = [&] { return words[1] != 0; };
 
-    // This lane's rows: g and g + 8 of each tile (rows past n repeat the last one),
-    // at its bytes of the first group; X's row g of each tile (likewise).
-    const uint8_t *wp[2 * RB];
-    int nrow[2 * RB];
+    float total[kN];
 #pragma unroll
-    for (int i = 0; i < 2 * RB; ++i) {
-        nrow[i] = min(n0 + (i >> 1) * 16 + (i & 1) * 8 + g, L.n - 1);
-        wp[i] = L.w + (size_t)nrow[i] * (L.k / 2) + st0 * (kStageK / 2) + j * 4 * V;
-    }
-    const char *xp[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-        xp[t] = static_cast<const char *>(L.x) + ((size_t)min(m0 + t * 8 + g, L.rows - 1) * L.k + st0 * kStageK + j * 8 * V) * kXB;
+    for (int i = 0; i < kN; ++i) total[i] = 0.0f;
+    const int wg = warp >> 2, row = tid & 127;
 
-    unsigned char *const ring = smem + (size_t)tid * kRowBytes;   // [stage][row][thread], 16 bytes each
-    const uint32_t ring32 = ptx::smem_u32(ring);
-    const auto copy = [&](int st, int s) {   // stage st into place s of the ring
-        if (st < st1) {
+    if (warp == 8) {
+        // ------------------------------------------------------- MMA issue
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kN >> 3) << 17) | ((kOut >> 4) << 24);
+        const uint32_t lead = elect_one();
+        const uint64_t d_x = ptx::smem_desc(sbase + C::kW, 16, 1024, 2);
+        int slot = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int i = 0; i < ns && ok; ++i) {
+            ok = wait(XI8 ? x_ready(slot) : full(slot), parity) && !lost();
+            ok = __all_sync(~0u, ok);
 #pragma unroll
-            for (int i = 0; i < 2 * RB; ++i) {
-                const uint32_t dst = ring32 + (s * 2 * RB + i) * kThreads * kRowBytes;
+            for (int pc = 0; pc < kPieces; ++pc) {
+                const int w = pc & 1, b = pc >> 1;   // two pieces a stage and group: buffers in turn
+                if (ok) ok = wait(a_ready(w, b), i & 1);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t x = d_x + (uint32_t)(slot * C::kSlot + pc * kN * 128) / 16;
 #pragma unroll
-                for (int gi = 0; gi < kGroups; ++gi) {
-                    const bool in = FULL || (st - st0) * kStageK + gi * GROUP < left;
-                    const uint8_t *src = in ? wp[i] + gi * (GROUP / 2) : L.w;
-                    const uint32_t bytes = in ? 4 * V : 0;
-                    if constexpr (V == 4) ptx::cp_async_16(dst, src, bytes);
-                    else if constexpr (V == 2) ptx::cp_async_8(dst + gi * 8, src, bytes);
-                    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + gi * 4), "l"(src), "r"(bytes) : "memory");
+                for (int k = 0; k < kPiece / 16; ++k) {
+                    constexpr int kPer = kPiece / 16 / C::kSubs;   // MMAs of a group
+                    mma_ts(lead, t_d(w, b, k / kPer), t_a(w, b) + 8 * k, x + 2u * k, idesc, k % kPer > 0);
                 }
-                wp[i] += kStageK / 2;
+                mma_commit(lead, d_ready(w, b));
             }
+            if (!ok) break;
+            mma_commit(lead, empty(slot));
+            if (++slot == C::kStages) slot = 0, parity ^= 1;
         }
-        ptx::cp_async_commit();
-    };
+        __syncwarp();
+        mma_commit(lead, drain);   // nothing leaves while an MMA reads shared memory
+        if (!ptx::mbar_wait_bounded(drain, 0, kWaitNs)) atomicOr(L.status, kStatusTimeout);
+    } else if (warp == 9) {
+        // ------------------------------------------------------- TMA
+        if (lane == 0) {
+            int slot = 0, done = 0;
+            uint32_t parity = 1;
+            for (int i = 0; i < ns; ++i) {
+                if (!wait(empty(slot), parity) || lost()) break;
+                const uint32_t at = sbase + slot * C::kSlot;
+                ptx::mbar_arrive_expect_tx(full(slot), XI8 ? C::kW : C::kSlot);
+                ptx::tma_load_2d(at, &tm_w, full(slot), (st0 + i) * (kStageK / 2), n0);
+                if (!XI8)
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) copy(st0 + s, s);
-
-    float total[RB][NT][4];
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) total[r][t][i] = 0.0f;
-
-    // The groups' scales and zero points: lane j of a row's four holds those of
-    // the stage's group j, some stages ahead and as they were loaded (arithmetic
-    // on them here would wait for the loads), and the row's lanes get a group's by
-    // a shuffle.
-    constexpr int kAhead = RB == 1 ? 4 : 2;
-    static_assert(kStages % kAhead == 0, "the rings turn together");
-    struct Scale { uint16_t s; uint8_t z; };
-    Scale sz[kAhead][2 * RB];
-    const uint16_t *sp = static_cast<const uint16_t *>(L.scales);
-    const uint8_t *zpt = L.zeros;
-    const int groups = L.k / GROUP;
-    const auto load_scales = [&](int st, Scale (&to)[2 * RB]) {
-        if (st >= st1) return;
-        const int gr = st * kGroups + j % kGroups;
-        const size_t at = (size_t)(FULL || gr < groups ? gr : groups - 1) * L.n;
-#pragma unroll
-        for (int i = 0; i < 2 * RB; ++i) {
-            to[i].s = __ldg(sp + at + nrow[i]);
-            if (zpt) to[i].z = __ldg(zpt + at + nrow[i]);
+                    for (int x = 0; x < kPieces; ++x)
+                        ptx::tma_load_2d(at + C::kW + x * kN * 128, &tm_x, full(slot), (st0 + i) * kStageK + x * kPiece, m0);
+                ++done;
+                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            }
+            if (lost())   // the copies in flight land before the CTA leaves
+                for (int x = max(0, done - C::kStages); x < done; ++x)
+                    ptx::mbar_wait_bounded(full(x % C::kStages), (x / C::kStages) & 1, kWaitNs);
         }
-    };
+    } else {
+        // ------------------------------------------------------- workers
+        const int n = min(n0 + row, L.n - 1);   // outputs past the end repeat the last one's scales
+        // Scales and zero points of this thread's next pieces, as loaded, a stage ahead.
+        struct Scale { uint16_t s; uint8_t z; };
+        Scale sz[2][C::kSubs];
+        const auto load_scales = [&](int i, int b) {
+            const int k = (st0 + i) * kStageK + (2 * b + wg) * kPiece;
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) load_scales(st0 + s, sz[s]);
-
-    using XWord = typename std::conditional<XI8, uint2, uint4>::type;   // eight consecutive inputs
-    XWord xs[kEarlyX ? NT : 1][4];
-    const auto load_x = [&](int t, int gi, int v) -> XWord {   // word v of group gi of xp's stage
-        return __ldg(reinterpret_cast<const XWord *>(xp[t] + (gi * GROUP + v * 8) * kXB));
-    };
-    if constexpr (kEarlyX) {
-#pragma unroll
-        for (int gi = 0; gi < kGroups; ++gi)
-            if (st0 < st1 && (FULL || gi * GROUP < left)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) xs[t][gi * V + v] = load_x(t, gi, v);
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) xp[t] += kStageK * kXB;
-    }
-    for (int sb = st0; sb < st1; sb += kStages) {
-#pragma unroll
-        for (int su = 0; su < kStages; ++su) {
-            const int st = sb + su;
-            if (st >= st1) break;
-            copy(st + kStages - 1, (su + kStages - 1) % kStages);
-            ptx::cp_async_wait<kStages - 1>();
-            uint32_t wv[2 * RB][4];
-#pragma unroll
-            for (int i = 0; i < 2 * RB; ++i) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(ring + (su * 2 * RB + i) * kThreads * kRowBytes);
-                wv[i][0] = w.x; wv[i][1] = w.y; wv[i][2] = w.z; wv[i][3] = w.w;
-            }
-            const int past = (st - st0) * kStageK;   // weights of the share before this stage
-#pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                if (!FULL && past + gi * GROUP >= left) break;
-                float acc[RB][NT][4], sx[NT][4];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sx[t][i] = 0.0f;
-#pragma unroll
-                        for (int r = 0; r < RB; ++r) acc[r][t][i] = 0.0f;
-                    }
-                uint32_t zp[2 * RB];   // 128 + z, a pair of bf16
-                float sc[2 * RB];
-#pragma unroll
-                for (int i = 0; i < 2 * RB; ++i) {
-                    const Scale &o = sz[su % kAhead][i];
-                    const uint32_t mine = (uint32_t)o.s << 16 | (zpt ? o.z & 15u : 8u);
-                    const uint32_t w = kGroups == 1 ? mine : __shfl_sync(~0u, mine, (lane & ~3) | gi);
-                    zp[i] = __byte_perm(w, 0x43u, 0x4040);
-                    sc[i] = __uint_as_float(w & 0xffff0000u);
+            for (int u = 0; u < C::kSubs; ++u) {
+                sz[b][u] = Scale{0, 8};
+                if (i < ns && k + u * GROUP < L.k) {
+                    const size_t at = (size_t)(k / GROUP + u) * L.n + n;
+                    sz[b][u].s = __ldg(static_cast<const uint16_t *>(L.scales) + at);
+                    if (L.zeros) sz[b][u].z = __ldg(L.zeros + at);
                 }
+            }
+        };
+        // 8-bit inputs: 16 codes a unit, a stage ahead.
+        constexpr int kXPer = XI8 ? kN * 16 / kWorkers : 1;
+        uint4 xr[kXPer];
+        const auto load_x = [&](int i) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    uint32_t x[NT][4];
+            for (int x = 0; x < kXPer; ++x) {
+                const int unit = x * kWorkers + tid, m = m0 + (unit >> 4), k = (st0 + i) * kStageK + (unit & 15) * 16;
+                xr[x] = make_uint4(0, 0, 0, 0);
+                if (i < ns && m < L.rows && k < L.k)
+                    xr[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(L.x) + (size_t)m * L.k + k));
+            }
+        };
+        load_scales(0, 0);
+        load_scales(0, 1);
+        if (XI8) load_x(0);
+        float sc[2][C::kSubs];
+        // The sums of the piece in buffer b, scaled into the totals.
+        const auto take = [&](int b) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        XWord w;
-                        if constexpr (kEarlyX) {
-                            w = xs[t][gi * V + v];
-                            if (st + 1 < st1 && (FULL || past + kStageK + gi * GROUP < left)) xs[t][gi * V + v] = load_x(t, gi, v);
-                        } else {
-                            w = load_x(t, gi, v);
-                        }
-                        if constexpr (XI8) {
-                            x[t][0] = frag::i8_pair(__byte_perm(w.x, 0, 0x4140));
-                            x[t][1] = frag::i8_pair(__byte_perm(w.x, 0, 0x4342));
-                            x[t][2] = frag::i8_pair(__byte_perm(w.y, 0, 0x4140));
-                            x[t][3] = frag::i8_pair(__byte_perm(w.y, 0, 0x4342));
-                            // a row of ones: the group's sum of x in every output's place
-                            constexpr uint32_t kOnes = 0x3f803f80u;
-                            frag::mma(sx[t], kOnes, kOnes, kOnes, kOnes, x[t][0], x[t][1]);
-                            frag::mma(sx[t], kOnes, kOnes, kOnes, kOnes, x[t][2], x[t][3]);
-                        } else {
-                            x[t][0] = w.x; x[t][1] = w.y; x[t][2] = w.z; x[t][3] = w.w;
-                        }
+            for (int u = 0; u < C::kSubs; ++u)
+#pragma unroll
+                for (int q = 0; q < kN / 16; ++q) {
+                    uint32_t v[16];
+                    ptx::tmem_ld16(t_d(wg, b, u) + ((uint32_t)(warp & 3) << 21) + 16 * q, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) total[16 * q + e] = fmaf(__uint_as_float(v[e]), sc[b][u], total[16 * q + e]);
+                }
+        };
+        int slot = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int i = 0; i < ns; ++i) {
+            ok = wait(full(slot), parity) && !lost();
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            const unsigned char *wt = smem + slot * C::kSlot + row * 128;
+            if constexpr (XI8) {
+                unsigned char *xt = smem + slot * C::kSlot + C::kW;
+#pragma unroll
+                for (int x = 0; x < kXPer; ++x) {
+                    const int unit = x * kWorkers + tid, m = unit >> 4, c = unit & 15;
+                    const uint32_t w[4] = {xr[x].x, xr[x].y, xr[x].z, xr[x].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[2 * e] = frag::i8_pair(__byte_perm(w[e], 0, 0x4140));
+                        o[2 * e + 1] = frag::i8_pair(__byte_perm(w[e], 0, 0x4342));
                     }
+                    unsigned char *p = xt + (c >> 2) * kN * 128 + m * 128;
+                    const int ch = (c & 3) * 2;
+                    *reinterpret_cast<uint4 *>(p + ((ch ^ (m & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(p + (((ch + 1) ^ (m & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(x_ready(slot));
+                load_x(i + 1);
+            }
 #pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        uint32_t a[2][4];
+            for (int b = 0; b < 2; ++b) {
+                const int pc = 2 * b + wg;
+                uint32_t w[8], a[32], zp[C::kSubs];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t w = wv[2 * r + i][gi * V + v];
-#pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                a[i][p] = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-                                if constexpr (!XI8) a[i][p] = frag::sub_bf16x2(a[i][p], zp[2 * r + i]);
-                            }
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            frag::mma(acc[r][t], a[0][0], a[1][0], a[0][1], a[1][1], x[t][0], x[t][1]);
-                            frag::mma(acc[r][t], a[0][2], a[1][2], a[0][3], a[1][3], x[t][2], x[t][3]);
-                        }
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(wt + (((2 * pc + q) ^ (row & 7)) << 4));
+                    w[4 * q] = y.x; w[4 * q + 1] = y.y; w[4 * q + 2] = y.z; w[4 * q + 3] = y.w;
+                }
+                if (b == 1) {
+                    __syncwarp();   // the warp has read all it needs of the stage's weights
+                    if (lane == 0) ptx::mbar_arrive(empty(slot));
                 }
 #pragma unroll
-                for (int r = 0; r < RB; ++r)
+                for (int u = 0; u < C::kSubs; ++u) zp[u] = 0x43004300u | (sz[b][u].z & 15u) * 0x00010001u;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                for (int q = 0; q < 8; ++q)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (XI8)
-                                acc[r][t][i] = fmaf(-__uint_as_float(zp[2 * r + (i >> 1)] & 0xffff0000u), sx[t][i], acc[r][t][i]);
-                            total[r][t][i] = fmaf(acc[r][t][i], sc[2 * r + (i >> 1)], total[r][t][i]);
-                        }
+                    for (int p = 0; p < 4; ++p)
+                        a[4 * q + p] = frag::sub_bf16x2(((w[q] >> (4 * p)) & 0x000f000fu) | 0x43004300u, zp[q * 8 / (kPiece / C::kSubs)]);
+                tmem_st32(t_a(wg, b) + ((uint32_t)(warp & 3) << 21), a);
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(a_ready(wg, b));
+                // While its MMA runs: the sums of the piece before.
+                if (b == 1 || i > 0) {
+                    ok = wait(d_ready(wg, b ^ 1), (b ? i : i - 1) & 1);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    take(b ^ 1);
+                    ptx::tc_fence_before();
+                }
+#pragma unroll
+                for (int u = 0; u < C::kSubs; ++u) sc[b][u] = __uint_as_float((uint32_t)sz[b][u].s << 16);
+                load_scales(i + 1, b);
             }
-            load_scales(st + kAhead, sz[su % kAhead]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) xp[t] += kStageK * kXB;
+            if (!ok) break;
+            if (++slot == C::kStages) slot = 0, parity ^= 1;
+        }
+        if (ok && ns > 0) {
+            ok = wait(d_ready(wg, 1), (ns - 1) & 1);
+            __syncwarp();
+            ptx::tc_fence_after();
+            if (__all_sync(~0u, ok)) take(1);
         }
     }
-    ptx::cp_async_wait<0>();
-    __syncthreads();   // the ring is free: the shares of k meet in it
-
-    // [warp][input row][output], then summed in the order of the shares.
-    constexpr int kN = 16 * RB, kM = 8 * NT, kPitch = kN + 1;
-    float *sum = reinterpret_cast<float *>(smem);
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum[((size_t)warp * kM + t * 8 + 2 * j + (i & 1)) * kPitch + r * 16 + (i >> 1) * 8 + g] = total[r][t][i];
+    ptx::tc_fence_before();
     __syncthreads();
-    const int outs = (kWarps / wk) * kN;
-    for (int i = tid; i < outs * kM; i += kThreads) {
-        const int m = i / outs, nn = i % outs, w0 = (nn / kN) * wk;
-        const int n = blockIdx.x * outs + nn;
-        if (m0 + m >= L.rows || n >= L.n) continue;
+    ptx::tc_fence_after();
+    if (warp == 8) ptx::tmem_dealloc(tmem, C::kTmem);
+
+    // The groups' sums, [group][input row][output] where the stages were, then the
+    // shares of k in order: each CTA of the cluster finishes its part.
+    constexpr int kPitch = kOut + 1;
+    float *sum = reinterpret_cast<float *>(smem);
+    if (warp < 8) {
+#pragma unroll
+        for (int m = 0; m < kN; ++m) sum[(wg * kN + m) * kPitch + row] = total[m];
+    }
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    const int rows = min(kN, L.rows - m0);
+    for (int i = tid + rank * kThreads; i < kOut * rows; i += kThreads * split) {
+        const int m = i / kOut, nn = i % kOut, n = n0 + nn;
+        if (n >= L.n) continue;
         float y = 0.0f;
-        for (int p = 0; p < wk; ++p) y += sum[((size_t)(w0 + p) * kM + m) * kPitch + nn % kN];
+        if (split > 1) {
+            for (int p = 0; p < split; ++p) {
+                const uint32_t at = sbase + (m * kPitch + nn) * 4;
+                y += ld_cluster(at, p);
+                y += ld_cluster(at + kN * kPitch * 4, p);
+            }
+        } else {
+            y = sum[m * kPitch + nn] + sum[(kN + m) * kPitch + nn];
+        }
         if (XI8) y *= L.x_scale[m0 + m];
         if (L.bias) y += L.bias[n];
         if (L.act == CBS_ACT_SILU) y = silu(y);
@@ -271,37 +356,64 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) w4_kernel(const W4La
         if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at] = __float2bfloat16_rn(y);
         else static_cast<float *>(L.y)[at] = y;
     }
+    if (split > 1) cluster_sync();   // nobody's sums go while another CTA reads them
 }
 
-template <int GROUP, int NT, int RB, bool XI8, bool FULL>
-cudaError_t launch_w4_one(const W4Launch &L, cudaStream_t s) {
-    const int ring = kStages * 2 * RB * kThreads * 16;
-    const int join = kWarps * 8 * NT * (16 * RB + 1) * 4;
-    const int smem = ring > join ? ring : join;
-    // Warps side by side along k: as few as give every SM one and a half CTAs,
-    // since a CTA's warps along n share X (its bytes are 4 rows / (outputs of the
-    // CTA) of the weights').
-    const int tiles = (L.n + 16 * RB - 1) / (16 * RB), stages = (L.k + kStageK - 1) / kStageK;
-    int wk = 1;
-    while (wk < kWarps && tiles * wk < current_device_sms() * 12 && wk * 2 <= stages) wk *= 2;
-    const int per = kWarps / wk;
-    const dim3 grid((tiles + per - 1) / per, (L.rows + 8 * NT - 1) / (8 * NT));
-    auto kern = w4_kernel<GROUP, NT, RB, XI8, FULL>;
-    cudaError_t e = set_max_dyn_smem(kern, smem);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(kern, grid, kThreads, smem, s, L, wk);
+template <int GROUP, int kN, bool XI8>
+cbs_status launch_w4_one(const W4Launch &L, cudaStream_t s) {
+    using C = W4Tile<GROUP, kN>;
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return fail(CBS_ERR_CUDA, "cannot resolve cuTensorMapEncodeTiled from the driver");
+    // Rows of k / 2 bytes by the CTA's outputs, and of inputs by its rows: boxes of
+    // 128 bytes a row.
+    alignas(64) CUtensorMap tw, tx;
+    const auto map = [&](CUtensorMap *tm, CUtensorMapDataType type, const void *p, int cols, int rows, int elem, int box_rows) {
+        const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * elem};
+        const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows}, es[2] = {1u, 1u};
+        return fn(tm, type, 2, const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.w, L.k / 2, L.n, 1, kOut);
+    if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (weights) failed (%d)", (int)r);
+    tx = tw;   // 8-bit inputs need no map
+    if (!XI8) {
+        r = map(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.x, L.k, L.rows, 2, kN);
+        if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (inputs) failed (%d)", (int)r);
+    }
+
+    // Shares of k: as many CTAs of a cluster as give every SM two CTAs, each of
+    // them two stages at least.
+    const int tiles = (L.n + kOut - 1) / kOut, stages = (L.k + kStageK - 1) / kStageK;
+    const int row_tiles = (L.rows + kN - 1) / kN;
+    int split = 1;
+    while (split < 8 && (long long)tiles * row_tiles * split < 2ll * current_device_sms() && stages >= 4 * split) split *= 2;
+    auto kern = w4_kernel<GROUP, kN, XI8>;
+    cudaError_t e = set_max_dyn_smem(kern, C::kSmem);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(tiles * split, row_tiles);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = (launch_options() & CBS_LAUNCH_PDL) ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, kern, tw, tx, L, split);
+    }
+    return cuda_check(e, "4-bit product launch");
 }
 
 template <int GROUP, bool XI8>
-cudaError_t launch_w4_rows(const W4Launch &L, cudaStream_t s) {
-    const bool full = L.k % kStageK == 0;
-    const auto run = [&](auto nt, auto rb) {
-        return full ? launch_w4_one<GROUP, nt, rb, XI8, true>(L, s) : launch_w4_one<GROUP, nt, rb, XI8, false>(L, s);
-    };
-    using std::integral_constant;
-    if (L.rows <= 8) return run(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    if (L.rows <= 16) return run(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    return run(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+cbs_status launch_w4_rows(const W4Launch &L, cudaStream_t s) {
+    if (L.rows <= 16) return launch_w4_one<GROUP, 16, XI8>(L, s);
+    // (groups of 32 have two results a piece: 64 columns of each would not fit tensor memory)
+    if (L.rows <= 32 || GROUP == 32) return launch_w4_one<GROUP, 32, XI8>(L, s);
+    return launch_w4_one<GROUP, GROUP == 32 ? 32 : 64, XI8>(L, s);
 }
 
 // One-time weight transform: symmetric codes q in 1..15 (zero point 8) with
@@ -340,7 +452,7 @@ __global__ void quantize_w4_kernel(const float *__restrict__ w, int n, int k, in
 
 }  // namespace
 
-cudaError_t launch_w4(const W4Launch &L, cudaStream_t s) {
+cbs_status launch_w4(const W4Launch &L, cudaStream_t s) {
     switch (L.group) {
     case 32: return L.x_int8 ? launch_w4_rows<32, true>(L, s) : launch_w4_rows<32, false>(L, s);
     case 64: return L.x_int8 ? launch_w4_rows<64, true>(L, s) : launch_w4_rows<64, false>(L, s);

@@ -69,9 +69,10 @@ struct W4Launch {
     const uint8_t *zeros;       // [k/group][n], nullable (8)
     const float *bias;          // [n], nullable
     void *y;
+    unsigned int *status;
     int rows, n, k, group, x_int8, out_bf16, act;
 };
-cudaError_t launch_w4(const W4Launch &L, cudaStream_t s);
+cbs_status launch_w4(const W4Launch &L, cudaStream_t s);
 cudaError_t launch_quantize_w4(const float *w, int n, int k, int group, uint8_t *packed, void *scales, cudaStream_t s);
 
 struct AttnLaunch {

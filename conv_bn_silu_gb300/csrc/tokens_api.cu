@@ -284,7 +284,7 @@ cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const 
     if (activation != CBS_ACT_SILU && activation != CBS_ACT_IDENTITY)
         return fail(CBS_ERR_INVALID_ARG, "unknown activation %d", activation);
     if (rows < 0) return fail(CBS_ERR_INVALID_ARG, "%d rows", rows);
-    if (rows > 8 * kGridMax) return fail(CBS_ERR_UNSUPPORTED, "%d rows: at most %d", rows, 8 * kGridMax);
+    if (rows > 16 * kGridMax) return fail(CBS_ERR_UNSUPPORTED, "%d rows: at most %d", rows, 16 * kGridMax);
     if (x_prec == CBS_BF16 && x_scale) return fail(CBS_ERR_INVALID_ARG, "x_scale given for BF16 inputs");
     if (rows == 0) return CBS_OK;
     CBS_TRY(need(x, "x"));
@@ -299,7 +299,9 @@ cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const 
     L.zeros = static_cast<const uint8_t *>(zeros); L.bias = bias; L.y = y;
     L.rows = rows; L.n = n; L.k = k; L.group = group; L.x_int8 = x_prec == CBS_INT8; L.out_bf16 = out_prec == CBS_BF16;
     L.act = activation;
-    return cuda_check(launch_w4(L, (cudaStream_t)stream), "4-bit product launch");
+    L.status = device_status_word();
+    if (!L.status) return fail(CBS_ERR_CUDA, "cannot resolve the device status word");
+    return launch_w4(L, (cudaStream_t)stream);
 }
 
 cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed, void *scales, void *stream) {
