@@ -6,7 +6,7 @@
 // bounds the call, and after it the instructions that turn nibbles into
 // operands.  Y^T = W X^T on tcgen05: 128 outputs are the rows of the product (the
 // lanes of tensor memory) and the input rows its 16, 32 or 64 columns.  A thread
-// owns an output: it takes 64 of its weights from shared memory, turns them into
+// owns an output: it takes 128 of its weights from shared memory, turns them into
 // bf16 and stores them to tensor memory as the MMA's A operand; X comes by TMA as
 // B (8-bit X is widened by the threads).  A piece's sums come back through tensor
 // memory, are scaled in 32 bits and added to the thread's running totals, so
@@ -20,10 +20,11 @@
 // leaves q - z exactly.  Products of bf16 pairs are exact in 32 bits, and sums of
 // 8-bit inputs are whole numbers below 2^24.
 //
-// Two warpgroups take alternate pieces, each with two operand and two result
-// buffers: while the MMA of one piece runs, the group dequantises its next and
-// drains its last.  Shares of k are CTAs of a cluster, which add their sums in
-// order through distributed shared memory.
+// Two warpgroups take a half of every stage of k each: while the MMA of a
+// group's piece runs, it dequantises the next.  A handshake costs 150 to 250
+// cycles and 64 weights about 300, so pieces are as large as registers allow.
+// Shares of k are CTAs of a cluster, which add their sums in order through
+// distributed shared memory.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -38,9 +39,9 @@ namespace cbs {
 namespace {
 
 constexpr int kOut = 128;                    // outputs of a CTA: tensor memory's lanes
-constexpr int kStageK = 256, kPiece = 64;    // weights along k in a stage (128 bytes a row) and in a piece
-constexpr int kPieces = kStageK / kPiece;    // of a stage; each group of warps takes two
-constexpr int kWorkers = 256, kThreads = kWorkers + 64;   // two warpgroups, an MMA warp, a TMA warp
+constexpr int kStageK = 256, kPiece = 128;   // weights along k in a stage (128 bytes a row) and in a warpgroup's piece of it
+constexpr int kPanels = kStageK / 64;        // of X in a stage: 64 inputs, 128 bytes a row
+constexpr int kWorkers = 256, kThreads = kWorkers + 96;    // two warpgroups; MMA, TMA and scales
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 
 __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
@@ -48,15 +49,19 @@ __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf
 // GROUP: weights a scale covers.  kN: input rows of a CTA.
 template <int GROUP, int kN>
 struct W4Tile {
-    static constexpr int kSubs = GROUP < kPiece ? kPiece / GROUP : 1;   // groups in a piece
-    static constexpr int kW = kOut * 128, kX = kPieces * kN * 128;      // a stage's weights; inputs, 64 a panel
-    static constexpr int kSlot = kW + kX;
+    static constexpr int kSubs = kPiece / GROUP;                        // groups in a piece
+    static constexpr int kW = kOut * 128, kX = kPanels * kN * 128;      // a stage's weights; inputs
+    static constexpr int kGroups = kStageK / GROUP;
+    static constexpr int kS = kGroups * kOut * 4;                       // scale << 16 | zero point
+    static constexpr int kSlot = kW + kX + kS;
     static constexpr int kStages = kN == 16 ? 4 : kN == 32 ? 3 : 2;
-    // full[], x_ready[], empty[], a_ready[2][2], d_ready[2][2], drain; TMEM address, flag
-    static constexpr int kBars = kStages * kSlot, kNumBars = 3 * kStages + 9;
+    static_assert(kSlot % 1024 == 0, "operands start at multiples of 1 KB");
+    static constexpr int kScaleAhead = GROUP == 32 ? 2 : 3;             // stages whose scales are on their way
+    // full[], x_ready[], empty[], a_ready[2], d_ready[2], drain; TMEM address, flag
+    static constexpr int kBars = kStages * kSlot, kNumBars = 3 * kStages + 5;
     static constexpr int kSmem = kBars + kNumBars * 8 + 16;
-    // tensor memory: A [group][buffer][32], then the results [group][buffer][sub][kN]
-    static constexpr int kACols = 4 * (kPiece / 2), kDCols = 4 * kSubs * kN;
+    // tensor memory: A [warpgroup][64], then the results [warpgroup][sub][kN]
+    static constexpr int kACols = 2 * (kPiece / 2), kDCols = 2 * kSubs * kN;
     static constexpr int kTmem = kACols + kDCols <= 256 ? 256 : 512;
     static_assert(kACols + kDCols <= 512, "tensor memory");
     // at the end: each group's sums [2][kN][kOut + 1]
@@ -95,21 +100,21 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     const auto full = [&](int s) { return bar(s); };                          // a stage has arrived
     const auto x_ready = [&](int s) { return bar(C::kStages + s); };          // its 8-bit inputs are widened
     const auto empty = [&](int s) { return bar(2 * C::kStages + s); };        // and it has been used
-    const auto a_ready = [&](int w, int b) { return bar(3 * C::kStages + 2 * w + b); };       // a piece's operand is stored
-    const auto d_ready = [&](int w, int b) { return bar(3 * C::kStages + 4 + 2 * w + b); };   // and its sums are there
-    const uint32_t drain = bar(3 * C::kStages + 8);
+    const auto a_ready = [&](int w) { return bar(3 * C::kStages + w); };       // a piece's operand is stored
+    const auto d_ready = [&](int w) { return bar(3 * C::kStages + 2 + w); };   // and its sums are there
+    const uint32_t drain = bar(3 * C::kStages + 4);
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kBars + 8 * C::kNumBars);
     // words[0]: TMEM address; [1]: a wait ran out
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(full(s), 2);                    // TMA's, and the scales'
             ptx::mbar_init(x_ready(s), kWorkers / 32);
             ptx::mbar_init(empty(s), kWorkers / 32 + 1);   // every worker warp, and the MMAs
         }
-        for (int i = 0; i < 4; ++i) {
-            ptx::mbar_init(a_ready(i >> 1, i & 1), 4);
-            ptx::mbar_init(d_ready(i >> 1, i & 1), 1);
+        for (int w = 0; w < 2; ++w) {
+            ptx::mbar_init(a_ready(w), 4);
+            ptx::mbar_init(d_ready(w), 1);
         }
         ptx::mbar_init(drain, 1);
         ptx::fence_mbar_init();
@@ -126,8 +131,8 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const uint32_t tmem = words[0];
-    const auto t_a = [&](int w, int b) { return tmem + (uint32_t)(2 * w + b) * (kPiece / 2); };
-    const auto t_d = [&](int w, int b, int sub) { return tmem + C::kACols + (uint32_t)((2 * w + b) * C::kSubs + sub) * kN; };
+    const auto t_a = [&](int w) { return tmem + (uint32_t)w * (kPiece / 2); };
+    const auto t_d = [&](int w, int sub) { return tmem + C::kACols + (uint32_t)(w * C::kSubs + sub) * kN; };
 
     const auto wait = [&](uint32_t bar_, uint32_t parity) -> bool {
         if (ptx::mbar_wait_bounded(bar_, parity, kWaitNs)) return true;
@@ -154,18 +159,17 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             ok = wait(XI8 ? x_ready(slot) : full(slot), parity) && !lost();
             ok = __all_sync(~0u, ok);
 #pragma unroll
-            for (int pc = 0; pc < kPieces; ++pc) {
-                const int w = pc & 1, b = pc >> 1;   // two pieces a stage and group: buffers in turn
-                if (ok) ok = wait(a_ready(w, b), i & 1);
+            for (int w = 0; w < 2; ++w) {
+                if (ok) ok = wait(a_ready(w), i & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint64_t x = d_x + (uint32_t)(slot * C::kSlot + pc * kN * 128) / 16;
+                const uint64_t x = d_x + (uint32_t)(slot * C::kSlot + w * (kPiece / 64) * kN * 128) / 16;
 #pragma unroll
                 for (int k = 0; k < kPiece / 16; ++k) {
-                    constexpr int kPer = kPiece / 16 / C::kSubs;   // MMAs of a group
-                    mma_ts(lead, t_d(w, b, k / kPer), t_a(w, b) + 8 * k, x + 2u * k, idesc, k % kPer > 0);
+                    constexpr int kPer = GROUP / 16;   // MMAs of a group
+                    mma_ts(lead, t_d(w, k / kPer), t_a(w) + 8 * k, x + (uint32_t)((k >> 2) * kN * 8 + (k & 3) * 2), idesc, k % kPer > 0);
                 }
-                mma_commit(lead, d_ready(w, b));
+                mma_commit(lead, d_ready(w));
             }
             if (!ok) break;
             mma_commit(lead, empty(slot));
@@ -182,12 +186,12 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             for (int i = 0; i < ns; ++i) {
                 if (!wait(empty(slot), parity) || lost()) break;
                 const uint32_t at = sbase + slot * C::kSlot;
-                ptx::mbar_arrive_expect_tx(full(slot), XI8 ? C::kW : C::kSlot);
+                ptx::mbar_arrive_expect_tx(full(slot), XI8 ? C::kW : C::kW + C::kX);
                 ptx::tma_load_2d(at, &tm_w, full(slot), (st0 + i) * (kStageK / 2), n0);
                 if (!XI8)
 #pragma unroll
-                    for (int x = 0; x < kPieces; ++x)
-                        ptx::tma_load_2d(at + C::kW + x * kN * 128, &tm_x, full(slot), (st0 + i) * kStageK + x * kPiece, m0);
+                    for (int x = 0; x < kPanels; ++x)
+                        ptx::tma_load_2d(at + C::kW + x * kN * 128, &tm_x, full(slot), (st0 + i) * kStageK + x * 64, m0);
                 ++done;
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
@@ -195,24 +199,69 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 for (int x = max(0, done - C::kStages); x < done; ++x)
                     ptx::mbar_wait_bounded(full(x % C::kStages), (x / C::kStages) & 1, kWaitNs);
         }
-    } else {
-        // ------------------------------------------------------- workers
-        const int n = min(n0 + row, L.n - 1);   // outputs past the end repeat the last one's scales
-        // Scales and zero points of this thread's next pieces, as loaded, a stage ahead.
-        struct Scale { uint16_t s; uint8_t z; };
-        Scale sz[2][C::kSubs];
-        const auto load_scales = [&](int i, int b) {
-            const int k = (st0 + i) * kStageK + (2 * b + wg) * kPiece;
+    } else if (warp == 10) {
+        // ------------------------------------------------------- scales
+        // Four outputs a lane, some stages ahead in registers: they come from HBM a
+        // row of [k / group][n] at a time, later than the threads that need them
+        // could ask.
+        constexpr int kAhead = C::kScaleAhead;
+        uint2 s4[kAhead][C::kGroups];      // four bf16 scales
+        uint32_t z4[kAhead][C::kGroups];   // four zero points
+        const int n = n0 + 4 * lane;
+        const bool whole = L.n % 4 == 0 && n + 4 <= L.n;   // then both loads are aligned
+        const uint16_t *sp = static_cast<const uint16_t *>(L.scales) + n;
+        const uint8_t *zp = L.zeros + n;
+        const auto load = [&](int i, uint2 (&s)[C::kGroups], uint32_t (&z)[C::kGroups]) {
 #pragma unroll
-            for (int u = 0; u < C::kSubs; ++u) {
-                sz[b][u] = Scale{0, 8};
-                if (i < ns && k + u * GROUP < L.k) {
-                    const size_t at = (size_t)(k / GROUP + u) * L.n + n;
-                    sz[b][u].s = __ldg(static_cast<const uint16_t *>(L.scales) + at);
-                    if (L.zeros) sz[b][u].z = __ldg(L.zeros + at);
+            for (int gr = 0; gr < C::kGroups; ++gr) {
+                const int k = (st0 + i) * kStageK + gr * GROUP;
+                s[gr] = make_uint2(0u, 0u);   // groups past k: nothing
+                z[gr] = 0x08080808u;
+                if (i >= ns || k >= L.k) continue;
+                const size_t at = (size_t)(k / GROUP) * L.n;
+                if (whole) {
+                    s[gr] = __ldg(reinterpret_cast<const uint2 *>(sp + at));
+                    if (L.zeros) z[gr] = __ldg(reinterpret_cast<const uint32_t *>(zp + at));
+                } else {
+                    uint32_t a[4], b = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int off = min(n + x, L.n - 1) - n;   // outputs past the end repeat the last one's
+                        a[x] = __ldg(sp + at + off);
+                        if (L.zeros) b |= (uint32_t)__ldg(zp + at + off) << (8 * x);
+                    }
+                    s[gr] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+                    if (L.zeros) z[gr] = b;
                 }
             }
         };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(i, s4[i], z4[i]);
+        int slot = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        for (int i0 = 0; i0 < ns && ok; i0 += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (i0 + u >= ns) break;
+                ok = __all_sync(~0u, wait(empty(slot), parity));
+                if (!ok) break;
+                uint4 *to = reinterpret_cast<uint4 *>(smem + slot * C::kSlot + C::kW + C::kX) + lane;
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    const uint2 s = s4[u][gr];
+                    const uint32_t z = z4[u][gr] & 0x0f0f0f0fu;
+                    to[gr * (kOut / 4)] = make_uint4(s.x << 16 | (z & 15u), (s.x & 0xffff0000u) | (z >> 8 & 15u),
+                                                     s.y << 16 | (z >> 16 & 15u), (s.y & 0xffff0000u) | z >> 24);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(full(slot));
+                load(i0 + u + kAhead, s4[u], z4[u]);
+                if (++slot == C::kStages) slot = 0, parity ^= 1;
+            }
+        }
+    } else {
+        // ------------------------------------------------------- workers
         // 8-bit inputs: 16 codes a unit, a stage ahead.
         constexpr int kXPer = XI8 ? kN * 16 / kWorkers : 1;
         uint4 xr[kXPer];
@@ -225,29 +274,27 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                     xr[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(L.x) + (size_t)m * L.k + k));
             }
         };
-        load_scales(0, 0);
-        load_scales(0, 1);
         if (XI8) load_x(0);
-        float sc[2][C::kSubs];
-        // The sums of the piece in buffer b, scaled into the totals.
-        const auto take = [&](int b) {
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        float sc[C::kSubs];
+        // The sums of the group's last piece, scaled into the totals.
+        const auto take = [&] {
 #pragma unroll
             for (int u = 0; u < C::kSubs; ++u)
 #pragma unroll
                 for (int q = 0; q < kN / 16; ++q) {
                     uint32_t v[16];
-                    ptx::tmem_ld16(t_d(wg, b, u) + ((uint32_t)(warp & 3) << 21) + 16 * q, v);
+                    ptx::tmem_ld16(t_d(wg, u) + lanes + 16 * q, v);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) total[16 * q + e] = fmaf(__uint_as_float(v[e]), sc[b][u], total[16 * q + e]);
+                    for (int e = 0; e < 16; ++e) total[16 * q + e] = fmaf(__uint_as_float(v[e]), sc[u], total[16 * q + e]);
                 }
         };
         int slot = 0;
         uint32_t parity = 0;
         bool ok = true;
         for (int i = 0; i < ns; ++i) {
-            ok = wait(full(slot), parity) && !lost();
-            ok = __all_sync(~0u, ok);
+            ok = __all_sync(~0u, wait(full(slot), parity));
             if (!ok) break;
             const unsigned char *wt = smem + slot * C::kSlot + row * 128;
             if constexpr (XI8) {
@@ -272,52 +319,50 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 if (lane == 0) ptx::mbar_arrive(x_ready(slot));
                 load_x(i + 1);
             }
+            uint32_t sz[C::kSubs];
+#pragma unroll
+            for (int u = 0; u < C::kSubs; ++u)
+                sz[u] = reinterpret_cast<const uint32_t *>(smem + slot * C::kSlot + C::kW + C::kX)[(wg * C::kSubs + u) * kOut + row];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int pc = 2 * b + wg;
-                uint32_t w[8], a[32], zp[C::kSubs];
+                uint32_t w[8], a[32];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(wt + (((2 * pc + q) ^ (row & 7)) << 4));
+                    const uint4 y = *reinterpret_cast<const uint4 *>(wt + (((4 * wg + 2 * b + q) ^ (row & 7)) << 4));
                     w[4 * q] = y.x; w[4 * q + 1] = y.y; w[4 * q + 2] = y.z; w[4 * q + 3] = y.w;
                 }
-                if (b == 1) {
-                    __syncwarp();   // the warp has read all it needs of the stage's weights
-                    if (lane == 0) ptx::mbar_arrive(empty(slot));
-                }
-#pragma unroll
-                for (int u = 0; u < C::kSubs; ++u) zp[u] = 0x43004300u | (sz[b][u].z & 15u) * 0x00010001u;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        a[4 * q + p] = frag::sub_bf16x2(((w[q] >> (4 * p)) & 0x000f000fu) | 0x43004300u, zp[q * 8 / (kPiece / C::kSubs)]);
-                tmem_st32(t_a(wg, b) + ((uint32_t)(warp & 3) << 21), a);
-                tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(a_ready(wg, b));
-                // While its MMA runs: the sums of the piece before.
-                if (b == 1 || i > 0) {
-                    ok = wait(d_ready(wg, b ^ 1), (b ? i : i - 1) & 1);
-                    ok = __all_sync(~0u, ok);
+                        a[4 * q + p] = frag::sub_bf16x2(((w[q] >> (4 * p)) & 0x000f000fu) | 0x43004300u,
+                                                        __byte_perm(sz[(64 * b + 8 * q) / GROUP], 0x43u, 0x4040));   // 128 + z
+                if (b == 0 && i > 0) {
+                    // The operand's place is free once the last piece's MMA is done,
+                    // and its sums are there.
+                    ok = __all_sync(~0u, wait(d_ready(wg), (i - 1) & 1));
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    take(b ^ 1);
-                    ptx::tc_fence_before();
                 }
-#pragma unroll
-                for (int u = 0; u < C::kSubs; ++u) sc[b][u] = __uint_as_float((uint32_t)sz[b][u].s << 16);
-                load_scales(i + 1, b);
+                tmem_st32(t_a(wg) + lanes + 32 * b, a);
+                if (b == 0 && i > 0) take();
             }
             if (!ok) break;
+            tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(a_ready(wg));
+                ptx::mbar_arrive(empty(slot));   // the warp has read all it needs of the stage
+            }
+#pragma unroll
+            for (int u = 0; u < C::kSubs; ++u) sc[u] = __uint_as_float(sz[u] & 0xffff0000u);
             if (++slot == C::kStages) slot = 0, parity ^= 1;
         }
         if (ok && ns > 0) {
-            ok = wait(d_ready(wg, 1), (ns - 1) & 1);
-            __syncwarp();
+            ok = __all_sync(~0u, wait(d_ready(wg), (ns - 1) & 1));
             ptx::tc_fence_after();
-            if (__all_sync(~0u, ok)) take(1);
+            if (ok) take();
         }
     }
     ptx::tc_fence_before();
@@ -381,12 +426,20 @@ cbs_status launch_w4_one(const W4Launch &L, cudaStream_t s) {
         if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (inputs) failed (%d)", (int)r);
     }
 
-    // Shares of k: as many CTAs of a cluster as give every SM two CTAs, each of
-    // them two stages at least.
+    // Shares of k, by what was measured: an SM's CTAs take 0.72 us a stage between
+    // them (two run at a time), a CTA's start and end 1.6 us (two at a time), a
+    // cluster of eight half a microsecond more.  16384 x 8192: 31, 28, 34, 41 us for
+    // 1, 2, 4, 8 shares; 6144 x 4096: 17.5, 10.9, 9.5, 11.4; 1001 x 2048: 13.9, 9.4,
+    // 6.8, 6.1.
     const int tiles = (L.n + kOut - 1) / kOut, stages = (L.k + kStageK - 1) / kStageK;
-    const int row_tiles = (L.rows + kN - 1) / kN;
+    const int row_tiles = (L.rows + kN - 1) / kN, sms = current_device_sms();
     int split = 1;
-    while (split < 8 && (long long)tiles * row_tiles * split < 2ll * current_device_sms() && stages >= 4 * split) split *= 2;
+    long long best = 0;
+    for (int x = 1; x <= 8 && x <= stages; x *= 2) {
+        const long long ctas = ((long long)tiles * row_tiles * x + sms - 1) / sms;
+        const long long cost = ctas * ((stages + x - 1) / x) * 72 + (ctas + 1) / 2 * 160 + (x == 8 ? 50 : 0);
+        if (x == 1 || cost < best) best = cost, split = x;
+    }
     auto kern = w4_kernel<GROUP, kN, XI8>;
     cudaError_t e = set_max_dyn_smem(kern, C::kSmem);
     if (e == cudaSuccess) {
@@ -411,7 +464,7 @@ cbs_status launch_w4_one(const W4Launch &L, cudaStream_t s) {
 template <int GROUP, bool XI8>
 cbs_status launch_w4_rows(const W4Launch &L, cudaStream_t s) {
     if (L.rows <= 16) return launch_w4_one<GROUP, 16, XI8>(L, s);
-    // (groups of 32 have two results a piece: 64 columns of each would not fit tensor memory)
+    // (groups of 32 have four results a piece: 64 columns of each would not fit tensor memory)
     if (L.rows <= 32 || GROUP == 32) return launch_w4_one<GROUP, 32, XI8>(L, s);
     return launch_w4_one<GROUP, GROUP == 32 ? 32 : 64, XI8>(L, s);
 }
