@@ -17,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libcbs.so")
+TOKENS = os.path.join(OUT, "_tokens.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -76,5 +77,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_tokens(verbose: bool = False) -> str:
+    """The token operators' Python calls (csrc/tokens_py.cpp), linked against
+    libcbs.so beside it.  Needs PyTorch's headers, which come with it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    os.makedirs(OUT, exist_ok=True)
+    src = os.path.join(CSRC, "tokens_py.cpp")
+    stamp = f"{torch.__version__} {sys.version}"
+    stamp_path = TOKENS + ".stamp"
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "cbs.h")))
+    if os.path.exists(TOKENS) and os.path.getmtime(TOKENS) >= newest and os.path.exists(stamp_path) and \
+            open(stamp_path).read() == stamp:
+        return TOKENS
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = TOKENS + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in inc for a in ("-isystem", i)], src, "-o", tmp, "-L" + OUT, "-l:libcbs.so", "-Wl,-rpath,$ORIGIN",
+           *["-L" + p for p in cpp_extension.library_paths()], "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
+    if verbose and res.stderr:
+        sys.stderr.write(res.stderr)
+    os.replace(tmp, TOKENS)
+    with open(stamp_path, "w") as f:
+        f.write(stamp)
+    return TOKENS
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_tokens(verbose="-v" in sys.argv))

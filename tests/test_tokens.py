@@ -11,6 +11,13 @@ from conv_bn_silu_gb300 import tokens
 from tests import token_refs as refs
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def token_calls(cuda_lib):
+    from conv_bn_silu_gb300 import build
+    build.build_tokens()
+
 U = 2.0 ** -24    # rounding to float moves a value by at most this share of it
 UB = 2.0 ** -8    # to bfloat16 (eight significant bits)
 
@@ -229,3 +236,64 @@ def test_linear_w4_not_finite_inputs_stay_in_their_row(cuda_lib):
     layer = tokens.LinearW4.quantize(torch.randn((40, 256), generator=gen(2)).cuda(), 64)
     out = layer(x.cuda()).cpu()
     assert out[1].isnan().all() and out[0].isfinite().all() and out[2].isfinite().all()
+
+
+def test_calls_refuse_unfit_tensors(cuda_lib):
+    """Types, shapes, layouts and devices are refused before anything runs;
+    what only the C call can tell comes back as CbsError."""
+    f32 = lambda *s: torch.zeros(s, device="cuda")
+    bf = lambda *s: torch.zeros(s, device="cuda", dtype=torch.bfloat16)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    bad = lambda f: pytest.raises(ValueError, f)
+    bad(lambda: tokens.rmsnorm(torch.zeros(2, 8), f32(8), 1e-5))
+    bad(lambda: tokens.rmsnorm(f32(2, 8).half(), f32(8), 1e-5))
+    bad(lambda: tokens.rmsnorm(f32(2, 8), f32(9), 1e-5))
+    bad(lambda: tokens.rmsnorm(f32(8, 2).t(), f32(8), 1e-5))
+    bad(lambda: tokens.rmsnorm(f32(2, 8), f32(8), 1e-5, residual=bf(2, 8)))
+    bad(lambda: tokens.rmsnorm(f32(2, 8), f32(8), 1e-5, h_out=f32(2, 8)))
+    bad(lambda: tokens.dequantize_rows(f32(2, 8), f32(2)))
+    bad(lambda: tokens.dequantize_rows(f32(2, 8).to(torch.int8), f32(2), torch.float16))
+    with pytest.raises(B.CbsError) as e:
+        tokens.rmsnorm(f32(2, 8), f32(8), -1.0)
+    assert e.value.status == B.CBS_ERR_INVALID_ARG
+    with pytest.raises(B.CbsError) as e:
+        tokens.rmsnorm(f32(3, 9).view(-1)[1:19].view(2, 9), f32(9), 1e-5)
+    assert e.value.status == B.CBS_ERR_MISALIGNED
+    layer = tokens.LinearW4.quantize(torch.randn((16, 128), device="cuda"), 64)
+    bad(lambda: layer(f32(2, 128)))
+    bad(lambda: layer(bf(2, 64)))
+    bad(lambda: layer(bf(2, 128), f32(2)))
+    bad(lambda: layer(bf(2, 128).to(torch.int8)))
+    bad(lambda: layer(bf(2, 128), out=f32(2, 15)))
+    bad(lambda: tokens.LinearW4.quantize(torch.randn((16, 100), device="cuda"), 64))
+    cache = tokens.PagedCache.empty(4, 2, 16, 64)
+    k = bf(3, 2, 64)
+    ok = (i32([0, 3]), i32([3]), i32([[0]]))
+    cache.write(k, k, *ok)
+    bad(lambda: cache.write(bf(3, 2, 32), k, *ok))
+    bad(lambda: cache.write(k, k[:2], *ok))
+    bad(lambda: cache.write(k, k, ok[0].long(), ok[1], ok[2]))
+    bad(lambda: cache.write(k, k, i32([0, 1, 3]), ok[1], ok[2]))
+    bad(lambda: cache.read(ok[1], i32([0]), 4))
+    bad(lambda: tokens.PagedCache(cache.k, cache.v))
+    attn = tokens.PagedAttention(cache, 1, 3, 16, 4)
+    bad(lambda: attn(f32(3, 4, 64), *ok))
+    bad(lambda: attn(bf(3, 2, 64), *ok))
+    bad(lambda: attn(bf(3, 4, 64), *ok, out=bf(2, 4, 64)))
+    assert attn(bf(3, 4, 64), *ok).shape == (3, 4, 64)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_nothing_to_do(cuda_lib, int8):
+    """Empty batches, rows and calls come back empty."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cache = tokens.PagedCache.empty(4, 2, 16, 64, dtype=torch.int8 if int8 else torch.bfloat16)
+    none = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    cache.write(none, none, i32([0, 0]), i32([0]), i32([[0]]))
+    k, v = cache.read(i32([0]), i32([[0]]), 3)
+    assert (k == 0).all() and (v == 0).all() and k.shape == (1, 3, 2, 64)
+    assert tokens.PagedAttention(cache, 1, 4, 16, 4)(none.new_zeros((0, 4, 64)), i32([0, 0]), i32([0]), i32([[0]])).shape == (0, 4, 64)
+    x = torch.zeros((0, 128), dtype=torch.bfloat16, device="cuda")
+    assert tokens.rmsnorm(x, torch.ones(128, device="cuda"), 1e-5, int8=int8).y.shape == (0, 128)
+    assert tokens.LinearW4.quantize(torch.randn((16, 128), device="cuda"), 64)(x).shape == (0, 16)
+    assert B.cbs_read_device_status(True, torch.cuda.current_stream().cuda_stream) == B.CBS_OK

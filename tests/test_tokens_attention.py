@@ -11,6 +11,13 @@ from tests import token_refs as refs
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(scope="module", autouse=True)
+def token_calls(cuda_lib):
+    from conv_bn_silu_gb300 import build
+    build.build_tokens()
+
+
+
 def starts_of(new):
     return [sum(new[:i]) for i in range(len(new) + 1)]
 
