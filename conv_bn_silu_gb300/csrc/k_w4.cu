@@ -44,6 +44,9 @@ constexpr int kPanels = kStageK / 64;        // of X in a stage: 64 inputs, 128 
 constexpr int kWorkers = 256, kThreads = kWorkers + 96;    // two warpgroups; MMA, TMA and scales
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 
+// Largest layer that k_w4_few.cu takes, for up to eight input rows.
+constexpr long long kFewMost = 48ll << 20;
+
 __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
 
 // GROUP: weights a scale covers.  kN: input rows of a CTA.
@@ -52,11 +55,11 @@ struct W4Tile {
     static constexpr int kSubs = kPiece / GROUP;                        // groups in a piece
     static constexpr int kW = kOut * 128, kX = kPanels * kN * 128;      // a stage's weights; inputs
     static constexpr int kGroups = kStageK / GROUP;
-    static constexpr int kS = kGroups * kOut * 4;                       // scale << 16 | zero point
+    static constexpr int kZAt = kGroups * kOut * 2;                     // scales [group][output], then zero points
+    static constexpr int kS = (kGroups * kOut * 3 + 1023) / 1024 * 1024;
     static constexpr int kSlot = kW + kX + kS;
     static constexpr int kStages = kN == 16 ? 4 : kN == 32 ? 3 : 2;
     static_assert(kSlot % 1024 == 0, "operands start at multiples of 1 KB");
-    static constexpr int kScaleAhead = GROUP == 32 ? 2 : 3;             // stages whose scales are on their way
     // full[], x_ready[], empty[], a_ready[2], d_ready[2], drain; TMEM address, flag
     static constexpr int kBars = kStages * kSlot, kNumBars = 3 * kStages + 5;
     static constexpr int kSmem = kBars + kNumBars * 8 + 16;
@@ -108,7 +111,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(full(s), 2);                    // TMA's, and the scales'
+            ptx::mbar_init(full(s), 1 + 32);               // TMA's, and the scale warp's lanes'
             ptx::mbar_init(x_ready(s), kWorkers / 32);
             ptx::mbar_init(empty(s), kWorkers / 32 + 1);   // every worker warp, and the MMAs
         }
@@ -201,65 +204,42 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         }
     } else if (warp == 10) {
         // ------------------------------------------------------- scales
-        // Four outputs a lane, some stages ahead in registers: they come from HBM a
-        // row of [k / group][n] at a time, later than the threads that need them
-        // could ask.
-        constexpr int kAhead = C::kScaleAhead;
-        uint2 s4[kAhead][C::kGroups];      // four bf16 scales
-        uint32_t z4[kAhead][C::kGroups];   // four zero points
+        // Four outputs a lane, copied as far ahead as the ring is deep: they come
+        // from HBM a row of [k / group][n] at a time, later than the threads that
+        // need them could ask.
         const int n = n0 + 4 * lane;
-        const bool whole = L.n % 4 == 0 && n + 4 <= L.n;   // then both loads are aligned
-        const uint16_t *sp = static_cast<const uint16_t *>(L.scales) + n;
-        const uint8_t *zp = L.zeros + n;
-        const auto load = [&](int i, uint2 (&s)[C::kGroups], uint32_t (&z)[C::kGroups]) {
+        const bool whole = L.n % 4 == 0 && n + 4 <= L.n;   // then both copies are aligned
+        const uint16_t *sp = static_cast<const uint16_t *>(L.scales);
+        int slot = 0;
+        uint32_t parity = 1;
+        for (int i = 0; i < ns; ++i) {
+            if (!__all_sync(~0u, wait(empty(slot), parity))) break;
+            unsigned char *to = smem + slot * C::kSlot + C::kW + C::kX;
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr) {
                 const int k = (st0 + i) * kStageK + gr * GROUP;
-                s[gr] = make_uint2(0u, 0u);   // groups past k: nothing
-                z[gr] = 0x08080808u;
-                if (i >= ns || k >= L.k) continue;
-                const size_t at = (size_t)(k / GROUP) * L.n;
+                const bool in = k < L.k;   // groups past k: scale zero
+                const size_t at = (size_t)(in ? k / GROUP : 0) * L.n;
+                unsigned char *s_to = to + (gr * kOut + 4 * lane) * 2, *z_to = to + C::kZAt + gr * kOut + 4 * lane;
                 if (whole) {
-                    s[gr] = __ldg(reinterpret_cast<const uint2 *>(sp + at));
-                    if (L.zeros) z[gr] = __ldg(reinterpret_cast<const uint32_t *>(zp + at));
+                    ptx::cp_async_8(ptx::smem_u32(s_to), sp + at + n, in ? 8 : 0);
+                    if (L.zeros)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(z_to)), "l"(L.zeros + at + n), "r"(in ? 4 : 0) : "memory");
                 } else {
-                    uint32_t a[4], b = 0;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int off = min(n + x, L.n - 1) - n;   // outputs past the end repeat the last one's
-                        a[x] = __ldg(sp + at + off);
-                        if (L.zeros) b |= (uint32_t)__ldg(zp + at + off) << (8 * x);
+                        const int o = min(n + x, L.n - 1);   // outputs past the end repeat the last one's
+                        reinterpret_cast<uint16_t *>(s_to)[x] = in ? __ldg(sp + at + o) : (uint16_t)0;
+                        if (L.zeros) z_to[x] = in ? __ldg(L.zeros + at + o) : (uint8_t)0;
                     }
-                    s[gr] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
-                    if (L.zeros) z[gr] = b;
                 }
             }
-        };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(i, s4[i], z4[i]);
-        int slot = 0;
-        uint32_t parity = 1;
-        bool ok = true;
-        for (int i0 = 0; i0 < ns && ok; i0 += kAhead) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (i0 + u >= ns) break;
-                ok = __all_sync(~0u, wait(empty(slot), parity));
-                if (!ok) break;
-                uint4 *to = reinterpret_cast<uint4 *>(smem + slot * C::kSlot + C::kW + C::kX) + lane;
-#pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) {
-                    const uint2 s = s4[u][gr];
-                    const uint32_t z = z4[u][gr] & 0x0f0f0f0fu;
-                    to[gr * (kOut / 4)] = make_uint4(s.x << 16 | (z & 15u), (s.x & 0xffff0000u) | (z >> 8 & 15u),
-                                                     s.y << 16 | (z >> 16 & 15u), (s.y & 0xffff0000u) | z >> 24);
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full(slot));
-                load(i0 + u + kAhead, s4[u], z4[u]);
-                if (++slot == C::kStages) slot = 0, parity ^= 1;
-            }
+            if (whole) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full(slot)) : "memory");
+            else ptx::mbar_arrive(full(slot));
+            if (++slot == C::kStages) slot = 0, parity ^= 1;
         }
+        ptx::cp_async_commit();
+        ptx::cp_async_wait<0>();   // nothing leaves while a copy is in flight
     } else {
         // ------------------------------------------------------- workers
         // 8-bit inputs: 16 codes a unit, a stage ahead.
@@ -319,10 +299,15 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 if (lane == 0) ptx::mbar_arrive(x_ready(slot));
                 load_x(i + 1);
             }
-            uint32_t sz[C::kSubs];
+            uint16_t sn[C::kSubs];
+            uint32_t zp[C::kSubs];   // 128 + z, a pair of bf16
 #pragma unroll
-            for (int u = 0; u < C::kSubs; ++u)
-                sz[u] = reinterpret_cast<const uint32_t *>(smem + slot * C::kSlot + C::kW + C::kX)[(wg * C::kSubs + u) * kOut + row];
+            for (int u = 0; u < C::kSubs; ++u) {
+                const unsigned char *from = smem + slot * C::kSlot + C::kW + C::kX;
+                const int at = (wg * C::kSubs + u) * kOut + row;
+                sn[u] = reinterpret_cast<const uint16_t *>(from)[at];
+                zp[u] = 0x43004300u | (L.zeros ? (from[C::kZAt + at] & 15u) * 0x00010001u : 0x00080008u);
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 uint32_t w[8], a[32];
@@ -335,8 +320,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 for (int q = 0; q < 8; ++q)
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        a[4 * q + p] = frag::sub_bf16x2(((w[q] >> (4 * p)) & 0x000f000fu) | 0x43004300u,
-                                                        __byte_perm(sz[(64 * b + 8 * q) / GROUP], 0x43u, 0x4040));   // 128 + z
+                        a[4 * q + p] = frag::sub_bf16x2(((w[q] >> (4 * p)) & 0x000f000fu) | 0x43004300u, zp[(64 * b + 8 * q) / GROUP]);
                 if (b == 0 && i > 0) {
                     // The operand's place is free once the last piece's MMA is done,
                     // and its sums are there.
@@ -356,7 +340,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 ptx::mbar_arrive(empty(slot));   // the warp has read all it needs of the stage
             }
 #pragma unroll
-            for (int u = 0; u < C::kSubs; ++u) sc[u] = __uint_as_float(sz[u] & 0xffff0000u);
+            for (int u = 0; u < C::kSubs; ++u) sc[u] = __uint_as_float((uint32_t)sn[u] << 16);
             if (++slot == C::kStages) slot = 0, parity ^= 1;
         }
         if (ok && ns > 0) {
@@ -506,6 +490,7 @@ __global__ void quantize_w4_kernel(const float *__restrict__ w, int n, int k, in
 }  // namespace
 
 cbs_status launch_w4(const W4Launch &L, cudaStream_t s) {
+    if (L.rows <= 8 && (long long)L.n * L.k <= kFewMost) return cuda_check(launch_w4_few(L, s), "4-bit product launch");
     switch (L.group) {
     case 32: return L.x_int8 ? launch_w4_rows<32, true>(L, s) : launch_w4_rows<32, false>(L, s);
     case 64: return L.x_int8 ? launch_w4_rows<64, true>(L, s) : launch_w4_rows<64, false>(L, s);

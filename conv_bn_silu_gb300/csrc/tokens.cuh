@@ -73,6 +73,7 @@ struct W4Launch {
     int rows, n, k, group, x_int8, out_bf16, act;
 };
 cbs_status launch_w4(const W4Launch &L, cudaStream_t s);
+cudaError_t launch_w4_few(const W4Launch &L, cudaStream_t s);   // up to eight rows
 cudaError_t launch_quantize_w4(const float *w, int n, int k, int group, uint8_t *packed, void *scales, cudaStream_t s);
 
 struct AttnLaunch {
