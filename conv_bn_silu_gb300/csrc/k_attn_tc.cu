@@ -116,19 +116,20 @@ __device__ __forceinline__ float2 split(F2 a) {
 template <bool I8, bool MASK>
 __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref, const float *ks, const float *vs, int first,
                                           int end, uint32_t (&p)[kCols / 2], float &top, float &sum) {
+    constexpr int kPart = 16;   // of 32 columns at a time, registers spilled
     const F2 scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
     F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
     float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int q = 0; q < kCols / 32; ++q) {
-        uint32_t v[32];
-        tmem_ld32(taddr + 32 * q, v);
+    for (int q = 0; q < kCols / kPart; ++q) {
+        uint32_t v[kPart];
+        tmem_ld16(taddr + kPart * q, v);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
+        for (int e = 0; e < kPart; e += 4) {
             F2 k2[2] = {scale2, scale2}, w2[2];
             if constexpr (I8) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(ks + 32 * q + e), v4 = *reinterpret_cast<const float4 *>(vs + 32 * q + e);
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + kPart * q + e), v4 = *reinterpret_cast<const float4 *>(vs + kPart * q + e);
                 k2[0] = pair(k4.x, k4.y); k2[1] = pair(k4.z, k4.w);
                 w2[0] = pair(v4.x, v4.y); w2[1] = pair(v4.z, v4.w);
             }
@@ -136,7 +137,7 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
             for (int x = 0; x < 2; ++x) {
                 float2 t = split(fma2(pair(__uint_as_float(v[e + 2 * x]), __uint_as_float(v[e + 2 * x + 1])), k2[x], ref2));
                 if constexpr (MASK) {
-                    const int col = 32 * q + e + 2 * x;
+                    const int col = kPart * q + e + 2 * x;
                     if (col < first || col >= end) t.x = -INFINITY;
                     if (col + 1 < first || col + 1 >= end) t.y = -INFINITY;
                 }
@@ -149,7 +150,7 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
                     if (t.x == -INFINITY) y.x = 0.0f;
                     if (t.y == -INFINITY) y.y = 0.0f;
                 }
-                p[16 * q + (e >> 1) + x] = frag::pack_bf16(y.x, y.y);
+                p[kPart / 2 * q + (e >> 1) + x] = frag::pack_bf16(y.x, y.y);
             }
         }
     }
