@@ -29,16 +29,17 @@ namespace {
 
 constexpr int kHalf = 128, kRows = kAttnChunkRows, kTile = kAttnChunkKeys;   // rows of a half and of a CTA; keys of a tile
 static_assert(kRows == 2 * kHalf, "two halves");
+constexpr int kMostRanges = kAttnChunkSplitMost;
 constexpr int kCols = kTile / 2;              // keys of a tile a softmax thread takes
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 template <int D, bool I8>
 struct Chunk {
-    // Warp 0: MMA issue; 1-3: TMA and two that check values (bf16), or
-    // converters (int8, with 20-23); 4-19: softmax, eight warps a half (two
+    // Warp 0: MMA issue; 1: loads; 2, 3: check values (bf16), or converters (int8,
+    // with 20 and 21); 4-19: softmax, eight warps a half (two
     // threads a row, 64 keys of the tile each).
-    static constexpr int kThreads = I8 ? 768 : 640;
-    static constexpr int kConverters = 7;
+    static constexpr int kThreads = I8 ? 704 : 640;
+    static constexpr int kConverters = 4;
     static constexpr int kPanel = kTile * 128;                 // 64 dimensions of 128 rows
     static constexpr int kOperand = (D / 64) * kPanel;         // one Q half, K tile or V tile
     // A ring of K and V tiles in turn (K of tile i is its item 2 i, V 2 i + 1): as
@@ -46,20 +47,26 @@ struct Chunk {
     // arrive and as long to use.
     static constexpr int kSlots = D == 64 ? 8 : I8 ? 4 : 5;
     static constexpr int kQ = 0, kRing = 2 * kOperand;
+    // int8: codes on their way, 64 keys' rows of K or V a piece, four pieces a tile.
+    static constexpr int kPieceKeys = kTile / 2, kPiece = kPieceKeys * D, kPieces = I8 ? (D == 64 ? 8 : 3) : 0;
+    static constexpr int kRaw = kRing + kSlots * kOperand;
     // int8: the scales of four tiles' keys, [K, V][tile % 4][128] floats.  Tile i's
     // are written once its V tile's slot is free, when V of tile i - kSlots / 2 (at
     // least i - 4) has been used, and so have that tile's scales.
     static constexpr int kScaleTiles = 4;
-    static constexpr int kScale = kRing + kSlots * kOperand;
+    static constexpr int kScale = kRaw + kPieces * kPiece;
     static constexpr int kShare = kScale + (I8 ? 2 * kScaleTiles * kTile * 4 : 0);   // a row's threads exchange here
     static constexpr int kBars = kShare + 2 * kRows * 4;
     // V tiles checked but not yet waited for: while the MMAs of tile i wait, items
     // up to 2 i + kSlots have had their slots, V of tile i + (kSlots - 1) / 2 the last.
     static constexpr int kReady = 4;
     static_assert((kSlots - 1) / 2 < kReady, "a check's turn comes after the last one's was seen");
-    // q_full[2], s_full[2], p_ready[2], pv_done[2], drain, ready[], full[], empty[];
+    // q_full[2], s_full[2], p_ready[2], pv_done[2], drain, ready[], full[], empty[], raw_full[], raw_empty[];
     // then the TMEM address and flags.
-    static constexpr int kNumBars = 9 + kReady + 2 * kSlots;
+    // The join's places in Q's: each row's maximum and sum, then the ranges' factors.
+    static constexpr int kJoinStats = 0, kJoinFacs = kRows * 8;
+    static_assert(kJoinFacs + (kMostRanges + 1) * kRows * 4 <= 2 * kOperand && 2 * kHalf * D * 4 <= kSlots * kOperand, "join");
+    static constexpr int kNumBars = 9 + kReady + 2 * kSlots + 2 * kPieces;
     static constexpr int kSmem = kBars + kNumBars * 8 + 16;
     static_assert(kSmem <= kMaxDynSmem, "ring");
     static_assert(!I8 || (kSlots % 2 == 0 && kSlots / 2 <= kScaleTiles), "scales are free when V's slot is");
@@ -116,14 +123,15 @@ __device__ __forceinline__ float2 split(F2 a) {
 template <bool I8, bool MASK>
 __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref, const float *ks, const float *vs, int first,
                                           int end, uint32_t (&p)[kCols / 2], float &top, float &sum) {
-    constexpr int kPart = 16;   // of 32 columns at a time, registers spilled
+    constexpr int kPart = I8 ? 8 : 16;   // columns at a time: of more, registers spilled
     const F2 scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
     F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
     float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int q = 0; q < kCols / kPart; ++q) {
         uint32_t v[kPart];
-        tmem_ld16(taddr + kPart * q, v);
+        if constexpr (I8) ptx::tmem_ld8(taddr + kPart * q, v);
+        else ptx::tmem_ld16(taddr + kPart * q, v);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < kPart; e += 4) {
@@ -164,14 +172,14 @@ template <bool I8, bool MASK>
 __device__ __forceinline__ float tile_top(uint32_t taddr, float scale, const float *ks, int first, int end) {
     float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int q = 0; q < kCols / 32; ++q) {
-        uint32_t v[32];
-        tmem_ld32(taddr + 32 * q, v);
+    for (int q = 0; q < kCols / 16; ++q) {
+        uint32_t v[16];
+        ptx::tmem_ld16(taddr + 16 * q, v);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            float t = __uint_as_float(v[e]) * (I8 ? ks[32 * q + e] : scale);
-            if (MASK && (32 * q + e < first || 32 * q + e >= end)) t = -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+            float t = __uint_as_float(v[e]) * (I8 ? ks[16 * q + e] : scale);
+            if (MASK && (16 * q + e < first || 16 * q + e >= end)) t = -INFINITY;
             tops[e & 1] = fmaxf(tops[e & 1], t);
         }
     }
@@ -217,9 +225,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const auto ready = [&](int i) { return bar(9 + i % C::kReady); };
     const auto full = [&](int s) { return bar(9 + C::kReady + s); };                // an item has arrived
     const auto empty = [&](int s) { return bar(9 + C::kReady + C::kSlots + s); };   // and been used
+    const auto raw_full = [&](int s) { return bar(9 + C::kReady + 2 * C::kSlots + s); };   // int8: a piece's codes
+    const auto raw_empty = [&](int s) { return bar(9 + C::kReady + 2 * C::kSlots + C::kPieces + s); };
     const auto slot_at = [&](int s) { return C::kRing + s * C::kOperand; };
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(sgen + C::kBars + 8 * C::kNumBars);
-    // words[0]: TMEM address; [1]: a wait ran out; [2]: a value is not finite; [3]: the join's flag
+    // words[0]: TMEM address; [1]: a wait ran out; [2]: a value is not finite
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -233,9 +243,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             ptx::mbar_init(full(s), I8 ? C::kConverters : 1);
             ptx::mbar_init(empty(s), 1);
         }
+        for (int s = 0; s < C::kPieces; ++s) {
+            ptx::mbar_init(raw_full(s), 1);
+            ptx::mbar_init(raw_empty(s), C::kConverters);
+        }
         ptx::mbar_init(drain, 1);
         ptx::fence_mbar_init();
-        words[1] = words[2] = words[3] = 0;
+        words[1] = words[2] = 0;
     }
     if (warp == 1) {
         ptx::tmem_alloc(sbase + C::kBars + 8 * C::kNumBars, 512);
@@ -395,108 +409,138 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ready(i));
         }
+    } else if (I8 && warp == 1) {
+        // ------------------------------------------------------- codes' loads
+        if constexpr (I8) {
+            using P = Turn<C::kPieces>;
+            const int run = min(1 << c.page_shift, C::kPieceKeys), runs = C::kPieceKeys / run;   // of a page's consecutive rows
+            // Lane x < 2 runs: the page of tile i's position x * run as loaded (two
+            // tiles ahead), and from it the pool's row (-1: no row that anybody sees).
+            const auto needed = [&](int i) {
+                const int pos = key0 + i * kTile + lane * run;
+                return i < n && lane < 2 * runs && pos + run > all.lo && pos < all.hi;
+            };
+            const auto page_entry = [&](int i) -> int {
+                return needed(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + lane * run) >> c.page_shift)) : 0;
+            };
+            int entry = page_entry(0), entry_next = page_entry(1), done = 0;
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                long long row = -1;
+                if (needed(i)) {
+                    if ((unsigned)entry < (unsigned)c.num_pages)
+                        row = ((entry * c.kv_heads + head) << c.page_shift) + ((key0 + i * kTile + lane * run) & ((1 << c.page_shift) - 1));
+                    else
+                        atomicOr(c.status, kStatusBadIndex);
+                }
+                entry = entry_next;
+                entry_next = page_entry(i + 2);
+                const unsigned with = __ballot_sync(~0u, row >= 0);
+#pragma unroll
+                for (int piece = 0; piece < 4 && ok; ++piece) {
+                    const P x(4 * i + piece);
+                    const int first = (piece & 1) * runs;
+                    if (lane == 0) {
+                        ok = wait(raw_empty(x.slot), x.parity ^ 1) && !lost();
+                        if (ok) ptx::mbar_arrive_expect_tx(raw_full(x.slot), __popc(with >> first & ((1u << runs) - 1u)) * run * D);
+                    }
+                    ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+                    if (ok && row >= 0 && lane >= first && lane < first + runs)
+                        bulk_load(sbase + C::kRaw + x.slot * C::kPiece + (lane - first) * run * D,
+                                  static_cast<const char *>(piece >> 1 ? c.v : c.k) + row * D, run * D, raw_full(x.slot));
+                    if (ok) ++done;
+                }
+            }
+            if (lane == 0 && lost()) {   // the copies in flight land before the CTA leaves
+                for (int x = max(0, done - C::kPieces); x < done; ++x) ptx::mbar_wait_bounded(raw_full(P(x).slot), P(x).parity, kWaitNs);
+            }
+        }
     } else if (I8 && (warp < 4 || warp >= 20)) {
         // ------------------------------------------------------- converters
         if constexpr (I8) {
-            // A tile is four pieces: 64 keys' rows of K, the other 64, then V's.
-            // Codes are loaded two pieces ahead.
-            constexpr int kU = D / 16;                       // 16-code units of a row
-            constexpr int kRowsOnce = 32 / kU;               // rows a warp takes at once (of one page: 4 or 8)
-            constexpr int kPiece = kTile / 2, kPer = (kPiece / kRowsOnce + C::kConverters - 1) / C::kConverters;
-            const int cw = warp < 4 ? warp - 1 : warp - 17, u = lane % kU, sub = lane / kU;
-            uint4 raw[2][kPer];
-            float sc[2] = {};
-            // Lane x < 8: the page of tile i's position 16 x as loaded, and from it
-            // the pool's row of that position (-1: no such page).
-            const auto needed = [&](int i) { return i < n && lane < kTile / 16 && key0 + i * kTile + lane * 16 < rs.len; };
+            using P = Turn<C::kPieces>;
+            constexpr int kU = D / 16;                                  // 16-code units of a row
+            constexpr int kLanes = C::kConverters * 32, kRowsOnce = kLanes / kU, kPer = C::kPieceKeys / kRowsOnce;
+            static_assert(kRowsOnce % 8 == 0 && kPer * kRowsOnce == C::kPieceKeys && kLanes == kTile, "a thread's rows are alike in the swizzle");
+            const int t = (warp < 4 ? warp - 2 : warp - 18) * 32 + lane, u = t % kU, row0 = t / kU;
+            // Where a unit's first 16 bytes go in an operand.  Lanes of the second 64
+            // dimensions write their upper 8 first: the eight lanes of a row are then
+            // in eight different banks' sixteen bytes.
+            const uint32_t second = D == 128 ? u >> 2 : 0;
+            const uint32_t place = C::kRing + (u >> 2) * C::kPanel + row0 * 128 + ((((u & 3) * 2 + second) ^ (row0 & 7)) << 4);
+            // Thread t takes the scales of tile i's key t: the page two tiles ahead, the scales one.
+            const auto sees = [&](int i) {
+                const int pos = key0 + i * kTile + t;
+                return i < n && pos >= all.lo && pos < all.hi;
+            };
             const auto page_entry = [&](int i) -> int {
-                return needed(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + lane * 16) >> c.page_shift)) : 0;
+                return sees(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + t) >> c.page_shift)) : -1;
             };
-            const auto first_row = [&](int i, int p) -> int {
-                if (!needed(i)) return -1;
-                if ((unsigned)p >= (unsigned)c.num_pages) {
-                    atomicOr(c.status, kStatusBadIndex);
-                    return -1;
-                }
-                return ((p * c.kv_heads + head) << c.page_shift) + ((key0 + i * kTile + lane * 16) & ((1 << c.page_shift) - 1));
+            const auto scales = [&](int i, int entry) -> float2 {
+                if (!sees(i) || (unsigned)entry >= (unsigned)c.num_pages) return make_float2(0.0f, 0.0f);
+                const int at = ((entry * c.kv_heads + head) << c.page_shift) + ((key0 + i * kTile + t) & ((1 << c.page_shift) - 1));
+                return make_float2(__ldg(c.k_scale + at), __ldg(c.v_scale + at));
             };
-            // A piece's codes; zeros for positions nobody sees.
-            const auto load = [&](int i, int side, int half, int rows) {
-                const int pos = key0 + i * kTile;
-                const char *pool = static_cast<const char *>(side ? c.v : c.k) + u * 16;
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    const int q = (x * C::kConverters + cw) * kRowsOnce + sub, r = half * kPiece + q;
-                    const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
-                    raw[half][x] = make_uint4(0, 0, 0, 0);
-                    if (q < kPiece && base >= 0 && pos + r >= all.lo && pos + r < all.hi)
-                        raw[half][x] = __ldg(reinterpret_cast<const uint4 *>(pool + (size_t)(base + (r & 15)) * D));
-                }
-            };
-            static_assert(C::kConverters >= kTile / 32, "a key's scales a lane");
-            const auto load_scales = [&](int i, int rows) {
-                const int pos = key0 + i * kTile, r = cw * 32 + lane;
-                const int base = __shfl_sync(~0u, rows, (r >> 4) & 7);
-                sc[0] = sc[1] = 0.0f;
-                if (r < kTile && base >= 0 && pos + r >= all.lo && pos + r < all.hi) {
-                    sc[0] = __ldg(c.k_scale + base + (r & 15));
-                    sc[1] = __ldg(c.v_scale + base + (r & 15));
-                }
-            };
-            const auto store = [&](int slot, int half) {
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    const int q = (x * C::kConverters + cw) * kRowsOnce + sub, r = half * kPiece + q;
-                    if (q >= kPiece) break;
-                    const uint32_t w[4] = {raw[half][x].x, raw[half][x].y, raw[half][x].z, raw[half][x].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[2 * e] = frag::i8_pair(__byte_perm(w[e], 0, 0x4140));
-                        o[2 * e + 1] = frag::i8_pair(__byte_perm(w[e], 0, 0x4342));
-                    }
-                    unsigned char *base = sgen + slot_at(slot) + (u >> 2) * C::kPanel + r * 128;
-                    const int ch = (u & 3) * 2;
-                    *reinterpret_cast<uint4 *>(base + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(base + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-            };
-            int rows = first_row(0, page_entry(0)), entry = page_entry(1);
-            load(0, 0, 0, rows);
-            load(0, 0, 1, rows);
-            for (int i = 0; i < n; ++i) {
-                bool ok = true;
-                const int rows_next = first_row(i + 1, entry);
+            float2 sc_next = scales(0, page_entry(0));
+            int entry = page_entry(1);
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const float2 sc = sc_next;
+                sc_next = scales(i + 1, entry);
                 entry = page_entry(i + 2);
 #pragma unroll
-                for (int side = 0; side < 2; ++side) {
+                for (int piece = 0; piece < 4; ++piece) {
+                    const int side = piece >> 1, half = piece & 1;
                     const T item(2 * i + side);
-                    ok = wait(empty(item.slot), item.parity ^ 1) && !lost();
-                    if (!__all_sync(~0u, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (side == 0) load_scales(i, rows);
+                    const P x(4 * i + piece);
+                    ok = wait(raw_full(x.slot), x.parity) && !lost();
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    uint4 raw[kPer];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        store(item.slot, half);
-                        if (side == 0) load(i, 1, half, rows);
-                        else load(i + 1, 0, half, rows_next);
-                    }
-                    if (side) {
-                        // both sides' scales go with the values
-                        float *at = reinterpret_cast<float *>(sgen + C::kScale) + (i % C::kScaleTiles) * kTile;
-                        if (cw * 32 + lane < kTile) {
-                            at[cw * 32 + lane] = sc[0] * L.scale_log2;
-                            at[C::kScaleTiles * kTile + cw * 32 + lane] = sc[1];
+                    for (int r = 0; r < kPer; ++r)
+                        raw[r] = *reinterpret_cast<const uint4 *>(sgen + C::kRaw + x.slot * C::kPiece + r * (kLanes * 16) + t * 16);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(raw_empty(x.slot));
+                    // Zeros for positions that nobody sees.
+                    const int pos = key0 + i * kTile + half * C::kPieceKeys;
+                    if (pos < all.lo || pos + C::kPieceKeys > all.hi) {
+#pragma unroll
+                        for (int r = 0; r < kPer; ++r) {
+                            const int key = pos + r * kRowsOnce + row0;
+                            if (key < all.lo || key >= all.hi) raw[r] = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(full(item.slot));
+                    if (half == 0) {
+                        ok = wait(empty(item.slot), item.parity ^ 1) && !lost();
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                    }
+                    unsigned char *const to = sgen + item.slot * C::kOperand + half * (C::kPieceKeys * 128);
+#pragma unroll
+                    for (int r = 0; r < kPer; ++r) {
+                        const uint4 a = raw[r];
+                        const uint32_t w[4] = {second ? a.z : a.x, second ? a.w : a.y, second ? a.x : a.z, second ? a.y : a.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[2 * e] = frag::i8_pair(__byte_perm(w[e], 0, 0x4140));
+                            o[2 * e + 1] = frag::i8_pair(__byte_perm(w[e], 0, 0x4342));
+                        }
+                        *reinterpret_cast<uint4 *>(to + place + r * (kRowsOnce * 128)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(to + (place ^ 16) + r * (kRowsOnce * 128)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    if (piece == 3) {   // both sides' scales go with the values
+                        float *at = reinterpret_cast<float *>(sgen + C::kScale) + (i % C::kScaleTiles) * kTile;
+                        at[t] = sc.x * L.scale_log2;
+                        at[C::kScaleTiles * kTile + t] = sc.y;
+                    }
+                    if (half == 1) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(full(item.slot));
+                    }
                 }
-                if (!ok) break;
-                rows = rows_next;
             }
         }
     }
@@ -615,9 +659,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::tc_fence_after();
 
     // ---------------------------------------------------------- output
-    const int tile = (b * c.kv_heads + head) * L.row_tiles + rt;
     if (softmax && !lost()) {
-        const size_t at = ((size_t)tile * L.split + sp) * kRows + (r - r0);
+        // Float rows of a range and their (maximum, sum), for the join: where the
+        // ring and Q were.
+        unsigned char *const f_rows = sgen + C::kRing + h * (kHalf * D * 4);
+        float2 *const stats = reinterpret_cast<float2 *>(sgen + C::kQ + C::kJoinStats);
         if (!I8 && words[2]) {
             constexpr int kE = D / 32;
             for (int x = part; x < 32; x += 2) {
@@ -633,8 +679,11 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         rs.out(L, row, D)[lane * kE + e] = __float2bfloat16_rn(z.hi > z.lo ? acc[e] * inv : 0.0f);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) L.partial[(at - lane + x) * D + lane * kE + e] = acc[e];
-                    if (lane == 0) L.stats[at - lane + x] = make_float2(mm, ll);
+                    for (int e = 0; e < kE; ++e) {
+                        const int d = lane * kE + e, hrow = hr - lane + x;
+                        *reinterpret_cast<float *>(f_rows + hrow * (D * 4) + (((d >> 2) ^ (hrow & 7)) << 4) + (d & 3) * 4) = acc[e];
+                    }
+                    if (lane == 0) stats[row - r0] = make_float2(mm, ll);
                 }
             }
         } else {
@@ -644,7 +693,6 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             l += share[(part ^ 1) * kRows + h * kHalf + hr];
             const bool any = z.hi > z.lo && n > 0;
             const float inv = __fdiv_rn(1.0f, l);
-            unsigned char *const f_rows = sgen + C::kRing + h * (kHalf * D * 4);
             unsigned char *const b_rows = sgen + C::kQ + h * C::kOperand;
 #pragma unroll
             for (int q = 0; q < kDims / 32; ++q) {
@@ -675,10 +723,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                 }
             }
-            if (active > 1 && part == 0 && r < rs.R) L.stats[at] = make_float2(m, l);
-            ptx::bar_red_or(9 + h, 256, false);   // the half's rows are in place
-            const int mine = part * 128 + hr;
+            if (active > 1 && part == 0) stats[r - r0] = make_float2(m, l);
             if (active == 1) {
+                ptx::bar_red_or(9 + h, 256, false);   // the half's rows are in place
+                const int mine = part * 128 + hr;
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const int unit = x * 256 + mine, row = unit / (D / 8), u = unit % (D / 8);
@@ -687,15 +735,6 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         reinterpret_cast<uint4 *>(rs.out(L, qr, D))[u] =
                             *reinterpret_cast<const uint4 *>(b_rows + row * (D * 2) + ((u ^ (row & 7)) << 4));
                 }
-            } else {
-                float *dst = L.partial + (((size_t)tile * L.split + sp) * kRows + h * kHalf) * D;
-#pragma unroll 4
-                for (int x = 0; x < D / 8; ++x) {
-                    const int unit = x * 256 + mine, row = unit / (D / 4), u = unit % (D / 4);
-                    if (r0 + h * kHalf + row < rs.R)
-                        reinterpret_cast<uint4 *>(dst)[unit] =
-                            *reinterpret_cast<const uint4 *>(f_rows + row * (D * 4) + ((u ^ (row & 7)) << 4));
-                }
             }
         }
     }
@@ -703,7 +742,51 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
-    if (active > 1) join_ranges<D, kRows, C::kThreads>(L, rs, tile, r0, active, tid, reinterpret_cast<int *>(const_cast<uint32_t *>(words + 3)));
+    if (active == 1) return;
+
+    // ------------------------------------------------------------ join
+    // Each CTA of the cluster finishes its part of the rows: the ranges in their
+    // order, read from the CTAs' shared memory.
+    cluster_sync();
+    const int all_rows = min(kRows, rs.R - r0), rows_each = (all_rows + active - 1) / active;
+    const int j0 = sp * rows_each, rows_mine = max(min(all_rows - j0, rows_each), 0);
+    float *const facs = reinterpret_cast<float *>(sgen + C::kQ + C::kJoinFacs);   // [range][row], then the sums
+    for (int j = tid; j < rows_mine; j += C::kThreads) {
+        const uint32_t at = sbase + C::kQ + C::kJoinStats + (j0 + j) * 8;
+        float2 st[kMostRanges];
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kMostRanges; ++x) {
+            if (x < active) st[x] = ld_cluster2(at, x), top = fmaxf(top, st[x].x);
+        }
+#pragma unroll
+        for (int x = 0; x < kMostRanges; ++x) {
+            if (x >= active) break;
+            const float fac = share_factor(st[x].x, st[x].y, top);
+            const bool skip = st[x].x == -INFINITY && fac == 0.0f;   // a range that saw nothing
+            facs[x * kRows + j] = skip ? -1.0f : fac;
+            if (!skip) sum = fmaf(st[x].y, fac, sum);
+        }
+        facs[kMostRanges * kRows + j] = sum;
+    }
+    __syncthreads();
+    constexpr int kU = D / 4;   // units of four dimensions
+    for (int i = tid; i < rows_mine * kU; i += C::kThreads) {
+        const int j = i / kU, u = i % kU, row = j0 + j;
+        const uint32_t at = sbase + C::kRing + row * (D * 4) + ((u ^ (row & 7)) << 4);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int x = 0; x < active; ++x) {
+            const float4 v = ld_cluster4(at, x);
+            const float fac = facs[x * kRows + j];
+            if (fac < 0.0f) continue;
+            acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
+            acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
+        }
+        store_out4(L, rs, r0 + row, D, 4 * u, acc, facs[kMostRanges * kRows + j]);
+    }
+    __syncthreads();
+    cluster_sync();   // nobody's rows go while another CTA reads them
 }
 
 // The pool's rows [pages * heads * page][D], boxes of a page (at most a tile)
@@ -731,8 +814,20 @@ cbs_status launch_chunk(const AttnLaunch &L, cudaStream_t s) {
     using C = Chunk<D, I8>;
     auto kern = attn_chunk_kernel<D, I8>;
     CBS_TRY(cuda_check(set_max_dyn_smem(kern, C::kSmem), "attention shared memory"));
-    const dim3 grid(L.split, L.c.kv_heads * L.row_tiles, L.c.batch);
-    return cuda_check(launch_kernel(kern, grid, C::kThreads, C::kSmem, s, tk, tv, L), "attention launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L.split, L.c.kv_heads * L.row_tiles, L.c.batch);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = (launch_options() & CBS_LAUNCH_PDL) ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.split > 1 ? 2 : 1;
+    return cuda_check(cudaLaunchKernelEx(&cfg, kern, tk, tv, L), "attention launch");
 }
 
 }  // namespace

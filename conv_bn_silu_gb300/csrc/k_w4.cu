@@ -71,14 +71,6 @@ struct W4Tile {
     static_assert(2 * kN * (kOut + 1) * 4 <= kBars, "sums fit where the stages were");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
 // A float of another CTA's shared memory (this CTA's address, that CTA's rank).
 __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
     uint32_t a;

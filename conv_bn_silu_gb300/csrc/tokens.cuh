@@ -94,5 +94,6 @@ cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
 // Tensor-core kernel: tiles of kAttnChunkRows rows.
 cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);
 constexpr int kAttnChunkRows = 256, kAttnChunkKeys = 128;
+constexpr int kAttnChunkSplitMost = 8;   // ranges of keys: CTAs of one cluster
 
 }  // namespace cbs

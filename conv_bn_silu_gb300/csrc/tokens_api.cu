@@ -163,14 +163,14 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
     const int keys = d->window > 0 ? std::min(d->max_len, d->window + d->max_new) : d->max_len;
     if (d->force_split) {
-        p.split = d->force_split;
+        p.split = chunk ? std::min(d->force_split, kAttnChunkSplitMost) : d->force_split;
     } else if (chunk) {
         // One CTA an SM: the split with the least rounds of CTAs times key tiles
         // of a range, where each range costs about two tiles more (filling the
         // pipeline, and writing and joining its share).
         const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
         long long best = LLONG_MAX;
-        for (int x = 1; x <= std::min(key_tiles, 32); ++x) {
+        for (int x = 1; x <= std::min(key_tiles, kAttnChunkSplitMost); ++x) {
             const long long rounds = (base * x + sms - 1) / sms;
             const long long cost = rounds * ((key_tiles + x - 1) / x + (x > 1 ? 3 : 1));
             if (cost < best) best = cost, p.split = x;
@@ -179,11 +179,11 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         const long long want = ((long long)sms * 4 + base - 1) / base;
         p.split = (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
     }
-    p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 768 : 640) : 128;
+    p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 704 : 640) : 128;
     const long long ctas = base * p.split;
     if (ctas > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld CTAs", ctas);
     p.grid_ctas = (int)ctas;
-    if (p.split > 1) {
+    if (p.split > 1 && !chunk) {
         const size_t rows_all = attn_stat_rows(p);
         p.workspace_bytes = attn_counter_bytes(p) + (rows_all * 8 + 255) / 256 * 256 + rows_all * d->head_dim * 4;
     }
@@ -224,7 +224,7 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
     L.group_magic = L.group > 1 ? (unsigned)(((1ull << 32) + L.group - 1) / L.group) : 0u;
     L.heads = d.heads; L.causal = d.causal != 0; L.window = d.window; L.max_new = d.max_new;
     L.split = p->split; L.row_tiles = p->row_tiles;
-    if (p->split > 1) {
+    if (p->workspace_bytes > 0) {
         char *w = static_cast<char *>(workspace);
         L.counters = reinterpret_cast<unsigned int *>(w);
         L.stats = reinterpret_cast<float2 *>(w + attn_counter_bytes(*p));
