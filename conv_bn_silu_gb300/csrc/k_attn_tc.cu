@@ -61,12 +61,12 @@ struct Chunk {
     // up to 2 i + kSlots have had their slots, V of tile i + (kSlots - 1) / 2 the last.
     static constexpr int kReady = 4;
     static_assert((kSlots - 1) / 2 < kReady, "a check's turn comes after the last one's was seen");
-    // q_full[2], s_full[2], p_ready[2], pv_done[2], drain, ready[], full[], empty[], raw_full[], raw_empty[];
+    // q_full[2], s_full[2], p_ready[2], pv_done[2], drain, ready[], full[K, V][], empty[], raw_full[], raw_empty[];
     // then the TMEM address and flags.
     // The join's places in Q's: each row's maximum and sum, then the ranges' factors.
     static constexpr int kJoinStats = 0, kJoinFacs = kRows * 8;
     static_assert(kJoinFacs + (kMostRanges + 1) * kRows * 4 <= 2 * kOperand && 2 * kHalf * D * 4 <= kSlots * kOperand, "join");
-    static constexpr int kNumBars = 9 + kReady + 2 * kSlots + 2 * kPieces;
+    static constexpr int kNumBars = 9 + kReady + 3 * kSlots + 2 * kPieces;
     static constexpr int kSmem = kBars + kNumBars * 8 + 16;
     static_assert(kSmem <= kMaxDynSmem, "ring");
     static_assert(!I8 || (kSlots % 2 == 0 && kSlots / 2 <= kScaleTiles), "scales are free when V's slot is");
@@ -202,7 +202,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
     const Rows rs = rows_of(L, b, head);
     const int r0 = rt * kRows;
-    if (r0 >= rs.R) return;
+    // CTAs of one cluster meet twice at the end, and none leaves before: whatever
+    // is read there is still some CTA's, even if the lengths change meanwhile.
+    const auto leave = [&] {
+        if (L.split == 1) return;
+        cluster_sync();
+        cluster_sync();
+    };
+    if (r0 >= rs.R) return leave();
     const int halves = r0 + kHalf < rs.R ? 2 : 1, r1 = min(rs.R, r0 + kRows);
     const Span all = span_of(L, rs, r0, r1);
     const int lo = all.lo & ~(kTile - 1);
@@ -210,7 +217,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int per = (tiles + L.split - 1) / L.split;
     const int active = per ? (tiles + per - 1) / per : 1;
     const int sp = blockIdx.x;
-    if (sp >= active) return;
+    if (sp >= active) return leave();
     const int i0 = sp * per, n = min(tiles, i0 + per) - i0;   // this CTA's key tiles
     const int key0 = lo + i0 * kTile;
 
@@ -223,10 +230,14 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // bf16: tile i's V has been checked.  Its own turns, by tile: a slot of the
     // ring holds K and V alternately, so the ring's parities do not count V's.
     const auto ready = [&](int i) { return bar(9 + i % C::kReady); };
-    const auto full = [&](int s) { return bar(9 + C::kReady + s); };                // an item has arrived
-    const auto empty = [&](int s) { return bar(9 + C::kReady + C::kSlots + s); };   // and been used
-    const auto raw_full = [&](int s) { return bar(9 + C::kReady + 2 * C::kSlots + s); };   // int8: a piece's codes
-    const auto raw_empty = [&](int s) { return bar(9 + C::kReady + 2 * C::kSlots + C::kPieces + s); };
+    // Tile i's K or V has arrived: barriers of each side's own, so that whoever
+    // waits for one side's tiles in order sees every turn of its barriers (loads
+    // end out of order, and of a slot's turns K's or V's alone are every other).
+    const auto full = [&](int i, int side) { return bar(9 + C::kReady + side * C::kSlots + i % C::kSlots); };
+    const auto full_turn = [&](int i) { return (uint32_t)(i / C::kSlots) & 1u; };
+    const auto empty = [&](int s) { return bar(9 + C::kReady + 2 * C::kSlots + s); };   // a slot's item has been used
+    const auto raw_full = [&](int s) { return bar(9 + C::kReady + 3 * C::kSlots + s); };   // int8: a piece's codes
+    const auto raw_empty = [&](int s) { return bar(9 + C::kReady + 3 * C::kSlots + C::kPieces + s); };
     const auto slot_at = [&](int s) { return C::kRing + s * C::kOperand; };
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(sgen + C::kBars + 8 * C::kNumBars);
     // words[0]: TMEM address; [1]: a wait ran out; [2]: a value is not finite
@@ -240,7 +251,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         for (int i = 0; i < C::kReady; ++i) ptx::mbar_init(ready(i), 2);
         for (int s = 0; s < C::kSlots; ++s) {
-            ptx::mbar_init(full(s), I8 ? C::kConverters : 1);
+            ptx::mbar_init(full(s, 0), I8 ? C::kConverters : 1);
+            ptx::mbar_init(full(s, 1), I8 ? C::kConverters : 1);
             ptx::mbar_init(empty(s), 1);
         }
         for (int s = 0; s < C::kPieces; ++s) {
@@ -299,7 +311,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int x = 0; x < kTile / 16; ++x) mma_ts(lead, t_o(h), t_s(h) + 8 * x, v + 128u * x, idesc_o, more || x > 0);
                 mma_commit(lead, pv_done(h));
             };
-            bool ok = wait(full(0), 0);
+            bool ok = wait(full(0, 0), 0);
             for (int h = 0; ok && h < halves; ++h) {
                 ok = wait(q_full(h), 0);
                 if (!ok) break;
@@ -307,14 +319,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 scores(h, 0);
             }
             if (ok) mma_commit(lead, empty(0));
-            int v_slot = 1, k_slot = 2 % C::kSlots;
-            uint32_t v_par = 0, k_par = 0;   // items 2 i + 1 and 2 i + 2
-            const auto advance = [](int &slot, uint32_t &par) {
+            int v_slot = 1, k_slot = 2 % C::kSlots;   // items 2 i + 1 and 2 i + 2
+            const auto advance = [](int &slot) {
                 slot += 2;
-                if (slot >= C::kSlots) slot -= C::kSlots, par ^= 1;
+                if (slot >= C::kSlots) slot -= C::kSlots;
             };
             for (int i = 0; ok && i < n; ++i) {
-                ok = (I8 ? wait(full(v_slot), v_par) : wait(ready(i), (i / C::kReady) & 1)) && !lost();
+                ok = (I8 ? wait(full(i, 1), full_turn(i)) : wait(ready(i), (i / C::kReady) & 1)) && !lost();
                 ok = __all_sync(~0u, ok);
                 for (int h = 0; ok && h < halves; ++h) {
                     ok = wait(p_ready(h), i & 1);
@@ -323,15 +334,15 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     output(h, v_slot, i > 0);
                     if (h == halves - 1) mma_commit(lead, empty(v_slot));
                     if (i + 1 < n) {
-                        if (h == 0) ok = wait(full(k_slot), k_par);
+                        if (h == 0) ok = wait(full(i + 1, 0), full_turn(i + 1));
                         if (!ok) break;
                         ptx::tc_fence_after();
                         scores(h, k_slot);
                         if (h == halves - 1) mma_commit(lead, empty(k_slot));
                     }
                 }
-                advance(v_slot, v_par);
-                advance(k_slot, k_par);
+                advance(v_slot);
+                advance(k_slot);
             }
             __syncwarp();
             mma_commit(lead, drain);   // nothing leaves while an MMA reads shared memory
@@ -364,28 +375,28 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const T x(2 * i + side);
                 if (lane == 0) {
                     ok = wait(empty(x.slot), x.parity ^ 1) && !lost();
-                    if (ok) ptx::mbar_arrive_expect_tx(full(x.slot), C::kOperand);
+                    if (ok) ptx::mbar_arrive_expect_tx(full(i, side), C::kOperand);
                 }
                 ok = __shfl_sync(~0u, (int)ok, 0) != 0;
                 if (ok && lane < boxes) {
                     const uint32_t dst = sbase + slot_at(x.slot) + lane * box * 128;
 #pragma unroll
                     for (int p = 0; p < D / 64; ++p)
-                        ptx::tma_load_2d(dst + p * C::kPanel, side ? &tm_v : &tm_k, full(x.slot), p * 64, row);
+                        ptx::tma_load_2d(dst + p * C::kPanel, side ? &tm_v : &tm_k, full(i, side), p * 64, row);
                 }
                 if (ok) ++done;
             }
             if (!ok) break;
         }
-        if (lane == 0 && lost()) {   // the copies in flight land before the CTA leaves
-            for (int x = max(0, done - C::kSlots); x < done; ++x) ptx::mbar_wait_bounded(full(T(x).slot), T(x).parity, kWaitNs);
-        }
+        // The copies in flight land before the CTA leaves, whoever gives up.
+        if (lane == 0)
+            for (int x = max(0, done - C::kSlots); x < done; ++x) wait(full(x >> 1, x & 1), full_turn(x >> 1));
     } else if (!I8 && warp < 4) {
         // ------------------------- values some row must not see (bf16 cache)
         for (int i = 0; i < n; ++i) {
             const T x(2 * i + 1);
             const int pos = key0 + i * kTile;
-            if (!wait(full(x.slot), x.parity)) break;
+            if (!wait(full(i, 1), full_turn(i))) break;
             if (pos < all.all_lo || pos + kTile > all.all_hi) {
                 // Rows that nobody sees become zeros (a page's slots past the
                 // length may hold anything, and 0 x NaN is NaN); a value that is
@@ -451,9 +462,9 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (ok) ++done;
                 }
             }
-            if (lane == 0 && lost()) {   // the copies in flight land before the CTA leaves
-                for (int x = max(0, done - C::kPieces); x < done; ++x) ptx::mbar_wait_bounded(raw_full(P(x).slot), P(x).parity, kWaitNs);
-            }
+            // The copies in flight land before the CTA leaves, whoever gives up.
+            if (lane == 0)
+                for (int x = max(0, done - C::kPieces); x < done; ++x) wait(raw_full(P(x).slot), P(x).parity);
         }
     } else if (I8 && (warp < 4 || warp >= 20)) {
         // ------------------------------------------------------- converters
@@ -538,7 +549,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (half == 1) {
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(full(item.slot));
+                        if (lane == 0) ptx::mbar_arrive(full(i, side));
                     }
                 }
             }
@@ -579,7 +590,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             ok = wait(s_full(h), i & 1) && !lost();
-            if (I8 && ok) ok = wait(full(T(2 * i + 1).slot), T(2 * i + 1).parity);   // the tile's scales
+            if (I8 && ok) ok = wait(full(i, 1), full_turn(i));   // the tile's scales
             __syncwarp();
             // The two warps leave together, whatever ran out.
             if (ptx::bar_red_or(pair_bar, 64, !ok)) break;
@@ -742,7 +753,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
-    if (active == 1) return;
+    if (active == 1) return leave();
 
     // ------------------------------------------------------------ join
     // Each CTA of the cluster finishes its part of the rows: the ranges in their

@@ -1,0 +1,59 @@
+"""GPU checks of attention over caches larger than L2: tiles arrive late, and
+not in the order they were asked for."""
+import pytest
+import torch
+
+from conv_bn_silu_gb300 import _binding as B
+from conv_bn_silu_gb300 import tokens
+from tests import token_refs as refs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def token_calls(cuda_lib):
+    from conv_bn_silu_gb300 import build
+    build.build_tokens()
+
+
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,kv", [(128, 8), (64, 16)])
+def test_chunks_over_a_cache_in_memory(cuda_lib, d, kv, int8, split):
+    batch, length, new, page, heads = 16, 4001, 2, 64, 2 * kv
+    g = torch.Generator("cuda").manual_seed(d + split)
+    count = -(-length // page)
+    shape = (batch * count, kv, page, d)
+    table = torch.randperm(batch * count, device="cuda", generator=g).to(torch.int32).view(batch, count)
+    if int8:
+        k, v = (torch.randint(-127, 128, shape, dtype=torch.int8, device="cuda", generator=g) for _ in range(2))
+        ks, vs = (torch.rand(shape[:3], device="cuda", generator=g) * 0.02 + 0.005 for _ in range(2))
+    else:
+        k, v = (torch.randn(shape, dtype=torch.bfloat16, device="cuda", generator=g) for _ in range(2))
+        ks = vs = None
+    q = torch.randn((batch * new, heads, d), dtype=torch.bfloat16, device="cuda", generator=g)
+    starts = torch.arange(0, batch * new + 1, new, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), length, dtype=torch.int32, device="cuda")
+    attn = tokens.PagedAttention(tokens.PagedCache(k, v, ks, vs), batch, new, length, heads,
+                                 force_kernel=B.CBS_ATTN_CHUNK, force_split=split)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(3):   # from memory each time
+        flush.zero_()
+        torch.cuda.synchronize()
+        outs.append(attn(q, starts, lens, table))
+    assert B.cbs_read_device_status(True, torch.cuda.current_stream().cuda_stream) == B.CBS_OK
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs)
+    for b in range(batch):
+        at = table[b].long()
+        rows = [x[at].double() * (1 if s is None else s[at].double()[..., None]) for x, s in ((k, ks), (v, vs))]
+        kk, vv = (x.permute(1, 0, 2, 3).reshape(kv, count * page, d)[:, :length] for x in rows)
+        qq = q[b * new:(b + 1) * new].double().view(new, kv, 2, d).permute(1, 0, 2, 3).reshape(kv, new * 2, d)
+        scores = qq @ kk.transpose(1, 2) * d ** -0.5
+        token = torch.arange(new, device="cuda").repeat_interleave(2)
+        seen = torch.arange(length, device="cuda")[None] <= (length - new + token)[:, None]
+        p = scores.masked_fill(~seen, float("-inf")).softmax(-1)
+        back = lambda x: x.view(kv, new, 2, d).permute(1, 0, 2, 3).reshape(new, heads, d)
+        ref, mag = back(p @ vv), back(p @ vv.abs())
+        err = (outs[0][b * new:(b + 1) * new].double() - ref).abs()
+        assert (err <= refs.attention_bound(ref, mag)).all(), (b, float((err / refs.attention_bound(ref, mag)).max()))
