@@ -82,8 +82,13 @@ cbs_status token_stride(long long stride, long long least, const char *what) {
 
 constexpr int kGridMax = 65535;
 
-// Most rows of a key head for the few-row kernel.
-constexpr int kAttnRowsMost = 64;
+// Most rows of a key head for the few-row kernel.  32 heads, 8 key heads of 128,
+// few-row / chunk kernel in us, for 8, 16, 32, 64 rows: bf16, one sequence of 4000
+// keys 14/12, 21/13, 21/13, 24/14; 16 of 4000 58/53, 79/53, 124/54, 190/55; 64 of
+// 1000 66/75, 66/75, 113/76, 186/84.  8 bits (the chunk kernel widens every code
+// first): 15/20, 21/20, 22/20, 26/21; 53/134, 73/134, 118/134, 185/134; 57/137,
+// 58/137, 106/137, 178/139.
+constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
 size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
     return ((size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * 4 + 255) / 256 * 256;
@@ -149,7 +154,8 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     p.abi_version = CBS_ABI_VERSION;
     p.desc = *d;
     const long long rows = (long long)d->max_new * (d->heads / d->kv_heads);
-    p.kernel = d->force_kernel >= 0 ? d->force_kernel : rows > kAttnRowsMost ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
+    const int rows_most = d->cache_prec == CBS_INT8 ? kAttnRowsMostInt8 : kAttnRowsMost;
+    p.kernel = d->force_kernel >= 0 ? d->force_kernel : rows > rows_most ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
     const bool chunk = p.kernel == CBS_ATTN_CHUNK;
     p.row_tile = chunk ? kAttnChunkRows : rows <= 8 ? 8 : 16;
     const long long tiles = (rows + p.row_tile - 1) / p.row_tile;
@@ -165,19 +171,32 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     if (d->force_split) {
         p.split = chunk ? std::min(d->force_split, kAttnChunkSplitMost) : d->force_split;
     } else if (chunk) {
-        // One CTA an SM: the split with the least rounds of CTAs times key tiles
-        // of a range, where each range costs about two tiles more (filling the
-        // pipeline, and writing and joining its share).
+        // One CTA an SM: the split with the least rounds of clusters times what a
+        // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
+        // A key tile is one unit (1.6 us, head dimension 128), a range's start and
+        // end 4.5, a cluster's join 2 and a fifth for each CTA.  64 tokens of 32
+        // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 57, 36,
+        // 28, 24, 22, 22, 21, 20 us; four sequences 61, 40, 33, 29, 52, 51, 68, 65.
+        // Less than a tenth is not worth a cluster: sequences are of unequal lengths.
+        static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
         const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
-        long long best = LLONG_MAX;
+        long long best = 0;
         for (int x = 1; x <= std::min(key_tiles, kAttnChunkSplitMost); ++x) {
-            const long long rounds = (base * x + sms - 1) / sms;
-            const long long cost = rounds * ((key_tiles + x - 1) / x + (x > 1 ? 3 : 1));
-            if (cost < best) best = cost, p.split = x;
+            const int at_once = std::max(kAtOnce[x - 1] * sms / 152, 1);
+            const long long rounds = (base + at_once - 1) / at_once;
+            const long long cost = rounds * ((key_tiles + x - 1) / x * 10 + 45 + (x > 1 ? 20 + 2 * x : 0));
+            if (x == 1) best = cost - cost / 10, p.split = 1;
+            else if (cost < best) best = cost, p.split = x;
         }
     } else {
-        const long long want = ((long long)sms * 4 + base - 1) / base;
-        p.split = (int)std::max(1ll, std::min(want, (long long)(keys + 63) / 64));
+        // At least a CTA for each SM if that leaves a range 64 keys, and up to
+        // twelve if it leaves 640.  Tokens of 32 heads, 8 key heads, 1, 2, 4, ... 32
+        // ranges: one sequence of 1000 keys 15, 11, 7.8, 6.6, 6.7 us; one of 8192 108,
+        // 58, 31, 18, 13, 14; 8 of 8192 192, 103, 65, 69, 61, 63; 32 of 8192 (8 bits)
+        // 234, 210, 169, 159, 169, 195; 32 of 1024 34, 39, 36, 37, 51.
+        const long long few = std::min((sms + base - 1) / base, ((long long)keys + 63) / 64);
+        const long long many = std::min((sms * 12ll + base - 1) / base, (long long)keys / 640);
+        p.split = (int)std::max(1ll, std::max(few, many));
     }
     p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 704 : 640) : 128;
     const long long ctas = base * p.split;
