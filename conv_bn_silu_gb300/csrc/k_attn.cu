@@ -15,6 +15,11 @@
 // consecutive elements, and 8-bit codes are widened to bf16 exactly in
 // registers (their scales multiply the scores and the probabilities).
 //
+// One token of 32 heads, 8 key heads of 128: 1000 keys 6.8 us (latency: 16 ranges of
+// 64 keys, then the join); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
+// and 226 us in 8 bits, 3.7 TB/s, where the instructions that widen the codes bound
+// it: a quarter of all, and three CTAs an SM do not fill the slots between them.
+//
 // Ranges of keys are joined by the range's CTA that finishes last (a counter
 // per row tile), in the order of the ranges: the result does not depend on
 // which CTA that is.
@@ -160,6 +165,17 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         return (((size_t)p * c.kv_heads + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
     };
 
+    // The block after the next one to the L2 cache, a lane a key's row of K or V: a
+    // block of a warp's own is all that its registers hold ahead (64 sequences of up
+    // to 8192 keys: 281 -> 250 us in bf16, 237 -> 226 in 8 bits).
+    const char *const ahead = static_cast<const char *>(lane < kBlock ? c.k : c.v) + (size_t)(lane & (kBlock - 1)) * (D * (I8 ? 1 : 2));
+    const auto prefetch = [&](size_t row0, unsigned on) {
+        if (!((on >> (lane & (kBlock - 1))) & 1)) return;
+        const char *p = ahead + row0 * (D * (I8 ? 1 : 2));
+#pragma unroll
+        for (int i = 0; i < D * (I8 ? 1 : 2); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+    };
+
     F f;
     int blk = b0 + warp;
     unsigned live, live_next;
@@ -203,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         live = live_next;
         f.load_k(c, row, lane, live);
         row_next = place_of(next + kWarps, live_next);
+        prefetch(row_next, live_next);
 
         // ---- scores, in base 2; keys a row does not see become -inf
         const bool partial = now != 0xffffu || pos < all_lo || pos + kBlock > all_hi;

@@ -508,7 +508,7 @@ typedef struct cbs_attn_desc {
     int window;        /* > 0: and only the last `window` positions up to its own; 0: no limit */
     int num_sms;       /* 0 = 152 */
     int force_kernel;  /* -1: choose; else a cbs_attn_kernel */
-    int force_split;   /* 0: choose; else how many ranges of keys are computed side by side */
+    int force_split;   /* 0: choose; else how many ranges of keys are computed side by side (CBS_ATTN_CHUNK: at most 8) */
 } cbs_attn_desc;
 
 typedef enum cbs_attn_kernel {
@@ -540,8 +540,10 @@ CBS_API cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out);
  * sees nothing gets zeros.  Positions that a token does not see cannot reach
  * it, whatever they hold (a NaN or infinity included).
  * q, out: bfloat16 [total][heads][head_dim] with q_stride, out_stride elements
- * between tokens (multiples of 8).  scale: finite.  workspace: zeroed once
- * with cbs_workspace_init; not shared by calls that may run at the same time.
+ * between tokens (multiples of 8).  scale: finite.  workspace (plan's
+ * workspace_bytes, which may be 0): zeroed once with cbs_workspace_init; not
+ * shared by calls that may run at the same time.  Where a page lies outside the
+ * pool, or a wait runs out, the sequence's outputs are unspecified (reported).
  */
 CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, const cbs_sequences *s,
                                        const void *q, long long q_stride, float scale, void *out, long long out_stride,
@@ -576,7 +578,8 @@ CBS_API cbs_status cbs_dequantize_rows(const int8_t *q, const float *scale, void
  * [k/group][n].  zeros: uint8 [k/group][n] in 0..15, or NULL for 8.  bias:
  * float[n] or NULL.  y: [rows][n], out_prec CBS_FP32 or CBS_BF16.  activation:
  * cbs_activation.  group: 32, 64 or 128; k a multiple of it.  Sums in 32 bits.
- * Made for few rows (every 32 rows read the weights again).
+ * Made for few rows (every 64 rows, or 32 with groups of 32, read the weights
+ * again).
  */
 CBS_API cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const void *w, const void *scales,
                                  const void *zeros, const float *bias, void *y, int out_prec, int rows, int n, int k,
