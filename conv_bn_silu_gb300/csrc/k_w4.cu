@@ -61,8 +61,10 @@ struct W4Tile {
     static constexpr int kSubs = kPiece / GROUP;                        // groups in a piece
     static constexpr int kW = kOut * 128, kX = kPanels * kN * 128;      // a stage's weights; inputs
     static constexpr int kGroups = kStageK / GROUP;
-    static constexpr int kZAt = kGroups * kOut * 2;                     // scales [group][output], then zero points
-    static constexpr int kS = (kGroups * kOut * 3 + 1023) / 1024 * 1024;
+    // Scales [group][output], then zero points; each group's from the word that
+    // holds its first, so a row may start a few elements late.
+    static constexpr int kSPitch = kOut * 2 + 8, kZPitch = kOut + 4, kZAt = kGroups * kSPitch;
+    static constexpr int kS = (kZAt + kGroups * kZPitch + 1023) / 1024 * 1024;
     static constexpr int kSlot = kW + kX + kS;
     static constexpr int kStages = kN == 16 ? 4 : kN == 32 ? 3 : 2;
     static_assert(kSlot % 1024 == 0, "operands start at multiples of 1 KB");
@@ -202,38 +204,54 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         }
     } else if (warp == 10) {
         // ------------------------------------------------------- scales
-        // Four outputs a lane, copied as far ahead as the ring is deep: they come
-        // from HBM a row of [k / group][n] at a time, later than the threads that
-        // need them could ask.
+        // Copied as far ahead as the ring is deep: they come from HBM a row of
+        // [k / group][n] at a time, later than the threads that need them could ask.
+        // Four outputs a lane where every row starts at a multiple of four (n does);
+        // else words of four bytes from the one that holds the row's first element.
+        // (9 rows of 4897 x 2944, bf16: 10.5 us; element by element 15.2 us; 4896
+        // outputs 8.5 us.)
         const int n = n0 + 4 * lane;
-        const bool whole = L.n % 4 == 0 && n + 4 <= L.n;   // then both copies are aligned
-        const uint16_t *sp = static_cast<const uint16_t *>(L.scales);
+        const bool fours = L.n % 4 == 0;
+        const char *sp = static_cast<const char *>(L.scales), *zp = reinterpret_cast<const char *>(L.zeros);
+        const long long all = (long long)(L.k / GROUP) * L.n;   // scales
+        const auto copy4 = [](uint32_t to, const char *from, int bytes) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+        };
+        const auto word = [&](uint32_t to, const char *from, long long at, long long bytes, bool in) {   // zeros past the end
+            const int left = in ? (int)max(0ll, min(4ll, bytes - at)) : 0;
+            copy4(to, from + (left ? at : 0), left);
+        };
         int slot = 0;
         uint32_t parity = 1;
         for (int i = 0; i < ns; ++i) {
             if (!__all_sync(~0u, wait(empty(slot), parity))) break;
-            unsigned char *to = smem + slot * C::kSlot + C::kW + C::kX;
+            const uint32_t to = sbase + slot * C::kSlot + C::kW + C::kX;
+            if (fours) {
 #pragma unroll
-            for (int gr = 0; gr < C::kGroups; ++gr) {
-                const int k = (st0 + i) * kStageK + gr * GROUP;
-                const bool in = k < L.k;   // groups past k: scale zero
-                const size_t at = (size_t)(in ? k / GROUP : 0) * L.n;
-                unsigned char *s_to = to + (gr * kOut + 4 * lane) * 2, *z_to = to + C::kZAt + gr * kOut + 4 * lane;
-                if (whole) {
-                    ptx::cp_async_8(ptx::smem_u32(s_to), sp + at + n, in ? 8 : 0);
-                    if (L.zeros)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(z_to)), "l"(L.zeros + at + n), "r"(in ? 4 : 0) : "memory");
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int o = min(n + x, L.n - 1);   // outputs past the end repeat the last one's
-                        reinterpret_cast<uint16_t *>(s_to)[x] = in ? __ldg(sp + at + o) : (uint16_t)0;
-                        if (L.zeros) z_to[x] = in ? __ldg(L.zeros + at + o) : (uint8_t)0;
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    const int k = (st0 + i) * kStageK + gr * GROUP;
+                    const bool on = k < L.k && n < L.n;   // groups past k: scale zero
+                    const size_t at = on ? (size_t)(k / GROUP) * L.n + n : 0;
+                    ptx::cp_async_8(to + gr * C::kSPitch + 8 * lane, sp + 2 * at, on ? 8 : 0);
+                    if (L.zeros) copy4(to + C::kZAt + gr * C::kZPitch + 4 * lane, zp + at, on ? 4 : 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    const int k = (st0 + i) * kStageK + gr * GROUP;
+                    const bool in = k < L.k;
+                    const long long at = (long long)(in ? k / GROUP : 0) * L.n + n0, s_at = 2 * at & ~3ll, z_at = at & ~3ll;
+                    const uint32_t s_to = to + gr * C::kSPitch, z_to = to + C::kZAt + gr * C::kZPitch;
+                    word(s_to + 4 * lane, sp, s_at + 4 * lane, 2 * all, in);
+                    word(s_to + 128 + 4 * lane, sp, s_at + 128 + 4 * lane, 2 * all, in);
+                    if (lane == 0) word(s_to + 256, sp, s_at + 256, 2 * all, in);
+                    if (L.zeros) {
+                        word(z_to + 4 * lane, zp, z_at + 4 * lane, all, in);
+                        if (lane == 0) word(z_to + 128, zp, z_at + 128, all, in);
                     }
                 }
             }
-            if (whole) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full(slot)) : "memory");
-            else ptx::mbar_arrive(full(slot));
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full(slot)) : "memory");
             if (++slot == C::kStages) slot = 0, parity ^= 1;
         }
         ptx::cp_async_commit();
@@ -302,9 +320,10 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
             for (int u = 0; u < C::kSubs; ++u) {
                 const unsigned char *from = smem + slot * C::kSlot + C::kW + C::kX;
-                const int at = (wg * C::kSubs + u) * kOut + row;
-                sn[u] = reinterpret_cast<const uint16_t *>(from)[at];
-                zp[u] = 0x43004300u | (L.zeros ? (from[C::kZAt + at] & 15u) * 0x00010001u : 0x00080008u);
+                const int gr = wg * C::kSubs + u;
+                const uint32_t late = (uint32_t)(((st0 + i) * C::kGroups + gr) * L.n) & 3u;   // the group's first element in its word
+                sn[u] = reinterpret_cast<const uint16_t *>(from + gr * C::kSPitch)[row + (late & 1u)];
+                zp[u] = 0x43004300u | (L.zeros ? (from[C::kZAt + gr * C::kZPitch + row + late] & 15u) * 0x00010001u : 0x00080008u);
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
