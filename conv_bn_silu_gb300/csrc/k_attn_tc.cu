@@ -834,7 +834,8 @@ cbs_status launch_chunk(const AttnLaunch &L, cudaStream_t s) {
     }
     using C = Chunk<D, I8>;
     auto kern = attn_chunk_kernel<D, I8>;
-    CBS_TRY(cuda_check(set_max_dyn_smem(kern, C::kSmem), "attention shared memory"));
+    static ContextOfDevice set;
+    CBS_TRY(cuda_check(set_max_dyn_smem_once(kern, C::kSmem, set), "attention shared memory"));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.split, L.c.kv_heads * L.row_tiles, L.c.batch);
     cfg.blockDim = dim3(C::kThreads);

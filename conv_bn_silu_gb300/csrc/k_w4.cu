@@ -442,7 +442,8 @@ cbs_status launch_w4_one(const W4Launch &L, cudaStream_t s) {
         if (x == 1 || cost < best) best = cost, split = x;
     }
     auto kern = w4_kernel<GROUP, kN, XI8>;
-    cudaError_t e = set_max_dyn_smem(kern, C::kSmem);
+    static ContextOfDevice set;
+    cudaError_t e = set_max_dyn_smem_once(kern, C::kSmem, set);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(tiles * split, row_tiles);

@@ -3,6 +3,8 @@
 // here is part of the public ABI (include/cbs.h is).
 #pragma once
 
+#include <atomic>
+
 #include "cbs_internal.cuh"
 #include "status.cuh"
 
@@ -90,6 +92,20 @@ struct AttnLaunch {
     float2 *stats;
     unsigned int *counters;     // [batch][kv_heads][row_tiles]
 };
+// set_max_dyn_smem, once in a context: a call's host time is a small call's whole
+// time.  `done`: the kernel's own, the contexts it was set in.
+using ContextOfDevice = std::atomic<unsigned long long>[64];
+template <typename F>
+cudaError_t set_max_dyn_smem_once(F *kern, int bytes, ContextOfDevice &done) {
+    int dev = 0;
+    unsigned long long ctx = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && current_context_id(&ctx) == CBS_OK && ctx;
+    if (known && done[dev].load(std::memory_order_relaxed) == ctx) return cudaSuccess;
+    const cudaError_t e = set_max_dyn_smem(kern, bytes);
+    if (e == cudaSuccess && known) done[dev].store(ctx, std::memory_order_relaxed);
+    return e;
+}
+
 cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
 // Tensor-core kernel: tiles of kAttnChunkRows rows.
 cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);

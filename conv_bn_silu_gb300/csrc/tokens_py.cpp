@@ -11,7 +11,7 @@
 #include <initializer_list>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -66,8 +66,8 @@ int64_t token_stride(const Tensor &t, const char *name, ScalarType type, int hea
 }
 
 void *stream_of(const Tensor &t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
-Tensor empty(at::IntArrayRef shape, ScalarType type, const Tensor &like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+Tensor empty(at::IntArrayRef shape, ScalarType type, const Tensor &like) {   // (past the dispatcher, which takes as long again)
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 void *pointer(PyObject *o) {
     void *p = o == Py_None ? nullptr : PyLong_AsVoidPtr(o);
