@@ -57,3 +57,27 @@ def test_chunks_over_a_cache_in_memory(cuda_lib, d, kv, int8, split):
         ref, mag = back(p @ vv), back(p @ vv.abs())
         err = (outs[0][b * new:(b + 1) * new].double() - ref).abs()
         assert (err <= refs.attention_bound(ref, mag)).all(), (b, float((err / refs.attention_bound(ref, mag)).max()))
+
+
+@pytest.mark.parametrize("split", [1, 3, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_only_later_tokens_see_over_ranges(cuda_lib, d, split):
+    """A NaN among the keys or values of a chunk's own tokens: those before it
+    keep their answers, in whichever range of keys it lies and however the
+    ranges are joined; after a value's only its dimension is NaN."""
+    n, new, page, lens = 1200, 140, 32, [1200, 40]
+    starts, i32 = [0, new, new + 3], lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    q = torch.randn((new + 3, 8, d), generator=torch.Generator().manual_seed(22)).to(torch.bfloat16)
+    for side, at in (("v", 1100), ("v", 1199), ("k", 1150)):
+        paged = refs.make_paged(lens, 2, d, page, False, 21)
+        place = paged[side][paged["table"][0, at // page], 1, at % page]
+        place[3 if side == "v" else slice(None)] = float("nan")
+        cache = tokens.PagedCache(paged["k"].cuda(), paged["v"].cuda())
+        attn = tokens.PagedAttention(cache, 2, new, n, 8, force_kernel=B.CBS_ATTN_CHUNK, force_split=split)
+        assert attn.plan.split == split
+        got = attn(q.cuda(), i32(starts), i32(lens), paged["table"].cuda()).double().cpu()
+        ref, mag = refs.attention(q, paged, starts, lens, page, True, 0, d ** -0.5)
+        nan = torch.zeros(got.shape, dtype=torch.bool)
+        nan[at - (n - new):new, 4:, 3 if side == "v" else slice(None)] = True   # the tokens that see it
+        assert torch.equal(got.isnan(), nan) and torch.equal(got.isfinite(), ~nan)
+        assert ((got - ref).abs() <= refs.attention_bound(ref, mag))[~nan].all()
