@@ -206,31 +206,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    // Before the kernel ahead has ended: barriers, tensor memory, the tensor maps.
     if (!I8 && warp == 1 && lane < 2) ptx::prefetch_tmap(lane ? &tm_v : &tm_k);
-    ptx::griddep_wait();
-    const int b = blockIdx.z, head = blockIdx.y % c.kv_heads;
-    const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
-    const Rows rs = rows_of(L, b, head);
-    const int r0 = rt * kRows;
-    // CTAs of one cluster meet twice at the end, and none leaves before: whatever
-    // is read there is still some CTA's, even if the lengths change meanwhile.
-    const auto leave = [&] {
-        if (L.split == 1) return;
-        cluster_sync();
-        cluster_sync();
-    };
-    if (r0 >= rs.R) return leave();
-    const int halves = r0 + kHalf < rs.R ? 2 : 1, r1 = min(rs.R, r0 + kRows);
-    const Span all = span_of(L, rs, r0, r1);
-    const int lo = all.lo & ~(kTile - 1);
-    const int tiles = all.hi > all.lo ? (all.hi - lo + kTile - 1) / kTile : 0;
-    const int per = (tiles + L.split - 1) / L.split;
-    const int active = per ? (tiles + per - 1) / per : 1;
-    const int sp = blockIdx.x;
-    if (sp >= active) return leave();
-    const int i0 = sp * per, n = min(tiles, i0 + per) - i0;   // this CTA's key tiles
-    const int key0 = lo + i0 * kTile;
-
     const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
     const auto q_full = [&](int h) { return bar(h); };
     const auto s_full = [&](int h) { return bar(2 + h); };
@@ -280,7 +257,32 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    const int b = blockIdx.z, head = blockIdx.y % c.kv_heads;
+    const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
+    const Rows rs = rows_of(L, b, head);
+    const int r0 = rt * kRows;
+    // CTAs of one cluster meet twice at the end, and none leaves before: whatever
+    // is read there is still some CTA's, even if the lengths change meanwhile.
+    const auto leave = [&] {
+        if (warp == 1) ptx::tmem_dealloc(words[0], 512);
+        if (L.split == 1) return;
+        cluster_sync();
+        cluster_sync();
+    };
+    if (r0 >= rs.R) return leave();
+    const int halves = r0 + kHalf < rs.R ? 2 : 1, r1 = min(rs.R, r0 + kRows);
+    const Span all = span_of(L, rs, r0, r1);
+    const int lo = all.lo & ~(kTile - 1);
+    const int tiles = all.hi > all.lo ? (all.hi - lo + kTile - 1) / kTile : 0;
+    const int per = (tiles + L.split - 1) / L.split;
+    const int active = per ? (tiles + per - 1) / per : 1;
+    const int sp = blockIdx.x;
+    if (sp >= active) return leave();
+    const int i0 = sp * per, n = min(tiles, i0 + per) - i0;   // this CTA's key tiles
+    const int key0 = lo + i0 * kTile;
+
     const uint32_t tmem = words[0];
     const auto t_s = [&](int h) { return tmem + 128u * h; };         // scores, then probabilities
     const auto t_o = [&](int h) { return tmem + 256u + 128u * h; };  // output
@@ -763,7 +765,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
-    if (active == 1) return leave();
+    if (active == 1) {
+        if (L.split > 1) cluster_sync(), cluster_sync();
+        return;
+    }
 
     // ------------------------------------------------------------ join
     // Each CTA of the cluster finishes its part of the rows: the ranges in their
