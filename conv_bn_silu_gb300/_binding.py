@@ -28,7 +28,7 @@ CBS_VARIANT_STEM = 4
 CBS_VARIANT_TC_TF32X3 = 5
 CBS_ACT_SILU, CBS_ACT_IDENTITY = 0, 1
 CBS_LAUNCH_PDL = 1
-CBS_ATTN_ROWS, CBS_ATTN_CHUNK = 0, 1
+CBS_ATTN_ROWS, CBS_ATTN_CHUNK, CBS_ATTN_CLUSTER = 0, 1, 2
 
 EXPORTED = (
     "cbs_plan", "cbs_fold_bn", "cbs_pack_input", "cbs_conv_bn_silu_f32", "cbs_conv_bn_silu_i8",

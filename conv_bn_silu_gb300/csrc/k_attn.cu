@@ -15,17 +15,19 @@
 // consecutive elements, and 8-bit codes are widened to bf16 exactly in
 // registers (their scales multiply the scores and the probabilities).
 //
-// One token of 32 heads, 8 key heads of 128: 1000 keys 6.8 us (latency: 16 ranges of
-// 64 keys, then the join); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
+// One token of 32 heads, 8 key heads of 128: 1000 keys 5.4 us (latency: 8 ranges in
+// clusters; 6.7 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
 // and 226 us in 8 bits, 3.7 TB/s, where the instructions that widen the codes bound
 // it: a quarter of all, and three CTAs an SM do not fill the slots between them.
 //
-// Ranges of keys are joined by the range's CTA that finishes last (a counter
-// per row tile), in the order of the ranges: the result does not depend on
-// which CTA that is.
+// Up to eight ranges of keys are the CTAs of a cluster, which join them from each
+// other's shared memory; more are joined through the workspace by the CTA that
+// finishes last (a counter per row tile).  Both in the order of the ranges: the
+// result does not depend on which CTA that is.
 #include "attn_common.cuh"
 #include "mma_frag.cuh"
 #include "tc_ptx.cuh"
+#include "tc_warp.cuh"
 #include "tokens.cuh"
 
 namespace cbs {
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     using F = KvFrag<D, I8>;
     __shared__ __align__(16) float s_o[kWarps][kRows][D + 4];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float2 s_stat[kRows];   // a range's (maximum, sum), for the other CTAs of a cluster
     __shared__ int s_flag;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -106,7 +109,15 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads, rt = blockIdx.y / c.kv_heads;
     const Rows rs = rows_of(L, b, head);
     const int R = rs.R, r0 = rt * kRows, len = rs.len, base = rs.base;
-    if (r0 >= R) return;
+    // CTAs of one cluster meet twice at the end, and none leaves before: what is read
+    // there is still some CTA's, even if the lengths change meanwhile.
+    const auto leave = [&] {
+        if (L.cluster) {
+            cluster_sync();
+            cluster_sync();
+        }
+    };
+    if (r0 >= R) return leave();
     const int t_lo = Rows::token(L, r0), t_hi = Rows::token(L, min(R, r0 + kRows) - 1);
     // Keys that some row of the tile sees, in blocks of 16 from a multiple of 16.
     const int lo = seen_by(base + t_lo, len, L.causal, L.window).lo;
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     const int per = (blocks + L.split - 1) / L.split;
     const int active = per ? (blocks + per - 1) / per : 1;   // ranges that hold keys (one for none)
     const int sp = blockIdx.x;
-    if (sp >= active) return;
+    if (sp >= active) return leave();
     const int b0 = sp * per, b1 = min(blocks, b0 + per);
     // From here on every key below is seen by every row: no masks.
     const int all_lo = L.window ? max(0, base + t_hi - L.window + 1) : 0;
@@ -382,20 +393,69 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         }
         if (active == 1) {
             store_out4(L, rs, r0 + r, D, 4 * u, acc, sum);
+        } else if (L.cluster) {   // (a unit's own place, which nobody else has read)
+            *reinterpret_cast<float4 *>(&s_o[0][r][4 * u]) = acc;
+            if (u == 0) s_stat[r] = make_float2(top, sum);
         } else {
             const size_t at = ((size_t)tile * L.split + sp) * kRows + r;
             *reinterpret_cast<float4 *>(L.partial + at * D + 4 * u) = acc;
             if (u == 0) L.stats[at] = make_float2(top, sum);
         }
     }
-    if (active > 1) join_ranges<D, kRows, kThreads>(L, rs, tile, r0, active, tid, &s_flag);
+    if (!L.cluster) {
+        if (active > 1) join_ranges<D, kRows, kThreads>(L, rs, tile, r0, active, tid, &s_flag);
+        return;
+    }
+    // The ranges of a cluster, in their order, from the CTAs' shared memory: each
+    // CTA finishes some of the units.
+    __syncthreads();
+    cluster_sync();
+    if (active > 1) {
+        for (int i = sp * kThreads + tid; i < kRows * kU; i += active * kThreads) {
+            const int r = i / kU, u = i % kU;
+            if (r0 + r >= R) break;
+            const uint32_t o_at = ptx::smem_u32(&s_o[0][r][4 * u]), s_at = ptx::smem_u32(&s_stat[r]);
+            float2 st[kAttnClusterMost];
+            float4 v[kAttnClusterMost];
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x)
+                if (x < active) st[x] = ld_cluster2(s_at, x), v[x] = ld_cluster4(o_at, x);
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x)
+                if (x < active) top = fmaxf(top, st[x].x);
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x) {
+                if (x >= active) break;
+                const float fac = share_factor(st[x].x, st[x].y, top);
+                if (st[x].x == -INFINITY && fac == 0.0f) continue;   // a range that saw nothing
+                acc.x = fmaf(v[x].x, fac, acc.x); acc.y = fmaf(v[x].y, fac, acc.y);
+                acc.z = fmaf(v[x].z, fac, acc.z); acc.w = fmaf(v[x].w, fac, acc.w);
+                sum = fmaf(st[x].y, fac, sum);
+            }
+            store_out4(L, rs, r0 + r, D, 4 * u, acc, sum);
+        }
+    }
+    __syncthreads();
+    cluster_sync();   // nobody's rows go while another CTA reads them
 }
 
 template <int D, bool I8>
 cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
-    const dim3 grid(L.split, L.c.kv_heads * L.row_tiles, L.c.batch);
-    if (row_tile == 8) return launch_kernel(attn_rows_kernel<D, I8, 1>, grid, kThreads, 0, s, L);
-    return launch_kernel(attn_rows_kernel<D, I8, 2>, grid, kThreads, 0, s, L);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L.split, L.c.kv_heads * L.row_tiles, L.c.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = (launch_options() & CBS_LAUNCH_PDL) ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, row_tile == 8 ? attn_rows_kernel<D, I8, 1> : attn_rows_kernel<D, I8, 2>, L);
 }
 
 }  // namespace

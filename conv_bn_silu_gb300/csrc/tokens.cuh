@@ -88,6 +88,7 @@ struct AttnLaunch {
     unsigned int group_magic;   // ceil(2^32 / group): r / group for r group < 2^32 (group > 1)
     int heads, causal, window, max_new;
     int split, row_tiles;
+    int cluster;                // few rows: the ranges are CTAs of a cluster
     float *partial;             // [batch][kv_heads][row_tiles][split][rows][head_dim], then (max, sum) of each row
     float2 *stats;
     unsigned int *counters;     // [batch][kv_heads][row_tiles]
@@ -110,6 +111,7 @@ cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
 // Tensor-core kernel: tiles of kAttnChunkRows rows.
 cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);
 constexpr int kAttnChunkRows = 256, kAttnChunkKeys = 128;
-constexpr int kAttnChunkSplitMost = 8;   // ranges of keys: CTAs of one cluster
+constexpr int kAttnClusterMost = 8;
+constexpr int kAttnChunkSplitMost = kAttnClusterMost;   // ranges of keys: CTAs of one cluster
 
 }  // namespace cbs

@@ -146,7 +146,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         return fail(CBS_ERR_INVALID_ARG, "%d heads do not share %d key heads evenly", d->heads, d->kv_heads);
     if (d->cache_prec != CBS_BF16 && d->cache_prec != CBS_INT8)
         return fail(CBS_ERR_INVALID_ARG, "a cache is BF16 or INT8");
-    if (d->force_kernel < -1 || d->force_kernel > CBS_ATTN_CHUNK)
+    if (d->force_kernel < -1 || d->force_kernel > CBS_ATTN_CLUSTER)
         return fail(CBS_ERR_INVALID_ARG, "unknown attention kernel %d", d->force_kernel);
     cbs_attn_plan_t p;
     std::memset(&p, 0, sizeof(p));
@@ -169,7 +169,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
     const int keys = d->window > 0 ? std::min(d->max_len, d->window + d->max_new) : d->max_len;
     if (d->force_split) {
-        p.split = chunk ? std::min(d->force_split, kAttnChunkSplitMost) : d->force_split;
+        p.split = p.kernel == CBS_ATTN_ROWS ? d->force_split : std::min(d->force_split, kAttnClusterMost);
     } else if (chunk) {
         // One CTA an SM: the split with the least rounds of clusters times what a
         // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
@@ -197,12 +197,25 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         const long long few = std::min((sms + base - 1) / base, ((long long)keys + 63) / 64);
         const long long many = std::min((sms * 12ll + base - 1) / base, (long long)keys / 640);
         p.split = (int)std::max(1ll, std::max(few, many));
+        // Up to eight ranges join in a cluster where it does not keep CTAs waiting (three
+        // an SM; more are made eight if that leaves a range 512 keys at most, and five to
+        // seven four).  Through the workspace / in a cluster: one token over 1000 keys, 8
+        // ranges 6.5/5.4 us (16 ranges 6.7 through the workspace), over 4000 11.9/10.7 (19
+        // ranges 11.1), two tokens over 1000 7.9/5.6; four sequences of 1000, 4 ranges
+        // 8.1/7.1, 5 ranges 9.2/8.5; 16 of 1000, 2 ranges 19.8/18.2; 8 of 8000, 8 ranges
+        // 62/60; 32 of 8000, 8 ranges 168/187.
+        const int most = std::min(p.split, kAttnClusterMost), x = most > 4 && most < 8 ? 4 : most;
+        const bool fits = p.split <= kAttnClusterMost || keys <= 512 * kAttnClusterMost;
+        if (d->force_kernel == CBS_ATTN_CLUSTER || (d->force_kernel < 0 && fits && base * x <= 3ll * sms)) {
+            p.kernel = CBS_ATTN_CLUSTER;
+            p.split = x;
+        }
     }
     p.threads = chunk ? (d->cache_prec == CBS_INT8 ? 704 : 640) : 128;
     const long long ctas = base * p.split;
     if (ctas > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld CTAs", ctas);
     p.grid_ctas = (int)ctas;
-    if (p.split > 1 && !chunk) {
+    if (p.split > 1 && p.kernel == CBS_ATTN_ROWS) {
         const size_t rows_all = attn_stat_rows(p);
         p.workspace_bytes = attn_counter_bytes(p) + (rows_all * 8 + 255) / 256 * 256 + rows_all * d->head_dim * 4;
     }
@@ -243,6 +256,7 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
     L.group_magic = L.group > 1 ? (unsigned)(((1ull << 32) + L.group - 1) / L.group) : 0u;
     L.heads = d.heads; L.causal = d.causal != 0; L.window = d.window; L.max_new = d.max_new;
     L.split = p->split; L.row_tiles = p->row_tiles;
+    L.cluster = p->kernel == CBS_ATTN_CLUSTER && p->split > 1;
     if (p->workspace_bytes > 0) {
         char *w = static_cast<char *>(workspace);
         L.counters = reinterpret_cast<unsigned int *>(w);

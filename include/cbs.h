@@ -508,12 +508,13 @@ typedef struct cbs_attn_desc {
     int window;        /* > 0: and only the last `window` positions up to its own; 0: no limit */
     int num_sms;       /* 0 = 152 */
     int force_kernel;  /* -1: choose; else a cbs_attn_kernel */
-    int force_split;   /* 0: choose; else how many ranges of keys are computed side by side (CBS_ATTN_CHUNK: at most 8) */
+    int force_split;   /* 0: choose; else how many ranges of keys are computed side by side (at most 8 but with CBS_ATTN_ROWS) */
 } cbs_attn_desc;
 
 typedef enum cbs_attn_kernel {
     CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 or 16 (token, head) rows, keys straight to registers */
-    CBS_ATTN_CHUNK = 1  /* many: tiles of 256 rows on tcgen05, scores and output in tensor memory */
+    CBS_ATTN_CHUNK = 1, /* many: tiles of 256 rows on tcgen05, scores and output in tensor memory */
+    CBS_ATTN_CLUSTER = 2 /* as CBS_ATTN_ROWS, with up to 8 ranges of keys joined in a cluster and no workspace */
 } cbs_attn_kernel;
 
 typedef struct cbs_attn_plan_t {

@@ -81,3 +81,34 @@ def test_values_only_later_tokens_see_over_ranges(cuda_lib, d, split):
         nan[at - (n - new):new, 4:, 3 if side == "v" else slice(None)] = True   # the tokens that see it
         assert torch.equal(got.isnan(), nan) and torch.equal(got.isfinite(), ~nan)
         assert ((got - ref).abs() <= refs.attention_bound(ref, mag))[~nan].all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("split", [1, 2, 3, 7, 8, 40])
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 1), (64, 4), (128, 3)])
+def test_ranges_of_few_rows_joined_in_a_cluster(cuda_lib, d, new, split, int8):
+    """Sequences shorter than the ranges leave CTAs of a cluster without keys."""
+    from tests.test_tokens_attention import run_case
+    got, attn = run_case([1000, 33, 0, 500, 17], [new, min(new, 2), 0, 1, new], 16, 4, d, 16, int8, split=split,
+                         kernel=B.CBS_ATTN_CLUSTER)
+    assert attn.plan.split == min(split, 8) and attn.plan.workspace_bytes == 0
+    run_case([1200, 700], [new, new], 8, 2, d, 32, int8, window=300, split=split, kernel=B.CBS_ATTN_CLUSTER)
+    run_case([900], [new], 6, 2, d, 64, int8, causal=False, split=split, kernel=B.CBS_ATTN_CLUSTER)
+
+
+def test_plans_choose_the_cluster(cuda_lib):
+    """Where the planner itself takes up to eight ranges, no workspace is needed."""
+    from tests.test_tokens_attention import run_case
+    got, attn = run_case([1000], [1], 32, 8, 128, 16, False)
+    assert attn.plan.kernel == B.CBS_ATTN_CLUSTER and attn.plan.split == 8 and attn.workspace is None
+
+
+@pytest.mark.parametrize("split", [2, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_only_later_tokens_see_in_a_cluster(cuda_lib, d, split):
+    n, new, page, lens = 600, 4, 32, [600, 40]
+    paged = refs.make_paged(lens, 2, d, page, False, 23)
+    paged["v"][paged["table"][0, 598 // page], 1, 598 % page][3] = float("nan")
+    from tests.test_tokens_attention import run_case
+    got, attn = run_case(lens, [new, 3], 4, 2, d, page, False, paged=paged, split=split, kernel=B.CBS_ATTN_CLUSTER)
+    assert got[:2].isfinite().all() and got[2:4, 2:, 3].isnan().all()
