@@ -12,13 +12,14 @@
 // fill the 16 rows of the MMA and the few query rows its 8 columns, so no lane
 // of a single-token call's MMA is spent on rows that do not exist twice over.
 // The contraction order is free, so a lane's share of a key is 16-byte loads of
-// consecutive elements, and 8-bit codes are widened to bf16 exactly in
-// registers (their scales multiply the scores and the probabilities).
+// consecutive elements, and 8-bit codes are widened exactly in registers, keys to
+// f16 and values to bf16 (their scales multiply the scores and the probabilities).
 //
 // One token of 32 heads, 8 key heads of 128: 1000 keys 5.4 us (latency: 8 ranges in
 // clusters; 6.7 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
-// and 226 us in 8 bits, 3.7 TB/s, where the instructions that widen the codes bound
-// it: a quarter of all, and three CTAs an SM do not fill the slots between them.
+// and 209 us in 8 bits, 4.0 TB/s (225 with keys widened to bf16), where the
+// instructions that widen the codes bound it: a fifth of all, and three CTAs an SM do
+// not fill the slots between them.
 //
 // Up to eight ranges of keys are the CTAs of a cluster, which join them from each
 // other's shared memory; more are joined through the workspace by the CTA that
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 
     // Q: column g of each 8-row tile, this lane's dimensions (those of its K loads).
     uint32_t q[NR][D / 8];
+    float q_back[NR][2];   // 8 bits: what rows 2 j and 2 j + 1 were multiplied with, taken back
     Seen seen[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -148,6 +150,24 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
             const int dim = I8 ? (u >> 1) * 64 + j * 16 + (u & 1) * 8 : u * 32 + j * 8;
             const uint4 w = r < R ? __ldg(reinterpret_cast<const uint4 *>(p + dim)) : make_uint4(0, 0, 0, 0);
             q[n][4 * u] = w.x; q[n][4 * u + 1] = w.y; q[n][4 * u + 2] = w.z; q[n][4 * u + 3] = w.w;
+        }
+        if constexpr (I8) {
+            // Codes widen to f16 with fewer instructions than to bf16, so the queries
+            // are f16 here, a row's largest moved to 2^14 by a power of two: exact but
+            // for values below 2^-28 of it, which keep an error of 2^-39 of it.
+            float top = 0.0f;
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[n][u] << 16)), fabsf(__uint_as_float(q[n][u] & 0xffff0000u))));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const int up = top > 0.0f ? min(268 - (int)(__float_as_uint(top) >> 23), 254) : 127;   // exponents with their bias
+            const float by = __int_as_float(up << 23), back = __int_as_float((254 - up) << 23);
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u)
+                q[n][u] = frag::pack_half(__uint_as_float(q[n][u] << 16) * by, __uint_as_float(q[n][u] & 0xffff0000u) * by);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) q_back[n][i] = __shfl_sync(~0u, back, (2 * j + i) * 4);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) seen[n][i] = rs.seen(L, r0 + n * 8 + 2 * j + i);
@@ -207,11 +227,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
             if constexpr (I8) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const uint32_t a0 = frag::i8_pair(__byte_perm(ka[w], 0, 0x4140)), a2 = frag::i8_pair(__byte_perm(ka[w], 0, 0x4342));
-                    const uint32_t a1 = frag::i8_pair(__byte_perm(kb[w], 0, 0x4140)), a3 = frag::i8_pair(__byte_perm(kb[w], 0, 0x4342));
+                    uint32_t a0, a1, a2, a3;
+                    frag::i8_halves(ka[w], a0, a2);
+                    frag::i8_halves(kb[w], a1, a3);
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
-                        frag::mma(s[n], a0, a1, a2, a3, q[n][u * 8 + w * 2], q[n][u * 8 + w * 2 + 1]);
+                        frag::mma_half(s[n], a0, a1, a2, a3, q[n][u * 8 + w * 2], q[n][u * 8 + w * 2 + 1]);
                 }
             } else {
 #pragma unroll
@@ -237,6 +258,10 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             s[n][0] *= ks0; s[n][1] *= ks0; s[n][2] *= ks1; s[n][3] *= ks1;
+            if constexpr (I8) {
+                s[n][0] *= q_back[n][0]; s[n][1] *= q_back[n][1];
+                s[n][2] *= q_back[n][0]; s[n][3] *= q_back[n][1];
+            }
         }
         if (partial) {
 #pragma unroll
