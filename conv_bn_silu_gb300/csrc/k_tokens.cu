@@ -137,6 +137,13 @@ __device__ __forceinline__ void store16(float *p, const Vec8<float> &a, const Ve
     }
 }
 
+// The larger of two magnitudes, or NaN if one is (fmaxf would pass it over).
+__device__ __forceinline__ float most_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -251,12 +258,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
             for (int i = 0; i < 8; ++i) {
                 sum = fmaf(h[v][i], h[v][i], sum);
                 h[v][i] = __fmul_rn(h[v][i], w[i]);
-                if (I8) top = fmaxf(top, fabsf(h[v][i]));
+                if (I8) top = most_or_nan(top, fabsf(h[v][i]));
             }
         }
     }
     // The two reductions of the block in one exchange.  (A magnitude's bits are in
-    // its order.  A NaN is passed over, as by the maximum above.)
+    // its order, an infinity's and then a NaN's above all others.)
     uint32_t most = I8 ? __reduce_max_sync(~0u, __float_as_uint(top)) : 0u;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -276,7 +283,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         if (!I8 || tid == 0) rstd = rstd_of(sum);
     }
-    const RowScale s = RowScale::of(__fdiv_rn(top, 127.0f));
+    // A NaN or an infinity in h makes one in u, under a weight of zero too.
+    const RowScale s = RowScale::of(top < INFINITY ? __fdiv_rn(top, 127.0f) : __int_as_float(0x7fc00000));
     if (I8 && tid == 0) L.scale[row] = __fmul_rn(s.s, rstd);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
