@@ -137,6 +137,40 @@ __device__ __forceinline__ void store16(float *p, const Vec8<float> &a, const Ve
     }
 }
 
+// A sum of squares that may pass the float range.  Below kBig it is itself;
+// from there on it is negative, that of the values times 2^-80 (a float's square
+// is then below 2^96).  kBig: 1024 threads' sums below it stay in range.
+// (Squares below the range count as zero.)
+struct Squares {
+    static constexpr float kBig = 0x1p112f, kDown = 0x1p-80f;
+    static __device__ __forceinline__ float scaled(float sum) { return sum < 0.0f ? -sum : sum * kDown * kDown; }
+    static __device__ __forceinline__ float add(float sum, const float (&h)[8]) {
+        float all = sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = fmaf(h[i], h[i], all);
+        if (sum >= 0.0f && all < kBig) return all;
+        all = scaled(sum);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = fmaf(h[i] * kDown, h[i] * kDown, all);
+        return -all;
+    }
+    // Over a warp.
+    static __device__ __forceinline__ float together(float sum) {
+        const bool down = __any_sync(~0u, !(sum >= 0.0f));
+        if (down) sum = scaled(sum);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        return down ? -sum : sum;
+    }
+    // 1 / sqrt(sum / n + eps)
+    static __device__ __forceinline__ float rsqrt_mean(float sum, float n, float eps) {
+        const bool down = !(sum >= 0.0f);
+        const float e = down ? eps * kDown * kDown : eps;
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(fabsf(sum), n), e)));
+        return down ? r * kDown : r;
+    }
+};
+
 // The larger of two magnitudes, or NaN if one is (fmaxf would pass it over).
 __device__ __forceinline__ float most_or_nan(float a, float b) {
     float r;
@@ -254,9 +288,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
         if (whole(e) || any(e)) {
             float w[8];
             weights8<WHOLE>(L.weight, e - e0, L.cols, w);
+            sum = Squares::add(sum, h[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum = fmaf(h[v][i], h[v][i], sum);
                 h[v][i] = __fmul_rn(h[v][i], w[i]);
                 if (I8) top = most_or_nan(top, fabsf(h[v][i]));
             }
@@ -265,8 +299,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
     // The two reductions of the block in one exchange.  (A magnitude's bits are in
     // its order, an infinity's and then a NaN's above all others.)
     uint32_t most = I8 ? __reduce_max_sync(~0u, __float_as_uint(top)) : 0u;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    sum = Squares::together(sum);
     const int nw = nt >> 5, lane = tid & 31;
     if (lane == 0) {
         red[0][tid >> 5] = sum;
@@ -276,12 +309,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormLaun
     sum = lane < nw ? red[0][lane] : 0.0f;
     if (I8) top = __uint_as_float(__reduce_max_sync(~0u, lane < nw ? __float_as_uint(red[1][lane]) : 0u));
     // With 8-bit codes only the row's scale needs the sum.
-    const auto rstd_of = [&](float v) { return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(v, (float)L.cols), L.eps))); };
     float rstd = 0.0f;
     if (!I8 || tid < 32) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (!I8 || tid == 0) rstd = rstd_of(sum);
+        sum = Squares::together(sum);
+        if (!I8 || tid == 0) rstd = Squares::rsqrt_mean(sum, (float)L.cols, L.eps);
     }
     // A NaN or an infinity in h makes one in u, under a weight of zero too.
     const RowScale s = RowScale::of(top < INFINITY ? __fdiv_rn(top, 127.0f) : __int_as_float(0x7fc00000));

@@ -559,7 +559,9 @@ CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache
  * y in that type, scale unused.  out_prec CBS_INT8: with u = h * weight,
  *   s = max|u| / 127,  y = clamp(rne(u / s), -127, 127),  scale[row] = s / sqrt(..)
  * so the codes do not depend on the order in which the squares are summed.  A
- * row whose h or u holds a NaN or an infinity gets the scale NaN.  cols: 1 .. 32768.
+ * row whose h or u holds a NaN or an infinity gets the scale NaN.  Finite rows may
+ * be as large as the float range, their squares beyond it; squares below the
+ * range count as zero.  cols: 1 .. 32768.
  */
 CBS_API cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight, void *h_out, void *y,
                                float *scale, int rows, int cols, float eps, int in_prec, int out_prec, void *stream);

@@ -60,3 +60,31 @@ def test_rmsnorm_8_bits_shows_what_is_not_finite(cuda_lib, cols, residual, dtype
         w[at] = kind
         q = tokens.rmsnorm(x[:1].cuda(), w.cuda(), 1e-5, residual=None if r is None else r[:1], int8=True)
         assert q.scale.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [7, 64, 1000, 4096, 6001, 8192, 32768])
+def test_rmsnorm_rows_whose_squares_pass_the_float_range(cuda_lib, cols, dtype):
+    """Finite rows of any size have finite answers.  The bound is that of rows
+    of ordinary size: moving a value by a power of two is exact."""
+    g = gen(cols + 1)
+    x = torch.randn((7, cols), generator=g)
+    x[0] *= 1e20
+    x[1, cols // 2] = 3e38
+    x[2] = 3e38
+    x[3, : cols // 2 + 1] *= 1e18    # squares within the range, their sum perhaps not
+    x[4, -1] = -1e25
+    x[5] *= 2.0 ** 62
+    x = x.to(dtype)
+    w = torch.rand(cols, generator=g) * 0.5 + 0.5
+    h = x.float()
+    root = (h.double().square().mean(1, keepdim=True) + 1e-5).sqrt()
+    ref = h.double() * w.double() / root
+    y = tokens.rmsnorm(x.cuda(), w.cuda(), 1e-5).y.double().cpu()
+    bound = ref.abs() * (40 * U + (UB if dtype == torch.bfloat16 else 0)) + 1e-37
+    assert ((y - ref).abs() <= bound).all()
+    q = tokens.rmsnorm(x.cuda(), w.cuda(), 1e-5, int8=True)
+    codes, s = refs.quantise_rows(h * w)
+    assert torch.equal(q.y.cpu(), codes)
+    want = s.double() / root[:, 0]
+    assert ((q.scale.double().cpu() - want).abs() <= want * 40 * U).all()
