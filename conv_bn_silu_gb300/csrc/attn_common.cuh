@@ -42,9 +42,22 @@ struct Rows {
     }
 };
 
+// Tokens from `end` on belong to no sequence: zeros, from the CTAs of the last
+// sequence together.
+__device__ __forceinline__ void zero_padding(const AttnLaunch &L, int end, int D) {
+    const int units = L.heads * D / 8;   // of 16 bytes, a token
+    const long long all = (long long)(L.c.total - end) * units, step = (long long)gridDim.x * gridDim.y * blockDim.x;
+    for (long long i = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
+        const int t = (int)(i / units);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(L.out) + (size_t)(end + t) * L.out_stride + (size_t)(i - (long long)t * units) * 8) =
+            make_uint4(0, 0, 0, 0);
+    }
+}
+
 // The rows of sequence b, its starts within the call's tokens and its chunk
-// within the plan's (the status bit otherwise).
-__device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head) {
+// within the plan's (the status bit otherwise).  Behind the last sequence's
+// tokens, the padding.
+__device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head, int D) {
     const CacheArgs &c = L.c;
     Rows s;
     const int s0 = c.new_start[b], s1 = c.new_start[b + 1];
@@ -52,10 +65,11 @@ __device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head) {
     s.start = max(0, min(s0, c.total));
     const int end = max(s.start, min(s1, c.total));
     s.fresh = end - s.start;
-    if (s.start != s0 || end != s1 || s.fresh > L.max_new) {
+    if (s.start != s0 || end != s1 || s.fresh > L.max_new || (b == 0 && s0 != 0)) {
         if (threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
         s.fresh = min(s.fresh, L.max_new);
     }
+    if (b == c.batch - 1 && end < c.total) zero_padding(L, end, D);
     s.R = s.fresh * L.group;
     s.head = head;
     s.base = s.len - s.fresh;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads, rt = blockIdx.y / c.kv_heads;
-    const Rows rs = rows_of(L, b, head);
+    const Rows rs = rows_of(L, b, head, D);
     const int R = rs.R, r0 = rt * kRows, len = rs.len, base = rs.base;
     // CTAs of one cluster meet twice at the end, and none leaves before: what is read
     // there is still some CTA's, even if the lengths change meanwhile.

@@ -261,7 +261,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::griddep_launch_dependents();
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads;
     const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
-    const Rows rs = rows_of(L, b, head);
+    const Rows rs = rows_of(L, b, head, D);
     const int r0 = rt * kRows;
     // CTAs of one cluster meet twice at the end, and none leaves before: whatever
     // is read there is still some CTA's, even if the lengths change meanwhile.

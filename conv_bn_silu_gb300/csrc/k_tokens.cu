@@ -439,12 +439,13 @@ __device__ __forceinline__ int sequence_of(const CacheArgs &a, int i) {
 }
 
 // Where a token's rows go: its page's first row of head 0 and its slot, or -1.
+// (Tokens behind the last sequence's are padding and go nowhere.)
 struct Place { int page, slot; };
 __device__ __forceinline__ Place place_of(const CacheArgs &a, int i) {
     const int b = sequence_of(a, i);
     const int pos = b < 0 ? -1 : seq_len(a, b) - (a.new_start[b + 1] - i);
     if (pos < 0) {
-        atomicOr(a.status, kStatusBadIndex);
+        if (b >= 0 || i < a.new_start[a.batch]) atomicOr(a.status, kStatusBadIndex);
         return Place{-1, 0};
     }
     return Place{page_of(a, b, pos), pos & ((1 << a.page_shift) - 1)};

@@ -239,7 +239,12 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
     CBS_TRY(token_stride(q_stride, width, "q_stride"));
     CBS_TRY(token_stride(out_stride, width, "out_stride"));
     if (!std::isfinite(scale)) return fail(CBS_ERR_INVALID_ARG, "scale is not finite");
-    if (s->batch == 0 || s->total == 0) return CBS_OK;
+    if (s->total == 0) return CBS_OK;
+    if (s->batch == 0) {   // all tokens are padding
+        CBS_TRY(need(out, "out"));
+        return cuda_check(cudaMemset2DAsync(out, (size_t)out_stride * 2, 0, (size_t)width * 2, s->total, (cudaStream_t)stream),
+                          "zero padding");
+    }
     if (d.max_new == 0) return fail(CBS_ERR_INVALID_ARG, "%d new tokens for a plan of none", s->total);
     CBS_TRY(need(q, "q"));
     CBS_TRY(need(out, "out"));

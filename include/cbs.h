@@ -467,7 +467,9 @@ typedef struct cbs_cache {
  * slot p % page_size of page page_table[b * max_pages + p / page_size].  The
  * new tokens of all sequences lie one after another: sequence b's are
  * new_start[b] .. new_start[b + 1] - 1 of the call's `total`.  A sequence may
- * have none, and may be empty. */
+ * have none, and may be empty.  Tokens from new_start[batch] on are padding (a
+ * call of a fixed size with fewer real tokens): the cache's write leaves them
+ * out, attention writes zeros for them. */
 typedef struct cbs_sequences {
     const int32_t *new_start;    /* [batch + 1], from 0, not decreasing, at most total */
     const int32_t *seq_lens;     /* [batch] */

@@ -88,3 +88,66 @@ def test_rmsnorm_rows_whose_squares_pass_the_float_range(cuda_lib, cols, dtype):
     assert torch.equal(q.y.cpu(), codes)
     want = s.double() / root[:, 0]
     assert ((q.scale.double().cpu() - want).abs() <= want * 40 * U).all()
+
+
+# ------------------------------------------------- tokens of no sequence
+KERNELS = [B.CBS_ATTN_ROWS, B.CBS_ATTN_CHUNK, B.CBS_ATTN_CLUSTER]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d,new,split", [(64, [1, 0, 1], 1), (128, [3, 20, 0], 3), (64, [70, 5, 0], 2)])
+def test_tokens_behind_the_last_sequence_are_padding(cuda_lib, d, new, split, kernel, int8):
+    """A call of a fixed number of tokens with fewer real ones: the rest are
+    zeros from attention and left out by the cache, and nothing is reported."""
+    lens, heads, kv, page, pad = [100, 33, 300], 6, 2, 16, 37
+    paged = refs.make_paged(lens, kv, d, page, int8, 31)
+    dev = on_gpu(paged)
+    starts = [sum(new[:i]) for i in range(4)]
+    q = torch.randn((starts[-1] + pad, heads, d), generator=gen(3)).to(torch.bfloat16)
+    cache = tokens.PagedCache(dev["k"], dev["v"], dev["k_scale"], dev["v_scale"])
+    attn = tokens.PagedAttention(cache, 3, max(new), 300, heads, force_kernel=kernel, force_split=split)
+    wide = torch.full((starts[-1] + pad, heads + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    attn(q.cuda(), i32(starts), i32(lens), dev["table"], out=wide[:, 1:])
+    assert status() == B.CBS_OK
+    got = wide.double().cpu()
+    ref, mag = refs.attention(q[:starts[-1]], paged, starts, lens, page, True, 0, d ** -0.5)
+    assert ((got[:starts[-1], 1:] - ref).abs() <= refs.attention_bound(ref, mag)).all()
+    assert (got[starts[-1]:, 1:] == 0).all() and (got[:, 0] == 7).all()
+
+    before = {n: None if t is None else t.clone() for n, t in dev.items()}
+    rows = torch.randn((starts[-1] + pad, kv, d), generator=gen(4)).to(torch.bfloat16).cuda()
+    cache.write(rows, rows, i32(starts), i32(lens), dev["table"])
+    assert status() == B.CBS_OK
+    changed = (dev["k"].view(torch.uint8) != before["k"].view(torch.uint8)).flatten(3).any(-1).cpu()
+    may = torch.zeros_like(changed)
+    for b, n in enumerate(lens):
+        for pos in range(n - new[b], n):
+            may[paged["table"][b, pos // page], :, pos % page] = True
+    assert torch.equal(changed, may)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_call_of_padding_alone(cuda_lib, int8):
+    cache = tokens.PagedCache.empty(4, 2, 16, 64, dtype=torch.int8 if int8 else torch.bfloat16)
+    q = torch.randn((5, 4, 64), device="cuda").to(torch.bfloat16)
+    for lens, table in (([3, 0], [[1], [0]]), ([], torch.zeros((0, 1), dtype=torch.int32))):
+        starts, table = i32([0] * (len(lens) + 1)), torch.as_tensor(table, dtype=torch.int32, device="cuda")
+        out = torch.full((5, 5, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        tokens.PagedAttention(cache, len(lens), 1, 16, 4)(q, starts, i32(lens), table, out=out[:, :4])
+        assert (out[:, :4] == 0).all() and (out[:, 4] == 7).all()
+        cache.write(q[:, :2], q[:, 2:], starts, i32(lens), table)
+        assert status() == B.CBS_OK
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_tokens_before_the_first_sequence_are_reported(cuda_lib, new):
+    cache = tokens.PagedCache.empty(8, 2, 16, 64)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        t.fill_(1)
+    q = torch.randn((new + 1, 4, 64), device="cuda").to(torch.bfloat16)
+    args = i32([1, new + 1]), i32([100]), torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8)
+    tokens.PagedAttention(cache, 1, new, 100, 4)(q, *args)
+    assert status() == B.CBS_ERR_INVALID_ARG
+    cache.write(q[:, :2], q[:, 2:], *args)
+    assert status() == B.CBS_ERR_INVALID_ARG
