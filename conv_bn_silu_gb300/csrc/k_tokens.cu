@@ -443,7 +443,9 @@ __device__ __forceinline__ int sequence_of(const CacheArgs &a, int i) {
 struct Place { int page, slot; };
 __device__ __forceinline__ Place place_of(const CacheArgs &a, int i) {
     const int b = sequence_of(a, i);
-    const int pos = b < 0 ? -1 : seq_len(a, b) - (a.new_start[b + 1] - i);
+    // (From the length as it is: from one cut to its table's end, tokens past that
+    // would go to other positions' places.  page_of refuses them.)
+    const int pos = b < 0 ? -1 : max(a.seq_lens[b], 0) - (a.new_start[b + 1] - i);
     if (pos < 0) {
         if (b >= 0 || i < a.new_start[a.batch]) atomicOr(a.status, kStatusBadIndex);
         return Place{-1, 0};

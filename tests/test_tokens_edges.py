@@ -151,3 +151,25 @@ def test_tokens_before_the_first_sequence_are_reported(cuda_lib, new):
     assert status() == B.CBS_ERR_INVALID_ARG
     cache.write(q[:, :2], q[:, 2:], *args)
     assert status() == B.CBS_ERR_INVALID_ARG
+
+
+# ----------------------------------------------- what a table does not hold
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_writes_past_the_table_change_nothing_else(cuda_lib, d, int8):
+    """A length its table cannot hold: the tokens that have a page are written
+    to it, the others are left out and reported."""
+    cache = tokens.PagedCache.empty(3, 2, 16, d, dtype=torch.int8 if int8 else torch.bfloat16)
+    table = i32([[2, 0]])
+    x = torch.randn((5, 2, d), device="cuda")
+    for new, length, slots in ((1, 33, []), (5, 34, [29, 30, 31]), (2, 1000, []), (3, -2, [])):
+        for t in (cache.k, cache.v) + ((cache.k_scale, cache.v_scale) if int8 else ()):
+            t.fill_(1)
+        cache.write(x[:new], x[:new], i32([0, new]), i32([length]), table)
+        assert status() == B.CBS_ERR_INVALID_ARG
+        for t in (cache.k, cache.v):
+            changed = (t != 1).any(-1).cpu()
+            may = torch.zeros_like(changed)
+            for pos in slots:
+                may[(2, 0)[pos // 16], :, pos % 16] = True
+            assert torch.equal(changed, may), (new, length)
