@@ -366,7 +366,10 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int none = c.num_pages * c.kv_heads << c.page_shift;   // a row past the pool: reads as zeros
         // Lane x < boxes: the page of tile i's position x * box as loaded (two
         // tiles ahead), and from it the pool's row.
-        const auto needed = [&](int i) { return i < n && lane < boxes && key0 + i * kTile + lane * box < rs.len; };
+        const auto needed = [&](int i) {   // (pages that no row sees may be gone)
+            const int pos = key0 + i * kTile + lane * box;
+            return i < n && lane < boxes && pos + box > all.lo && pos < all.hi;
+        };
         const auto page_entry = [&](int i) -> int {
             return needed(i) ? __ldg(c.page_table + (size_t)b * c.max_pages + ((key0 + i * kTile + lane * box) >> c.page_shift)) : 0;
         };

@@ -473,7 +473,8 @@ typedef struct cbs_cache {
 typedef struct cbs_sequences {
     const int32_t *new_start;    /* [batch + 1], from 0, not decreasing, at most total */
     const int32_t *seq_lens;     /* [batch] */
-    const int32_t *page_table;   /* [batch][max_pages]; entries past a sequence's length are not read */
+    const int32_t *page_table;   /* [batch][max_pages]; entries past a sequence's length are not read,
+                                  * nor by attention those of pages that no new token sees */
     int batch, max_pages, total;
 } cbs_sequences;
 

@@ -173,3 +173,26 @@ def test_writes_past_the_table_change_nothing_else(cuda_lib, d, int8):
             for pos in slots:
                 may[(2, 0)[pos // 16], :, pos % 16] = True
             assert torch.equal(changed, may), (new, length)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("page,window,new,split", [(16, 20, 1, 1), (16, 100, 5, 2), (32, 200, 130, 1), (64, 64, 40, 3), (256, 1, 2, 1)])
+def test_pages_behind_the_window_may_be_gone(cuda_lib, page, window, new, split, kernel, int8):
+    """Table entries of pages wholly before every new token's window are not
+    looked at: a program may have released them."""
+    lens, heads, kv, d = [700, 333], 4, 2, 64
+    paged = refs.make_paged(lens, kv, d, page, int8, 33)
+    starts = [0, new, 2 * new]
+    q = torch.randn((2 * new, heads, d), generator=gen(5)).to(torch.bfloat16)
+    ref, mag = refs.attention(q, paged, starts, lens, page, True, window, d ** -0.5)
+    table = paged["table"].clone()
+    for b, n in enumerate(lens):
+        first = max(n - new - window + 1, 0)
+        table[b, : first // page] = -1
+    dev = on_gpu(paged)
+    attn = tokens.PagedAttention(tokens.PagedCache(dev["k"], dev["v"], dev["k_scale"], dev["v_scale"]), 2, new, 700, heads,
+                                 window=window, force_kernel=kernel, force_split=split)
+    got = attn(q.cuda(), i32(starts), i32(lens), table.cuda()).double().cpu()
+    assert status() == B.CBS_OK
+    assert ((got - ref).abs() <= refs.attention_bound(ref, mag)).all()
