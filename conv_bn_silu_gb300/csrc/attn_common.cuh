@@ -18,7 +18,7 @@ struct Seen { int lo, hi; };
 __device__ __forceinline__ Seen seen_by(int place, int len, int causal, int window) {
     Seen s;
     s.hi = causal ? min(len, place + 1) : len;
-    s.lo = window ? max(0, place - window + 1) : 0;
+    s.lo = window && window <= place ? place - window + 1 : 0;
     return s;
 }
 

@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     if (sp >= active) return leave();
     const int b0 = sp * per, b1 = min(blocks, b0 + per);
     // From here on every key below is seen by every row: no masks.
-    const int all_lo = L.window ? max(0, base + t_hi - L.window + 1) : 0;
-    const int all_hi = L.causal ? min(len, base + t_lo + 1) : len;
+    const int all_lo = seen_by(base + t_hi, len, L.causal, L.window).lo;
+    const int all_hi = seen_by(base + t_lo, len, L.causal, L.window).hi;
 
     if (tid == 0) s_flag = 0;
     __syncthreads();

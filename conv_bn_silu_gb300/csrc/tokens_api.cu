@@ -167,7 +167,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     p.row_tiles = (int)std::max(tiles, 1ll);
     const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
     const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p.row_tiles;
-    const int keys = d->window > 0 ? std::min(d->max_len, d->window + d->max_new) : d->max_len;
+    const int keys = d->window > 0 ? (int)std::min<long long>(d->max_len, (long long)d->window + d->max_new) : d->max_len;
     if (d->force_split) {
         p.split = p.kernel == CBS_ATTN_ROWS ? d->force_split : std::min(d->force_split, kAttnClusterMost);
     } else if (chunk) {

@@ -196,3 +196,12 @@ def test_pages_behind_the_window_may_be_gone(cuda_lib, page, window, new, split,
     got = attn(q.cuda(), i32(starts), i32(lens), table.cuda()).double().cpu()
     assert status() == B.CBS_OK
     assert ((got - ref).abs() <= refs.attention_bound(ref, mag)).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_window_as_large_as_an_int(cuda_lib, kernel, int8):
+    """It hides nothing, from tokens before a sequence's start either."""
+    from tests.test_tokens_attention import run_case
+    for causal in (True, False):
+        run_case([3, 100], [6, 2], 4, 2, 64, 16, int8, causal=causal, window=2 ** 31 - 1, kernel=kernel)
