@@ -154,14 +154,15 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         if constexpr (I8) {
             // Codes widen to f16 with fewer instructions than to bf16, so the queries
             // are f16 here, a row's largest moved to 2^14 by a power of two: exact but
-            // for values below 2^-28 of it, which keep an error of 2^-39 of it.
+            // for values below 2^-28 of it, which keep an error of 2^-39 of it.  (By
+            // 2^126 at most, whose reciprocal is a normal float.)
             float top = 0.0f;
 #pragma unroll
             for (int u = 0; u < D / 8; ++u)
                 top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[n][u] << 16)), fabsf(__uint_as_float(q[n][u] & 0xffff0000u))));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const int up = top > 0.0f ? min(268 - (int)(__float_as_uint(top) >> 23), 254) : 127;   // exponents with their bias
+            const int up = top > 0.0f ? min(268 - (int)(__float_as_uint(top) >> 23), 253) : 127;   // exponents with their bias
             const float by = __int_as_float(up << 23), back = __int_as_float((254 - up) << 23);
 #pragma unroll
             for (int u = 0; u < D / 8; ++u)
@@ -257,10 +258,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         const bool partial = now != 0xffffu || pos < all_lo || pos + kBlock > all_hi;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            s[n][0] *= ks0; s[n][1] *= ks0; s[n][2] *= ks1; s[n][3] *= ks1;
-            if constexpr (I8) {
-                s[n][0] *= q_back[n][0]; s[n][1] *= q_back[n][1];
-                s[n][2] *= q_back[n][0]; s[n][3] *= q_back[n][1];
+            // (A key's scale and the row's power of two first: their product is of
+            // ordinary size where the score is, the sum with one of them may not be.)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float ks = i < 2 ? ks0 : ks1;
+                s[n][i] *= I8 ? ks * q_back[n][i & 1] : ks;
             }
         }
         if (partial) {

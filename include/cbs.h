@@ -543,6 +543,8 @@ CBS_API cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out);
  * pos(t) = length - new + t; with a window j > pos(t) - window.  A token that
  * sees nothing gets zeros.  Positions that a token does not see cannot reach
  * it, whatever they hold (a NaN or infinity included).
+ * CBS_INT8: a score is the sum of q times the codes, times the key's scale; that
+ * sum has to stay in float's range too (|q| below 2^112 does).
  * q, out: bfloat16 [total][heads][head_dim] with q_stride, out_stride elements
  * between tokens (multiples of 8).  scale: finite.  workspace (plan's
  * workspace_bytes, which may be 0): zeroed once with cbs_workspace_init; not

@@ -205,3 +205,19 @@ def test_a_window_as_large_as_an_int(cuda_lib, kernel, int8):
     from tests.test_tokens_attention import run_case
     for causal in (True, False):
         run_case([3, 100], [6, 2], 4, 2, 64, 16, int8, causal=causal, window=2 ** 31 - 1, kernel=kernel)
+
+
+# -------------------------------------------------- attention's number range
+@pytest.mark.parametrize("kernel,size", [(k, 1e-36) for k in KERNELS] + [(k, 1e33) for k in KERNELS] +
+                         [(B.CBS_ATTN_ROWS, 1e36), (B.CBS_ATTN_CLUSTER, 1e36)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_of_any_size_over_an_8_bit_cache(cuda_lib, d, kernel, size):
+    """Queries near the float range's ends with keys that bring the scores back
+    to ordinary size: the same bound as at ordinary sizes.  (Up to 2^112, beyond
+    which sums of queries times codes may pass the range; the kernel of few rows
+    moves the queries by a power of two first.)"""
+    from tests.test_tokens_attention import run_case
+    paged = refs.make_paged([200, 77], 2, d, 16, True, 35)
+    paged["k_scale"] = paged["k_scale"] / size
+    q = (torch.randn((3, 4, d), generator=gen(6)) * size).to(torch.bfloat16)
+    run_case([200, 77], [2, 1], 4, 2, d, 16, True, q=q, paged=paged, kernel=kernel)
