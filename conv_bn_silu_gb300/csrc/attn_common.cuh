@@ -96,10 +96,11 @@ __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, i
     *reinterpret_cast<uint2 *>(s.out(L, r, D) + dim) = w;
 }
 
-// A bf16 cache's row by itself over keys [k0, k1): what the kernels fall back
-// to when a block that some rows must not see in full holds a value that is not
-// finite (0 x inf would reach them).  A warp; lane holds D / 32 dimensions.
-template <int D>
+// A row by itself over keys [k0, k1): what the kernels fall back to when a block
+// that some rows must not see in full holds a value that is not finite (0 x inf
+// would reach them; a bf16 cache), or when scores are too large for the fast
+// pass.  A warp; lane holds D / 32 dimensions.
+template <int D, bool I8>
 __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b, int r, int k0, int k1, int lane,
                                       float (&acc)[D / 32], float &mm, float &ll) {
     constexpr int kE = D / 32;
@@ -114,23 +115,28 @@ __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b,
         qv[e] = __bfloat162float(qp[e]);
         acc[e] = 0.0f;
     }
+    const auto value = [&](const void *pool, size_t at) {
+        if constexpr (I8) return (float)static_cast<const int8_t *>(pool)[at];
+        else return __bfloat162float(static_cast<const __nv_bfloat16 *>(pool)[at]);
+    };
     for (int key = max(z.lo, k0); key < min(z.hi, k1); ++key) {
         const int p = page_of(c, b, key);
         if (p < 0) continue;
-        const size_t at = ((((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1))) * D + lane * kE;
-        const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(c.k) + at, *vp = static_cast<const __nv_bfloat16 *>(c.v) + at;
+        const size_t row = (((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+        const size_t at = row * D + lane * kE;
         float dot = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) dot = fmaf(qv[e], __bfloat162float(kp[e]), dot);
+        for (int e = 0; e < kE; ++e) dot = fmaf(qv[e], value(c.k, at + e), dot);
 #pragma unroll
         for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(~0u, dot, x);
-        dot *= L.scale_log2;
+        dot = __fmul_rn(dot, I8 ? c.k_scale[row] * L.scale_log2 : L.scale_log2);   // rounded, as the maximum is
         const float nm = fmaxf(mm, dot);
         const float use = nm == -INFINITY ? 0.0f : nm;
         const float fac = mm == -INFINITY ? 0.0f : frag::ex2(mm - use), pr = frag::ex2(dot - use);
+        const float pv = I8 ? pr * c.v_scale[row] : pr;
         ll = ll * fac + pr;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = acc[e] * fac + pr * __bfloat162float(vp[e]);
+        for (int e = 0; e < kE; ++e) acc[e] = acc[e] * fac + pv * value(c.v, at + e);
         mm = nm;
     }
 }

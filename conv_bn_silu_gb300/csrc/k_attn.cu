@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float ks = i < 2 ? ks0 : ks1;
-                s[n][i] *= I8 ? ks * q_back[n][i & 1] : ks;
+                s[n][i] = __fmul_rn(s[n][i], I8 ? ks * q_back[n][i & 1] : ks);   // rounded, as the maximum is
             }
         }
         if (partial) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         constexpr int kE = D / 32;   // dimensions a lane
         for (int r = warp; r < kRows && r0 + r < R; r += kWarps) {
             float acc[kE], mm, ll;
-            slow_row<D>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
+            slow_row<D, false>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
 #pragma unroll
             for (int e = 0; e < kE; ++e) s_o[0][r][lane * kE + e] = acc[e];
             if (lane < kWarps) {

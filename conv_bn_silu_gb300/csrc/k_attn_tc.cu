@@ -196,6 +196,12 @@ __device__ __forceinline__ float tile_top(uint32_t taddr, float scale, const flo
     return fmaxf(tops[0], tops[1]);
 }
 
+// Beyond 2^22 a float's last place is more than a quarter: a score's product with
+// the scale, which tile_pass does not round, may then lie far from the reference,
+// which is rounded (from 2^31 on by 2^128 and more).  Such rows, seldom met, go
+// the slow path.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
+
 template <int D, bool I8>
 __global__ void __launch_bounds__(Chunk<D, I8>::kThreads, 1)
 attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnLaunch L) {
@@ -227,7 +233,8 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const auto raw_empty = [&](int s) { return bar(9 + C::kReady + 3 * C::kSlots + C::kPieces + s); };
     const auto slot_at = [&](int s) { return C::kRing + s * C::kOperand; };
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(sgen + C::kBars + 8 * C::kNumBars);
-    // words[0]: TMEM address; [1]: a wait ran out; [2]: a value is not finite
+    // words[0]: TMEM address; [1]: a wait ran out; [2]: the rows go the slow path (a
+    // value that some must not see is not finite, or a row's scores are far from zero)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -669,6 +676,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 m = nm;
                 ptx::bar_red_or(pair_bar, 64, false);   // `share` may be written again
             }
+            if (is_far(m)) words[2] = 1;
             tmem_st32(t_mine + part * (kCols / 2), p);
             tmem_st_wait();
             ptx::tc_fence_before();
@@ -690,13 +698,13 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // ring and Q were.
         unsigned char *const f_rows = sgen + C::kRing + h * (kHalf * D * 4);
         float2 *const stats = reinterpret_cast<float2 *>(sgen + C::kQ + C::kJoinStats);
-        if (!I8 && words[2]) {
+        if (words[2]) {
             constexpr int kE = D / 32;
             for (int x = part; x < 32; x += 2) {
                 const int row = r - lane + x;
                 if (row >= rs.R) break;
                 float acc[kE], mm, ll;
-                slow_row<D>(L, rs, b, row, key0, key0 + n * kTile, lane, acc, mm, ll);
+                slow_row<D, I8>(L, rs, b, row, key0, key0 + n * kTile, lane, acc, mm, ll);
                 if (active == 1) {
                     const Seen z = rs.seen(L, row);
                     const float inv = __fdiv_rn(1.0f, ll);

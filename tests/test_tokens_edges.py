@@ -221,3 +221,28 @@ def test_queries_of_any_size_over_an_8_bit_cache(cuda_lib, d, kernel, size):
     paged["k_scale"] = paged["k_scale"] / size
     q = (torch.randn((3, 4, d), generator=gen(6)) * size).to(torch.bfloat16)
     run_case([200, 77], [2, 1], 4, 2, d, 16, True, q=q, paged=paged, kernel=kernel)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("split", [1, 3])
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e8])
+def test_scores_far_from_zero(cuda_lib, size, split, kernel, int8):
+    """Scores so large that a float's last place is worth many powers of two:
+    the largest takes all (equal ones share).  Keys are whole multiples of one
+    vector, so scores are either equal or apart by 1/127 of the largest."""
+    from tests.test_tokens_attention import run_case
+    n, d, page, new = 500, 64, 16, 40
+    paged = refs.make_paged([n], 1, d, page, int8, 36)
+    g = torch.randint(-127, 128, (n,), generator=gen(7))
+    for pos in range(n):
+        p, slot = paged["table"][0, pos // page], pos % page
+        if int8:
+            paged["k"][p, 0, slot], paged["k_scale"][p, 0, slot] = g[pos].to(torch.int8), size
+        else:
+            paged["k"][p, 0, slot] = (g[pos] * torch.ones(d)).to(torch.bfloat16) * size
+    q = torch.ones((new, 4, d)) * size
+    q[:, 1] *= -1
+    q[::2, 2] *= -0.25
+    q[:, 3] = 0
+    run_case([n], [new], 4, 1, d, page, int8, q=q.to(torch.bfloat16), paged=paged, kernel=kernel, split=split)
