@@ -314,14 +314,23 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
             for (int i = 0; i < 4; ++i) {
                 const float mm = m[n][i & 1] == -INFINITY ? 0.0f : m[n][i & 1];
                 p[i] = frag::ex2(s[n][i] - mm);
-                l[n][i & 1] += p[i];
-                // a masked key's scale may be anything
-                if (I8) p[i] = s[n][i] == -INFINITY ? 0.0f : p[i] * f.vs[i >> 1];
+                if (I8) {
+                    l[n][i & 1] += p[i];
+                    // a masked key's scale may be anything
+                    p[i] = s[n][i] == -INFINITY ? 0.0f : p[i] * f.vs[i >> 1];
+                }
             }
             // Rounded to bf16 for the second product: half a unit in 2^-8 of
-            // each term, of either sign, below the output's own rounding.
-            p0[n] = frag::transpose8x8(frag::pack_bf16(p[0], p[1]));
-            p1[n] = frag::transpose8x8(frag::pack_bf16(p[2], p[3]));
+            // each term, of either sign, below the output's own rounding.  The sum
+            // that divides is of the rounded ones; in 8 bits they carry the values'
+            // scales, and it is of the probabilities before them.
+            const uint32_t w0 = frag::pack_bf16(p[0], p[1]), w1 = frag::pack_bf16(p[2], p[3]);
+            if (!I8) {
+                l[n][0] = frag::add_bf16(frag::add_bf16(l[n][0], w0), w1);
+                l[n][1] = frag::add_bf16(frag::add_bf16(l[n][1], w0 >> 16), w1 >> 16);
+            }
+            p0[n] = frag::transpose8x8(w0);
+            p1[n] = frag::transpose8x8(w1);
         }
         // ---- O^T += V^T P^T
         if (!I8 && partial) {

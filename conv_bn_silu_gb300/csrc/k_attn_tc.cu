@@ -127,7 +127,8 @@ __device__ __forceinline__ float2 split(F2 a) {
 
 // A thread's pass over its kCols of a row's scores: t = s * scale - ref (ks: a scale a key,
 // for 8-bit keys), p = 2^t (times vs, for 8-bit values) as bf16 pairs, the
-// largest t and the sum of 2^t.  MASK: columns outside [first, end) are not
+// largest t and the sum of p as rounded (8 bits: of 2^t, since p has the value's
+// scale in it).  MASK: columns outside [first, end) are not
 // seen.  Rounding p to bf16 moves each term by at most 2^-8 of itself, either
 // way, as the output's own rounding does.
 template <bool I8, bool MASK>
@@ -136,6 +137,7 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
     constexpr int kPart = I8 ? 8 : 16;   // columns at a time: of more, registers spilled
     const F2 scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
     F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+    float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int q = 0; q < kCols / kPart; ++q) {
@@ -161,20 +163,28 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
                 }
                 tops[x] = fmaxf(tops[x], fmaxf(t.x, t.y));
                 F2 pr = pair(frag::ex2(t.x), frag::ex2(t.y));
-                acc[x] = add2(acc[x], pr);
-                if constexpr (I8) pr = mul2(pr, w2[x]);
+                if constexpr (I8) {
+                    acc[x] = add2(acc[x], pr);
+                    pr = mul2(pr, w2[x]);
+                }
                 float2 y = split(pr);
                 if constexpr (I8 && MASK) {   // a hidden key's scale may be anything
                     if (t.x == -INFINITY) y.x = 0.0f;
                     if (t.y == -INFINITY) y.y = 0.0f;
                 }
-                p[kPart / 2 * q + (e >> 1) + x] = frag::pack_bf16(y.x, y.y);
+                const uint32_t both = frag::pack_bf16(y.x, y.y);
+                if constexpr (!I8) sums[x].x = frag::add_bf16(sums[x].x, both), sums[x].y = frag::add_bf16(sums[x].y, both >> 16);
+                p[kPart / 2 * q + (e >> 1) + x] = both;
             }
         }
     }
     top = fmaxf(tops[0], tops[1]);
-    const float2 a = split(add2(acc[0], acc[1]));
-    sum = a.x + a.y;
+    if constexpr (I8) {
+        const float2 a = split(add2(acc[0], acc[1]));
+        sum = a.x + a.y;
+    } else {
+        sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+    }
 }
 
 // The largest of a thread's scores, in base 2.

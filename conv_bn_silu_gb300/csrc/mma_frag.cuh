@@ -59,6 +59,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
+// sum + the bf16 value in the low half of v.
+__device__ __forceinline__ float add_bf16(float sum, uint32_t v) {
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(sum) : "h"((uint16_t)v));
+    return sum;
+}
+
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

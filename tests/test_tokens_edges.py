@@ -246,3 +246,28 @@ def test_scores_far_from_zero(cuda_lib, size, split, kernel, int8):
     q[::2, 2] *= -0.25
     q[:, 3] = 0
     run_case([n], [new], 4, 1, d, page, int8, q=q.to(torch.bfloat16), paged=paged, kernel=kernel, split=split)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("split", [1, 3])
+def test_equal_values_come_back(cuda_lib, split, d, kernel):
+    """An average of equal values is that value, however the probabilities were
+    rounded: the sum that divides is of the rounded ones.  Sixty keys carry 93% to
+    99% of the weight, at probabilities of 2^4 to 2^7.9 (the running maximum is not
+    raised for them).  Sums of 900 products in float are within 2^-13 of
+    themselves, far less than half a place of bfloat16."""
+    n, page, heads, new = 900, 16, 4, 60
+    paged = refs.make_paged([n], 1, d, page, False, 37)
+    value = torch.tensor(255 / 128, dtype=torch.bfloat16)
+    for side, x in (("k", 0.0), ("v", value)):
+        paged[side][~paged[side].isnan()] = x
+    for pos in range(n - 60, n):
+        paged["k"][paged["table"][0, pos // page], 0, pos % page] = 1.0
+    rows = torch.linspace(4, 7.9, new * heads) * math.log(2)
+    q = rows.view(new, heads, 1).expand(new, heads, d).to(torch.bfloat16)
+    dev = on_gpu(paged)
+    attn = tokens.PagedAttention(tokens.PagedCache(dev["k"], dev["v"]), 1, new, n, heads, causal=False, scale=1 / d,
+                                 force_kernel=kernel, force_split=split)
+    out = attn(q.cuda().contiguous(), i32([0, new]), i32([n]), dev["table"])
+    assert (out == value.cuda()).all()
