@@ -30,16 +30,19 @@ struct Refused {};   // a Python error is set
     throw Refused{};
 }
 
-const Tensor &tensor(PyObject *o, const char *name) {
+// A CUDA tensor, on the device of `like` if one is given: addresses of another
+// device's memory must not reach a kernel.
+const Tensor &tensor(PyObject *o, const char *name, const Tensor *like = nullptr) {
     if (!THPVariable_Check(o)) refuse(name, "expected a CUDA tensor");
     const Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse(name, "expected a CUDA tensor");
+    if (like && t.device() != like->device()) refuse(name, "on another device");
     return t;
 }
 
 // A contiguous tensor of a type and shape (-1: any extent).
-const Tensor &dense(PyObject *o, const char *name, ScalarType type, std::initializer_list<int64_t> shape) {
-    const Tensor &t = tensor(o, name);
+const Tensor &dense(PyObject *o, const char *name, const Tensor *like, ScalarType type, std::initializer_list<int64_t> shape) {
+    const Tensor &t = tensor(o, name, like);
     if (t.scalar_type() != type) refuse(name, "unexpected type");
     if (!t.is_contiguous()) refuse(name, "not contiguous");
     if (t.dim() != (int64_t)shape.size()) refuse(name, "unexpected number of dimensions");
@@ -79,6 +82,10 @@ long integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw Refused{};
     return v;
 }
+// The device of a layer's or a cache's own arrays, which their owner has checked.
+void at_home(const Tensor &t, const char *name, PyObject *device) {
+    if (t.get_device() != integer(device)) refuse(name, "not on the device of the layer or cache");
+}
 PyObject *status(cbs_status s) { return PyLong_FromLong(s); }
 PyObject *none() { Py_RETURN_NONE; }
 PyObject *triple(PyObject *a, PyObject *b, PyObject *c) {
@@ -90,15 +97,17 @@ PyObject *triple(PyObject *a, PyObject *b, PyObject *c) {
 }
 
 // The sequences of a call, their arrays checked.
-cbs_sequences sequences(PyObject *starts, PyObject *lens, PyObject *table, int64_t total) {
+cbs_sequences sequences(PyObject *starts, PyObject *lens, PyObject *table, int64_t total, const Tensor *like) {
+    const Tensor &t = dense(table, "page_table", like, ScalarType::Int, {-1, -1});
+    const Tensor &n = dense(lens, "seq_lens", &t, ScalarType::Int, {t.size(0)});
+    const Tensor *s0 = starts == Py_None ? nullptr : &dense(starts, "new_start", &t, ScalarType::Int, {t.size(0) + 1});
     cbs_sequences s;
-    const Tensor &t = dense(table, "page_table", ScalarType::Int, {-1, -1});
     s.batch = (int)t.size(0);
     s.max_pages = (int)t.size(1);
     s.total = (int)total;
     s.page_table = t.data_ptr<int>();
-    s.seq_lens = dense(lens, "seq_lens", ScalarType::Int, {t.size(0)}).data_ptr<int>();
-    s.new_start = starts == Py_None ? nullptr : dense(starts, "new_start", ScalarType::Int, {t.size(0) + 1}).data_ptr<int>();
+    s.seq_lens = n.data_ptr<int>();
+    s.new_start = s0 ? s0->data_ptr<int>() : nullptr;
     return s;
 }
 
@@ -106,37 +115,32 @@ cbs_sequences sequences(PyObject *starts, PyObject *lens, PyObject *table, int64
 PyObject *rmsnorm(PyObject *const *a) {
     const Tensor &x = tensor(a[0], "x");
     if (!is_float(x.scalar_type())) refuse("x", "expected float32 or bfloat16");
-    dense(a[0], "x", x.scalar_type(), {-1, -1});
+    dense(a[0], "x", nullptr, x.scalar_type(), {-1, -1});
     const int64_t rows = x.size(0), cols = x.size(1);
-    const Tensor &w = dense(a[1], "weight", ScalarType::Float, {cols});
+    const Tensor &w = dense(a[1], "weight", &x, ScalarType::Float, {cols});
     const double eps = PyFloat_AsDouble(a[2]);
     if (PyErr_Occurred()) throw Refused{};
     const bool int8 = PyObject_IsTrue(a[4]) == 1;
-    const c10::cuda::CUDAGuard guard(x.device());
+    const Tensor *residual = a[3] == Py_None ? nullptr : &dense(a[3], "residual", &x, x.scalar_type(), {rows, cols});
+    if (!residual && a[5] != Py_None) refuse("h_out", "without a residual it is x itself");
     Tensor h;
-    const void *residual = nullptr;
-    void *h_at = nullptr;
-    if (a[3] != Py_None) {
-        residual = dense(a[3], "residual", x.scalar_type(), {rows, cols}).data_ptr();
-        h = a[5] != Py_None ? dense(a[5], "h_out", x.scalar_type(), {rows, cols}) : empty({rows, cols}, x.scalar_type(), x);
-        h_at = h.data_ptr();
-    } else if (a[5] != Py_None) {
-        refuse("h_out", "without a residual it is x itself");
-    }
+    if (a[5] != Py_None) h = dense(a[5], "h_out", &x, x.scalar_type(), {rows, cols});
+    const c10::cuda::CUDAGuard guard(x.device());
+    if (residual && !h.defined()) h = empty({rows, cols}, x.scalar_type(), x);
     Tensor y = empty({rows, cols}, int8 ? ScalarType::Char : x.scalar_type(), x), scale;
     if (int8) scale = empty({rows}, ScalarType::Float, x);
-    const cbs_status s = cbs_rmsnorm(x.data_ptr(), residual, w.data_ptr<float>(), h_at, y.data_ptr(),
-                                     int8 ? scale.data_ptr<float>() : nullptr, (int)rows, (int)cols, (float)eps,
-                                     prec(x.scalar_type()), prec(y.scalar_type()), stream_of(x));
+    const cbs_status s = cbs_rmsnorm(x.data_ptr(), residual ? residual->data_ptr() : nullptr, w.data_ptr<float>(),
+                                     h.defined() ? h.data_ptr() : nullptr, y.data_ptr(), int8 ? scale.data_ptr<float>() : nullptr,
+                                     (int)rows, (int)cols, (float)eps, prec(x.scalar_type()), prec(y.scalar_type()), stream_of(x));
     if (s != CBS_OK) return status(s);
-    PyObject *h_py = a[3] == Py_None ? Py_NewRef(a[0]) : a[5] != Py_None ? Py_NewRef(a[5]) : THPVariable_Wrap(h);
+    PyObject *h_py = !residual ? Py_NewRef(a[0]) : a[5] != Py_None ? Py_NewRef(a[5]) : THPVariable_Wrap(h);
     return triple(THPVariable_Wrap(y), int8 ? THPVariable_Wrap(scale) : none(), h_py);
 }
 
 // dequantize_rows(q, scale, bf16) -> out
 PyObject *dequantize_rows(PyObject *const *a) {
-    const Tensor &q = dense(a[0], "q", ScalarType::Char, {-1, -1});
-    const Tensor &scale = dense(a[1], "scale", ScalarType::Float, {q.size(0)});
+    const Tensor &q = dense(a[0], "q", nullptr, ScalarType::Char, {-1, -1});
+    const Tensor &scale = dense(a[1], "scale", &q, ScalarType::Float, {q.size(0)});
     const c10::cuda::CUDAGuard guard(q.device());
     Tensor out = empty(q.sizes(), PyObject_IsTrue(a[2]) == 1 ? ScalarType::BFloat16 : ScalarType::Float, q);
     const cbs_status s = cbs_dequantize_rows(q.data_ptr<int8_t>(), scale.data_ptr<float>(), out.data_ptr(), (int)q.size(0),
@@ -144,87 +148,90 @@ PyObject *dequantize_rows(PyObject *const *a) {
     return s != CBS_OK ? status(s) : THPVariable_Wrap(out);
 }
 
-// linear_w4(x, x_scale, out, bf16, n, k, group, activation, w, scales, zeros, bias) -> out;
+// linear_w4(x, x_scale, out, bf16, device, n, k, group, activation, w, scales, zeros, bias) -> out;
 // the layer's own arrays as addresses (their owner has checked and keeps them)
 PyObject *linear_w4(PyObject *const *a) {
     const Tensor &x = tensor(a[0], "x");
     const bool int8 = x.scalar_type() == ScalarType::Char;
     if (!int8 && x.scalar_type() != ScalarType::BFloat16) refuse("x", "expected bfloat16 or int8");
-    const int n = (int)integer(a[4]), k = (int)integer(a[5]);
-    dense(a[0], "x", x.scalar_type(), {-1, k});
+    const int n = (int)integer(a[5]), k = (int)integer(a[6]);
+    dense(a[0], "x", nullptr, x.scalar_type(), {-1, k});
+    at_home(x, "x", a[4]);
     const int64_t rows = x.size(0);
     if ((a[1] != Py_None) != int8) refuse("x_scale", "with int8 inputs, and only with them");
-    const float *x_scale = int8 ? dense(a[1], "x_scale", ScalarType::Float, {rows}).data_ptr<float>() : nullptr;
-    const c10::cuda::CUDAGuard guard(x.device());
+    const Tensor *x_scale = int8 ? &dense(a[1], "x_scale", &x, ScalarType::Float, {rows}) : nullptr;
     Tensor out;
     if (a[2] != Py_None) {
         out = tensor(a[2], "out");
         if (!is_float(out.scalar_type())) refuse("out", "expected float32 or bfloat16");
-        dense(a[2], "out", out.scalar_type(), {rows, n});
-    } else {
-        out = empty({rows, n}, PyObject_IsTrue(a[3]) == 1 ? ScalarType::BFloat16 : ScalarType::Float, x);
+        dense(a[2], "out", &x, out.scalar_type(), {rows, n});
     }
-    const cbs_status s = cbs_linear_w4(x.data_ptr(), prec(x.scalar_type()), x_scale, pointer(a[8]), pointer(a[9]), pointer(a[10]),
-                                       static_cast<const float *>(pointer(a[11])), out.data_ptr(), prec(out.scalar_type()),
-                                       (int)rows, n, k, (int)integer(a[6]), (int)integer(a[7]), stream_of(x));
+    const c10::cuda::CUDAGuard guard(x.device());
+    if (!out.defined()) out = empty({rows, n}, PyObject_IsTrue(a[3]) == 1 ? ScalarType::BFloat16 : ScalarType::Float, x);
+    const cbs_status s = cbs_linear_w4(x.data_ptr(), prec(x.scalar_type()), int8 ? x_scale->data_ptr<float>() : nullptr,
+                                       pointer(a[9]), pointer(a[10]), pointer(a[11]), static_cast<const float *>(pointer(a[12])),
+                                       out.data_ptr(), prec(out.scalar_type()), (int)rows, n, k, (int)integer(a[7]),
+                                       (int)integer(a[8]), stream_of(x));
     if (s != CBS_OK) return status(s);
     return a[2] != Py_None ? Py_NewRef(a[2]) : THPVariable_Wrap(out);
 }
 
-// cache_write(cache, k, v, new_start, seq_lens, page_table)
+// cache_write(cache, device, k, v, new_start, seq_lens, page_table)
 PyObject *cache_write(PyObject *const *a) {
     const auto *c = static_cast<const cbs_cache *>(pointer(a[0]));
-    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v", &k);
+    at_home(k, "k", a[1]);
     if (!is_float(k.scalar_type())) refuse("k", "expected float32 or bfloat16");
     const int64_t ks = token_stride(k, "k", k.scalar_type(), c->kv_heads, c->head_dim);
     const int64_t vs = token_stride(v, "v", k.scalar_type(), c->kv_heads, c->head_dim);
     if (k.size(0) != v.size(0)) refuse("v", "expected the tokens of k");
-    const cbs_sequences seqs = sequences(a[3], a[4], a[5], k.size(0));
+    const cbs_sequences seqs = sequences(a[4], a[5], a[6], k.size(0), &k);
     const c10::cuda::CUDAGuard guard(k.device());
     const cbs_status s = cbs_cache_write(c, &seqs, k.data_ptr(), ks, v.data_ptr(), vs, prec(k.scalar_type()), stream_of(k));
     if (s != CBS_OK) return status(s);
     Py_RETURN_NONE;
 }
 
-// cache_read(cache, seq_lens, page_table, max_len, bf16) -> (k, v, None)
+// cache_read(cache, device, seq_lens, page_table, max_len, bf16) -> (k, v, None)
 PyObject *cache_read(PyObject *const *a) {
     const auto *c = static_cast<const cbs_cache *>(pointer(a[0]));
-    const cbs_sequences seqs = sequences(Py_None, a[1], a[2], 0);
-    const long max_len = integer(a[3]);
+    const Tensor &like = tensor(a[2], "seq_lens");
+    at_home(like, "seq_lens", a[1]);
+    const long max_len = integer(a[4]);
     if (max_len < 0 || max_len > INT_MAX) refuse("max_len", "out of range");
-    const Tensor &like = THPVariable_Unpack(a[1]);
+    const cbs_sequences seqs = sequences(Py_None, a[2], a[3], 0, &like);
     const c10::cuda::CUDAGuard guard(like.device());
-    const ScalarType type = PyObject_IsTrue(a[4]) == 1 ? ScalarType::BFloat16 : ScalarType::Float;
+    const ScalarType type = PyObject_IsTrue(a[5]) == 1 ? ScalarType::BFloat16 : ScalarType::Float;
     Tensor k = empty({seqs.batch, max_len, c->kv_heads, c->head_dim}, type, like);
     Tensor v = empty({seqs.batch, max_len, c->kv_heads, c->head_dim}, type, like);
     const cbs_status s = cbs_cache_read(c, &seqs, (int)max_len, k.data_ptr(), v.data_ptr(), prec(type), stream_of(like));
     return s != CBS_OK ? status(s) : triple(THPVariable_Wrap(k), THPVariable_Wrap(v), none());
 }
 
-// attention(plan, cache, q, new_start, seq_lens, page_table, scale, out, workspace) -> out
+// attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace) -> out
 PyObject *attention(PyObject *const *a) {
     const auto *p = static_cast<const cbs_attn_plan_t *>(pointer(a[0]));
     const auto *c = static_cast<const cbs_cache *>(pointer(a[1]));
     const int heads = p->desc.heads, d = c->head_dim;
-    const Tensor &q = tensor(a[2], "q");
+    const Tensor &q = tensor(a[3], "q");
+    at_home(q, "q", a[2]);
     const int64_t qs = token_stride(q, "q", ScalarType::BFloat16, heads, d);
-    const cbs_sequences seqs = sequences(a[3], a[4], a[5], q.size(0));
-    const double scale = PyFloat_AsDouble(a[6]);
+    const double scale = PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) throw Refused{};
-    const c10::cuda::CUDAGuard guard(q.device());
     Tensor out;
     int64_t os = (int64_t)heads * d;
-    if (a[7] != Py_None) {
-        out = tensor(a[7], "out");
+    if (a[8] != Py_None) {
+        out = tensor(a[8], "out", &q);
         os = token_stride(out, "out", ScalarType::BFloat16, heads, d);
         if (out.size(0) != q.size(0)) refuse("out", "expected the tokens of q");
-    } else {
-        out = empty({q.size(0), heads, d}, ScalarType::BFloat16, q);
     }
-    const cbs_status s = cbs_paged_attention(p, c, &seqs, q.data_ptr(), qs, (float)scale, out.data_ptr(), os, pointer(a[8]),
+    const cbs_sequences seqs = sequences(a[4], a[5], a[6], q.size(0), &q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    if (!out.defined()) out = empty({q.size(0), heads, d}, ScalarType::BFloat16, q);
+    const cbs_status s = cbs_paged_attention(p, c, &seqs, q.data_ptr(), qs, (float)scale, out.data_ptr(), os, pointer(a[9]),
                                              p->workspace_bytes, stream_of(q));
     if (s != CBS_OK) return status(s);
-    return a[7] != Py_None ? Py_NewRef(a[7]) : THPVariable_Wrap(out);
+    return a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(out);
 }
 
 template <PyObject *(*F)(PyObject *const *), int N>
@@ -244,8 +251,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 #define CBS_PY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 12), CBS_PY(cache_write, 6),
-                         CBS_PY(cache_read, 5), CBS_PY(attention, 9),       {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 13), CBS_PY(cache_write, 7),
+                         CBS_PY(cache_read, 6), CBS_PY(attention, 10),       {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", "The token operators' calls (see tokens.py).", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -4,8 +4,8 @@ tokens over it.  One quantised step of a model that answers in tokens about
 what the layers saw; `token_head` runs them together.
 
 PyTorch supplies device memory and streams; every value is computed in
-libcbs.so's kernels, on the current stream.  Tensors are contiguous unless an
-argument says that it may be a slice.  Types and shapes are checked by the calls
+libcbs.so's kernels, on the current stream of the tensors' device (all of a call's
+are on one).  Tensors are contiguous unless an argument says that it may be a slice.  Types and shapes are checked by the calls
 of csrc/tokens_py.cpp (ValueError), the rest (alignment, limits) by the C calls
 behind them, which raise CbsError.
 """
@@ -54,9 +54,11 @@ def _refuse(message: str):
     raise ValueError(message)
 
 
-def _dense(t: torch.Tensor, name: str, dtypes, shape=None):
+def _dense(t: torch.Tensor, name: str, dtypes, shape=None, device=None):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         _refuse(f"{name}: expected a CUDA tensor")
+    if device is not None and t.device != device:
+        _refuse(f"{name}: on {t.device}, not on {device}")
     if t.dtype not in dtypes:
         _refuse(f"{name}: {t.dtype}, expected one of {[str(d) for d in dtypes]}")
     if not t.is_contiguous():
@@ -97,14 +99,14 @@ class LinearW4:
         if self.k % group:
             _refuse(f"k = {self.k} is not a multiple of the group ({group})")
         shape = (self.k // group, self.n)
-        _dense(scales, "scales", (_BF16,), shape)
+        _dense(scales, "scales", (_BF16,), shape, packed.device)
         if zeros is not None:
-            _dense(zeros, "zeros", (torch.uint8,), shape)
+            _dense(zeros, "zeros", (torch.uint8,), shape, packed.device)
         if bias is not None:
-            _dense(bias, "bias", (_F32,), (self.n,))
+            _dense(bias, "bias", (_F32,), (self.n,), packed.device)
         self.packed, self.scales, self.zeros, self.bias, self.activation = packed, scales, zeros, bias, activation
-        # what a call needs of the layer: its sizes, and its own tensors (held above)
-        self._args = (self.n, self.k, group, activation, *map(B._p, (packed, scales, zeros, bias)))
+        # what a call needs of the layer: its device and sizes, and its own tensors (held above)
+        self._args = (packed.device.index, self.n, self.k, group, activation, *map(B._p, (packed, scales, zeros, bias)))
 
     @classmethod
     def quantize(cls, w: torch.Tensor, group: int = 64, bias: torch.Tensor | None = None,
@@ -117,7 +119,8 @@ class LinearW4:
         n, k = w.shape
         packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty((k // group, n), dtype=_BF16, device=w.device)
-        B.cbs_quantize_w4(w, n, k, group, packed, scales, current_stream())
+        with torch.cuda.device(w.device):
+            B.cbs_quantize_w4(w, n, k, group, packed, scales, current_stream())
         return cls(packed, scales, group, bias=bias, activation=activation)
 
     def __call__(self, x: torch.Tensor, x_scale: torch.Tensor | None = None, dtype=torch.bfloat16,
@@ -137,19 +140,19 @@ class PagedCache:
         _dense(k, "k", (_BF16, _I8))
         if k.dim() != 4:
             _refuse("k: expected [num_pages, kv_heads, page_size, head_dim]")
-        _dense(v, "v", (k.dtype,), k.shape)
+        _dense(v, "v", (k.dtype,), k.shape, k.device)
         int8 = k.dtype == _I8
         if (k_scale is not None) != int8 or (v_scale is not None) != int8:
             _refuse("scales: with an int8 cache, and only there")
         if int8:
-            _dense(k_scale, "k_scale", (_F32,), k.shape[:3])
-            _dense(v_scale, "v_scale", (_F32,), k.shape[:3])
+            _dense(k_scale, "k_scale", (_F32,), k.shape[:3], k.device)
+            _dense(v_scale, "v_scale", (_F32,), k.shape[:3], k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.prec = B.CBS_INT8 if int8 else B.CBS_BF16
         self.desc = B.cbs_cache(B._p(k), B._p(v), B._p(k_scale), B._p(v_scale), self.prec, *(
             self.num_pages, self.page_size, self.kv_heads, self.head_dim))
-        self._at = ctypes.addressof(self.desc)
+        self._at = ctypes.addressof(self.desc), k.device.index
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=torch.int8, device="cuda"):
@@ -164,14 +167,14 @@ class PagedCache:
         """The new tokens' keys and values ([tokens, kv_heads, head_dim],
         float32 or bfloat16; slices of a fused product's rows do) into their
         pages.  seq_lens counts the new tokens."""
-        _done(_calls().cache_write(self._at, k, v, new_start, seq_lens, page_table), "cbs_cache_write")
+        _done(_calls().cache_write(*self._at, k, v, new_start, seq_lens, page_table), "cbs_cache_write")
 
     def read(self, seq_lens: torch.Tensor, page_table: torch.Tensor, max_len: int, dtype=torch.bfloat16):
         """The sequences' keys and values in order, each
         [batch, max_len, kv_heads, head_dim], zero past a sequence's length."""
         if dtype not in _FLOATS:
             _refuse("dtype: float32 or bfloat16")
-        return _done(_calls().cache_read(self._at, seq_lens, page_table, max_len, dtype is _BF16), "cbs_cache_read")[:2]
+        return _done(_calls().cache_read(*self._at, seq_lens, page_table, max_len, dtype is _BF16), "cbs_cache_read")[:2]
 
 
 class PagedAttention:
@@ -183,8 +186,10 @@ class PagedAttention:
                  window: int = 0, scale: float | None = None, force_kernel: int = -1, force_split: int = 0):
         self.cache, self.heads = cache, heads
         self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        with torch.cuda.device(cache.k.device):
+            sms = device_sms()
         desc = B.cbs_attn_desc(batch, max_new, max_len, heads, cache.kv_heads, cache.head_dim, cache.prec, int(causal),
-                               window, device_sms(), force_kernel, force_split)
+                               window, sms, force_kernel, force_split)
         self.plan = B.cbs_attn_plan(desc)
         self._plan_at = ctypes.addressof(self.plan)
         self._make_workspace()
@@ -194,7 +199,8 @@ class PagedAttention:
         self.workspace = self._workspace_at = None
         if self.workspace_bytes:
             self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.cache.k.device)
-            B.cbs_workspace_init(self.workspace, self.workspace_bytes, current_stream())
+            with torch.cuda.device(self.workspace.device):
+                B.cbs_workspace_init(self.workspace, self.workspace_bytes, current_stream())
             self._workspace_at = self.workspace.data_ptr()
 
     def fork(self) -> "PagedAttention":
@@ -208,5 +214,5 @@ class PagedAttention:
                  out: torch.Tensor | None = None) -> torch.Tensor:
         """q: bfloat16 [tokens, heads, head_dim] (a slice of a fused product's
         rows does).  The cache already holds the new tokens."""
-        return _done(_calls().attention(self._plan_at, self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
+        return _done(_calls().attention(self._plan_at, *self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
                                         self._workspace_at), "cbs_paged_attention")
