@@ -14,6 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/cbs.h"
@@ -82,6 +83,11 @@ long integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw Refused{};
     return v;
 }
+bool flag(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v != 0;
+}
 // The device of a layer's or a cache's own arrays, which their owner has checked.
 void at_home(const Tensor &t, const char *name, PyObject *device) {
     if (t.get_device() != integer(device)) refuse(name, "not on the device of the layer or cache");
@@ -120,7 +126,7 @@ PyObject *rmsnorm(PyObject *const *a) {
     const Tensor &w = dense(a[1], "weight", &x, ScalarType::Float, {cols});
     const double eps = PyFloat_AsDouble(a[2]);
     if (PyErr_Occurred()) throw Refused{};
-    const bool int8 = PyObject_IsTrue(a[4]) == 1;
+    const bool int8 = flag(a[4]);
     const Tensor *residual = a[3] == Py_None ? nullptr : &dense(a[3], "residual", &x, x.scalar_type(), {rows, cols});
     if (!residual && a[5] != Py_None) refuse("h_out", "without a residual it is x itself");
     Tensor h;
@@ -141,8 +147,9 @@ PyObject *rmsnorm(PyObject *const *a) {
 PyObject *dequantize_rows(PyObject *const *a) {
     const Tensor &q = dense(a[0], "q", nullptr, ScalarType::Char, {-1, -1});
     const Tensor &scale = dense(a[1], "scale", &q, ScalarType::Float, {q.size(0)});
+    const ScalarType type = flag(a[2]) ? ScalarType::BFloat16 : ScalarType::Float;
     const c10::cuda::CUDAGuard guard(q.device());
-    Tensor out = empty(q.sizes(), PyObject_IsTrue(a[2]) == 1 ? ScalarType::BFloat16 : ScalarType::Float, q);
+    Tensor out = empty(q.sizes(), type, q);
     const cbs_status s = cbs_dequantize_rows(q.data_ptr<int8_t>(), scale.data_ptr<float>(), out.data_ptr(), (int)q.size(0),
                                              (int)q.size(1), prec(out.scalar_type()), stream_of(q));
     return s != CBS_OK ? status(s) : THPVariable_Wrap(out);
@@ -167,7 +174,7 @@ PyObject *linear_w4(PyObject *const *a) {
         dense(a[2], "out", &x, out.scalar_type(), {rows, n});
     }
     const c10::cuda::CUDAGuard guard(x.device());
-    if (!out.defined()) out = empty({rows, n}, PyObject_IsTrue(a[3]) == 1 ? ScalarType::BFloat16 : ScalarType::Float, x);
+    if (!out.defined()) out = empty({rows, n}, flag(a[3]) ? ScalarType::BFloat16 : ScalarType::Float, x);
     const cbs_status s = cbs_linear_w4(x.data_ptr(), prec(x.scalar_type()), int8 ? x_scale->data_ptr<float>() : nullptr,
                                        pointer(a[9]), pointer(a[10]), pointer(a[11]), static_cast<const float *>(pointer(a[12])),
                                        out.data_ptr(), prec(out.scalar_type()), (int)rows, n, k, (int)integer(a[7]),
@@ -201,7 +208,7 @@ PyObject *cache_read(PyObject *const *a) {
     if (max_len < 0 || max_len > INT_MAX) refuse("max_len", "out of range");
     const cbs_sequences seqs = sequences(Py_None, a[2], a[3], 0, &like);
     const c10::cuda::CUDAGuard guard(like.device());
-    const ScalarType type = PyObject_IsTrue(a[5]) == 1 ? ScalarType::BFloat16 : ScalarType::Float;
+    const ScalarType type = flag(a[5]) ? ScalarType::BFloat16 : ScalarType::Float;
     Tensor k = empty({seqs.batch, max_len, c->kv_heads, c->head_dim}, type, like);
     Tensor v = empty({seqs.batch, max_len, c->kv_heads, c->head_dim}, type, like);
     const cbs_status s = cbs_cache_read(c, &seqs, (int)max_len, k.data_ptr(), v.data_ptr(), prec(type), stream_of(like));
@@ -244,8 +251,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
         return F(args);
     } catch (const Refused &) {
         return nullptr;
-    } catch (const std::exception &e) {   // an allocation that failed, for one
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {   // PyTorch's own, as from its own calls: an allocation that failed, for one
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

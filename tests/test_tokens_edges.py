@@ -271,3 +271,17 @@ def test_equal_values_come_back(cuda_lib, split, d, kernel):
                                  force_kernel=kernel, force_split=split)
     out = attn(q.cuda().contiguous(), i32([0, new]), i32([n]), dev["table"])
     assert (out == value.cuda()).all()
+
+
+# ------------------------------------------------------- calls from Python
+def test_errors_of_the_calls(cuda_lib):
+    """An output that does not fit memory raises what an allocation raises;
+    a flag that has no truth value raises its own error."""
+    cache = tokens.PagedCache.empty(4, 2, 16, 64)
+    with pytest.raises(torch.OutOfMemoryError):
+        cache.read(i32([3]), i32([[0]]), 2 ** 31 - 1)
+    x = torch.zeros((2, 8), device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        tokens.rmsnorm(x, torch.ones(8, device="cuda"), 1e-5, int8=torch.ones(2))
+    k, _ = cache.read(i32([0]), i32([[0]]), 3)
+    assert (k == 0).all() and status() == B.CBS_OK
