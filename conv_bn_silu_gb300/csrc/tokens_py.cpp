@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -215,7 +216,7 @@ PyObject *cache_read(PyObject *const *a) {
     return s != CBS_OK ? status(s) : triple(THPVariable_Wrap(k), THPVariable_Wrap(v), none());
 }
 
-// attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace) -> out
+// attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace, its stream) -> out
 PyObject *attention(PyObject *const *a) {
     const auto *p = static_cast<const cbs_attn_plan_t *>(pointer(a[0]));
     const auto *c = static_cast<const cbs_cache *>(pointer(a[1]));
@@ -235,8 +236,16 @@ PyObject *attention(PyObject *const *a) {
     const cbs_sequences seqs = sequences(a[4], a[5], a[6], q.size(0), &q);
     const c10::cuda::CUDAGuard guard(q.device());
     if (!out.defined()) out = empty({q.size(0), heads, d}, ScalarType::BFloat16, q);
-    const cbs_status s = cbs_paged_attention(p, c, &seqs, q.data_ptr(), qs, (float)scale, out.data_ptr(), os, pointer(a[9]),
-                                             p->workspace_bytes, stream_of(q));
+    const auto stream = c10::cuda::getCurrentCUDAStream(q.get_device());
+    void *workspace = nullptr;
+    if (a[9] != Py_None) {
+        const Tensor &w = tensor(a[9], "workspace", &q);
+        workspace = w.data_ptr();
+        // Used on another stream than its own: its memory is not given away before this call has ended.
+        if (stream.stream() != pointer(a[10])) c10::cuda::CUDACachingAllocator::recordStream(w.storage().data_ptr(), stream);
+    }
+    const cbs_status s = cbs_paged_attention(p, c, &seqs, q.data_ptr(), qs, (float)scale, out.data_ptr(), os, workspace,
+                                             p->workspace_bytes, stream.stream());
     if (s != CBS_OK) return status(s);
     return a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(out);
 }
@@ -259,7 +268,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define CBS_PY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 13), CBS_PY(cache_write, 7),
-                         CBS_PY(cache_read, 6), CBS_PY(attention, 10),       {nullptr, nullptr, 0, nullptr}};
+                         CBS_PY(cache_read, 6), CBS_PY(attention, 11),       {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", "The token operators' calls (see tokens.py).", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -179,8 +179,9 @@ class PagedCache:
 
 class PagedAttention:
     """Attention of new tokens over a paged cache: the plan for one kind of
-    call and the workspace it needs.  Calls that may run at the same time need
-    an instance each (`fork`)."""
+    call and the workspace it needs, ready for any stream once the constructor
+    has returned.  Calls that may run at the same time need an instance each
+    (`fork`); a captured call needs its instance for as long as its graph."""
 
     def __init__(self, cache: PagedCache, batch: int, max_new: int, max_len: int, heads: int, causal: bool = True,
                  window: int = 0, scale: float | None = None, force_kernel: int = -1, force_split: int = 0):
@@ -196,12 +197,16 @@ class PagedAttention:
 
     def _make_workspace(self):
         self.workspace_bytes = int(self.plan.workspace_bytes)
-        self.workspace = self._workspace_at = None
+        self.workspace, self._stream = None, 0
         if self.workspace_bytes:
-            self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.cache.k.device)
-            with torch.cuda.device(self.workspace.device):
-                B.cbs_workspace_init(self.workspace, self.workspace_bytes, current_stream())
-            self._workspace_at = self.workspace.data_ptr()
+            with torch.cuda.device(self.cache.k.device):
+                self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device="cuda")
+                self._stream = current_stream()
+                B.cbs_workspace_init(self.workspace, self.workspace_bytes, self._stream)
+                # Zeroed before anyone can use it on another stream.  (Within a capture
+                # the zeroing is part of the graph, and what follows it is ordered.)
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
 
     def fork(self) -> "PagedAttention":
         """The same plan and cache with a workspace of its own."""
@@ -215,4 +220,4 @@ class PagedAttention:
         """q: bfloat16 [tokens, heads, head_dim] (a slice of a fused product's
         rows does).  The cache already holds the new tokens."""
         return _done(_calls().attention(self._plan_at, *self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
-                                        self._workspace_at), "cbs_paged_attention")
+                                        self.workspace, self._stream), "cbs_paged_attention")

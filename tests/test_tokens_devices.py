@@ -87,5 +87,5 @@ def test_cache_reads(calls, cache, at):
 def test_attention(calls, cache, at):
     plan = B.cbs_attn_plan(B.cbs_attn_desc(1, 3, 64, 4, 2, 64, B.CBS_INT8, 1, 0, 152, -1, 0))
     rows = ((3, 4, 64), BF)
-    refused(lambda q, out, *s: calls.attention(ctypes.addressof(plan), *cache, q, *s, 0.1, out, None), [rows, rows, *SEQUENCES],
+    refused(lambda q, out, *s: calls.attention(ctypes.addressof(plan), *cache, q, *s, 0.1, out, None, 0), [rows, rows, *SEQUENCES],
             at, "device")

@@ -285,3 +285,34 @@ def test_errors_of_the_calls(cuda_lib):
         tokens.rmsnorm(x, torch.ones(8, device="cuda"), 1e-5, int8=torch.ones(2))
     k, _ = cache.read(i32([0]), i32([[0]]), 3)
     assert (k == 0).all() and status() == B.CBS_OK
+
+
+def test_a_workspace_is_ready_for_any_stream(cuda_lib):
+    """Made while its stream is busy, used at once on another one, and dropped
+    while that one is: the counters are zero, and the memory is not given away
+    before the call has ended."""
+    paged = refs.make_paged([1000], 2, 64, 16, False, 41)
+    dev = on_gpu(paged)
+    cache = tokens.PagedCache(dev["k"], dev["v"])
+    q = torch.randn((1, 4, 64), generator=gen(9)).to(torch.bfloat16)
+    args = q.cuda(), i32([0, 1]), i32([1000]), dev["table"]
+    ref, mag = refs.attention(q, paged, [0, 1], [1000], 16, True, 0, 64 ** -0.5)
+    make = lambda: tokens.PagedAttention(cache, 1, 1, 1000, 4, force_kernel=B.CBS_ATTN_ROWS, force_split=7)
+    size = make().workspace_bytes
+    side, outs = torch.cuda.Stream(), []
+    for _ in range(3):
+        junk = torch.full((size,), 255, dtype=torch.uint8, device="cuda")   # what the allocator hands out next
+        del junk
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)   # ten milliseconds or so
+        attn = make()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            outs.append(attn(*args))
+        del attn
+        again = torch.full((size,), 255, dtype=torch.uint8, device="cuda")   # on the first stream, at once
+        del again
+    torch.cuda.synchronize()
+    for out in outs:
+        assert ((out.double().cpu() - ref).abs() <= refs.attention_bound(ref, mag)).all()
+    assert status() == B.CBS_OK
