@@ -198,9 +198,9 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 ++done;
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
-            if (lost())   // the copies in flight land before the CTA leaves
-                for (int x = max(0, done - C::kStages); x < done; ++x)
-                    ptx::mbar_wait_bounded(full(x % C::kStages), (x / C::kStages) & 1, kWaitNs);
+            // The copies in flight land before the CTA leaves, whoever gives up, and when.
+            for (int x = max(0, done - C::kStages); x < done; ++x)
+                ptx::mbar_wait_bounded(full(x % C::kStages), (x / C::kStages) & 1, kWaitNs);
         }
     } else if (warp == 10) {
         // ------------------------------------------------------- scales
