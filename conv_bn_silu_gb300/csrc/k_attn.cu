@@ -492,7 +492,9 @@ cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, row_tile == 8 ? attn_rows_kernel<D, I8, 1> : attn_rows_kernel<D, I8, 2>, L);
+    if constexpr (I8)
+        if (row_tile == 16) return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 2>, L);
+    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 1>, L);
 }
 
 }  // namespace

@@ -157,7 +157,9 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     const int rows_most = d->cache_prec == CBS_INT8 ? kAttnRowsMostInt8 : kAttnRowsMost;
     p.kernel = d->force_kernel >= 0 ? d->force_kernel : rows > rows_most ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
     const bool chunk = p.kernel == CBS_ATTN_CHUNK;
-    p.row_tile = chunk ? kAttnChunkRows : rows <= 8 ? 8 : 16;
+    // (Tiles of 16 rows in 8 bits alone: a bf16 cache's call of more than eight takes
+    // the chunk kernel, unless told otherwise.)
+    p.row_tile = chunk ? kAttnChunkRows : rows <= 8 || d->cache_prec == CBS_BF16 ? 8 : 16;
     const long long tiles = (rows + p.row_tile - 1) / p.row_tile;
     if (tiles * d->kv_heads > kGridMax || d->batch > kGridMax)
         return fail(CBS_ERR_UNSUPPORTED, "%lld row tiles of %d heads, %d sequences: at most %d", tiles, d->kv_heads,

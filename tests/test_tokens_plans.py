@@ -19,3 +19,15 @@ def test_a_window_that_hides_nothing_changes_no_plan(cuda_lib, new, window):
         wide, none = plan(max_new=new, window=window, cache_prec=prec), plan(max_new=new, cache_prec=prec)
         assert (wide.kernel, wide.split, wide.workspace_bytes) == (none.kernel, none.split, none.workspace_bytes)
         assert new > 64 or none.split > 1
+
+
+@pytest.mark.parametrize("kernel", [-1, B.CBS_ATTN_ROWS, B.CBS_ATTN_CLUSTER])
+@pytest.mark.parametrize("new", [1, 2, 3, 8, 9, 40])
+def test_row_tiles_hold_the_rows(cuda_lib, new, kernel):
+    """Tiles of 8 rows, 16 over an 8-bit cache where there are more than 8."""
+    for prec in (B.CBS_BF16, B.CBS_INT8):
+        p = plan(max_new=new, cache_prec=prec, force_kernel=kernel)
+        rows = 4 * new
+        if p.kernel != B.CBS_ATTN_CHUNK:
+            assert p.row_tile == (16 if rows > 8 and prec == B.CBS_INT8 else 8)
+        assert p.row_tiles == -(-rows // p.row_tile)
