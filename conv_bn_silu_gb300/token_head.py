@@ -124,9 +124,10 @@ class TokenHead:
         if self.graph is None:
             self.start(cells)
             self._advance()   # (everything a launch needs is set up before a capture)
-            self.graph = torch.cuda.CUDAGraph()
-            with torch.cuda.graph(self.graph):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
                 self._advance()
+            self.graph = graph
             self.step_rows = self.answer_rows   # the buffers that each launch writes
         out = torch.empty((self.batch, tokens), dtype=torch.int64, device=self.token.device)
         self.token.copy_(self.start(cells).argmax(1))

@@ -88,3 +88,23 @@ def test_a_head_over_the_chain(cuda_lib):
         head.answer(chain.outs[-1], 200)
     with pytest.raises(ValueError):
         head.start(chain.outs[-1][:1])
+
+
+def test_a_capture_that_fails_leaves_no_graph(cuda_lib):
+    from conv_bn_silu_gb300.token_head import TokenHead
+    head = TokenHead(2, cells=20, max_len=32, layers=1)
+    cells = torch.randn((2, 20, 256), dtype=torch.bfloat16, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    step, calls = head.step, []
+
+    def failing(token):
+        calls.append(torch.cuda.is_current_stream_capturing())
+        if calls[-1]:
+            raise KeyboardInterrupt
+        return step(token)
+    head.step = failing
+    with pytest.raises(KeyboardInterrupt):
+        head.answer(cells, 4)
+    assert calls == [False, True] and head.graph is None
+    head.step = step
+    answer = head.answer(cells, 4)
+    assert torch.equal(answer, TokenHead(2, cells=20, max_len=32, layers=1).answer(cells, 4))
