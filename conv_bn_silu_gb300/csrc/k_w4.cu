@@ -53,8 +53,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 // and 33.
 constexpr long long kFewMost = 48ll << 20;
 
-__device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
-
 // GROUP: weights a scale covers.  kN: input rows of a CTA.
 template <int GROUP, int kN>
 struct W4Tile {

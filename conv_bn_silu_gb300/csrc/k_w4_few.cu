@@ -31,8 +31,6 @@ constexpr int kStageK = 128;    // weights along k in one stage of the ring
 constexpr int kStages = 4;
 constexpr int kSlotBytes = 2 * kThreads * 16;   // a stage: two rows a lane, 16 bytes each
 
-__device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
-
 // GROUP: weights a scale covers.  FULL: k is a multiple of the stage's 128, so no
 // stage ends early.  wk: warps side by side along k.
 template <int GROUP, bool XI8, bool FULL>

@@ -21,6 +21,8 @@ struct CacheArgs {
 };
 
 #ifdef __CUDACC__
+__device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
+
 // Length of sequence b: what the array says, within what its table can hold.
 __device__ __forceinline__ int seq_len(const CacheArgs &a, int b) {
     const int n = a.seq_lens[b];
