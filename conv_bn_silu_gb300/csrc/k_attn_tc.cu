@@ -127,9 +127,9 @@ __device__ __forceinline__ float2 split(F2 a) {
 
 // A thread's pass over its kCols of a row's scores: t = s * scale - ref (ks: a scale a key,
 // for 8-bit keys), p = 2^t (times vs, for 8-bit values) as bf16 pairs, the
-// largest t and the sum of p as rounded (8 bits: of 2^t, since p has the value's
-// scale in it).  MASK: columns outside [first, end) are not
-// seen.  Rounding p to bf16 moves each term by at most 2^-8 of itself, either
+// largest t and, in 8 bits, the sum of 2^t (p has the value's scale in it; in
+// bf16 the sum is of p as rounded, below).  MASK: columns outside [first, end) are
+// not seen.  Rounding p to bf16 moves each term by at most 2^-8 of itself, either
 // way, as the output's own rounding does.
 template <bool I8, bool MASK>
 __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref, const float *ks, const float *vs, int first,
@@ -137,7 +137,6 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
     constexpr int kPart = I8 ? 8 : 16;   // columns at a time: of more, registers spilled
     const F2 scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
     F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-    float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int q = 0; q < kCols / kPart; ++q) {
@@ -172,19 +171,26 @@ __device__ __forceinline__ void tile_pass(uint32_t taddr, float scale, float ref
                     if (t.x == -INFINITY) y.x = 0.0f;
                     if (t.y == -INFINITY) y.y = 0.0f;
                 }
-                const uint32_t both = frag::pack_bf16(y.x, y.y);
-                if constexpr (!I8) sums[x].x = frag::add_bf16(sums[x].x, both), sums[x].y = frag::add_bf16(sums[x].y, both >> 16);
-                p[kPart / 2 * q + (e >> 1) + x] = both;
+                p[kPart / 2 * q + (e >> 1) + x] = frag::pack_bf16(y.x, y.y);
             }
         }
     }
     top = fmaxf(tops[0], tops[1]);
-    if constexpr (I8) {
-        const float2 a = split(add2(acc[0], acc[1]));
-        sum = a.x + a.y;
-    } else {
-        sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+    const float2 a = split(add2(acc[0], acc[1]));
+    sum = a.x + a.y;   // (bf16: none)
+}
+
+// The sum of a thread's probabilities as they were rounded, taken while their
+// store to tensor memory is under way (16 maps of 20x20 23.3 us, in the pass
+// itself 24.0; the chunk of 2048 797 and 809).
+__device__ __forceinline__ float sum_rounded(const uint32_t (&p)[kCols / 2]) {
+    float sums[4] = {};
+#pragma unroll
+    for (int e = 0; e < kCols / 2; ++e) {
+        sums[2 * (e & 1)] = frag::add_bf16(sums[2 * (e & 1)], p[e]);
+        sums[2 * (e & 1) + 1] = frag::add_bf16(sums[2 * (e & 1) + 1], p[e] >> 16);
     }
+    return (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // The largest of a thread's scores, in base 2.
@@ -688,6 +694,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
             if (is_far(m)) words[2] = 1;
             tmem_st32(t_mine + part * (kCols / 2), p);
+            if constexpr (!I8) l += sum_rounded(p);
             tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
