@@ -171,13 +171,6 @@ struct Squares {
     }
 };
 
-// The larger of two magnitudes, or NaN if one is (fmaxf would pass it over).
-__device__ __forceinline__ float most_or_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }

@@ -471,7 +471,8 @@ cbs_status launch_w4_rows(const W4Launch &L, cudaStream_t s) {
 
 // One-time weight transform: symmetric codes q in 1..15 (zero point 8) with
 // s = bf16(max|w| / 7) over each group, q = 8 + clamp(rne(w / s), -7, 7).  A
-// warp per group of one output.
+// warp per group of one output.  A NaN in a group is its scale (and an infinity
+// its own), so what the group adds to is NaN.
 __global__ void quantize_w4_kernel(const float *__restrict__ w, int n, int k, int group, uint32_t *__restrict__ packed,
                                    __nv_bfloat16 *__restrict__ scales) {
     ptx::griddep_wait();
@@ -483,9 +484,9 @@ __global__ void quantize_w4_kernel(const float *__restrict__ w, int n, int k, in
         const int row = (int)(t / groups), gi = (int)(t % groups);
         const float *src = w + (size_t)row * k + (size_t)gi * group;
         float top = 0.0f;
-        for (int i = lane; i < group; i += 32) top = fmaxf(top, fabsf(src[i]));
+        for (int i = lane; i < group; i += 32) top = most_or_nan(top, fabsf(src[i]));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        for (int o = 16; o; o >>= 1) top = most_or_nan(top, __shfl_xor_sync(~0u, top, o));
         const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(top, 7.0f));
         const float s = __bfloat162float(sb);
         if (lane == 0) scales[(size_t)gi * n + row] = sb;

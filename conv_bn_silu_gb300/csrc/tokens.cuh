@@ -23,6 +23,13 @@ struct CacheArgs {
 #ifdef __CUDACC__
 __device__ __forceinline__ float silu(float z) { return __fdiv_rn(z, 1.0f + expf(-z)); }
 
+// The larger of two magnitudes, or NaN if one is (fmaxf would pass it over).
+__device__ __forceinline__ float most_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Length of sequence b: what the array says, within what its table can hold.
 __device__ __forceinline__ int seq_len(const CacheArgs &a, int b) {
     const int n = a.seq_lens[b];

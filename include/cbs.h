@@ -595,7 +595,9 @@ CBS_API cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale
 
 /* cbs_quantize_w4 -- one-time weight transform for cbs_linear_w4: w float
  * [n][k] -> packed codes and scales, symmetric (zero point 8):
- * s = bf16(max|w| / 7) over a group, q = 8 + clamp(rne(w / s), -7, 7). */
+ * s = bf16(max|w| / 7) over a group, q = 8 + clamp(rne(w / s), -7, 7).  A group
+ * that holds a NaN or an infinity gets that as its scale: outputs that it is part
+ * of are NaN. */
 CBS_API cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed, void *scales, void *stream);
 
 /* Zero a workspace before its first use (cudaMemsetAsync on `stream`). */

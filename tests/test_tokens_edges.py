@@ -90,6 +90,22 @@ def test_rmsnorm_rows_whose_squares_pass_the_float_range(cuda_lib, cols, dtype):
     assert ((q.scale.double().cpu() - want).abs() <= want * 40 * U).all()
 
 
+@pytest.mark.parametrize("kind", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantised_weights_show_what_is_not_finite(cuda_lib, group, kind):
+    """An output that such a weight is part of is NaN; the others are as without it."""
+    w = torch.randn((40, 4 * group), generator=gen(10))
+    x = torch.randn((12, 4 * group), generator=gen(11)).to(torch.bfloat16).cuda()
+    clean = tokens.LinearW4.quantize(w.cuda(), group)(x, dtype=torch.float32)
+    w[7, group + 3] = kind
+    layer = tokens.LinearW4.quantize(w.cuda(), group)
+    codes, scale = torch.randint(-127, 128, x.shape, generator=gen(12), dtype=torch.int8).cuda(), torch.ones(12, device="cuda")
+    for out in (layer(x, dtype=torch.float32), layer(x[:3], dtype=torch.float32), layer(codes, scale), layer(codes[:3], scale[:3])):
+        assert out[:, 7].isnan().all() and int(out.isnan().sum()) == out.shape[0]
+    keep = torch.arange(40) != 7
+    assert torch.equal(layer(x, dtype=torch.float32)[:, keep], clean[:, keep])
+
+
 # ------------------------------------------------- tokens of no sequence
 KERNELS = [B.CBS_ATTN_ROWS, B.CBS_ATTN_CHUNK, B.CBS_ATTN_CLUSTER]
 
