@@ -80,6 +80,23 @@ cbs_status token_stride(long long stride, long long least, const char *what) {
     return CBS_OK;
 }
 
+// Outputs must not lie on what other CTAs still read.
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+// Rows of `width` 16-bit elements, `total` of them: side by side in wider rows of
+// one pitch is not on one another.  (Of two pitches, where the ranges meet, taken to be.)
+bool rows_overlap(const void *a, long long a_stride, const void *b, long long b_stride, long long width, int total) {
+    const auto bytes = [&](long long stride) { return (size_t)((total - 1) * stride + width) * 2; };
+    if (!overlap(a, bytes(a_stride), b, bytes(b_stride))) return false;
+    if (a_stride != b_stride) return true;
+    const long long at = (static_cast<const char *>(b) - static_cast<const char *>(a)) / 2 % a_stride;
+    const long long r = at < 0 ? at + a_stride : at;
+    return r < width || r + width > a_stride;
+}
+
 constexpr int kGridMax = 65535;
 
 // Most rows of a key head for the few-row kernel.  32 heads, 8 key heads of 128,
@@ -256,6 +273,7 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
                         p->workspace_bytes);
         CBS_TRY(need(workspace, "workspace"));
     }
+    if (rows_overlap(q, q_stride, out, out_stride, width, s->total)) return fail(CBS_ERR_INVALID_ARG, "out lies on q");
     CBS_TRY(status_word(&L.c));
     L.q = q; L.out = out; L.q_stride = q_stride; L.out_stride = out_stride;
     L.scale_log2 = scale * 1.44269504088896340736f;
@@ -290,6 +308,15 @@ cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight,
     CBS_TRY(may(h_out, "h_out"));
     CBS_TRY(need(y, "y"));
     if (out_prec == CBS_INT8) CBS_TRY(need(scale, "scale"));
+    const size_t in_bytes = (size_t)rows * cols * (in_prec == CBS_BF16 ? 2 : 4);
+    const size_t y_bytes = out_prec == CBS_INT8 ? (size_t)rows * cols : in_bytes;
+    for (const void *in : {x, residual}) {
+        if (h_out != in && overlap(h_out, in_bytes, in, in_bytes)) return fail(CBS_ERR_INVALID_ARG, "h_out lies across an input");
+        if ((y != in || out_prec == CBS_INT8) && overlap(y, y_bytes, in, in_bytes))
+            return fail(CBS_ERR_INVALID_ARG, "y lies on an input");
+        if (out_prec == CBS_INT8 && overlap(scale, (size_t)rows * 4, in, in_bytes)) return fail(CBS_ERR_INVALID_ARG, "scale lies on an input");
+    }
+    if (overlap(y, y_bytes, h_out, in_bytes)) return fail(CBS_ERR_INVALID_ARG, "y lies on h_out");
     NormLaunch L;
     L.x = x; L.residual = residual; L.weight = weight; L.h = h_out; L.y = y; L.scale = scale;
     L.eps = eps; L.rows = rows; L.cols = cols; L.in_bf16 = in_prec == CBS_BF16; L.out_int8 = out_prec == CBS_INT8;
@@ -304,6 +331,9 @@ cbs_status cbs_dequantize_rows(const int8_t *q, const float *scale, void *out, i
     CBS_TRY(need(q, "q"));
     CBS_TRY(need(scale, "scale"));
     CBS_TRY(need(out, "out"));
+    const size_t count = (size_t)rows * cols, out_bytes = count * (out_prec == CBS_BF16 ? 2 : 4);
+    if (overlap(out, out_bytes, q, count) || overlap(out, out_bytes, scale, (size_t)rows * 4))
+        return fail(CBS_ERR_INVALID_ARG, "out lies on an input");
     return cuda_check(launch_dequantize_rows(q, scale, out, rows, cols, out_prec == CBS_BF16, (cudaStream_t)stream),
                       "dequantise launch");
 }
@@ -334,6 +364,9 @@ cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale, const 
     CBS_TRY(may(zeros, "zeros"));
     CBS_TRY(may(bias, "bias"));
     CBS_TRY(need(y, "y"));
+    const size_t y_bytes = (size_t)rows * n * (out_prec == CBS_BF16 ? 2 : 4);
+    if (overlap(y, y_bytes, x, (size_t)rows * k * (x_prec == CBS_BF16 ? 2 : 1)) || overlap(y, y_bytes, x_scale, (size_t)rows * 4))
+        return fail(CBS_ERR_INVALID_ARG, "y lies on an input");
     W4Launch L;
     L.x = x; L.x_scale = x_scale; L.w = static_cast<const uint8_t *>(w); L.scales = scales;
     L.zeros = static_cast<const uint8_t *>(zeros); L.bias = bias; L.y = y;

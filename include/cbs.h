@@ -448,6 +448,8 @@ CBS_API int cbs_launch_options(void);
  * starts) are checked on the device: a value out of range makes the kernel
  * skip what it would have named and cbs_read_device_status report
  * CBS_ERR_INVALID_ARG.
+ * An output must not lie on a call's inputs unless its comment allows it (where
+ * a call can tell, it is refused): other parts of the call may still read them.
  * ------------------------------------------------------------------------ */
 
 /* A paged cache.  A page holds page_size consecutive positions of one
@@ -560,7 +562,8 @@ CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache
  *   h = x + residual,   y = h * weight / sqrt(mean(h^2) + eps)   per row
  * x, residual (NULL: h = x), h_out: [rows][cols] of in_prec (CBS_FP32 or
  * CBS_BF16; h rounded once, the norm computed from the sum in 32 bits);
- * h_out may be NULL, x or residual.  weight: float[cols].  out_prec = in_prec:
+ * h_out may be NULL, x or residual; y of in_prec may be x or residual too, if
+ * h_out is not.  weight: float[cols].  out_prec = in_prec:
  * y in that type, scale unused.  out_prec CBS_INT8: with u = h * weight,
  *   s = max|u| / 127,  y = clamp(rne(u / s), -127, 127),  scale[row] = s / sqrt(..)
  * so the codes do not depend on the order in which the squares are summed.  A

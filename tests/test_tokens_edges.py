@@ -332,3 +332,27 @@ def test_a_workspace_is_ready_for_any_stream(cuda_lib):
     for out in outs:
         assert ((out.double().cpu() - ref).abs() <= refs.attention_bound(ref, mag)).all()
     assert status() == B.CBS_OK
+
+
+def test_outputs_beside_their_inputs(cuda_lib):
+    """Slices of one tensor that share its rows but no element, and what may be
+    written in place."""
+    paged = refs.make_paged([90, 33], 2, 64, 16, False, 43)
+    dev = on_gpu(paged)
+    cache = tokens.PagedCache(dev["k"], dev["v"])
+    rows = torch.randn((12, 10, 64), generator=gen(13)).to(torch.bfloat16)
+    d = rows.cuda()
+    for new in ([10, 2], [1, 1]):
+        n = sum(new)
+        starts = [0, new[0], n]
+        attn = tokens.PagedAttention(cache, 2, new[0], 90, 4)
+        out = attn(d[:n, :4], i32(starts), i32([90, 33]), dev["table"], out=d[:n, 4:8])
+        ref, mag = refs.attention(rows[:n, :4], paged, starts, [90, 33], 16, True, 0, 64 ** -0.5)
+        assert ((out.double().cpu() - ref).abs() <= refs.attention_bound(ref, mag)).all()
+        with pytest.raises(B.CbsError, match="lies on q"):
+            attn(d[:n, :4], i32(starts), i32([90, 33]), dev["table"], out=d[:n, 2:6])
+    layer = tokens.LinearW4.quantize(torch.randn((64, 64), device="cuda"), 64)
+    x = torch.randn((5, 64), generator=gen(14)).to(torch.bfloat16).cuda()
+    with pytest.raises(B.CbsError, match="lies on an input"):
+        layer(x, out=x)
+    assert status() == B.CBS_OK
