@@ -15,11 +15,12 @@
 // consecutive elements, and 8-bit codes are widened exactly in registers, keys to
 // f16 and values to bf16 (their scales multiply the scores and the probabilities).
 //
-// One token of 32 heads, 8 key heads of 128: 1000 keys 5.4 us (latency: 8 ranges in
-// clusters; 6.7 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
-// and 209 us in 8 bits, 4.0 TB/s (225 with keys widened to bf16), where the
-// instructions that widen the codes bound it: a fifth of all, and three CTAs an SM do
-// not fill the slots between them.
+// One token of 32 heads, 8 key heads of 128: 1000 keys 5.6 us (latency: 8 ranges in
+// clusters; 6.8 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
+// and 208 us in 8 bits, 4.0 TB/s (225 with keys widened to bf16).  In 8 bits neither
+// memory (half its rate) nor the issue slots (46%) are full: warps wait for their
+// loads, twelve of them an SM with a block of 16 keys each, half the bytes in
+// flight of bf16.
 //
 // Up to eight ranges of keys are the CTAs of a cluster, which join them from each
 // other's shared memory; more are joined through the workspace by the CTA that
@@ -91,8 +92,8 @@ struct KvFrag {
 };
 
 // CTAs an SM: what fits without spilled registers (head dimension 64 at five in
-// place of three: 64 x 8000 keys 186 -> 163 us in 8 bits, 208 -> 180 in bf16;
-// 128 at four in place of three, 8 x 8000 keys in 8 bits: 50 -> 53).
+// place of three: 64 x 8000 keys 202 -> 150 us in 8 bits, 185 -> 163 in bf16;
+// 128 at four in place of three, 8 x 8000 keys: 44 -> 53 in 8 bits, 51 -> 69).
 template <int D, bool I8, int NR>
 __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR == 2 ? 4 : 5)) attn_rows_kernel(const AttnLaunch L) {
     constexpr int kRows = 8 * NR;
@@ -199,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 
     // The block after the next one to the L2 cache, a lane a key's row of K or V: a
     // block of a warp's own is all that its registers hold ahead (64 sequences of up
-    // to 8192 keys: 281 -> 250 us in bf16, 237 -> 226 in 8 bits).
+    // to 8192 keys: 281 -> 250 us in bf16, 237 -> 226 in 8 bits, when keys were still
+    // widened to bf16).
     const char *const ahead = static_cast<const char *>(lane < kBlock ? c.k : c.v) + (size_t)(lane & (kBlock - 1)) * (D * (I8 ? 1 : 2));
     const auto prefetch = [&](size_t row0, unsigned on) {
         if (!((on >> (lane & (kBlock - 1))) & 1)) return;
@@ -322,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
             }
             // Rounded to bf16 for the second product: half a unit in 2^-8 of
             // each term, of either sign, below the output's own rounding.  The sum
-            // that divides is of the rounded ones; in 8 bits they carry the values'
-            // scales, and it is of the probabilities before them.
+            // that divides is of the rounded ones, so that the weights add up to one;
+            // in 8 bits they carry the values' scales, so it is of the probabilities
+            // before them, and the weights add up to one within 2^-8.
             const uint32_t w0 = frag::pack_bf16(p[0], p[1]), w1 = frag::pack_bf16(p[2], p[3]);
             if (!I8) {
                 l[n][0] = frag::add_bf16(frag::add_bf16(l[n][0], w0), w1);

@@ -22,11 +22,11 @@
 // Ranges of keys are the CTAs of a cluster; each joins its part of the rows from
 // the others' shared memory, in the ranges' order.
 //
-// The softmax's instructions and exponentials bound it: a tile of 128 keys takes
-// 1.6 us (head dimension 128; 1.4 at 64), the products alone 1.1 us, a CTA's start
-// and end 7 us.  2048 tokens of 32 heads over 32768 keys of 8 key heads: 790 us,
-// 1.35 PFLOP/s.  8 bits: 2.7 us a tile alone and up to 3.4 with every SM busy
-// (2.5 at 64), where widening the codes takes as many issue slots again.
+// The softmax bounds it: a tile of 128 keys takes 1.6 us (head dimension 128; 1.4
+// at 64), the products alone 1.1 us, a CTA's start and end 7 to 10 us.  2048 tokens
+// of 32 heads over 32768 keys of 8 key heads: 797 us, 1.34 PFLOP/s.  8 bits: 2.7 us
+// a tile alone and 3.5 with every SM busy (2.2 and 2.7 at 64), where widening the
+// codes takes as many issue slots again.
 #include <cuda.h>
 
 #include "attn_common.cuh"

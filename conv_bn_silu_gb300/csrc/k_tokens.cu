@@ -187,7 +187,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // read once and h, y written once.  A thread's unit is eight elements at a
 // multiple of eight of the whole array, so rows of any width take 16-byte
 // accesses; only a row's first and last unit, shared with its neighbours, go
-// element by element.  8192 x 4096 bf16 with a residual to 8 bits: 42.6 us, 5.5
+// element by element.  8192 x 4096 bf16 with a residual to 8 bits: 44.1 us, 5.3
 // TB/s of its 235 MB (a unit a thread; with two, 48 us: fewer rows in flight).
 constexpr int kNormMaxThreads = 1024;
 
@@ -373,7 +373,7 @@ cudaError_t launch_norm_typed(const NormLaunch &L, cudaStream_t s) {
 // out[r][c] = q[r][c] * scale[r]: the seam behind an operator that scales each
 // row by itself.  Sixteen codes a thread, at multiples of sixteen of the whole
 // array; a unit that spans rows looks each element's row up.  8192 x 4096 to
-// bf16: 14.0 us, 7.2 TB/s (17.8 us with stores of 16 bytes).
+// bf16: 13.7 us, 7.3 TB/s (17.8 us with stores of 16 bytes).
 template <typename T>
 __global__ void dequantize_rows_kernel(const int8_t *__restrict__ q, const float *__restrict__ scale,
                                        T *__restrict__ out, size_t count, int cols) {
@@ -449,7 +449,7 @@ __device__ __forceinline__ Place place_of(const CacheArgs &a, int i) {
 // New tokens into their pages.  A row is a token's key or value of one head;
 // D / 8 lanes take it, eight elements each, and its largest magnitude comes from
 // a butterfly over them.  Instructions bound it, not memory (8192 tokens, 8 heads
-// of 128 to 8 bits: 18.8 us, 2.7 TB/s).  A warp takes kRowsWarp rows of one token (rows 2 head +
+// of 128 to 8 bits: 17.1 us, 3.0 TB/s).  A warp takes kRowsWarp rows of one token (rows 2 head +
 // side): the token's place is looked up once for all of them, behind their
 // loads, which need only the token's number.
 constexpr int kRowsWarp = 4;
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const CacheArgs a, con
 // CTA takes consecutive positions of one sequence and some of its heads
 // (blockIdx.z and every gridDim.z after it); a thread 16 bytes of the cache a
 // row, of K and V, so the pages' rows are read as they lie and every index but
-// the page is a shift.  4 x 16384 positions, 8 heads of 128, 8 bits to bf16: 64.6
+// the page is a shift.  4 x 16384 positions, 8 heads of 128, 8 bits to bf16: 65.1
 // us, 6.3 TB/s of its 407 MB (80 us with stores of 16 bytes).
 constexpr int kReadThreads = 256;
 template <int D, bool I8>

@@ -22,10 +22,12 @@
 //
 // Two warpgroups take a half of every stage of k each: while the MMA of a
 // group's piece runs, it dequantises the next.  A handshake costs 150 to 250
-// cycles and 64 weights about 300, so pieces are as large as registers allow.
-// 16 rows of 16384 x 8192, groups of 64: 30 us, 2.4 TB/s of its 73 MB; the issue
+// cycles and 64 weights about 300, so pieces are of 128.
+// 16 rows of 16384 x 8192, groups of 64: 29 us, 2.5 TB/s of its 73 MB; the issue
 // slots that dequantise are half full, and the hand-offs between the threads and
-// the MMA take most of the rest.
+// the MMA take most of the rest.  Made for few rows: from 17 on a thread's running
+// totals are 32 or 64, and where two CTAs an SM leave it 80 registers (by tensor
+// memory they could), some of them are spilled.
 // Shares of k are CTAs of a cluster, which add their sums in order through
 // distributed shared memory.
 #include <type_traits>
@@ -427,9 +429,15 @@ cbs_status launch_w4_one(const W4Launch &L, cudaStream_t s) {
 
     // Shares of k, by what was measured: an SM's CTAs take 0.72 us a stage between
     // them (two run at a time), a CTA's start and end 1.6 us (two at a time), a
-    // cluster of eight half a microsecond more.  16384 x 8192: 31, 28, 34, 41 us for
-    // 1, 2, 4, 8 shares; 6144 x 4096: 17.5, 10.9, 9.5, 11.4; 1001 x 2048: 13.9, 9.4,
-    // 6.8, 6.1.
+    // cluster of eight half a microsecond more; of shares that cost the same, the
+    // fewest.  Groups of 64, 1, 2, 4, 8 shares in us, the one taken in brackets.  16
+    // rows: 16384 x 8192 [28.6], 25.9, 29.5, 37.1; 6144 x 4096 15.7, [10.4], 9.6, 12.8;
+    // 4096 x 4096 15.7, 10.4, [7.2], 8.1; 1001 x 2048 12.0, 8.5, 6.0, [5.1].  32 rows:
+    // [36.5], 32.9, 36.9, 49; 20.2, [13.3], 12.3, 17.9; 20.1, 13.2, [8.7], 10.6; 13.9,
+    // 10.1, 6.9, [6.2].  64 rows: [37.7], 45.6, 54, 92; 21.0, [14.9], 19.2, 33; 21.1,
+    // 14.7, [10.1], 24; 16.0, 12.1, 7.9, [7.6].  So up to 32 rows two layers get a share
+    // 8% to 11% slower than their best, where two cost the same by the rule; with 64
+    // the fewest is right.
     const int tiles = (L.n + kOut - 1) / kOut, stages = (L.k + kStageK - 1) / kStageK;
     const int row_tiles = (L.rows + kN - 1) / kN, sms = current_device_sms();
     int split = 1;

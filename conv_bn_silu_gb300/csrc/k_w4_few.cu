@@ -7,7 +7,7 @@
 // through a ring of its own in shared memory (cp.async, three stages ahead, no
 // barrier), X and the scales through registers.  There is no tensor memory to
 // allocate, no cluster and no hand-off between warps, so a call of 6144 x 4096
-// ends in 8 us and one of 1001 x 2048 in 3.3, where k_w4.cu takes 10.7 and 6.9;
+// ends in 8.7 us and one of 1001 x 2048 in 3.4, where k_w4.cu takes 10.4 and 5.1;
 // per weight it spends half as many instructions again (16384 x 8192: 42 us
 // against 33).
 //

@@ -100,11 +100,12 @@ bool rows_overlap(const void *a, long long a_stride, const void *b, long long b_
 constexpr int kGridMax = 65535;
 
 // Most rows of a key head for the few-row kernel.  32 heads, 8 key heads of 128,
-// few-row / chunk kernel in us, for 8, 16, 32, 64 rows: bf16, one sequence of 4000
-// keys 14/12, 21/13, 21/13, 24/14; 16 of 4000 58/53, 79/53, 124/54, 190/55; 64 of
-// 1000 66/75, 66/75, 113/76, 186/84.  8 bits (the chunk kernel widens every code
-// first): 15/20, 21/20, 22/20, 26/21; 53/134, 73/134, 118/134, 185/134; 57/137,
-// 58/137, 106/137, 178/139.
+// few-row (the better of its two ways to join ranges) / chunk kernel in us, for 8,
+// 16, 32, 64 rows: bf16 (tiles of 8 rows), one sequence of 4000 keys 11/13, 13/13,
+// 18/14, 24/14; 16 of 4000 53/56, 82/56, 134/56, 238/57; 64 of 1000 59/79, 78/80,
+// 127/82, 226/85.  8 bits (tiles of 16 from 16 rows on; the chunk kernel widens every
+// code first): 11/19, 11/19, 14/19, 17/20; 46/119, 54/120, 100/120, 165/119; 50/126,
+// 51/127, 94/126, 160/127.
 constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
 size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
@@ -194,8 +195,8 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
         // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
         // A key tile is one unit (1.6 us, head dimension 128), a range's start and
         // end 4.5, a cluster's join 2 and a fifth for each CTA.  64 tokens of 32
-        // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 57, 36,
-        // 28, 24, 22, 22, 21, 20 us; four sequences 61, 40, 33, 29, 52, 51, 68, 65.
+        // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 60, 39,
+        // 30, 26, 23, 22, 21, 22 us; four sequences 61, 40, 31, 28, 47, 45, 62, 64.
         // Less than a tenth is not worth a cluster: sequences are of unequal lengths.
         static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
         const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
@@ -210,19 +211,21 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     } else {
         // At least a CTA for each SM if that leaves a range 64 keys, and up to
         // twelve if it leaves 640.  Tokens of 32 heads, 8 key heads, 1, 2, 4, ... 32
-        // ranges: one sequence of 1000 keys 15, 11, 7.8, 6.6, 6.7 us; one of 8192 108,
-        // 58, 31, 18, 13, 14; 8 of 8192 192, 103, 65, 69, 61, 63; 32 of 8192 (8 bits)
-        // 234, 210, 169, 159, 169, 195; 32 of 1024 34, 39, 36, 37, 51.
+        // ranges: one sequence of 1000 keys 16, 12, 8.1, 6.8, 6.8, 9.8 us; one of 8192
+        // 112, 59, 32, 19, 13, 14; 8 of 8192 140, 76, 55, 63, 57, 61 (12 ranges 52); 32
+        // of 1024 29, 37, 34, 37, 51, 88.  8 bits: one of 1000 15, 11, 7.8, 6.8, 7.1, 10;
+        // one of 8192 99, 54, 29, 18, 12, 15; 32 of 8192 194, 178, 146, 137, 150, 180.
         const long long few = std::min((sms + base - 1) / base, ((long long)keys + 63) / 64);
         const long long many = std::min((sms * 12ll + base - 1) / base, (long long)keys / 640);
         p.split = (int)std::max(1ll, std::max(few, many));
         // Up to eight ranges join in a cluster where it does not keep CTAs waiting (three
         // an SM; more are made eight if that leaves a range 512 keys at most, and five to
         // seven four).  Through the workspace / in a cluster: one token over 1000 keys, 8
-        // ranges 6.5/5.4 us (16 ranges 6.7 through the workspace), over 4000 11.9/10.7 (19
-        // ranges 11.1), two tokens over 1000 7.9/5.6; four sequences of 1000, 4 ranges
-        // 8.1/7.1, 5 ranges 9.2/8.5; 16 of 1000, 2 ranges 19.8/18.2; 8 of 8000, 8 ranges
-        // 62/60; 32 of 8000, 8 ranges 168/187.
+        // ranges 6.8/5.7 us (16 ranges 6.8 through the workspace), over 4000 12.0/10.9 (19
+        // ranges 10.1), two tokens over 1000 8.1/5.9; four sequences of 1000, 4 ranges
+        // 8.3/7.3, 5 ranges 9.2/8.5; 16 of 1000, 2 ranges 16.8/15.5; 8 of 8000, 8 ranges
+        // 62/60; 32 of 8000, 8 ranges 168/187.  8 bits: 6.9/5.7 (7.1), 11.4/10.2 (10.0),
+        // 8.3/5.9; 8.0/7.0, 9.2/8.6; 16.5/15.2; 52/53; 135/159.
         const int most = std::min(p.split, kAttnClusterMost), x = most > 4 && most < 8 ? 4 : most;
         const bool fits = p.split <= kAttnClusterMost || keys <= 512 * kAttnClusterMost;
         if (d->force_kernel == CBS_ATTN_CLUSTER || (d->force_kernel < 0 && fits && base * x <= 3ll * sms)) {

@@ -6,8 +6,12 @@ what the layers saw; `token_head` runs them together.
 PyTorch supplies device memory and streams; every value is computed in
 libcbs.so's kernels, on the current stream of the tensors' device (all of a call's
 are on one).  Tensors are contiguous unless an argument says that it may be a slice.  Types and shapes are checked by the calls
-of csrc/tokens_py.cpp (ValueError), the rest (alignment, limits) by the C calls
-behind them, which raise CbsError.
+of csrc/tokens_py.cpp (ValueError), the rest (alignment, limits, outputs on their
+inputs) by the C calls behind them, which raise CbsError.
+
+For inference only: a tensor that requires a gradient is taken as it is, and the
+result carries none.  The calls are not traced: a tensor without memory (a fake
+one) raises PyTorch's own error.
 """
 from __future__ import annotations
 
@@ -125,7 +129,8 @@ class LinearW4:
 
     def __call__(self, x: torch.Tensor, x_scale: torch.Tensor | None = None, dtype=torch.bfloat16,
                  out: torch.Tensor | None = None) -> torch.Tensor:
-        """x: bfloat16 [rows, k], or int8 codes with x_scale float [rows]."""
+        """x: bfloat16 [rows, k], or int8 codes with x_scale float [rows].  The
+        result is of `dtype`, or of out's type where out is given."""
         if dtype not in _FLOATS:
             _refuse("dtype: float32 or bfloat16")
         return _done(_calls().linear_w4(x, x_scale, out, dtype is _BF16, *self._args), "cbs_linear_w4")

@@ -517,7 +517,7 @@ typedef struct cbs_attn_desc {
 } cbs_attn_desc;
 
 typedef enum cbs_attn_kernel {
-    CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 or 16 (token, head) rows, keys straight to registers */
+    CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 (token, head) rows, or 16 over 8 bits, keys straight to registers */
     CBS_ATTN_CHUNK = 1, /* many: tiles of 256 rows on tcgen05, scores and output in tensor memory */
     CBS_ATTN_CLUSTER = 2 /* as CBS_ATTN_ROWS, with up to 8 ranges of keys joined in a cluster and no workspace */
 } cbs_attn_kernel;
