@@ -2,6 +2,7 @@
 tensors here are fakes that name a device and hold no memory, so none of this
 needs a GPU."""
 import ctypes
+from unittest import mock
 
 import pytest
 import torch
@@ -19,7 +20,8 @@ def calls(cuda_lib):
 
 
 def fake(shape, dtype, device=0):
-    with FakeTensorMode(allow_non_fake_inputs=True):
+    # (Where there is a GPU, making one would open the device it names, which need not exist.)
+    with mock.patch("torch.cuda.is_available", return_value=False), FakeTensorMode(allow_non_fake_inputs=True):
         return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
 
