@@ -37,7 +37,7 @@ EXPORTED = (
     "cbs_conv_bn_act_cat", "cbs_set_launch_options", "cbs_launch_options", "cbs_maxpool2d",
     "cbs_conv_bn_silu_i8_cat", "cbs_selftest_wait_timeout", "cbs_sppf_pool", "cbs_dequantize_i8",
     "cbs_quantize_i8", "cbs_cache_write", "cbs_cache_read", "cbs_attn_plan", "cbs_paged_attention", "cbs_rmsnorm",
-    "cbs_dequantize_rows", "cbs_linear_w4", "cbs_quantize_w4",
+    "cbs_dequantize_rows", "cbs_linear_w4", "cbs_quantize_w4", "cbs_cache_evict",
 )
 
 
@@ -116,6 +116,7 @@ def lib():
         LL, CP, SP = ctypes.c_longlong, ctypes.POINTER(cbs_cache), ctypes.POINTER(cbs_sequences)
         L.cbs_cache_write.argtypes = [CP, SP, P, LL, P, LL, I, P]
         L.cbs_cache_read.argtypes = [CP, SP, I, P, P, I, P]
+        L.cbs_cache_evict.argtypes = [CP, SP, P, P, I, I, I, P, P, P]
         L.cbs_attn_plan.argtypes = [ctypes.POINTER(cbs_attn_desc), ctypes.POINTER(cbs_attn_plan_t)]
         L.cbs_paged_attention.argtypes = [ctypes.POINTER(cbs_attn_plan_t), CP, SP, P, LL, F, P, LL, P, Z, P]
         L.cbs_rmsnorm.argtypes = [P, P, P, P, P, P, I, I, F, I, I, P]
@@ -277,6 +278,11 @@ def cbs_cache_write(cache, seqs, k, k_stride, v, v_stride, in_prec, stream):
 
 def cbs_cache_read(cache, seqs, max_len, k_out, v_out, out_prec, stream):
     _check(lib().cbs_cache_read(cache, seqs, max_len, _p(k_out), _p(v_out), out_prec, stream), "cbs_cache_read")
+
+
+def cbs_cache_evict(cache, seqs, mass, new_table, new_max_pages, keep, recent, kept, new_lens, stream):
+    _check(lib().cbs_cache_evict(cache, seqs, _p(mass), _p(new_table), new_max_pages, keep, recent, _p(kept), _p(new_lens),
+                                 stream), "cbs_cache_evict")
 
 
 def cbs_attn_plan(desc: cbs_attn_desc) -> cbs_attn_plan_t:

@@ -72,6 +72,19 @@ cudaError_t launch_cache_write(const CacheArgs &a, const void *k, long long k_st
                                long long v_stride, int in_bf16, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheArgs &a, int max_len, void *k_out, void *v_out, int out_bf16, cudaStream_t s);
 
+struct EvictLaunch {
+    CacheArgs c;
+    float *mass;                // [num_pages][kv_heads][page]
+    const int *new_table;       // [batch][new_max_pages]
+    int new_max_pages, keep, recent;
+    int *kept, *new_lens;       // [batch][kv_heads][keep], [batch]
+    int ctas;                   // of a cluster (set by the launch)
+};
+cudaError_t launch_evict(EvictLaunch L, cudaStream_t s);
+// Positions of a CTA of eight at most: what its shared memory holds.
+constexpr int kEvictRun = 48 * 1024;
+constexpr long long kEvictMost = 8ll * kEvictRun;
+
 struct W4Launch {
     const void *x;              // bf16, or int8 codes
     const float *x_scale;       // int8: [rows]

@@ -153,6 +153,46 @@ cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_le
                       "cache read launch");
 }
 
+cbs_status cbs_cache_evict(const cbs_cache *c, const cbs_sequences *s, float *mass, const int32_t *new_table,
+                           int new_max_pages, int keep, int recent, int32_t *kept, int32_t *new_lens, void *stream) {
+    EvictLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    CBS_TRY(cache_args(c, s, false, &L.c));
+    if (keep < 1 || recent < 0 || recent > keep) return fail(CBS_ERR_INVALID_ARG, "keep %d, recent %d of them", keep, recent);
+    if (new_max_pages < 0) return fail(CBS_ERR_INVALID_ARG, "new_max_pages %d", new_max_pages);
+    const long long held = (long long)s->max_pages * c->page_size;
+    if ((long long)new_max_pages * c->page_size < std::min<long long>(keep, held))
+        return fail(CBS_ERR_INVALID_ARG, "%d new pages of %d do not hold %lld positions", new_max_pages, c->page_size,
+                    std::min<long long>(keep, held));
+    if (held > kEvictMost) return fail(CBS_ERR_UNSUPPORTED, "tables of %lld positions: at most %lld", held, kEvictMost);
+    if (s->batch > kGridMax || c->kv_heads > kGridMax)
+        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
+    if (s->batch == 0) return CBS_OK;
+    CBS_TRY(need(mass, "mass"));
+    CBS_TRY(need(kept, "kept"));
+    CBS_TRY(need(new_lens, "new_lens"));
+    if (!new_table && new_max_pages > 0) return fail(CBS_ERR_INVALID_ARG, "new_table is NULL");
+    if (reinterpret_cast<uintptr_t>(new_table) & 3u) return fail(CBS_ERR_MISALIGNED, "new_table is not 4-byte aligned");
+    // What one part of the call writes, others still read.
+    const size_t rows = (size_t)c->num_pages * c->kv_heads * c->page_size, row = (size_t)c->head_dim * (c->prec == CBS_INT8 ? 1 : 2);
+    const size_t kept_bytes = (size_t)s->batch * c->kv_heads * keep * 4, lens_bytes = (size_t)s->batch * 4;
+    const struct { const void *p; size_t bytes; const char *what; } parts[] = {
+        {c->k, rows * row, "k"}, {c->v, rows * row, "v"}, {c->k_scale, rows * 4, "k_scale"}, {c->v_scale, rows * 4, "v_scale"},
+        {mass, rows * 4, "mass"}, {s->seq_lens, lens_bytes, "seq_lens"}, {s->page_table, (size_t)s->batch * s->max_pages * 4, "page_table"},
+        {new_table, (size_t)s->batch * new_max_pages * 4, "new_table"}, {new_lens, lens_bytes, "new_lens"}, {kept, kept_bytes, "kept"}};
+    constexpr int kParts = sizeof(parts) / sizeof(parts[0]);
+    for (int out = 4; out < kParts; ++out) {
+        if (out > 4 && out < 8) continue;   // inputs
+        for (int other = 0; other < out; ++other)
+            if (overlap(parts[out].p, parts[out].bytes, parts[other].p, parts[other].bytes))
+                return fail(CBS_ERR_INVALID_ARG, "%s lies on %s", parts[out].what, parts[other].what);
+    }
+    CBS_TRY(status_word(&L.c));
+    L.mass = mass; L.new_table = new_table; L.new_max_pages = new_max_pages;
+    L.keep = keep; L.recent = recent; L.kept = kept; L.new_lens = new_lens;
+    return cuda_check(launch_evict(L, (cudaStream_t)stream), "eviction launch");
+}
+
 cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     if (!d || !out) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", d ? "out" : "desc");
     if (d->batch < 0 || d->max_new < 0 || d->max_len < 0 || d->heads < 1 || d->window < 0 || d->force_split < 0 ||

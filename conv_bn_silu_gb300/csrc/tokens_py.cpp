@@ -216,6 +216,24 @@ PyObject *cache_read(PyObject *const *a) {
     return s != CBS_OK ? status(s) : triple(THPVariable_Wrap(k), THPVariable_Wrap(v), none());
 }
 
+// cache_evict(cache, device, mass, seq_lens, page_table, new_table, keep, recent) -> (kept, new_lens, None)
+PyObject *cache_evict(PyObject *const *a) {
+    const auto *c = static_cast<const cbs_cache *>(pointer(a[0]));
+    const Tensor &mass = dense(a[2], "mass", nullptr, ScalarType::Float, {c->num_pages, c->kv_heads, c->page_size});
+    at_home(mass, "mass", a[1]);
+    const int64_t batch = dense(a[4], "page_table", &mass, ScalarType::Int, {-1, -1}).size(0);
+    const Tensor &table = dense(a[5], "new_table", &mass, ScalarType::Int, {batch, -1});
+    const long keep = integer(a[6]), recent = integer(a[7]);
+    if (keep < 1 || keep > INT_MAX) refuse("keep", "out of range");
+    if (recent < 0 || recent > keep) refuse("recent", "0 to keep");
+    const cbs_sequences seqs = sequences(Py_None, a[3], a[4], 0, &mass);
+    const c10::cuda::CUDAGuard guard(mass.device());
+    Tensor kept = empty({seqs.batch, c->kv_heads, keep}, ScalarType::Int, mass), lens = empty({seqs.batch}, ScalarType::Int, mass);
+    const cbs_status s = cbs_cache_evict(c, &seqs, mass.data_ptr<float>(), table.data_ptr<int>(), (int)table.size(1), (int)keep, (int)recent,
+                                         kept.data_ptr<int>(), lens.data_ptr<int>(), stream_of(mass));
+    return s != CBS_OK ? status(s) : triple(THPVariable_Wrap(kept), THPVariable_Wrap(lens), none());
+}
+
 // attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace, its stream) -> out
 PyObject *attention(PyObject *const *a) {
     const auto *p = static_cast<const cbs_attn_plan_t *>(pointer(a[0]));
@@ -268,7 +286,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define CBS_PY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 13), CBS_PY(cache_write, 7),
-                         CBS_PY(cache_read, 6), CBS_PY(attention, 11),       {nullptr, nullptr, 0, nullptr}};
+                         CBS_PY(cache_read, 6), CBS_PY(attention, 11),       CBS_PY(cache_evict, 8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", "The token operators' calls (see tokens.py).", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -181,6 +181,16 @@ class PagedCache:
             _refuse("dtype: float32 or bfloat16")
         return _done(_calls().cache_read(*self._at, seq_lens, page_table, max_len, dtype is _BF16), "cbs_cache_read")[:2]
 
+    def evict(self, mass: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor, new_table: torch.Tensor, keep: int,
+              recent: int = 0):
+        """The last `recent` positions of each sequence and the heaviest others,
+        `keep` in all, in order to the pages of new_table (int32 [batch, pages],
+        none of them the sequences' own); each key head chooses by itself.  mass:
+        float32 [num_pages, kv_heads, page_size] (WeighedAttention adds it up), which
+        moves along.  Returns the old positions (int32 [batch, kv_heads, keep], -1
+        past them) and the new lengths."""
+        return _done(_calls().cache_evict(*self._at, mass, seq_lens, page_table, new_table, keep, recent), "cbs_cache_evict")[:2]
+
 
 class PagedAttention:
     """Attention of new tokens over a paged cache: the plan for one kind of

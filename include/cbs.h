@@ -502,6 +502,28 @@ CBS_API cbs_status cbs_cache_write(const cbs_cache *c, const cbs_sequences *s, c
 CBS_API cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_len, void *k_out, void *v_out,
                                   int out_prec, void *stream);
 
+/*
+ * cbs_cache_evict -- thins sequences out by the weight that their positions have
+ * received (cbs_weighed_attention adds it up): of each sequence and head, which
+ * each make a choice of their own, the last min(recent, length) positions stay,
+ * and of the others the heaviest, min(keep, length) in all; of equal weights the
+ * earlier position stays, a NaN is heavier than any number.  What stays goes, in
+ * order, to positions 0, 1, ... of new pages: keys, values, scales and weights.
+ *   mass: float [num_pages][kv_heads][page_size];
+ *   new_table: [batch][new_max_pages], pages that none of the call's sequences
+ *     holds (the old ones are left as they are, and free after the call unless
+ *     others share them); 0 <= recent <= keep, and the pages hold
+ *     min(keep, max_pages * page_size) positions (more is refused);
+ *   kept: [batch][kv_heads][keep], the old position of each new one, -1 past them;
+ *   new_lens: [batch], min(keep, length).  kept and new_lens are outputs (16-byte
+ *     aligned) and on none of the inputs.
+ * new_start is not read and may be NULL.  max_pages * page_size is at most
+ * 393216.  Equal calls give equal results.
+ */
+CBS_API cbs_status cbs_cache_evict(const cbs_cache *c, const cbs_sequences *s, float *mass, const int32_t *new_table,
+                                   int new_max_pages, int keep, int recent, int32_t *kept, int32_t *new_lens,
+                                   void *stream);
+
 /* One kind of attention call. */
 typedef struct cbs_attn_desc {
     int batch;         /* sequences */
