@@ -38,6 +38,7 @@ EXPORTED = (
     "cbs_conv_bn_silu_i8_cat", "cbs_selftest_wait_timeout", "cbs_sppf_pool", "cbs_dequantize_i8",
     "cbs_quantize_i8", "cbs_cache_write", "cbs_cache_read", "cbs_attn_plan", "cbs_paged_attention", "cbs_rmsnorm",
     "cbs_dequantize_rows", "cbs_linear_w4", "cbs_quantize_w4", "cbs_cache_evict",
+    "cbs_linear_w8", "cbs_quantize_w8",
 )
 
 
@@ -123,6 +124,8 @@ def lib():
         L.cbs_dequantize_rows.argtypes = [P, P, P, I, I, I, P]
         L.cbs_linear_w4.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, P]
         L.cbs_quantize_w4.argtypes = [P, I, I, I, P, P, P]
+        L.cbs_linear_w8.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
+        L.cbs_quantize_w8.argtypes = [P, I, I, P, P, P]
         L.cbs_workspace_init.argtypes = [P, Z, P]
         L.cbs_read_device_status.argtypes = [ctypes.POINTER(I), I, P]
         L.cbs_selftest_wait_timeout.argtypes = [I, P]
@@ -312,3 +315,12 @@ def cbs_linear_w4(x, x_prec, x_scale, w, scales, zeros, bias, y, out_prec, rows,
 
 def cbs_quantize_w4(w, n, k, group, packed, scales, stream):
     _check(lib().cbs_quantize_w4(_p(w), n, k, group, _p(packed), _p(scales), stream), "cbs_quantize_w4")
+
+
+def cbs_linear_w8(x, x_scale, w, w_scale, bias, y, out_prec, rows, n, k, activation, stream):
+    _check(lib().cbs_linear_w8(_p(x), _p(x_scale), _p(w), _p(w_scale), _p(bias), _p(y), out_prec, rows, n, k, activation,
+                               stream), "cbs_linear_w8")
+
+
+def cbs_quantize_w8(w, n, k, codes, scales, stream):
+    _check(lib().cbs_quantize_w8(_p(w), n, k, _p(codes), _p(scales), stream), "cbs_quantize_w8")

@@ -100,6 +100,16 @@ cbs_status launch_w4(const W4Launch &L, cudaStream_t s);
 cudaError_t launch_w4_few(const W4Launch &L, cudaStream_t s);   // up to eight rows
 cudaError_t launch_quantize_w4(const float *w, int n, int k, int group, uint8_t *packed, void *scales, cudaStream_t s);
 
+struct W8Launch {
+    const int8_t *x, *w;        // [rows][k], [n][k]
+    const float *x_scale, *w_scale, *bias;   // [rows], [n], [n] (nullable)
+    void *y;
+    unsigned int *status;
+    int rows, n, k, out_bf16, act;
+};
+cbs_status launch_w8(const W8Launch &L, cudaStream_t s);
+cudaError_t launch_quantize_w8(const float *w, int n, int k, int8_t *codes, float *scales, cudaStream_t s);
+
 struct AttnLaunch {
     CacheArgs c;
     const void *q;              // bf16 [total][heads][head_dim], q_stride elements between tokens

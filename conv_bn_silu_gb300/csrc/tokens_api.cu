@@ -429,4 +429,50 @@ cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed
                       "4-bit quantiser launch");
 }
 
+static cbs_status w8_shape(int n, int k) {
+    if (n < 1 || k < 1) return fail(CBS_ERR_INVALID_ARG, "bad weight shape (%d x %d)", n, k);
+    if (k % 16) return fail(CBS_ERR_UNSUPPORTED, "k = %d is not a multiple of 16", k);
+    return CBS_OK;
+}
+
+cbs_status cbs_linear_w8(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale, const float *bias,
+                         void *y, int out_prec, int rows, int n, int k, int activation, void *stream) {
+    CBS_TRY(float_type(out_prec, "output"));
+    CBS_TRY(w8_shape(n, k));
+    if (activation != CBS_ACT_SILU && activation != CBS_ACT_IDENTITY)
+        return fail(CBS_ERR_INVALID_ARG, "unknown activation %d", activation);
+    if (rows < 0) return fail(CBS_ERR_INVALID_ARG, "%d rows", rows);
+    if (rows > 256 * kGridMax) return fail(CBS_ERR_UNSUPPORTED, "%d rows: at most %d", rows, 256 * kGridMax);
+    if (rows == 0) return CBS_OK;
+    CBS_TRY(need(x, "x"));
+    CBS_TRY(need(x_scale, "x_scale"));
+    CBS_TRY(need(w, "w"));
+    CBS_TRY(need(w_scale, "w_scale"));
+    CBS_TRY(may(bias, "bias"));
+    CBS_TRY(need(y, "y"));
+    const size_t y_bytes = (size_t)rows * n * (out_prec == CBS_BF16 ? 2 : 4);
+    const struct { const void *p; size_t bytes; } inputs[] = {
+        {x, (size_t)rows * k}, {x_scale, (size_t)rows * 4}, {w, (size_t)n * k}, {w_scale, (size_t)n * 4}, {bias, (size_t)n * 4}};
+    for (const auto &in : inputs)
+        if (overlap(y, y_bytes, in.p, in.bytes)) return fail(CBS_ERR_INVALID_ARG, "y lies on an input");
+    W8Launch L;
+    L.x = x; L.x_scale = x_scale; L.w = w; L.w_scale = w_scale; L.bias = bias; L.y = y;
+    L.rows = rows; L.n = n; L.k = k; L.out_bf16 = out_prec == CBS_BF16; L.act = activation;
+    L.status = device_status_word();
+    if (!L.status) return fail(CBS_ERR_CUDA, "cannot resolve the device status word");
+    return launch_w8(L, (cudaStream_t)stream);
+}
+
+cbs_status cbs_quantize_w8(const float *w, int n, int k, int8_t *codes, float *scales, void *stream) {
+    CBS_TRY(w8_shape(n, k));
+    CBS_TRY(need(w, "w"));
+    CBS_TRY(need(codes, "codes"));
+    CBS_TRY(need(scales, "scales"));
+    const size_t w_bytes = (size_t)n * k * 4;
+    if (overlap(codes, (size_t)n * k, w, w_bytes) || overlap(scales, (size_t)n * 4, w, w_bytes) ||
+        overlap(codes, (size_t)n * k, scales, (size_t)n * 4))
+        return fail(CBS_ERR_INVALID_ARG, "an output lies on the weights or another");
+    return cuda_check(launch_quantize_w8(w, n, k, codes, scales, (cudaStream_t)stream), "8-bit quantiser launch");
+}
+
 }  // extern "C"

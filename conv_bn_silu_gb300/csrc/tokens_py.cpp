@@ -184,6 +184,29 @@ PyObject *linear_w4(PyObject *const *a) {
     return a[2] != Py_None ? Py_NewRef(a[2]) : THPVariable_Wrap(out);
 }
 
+// linear_w8(x, x_scale, out, bf16, device, n, k, activation, w, w_scale, bias) -> out; the
+// layer's own arrays as addresses
+PyObject *linear_w8(PyObject *const *a) {
+    const int n = (int)integer(a[5]), k = (int)integer(a[6]);
+    const Tensor &x = dense(a[0], "x", nullptr, ScalarType::Char, {-1, k});
+    at_home(x, "x", a[4]);
+    const int64_t rows = x.size(0);
+    const Tensor &x_scale = dense(a[1], "x_scale", &x, ScalarType::Float, {rows});
+    Tensor out;
+    if (a[2] != Py_None) {
+        out = tensor(a[2], "out");
+        if (!is_float(out.scalar_type())) refuse("out", "expected float32 or bfloat16");
+        dense(a[2], "out", &x, out.scalar_type(), {rows, n});
+    }
+    const c10::cuda::CUDAGuard guard(x.device());
+    if (!out.defined()) out = empty({rows, n}, flag(a[3]) ? ScalarType::BFloat16 : ScalarType::Float, x);
+    const cbs_status s = cbs_linear_w8(x.data_ptr<int8_t>(), x_scale.data_ptr<float>(), static_cast<const int8_t *>(pointer(a[8])),
+                                       static_cast<const float *>(pointer(a[9])), static_cast<const float *>(pointer(a[10])),
+                                       out.data_ptr(), prec(out.scalar_type()), (int)rows, n, k, (int)integer(a[7]), stream_of(x));
+    if (s != CBS_OK) return status(s);
+    return a[2] != Py_None ? Py_NewRef(a[2]) : THPVariable_Wrap(out);
+}
+
 // cache_write(cache, device, k, v, new_start, seq_lens, page_table)
 PyObject *cache_write(PyObject *const *a) {
     const auto *c = static_cast<const cbs_cache *>(pointer(a[0]));
@@ -286,7 +309,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define CBS_PY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 13), CBS_PY(cache_write, 7),
-                         CBS_PY(cache_read, 6), CBS_PY(attention, 11),       CBS_PY(cache_evict, 8), {nullptr, nullptr, 0, nullptr}};
+                         CBS_PY(cache_read, 6), CBS_PY(attention, 11),       CBS_PY(cache_evict, 8),
+                         CBS_PY(linear_w8, 11),  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", "The token operators' calls (see tokens.py).", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

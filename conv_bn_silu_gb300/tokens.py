@@ -136,6 +136,45 @@ class LinearW4:
         return _done(_calls().linear_w4(x, x_scale, out, dtype is _BF16, *self._args), "cbs_linear_w4")
 
 
+class LinearW8:
+    """A layer of 8-bit weights [n, k], a float scale for each output: y = act(x_scale
+    w_scale (x W^T) + bias), for one row of codes as for thousands."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
+                 activation: int = B.CBS_ACT_IDENTITY):
+        _dense(codes, "codes", (_I8,))
+        if codes.dim() != 2:
+            _refuse("codes: expected [n, k]")
+        self.n, self.k = codes.shape
+        if self.k % 16:
+            _refuse(f"k = {self.k} is not a multiple of 16")
+        _dense(scales, "scales", (_F32,), (self.n,), codes.device)
+        if bias is not None:
+            _dense(bias, "bias", (_F32,), (self.n,), codes.device)
+        self.codes, self.scales, self.bias, self.activation = codes, scales, bias, activation
+        self._args = (codes.device.index, self.n, self.k, activation, *map(B._p, (codes, scales, bias)))
+
+    @classmethod
+    def quantize(cls, w: torch.Tensor, bias: torch.Tensor | None = None, activation: int = B.CBS_ACT_IDENTITY) -> "LinearW8":
+        """The layer of float weights w [n, k], quantised once on the GPU (an
+        output's largest weight at 127)."""
+        _dense(w, "w", (_F32,))
+        if w.dim() != 2 or w.shape[1] % 16:
+            _refuse("w: expected [n, k], with k a multiple of 16")
+        codes = torch.empty(w.shape, dtype=_I8, device=w.device)
+        scales = torch.empty(w.shape[0], dtype=_F32, device=w.device)
+        with torch.cuda.device(w.device):
+            B.cbs_quantize_w8(w, *w.shape, codes, scales, current_stream())
+        return cls(codes, scales, bias=bias, activation=activation)
+
+    def __call__(self, x: torch.Tensor, x_scale: torch.Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+        """x: int8 codes [rows, k] with x_scale float [rows].  The result is of
+        `dtype`, or of out's type where out is given."""
+        if dtype not in _FLOATS:
+            _refuse("dtype: float32 or bfloat16")
+        return _done(_calls().linear_w8(x, x_scale, out, dtype is _BF16, *self._args), "cbs_linear_w8")
+
+
 class PagedCache:
     """Keys and values in pages [num_pages, kv_heads, page_size, head_dim]:
     bfloat16, or int8 with a float scale for each page, head and position."""

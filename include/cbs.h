@@ -625,6 +625,27 @@ CBS_API cbs_status cbs_linear_w4(const void *x, int x_prec, const float *x_scale
  * of are NaN. */
 CBS_API cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed, void *scales, void *stream);
 
+/*
+ * cbs_linear_w8 -- product of 8-bit integers with a scale for each token and each
+ * channel:
+ *   y[m,n] = act( x_scale[m] w_scale[n] sum_k x[m,k] w[n,k] + bias[n] )
+ * x: int8 [rows][k], x_scale float[rows] (cbs_rmsnorm's rows).  w: int8 [n][k],
+ * w_scale float[n].  k a multiple of 16.  bias: float[n] or NULL.  y: [rows][n],
+ * out_prec CBS_FP32 or CBS_BF16.  activation: cbs_activation.  The sums are exact
+ * where they and their parts stay below 2^24 (any codes up to k = 1024; codes of
+ * ordinary rows far beyond), and rounded to 24 bits past that.  For one row as for
+ * thousands.
+ */
+CBS_API cbs_status cbs_linear_w8(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale,
+                                 const float *bias, void *y, int out_prec, int rows, int n, int k, int activation,
+                                 void *stream);
+
+/* cbs_quantize_w8 -- one-time weight transform for cbs_linear_w8: w float
+ * [n][k] -> codes and scales: s = max|w| / 127 over an output's weights, code =
+ * clamp(rne(w / s), -127, 127).  Weights that hold a NaN or an infinity get the
+ * scale NaN: the output is NaN. */
+CBS_API cbs_status cbs_quantize_w8(const float *w, int n, int k, int8_t *codes, float *scales, void *stream);
+
 /* Zero a workspace before its first use (cudaMemsetAsync on `stream`). */
 CBS_API cbs_status cbs_workspace_init(void *workspace, size_t bytes, void *stream);
 
