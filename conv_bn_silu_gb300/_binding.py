@@ -38,7 +38,7 @@ EXPORTED = (
     "cbs_conv_bn_silu_i8_cat", "cbs_selftest_wait_timeout", "cbs_sppf_pool", "cbs_dequantize_i8",
     "cbs_quantize_i8", "cbs_cache_write", "cbs_cache_read", "cbs_attn_plan", "cbs_paged_attention", "cbs_rmsnorm",
     "cbs_dequantize_rows", "cbs_linear_w4", "cbs_quantize_w4", "cbs_cache_evict",
-    "cbs_linear_w8", "cbs_quantize_w8",
+    "cbs_linear_w8", "cbs_quantize_w8", "cbs_weighed_plan", "cbs_weighed_attention", "cbs_shared_plan", "cbs_shared_attention",
 )
 
 
@@ -84,6 +84,28 @@ class cbs_attn_plan_t(ctypes.Structure):
         [("workspace_bytes", ctypes.c_size_t), ("desc", cbs_attn_desc)]
 
 
+class cbs_weighed_plan_t(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("abi_version", ctypes.c_uint32), ("attention", cbs_attn_plan_t),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class cbs_prefixes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("group_start", "prefix_lens", "page_table")] + \
+        [(n, ctypes.c_int) for n in ("groups", "max_pages")]
+
+
+class cbs_shared_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "batch", "groups", "max_new", "max_group_new", "max_len", "max_prefix", "heads", "kv_heads", "head_dim", "cache_prec",
+        "num_sms")]
+
+
+class cbs_shared_plan_t(ctypes.Structure):
+    _fields_ = [("size", ctypes.c_uint32), ("abi_version", ctypes.c_uint32), ("prefix", cbs_attn_plan_t),
+                ("own", cbs_attn_plan_t), ("max_total", ctypes.c_int), ("zeroed_bytes", ctypes.c_size_t),
+                ("workspace_bytes", ctypes.c_size_t), ("desc", cbs_shared_desc)]
+
+
 class CbsError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         super().__init__(f"{where}: {status_name(status)} ({status}): {message}")
@@ -120,6 +142,11 @@ def lib():
         L.cbs_cache_evict.argtypes = [CP, SP, P, P, I, I, I, P, P, P]
         L.cbs_attn_plan.argtypes = [ctypes.POINTER(cbs_attn_desc), ctypes.POINTER(cbs_attn_plan_t)]
         L.cbs_paged_attention.argtypes = [ctypes.POINTER(cbs_attn_plan_t), CP, SP, P, LL, F, P, LL, P, Z, P]
+        WP, HP = ctypes.POINTER(cbs_weighed_plan_t), ctypes.POINTER(cbs_shared_plan_t)
+        L.cbs_weighed_plan.argtypes = [ctypes.POINTER(cbs_attn_desc), WP]
+        L.cbs_weighed_attention.argtypes = [WP, CP, SP, P, LL, F, P, LL, P, F, P, Z, P]
+        L.cbs_shared_plan.argtypes = [ctypes.POINTER(cbs_shared_desc), HP]
+        L.cbs_shared_attention.argtypes = [HP, CP, SP, ctypes.POINTER(cbs_prefixes), P, LL, F, P, LL, P, Z, P]
         L.cbs_rmsnorm.argtypes = [P, P, P, P, P, P, I, I, F, I, I, P]
         L.cbs_dequantize_rows.argtypes = [P, P, P, I, I, I, P]
         L.cbs_linear_w4.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, P]
@@ -324,3 +351,25 @@ def cbs_linear_w8(x, x_scale, w, w_scale, bias, y, out_prec, rows, n, k, activat
 
 def cbs_quantize_w8(w, n, k, codes, scales, stream):
     _check(lib().cbs_quantize_w8(_p(w), n, k, _p(codes), _p(scales), stream), "cbs_quantize_w8")
+
+
+def cbs_weighed_plan(desc: cbs_attn_desc) -> cbs_weighed_plan_t:
+    plan = cbs_weighed_plan_t()
+    _check(lib().cbs_weighed_plan(ctypes.byref(desc), ctypes.byref(plan)), "cbs_weighed_plan")
+    return plan
+
+
+def cbs_weighed_attention(plan, cache, seqs, q, q_stride, scale, out, out_stride, mass, decay, workspace, workspace_bytes, stream):
+    _check(lib().cbs_weighed_attention(plan, cache, seqs, _p(q), q_stride, scale, _p(out), out_stride, _p(mass), decay,
+                                       _p(workspace), workspace_bytes, stream), "cbs_weighed_attention")
+
+
+def cbs_shared_plan(desc: cbs_shared_desc) -> cbs_shared_plan_t:
+    plan = cbs_shared_plan_t()
+    _check(lib().cbs_shared_plan(ctypes.byref(desc), ctypes.byref(plan)), "cbs_shared_plan")
+    return plan
+
+
+def cbs_shared_attention(plan, cache, seqs, prefixes, q, q_stride, scale, out, out_stride, workspace, workspace_bytes, stream):
+    _check(lib().cbs_shared_attention(plan, cache, seqs, prefixes, _p(q), q_stride, scale, _p(out), out_stride, _p(workspace),
+                                      workspace_bytes, stream), "cbs_shared_attention")

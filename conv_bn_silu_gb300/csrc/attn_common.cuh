@@ -13,6 +13,14 @@ namespace cbs {
 // neither an exchange between lanes nor a rescaling of the output.
 constexpr float kLazy = 8.0f;
 
+// What becomes of a row's softmax beside or in place of its output.
+enum AttnMode {
+    kAttnPlain = 0,
+    kAttnPrefix = 1,   // a group's prefix: the rows' shares go to L.share, unnormalised
+    kAttnOwn = 2,      // the sequences' own keys: joined with those shares
+    kAttnWeighed = 3   // the output, and each row's (maximum, 1 / sum) to L.row_stats
+};
+
 // Keys [lo, hi) are what a row at `place` sees of a sequence.
 struct Seen { int lo, hi; };
 __device__ __forceinline__ Seen seen_by(int place, int len, int causal, int window) {
@@ -36,6 +44,11 @@ struct Rows {
         const int t = token(L, r);
         return static_cast<const __nv_bfloat16 *>(L.q) + (size_t)(start + t) * L.q_stride + (size_t)(head * L.group + r - t * L.group) * D;
     }
+    // Of all (token, query head) rows of the call, this one's number.
+    __device__ __forceinline__ size_t number(const AttnLaunch &L, int r) const {
+        const int t = token(L, r);
+        return (size_t)(start + t) * L.heads + head * L.group + r - t * L.group;
+    }
     __device__ __forceinline__ __nv_bfloat16 *out(const AttnLaunch &L, int r, int D) const {
         const int t = token(L, r);
         return static_cast<__nv_bfloat16 *>(L.out) + (size_t)(start + t) * L.out_stride + (size_t)(head * L.group + r - t * L.group) * D;
@@ -57,19 +70,29 @@ __device__ __forceinline__ void zero_padding(const AttnLaunch &L, int end, int D
 // The rows of sequence b, its starts within the call's tokens and its chunk
 // within the plan's (the status bit otherwise).  Behind the last sequence's
 // tokens, the padding.
+// (kAttnPrefix: b is a group, its rows those of all its sequences.)
+template <int MODE>
 __device__ __forceinline__ Rows rows_of(const AttnLaunch &L, int b, int head, int D) {
     const CacheArgs &c = L.c;
     Rows s;
-    const int s0 = c.new_start[b], s1 = c.new_start[b + 1];
+    int i0 = b, i1 = b + 1;
+    if constexpr (MODE == kAttnPrefix) {
+        const int g0 = L.group_start[b], g1 = L.group_start[b + 1];
+        i0 = max(0, min(g0, L.sequences));
+        i1 = max(i0, min(g1, L.sequences));
+        if ((i0 != g0 || i1 != g1 || (b == 0 && g0 != 0) || (b == c.batch - 1 && g1 != L.sequences)) && threadIdx.x == 0)
+            atomicOr(c.status, kStatusBadIndex);
+    }
+    const int s0 = c.new_start[i0], s1 = c.new_start[i1];
     s.len = seq_len(c, b);
     s.start = max(0, min(s0, c.total));
     const int end = max(s.start, min(s1, c.total));
     s.fresh = end - s.start;
-    if (s.start != s0 || end != s1 || s.fresh > L.max_new || (b == 0 && s0 != 0)) {
+    if (s.start != s0 || end != s1 || s.fresh > L.max_new || (i0 == 0 && s0 != 0)) {
         if (threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
         s.fresh = min(s.fresh, L.max_new);
     }
-    if (b == c.batch - 1 && end < c.total) zero_padding(L, end, D);
+    if (MODE != kAttnPrefix && b == c.batch - 1 && end < c.total) zero_padding(L, end, D);
     s.R = s.fresh * L.group;
     s.head = head;
     s.base = s.len - s.fresh;
@@ -85,10 +108,40 @@ __device__ __forceinline__ float share_factor(float m, float l, float top) {
 }
 
 // Four dimensions of a row's output: acc / sum, zeros for a row that sees nothing.
-__device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, int r, int D, int dim, float4 acc, float sum) {
+// `top`: the maximum that acc and sum are above; `exact`: kAttnWeighed, the sum of
+// the probabilities before any rounding.
+template <int MODE>
+__device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, int r, int D, int dim, float4 acc, float sum, float top,
+                                           float exact) {
+    if constexpr (MODE == kAttnPrefix) {
+        const size_t row = s.number(L, r);
+        if (dim == 0) L.share_stats[row] = make_float2(top, sum);
+        *reinterpret_cast<float4 *>(L.share + row * D + dim) = acc;
+        return;
+    }
     const Seen z = s.seen(L, r);
     uint2 w = make_uint2(0u, 0u);
-    if (z.hi > z.lo) {
+    bool any = z.hi > z.lo;
+    if constexpr (MODE == kAttnOwn) {
+        const size_t row = s.number(L, r);
+        const float2 st = __ldcg(&L.share_stats[row]);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(L.share + row * D + dim));
+        const float both = fmaxf(top, st.x), mine = share_factor(top, sum, both), theirs = share_factor(st.x, st.y, both);
+        const bool none = !any || (top == -INFINITY && mine == 0.0f);   // (acc may hold anything)
+        acc = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(acc.x * mine, acc.y * mine, acc.z * mine, acc.w * mine);
+        sum = none ? 0.0f : sum * mine;
+        if (!(st.x == -INFINITY && theirs == 0.0f)) {
+            acc.x = fmaf(v.x, theirs, acc.x); acc.y = fmaf(v.y, theirs, acc.y);
+            acc.z = fmaf(v.z, theirs, acc.z); acc.w = fmaf(v.w, theirs, acc.w);
+            sum = fmaf(st.y, theirs, sum);
+            any = true;
+        }
+    }
+    if constexpr (MODE == kAttnWeighed) {
+        if (dim == 0)
+            L.row_stats[s.number(L, r)] = any ? make_float2(top == -INFINITY ? 0.0f : top, __fdiv_rn(1.0f, exact)) : make_float2(0.0f, 0.0f);
+    }
+    if (any) {
         const float inv = __fdiv_rn(1.0f, sum);
         w.x = frag::pack_bf16(acc.x * inv, acc.y * inv);
         w.y = frag::pack_bf16(acc.z * inv, acc.w * inv);
@@ -144,7 +197,7 @@ __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b,
 // After a CTA has written its range's share of a tile (L.partial, L.stats):
 // the CTA that comes last joins the ranges, in their order, so that the result
 // does not depend on which one that is.  `flag`: a word of shared memory.
-template <int D, int kRows, int kThreads>
+template <int D, int kRows, int kThreads, int MODE>
 __device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, int tile, int r0, int active, int tid, int *flag) {
     __threadfence();
     __syncthreads();
@@ -164,7 +217,7 @@ __device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, 
         float top = -INFINITY;
         for (int x = 0; x < active; ++x) top = fmaxf(top, __ldcg(&L.stats[at + (size_t)x * kRows]).x);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
+        float sum = 0.0f, exact = 0.0f;
         for (int x = 0; x < active; ++x) {
             const float2 st = __ldcg(&L.stats[at + (size_t)x * kRows]);
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(L.partial + (at + (size_t)x * kRows) * D + 4 * u));
@@ -173,8 +226,9 @@ __device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, 
             acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
             acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
             sum = fmaf(st.y, fac, sum);
+            if constexpr (MODE == kAttnWeighed) exact = fmaf(__ldcg(&L.sums[at + (size_t)x * kRows]), fac, exact);
         }
-        store_out4(L, s, r0 + r, D, 4 * u, acc, sum);
+        store_out4<MODE>(L, s, r0 + r, D, 4 * u, acc, sum, top, exact);
     }
 }
 

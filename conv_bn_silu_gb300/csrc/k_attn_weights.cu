@@ -1,0 +1,356 @@
+// k_attn_weights.cu -- the weight that each position of a paged cache received from
+// a call's new tokens: over the rows (token, query head) of its key head
+//
+//   mass[key] = decay mass[key] + sum_r p[r, key],   p = 2^(score - m_r) / l_r
+//
+// (a key that is new in the call starts at zero), with the rows' maxima m_r and sums
+// l_r from the attention that ran before.  Every key has one owner, so nothing is
+// added atomically and equal calls give equal results.
+//
+// Few rows: the attention left its scores, 4 bytes a row and key where the key itself
+// has 64 to 256, and the first kernel sums them up.  Chunks would leave too many: the
+// second kernel takes the first product again, S^T = K Q^T on tcgen05 with 128 keys as
+// the lanes of tensor memory.  A key tile stays where it is while the rows' tiles
+// pass, and a thread's sum over them never leaves its registers.  The exponentials
+// bound it: one a score, sixteen a clock and SM.
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+#include "tc_warp.cuh"
+
+namespace cbs {
+
+namespace {
+
+// A sequence's rows as the attention took them (which has reported what is wrong with them).
+__device__ __forceinline__ Rows rows_again(const AttnLaunch &L, int b, int head) {
+    const CacheArgs &c = L.c;
+    Rows s;
+    s.len = seq_len(c, b);
+    s.start = max(0, min(c.new_start[b], c.total));
+    s.fresh = min(max(s.start, min(c.new_start[b + 1], c.total)) - s.start, L.max_new);
+    s.R = s.fresh * L.group;
+    s.head = head;
+    s.base = s.len - s.fresh;
+    return s;
+}
+
+// A key's weight: what it was, and what came.
+__device__ __forceinline__ float weight_after(const AttnLaunch &L, const Rows &s, int key, float before, float came) {
+    return (key < s.base && L.decay != 0.0f ? L.decay * before : 0.0f) + came;
+}
+
+constexpr int kSumThreads = 128, kSumKeys = 4;   // keys of a thread
+
+__global__ void __launch_bounds__(kSumThreads) weights_of_scores_kernel(const AttnLaunch L) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const CacheArgs &c = L.c;
+    const int head = blockIdx.y, b = blockIdx.z;
+    const Rows rs = rows_again(L, b, head);
+    if (rs.fresh == 0) return;
+    if (rs.len > L.len_pad && threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
+    const int key = (blockIdx.x * kSumThreads + threadIdx.x) * kSumKeys, end = min(rs.len, L.len_pad);
+    if (key >= end) return;
+    const float *scores = L.scores + (size_t)(b * c.kv_heads + head) * L.rows_pad * L.len_pad + key;
+    float sum[kSumKeys] = {};
+    for (int r = 0; r < rs.R; ++r) {
+        const Seen z = rs.seen(L, r);
+        if (z.hi <= key || z.lo >= key + kSumKeys) continue;
+        const float2 st = __ldg(&L.row_stats[rs.number(L, r)]);
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(scores + (size_t)r * L.len_pad));
+        const float s[kSumKeys] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < kSumKeys; ++i)
+            if (key + i >= z.lo && key + i < z.hi) sum[i] = fmaf(frag::ex2(s[i] - st.x), st.y, sum[i]);
+    }
+    const int p = page_of(c, b, key);   // (all of them: pages hold multiples of sixteen)
+    if (p < 0) return;
+    float *mass = L.mass + (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+#pragma unroll
+    for (int i = 0; i < kSumKeys; ++i)
+        if (key + i < end) mass[i] = weight_after(L, rs, key + i, mass[i], sum[i]);
+}
+
+// ------------------------------------------------------------------- chunks
+constexpr int kKeys = 128, kRowTile = 128, kBufs = 4;
+constexpr int kLoaders = 4, kWarps = 4 * kBufs + kLoaders + 1, kThreads = kWarps * 32;   // a warpgroup a buffer sums up
+constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
+
+template <int D>
+struct Weigh {
+    static constexpr int kOperand = (D / 64) * kKeys * 128;   // panels of 64 dimensions
+    static constexpr int kQ = kOperand, kStats = kQ + kBufs * kOperand;
+    // each buffer's rows: m[128], 1 / l[128], lo[128], hi[128]; after them whether one is far
+    static constexpr int kStat = 4 * kRowTile * 4, kFar = kStats + kBufs * kStat, kBars = kFar + kBufs * 4;
+    static constexpr int kNumBars = 3 * kBufs;   // full[], s_full[], s_free[]
+    static constexpr int kSum = kBars + kNumBars * 8, kSmem = kSum + (kBufs - 1) * kKeys * 4 + 16;
+    static_assert(kSmem <= kMaxDynSmem && kBars % 8 == 0, "shared memory");
+};
+
+// As slow_row takes a row's score of a key, to the bit.
+template <int D, bool I8>
+__device__ __noinline__ float slow_score(const AttnLaunch &L, const Rows &s, int r, size_t row, int lane) {
+    constexpr int kE = D / 32;
+    const __nv_bfloat16 *q = s.query(L, r, D) + lane * kE;
+    const size_t at = row * D + lane * kE;
+    float dot = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        const float k = I8 ? (float)static_cast<const int8_t *>(L.c.k)[at + e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(L.c.k)[at + e]);
+        dot = fmaf(__bfloat162float(q[e]), k, dot);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(~0u, dot, x);
+    return __fmul_rn(dot, I8 ? L.c.k_scale[row] * L.scale_log2 : L.scale_log2);
+}
+
+__device__ __forceinline__ bool far_row(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const AttnLaunch L) {
+    using C = Weigh<D>;
+    extern __shared__ __align__(1024) unsigned char smem[];   // the only shared memory: starts at a multiple of 1 KB
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const CacheArgs &c = L.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    ptx::griddep_wait();
+    const int head = blockIdx.y, b = blockIdx.z, key0 = blockIdx.x * kKeys;
+    const Rows rs = rows_again(L, b, head);
+    if (rs.len > L.len_pad && tid == 0) atomicOr(c.status, kStatusBadIndex);
+    const int end = min(min(rs.len, L.len_pad), key0 + kKeys);
+    if (rs.fresh == 0 || key0 >= end) return;
+    // The tokens that see one of the keys, and the tiles of their rows.
+    const long long t0 = L.causal ? max(0ll, (long long)key0 - rs.base) : 0ll;
+    const long long t1 = L.window ? min((long long)rs.fresh, (long long)end - 1 + L.window - rs.base) : rs.fresh;
+    const int first = (int)(t0 * L.group / kRowTile), tiles = t0 < t1 ? (int)((t1 * L.group + kRowTile - 1) / kRowTile) - first : 0;
+
+    const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+    const auto full = [&](int s) { return bar(s); };                 // a tile's rows and their statistics are there
+    const auto s_full = [&](int s) { return bar(kBufs + s); };       // its scores
+    const auto s_free = [&](int s) { return bar(2 * kBufs + s); };   // all of them have been summed up
+    volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kSum + (kBufs - 1) * kKeys * 4);
+    // words[0]: TMEM address; [1]: a wait ran out
+    if (tid == 0) {
+        for (int s = 0; s < kBufs; ++s) {
+            ptx::mbar_init(full(s), kLoaders);
+            ptx::mbar_init(s_full(s), 1);
+            ptx::mbar_init(s_free(s), 4);
+        }
+        ptx::fence_mbar_init();
+        words[1] = 0;
+    }
+    if (warp == kWarps - 1) {
+        ptx::tmem_alloc(sbase + C::kSum + (kBufs - 1) * kKeys * 4, 512);
+        ptx::tmem_relinquish();
+    }
+    // The keys, widened, in the operand's swizzled rows; zeros past the end.
+    constexpr int kU = D / (I8 ? 16 : 8);   // units of 16 bytes of the cache
+    for (int i = tid; i < kKeys * kU; i += kThreads) {
+        const int row = i / kU, u = i % kU, key = key0 + row;
+        const int p = key < end ? page_of(c, b, key) : -1;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (p >= 0) {
+            const size_t at = (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+            w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(c.k) + at * (D * (I8 ? 1 : 2))) + u);
+        }
+        if constexpr (I8) {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = frag::i8_pair(__byte_perm(x[e], 0, 0x4140));
+                o[2 * e + 1] = frag::i8_pair(__byte_perm(x[e], 0, 0x4342));
+            }
+            unsigned char *to = smem + (u >> 2) * (kKeys * 128) + row * 128;
+            const int ch = (u & 3) * 2;
+            *reinterpret_cast<uint4 *>(to + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(to + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(smem + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
+        }
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = words[0];
+
+    const auto wait = [&](uint32_t bar_, uint32_t parity) -> bool {
+        if (ptx::mbar_wait_bounded(bar_, parity, kWaitNs)) return true;
+        words[1] = 1;
+        atomicOr(c.status, kStatusTimeout);
+        return false;
+    };
+    const auto lost = [&] { return words[1] != 0; };
+
+    const int key = key0 + (warp & 3) * 32 + lane;   // a summing thread's
+    float acc = 0.0f;
+    if (warp == kWarps - 1) {
+        // ------------------------------------------------------- MMA issue
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kRowTile >> 3) << 17) | ((kKeys >> 4) << 24);
+        const uint32_t lead = elect_one();
+        const uint64_t d_k = ptx::smem_desc(sbase, 16, 1024, 2), d_q = ptx::smem_desc(sbase + C::kQ, 16, 1024, 2);
+        int issued = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i % kBufs;
+            // (A tile's rows are loaded once its buffer's last scores have been summed up.)
+            if (!__all_sync(~0u, wait(full(s), (i / kBufs) & 1) && !lost())) break;
+            ptx::tc_fence_after();
+            const uint64_t q = d_q + (uint32_t)(s * C::kOperand) / 16;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                const uint32_t off = (x >> 2) * (kKeys * 128 / 16) + (x & 3) * 2;
+                mma_ss(lead, tmem + (uint32_t)(s * kRowTile), d_k + off, q + off, idesc, x > 0);
+            }
+            mma_commit(lead, s_full(s));
+            ++issued;
+        }
+        // Nothing leaves while an MMA reads shared memory.
+        for (int i = max(0, issued - kBufs); i < issued; ++i)
+            if (!ptx::mbar_wait_bounded(s_full(i % kBufs), (i / kBufs) & 1, kWaitNs)) atomicOr(c.status, kStatusTimeout);
+    } else if (warp >= 4 * kBufs) {
+        // ------------------------------------------------------- rows
+        const int t = tid - 4 * kBufs * 32;
+        const auto finish = [&](int i) {   // tile i has landed
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full(i % kBufs));
+        };
+        int loaded = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i % kBufs;
+            const bool ok = wait(s_free(s), (i / kBufs + 1) & 1) && !lost();
+            if (ok && t == 0) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 0;
+            if (ptx::bar_red_or(1, kLoaders * 32, !ok)) break;   // (together, whatever ran out)
+            float *const stat = reinterpret_cast<float *>(smem + C::kStats + s * C::kStat);
+            const int r0 = (first + i) * kRowTile;
+            {   // a row a thread
+                const int r = r0 + t;
+                float2 st = make_float2(0.0f, 0.0f);
+                Seen z = {0, 0};
+                if (r < rs.R) st = __ldg(&L.row_stats[rs.number(L, r)]), z = rs.seen(L, r);
+                // A far row: by itself, from its own loads; here it counts for nothing.
+                const bool far = far_row(st.x);
+                if (far) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 1;
+                stat[t] = far ? 0.0f : st.x;
+                stat[kRowTile + t] = far ? 0.0f : st.y;
+                reinterpret_cast<int *>(stat)[2 * kRowTile + t] = z.lo;
+                reinterpret_cast<int *>(stat)[3 * kRowTile + t] = z.hi;
+            }
+#pragma unroll 4
+            for (int x = 0; x < D / 8; ++x) {
+                const int unit = x * (kLoaders * 32) + t, row = unit / (D / 8), u = unit % (D / 8), r = r0 + row;
+                const bool on = r < rs.R && !far_row(__ldg(&L.row_stats[rs.number(L, r)].x));
+                const __nv_bfloat16 *q = on ? rs.query(L, r, D) + u * 8 : static_cast<const __nv_bfloat16 *>(L.q);
+                ptx::cp_async_16(sbase + C::kQ + s * C::kOperand + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), q, on ? 16 : 0);
+            }
+            ptx::cp_async_commit();
+            ++loaded;
+            if (i > 0) {
+                ptx::cp_async_wait<1>();
+                finish(i - 1);
+            }
+        }
+        ptx::cp_async_wait<0>();
+        if (loaded > 0) finish(loaded - 1);
+    } else {
+        // ------------------------------------------------------- sums
+        const int wg = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const int p = key < end ? page_of(c, b, key) : -1;
+        const size_t at = p < 0 ? 0 : (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+        const float scale = I8 ? (p < 0 ? 0.0f : c.k_scale[at] * L.scale_log2) : L.scale_log2;
+        float2 sums = make_float2(0.0f, 0.0f);
+        for (int i = wg; i < tiles; i += kBufs) {
+            const int r0 = (first + i) * kRowTile, r1 = min(rs.R, r0 + kRowTile);
+            const uint32_t turn = (i / kBufs) & 1;
+            if (!__all_sync(~0u, wait(s_full(wg), turn) && wait(full(wg), turn) && !lost())) break;   // scores; statistics
+            ptx::tc_fence_after();
+            const float *stat = reinterpret_cast<const float *>(smem + C::kStats + wg * C::kStat);
+            const int *lo = reinterpret_cast<const int *>(stat) + 2 * kRowTile, *hi = lo + kRowTile;
+            const bool whole = rs.seen(L, r1 - 1).lo <= key0 && rs.seen(L, r0).hi >= end;   // every row sees every key
+#pragma unroll 1
+            for (int q = 0; q < kRowTile / 16; ++q) {
+                uint32_t v[16];
+                ptx::tmem_ld16(tmem + (uint32_t)(wg * kRowTile) + lanes + 16 * q, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(stat + 16 * q + e), inv = *reinterpret_cast<const float4 *>(stat + kRowTile + 16 * q + e);
+                    float x[4] = {frag::ex2(fmaf(__uint_as_float(v[e]), scale, -m.x)), frag::ex2(fmaf(__uint_as_float(v[e + 1]), scale, -m.y)),
+                                  frag::ex2(fmaf(__uint_as_float(v[e + 2]), scale, -m.z)), frag::ex2(fmaf(__uint_as_float(v[e + 3]), scale, -m.w))};
+                    if (!whole) {
+                        const int4 l4 = *reinterpret_cast<const int4 *>(lo + 16 * q + e), h4 = *reinterpret_cast<const int4 *>(hi + 16 * q + e);
+                        x[0] = key >= l4.x && key < h4.x ? x[0] * inv.x : 0.0f;
+                        x[1] = key >= l4.y && key < h4.y ? x[1] * inv.y : 0.0f;
+                        x[2] = key >= l4.z && key < h4.z ? x[2] * inv.z : 0.0f;
+                        x[3] = key >= l4.w && key < h4.w ? x[3] * inv.w : 0.0f;
+                        sums.x += x[0] + x[2];
+                        sums.y += x[1] + x[3];
+                    } else {
+                        sums.x = fmaf(x[0], inv.x, sums.x);
+                        sums.y = fmaf(x[1], inv.y, sums.y);
+                        sums.x = fmaf(x[2], inv.z, sums.x);
+                        sums.y = fmaf(x[3], inv.w, sums.y);
+                    }
+                }
+            }
+            const bool far = *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * wg) != 0;
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(s_free(wg));
+            if (far) {   // seldom met
+                for (int r = r0; r < r1; ++r) {
+                    const float2 st = __ldg(&L.row_stats[rs.number(L, r)]);
+                    if (!far_row(st.x)) continue;
+                    const Seen z = rs.seen(L, r);
+                    for (int x = 0; x < 32; ++x) {
+                        const int k = __shfl_sync(~0u, key, x), kp = __shfl_sync(~0u, p, x);
+                        const size_t row = (size_t)__shfl_sync(~0u, (unsigned long long)at, x);
+                        if (kp < 0 || k < z.lo || k >= z.hi) continue;
+                        const float w = frag::ex2(slow_score<D, I8>(L, rs, r, row, lane) - st.x) * st.y;
+                        if (lane == x) sums.x += w;
+                    }
+                }
+            }
+        }
+        acc = sums.x + sums.y;
+        if (wg > 0) reinterpret_cast<float *>(smem + C::kSum)[(wg - 1) * kKeys + key - key0] = acc;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kWarps - 1) ptx::tmem_dealloc(tmem, 512);
+    if (warp < 4 && key < end && !lost()) {
+#pragma unroll
+        for (int g = 0; g < kBufs - 1; ++g) acc += reinterpret_cast<const float *>(smem + C::kSum)[g * kKeys + key - key0];
+        const int p = page_of(c, b, key);
+        if (p >= 0) {
+            float *mass = L.mass + (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+            *mass = weight_after(L, rs, key, *mass, acc);
+        }
+    }
+}
+
+template <int D, bool I8>
+cbs_status launch_chunk_weights(const AttnLaunch &L, cudaStream_t s) {
+    static ContextOfDevice set;
+    CBS_TRY(cuda_check(set_max_dyn_smem_once(weights_of_chunk_kernel<D, I8>, Weigh<D>::kSmem, set), "weights' shared memory"));
+    return cuda_check(launch_kernel(weights_of_chunk_kernel<D, I8>, dim3((L.len_pad + kKeys - 1) / kKeys, L.c.kv_heads, L.c.batch), kThreads,
+                                    Weigh<D>::kSmem, s, L), "weights launch");
+}
+
+}  // namespace
+
+cbs_status launch_attn_weights(const AttnLaunch &L, cudaStream_t s) {
+    if (L.scores) {
+        const int keys = kSumThreads * kSumKeys;
+        return cuda_check(launch_kernel(weights_of_scores_kernel, dim3((L.len_pad + keys - 1) / keys, L.c.kv_heads, L.c.batch), kSumThreads, 0, s, L),
+                          "weights launch");
+    }
+    if (L.c.head_dim == 64) return L.c.int8 ? launch_chunk_weights<64, true>(L, s) : launch_chunk_weights<64, false>(L, s);
+    return L.c.int8 ? launch_chunk_weights<128, true>(L, s) : launch_chunk_weights<128, false>(L, s);
+}
+
+}  // namespace cbs

@@ -74,14 +74,6 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint
         else if (t - t0 > limit_ns) return false;
     }
 }
-__device__ __forceinline__ float ld_cluster1(uint32_t addr, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-
 // The instructions whose form names the number of CTAs (one kernel uses one form).
 template <int kPair>
 struct Tc {

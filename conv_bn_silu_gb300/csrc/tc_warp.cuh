@@ -49,7 +49,14 @@ __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Two and four floats of another CTA's shared memory (this CTA's address, that CTA's rank).
+// One, two and four floats of another CTA's shared memory (this CTA's address, that CTA's rank).
+__device__ __forceinline__ float ld_cluster1(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr, uint32_t rank) {
     uint32_t a;
     float2 v;

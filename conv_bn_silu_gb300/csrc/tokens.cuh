@@ -124,6 +124,17 @@ struct AttnLaunch {
     float *partial;             // [batch][kv_heads][row_tiles][split][rows][head_dim], then (max, sum) of each row
     float2 *stats;
     unsigned int *counters;     // [batch][kv_heads][row_tiles]
+    // A shared prefix: batch counts groups in the prefix's part, of `sequences` in all.
+    const int *group_start;     // [groups + 1]
+    int sequences;
+    float *share;               // [total][heads][head_dim], unnormalised, and (max, sum)
+    float2 *share_stats;
+    // A weighed call: (max, 1 / sum) [total][heads]; the ranges' sums as `stats` lie;
+    // scores [batch][kv_heads][rows_pad][len_pad] of the few-row kernels.
+    float2 *row_stats;
+    float *sums, *scores, *mass;
+    int rows_pad, len_pad;
+    float decay;
 };
 // set_max_dyn_smem, once in a context: a call's host time is a small call's whole
 // time.  `done`: the kernel's own, the contexts it was set in.
@@ -142,6 +153,12 @@ cudaError_t set_max_dyn_smem_once(F *kern, int bytes, ContextOfDevice &done) {
 cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
 // Tensor-core kernel: tiles of kAttnChunkRows rows.
 cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);
+// The same in the other modes (either kernel, by the plan's row tile), and the
+// weights of a weighed call's keys.
+cbs_status launch_attn_prefix(const AttnLaunch &L, int row_tile, cudaStream_t s);
+cbs_status launch_attn_own(const AttnLaunch &L, int row_tile, cudaStream_t s);
+cbs_status launch_attn_weighed(const AttnLaunch &L, int row_tile, cudaStream_t s);
+cbs_status launch_attn_weights(const AttnLaunch &L, cudaStream_t s);
 constexpr int kAttnChunkRows = 256, kAttnChunkKeys = 128;
 constexpr int kAttnClusterMost = 8;
 constexpr int kAttnChunkSplitMost = kAttnClusterMost;   // ranges of keys: CTAs of one cluster

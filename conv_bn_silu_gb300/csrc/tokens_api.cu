@@ -114,6 +114,85 @@ size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
 size_t attn_stat_rows(const cbs_attn_plan_t &p) {
     return (size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * p.split * p.row_tile;
 }
+size_t round256(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// A workspace's parts, as offsets.
+struct WeighedParts { size_t row_stats, sums, scores, all; int rows_pad, len_pad; };
+WeighedParts weighed_parts(const cbs_attn_plan_t &p) {
+    const cbs_attn_desc &d = p.desc;
+    WeighedParts w;
+    w.rows_pad = (int)((long long)d.max_new * (d.heads / d.kv_heads));
+    w.len_pad = (int)((d.max_len + 15ll) / 16 * 16);
+    w.row_stats = round256(p.workspace_bytes);
+    w.sums = w.row_stats + round256((size_t)d.batch * d.max_new * d.heads * 8);
+    w.scores = w.sums + (p.workspace_bytes ? round256(attn_stat_rows(p) * 4) : 0);
+    w.all = w.scores + (p.kernel == CBS_ATTN_CHUNK ? 0 : (size_t)d.batch * d.kv_heads * w.rows_pad * w.len_pad * 4);
+    return w;
+}
+struct SharedParts { size_t own, stats, share, all; };
+SharedParts shared_parts(const cbs_shared_plan_t &p) {
+    SharedParts w;
+    w.own = round256(p.prefix.workspace_bytes);
+    w.stats = w.own + round256(p.own.workspace_bytes);
+    w.share = w.stats + round256((size_t)p.max_total * p.desc.heads * 8);
+    w.all = w.share + (size_t)p.max_total * p.desc.heads * p.desc.head_dim * 4;
+    return w;
+}
+
+// What a plan says of a launch.
+void attn_fill(const cbs_attn_plan_t &p, AttnLaunch *L) {
+    const cbs_attn_desc &d = p.desc;
+    L->group = d.heads / d.kv_heads;
+    L->group_magic = L->group > 1 ? (unsigned)(((1ull << 32) + L->group - 1) / L->group) : 0u;
+    L->heads = d.heads; L->causal = d.causal != 0; L->window = d.window; L->max_new = d.max_new;
+    L->split = p.split; L->row_tiles = p.row_tiles;
+    L->cluster = p.kernel == CBS_ATTN_CLUSTER && p.split > 1;
+}
+void attn_workspace(const cbs_attn_plan_t &p, void *workspace, AttnLaunch *L) {
+    if (p.workspace_bytes == 0) return;
+    char *w = static_cast<char *>(workspace);
+    L->counters = reinterpret_cast<unsigned int *>(w);
+    L->stats = reinterpret_cast<float2 *>(w + attn_counter_bytes(p));
+    L->partial = reinterpret_cast<float *>(w + attn_counter_bytes(p) + round256(attn_stat_rows(p) * 8));
+}
+
+// Checks of an attention call and its launch but for the workspace's parts and the
+// status word; *run: there is something to compute.
+cbs_status attn_call(const cbs_attn_plan_t &p, const cbs_cache *c, const cbs_sequences *s, const void *q, long long q_stride, float scale,
+                     void *out, long long out_stride, void *workspace, size_t workspace_bytes, size_t needed, int batch,
+                     cudaStream_t stream, AttnLaunch *L, bool *run) {
+    *run = false;
+    if (p.size != sizeof(cbs_attn_plan_t) || p.abi_version != CBS_ABI_VERSION)
+        return fail(CBS_ERR_PLAN_MISMATCH, "plan of another library version");
+    const cbs_attn_desc &d = p.desc;
+    std::memset(L, 0, sizeof(*L));
+    CBS_TRY(cache_args(c, s, true, &L->c));
+    if (c->prec != d.cache_prec || c->kv_heads != d.kv_heads || c->head_dim != d.head_dim || s->batch != batch)
+        return fail(CBS_ERR_PLAN_MISMATCH, "the plan is for another cache or batch");
+    const long long width = (long long)d.heads * d.head_dim;
+    CBS_TRY(token_stride(q_stride, width, "q_stride"));
+    CBS_TRY(token_stride(out_stride, width, "out_stride"));
+    if (!std::isfinite(scale)) return fail(CBS_ERR_INVALID_ARG, "scale is not finite");
+    if (s->total == 0) return CBS_OK;
+    if (s->batch == 0) {   // all tokens are padding
+        CBS_TRY(need(out, "out"));
+        return cuda_check(cudaMemset2DAsync(out, (size_t)out_stride * 2, 0, (size_t)width * 2, s->total, stream), "zero padding");
+    }
+    if (d.max_new == 0) return fail(CBS_ERR_INVALID_ARG, "%d new tokens for a plan of none", s->total);
+    CBS_TRY(need(q, "q"));
+    CBS_TRY(need(out, "out"));
+    if (needed > 0) {
+        if (!workspace || workspace_bytes < needed)
+            return fail(CBS_ERR_WORKSPACE, "workspace of %zu bytes, %zu required", workspace ? workspace_bytes : (size_t)0, needed);
+        CBS_TRY(need(workspace, "workspace"));
+    }
+    if (rows_overlap(q, q_stride, out, out_stride, width, s->total)) return fail(CBS_ERR_INVALID_ARG, "out lies on q");
+    L->q = q; L->out = out; L->q_stride = q_stride; L->out_stride = out_stride;
+    L->scale_log2 = scale * 1.44269504088896340736f;
+    attn_fill(p, L);
+    *run = true;
+    return CBS_OK;
+}
 
 }  // namespace
 }  // namespace cbs
@@ -289,50 +368,123 @@ cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, con
                                long long q_stride, float scale, void *out, long long out_stride, void *workspace,
                                size_t workspace_bytes, void *stream) {
     if (!p) return fail(CBS_ERR_INVALID_ARG, "plan is NULL");
-    if (p->size != sizeof(cbs_attn_plan_t) || p->abi_version != CBS_ABI_VERSION)
-        return fail(CBS_ERR_PLAN_MISMATCH, "plan of another library version");
-    const cbs_attn_desc &d = p->desc;
     AttnLaunch L;
-    std::memset(&L, 0, sizeof(L));
-    CBS_TRY(cache_args(c, s, true, &L.c));
-    if (c->prec != d.cache_prec || c->kv_heads != d.kv_heads || c->head_dim != d.head_dim || s->batch != d.batch)
-        return fail(CBS_ERR_PLAN_MISMATCH, "the plan is for another cache or batch");
-    const long long width = (long long)d.heads * d.head_dim;
-    CBS_TRY(token_stride(q_stride, width, "q_stride"));
-    CBS_TRY(token_stride(out_stride, width, "out_stride"));
-    if (!std::isfinite(scale)) return fail(CBS_ERR_INVALID_ARG, "scale is not finite");
-    if (s->total == 0) return CBS_OK;
-    if (s->batch == 0) {   // all tokens are padding
-        CBS_TRY(need(out, "out"));
-        return cuda_check(cudaMemset2DAsync(out, (size_t)out_stride * 2, 0, (size_t)width * 2, s->total, (cudaStream_t)stream),
-                          "zero padding");
-    }
-    if (d.max_new == 0) return fail(CBS_ERR_INVALID_ARG, "%d new tokens for a plan of none", s->total);
-    CBS_TRY(need(q, "q"));
-    CBS_TRY(need(out, "out"));
-    if (p->workspace_bytes > 0) {
-        if (!workspace || workspace_bytes < p->workspace_bytes)
-            return fail(CBS_ERR_WORKSPACE, "workspace of %zu bytes, %zu required", workspace ? workspace_bytes : (size_t)0,
-                        p->workspace_bytes);
-        CBS_TRY(need(workspace, "workspace"));
-    }
-    if (rows_overlap(q, q_stride, out, out_stride, width, s->total)) return fail(CBS_ERR_INVALID_ARG, "out lies on q");
+    bool run;
+    CBS_TRY(attn_call(*p, c, s, q, q_stride, scale, out, out_stride, workspace, workspace_bytes, p->workspace_bytes, p->desc.batch,
+                      (cudaStream_t)stream, &L, &run));
+    if (!run) return CBS_OK;
     CBS_TRY(status_word(&L.c));
-    L.q = q; L.out = out; L.q_stride = q_stride; L.out_stride = out_stride;
-    L.scale_log2 = scale * 1.44269504088896340736f;
-    L.group = d.heads / d.kv_heads;
-    L.group_magic = L.group > 1 ? (unsigned)(((1ull << 32) + L.group - 1) / L.group) : 0u;
-    L.heads = d.heads; L.causal = d.causal != 0; L.window = d.window; L.max_new = d.max_new;
-    L.split = p->split; L.row_tiles = p->row_tiles;
-    L.cluster = p->kernel == CBS_ATTN_CLUSTER && p->split > 1;
-    if (p->workspace_bytes > 0) {
-        char *w = static_cast<char *>(workspace);
-        L.counters = reinterpret_cast<unsigned int *>(w);
-        L.stats = reinterpret_cast<float2 *>(w + attn_counter_bytes(*p));
-        L.partial = reinterpret_cast<float *>(w + attn_counter_bytes(*p) + (attn_stat_rows(*p) * 8 + 255) / 256 * 256);
-    }
+    attn_workspace(*p, workspace, &L);
     if (p->kernel == CBS_ATTN_CHUNK) return launch_attn_chunk(L, (cudaStream_t)stream);
     return cuda_check(launch_attn_rows(L, p->row_tile, (cudaStream_t)stream), "attention launch");
+}
+
+cbs_status cbs_weighed_plan(const cbs_attn_desc *d, cbs_weighed_plan_t *out) {
+    if (!d || !out) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", d ? "out" : "desc");
+    cbs_weighed_plan_t p;
+    std::memset(&p, 0, sizeof(p));
+    p.size = sizeof(p);
+    p.abi_version = CBS_ABI_VERSION;
+    CBS_TRY(cbs_attn_plan(d, &p.attention));
+    if ((d->max_len + 15ll) / 16 * 16 > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "max_len %d", d->max_len);
+    p.workspace_bytes = weighed_parts(p.attention).all;
+    *out = p;
+    return CBS_OK;
+}
+
+cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c, const cbs_sequences *s, const void *q,
+                                 long long q_stride, float scale, void *out, long long out_stride, float *mass, float decay,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!p) return fail(CBS_ERR_INVALID_ARG, "plan is NULL");
+    if (p->size != sizeof(*p) || p->abi_version != CBS_ABI_VERSION)
+        return fail(CBS_ERR_PLAN_MISMATCH, "plan of another library version");
+    const cbs_attn_plan_t &a = p->attention;
+    if (!std::isfinite(decay)) return fail(CBS_ERR_INVALID_ARG, "decay is not finite");
+    AttnLaunch L;
+    bool run;
+    CBS_TRY(attn_call(a, c, s, q, q_stride, scale, out, out_stride, workspace, workspace_bytes, p->workspace_bytes, a.desc.batch,
+                      (cudaStream_t)stream, &L, &run));
+    if (!run) return CBS_OK;
+    CBS_TRY(need(mass, "mass"));
+    if (s->total > (long long)a.desc.batch * a.desc.max_new)
+        return fail(CBS_ERR_INVALID_ARG, "%d tokens for a plan of %d sequences of %d", s->total, a.desc.batch, a.desc.max_new);
+    const size_t rows = (size_t)c->num_pages * c->kv_heads * c->page_size, row = (size_t)c->head_dim * (c->prec == CBS_INT8 ? 1 : 2);
+    const long long width = (long long)a.desc.heads * c->head_dim;
+    const struct { const void *p; size_t bytes; const char *what; } others[] = {
+        {c->k, rows * row, "k"}, {c->v, rows * row, "v"}, {c->k_scale, rows * 4, "k_scale"}, {c->v_scale, rows * 4, "v_scale"},
+        {q, (size_t)((s->total - 1) * q_stride + width) * 2, "q"}, {out, (size_t)((s->total - 1) * out_stride + width) * 2, "out"},
+        {workspace, p->workspace_bytes, "workspace"}};
+    for (const auto &o : others)
+        if (overlap(mass, rows * 4, o.p, o.bytes)) return fail(CBS_ERR_INVALID_ARG, "mass lies on %s", o.what);
+    CBS_TRY(status_word(&L.c));
+    attn_workspace(a, workspace, &L);
+    const WeighedParts w = weighed_parts(a);
+    char *at = static_cast<char *>(workspace);
+    L.row_stats = reinterpret_cast<float2 *>(at + w.row_stats);
+    L.sums = reinterpret_cast<float *>(at + w.sums);
+    L.len_pad = w.len_pad;
+    L.rows_pad = w.rows_pad;
+    if (a.kernel != CBS_ATTN_CHUNK) L.scores = reinterpret_cast<float *>(at + w.scores);
+    L.mass = mass;
+    L.decay = decay;
+    CBS_TRY(launch_attn_weighed(L, a.row_tile, (cudaStream_t)stream));
+    return launch_attn_weights(L, (cudaStream_t)stream);
+}
+
+cbs_status cbs_shared_plan(const cbs_shared_desc *d, cbs_shared_plan_t *out) {
+    if (!d || !out) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", d ? "out" : "desc");
+    if (d->groups < 0 || d->max_group_new < 0 || d->max_prefix < 0)
+        return fail(CBS_ERR_INVALID_ARG, "bad groups (%d, of %d new tokens, prefixes of %d)", d->groups, d->max_group_new, d->max_prefix);
+    cbs_shared_plan_t p;
+    std::memset(&p, 0, sizeof(p));
+    p.size = sizeof(p);
+    p.abi_version = CBS_ABI_VERSION;
+    p.desc = *d;
+    cbs_attn_desc part = {d->batch, d->max_new, d->max_len, d->heads, d->kv_heads, d->head_dim, d->cache_prec, 1, 0, d->num_sms, -1, 0};
+    CBS_TRY(cbs_attn_plan(&part, &p.own));
+    part.batch = d->groups; part.max_new = d->max_group_new; part.max_len = d->max_prefix; part.causal = 0;
+    CBS_TRY(cbs_attn_plan(&part, &p.prefix));
+    const long long total = std::min((long long)d->batch * d->max_new, (long long)d->groups * d->max_group_new);
+    if (total > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld new tokens", total);
+    p.max_total = (int)total;
+    const SharedParts parts = shared_parts(p);
+    p.zeroed_bytes = parts.stats;
+    p.workspace_bytes = parts.all;
+    *out = p;
+    return CBS_OK;
+}
+
+cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, const cbs_sequences *s, const cbs_prefixes *prefixes,
+                                const void *q, long long q_stride, float scale, void *out, long long out_stride, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    if (!p || !prefixes) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", p ? "prefixes" : "plan");
+    if (p->size != sizeof(*p) || p->abi_version != CBS_ABI_VERSION)
+        return fail(CBS_ERR_PLAN_MISMATCH, "plan of another library version");
+    if (prefixes->groups != p->desc.groups) return fail(CBS_ERR_PLAN_MISMATCH, "the plan is for %d groups", p->desc.groups);
+    AttnLaunch own;
+    bool run;
+    CBS_TRY(attn_call(p->own, c, s, q, q_stride, scale, out, out_stride, workspace, workspace_bytes, p->workspace_bytes, p->desc.batch,
+                      (cudaStream_t)stream, &own, &run));
+    if (!run) return CBS_OK;
+    if (s->total > p->max_total) return fail(CBS_ERR_INVALID_ARG, "%d tokens for a plan of %d", s->total, p->max_total);
+    cbs_sequences ps = {s->new_start, prefixes->prefix_lens, prefixes->page_table, prefixes->groups, prefixes->max_pages, s->total};
+    AttnLaunch pre = own;
+    CBS_TRY(cache_args(c, &ps, true, &pre.c));
+    if (!prefixes->group_start) return fail(CBS_ERR_INVALID_ARG, "group_start is NULL");
+    if (reinterpret_cast<uintptr_t>(prefixes->group_start) & 3u) return fail(CBS_ERR_MISALIGNED, "group_start is not 4-byte aligned");
+    CBS_TRY(status_word(&own.c));
+    pre.c.status = own.c.status;
+    const SharedParts parts = shared_parts(*p);
+    char *at = static_cast<char *>(workspace);
+    attn_fill(p->prefix, &pre);
+    attn_workspace(p->prefix, at, &pre);
+    attn_workspace(p->own, at + parts.own, &own);
+    pre.group_start = prefixes->group_start;
+    pre.sequences = s->batch;
+    pre.share_stats = own.share_stats = reinterpret_cast<float2 *>(at + parts.stats);
+    pre.share = own.share = reinterpret_cast<float *>(at + parts.share);
+    CBS_TRY(launch_attn_prefix(pre, p->prefix.row_tile, (cudaStream_t)stream));
+    return launch_attn_own(own, p->own.row_tile, (cudaStream_t)stream);
 }
 
 cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight, void *h_out, void *y, float *scale,

@@ -257,38 +257,103 @@ PyObject *cache_evict(PyObject *const *a) {
     return s != CBS_OK ? status(s) : triple(THPVariable_Wrap(kept), THPVariable_Wrap(lens), none());
 }
 
+// What the attention calls share: q and out, the sequences, the workspace.
+struct Attention {
+    const Tensor *q;
+    Tensor out;
+    int64_t q_stride, out_stride;
+    double scale;
+    cbs_sequences seqs;
+    // The arguments that follow (cache, device, q, new_start, seq_lens, page_table, scale, out).
+    // (`more`: checks that come before an address is taken.)
+    template <typename More>
+    Attention(PyObject *const *a, int heads, More more) {
+        const auto *c = static_cast<const cbs_cache *>(pointer(a[0]));
+        const int d = c->head_dim;
+        q = &tensor(a[2], "q");
+        at_home(*q, "q", a[1]);
+        q_stride = token_stride(*q, "q", ScalarType::BFloat16, heads, d);
+        scale = PyFloat_AsDouble(a[6]);
+        if (PyErr_Occurred()) throw Refused{};
+        out_stride = (int64_t)heads * d;
+        if (a[7] != Py_None) {
+            out = tensor(a[7], "out", q);
+            out_stride = token_stride(out, "out", ScalarType::BFloat16, heads, d);
+            if (out.size(0) != q->size(0)) refuse("out", "expected the tokens of q");
+        }
+        more(*c);
+        seqs = sequences(a[3], a[4], a[5], q->size(0), q);
+    }
+    void make_out(int heads, int d) {
+        if (!out.defined()) out = empty({q->size(0), heads, d}, ScalarType::BFloat16, *q);
+    }
+    PyObject *result(PyObject *given, cbs_status s) const {
+        if (s != CBS_OK) return status(s);
+        return given != Py_None ? Py_NewRef(given) : THPVariable_Wrap(out);
+    }
+};
+// A workspace's address.  Used on another stream than its own, its memory is not
+// given away before the call has ended.
+void *workspace_of(PyObject *o, PyObject *its_stream, const Tensor &like, const c10::cuda::CUDAStream &stream) {
+    if (o == Py_None) return nullptr;
+    const Tensor &w = tensor(o, "workspace", &like);
+    if (stream.stream() != pointer(its_stream)) c10::cuda::CUDACachingAllocator::recordStream(w.storage().data_ptr(), stream);
+    return w.data_ptr();
+}
+
 // attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace, its stream) -> out
 PyObject *attention(PyObject *const *a) {
     const auto *p = static_cast<const cbs_attn_plan_t *>(pointer(a[0]));
-    const auto *c = static_cast<const cbs_cache *>(pointer(a[1]));
-    const int heads = p->desc.heads, d = c->head_dim;
-    const Tensor &q = tensor(a[3], "q");
-    at_home(q, "q", a[2]);
-    const int64_t qs = token_stride(q, "q", ScalarType::BFloat16, heads, d);
-    const double scale = PyFloat_AsDouble(a[7]);
+    const int heads = p->desc.heads;
+    Attention t(a + 1, heads, [](const cbs_cache &) {});
+    const c10::cuda::CUDAGuard guard(t.q->device());
+    t.make_out(heads, p->desc.head_dim);
+    const auto stream = c10::cuda::getCurrentCUDAStream(t.q->get_device());
+    void *workspace = workspace_of(a[9], a[10], *t.q, stream);
+    return t.result(a[8], cbs_paged_attention(p, static_cast<const cbs_cache *>(pointer(a[1])), &t.seqs, t.q->data_ptr(), t.q_stride,
+                                              (float)t.scale, t.out.data_ptr(), t.out_stride, workspace, p->workspace_bytes, stream.stream()));
+}
+
+// weighed_attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace, its stream, mass, decay) -> out
+PyObject *weighed_attention(PyObject *const *a) {
+    const auto *p = static_cast<const cbs_weighed_plan_t *>(pointer(a[0]));
+    const int heads = p->attention.desc.heads;
+    const double decay = PyFloat_AsDouble(a[12]);
     if (PyErr_Occurred()) throw Refused{};
-    Tensor out;
-    int64_t os = (int64_t)heads * d;
-    if (a[8] != Py_None) {
-        out = tensor(a[8], "out", &q);
-        os = token_stride(out, "out", ScalarType::BFloat16, heads, d);
-        if (out.size(0) != q.size(0)) refuse("out", "expected the tokens of q");
-    }
-    const cbs_sequences seqs = sequences(a[4], a[5], a[6], q.size(0), &q);
-    const c10::cuda::CUDAGuard guard(q.device());
-    if (!out.defined()) out = empty({q.size(0), heads, d}, ScalarType::BFloat16, q);
-    const auto stream = c10::cuda::getCurrentCUDAStream(q.get_device());
-    void *workspace = nullptr;
-    if (a[9] != Py_None) {
-        const Tensor &w = tensor(a[9], "workspace", &q);
-        workspace = w.data_ptr();
-        // Used on another stream than its own: its memory is not given away before this call has ended.
-        if (stream.stream() != pointer(a[10])) c10::cuda::CUDACachingAllocator::recordStream(w.storage().data_ptr(), stream);
-    }
-    const cbs_status s = cbs_paged_attention(p, c, &seqs, q.data_ptr(), qs, (float)scale, out.data_ptr(), os, workspace,
-                                             p->workspace_bytes, stream.stream());
-    if (s != CBS_OK) return status(s);
-    return a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(out);
+    const Tensor *mass = nullptr;
+    Attention t(a + 1, heads, [&](const cbs_cache &c) {
+        mass = &dense(a[11], "mass", &tensor(a[3], "q"), ScalarType::Float, {c.num_pages, c.kv_heads, c.page_size});
+    });
+    const c10::cuda::CUDAGuard guard(t.q->device());
+    t.make_out(heads, p->attention.desc.head_dim);
+    const auto stream = c10::cuda::getCurrentCUDAStream(t.q->get_device());
+    void *workspace = workspace_of(a[9], a[10], *t.q, stream);
+    return t.result(a[8], cbs_weighed_attention(p, static_cast<const cbs_cache *>(pointer(a[1])), &t.seqs, t.q->data_ptr(), t.q_stride,
+                                                (float)t.scale, t.out.data_ptr(), t.out_stride, mass->data_ptr<float>(), (float)decay,
+                                                workspace, p->workspace_bytes, stream.stream()));
+}
+
+// shared_attention(plan, cache, device, q, new_start, seq_lens, page_table, scale, out, workspace, its stream, group_start,
+// prefix_lens, prefix_table) -> out
+PyObject *shared_attention(PyObject *const *a) {
+    const auto *p = static_cast<const cbs_shared_plan_t *>(pointer(a[0]));
+    const int heads = p->desc.heads;
+    const Tensor *starts = nullptr, *lens = nullptr, *table = nullptr;
+    Attention t(a + 1, heads, [&](const cbs_cache &) {
+        const Tensor &q = tensor(a[3], "q");
+        table = &dense(a[13], "prefix_table", &q, ScalarType::Int, {-1, -1});
+        lens = &dense(a[12], "prefix_lens", &q, ScalarType::Int, {table->size(0)});
+        starts = &dense(a[11], "group_start", &q, ScalarType::Int, {table->size(0) + 1});
+    });
+    const cbs_prefixes prefixes = {starts->data_ptr<int>(), lens->data_ptr<int>(), table->data_ptr<int>(), (int)table->size(0),
+                                   (int)table->size(1)};
+    const c10::cuda::CUDAGuard guard(t.q->device());
+    t.make_out(heads, p->desc.head_dim);
+    const auto stream = c10::cuda::getCurrentCUDAStream(t.q->get_device());
+    void *workspace = workspace_of(a[9], a[10], *t.q, stream);
+    return t.result(a[8], cbs_shared_attention(p, static_cast<const cbs_cache *>(pointer(a[1])), &t.seqs, &prefixes, t.q->data_ptr(),
+                                               t.q_stride, (float)t.scale, t.out.data_ptr(), t.out_stride, workspace, p->workspace_bytes,
+                                               stream.stream()));
 }
 
 template <PyObject *(*F)(PyObject *const *), int N>
@@ -310,7 +375,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define CBS_PY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CBS_PY(rmsnorm, 6),     CBS_PY(dequantize_rows, 3), CBS_PY(linear_w4, 13), CBS_PY(cache_write, 7),
                          CBS_PY(cache_read, 6), CBS_PY(attention, 11),       CBS_PY(cache_evict, 8),
-                         CBS_PY(linear_w8, 11),  {nullptr, nullptr, 0, nullptr}};
+                         CBS_PY(linear_w8, 11),  CBS_PY(weighed_attention, 13), CBS_PY(shared_attention, 14), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", "The token operators' calls (see tokens.py).", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

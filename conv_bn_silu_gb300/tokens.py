@@ -250,21 +250,24 @@ class PagedAttention:
         self._make_workspace()
 
     def _make_workspace(self):
-        self.workspace_bytes = int(self.plan.workspace_bytes)
+        self.workspace_bytes, zeroed = int(self.plan.workspace_bytes), self._zeroed_bytes()
         self.workspace, self._stream = None, 0
         if self.workspace_bytes:
             with torch.cuda.device(self.cache.k.device):
                 self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device="cuda")
                 self._stream = current_stream()
-                B.cbs_workspace_init(self.workspace, self.workspace_bytes, self._stream)
+                B.cbs_workspace_init(self.workspace, zeroed, self._stream)
                 # Zeroed before anyone can use it on another stream.  (Within a capture
                 # the zeroing is part of the graph, and what follows it is ordered.)
                 if not torch.cuda.is_current_stream_capturing():
                     torch.cuda.current_stream().synchronize()
 
-    def fork(self) -> "PagedAttention":
+    def _zeroed_bytes(self) -> int:
+        return int(self.plan.workspace_bytes)
+
+    def fork(self):
         """The same plan and cache with a workspace of its own."""
-        twin = object.__new__(PagedAttention)
+        twin = object.__new__(type(self))
         twin.__dict__.update(self.__dict__)
         twin._make_workspace()
         return twin
@@ -275,3 +278,65 @@ class PagedAttention:
         rows does).  The cache already holds the new tokens."""
         return _done(_calls().attention(self._plan_at, *self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
                                         self.workspace, self._stream), "cbs_paged_attention")
+
+
+class WeighedAttention(PagedAttention):
+    """PagedAttention that also adds up the weight each position of the cache
+    receives, for PagedCache.evict.  Lengths are at most max_len."""
+
+    def __init__(self, cache: PagedCache, batch: int, max_new: int, max_len: int, heads: int, causal: bool = True,
+                 window: int = 0, scale: float | None = None, force_kernel: int = -1, force_split: int = 0):
+        self.cache, self.heads = cache, heads
+        self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        with torch.cuda.device(cache.k.device):
+            sms = device_sms()
+        self.plan = B.cbs_weighed_plan(B.cbs_attn_desc(batch, max_new, max_len, heads, cache.kv_heads, cache.head_dim, cache.prec,
+                                                       int(causal), window, sms, force_kernel, force_split))
+        self._plan_at = ctypes.addressof(self.plan)
+        self._make_workspace()
+
+    def _zeroed_bytes(self) -> int:
+        return int(self.plan.attention.workspace_bytes)
+
+    def __call__(self, q: torch.Tensor, new_start: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor,
+                 mass: torch.Tensor, decay: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+        """As PagedAttention, and mass (float32 [num_pages, kv_heads, page_size])
+        becomes decay * mass plus the softmax weights that the call's tokens gave each
+        position, summed over the query heads of its key head; positions that are new
+        in the call count from zero."""
+        return _done(_calls().weighed_attention(self._plan_at, *self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
+                                                self.workspace, self._stream, mass, decay), "cbs_weighed_attention")
+
+
+class SharedPrefixAttention(PagedAttention):
+    """Attention of sequences that go on from prefixes which groups of them share
+    (several answers about one image, streams with one instruction): a prefix's
+    keys and values are read once for its group.  Workspaces and `fork` as
+    PagedAttention's."""
+
+    def __init__(self, cache: PagedCache, batch: int, groups: int, max_new: int, max_len: int, max_prefix: int, heads: int,
+                 max_group_new: int | None = None, scale: float | None = None):
+        self.cache, self.heads = cache, heads
+        self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        with torch.cuda.device(cache.k.device):
+            sms = device_sms()
+        if max_group_new is None:
+            max_group_new = batch * max_new
+        self.plan = B.cbs_shared_plan(B.cbs_shared_desc(batch, groups, max_new, max_group_new, max_len, max_prefix, heads,
+                                                        cache.kv_heads, cache.head_dim, cache.prec, sms))
+        self._plan_at = ctypes.addressof(self.plan)
+        self._make_workspace()
+
+    def _zeroed_bytes(self) -> int:
+        return int(self.plan.zeroed_bytes)
+
+    def __call__(self, q: torch.Tensor, new_start: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor,
+                 group_start: torch.Tensor, prefix_lens: torch.Tensor, prefix_table: torch.Tensor,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+        """q: bfloat16 [tokens, heads, head_dim].  Sequences group_start[g] to
+        group_start[g + 1] - 1 share prefix_lens[g] positions in prefix_table[g]'s
+        pages; seq_lens and page_table are their own, behind it.  A new token sees its
+        whole prefix, and its own sequence up to itself."""
+        return _done(_calls().shared_attention(self._plan_at, *self.cache._at, q, new_start, seq_lens, page_table, self.scale, out,
+                                               self.workspace, self._stream, group_start, prefix_lens, prefix_table),
+                     "cbs_shared_attention")

@@ -580,6 +580,77 @@ CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache
                                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * cbs_weighed_plan, cbs_weighed_attention -- cbs_paged_attention that also adds up
+ * the weight each position receives, for cbs_cache_evict: with p as above over the
+ * call's new tokens t and the query heads h that read key head g,
+ *   mass[g, j] = decay * mass[g, j] + sum_t sum_h p_j / sum_i p_i
+ * over all positions j of the sequences that have new tokens; a position that is
+ * new in the call counts from zero, and with decay 0 every one does (what mass
+ * held is then not read).  Positions that nobody sees receive nothing; other
+ * sequences' pages are left as they are.
+ *   mass: float [num_pages][kv_heads][page_size].  No page may belong to two of
+ *     the call's sequences (they would overwrite each other's weights).
+ *   decay: finite.  out: as cbs_paged_attention's, the same bits.
+ * A sequence longer than the plan's max_len is reported, and its positions past
+ * that (rounded up to 16) get no weight.  total is at most batch * max_new.  Sums
+ * are in 32 bits; equal calls give equal results.  workspace: workspace_bytes, of
+ * which the first attention.workspace_bytes are zeroed once (cbs_workspace_init).
+ */
+typedef struct cbs_weighed_plan_t {
+    uint32_t size, abi_version;
+    cbs_attn_plan_t attention;
+    size_t workspace_bytes;
+} cbs_weighed_plan_t;
+CBS_API cbs_status cbs_weighed_plan(const cbs_attn_desc *d, cbs_weighed_plan_t *out);
+CBS_API cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c, const cbs_sequences *s,
+                                         const void *q, long long q_stride, float scale, void *out, long long out_stride,
+                                         float *mass, float decay, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Prefixes that groups of a call's sequences share (device arrays).  Group g is
+ * sequences group_start[g] .. group_start[g + 1] - 1; what they share is
+ * prefix_lens[g] positions, position p in slot p % page_size of page
+ * page_table[g * max_pages + p / page_size]. */
+typedef struct cbs_prefixes {
+    const int32_t *group_start;  /* [groups + 1], from 0, not decreasing, to the call's batch */
+    const int32_t *prefix_lens;  /* [groups]; 0 is fine */
+    const int32_t *page_table;   /* [groups][max_pages] */
+    int groups, max_pages;
+} cbs_prefixes;
+
+/* One kind of call over shared prefixes.  max_len, max_prefix: the longest
+ * expected, as cbs_attn_desc's; max_new and max_group_new: the most new tokens of a
+ * sequence and of a group's sequences together. */
+typedef struct cbs_shared_desc {
+    int batch, groups, max_new, max_group_new, max_len, max_prefix;
+    int heads, kv_heads, head_dim, cache_prec;
+    int num_sms;       /* 0 = 152 */
+} cbs_shared_desc;
+
+typedef struct cbs_shared_plan_t {
+    uint32_t size, abi_version;
+    cbs_attn_plan_t prefix, own;
+    int max_total;            /* new tokens of a call at most */
+    size_t zeroed_bytes;      /* of the workspace, once, with cbs_workspace_init */
+    size_t workspace_bytes;
+    cbs_shared_desc desc;
+} cbs_shared_plan_t;
+
+/*
+ * cbs_shared_plan, cbs_shared_attention -- cbs_paged_attention of sequences that
+ * go on from shared prefixes, whose keys and values are read once a group: a new
+ * token sees its group's whole prefix and of its sequence's own positions
+ * (seq_lens and page_table of cbs_sequences: without the prefix) those up to its
+ * own.  The cache holds both.  total is at most the plan's max_total, the lesser of
+ * batch * max_new and groups * max_group_new.  A token that sees nothing gets zeros.
+ * A value out of range in the groups is reported, and outputs are then unspecified.
+ */
+CBS_API cbs_status cbs_shared_plan(const cbs_shared_desc *d, cbs_shared_plan_t *out);
+CBS_API cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, const cbs_sequences *s,
+                                        const cbs_prefixes *prefixes, const void *q, long long q_stride, float scale,
+                                        void *out, long long out_stride, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/*
  * cbs_rmsnorm -- RMS normalisation with the residual's addition:
  *   h = x + residual,   y = h * weight / sqrt(mean(h^2) + eps)   per row
  * x, residual (NULL: h = x), h_out: [rows][cols] of in_prec (CBS_FP32 or
