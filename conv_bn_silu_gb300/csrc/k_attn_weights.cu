@@ -217,34 +217,37 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(full(i % kBufs));
         };
+        // A row a thread: what the attention left of it, a tile ahead.
+        const auto statistics = [&](int i) -> float2 {
+            const int r = (first + i) * kRowTile + t;
+            return i < tiles && r < rs.R ? __ldg(&L.row_stats[rs.number(L, r)]) : make_float2(0.0f, 0.0f);
+        };
+        float2 next = statistics(0);
         int loaded = 0;
         for (int i = 0; i < tiles; ++i) {
             const int s = i % kBufs;
+            const float2 st = next;
+            next = statistics(i + 1);
             const bool ok = wait(s_free(s), (i / kBufs + 1) & 1) && !lost();
             if (ok && t == 0) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 0;
             if (ptx::bar_red_or(1, kLoaders * 32, !ok)) break;   // (together, whatever ran out)
             float *const stat = reinterpret_cast<float *>(smem + C::kStats + s * C::kStat);
             const int r0 = (first + i) * kRowTile;
-            {   // a row a thread
-                const int r = r0 + t;
-                float2 st = make_float2(0.0f, 0.0f);
-                Seen z = {0, 0};
-                if (r < rs.R) st = __ldg(&L.row_stats[rs.number(L, r)]), z = rs.seen(L, r);
-                // A far row: by itself, from its own loads; here it counts for nothing.
-                const bool far = far_row(st.x);
-                if (far) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 1;
-                stat[t] = far ? 0.0f : st.x;
-                stat[kRowTile + t] = far ? 0.0f : st.y;
-                reinterpret_cast<int *>(stat)[2 * kRowTile + t] = z.lo;
-                reinterpret_cast<int *>(stat)[3 * kRowTile + t] = z.hi;
-            }
-#pragma unroll 4
+#pragma unroll
             for (int x = 0; x < D / 8; ++x) {
                 const int unit = x * (kLoaders * 32) + t, row = unit / (D / 8), u = unit % (D / 8), r = r0 + row;
-                const bool on = r < rs.R && !far_row(__ldg(&L.row_stats[rs.number(L, r)].x));
-                const __nv_bfloat16 *q = on ? rs.query(L, r, D) + u * 8 : static_cast<const __nv_bfloat16 *>(L.q);
-                ptx::cp_async_16(sbase + C::kQ + s * C::kOperand + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4), q, on ? 16 : 0);
+                const bool on = r < rs.R;
+                ptx::cp_async_16(sbase + C::kQ + s * C::kOperand + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                                 on ? rs.query(L, r, D) + u * 8 : static_cast<const __nv_bfloat16 *>(L.q), on ? 16 : 0);
             }
+            // A far row: by itself, from its own loads; here every exponential of it is zero.
+            const bool far = far_row(st.x);
+            if (far) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 1;
+            const Seen z = r0 + t < rs.R ? rs.seen(L, r0 + t) : Seen{0, 0};
+            stat[t] = far ? INFINITY : st.x;
+            stat[kRowTile + t] = far ? 0.0f : st.y;
+            reinterpret_cast<int *>(stat)[2 * kRowTile + t] = z.lo;
+            reinterpret_cast<int *>(stat)[3 * kRowTile + t] = z.hi;
             ptx::cp_async_commit();
             ++loaded;
             if (i > 0) {

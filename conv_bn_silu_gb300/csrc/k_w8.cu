@@ -17,6 +17,8 @@
 //
 // For few rows the weights' bytes bound it.  Shares of k are then CTAs of a cluster,
 // which add their sums in order through distributed shared memory.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "mma_frag.cuh"
@@ -41,24 +43,36 @@ struct W8Tile {
     static constexpr int kOp = kRows * 256;                  // a stage of B: two panels of 64
     static constexpr int kStages = kN == 16 ? 5 : kN == 32 ? 4 : kN == 64 ? 3 : 4;
     static constexpr int kOps = kN <= 64 ? 2 : 3;
-    static constexpr int kWiden = kRows >= 128 ? 8 : kRows / 16;   // warps that widen inputs
+    // Warps that widen inputs, and the groups of them that take stages in turn: a
+    // group then has two stages' time for its loads, stores and fence.
+    static constexpr int kWiden = kRows >= 128 ? 8 : kRows / 16, kTurns = kRows >= 128 ? 2 : 1;
+    static constexpr int kStoreWarps = kWiden >= 8 ? 16 : 8;   // at the end: each has 32 outputs of its part of the rows
     static constexpr int kWarpMma = 8 + kWiden, kWarpTma = kWarpMma + 1, kThreads = (kWarpTma + 1) * 32;
     static constexpr int kOpAt = kStages * kRaw, kBars = kOpAt + kOps * kOp;
-    // raw_full[], raw_empty[], b_ready[], b_free[], a_ready[2], a_free[2], done; TMEM address, flag
-    static constexpr int kNumBars = 2 * kStages + 2 * kOps + 5;
-    static constexpr int kSmem = kBars + kNumBars * 8 + 16;
-    static constexpr int kACols = kStageK / 2, kTmem = 2 * kACols + kN <= 256 ? 256 : 512;
-    static_assert(2 * kACols + kN <= 512 && kRaw % 1024 == 0 && kOp % 1024 == 0, "tensor memory; operands at multiples of 1 KB");
+    // Places of A in tensor memory, a stage each: from a place's MMA back to its next one
+    // takes some 2500 cycles of hand-offs, so as many as fit.
+    static constexpr int kABufs = kN >= 128 ? 4 : 2, kACols = kStageK / 2;
+    static constexpr int kTmem = kABufs * kACols + kN <= 256 ? 256 : 512;
+    // raw_full[], raw_empty[], b_ready[], b_free[], peer[], a_ready[], a_free[], done;
+    // TMEM address, flag; the input rows' scales
+    static constexpr int kNumBars = 2 * kStages + 3 * kOps + 2 * kABufs + 1;
+    static constexpr int kScales = kBars + kNumBars * 8 + 16, kSmem = kScales + kN * 4;
+    static_assert(kABufs * kACols + kN <= 512 && kScales % 8 == 0 && kRaw % 1024 == 0 && kOp % 1024 == 0, "tensor memory; operands at multiples of 1 KB");
     static_assert(kSmem <= kMaxDynSmem, "shared memory");
     static_assert(kPair == 2 || kN * (kOut + 1) * 4 <= kBars, "a share's sums fit where the stages were");
 };
 
-__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {   // another CTA's barrier (or this one's)
+// Another CTA's barrier.  What this announces lies in the sender's own shared and
+// tensor memory, where its writers' fences have made it visible to the MMA's reads
+// before they arrived here; no thread of the other CTA reads it.  So nothing is
+// released in the cluster's scope, which took the sender some 1700 cycles a stage (256
+// rows of 8192 x 8192: 62.6 us, and 43.7 without).
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(bar), "r"(rank));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
-// As mbar_wait_bounded, for arrivals from both CTAs of a pair.
+// As mbar_wait_bounded, for the arrival of the pair's other CTA.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     while (true) {
@@ -133,23 +147,25 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     const auto raw_empty = [&](int s) { return bar(C::kStages + s); };
     const auto b_ready = [&](int s) { return bar(2 * C::kStages + s); };
     const auto b_free = [&](int s) { return bar(2 * C::kStages + C::kOps + s); };
-    const auto a_ready = [&](int w) { return bar(2 * C::kStages + 2 * C::kOps + w); };
-    const auto a_free = [&](int w) { return bar(2 * C::kStages + 2 * C::kOps + 2 + w); };
-    const uint32_t done = bar(2 * C::kStages + 2 * C::kOps + 4);
+    const auto peer = [&](int s) { return bar(2 * C::kStages + 2 * C::kOps + s); };   // the other CTA's operands are ready
+    const auto a_ready = [&](int w) { return bar(2 * C::kStages + 3 * C::kOps + w); };
+    const auto a_free = [&](int w) { return bar(2 * C::kStages + 3 * C::kOps + C::kABufs + w); };
+    const uint32_t done = bar(2 * C::kStages + 3 * C::kOps + 2 * C::kABufs);
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kBars + 8 * C::kNumBars);
     // words[0]: TMEM address; [1]: a wait ran out
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(raw_full(s), 1);
-            ptx::mbar_init(raw_empty(s), 4 + C::kWiden);   // the warpgroup whose turn it is, and the inputs' warps
+            ptx::mbar_init(raw_empty(s), 4 + C::kWiden / C::kTurns);   // the warps whose turn it is
         }
         for (int s = 0; s < C::kOps; ++s) {
-            ptx::mbar_init(b_ready(s), C::kWiden * kPair);
+            ptx::mbar_init(b_ready(s), C::kWiden / C::kTurns);
             ptx::mbar_init(b_free(s), 1);
+            ptx::mbar_init(peer(s), 1);
         }
-        for (int w = 0; w < 2; ++w) {
-            ptx::mbar_init(a_ready(w), 4 * kPair);
+        for (int w = 0; w < C::kABufs; ++w) {
+            ptx::mbar_init(a_ready(w), 4);
             ptx::mbar_init(a_free(w), 1);
         }
         ptx::mbar_init(done, 1);
@@ -166,7 +182,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     ptx::griddep_launch_dependents();
     const uint32_t tmem = words[0];
     const auto t_a = [&](int w) { return tmem + (uint32_t)(w * C::kACols); };
-    const uint32_t t_d = tmem + 2 * C::kACols;
+    const uint32_t t_d = tmem + C::kABufs * C::kACols;
 
     const auto wait = [&](uint32_t bar_, uint32_t parity) -> bool {
         if (ptx::mbar_wait_bounded(bar_, parity, kWaitNs)) return true;
@@ -174,18 +190,16 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         atomicOr(L.status, kStatusTimeout);
         return false;
     };
-    const auto wait_both = [&](uint32_t bar_, uint32_t parity) -> bool {
-        if (kPair == 1) return wait(bar_, parity);
-        if (wait_cluster(bar_, parity, kWaitNs)) return true;
-        words[1] = 1;
-        atomicOr(L.status, kStatusTimeout);
-        return false;
-    };
     const auto lost = [&] { return words[1] != 0; };
-    const auto arrive = [&](uint32_t bar_) {   // at the CTA that issues
-        if (kPair == 1) ptx::mbar_arrive(bar_);
-        else arrive_at(bar_, 0);
-    };
+    float *const xs = reinterpret_cast<float *>(smem + C::kScales);
+    float ws = 0.0f, bias = 0.0f;   // of a thread's output
+    if (warp < C::kStoreWarps) {
+        for (int i = tid; i < kN; i += C::kStoreWarps * 32) xs[i] = m0 + i < L.rows ? L.x_scale[m0 + i] : 0.0f;
+        if (n0 + (tid & 127) < L.n) {
+            ws = L.w_scale[n0 + (tid & 127)];
+            if (L.bias) bias = L.bias[n0 + (tid & 127)];
+        }
+    }
 
     if (warp == C::kWarpMma) {
         // ------------------------------------------------------- MMA issue
@@ -196,19 +210,37 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             int op = 0;
             uint32_t op_parity = 0;
             for (int i = 0; i < ns; ++i) {
-                bool ok = wait_both(a_ready(i & 1), (i >> 1) & 1) && wait_both(b_ready(op), op_parity) && !lost();
+                bool ok = wait(a_ready(i % C::kABufs), (i / C::kABufs) & 1) && wait(b_ready(op), op_parity);
+                if (kPair > 1 && ok && !wait_cluster(peer(op), op_parity, kWaitNs)) {
+                    ok = false;
+                    words[1] = 1;
+                    atomicOr(L.status, kStatusTimeout);
+                }
+                ok = ok && !lost();
                 if (!__all_sync(~0u, ok)) break;
                 ptx::tc_fence_after();
                 const uint64_t b = d_b + (uint32_t)(op * C::kOp) / 16;
 #pragma unroll
                 for (int x = 0; x < kStageK / 16; ++x)
-                    T::mma(lead, t_d, t_a(i & 1) + 8 * x, b + (uint32_t)((x >> 2) * C::kRows * 8 + (x & 3) * 2), idesc, i > 0 || x > 0);
-                T::commit(lead, a_free(i & 1));
+                    T::mma(lead, t_d, t_a(i % C::kABufs) + 8 * x, b + (uint32_t)((x >> 2) * C::kRows * 8 + (x & 3) * 2), idesc, i > 0 || x > 0);
+                T::commit(lead, a_free(i % C::kABufs));
                 T::commit(lead, b_free(op));
                 if (++op == C::kOps) op = 0, op_parity ^= 1;
             }
             __syncwarp();
             T::commit(lead, done);   // all that was issued, however the loop ended
+        } else {
+            // The other CTA's operands are announced once a stage.
+            int op = 0;
+            uint32_t op_parity = 0;
+            for (int i = 0; i < ns; ++i) {
+                const bool ok = wait(a_ready(i % C::kABufs), (i / C::kABufs) & 1) && wait(b_ready(op), op_parity) && !lost();
+                if (!__all_sync(~0u, ok)) break;
+                ptx::tc_fence_after();
+                ptx::tc_fence_before();
+                if (lane == 0) arrive_at(peer(op), 0);
+                if (++op == C::kOps) op = 0, op_parity ^= 1;
+            }
         }
     } else if (warp == C::kWarpTma) {
         // ------------------------------------------------------- TMA
@@ -234,13 +266,12 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         // Sixteen codes a unit, eight units a row.  Lanes of a row's second 64 write
         // their upper half first: eight lanes are then in eight different sixteen-byte
         // banks.
-        constexpr int kLanes = C::kWiden * 32, kPer = C::kRows * 8 / kLanes;
-        const int t = tid - 256, u = t & 7, row0 = t >> 3;
+        constexpr int kLanes = C::kWiden / C::kTurns * 32, kPer = C::kRows * 8 / kLanes;
+        const int turn = (tid - 256) / kLanes, t = (tid - 256) % kLanes, u = t & 7, row0 = t >> 3;
         const uint32_t second = u >> 2;
-        int slot = 0, op = 0;
-        uint32_t parity = 0, op_parity = 1;
-        for (int i = 0; i < ns; ++i) {
-            bool ok = wait(raw_full(slot), parity);
+        for (int i = turn; i < ns; i += C::kTurns) {
+            const int slot = i % C::kStages, op = i % C::kOps;
+            bool ok = wait(raw_full(slot), (i / C::kStages) & 1);
             if (!__all_sync(~0u, ok)) break;
             uint4 raw[kPer];
 #pragma unroll
@@ -250,7 +281,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(raw_empty(slot));
-            ok = wait_both(b_free(op), op_parity) && !lost();
+            ok = wait(b_free(op), (i / C::kOps + 1) & 1) && !lost();
             if (!__all_sync(~0u, ok)) break;
             unsigned char *const to = smem + C::kOpAt + op * C::kOp + (u >> 2) * C::kRows * 128;
 #pragma unroll
@@ -268,16 +299,14 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(b_ready(op));
-            if (++slot == C::kStages) slot = 0, parity ^= 1;
-            if (++op == C::kOps) op = 0, op_parity ^= 1;
+            if (lane == 0) ptx::mbar_arrive(b_ready(op));
         }
     } else {
         // ------------------------------------------------------- weights
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         for (int i = wg; i < ns; i += 2) {
-            const int slot = i % C::kStages;
+            const int slot = i % C::kStages, buf = i % C::kABufs;
             bool ok = wait(raw_full(slot), (i / C::kStages) & 1);
             if (!__all_sync(~0u, ok)) break;
             const unsigned char *const from = smem + slot * C::kRaw + row * 128;
@@ -292,12 +321,12 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                     frag::i8_halves(w.z, a[8 * q + 4], a[8 * q + 5]);
                     frag::i8_halves(w.w, a[8 * q + 6], a[8 * q + 7]);
                 }
-                if (h == 0 && i >= 2) {
-                    ok = wait_both(a_free(wg), ((i >> 1) - 1) & 1) && !lost();
+                if (h == 0) {
+                    ok = wait(a_free(buf), (i / C::kABufs + 1) & 1) && !lost();
                     if (!__all_sync(~0u, ok)) break;
                     ptx::tc_fence_after();
                 }
-                tmem_st32(t_a(wg) + lanes + 32 * h, a);
+                tmem_st32(t_a(buf) + lanes + 32 * h, a);
             }
             if (!__all_sync(~0u, ok)) break;
             __syncwarp();
@@ -305,29 +334,27 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive(a_ready(wg));
+            if (lane == 0) ptx::mbar_arrive(a_ready(buf));
         }
     }
     __syncwarp();
     // Nothing goes on while an MMA reads shared or tensor memory.
-    if (!(kPair == 1 ? ptx::mbar_wait_bounded(done, 0, kWaitNs) : wait_cluster(done, 0, kWaitNs)))
-        atomicOr(L.status, kStatusTimeout);
+    if (!ptx::mbar_wait_bounded(done, 0, kWaitNs)) atomicOr(L.status, kStatusTimeout);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
 
     // ------------------------------------------------------------ output
-    if (warp < 8) {
-        // A thread has one output of half the input rows.
-        const int wg = warp >> 2, row = tid & 127, n = n0 + row;
+    if (warp < C::kStoreWarps) {
+        // A thread has one output of some of the input rows.
+        const int part = warp >> 2, row = tid & 127, n = n0 + row;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const float ws = n < L.n ? L.w_scale[n] : 0.0f, bias = n < L.n && L.bias ? L.bias[n] : 0.0f;
-        constexpr int kCols = kN / 2, kPart = kCols < 16 ? 8 : 16;
+        constexpr int kCols = kN / (C::kStoreWarps / 4), kPart = kCols < 16 ? 8 : 16;
         float *const sum = reinterpret_cast<float *>(smem);   // [input row][output] of this share
 #pragma unroll 1
         for (int q = 0; q < kCols / kPart; ++q) {
             uint32_t v[kPart];
-            const int col = wg * kCols + q * kPart;
+            const int col = part * kCols + q * kPart;
             if (ns > 0) {
                 if constexpr (kPart == 8) ptx::tmem_ld8(t_d + lanes + col, v);
                 else ptx::tmem_ld16(t_d + lanes + col, v);
@@ -342,7 +369,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
                 if (kPair == 1 && split > 1) {
                     sum[(col + e) * (kOut + 1) + row] = __uint_as_float(v[e]);
                 } else if (m < L.rows && n < L.n) {
-                    float y = __uint_as_float(v[e]) * (L.x_scale[m] * ws) + bias;
+                    float y = __uint_as_float(v[e]) * (xs[col + e] * ws) + bias;
                     if (L.act == CBS_ACT_SILU) y = silu(y);
                     const size_t at = (size_t)m * L.n + n;
                     if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at] = __float2bfloat16_rn(y);
@@ -372,7 +399,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 }
 
 template <int kN, int kPair>
-cbs_status launch_w8_one(const W8Launch &L, cudaStream_t s) {
+cbs_status launch_w8_one(const W8Launch &L, int split, cudaStream_t s) {
     using C = W8Tile<kN, kPair>;
     EncodeTiledFn fn = encode_tiled();
     if (!fn) return fail(CBS_ERR_CUDA, "cannot resolve cuTensorMapEncodeTiled from the driver");
@@ -387,12 +414,7 @@ cbs_status launch_w8_one(const W8Launch &L, cudaStream_t s) {
     if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (weights) failed (%d)", (int)r);
     r = map(&tx, L.x, L.rows, C::kRows);
     if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (inputs) failed (%d)", (int)r);
-    const int tiles = (L.n + kOut * kPair - 1) / (kOut * kPair), stages = (L.k + kStageK - 1) / kStageK;
-    const int row_tiles = (L.rows + kN - 1) / kN, sms = current_device_sms();
-    // Shares of k until every SM has a CTA.
-    int split = 1;
-    if (kPair == 1)
-        while (split < kShareMost && split * 4 <= stages && tiles * row_tiles * split < sms) split *= 2;
+    const int tiles = (L.n + kOut * kPair - 1) / (kOut * kPair), row_tiles = (L.rows + kN - 1) / kN;
     auto kern = w8_kernel<kN, kPair>;
     static ContextOfDevice set;
     cudaError_t e = set_max_dyn_smem_once(kern, C::kSmem, set);
@@ -439,12 +461,54 @@ __global__ void quantize_w8_kernel(const float *__restrict__ w, int n, int k, in
 
 }  // namespace
 
+// The tile and the shares of k, by what was measured (hundredths of a microsecond; 60
+// sizes of 256 x 1024 to 16384 x 8192, 1 to 6400 rows, every tile with 1 to 8 shares):
+// a CTA's start and end and each of its stages, alone on its SM and, for the tiles of
+// which two fit, for two side by side; and a share's part of the join.  What it takes
+// is 3% slower than the best on average and 20% at worst but for one (256 x 1024, 1600
+// rows: 9.5 us for 7.0).
+struct W8Cost { int rows, alone, stage, two, stage2, share; };
+constexpr W8Cost kCosts[] = {{16, 180, 47, 350, 61, 13}, {32, 200, 47, 380, 68, 28}, {64, 270, 53, 510, 79, 34},
+                             {128, 540, 49, 0, 0, 56}, {256, 560, 56, 0, 0, 0}};
+
+//
+// Few rows go to k_w8_few.cu: its time and this file's, one row: 1001 x 2064 4.0 and 5.6
+// us, 4096 x 4096 5.1 and 8.1, 6144 x 4096 6.6 and 9.1, 8192 x 8192 14.6 and 15.9, 16384 x
+// 8192 27.2 and 26.6; sixteen rows: 4.0 and 6.0, 6.6 and 8.6, 9.7 and 10.0, 20 and 17; 70000
+// x 256 14 and 9.0.
+constexpr long long kFewMost8 = 96ll << 20, kFewMost16 = 28ll << 20;
+constexpr int kFewMostOutputs16 = 16384;
+
 cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
-    if (L.rows <= 16) return launch_w8_one<16, 1>(L, s);
-    if (L.rows <= 32) return launch_w8_one<32, 1>(L, s);
-    if (L.rows <= 64) return launch_w8_one<64, 1>(L, s);
-    if (L.rows <= 128) return launch_w8_one<128, 1>(L, s);
-    return launch_w8_one<256, 2>(L, s);
+    const long long weights = (long long)L.n * L.k;
+    if (L.rows <= 8 ? weights <= kFewMost8 : L.rows <= 16 && weights <= kFewMost16 && L.n <= kFewMostOutputs16)
+        return cuda_check(launch_w8_few(L, s), "8-bit product launch");
+    const long long sms = current_device_sms(), stages = (L.k + kStageK - 1) / kStageK;
+    long long best = 0;
+    int rows = 0, split = 1;
+    for (const W8Cost &c : kCosts) {
+        if (rows && c.rows >= 2 * L.rows) break;   // (half of a larger tile would be empty)
+        for (int x = 1; x <= (c.rows == 256 ? 1 : kShareMost) && (x == 1 || 2 * x <= stages); x *= 2) {
+            const long long each = (stages + x - 1) / x, row_tiles = (L.rows + c.rows - 1) / c.rows;
+            long long cost;
+            if (c.rows == 256) {   // pairs of CTAs
+                const long long pairs = std::max(sms / 2, 1ll), tiles = (L.n + 2 * kOut - 1) / (2 * kOut) * row_tiles;
+                cost = (tiles + pairs - 1) / pairs * (c.alone + each * c.stage);
+            } else {
+                const long long per = ((L.n + kOut - 1) / kOut * row_tiles * x + sms - 1) / sms;
+                cost = c.two ? per / 2 * (c.two + each * c.stage2) + per % 2 * (c.alone + each * c.stage) : per * (c.alone + each * c.stage);
+                if (x > 1) cost += x * c.share;
+            }
+            if (!rows || cost < best) best = cost, rows = c.rows, split = x;
+        }
+    }
+    switch (rows) {
+    case 16: return launch_w8_one<16, 1>(L, split, s);
+    case 32: return launch_w8_one<32, 1>(L, split, s);
+    case 64: return launch_w8_one<64, 1>(L, split, s);
+    case 128: return launch_w8_one<128, 1>(L, split, s);
+    default: return launch_w8_one<256, 2>(L, 1, s);
+    }
 }
 
 cudaError_t launch_quantize_w8(const float *w, int n, int k, int8_t *codes, float *scales, cudaStream_t s) {
