@@ -72,19 +72,23 @@ __global__ void __launch_bounds__(kSumThreads) weights_of_scores_kernel(const At
 }
 
 // ------------------------------------------------------------------- chunks
-constexpr int kKeys = 128, kRowTile = 128, kBufs = 4;
-constexpr int kLoaders = 4, kWarps = 4 * kBufs + kLoaders + 1, kThreads = kWarps * 32;   // a warpgroup a buffer sums up
+// A tile of rows is kRowTile of them at most: T tokens' S query heads each, where S is
+// all of a key head's (or, of more than 128, its largest divisor that fits) and T as
+// many as fit, so that one box of TMA brings them.  Two warpgroups take tiles in turn,
+// a thread a key; two CTAs an SM, so that one's start runs beside the other's sums.
+constexpr int kKeys = 128, kRowTile = 128, kBufs = 2;
+constexpr int kStatWarps = 4, kWarpMma = 4 * kBufs + kStatWarps, kWarpTma = kWarpMma + 1, kThreads = (kWarpTma + 1) * 32;
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 template <int D>
 struct Weigh {
     static constexpr int kOperand = (D / 64) * kKeys * 128;   // panels of 64 dimensions
     static constexpr int kQ = kOperand, kStats = kQ + kBufs * kOperand;
-    // each buffer's rows: m[128], 1 / l[128], lo[128], hi[128]; after them whether one is far
-    static constexpr int kStat = 4 * kRowTile * 4, kFar = kStats + kBufs * kStat, kBars = kFar + kBufs * 4;
-    static constexpr int kNumBars = 3 * kBufs;   // full[], s_full[], s_free[]
+    // each buffer's rows: -m[128], 1 / l[128], lo[128], hi[128]; after them whether one is far
+    static constexpr int kStat = 4 * kRowTile * 4, kFar = kStats + kBufs * kStat, kBars = kFar + kBufs * 8;
+    static constexpr int kNumBars = 4 * kBufs;   // q_full[], stat_full[], s_full[], s_free[]
     static constexpr int kSum = kBars + kNumBars * 8, kSmem = kSum + (kBufs - 1) * kKeys * 4 + 16;
-    static_assert(kSmem <= kMaxDynSmem && kBars % 8 == 0, "shared memory");
+    static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
 };
 
 // As slow_row takes a row's score of a key, to the bit.
@@ -106,13 +110,94 @@ __device__ __noinline__ float slow_score(const AttnLaunch &L, const Rows &s, int
 
 __device__ __forceinline__ bool far_row(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// A thread's sum over a tile's rows: scores, as they come from tensor memory, to
+// exponentials times what belongs to each row.  Two lanes of an instruction at a time,
+// and the next sixteen scores on their way.
+struct F2 { unsigned long long v; };
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// MASK: rows that do not see `key` are left out.
+template <bool MASK>
+__device__ __forceinline__ void tile_sum(uint32_t taddr, const float *stat, float scale, int key, F2 (&sums)[2]) {
+    const int *lo = reinterpret_cast<const int *>(stat) + 2 * kRowTile, *hi = lo + kRowTile;
+    const F2 scale2 = pair(scale, scale);
+    const auto part = [&](const uint32_t (&v)[16], int q) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(stat + 16 * q + e), inv = *reinterpret_cast<const float4 *>(stat + kRowTile + 16 * q + e);
+            const float2 a = split(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, pair(m.x, m.y)));
+            const float2 b = split(fma2(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), scale2, pair(m.z, m.w)));
+            float x[4] = {frag::ex2(a.x), frag::ex2(a.y), frag::ex2(b.x), frag::ex2(b.y)};
+            if constexpr (MASK) {
+                const int4 l4 = *reinterpret_cast<const int4 *>(lo + 16 * q + e), h4 = *reinterpret_cast<const int4 *>(hi + 16 * q + e);
+                x[0] = key >= l4.x && key < h4.x ? x[0] * inv.x : 0.0f;
+                x[1] = key >= l4.y && key < h4.y ? x[1] * inv.y : 0.0f;
+                x[2] = key >= l4.z && key < h4.z ? x[2] * inv.z : 0.0f;
+                x[3] = key >= l4.w && key < h4.w ? x[3] * inv.w : 0.0f;
+                const F2 one = pair(1.0f, 1.0f);
+                sums[0] = fma2(pair(x[0], x[1]), one, sums[0]);
+                sums[1] = fma2(pair(x[2], x[3]), one, sums[1]);
+            } else {
+                sums[0] = fma2(pair(x[0], x[1]), pair(inv.x, inv.y), sums[0]);
+                sums[1] = fma2(pair(x[2], x[3]), pair(inv.z, inv.w), sums[1]);
+            }
+        }
+    };
+    uint32_t u[16], v[16];
+    ptx::tmem_ld16(taddr, u);
+#pragma unroll
+    for (int q = 0; q < kRowTile / 16; q += 2) {
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld16(taddr + 16 * (q + 1), v);
+        part(u, q);
+        ptx::tmem_ld_wait();
+        if (q + 2 < kRowTile / 16) ptx::tmem_ld16(taddr + 16 * (q + 2), u);
+        part(v, q + 1);
+    }
+}
+
+// Tiles of a call: S heads, T tokens, and how many tiles a token's heads make.
+struct RowTiles {
+    int heads, tokens, parts;
+    static RowTiles of(int group) {
+        RowTiles t = {group, 1, 1};
+        if (group <= kRowTile) t.tokens = kRowTile / group;
+        else
+            for (t.heads = kRowTile; group % t.heads; --t.heads) {}
+        t.parts = group / t.heads;
+        return t;
+    }
+};
+
 template <int D, bool I8>
-__global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const AttnLaunch L) {
+__global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnLaunch L, const RowTiles rt) {
     using C = Weigh<D>;
     extern __shared__ __align__(1024) unsigned char smem[];   // the only shared memory: starts at a multiple of 1 KB
     const uint32_t sbase = ptx::smem_u32(smem);
     const CacheArgs &c = L.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == kWarpTma && lane == 0) ptx::prefetch_tmap(&tm_q);
     ptx::griddep_wait();
     const int head = blockIdx.y, b = blockIdx.z, key0 = blockIdx.x * kKeys;
     const Rows rs = rows_again(L, b, head);
@@ -120,27 +205,34 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
     const int end = min(min(rs.len, L.len_pad), key0 + kKeys);
     if (rs.fresh == 0 || key0 >= end) return;
     // The tokens that see one of the keys, and the tiles of their rows.
-    const long long t0 = L.causal ? max(0ll, (long long)key0 - rs.base) : 0ll;
-    const long long t1 = L.window ? min((long long)rs.fresh, (long long)end - 1 + L.window - rs.base) : rs.fresh;
-    const int first = (int)(t0 * L.group / kRowTile), tiles = t0 < t1 ? (int)((t1 * L.group + kRowTile - 1) / kRowTile) - first : 0;
+    const int t0 = (int)min((long long)rs.fresh, L.causal ? max(0ll, (long long)key0 - rs.base) : 0ll);
+    const int t1 = (int)max((long long)t0, L.window ? min((long long)rs.fresh, (long long)end - 1 + L.window - rs.base) : (long long)rs.fresh);
+    const int tiles = (t1 - t0 + rt.tokens - 1) / rt.tokens * rt.parts;
+    struct Tile { int token, head, tokens; };   // of the sequence and of the key head; of them within t1
+    const auto tile_of = [&](int i) {
+        const int group = rt.parts == 1 ? i : i / rt.parts;
+        return Tile{t0 + group * rt.tokens, (i - group * rt.parts) * rt.heads, min(rt.tokens, t1 - t0 - group * rt.tokens)};
+    };
 
     const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
-    const auto full = [&](int s) { return bar(s); };                 // a tile's rows and their statistics are there
-    const auto s_full = [&](int s) { return bar(kBufs + s); };       // its scores
-    const auto s_free = [&](int s) { return bar(2 * kBufs + s); };   // all of them have been summed up
+    const auto q_full = [&](int s) { return bar(s); };                // a tile's rows have arrived
+    const auto stat_full = [&](int s) { return bar(kBufs + s); };     // and what the attention left of them
+    const auto s_full = [&](int s) { return bar(2 * kBufs + s); };    // its scores are there (and its rows have been used)
+    const auto s_free = [&](int s) { return bar(3 * kBufs + s); };    // and have been summed up
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kSum + (kBufs - 1) * kKeys * 4);
     // words[0]: TMEM address; [1]: a wait ran out
     if (tid == 0) {
         for (int s = 0; s < kBufs; ++s) {
-            ptx::mbar_init(full(s), kLoaders);
+            ptx::mbar_init(q_full(s), 1);
+            ptx::mbar_init(stat_full(s), kStatWarps);
             ptx::mbar_init(s_full(s), 1);
             ptx::mbar_init(s_free(s), 4);
         }
         ptx::fence_mbar_init();
         words[1] = 0;
     }
-    if (warp == kWarps - 1) {
-        ptx::tmem_alloc(sbase + C::kSum + (kBufs - 1) * kKeys * 4, 512);
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(sbase + C::kSum + (kBufs - 1) * kKeys * 4, kBufs * kRowTile);
         ptx::tmem_relinquish();
     }
     // The keys, widened, in the operand's swizzled rows; zeros past the end.
@@ -169,6 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
             *reinterpret_cast<uint4 *>(smem + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
         }
     }
+    // Rows that no box brings: zeros, whose exponentials then count for nothing.
+    const int boxed = rt.heads * rt.tokens, rest = (kRowTile - boxed) * 8;
+    for (int i = tid; i < kBufs * (D / 64) * rest; i += kThreads)
+        *reinterpret_cast<uint4 *>(smem + C::kQ + (i / rest) * (kKeys * 128) + boxed * 128 + i % rest * 16) = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
@@ -186,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
 
     const int key = key0 + (warp & 3) * 32 + lane;   // a summing thread's
     float acc = 0.0f;
-    if (warp == kWarps - 1) {
+    if (warp == kWarpMma) {
         // ------------------------------------------------------- MMA issue
         constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kRowTile >> 3) << 17) | ((kKeys >> 4) << 24);
         const uint32_t lead = elect_one();
@@ -194,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
         int issued = 0;
         for (int i = 0; i < tiles; ++i) {
             const int s = i % kBufs;
-            // (A tile's rows are loaded once its buffer's last scores have been summed up.)
-            if (!__all_sync(~0u, wait(full(s), (i / kBufs) & 1) && !lost())) break;
+            const uint32_t turn = (i / kBufs) & 1;
+            if (!__all_sync(~0u, wait(q_full(s), turn) && wait(s_free(s), turn ^ 1) && !lost())) break;
             ptx::tc_fence_after();
             const uint64_t q = d_q + (uint32_t)(s * C::kOperand) / 16;
 #pragma unroll
@@ -209,54 +305,54 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
         // Nothing leaves while an MMA reads shared memory.
         for (int i = max(0, issued - kBufs); i < issued; ++i)
             if (!ptx::mbar_wait_bounded(s_full(i % kBufs), (i / kBufs) & 1, kWaitNs)) atomicOr(c.status, kStatusTimeout);
-    } else if (warp >= 4 * kBufs) {
+    } else if (warp == kWarpTma) {
         // ------------------------------------------------------- rows
-        const int t = tid - 4 * kBufs * 32;
-        const auto finish = [&](int i) {   // tile i has landed
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(full(i % kBufs));
-        };
-        // A row a thread: what the attention left of it, a tile ahead.
-        const auto statistics = [&](int i) -> float2 {
-            const int r = (first + i) * kRowTile + t;
-            return i < tiles && r < rs.R ? __ldg(&L.row_stats[rs.number(L, r)]) : make_float2(0.0f, 0.0f);
-        };
-        float2 next = statistics(0);
-        int loaded = 0;
-        for (int i = 0; i < tiles; ++i) {
-            const int s = i % kBufs;
-            const float2 st = next;
-            next = statistics(i + 1);
-            const bool ok = wait(s_free(s), (i / kBufs + 1) & 1) && !lost();
-            if (ok && t == 0) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 0;
-            if (ptx::bar_red_or(1, kLoaders * 32, !ok)) break;   // (together, whatever ran out)
-            float *const stat = reinterpret_cast<float *>(smem + C::kStats + s * C::kStat);
-            const int r0 = (first + i) * kRowTile;
+        if (lane == 0) {
+            int loaded = 0;
+            for (int i = 0; i < tiles; ++i) {
+                const int s = i % kBufs;
+                if (!wait(s_full(s), (i / kBufs + 1) & 1) || lost()) break;   // (used: their scores are there)
+                const Tile t = tile_of(i);
+                ptx::mbar_arrive_expect_tx(q_full(s), (uint32_t)(boxed * D * 2));
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-                const int unit = x * (kLoaders * 32) + t, row = unit / (D / 8), u = unit % (D / 8), r = r0 + row;
-                const bool on = r < rs.R;
-                ptx::cp_async_16(sbase + C::kQ + s * C::kOperand + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4),
-                                 on ? rs.query(L, r, D) + u * 8 : static_cast<const __nv_bfloat16 *>(L.q), on ? 16 : 0);
+                for (int p = 0; p < D / 64; ++p)
+                    tma_load_3d(sbase + C::kQ + s * C::kOperand + p * (kKeys * 128), &tm_q, q_full(s), p * 64, head * L.group + t.head, rs.start + t.token);
+                ++loaded;
             }
+            // The copies in flight land before the CTA leaves, whoever gives up.
+            for (int i = max(0, loaded - kBufs); i < loaded; ++i) ptx::mbar_wait_bounded(q_full(i % kBufs), (i / kBufs) & 1, kWaitNs);
+        }
+    } else if (warp >= 4 * kBufs) {
+        // ------------------------------------------- what the attention left
+        // A row a thread, a tile ahead.
+        const int t = tid - 4 * kBufs * 32, my_token = t / rt.heads, my_head = t - my_token * rt.heads;
+        const auto row_of = [&](int i) {   // of the key head's, or -1
+            if (i >= tiles) return -1;
+            const Tile x = tile_of(i);
+            return my_token < x.tokens ? (x.token + my_token) * L.group + x.head + my_head : -1;
+        };
+        const auto statistics = [&](int r) { return r >= 0 ? __ldg(&L.row_stats[rs.number(L, r)]) : make_float2(0.0f, 0.0f); };
+        int row_next = row_of(0);
+        float2 next = statistics(row_next);
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i % kBufs, r = row_next;
+            const float2 st = next;
+            row_next = row_of(i + 1);
+            next = statistics(row_next);
+            const bool ok = wait(s_free(s), (i / kBufs + 1) & 1) && !lost();
             // A far row: by itself, from its own loads; here every exponential of it is zero.
-            const bool far = far_row(st.x);
-            if (far) *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * s) = 1;
-            const Seen z = r0 + t < rs.R ? rs.seen(L, r0 + t) : Seen{0, 0};
-            stat[t] = far ? INFINITY : st.x;
+            const bool far = far_row(st.x), any_far = ptx::bar_red_or(1, kStatWarps * 32, far);
+            if (ptx::bar_red_or(1, kStatWarps * 32, !ok)) break;   // (together, whatever ran out)
+            float *const stat = reinterpret_cast<float *>(smem + C::kStats + s * C::kStat);
+            const Seen z = r >= 0 ? rs.seen(L, r) : Seen{0, 0};
+            stat[t] = far ? -INFINITY : -st.x;
             stat[kRowTile + t] = far ? 0.0f : st.y;
             reinterpret_cast<int *>(stat)[2 * kRowTile + t] = z.lo;
             reinterpret_cast<int *>(stat)[3 * kRowTile + t] = z.hi;
-            ptx::cp_async_commit();
-            ++loaded;
-            if (i > 0) {
-                ptx::cp_async_wait<1>();
-                finish(i - 1);
-            }
+            if (t == 0) *reinterpret_cast<volatile int *>(smem + C::kFar + 8 * s) = any_far;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(stat_full(s));
         }
-        ptx::cp_async_wait<0>();
-        if (loaded > 0) finish(loaded - 1);
     } else {
         // ------------------------------------------------------- sums
         const int wg = warp >> 2;
@@ -264,67 +360,48 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
         const int p = key < end ? page_of(c, b, key) : -1;
         const size_t at = p < 0 ? 0 : (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
         const float scale = I8 ? (p < 0 ? 0.0f : c.k_scale[at] * L.scale_log2) : L.scale_log2;
-        float2 sums = make_float2(0.0f, 0.0f);
+        F2 sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+        float slow = 0.0f;
         for (int i = wg; i < tiles; i += kBufs) {
-            const int r0 = (first + i) * kRowTile, r1 = min(rs.R, r0 + kRowTile);
+            const Tile t = tile_of(i);
             const uint32_t turn = (i / kBufs) & 1;
-            if (!__all_sync(~0u, wait(s_full(wg), turn) && wait(full(wg), turn) && !lost())) break;   // scores; statistics
+            if (!__all_sync(~0u, wait(s_full(wg), turn) && wait(stat_full(wg), turn) && !lost())) break;
             ptx::tc_fence_after();
             const float *stat = reinterpret_cast<const float *>(smem + C::kStats + wg * C::kStat);
-            const int *lo = reinterpret_cast<const int *>(stat) + 2 * kRowTile, *hi = lo + kRowTile;
-            const bool whole = rs.seen(L, r1 - 1).lo <= key0 && rs.seen(L, r0).hi >= end;   // every row sees every key
-#pragma unroll 1
-            for (int q = 0; q < kRowTile / 16; ++q) {
-                uint32_t v[16];
-                ptx::tmem_ld16(tmem + (uint32_t)(wg * kRowTile) + lanes + 16 * q, v);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(stat + 16 * q + e), inv = *reinterpret_cast<const float4 *>(stat + kRowTile + 16 * q + e);
-                    float x[4] = {frag::ex2(fmaf(__uint_as_float(v[e]), scale, -m.x)), frag::ex2(fmaf(__uint_as_float(v[e + 1]), scale, -m.y)),
-                                  frag::ex2(fmaf(__uint_as_float(v[e + 2]), scale, -m.z)), frag::ex2(fmaf(__uint_as_float(v[e + 3]), scale, -m.w))};
-                    if (!whole) {
-                        const int4 l4 = *reinterpret_cast<const int4 *>(lo + 16 * q + e), h4 = *reinterpret_cast<const int4 *>(hi + 16 * q + e);
-                        x[0] = key >= l4.x && key < h4.x ? x[0] * inv.x : 0.0f;
-                        x[1] = key >= l4.y && key < h4.y ? x[1] * inv.y : 0.0f;
-                        x[2] = key >= l4.z && key < h4.z ? x[2] * inv.z : 0.0f;
-                        x[3] = key >= l4.w && key < h4.w ? x[3] * inv.w : 0.0f;
-                        sums.x += x[0] + x[2];
-                        sums.y += x[1] + x[3];
-                    } else {
-                        sums.x = fmaf(x[0], inv.x, sums.x);
-                        sums.y = fmaf(x[1], inv.y, sums.y);
-                        sums.x = fmaf(x[2], inv.z, sums.x);
-                        sums.y = fmaf(x[3], inv.w, sums.y);
-                    }
-                }
-            }
-            const bool far = *reinterpret_cast<volatile int *>(smem + C::kFar + 4 * wg) != 0;
+            // Every row of the box is the sequence's, and sees every key.
+            const bool whole = t.tokens == rt.tokens && seen_by(rs.base + t.token + t.tokens - 1, rs.len, L.causal, L.window).lo <= key0 &&
+                               seen_by(rs.base + t.token, rs.len, L.causal, L.window).hi >= end;
+            const uint32_t taddr = tmem + (uint32_t)(wg * kRowTile) + lanes;
+            if (whole) tile_sum<false>(taddr, stat, scale, key, sums);
+            else tile_sum<true>(taddr, stat, scale, key, sums);
+            const bool far = *reinterpret_cast<volatile int *>(smem + C::kFar + 8 * wg) != 0;
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(s_free(wg));
             if (far) {   // seldom met
-                for (int r = r0; r < r1; ++r) {
+                for (int x = 0; x < t.tokens * rt.heads; ++x) {
+                    const int r = (t.token + x / rt.heads) * L.group + t.head + x % rt.heads;
                     const float2 st = __ldg(&L.row_stats[rs.number(L, r)]);
                     if (!far_row(st.x)) continue;
                     const Seen z = rs.seen(L, r);
-                    for (int x = 0; x < 32; ++x) {
-                        const int k = __shfl_sync(~0u, key, x), kp = __shfl_sync(~0u, p, x);
-                        const size_t row = (size_t)__shfl_sync(~0u, (unsigned long long)at, x);
+                    for (int y = 0; y < 32; ++y) {
+                        const int k = __shfl_sync(~0u, key, y), kp = __shfl_sync(~0u, p, y);
+                        const size_t row = (size_t)__shfl_sync(~0u, (unsigned long long)at, y);
                         if (kp < 0 || k < z.lo || k >= z.hi) continue;
                         const float w = frag::ex2(slow_score<D, I8>(L, rs, r, row, lane) - st.x) * st.y;
-                        if (lane == x) sums.x += w;
+                        if (lane == y) slow += w;
                     }
                 }
             }
         }
-        acc = sums.x + sums.y;
+        const float2 a = split(sums[0]), d = split(sums[1]);
+        acc = ((a.x + a.y) + (d.x + d.y)) + slow;
         if (wg > 0) reinterpret_cast<float *>(smem + C::kSum)[(wg - 1) * kKeys + key - key0] = acc;
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kWarps - 1) ptx::tmem_dealloc(tmem, 512);
+    if (warp == kWarpMma) ptx::tmem_dealloc(tmem, kBufs * kRowTile);
     if (warp < 4 && key < end && !lost()) {
 #pragma unroll
         for (int g = 0; g < kBufs - 1; ++g) acc += reinterpret_cast<const float *>(smem + C::kSum)[g * kKeys + key - key0];
@@ -338,10 +415,21 @@ __global__ void __launch_bounds__(kThreads, 1) weights_of_chunk_kernel(const Att
 
 template <int D, bool I8>
 cbs_status launch_chunk_weights(const AttnLaunch &L, cudaStream_t s) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return fail(CBS_ERR_CUDA, "cannot resolve cuTensorMapEncodeTiled from the driver");
+    // The call's rows [total][heads][D], boxes of T tokens, S heads and 64 dimensions.
+    const RowTiles rt = RowTiles::of(L.group);
+    alignas(64) CUtensorMap tq;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L.heads, (cuuint64_t)L.c.total};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)L.q_stride * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)rt.heads, (cuuint32_t)rt.tokens}, es[3] = {1u, 1u, 1u};
+    const CUresult r = fn(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(L.q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", (int)r);
     static ContextOfDevice set;
     CBS_TRY(cuda_check(set_max_dyn_smem_once(weights_of_chunk_kernel<D, I8>, Weigh<D>::kSmem, set), "weights' shared memory"));
     return cuda_check(launch_kernel(weights_of_chunk_kernel<D, I8>, dim3((L.len_pad + kKeys - 1) / kKeys, L.c.kv_heads, L.c.batch), kThreads,
-                                    Weigh<D>::kSmem, s, L), "weights launch");
+                                    Weigh<D>::kSmem, s, tq, L, rt), "weights launch");
 }
 
 }  // namespace

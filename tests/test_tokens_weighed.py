@@ -150,6 +150,8 @@ def test_many_rows():
     run_case([130], [130], 64, 1, 64, 16, False)
     run_case([64], [64], 96, 1, 128, 64, True, causal=False)
     run_case([3000], [260], 8, 1, 128, 64, False, window=700)
+    for heads in (129, 131, 160, 256):   # more query heads of a key head than a tile has rows
+        run_case([140, 20], [3, 2], heads, 1, 64, 16, heads % 2 == 0, kernel=CHUNK)
 
 
 @pytest.mark.gpu
