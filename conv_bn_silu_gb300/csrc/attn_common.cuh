@@ -4,6 +4,7 @@
 #pragma once
 
 #include "mma_frag.cuh"
+#include "tc_ptx.cuh"
 #include "tokens.cuh"
 
 namespace cbs {
@@ -20,6 +21,18 @@ enum AttnMode {
     kAttnOwn = 2,      // the sequences' own keys: joined with those shares
     kAttnWeighed = 3   // the output, and each row's (maximum, 1 / sum) to L.row_stats
 };
+
+// Until what a call reads is there.  The sequences' own part begins while their
+// prefixes' part, the kernel before it, still runs, and waits for that only where it
+// needs the shares (every CTA does, also one without rows: what comes after this
+// kernel comes after both).  All else that it reads and writes is older: it is
+// launched once every CTA of the prefixes' part has let it, which they do after their
+// own wait for the kernels before.  The fence drops what this SM's L1 held until then.
+template <int MODE>
+__device__ __forceinline__ void begin_attention() {
+    if constexpr (MODE == kAttnOwn) __threadfence();
+    else ptx::griddep_wait();
+}
 
 // Keys [lo, hi) are what a row at `place` sees of a sequence.
 struct Seen { int lo, hi; };

@@ -284,7 +284,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    ptx::griddep_wait();
+    begin_attention<MODE>();
     ptx::griddep_launch_dependents();
     const int b = blockIdx.z, head = blockIdx.y % c.kv_heads;
     const int rt = L.row_tiles - 1 - blockIdx.y / c.kv_heads;   // later rows see more keys: they start first
@@ -293,6 +293,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // CTAs of one cluster meet twice at the end, and none leaves before: whatever
     // is read there is still some CTA's, even if the lengths change meanwhile.
     const auto leave = [&] {
+        if constexpr (MODE == kAttnOwn) ptx::griddep_wait();
         if (warp == 1) ptx::tmem_dealloc(words[0], 512);
         if (L.split == 1) return;
         cluster_sync();
@@ -717,6 +718,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::tc_fence_after();
 
     // ---------------------------------------------------------- output
+    if constexpr (MODE == kAttnOwn) ptx::griddep_wait();   // the prefix's shares
     const bool join = MODE != kAttnPlain || active > 1;
     if (softmax && !lost()) {
         // Float rows of a range and their (maximum, sum), for the join: where the

@@ -108,6 +108,29 @@ constexpr int kGridMax = 65535;
 // 51/127, 94/126, 160/127.
 constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
+// Ranges of keys of the chunk kernel, for `base` row tiles of all sequences and heads.
+int chunk_split(long long base, int keys, int sms) {
+    // One CTA an SM: the split with the least rounds of clusters times what a
+    // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
+    // A key tile is one unit (1.6 us, head dimension 128), a range's start and
+    // end 4.5, a cluster's join 2 and a fifth for each CTA.  64 tokens of 32
+    // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 60, 39,
+    // 30, 26, 23, 22, 21, 22 us; four sequences 61, 40, 31, 28, 47, 45, 62, 64.
+    // Less than a tenth is not worth a cluster: sequences are of unequal lengths.
+    static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
+    const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
+    long long best = 0;
+    int split = 1;
+    for (int x = 1; x <= std::min(key_tiles, kAttnChunkSplitMost); ++x) {
+        const int at_once = std::max(kAtOnce[x - 1] * sms / 152, 1);
+        const long long rounds = (base + at_once - 1) / at_once;
+        const long long cost = rounds * ((key_tiles + x - 1) / x * 10 + 45 + (x > 1 ? 20 + 2 * x : 0));
+        if (x == 1) best = cost - cost / 10;
+        else if (cost < best) best = cost, split = x;
+    }
+    return split;
+}
+
 size_t attn_counter_bytes(const cbs_attn_plan_t &p) {
     return ((size_t)p.desc.batch * p.desc.kv_heads * p.row_tiles * 4 + 255) / 256 * 256;
 }
@@ -310,23 +333,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     if (d->force_split) {
         p.split = p.kernel == CBS_ATTN_ROWS ? d->force_split : std::min(d->force_split, kAttnClusterMost);
     } else if (chunk) {
-        // One CTA an SM: the split with the least rounds of clusters times what a
-        // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
-        // A key tile is one unit (1.6 us, head dimension 128), a range's start and
-        // end 4.5, a cluster's join 2 and a fifth for each CTA.  64 tokens of 32
-        // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 60, 39,
-        // 30, 26, 23, 22, 21, 22 us; four sequences 61, 40, 31, 28, 47, 45, 62, 64.
-        // Less than a tenth is not worth a cluster: sequences are of unequal lengths.
-        static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
-        const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
-        long long best = 0;
-        for (int x = 1; x <= std::min(key_tiles, kAttnChunkSplitMost); ++x) {
-            const int at_once = std::max(kAtOnce[x - 1] * sms / 152, 1);
-            const long long rounds = (base + at_once - 1) / at_once;
-            const long long cost = rounds * ((key_tiles + x - 1) / x * 10 + 45 + (x > 1 ? 20 + 2 * x : 0));
-            if (x == 1) best = cost - cost / 10, p.split = 1;
-            else if (cost < best) best = cost, p.split = x;
-        }
+        p.split = chunk_split(base, keys, sms);
     } else {
         // At least a CTA for each SM if that leaves a range 64 keys, and up to
         // twelve if it leaves 640.  Tokens of 32 heads, 8 key heads, 1, 2, 4, ... 32
@@ -477,6 +484,14 @@ cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, 
     const SharedParts parts = shared_parts(*p);
     char *at = static_cast<char *>(workspace);
     attn_fill(p->prefix, &pre);
+    if (p->prefix.kernel == CBS_ATTN_CHUNK) {
+        // Groups differ in size: the tiles that a call of so many tokens has, half of each
+        // group's last one empty, are fewer than the largest group's for every group.
+        const cbs_attn_desc &d = p->prefix.desc;
+        const long long tiles = ((long long)s->total * pre.group / kAttnChunkRows) + (d.batch + 1) / 2;
+        pre.split = chunk_split(std::min<long long>(tiles, (long long)d.batch * pre.row_tiles) * d.kv_heads, d.max_len,
+                                d.num_sms > 0 ? d.num_sms : kDefaultNumSMs);
+    }
     attn_workspace(p->prefix, at, &pre);
     attn_workspace(p->own, at + parts.own, &own);
     pre.group_start = prefixes->group_start;
