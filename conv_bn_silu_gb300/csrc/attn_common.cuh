@@ -19,19 +19,29 @@ enum AttnMode {
     kAttnPlain = 0,
     kAttnPrefix = 1,   // a group's prefix: the rows' shares go to L.share, unnormalised
     kAttnOwn = 2,      // the sequences' own keys: joined with those shares
+    kAttnBeside = 4,   // the sequences' own keys, their shares left for a kernel that joins both
     kAttnWeighed = 3   // the output, and each row's (maximum, 1 / sum) to L.row_stats
 };
 
 // Until what a call reads is there.  The sequences' own part begins while their
-// prefixes' part, the kernel before it, still runs, and waits for that only where it
-// needs the shares (every CTA does, also one without rows: what comes after this
-// kernel comes after both).  All else that it reads and writes is older: it is
-// launched once every CTA of the prefixes' part has let it, which they do after their
-// own wait for the kernels before.  The fence drops what this SM's L1 held until then.
+// prefixes' part, the kernel before it, still runs.  All that it reads and writes but
+// the shares is older: it is launched once every CTA of the prefixes' part has let it,
+// which they do after their own wait for the kernels before.  The fence drops what this
+// SM's L1 held until then.
+constexpr bool runs_beside(int mode) { return mode == kAttnOwn || mode == kAttnBeside; }
 template <int MODE>
 __device__ __forceinline__ void begin_attention() {
-    if constexpr (MODE == kAttnOwn) __threadfence();
+    if constexpr (runs_beside(MODE)) __threadfence();
     else ptx::griddep_wait();
+}
+// Before the shares are read (kAttnOwn), and before a CTA ends: what comes after this
+// kernel has to come after both parts.  One waiting CTA is enough for that; with
+// kAttnBeside the others make room for the next.
+template <int MODE>
+__device__ __forceinline__ void end_attention() {
+    if constexpr (MODE == kAttnOwn) ptx::griddep_wait();
+    if constexpr (MODE == kAttnBeside)
+        if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) ptx::griddep_wait();
 }
 
 // Keys [lo, hi) are what a row at `place` sees of a sequence.
@@ -120,13 +130,28 @@ __device__ __forceinline__ float share_factor(float m, float l, float top) {
     return frag::ex2(m - top);
 }
 
+// A prefix's share and a row's own of the same dimensions, joined into acc and sum;
+// false where neither saw a key.
+__device__ __forceinline__ bool join_shares(float2 pre, float4 pre_acc, float2 own, float4 &acc, float &sum) {
+    const float both = fmaxf(own.x, pre.x), mine = share_factor(own.x, own.y, both), theirs = share_factor(pre.x, pre.y, both);
+    const bool no_own = own.x == -INFINITY && mine == 0.0f, no_pre = pre.x == -INFINITY && theirs == 0.0f;
+    acc = no_own ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(acc.x * mine, acc.y * mine, acc.z * mine, acc.w * mine);
+    sum = no_own ? 0.0f : own.y * mine;
+    if (!no_pre) {
+        acc.x = fmaf(pre_acc.x, theirs, acc.x); acc.y = fmaf(pre_acc.y, theirs, acc.y);
+        acc.z = fmaf(pre_acc.z, theirs, acc.z); acc.w = fmaf(pre_acc.w, theirs, acc.w);
+        sum = fmaf(pre.y, theirs, sum);
+    }
+    return !(no_own && no_pre);
+}
+
 // Four dimensions of a row's output: acc / sum, zeros for a row that sees nothing.
 // `top`: the maximum that acc and sum are above; `exact`: kAttnWeighed, the sum of
 // the probabilities before any rounding.
 template <int MODE>
 __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, int r, int D, int dim, float4 acc, float sum, float top,
                                            float exact) {
-    if constexpr (MODE == kAttnPrefix) {
+    if constexpr (MODE == kAttnPrefix || MODE == kAttnBeside) {
         const size_t row = s.number(L, r);
         if (dim == 0) L.share_stats[row] = make_float2(top, sum);
         *reinterpret_cast<float4 *>(L.share + row * D + dim) = acc;
@@ -137,18 +162,8 @@ __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, i
     bool any = z.hi > z.lo;
     if constexpr (MODE == kAttnOwn) {
         const size_t row = s.number(L, r);
-        const float2 st = __ldcg(&L.share_stats[row]);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(L.share + row * D + dim));
-        const float both = fmaxf(top, st.x), mine = share_factor(top, sum, both), theirs = share_factor(st.x, st.y, both);
-        const bool none = !any || (top == -INFINITY && mine == 0.0f);   // (acc may hold anything)
-        acc = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(acc.x * mine, acc.y * mine, acc.z * mine, acc.w * mine);
-        sum = none ? 0.0f : sum * mine;
-        if (!(st.x == -INFINITY && theirs == 0.0f)) {
-            acc.x = fmaf(v.x, theirs, acc.x); acc.y = fmaf(v.y, theirs, acc.y);
-            acc.z = fmaf(v.z, theirs, acc.z); acc.w = fmaf(v.w, theirs, acc.w);
-            sum = fmaf(st.y, theirs, sum);
-            any = true;
-        }
+        any = join_shares(__ldcg(&L.share_stats[row]), __ldcg(reinterpret_cast<const float4 *>(L.share + row * D + dim)),
+                          any ? make_float2(top, sum) : make_float2(-INFINITY, 0.0f), acc, sum);
     }
     if constexpr (MODE == kAttnWeighed) {
         if (dim == 0)

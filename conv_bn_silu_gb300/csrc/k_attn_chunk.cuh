@@ -293,7 +293,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // CTAs of one cluster meet twice at the end, and none leaves before: whatever
     // is read there is still some CTA's, even if the lengths change meanwhile.
     const auto leave = [&] {
-        if constexpr (MODE == kAttnOwn) ptx::griddep_wait();
+        end_attention<MODE>();
         if (warp == 1) ptx::tmem_dealloc(words[0], 512);
         if (L.split == 1) return;
         cluster_sync();
@@ -718,7 +718,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     ptx::tc_fence_after();
 
     // ---------------------------------------------------------- output
-    if constexpr (MODE == kAttnOwn) ptx::griddep_wait();   // the prefix's shares
+    end_attention<MODE>();   // the prefix's shares
     const bool join = MODE != kAttnPlain || active > 1;
     if (softmax && !lost()) {
         // Float rows of a range and their (maximum, sum), for the join: where the

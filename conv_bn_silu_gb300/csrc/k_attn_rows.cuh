@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     // CTAs of one cluster meet twice at the end, and none leaves before: what is read
     // there is still some CTA's, even if the lengths change meanwhile.
     const auto leave = [&] {
-        if constexpr (MODE == kAttnOwn) ptx::griddep_wait();
+        end_attention<MODE>();
         if (L.cluster) {
             cluster_sync();
             cluster_sync();
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         __syncthreads();
     }
 
-    if constexpr (MODE == kAttnOwn) ptx::griddep_wait();   // the prefix's shares
+    end_attention<MODE>();   // the prefix's shares
     const int tile = (b * c.kv_heads + head) * L.row_tiles + rt;
     constexpr int kU = D / 4;   // units of four dimensions
     for (int i = tid; i < kRows * kU; i += kThreads) {

@@ -17,8 +17,8 @@ namespace cbs {
 
 namespace {
 
-constexpr int kThreads = 1024, kBins = 2048, kMostCtas = 8;
-static_assert(kEvictRun * 4 + kBins * 4 + 1024 <= kMaxDynSmem, "a CTA's weights and its histogram");
+constexpr int kThreads = 1024, kBins = 2048, kMostCtas = 8, kRunLeast = 2048;
+static_assert(kEvictRun * 4 + 3 * kBins * 4 + 1024 <= kMaxDynSmem, "a CTA's weights and its histogram");
 
 // A weight as a whole number of the same order; a NaN above all.
 __device__ __forceinline__ uint32_t ordered(float w) {
@@ -27,6 +27,13 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
+__device__ __forceinline__ int2 ld_cluster_pair(const int *p, uint32_t rank) {
+    uint32_t a;
+    int2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ int ld_cluster_int(const int *p, uint32_t rank) {
     uint32_t a;
     int v;
@@ -35,40 +42,52 @@ __device__ __forceinline__ int ld_cluster_int(const int *p, uint32_t rank) {
     return v;
 }
 
-// Sum of `v` over the threads before this one, for a pair of counts (16 bits are
-// too few, so two words).  `total`: over all.
+// Sum of a count over the threads before this one; one barrier.  `warps` is written
+// anew by the next call but one.
+__device__ __forceinline__ int scan(int v, int *warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const auto inclusive = [&](int s) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(~0u, s, o);
+            if (lane >= o) s += a;
+        }
+        return s;
+    };
+    const int s = inclusive(v);
+    if (lane == 31) warps[warp] = s;
+    __syncthreads();
+    const int before = __shfl_sync(~0u, inclusive(warps[lane]), warp ? warp - 1 : 0);
+    return s - v + (warp ? before : 0);
+}
+
+// The same of a pair of counts, and over all threads.
 struct Pair { int a, b; };
 __device__ __forceinline__ Pair scan(Pair v, Pair &total, Pair *warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Pair s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(~0u, s.a, o), b = __shfl_up_sync(~0u, s.b, o);
-        if (lane >= o) s.a += a, s.b += b;
-    }
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    if (warp == 0) {
-        Pair w = warps[lane];
+    const auto inclusive = [&](Pair s) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(~0u, w.a, o), b = __shfl_up_sync(~0u, w.b, o);
-            if (lane >= o) w.a += a, w.b += b;
+            const int a = __shfl_up_sync(~0u, s.a, o), b = __shfl_up_sync(~0u, s.b, o);
+            if (lane >= o) s.a += a, s.b += b;
         }
-        warps[lane] = w;
-    }
+        return s;
+    };
+    const Pair s = inclusive(v);
+    if (lane == 31) warps[warp] = s;
     __syncthreads();
-    total = warps[kThreads / 32 - 1];
-    const Pair before = warp ? warps[warp - 1] : Pair{0, 0};
-    __syncthreads();   // `warps` may be written again
-    return Pair{s.a - v.a + before.a, s.b - v.b + before.b};
+    const Pair w = inclusive(warps[lane]);
+    total = Pair{__shfl_sync(~0u, w.a, 31), __shfl_sync(~0u, w.b, 31)};
+    const int from = warp ? warp - 1 : 0, a = __shfl_sync(~0u, w.a, from), b = __shfl_sync(~0u, w.b, from);
+    return Pair{s.a - v.a + (warp ? a : 0), s.b - v.b + (warp ? b : 0)};
 }
 
 __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunch L) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // this CTA's positions, at most L.run
-    __shared__ int s_hist[kBins];
+    __shared__ int s_hist[3][kBins];
     __shared__ Pair s_warps[kThreads / 32];
-    __shared__ int s_found[2];      // a digit, and how many are to be taken of those that have it
+    __shared__ int s_totals[2][kThreads / 32];
+    __shared__ int s_found[3][2];   // a pass's digit, and how many are to be taken of those that have it
     __shared__ int s_counts[2];     // heavier than the threshold, equal to it
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -88,11 +107,15 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     // length: 32 lanes of a scan are in 32 banks.)
     const int share = (others + ctas - 1) / ctas, p0 = min(others, rank * share), m = min(others - p0, share);
     const int shift = c.page_shift, slots = 1 << shift;
+    for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
+    if (tid < 6) s_found[0][tid] = 0;
+#pragma unroll 4
     for (int i = tid; i < m; i += kThreads) {
         const int pos = p0 + i, p = page_of(c, b, pos);
         // (A page outside the pool: reported; its positions go first.)
         s_keys[i] = p < 0 ? 0u : ordered(L.mass[(((size_t)p * c.kv_heads + head) << shift) + (pos & (slots - 1))]);
     }
+    __syncthreads();
     uint32_t prefix = 0, mask = 0;   // the threshold's digits so far
     int left = take;                 // how many stay of those that share them
     // (A cluster's CTAs meet as often whatever they read: the lengths could change meanwhile.)
@@ -101,33 +124,35 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
         for (int pass = 0; pass < 3; ++pass) {
             const int shift_to = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t digits = pass == 2 ? 1023u : 2047u;
-            for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
-            __syncthreads();
-            if (tid == 0) s_found[0] = s_found[1] = 0;   // (everyone has read the last digit's)
+            int *const hist = s_hist[pass];
             for (int i = tid; i < m; i += kThreads) {
                 const uint32_t k = s_keys[i];
-                if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift_to) & digits], 1);
+                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift_to) & digits], 1);
             }
             meet();
             // Bins from the top: thread t has bins 2047 - 2t and 2046 - 2t, of all CTAs.
             const int top = kBins - 1 - 2 * tid;
             int x = 0, y = 0;
             if (ctas == 1) {
-                x = s_hist[top], y = s_hist[top - 1];
+                x = hist[top], y = hist[top - 1];
             } else {
-                for (int r = 0; r < ctas; ++r) x += ld_cluster_int(&s_hist[top], r), y += ld_cluster_int(&s_hist[top - 1], r);
+                int2 v[kMostCtas];
+#pragma unroll
+                for (int r = 0; r < kMostCtas; ++r)
+                    if (r < ctas) v[r] = ld_cluster_pair(&hist[top - 1], r);
+#pragma unroll
+                for (int r = 0; r < kMostCtas; ++r)
+                    if (r < ctas) x += v[r].y, y += v[r].x;
             }
-            Pair all;
-            const int before = scan(Pair{x + y, 0}, all, s_warps).a;
-            if (before < left && left <= before + x) s_found[0] = top, s_found[1] = left - before;
-            else if (before + x < left && left <= before + x + y) s_found[0] = top - 1, s_found[1] = left - before - x;
-            meet();   // nobody's histogram goes while another CTA reads it
-            prefix |= (uint32_t)s_found[0] << shift_to;
+            const int before = scan(x + y, s_totals[pass & 1]);
+            if (before < left && left <= before + x) s_found[pass][0] = top, s_found[pass][1] = left - before;
+            else if (before + x < left && left <= before + x + y) s_found[pass][0] = top - 1, s_found[pass][1] = left - before - x;
+            __syncthreads();
+            prefix |= (uint32_t)s_found[pass][0] << shift_to;
             mask |= digits << shift_to;
-            left = s_found[1];
+            left = s_found[pass][1];
         }
     }
-    __syncthreads();
     // Everything stays, or nothing but the recent ones, or those above `prefix` and
     // the first `left` that equal it.
     const bool all_stay = take >= others;
@@ -160,11 +185,13 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
 }
 
 // Rows of K and V by the list, and what goes with them.  D * element bytes / 16
-// threads a row, kSteps rows of each thread on their way at a time.
-constexpr int kMoveThreads = 256, kSteps = 4;
+// threads a row, kSteps rows of each thread on their way at a time: fewer a thread and
+// more CTAs hide the list's and the tables' loads better (16 sequences of 8192 to 4096
+// in bf16: four rows 124 us, two 115; in 8 bits 78 and 74, 4.9 TB/s with the choice).
+constexpr int kMoveThreads = 256, kSteps = 2;
 
 template <int ROW>   // bytes of a row
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictLaunch L) {
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const EvictLaunch L) {
     constexpr int kU = ROW / 16, kRows = kMoveThreads / kU;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -216,10 +243,13 @@ cudaError_t launch_move(const EvictLaunch &L, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_evict(EvictLaunch L, cudaStream_t s) {
-    // Positions a CTA may meet: what the table can hold, in as few CTAs as hold it.
-    const long long most = (long long)L.c.max_pages << L.c.page_shift;
+    // Positions a CTA may meet: what the table can hold, in as few CTAs as hold it, or
+    // more while each still has kRunLeast and every one an SM.  1, 2, 4 and 8 CTAs: 8
+    // heads of 16000 39, 34, 28, 34 us; 128 heads of 8192 (16 sequences, 8 bits) 74, 84.
+    const long long most = (long long)L.c.max_pages << L.c.page_shift, heads = (long long)L.c.kv_heads * L.c.batch;
+    const auto each = [&](int ctas) { return (most + ctas - 1) / ctas; };
     L.ctas = 1;
-    while (L.ctas < kMostCtas && (most + L.ctas - 1) / L.ctas > kEvictRun) L.ctas *= 2;
+    while (L.ctas < kMostCtas && (each(L.ctas) > kEvictRun || (each(2 * L.ctas) >= kRunLeast && 2 * L.ctas * heads <= current_device_sms()))) L.ctas *= 2;
     const int smem = (int)((most + L.ctas - 1) / L.ctas) * 4;
     static ContextOfDevice set;
     cudaError_t e = set_max_dyn_smem_once(evict_choose_kernel, smem, set);

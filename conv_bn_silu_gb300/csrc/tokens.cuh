@@ -158,6 +158,8 @@ cbs_status launch_attn_chunk(const AttnLaunch &L, cudaStream_t s);
 // weights of a weighed call's keys.
 cbs_status launch_attn_prefix(const AttnLaunch &L, int row_tile, cudaStream_t s);
 cbs_status launch_attn_own(const AttnLaunch &L, int row_tile, cudaStream_t s);
+cbs_status launch_attn_beside(const AttnLaunch &L, int row_tile, cudaStream_t s);
+cudaError_t launch_join_shares(const AttnLaunch &L, const float *pre, const float2 *pre_stats, cudaStream_t s);   // L's and a prefix's
 cbs_status launch_attn_weighed(const AttnLaunch &L, int row_tile, cudaStream_t s);
 cbs_status launch_attn_weights(const AttnLaunch &L, cudaStream_t s);
 constexpr int kAttnChunkRows = 256, kAttnChunkKeys = 128;

@@ -108,25 +108,55 @@ constexpr int kGridMax = 65535;
 // 51/127, 94/126, 160/127.
 constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
+// Of 152 SMs with one CTA each, that many clusters of x of the chunk kernel's CTAs run at once.
+long long chunk_rounds(long long base, int x, int sms) {
+    static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
+    const int at_once = std::max(kAtOnce[x - 1] * sms / 152, 1);
+    return (base + at_once - 1) / at_once;
+}
+int chunk_key_tiles(int keys) { return std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1); }
+
 // Ranges of keys of the chunk kernel, for `base` row tiles of all sequences and heads.
 int chunk_split(long long base, int keys, int sms) {
-    // One CTA an SM: the split with the least rounds of clusters times what a
-    // range costs.  Of 152 SMs, that many clusters of x such CTAs run at once.
-    // A key tile is one unit (1.6 us, head dimension 128), a range's start and
-    // end 4.5, a cluster's join 2 and a fifth for each CTA.  64 tokens of 32
-    // heads over 4096 keys of 8 key heads, 1 to 8 ranges: one sequence 60, 39,
-    // 30, 26, 23, 22, 21, 22 us; four sequences 61, 40, 31, 28, 47, 45, 62, 64.
+    // The split with the least rounds of clusters times what a range costs.  A key tile
+    // is one unit (1.6 us, head dimension 128), a range's start and end 4.5, a cluster's
+    // join 2 and a fifth for each CTA.  64 tokens of 32 heads over 4096 keys of 8 key
+    // heads, 1 to 8 ranges: one sequence 60, 39, 30, 26, 23, 22, 21, 22 us; four
+    // sequences 61, 40, 31, 28, 47, 45, 62, 64.
     // Less than a tenth is not worth a cluster: sequences are of unequal lengths.
-    static constexpr int kAtOnce[kAttnChunkSplitMost] = {152, 76, 46, 36, 28, 23, 15, 15};
-    const int key_tiles = std::max((keys + kAttnChunkKeys - 1) / kAttnChunkKeys, 1);
+    const int key_tiles = chunk_key_tiles(keys);
     long long best = 0;
     int split = 1;
     for (int x = 1; x <= std::min(key_tiles, kAttnChunkSplitMost); ++x) {
-        const int at_once = std::max(kAtOnce[x - 1] * sms / 152, 1);
-        const long long rounds = (base + at_once - 1) / at_once;
-        const long long cost = rounds * ((key_tiles + x - 1) / x * 10 + 45 + (x > 1 ? 20 + 2 * x : 0));
+        const long long cost = chunk_rounds(base, x, sms) * ((key_tiles + x - 1) / x * 10 + 45 + (x > 1 ? 20 + 2 * x : 0));
         if (x == 1) best = cost - cost / 10;
         else if (cost < best) best = cost, split = x;
+    }
+    return split;
+}
+
+// Its time in nanoseconds, in the same terms: a key tile's by head dimension and type.
+long long chunk_ns(const cbs_attn_desc &d, long long base, int x, int sms) {
+    const int tile = d.cache_prec == CBS_INT8 ? (d.head_dim == 64 ? 2400 : 3000) : d.head_dim == 64 ? 1400 : 1600;
+    return chunk_rounds(base, x, sms) * ((long long)((chunk_key_tiles(d.max_len) + x - 1) / x) * tile + 7200 + (x > 1 ? 3200 + 320 * x : 0));
+}
+
+// Ranges of a shared prefix, whose CTAs run beside those of the sequences' own part and
+// keep their SMs from it: the least of the two parts' end.  The own part takes its bytes at
+// 4.4 TB/s (few rows; sequences three quarters of the longest on average) or its tiles'
+// time; beside it a prefix's takes a fifth longer.  64 streams over a prefix of 8192
+// (bf16, own part of up to 1000 keys 45 us alone), 1, 2, 3, 4 and 8 ranges (8 to 64 CTAs,
+// alone 107, 62, 47, 37, 27 us): 121, 73, 57, 52, 57 us.
+int prefix_split(const cbs_shared_plan_t &p, long long base, int sms) {
+    const cbs_attn_desc &d = p.prefix.desc, &o = p.own.desc;
+    const long long bytes = (long long)o.batch * o.max_len * 3 / 4 * d.kv_heads * d.head_dim * (d.cache_prec == CBS_INT8 ? 2 : 4);
+    const long long own = p.own.kernel == CBS_ATTN_CHUNK ? chunk_ns(o, (long long)o.batch * o.kv_heads * p.own.row_tiles, p.own.split, sms)
+                                                         : bytes / 4400;
+    long long best = 0;
+    int split = 1;
+    for (int x = 1; x <= std::min(chunk_key_tiles(d.max_len), kAttnChunkSplitMost); ++x) {
+        const long long prefix = chunk_ns(d, base, x, sms) * 6 / 5, end = std::max(prefix, own + prefix * std::min<long long>(base * x, sms) / sms);
+        if (x == 1 || end < best) best = end, split = x;
     }
     return split;
 }
@@ -152,13 +182,16 @@ WeighedParts weighed_parts(const cbs_attn_plan_t &p) {
     w.all = w.scores + (p.kernel == CBS_ATTN_CHUNK ? 0 : (size_t)d.batch * d.kv_heads * w.rows_pad * w.len_pad * 4);
     return w;
 }
-struct SharedParts { size_t own, stats, share, all; };
+struct SharedParts { size_t own, stats, share, own_stats, own_share, all; };
 SharedParts shared_parts(const cbs_shared_plan_t &p) {
     SharedParts w;
     w.own = round256(p.prefix.workspace_bytes);
     w.stats = w.own + round256(p.own.workspace_bytes);
     w.share = w.stats + round256((size_t)p.max_total * p.desc.heads * 8);
-    w.all = w.share + (size_t)p.max_total * p.desc.heads * p.desc.head_dim * 4;
+    const size_t stats = w.share - w.stats, share = round256((size_t)p.max_total * p.desc.heads * p.desc.head_dim * 4);
+    w.own_stats = w.share + share;
+    w.own_share = w.own_stats + stats;
+    w.all = w.own_share + share;
     return w;
 }
 
@@ -484,13 +517,14 @@ cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, 
     const SharedParts parts = shared_parts(*p);
     char *at = static_cast<char *>(workspace);
     attn_fill(p->prefix, &pre);
+    long long prefix_base = 0;
     if (p->prefix.kernel == CBS_ATTN_CHUNK) {
         // Groups differ in size: the tiles that a call of so many tokens has, half of each
         // group's last one empty, are fewer than the largest group's for every group.
         const cbs_attn_desc &d = p->prefix.desc;
         const long long tiles = ((long long)s->total * pre.group / kAttnChunkRows) + (d.batch + 1) / 2;
-        pre.split = chunk_split(std::min<long long>(tiles, (long long)d.batch * pre.row_tiles) * d.kv_heads, d.max_len,
-                                d.num_sms > 0 ? d.num_sms : kDefaultNumSMs);
+        prefix_base = std::min<long long>(tiles, (long long)d.batch * pre.row_tiles) * d.kv_heads;
+        pre.split = prefix_split(*p, prefix_base, d.num_sms > 0 ? d.num_sms : kDefaultNumSMs);
     }
     attn_workspace(p->prefix, at, &pre);
     attn_workspace(p->own, at + parts.own, &own);
@@ -499,7 +533,18 @@ cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, 
     pre.share_stats = own.share_stats = reinterpret_cast<float2 *>(at + parts.stats);
     pre.share = own.share = reinterpret_cast<float *>(at + parts.share);
     CBS_TRY(launch_attn_prefix(pre, p->prefix.row_tile, (cudaStream_t)stream));
-    return launch_attn_own(own, p->own.row_tile, (cudaStream_t)stream);
+    // An own part of one round of CTAs waits for the prefixes' shares and joins them
+    // itself; a longer one would wait with its first round, and is joined afterwards
+    // (64 streams over a prefix of 8192, 8 ranges: 63 and 57 us).
+    const bool chunk = p->prefix.kernel == CBS_ATTN_CHUNK;
+    const int sms = p->desc.num_sms > 0 ? p->desc.num_sms : kDefaultNumSMs;
+    const long long taken = chunk ? std::min<long long>(sms, prefix_base * pre.split) : 0;
+    const int per_sm = p->own.kernel == CBS_ATTN_CHUNK ? 1 : p->desc.head_dim == 64 ? 5 : 3;
+    if (p->own.grid_ctas <= (sms - taken) * per_sm) return launch_attn_own(own, p->own.row_tile, (cudaStream_t)stream);
+    own.share_stats = reinterpret_cast<float2 *>(at + parts.own_stats);
+    own.share = reinterpret_cast<float *>(at + parts.own_share);
+    CBS_TRY(launch_attn_beside(own, p->own.row_tile, (cudaStream_t)stream));
+    return cuda_check(launch_join_shares(own, pre.share, pre.share_stats, (cudaStream_t)stream), "join launch");
 }
 
 cbs_status cbs_rmsnorm(const void *x, const void *residual, const float *weight, void *h_out, void *y, float *scale,
