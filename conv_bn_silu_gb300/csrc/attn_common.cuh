@@ -145,6 +145,49 @@ __device__ __forceinline__ bool join_shares(float2 pre, float4 pre_acc, float2 o
     return !(no_own && no_pre);
 }
 
+// A weighed row's maximum and 1 / sum; zeros for a row that sees nothing.
+__device__ __forceinline__ float2 row_stats(bool any, float top, float exact) {
+    return any ? make_float2(top == -INFINITY ? 0.0f : top, __fdiv_rn(1.0f, exact)) : make_float2(0.0f, 0.0f);
+}
+
+// A key's weight: what it was (nothing, if the key is new or decay is 0), and what came.
+__device__ __forceinline__ float weight_after(const AttnLaunch &L, const Rows &s, int key, float before, float came) {
+    return (key < s.base && L.decay != 0.0f ? L.decay * before : 0.0f) + came;
+}
+
+// The weights of the four keys from `key` on (a multiple of four) that lie before
+// `end`: of all the head's rows, from the scores that the attention left.
+template <typename Stats>
+__device__ __forceinline__ void weigh_four(const AttnLaunch &L, const Rows &s, int b, int key, int end, Stats stats_of) {
+    const CacheArgs &c = L.c;
+    const float *scores = L.scores + (size_t)(b * c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
+    float sum[4] = {};
+    for (int r = 0; r < s.R; ++r) {
+        const Seen z = s.seen(L, r);
+        if (z.hi <= key || z.lo >= key + 4) continue;
+        const float2 st = stats_of(r);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(scores + (size_t)r * L.len_pad));
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (key + i >= z.lo && key + i < z.hi) sum[i] = fmaf(frag::ex2(x[i] - st.x), st.y, sum[i]);
+    }
+    const int p = page_of(c, b, key);   // (all of them: pages hold multiples of sixteen)
+    if (p < 0) return;
+    float *mass = L.mass + (((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+    float4 before = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (L.decay != 0.0f) before = *reinterpret_cast<const float4 *>(mass);
+    const float4 after = make_float4(weight_after(L, s, key, before.x, sum[0]), weight_after(L, s, key + 1, before.y, sum[1]),
+                                     weight_after(L, s, key + 2, before.z, sum[2]), weight_after(L, s, key + 3, before.w, sum[3]));
+    if (key + 4 <= end) {
+        *reinterpret_cast<float4 *>(mass) = after;
+    } else {
+        mass[0] = after.x;
+        if (key + 1 < end) mass[1] = after.y;
+        if (key + 2 < end) mass[2] = after.z;
+    }
+}
+
 // Four dimensions of a row's output: acc / sum, zeros for a row that sees nothing.
 // `top`: the maximum that acc and sum are above; `exact`: kAttnWeighed, the sum of
 // the probabilities before any rounding.
@@ -165,10 +208,8 @@ __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, i
         any = join_shares(__ldcg(&L.share_stats[row]), __ldcg(reinterpret_cast<const float4 *>(L.share + row * D + dim)),
                           any ? make_float2(top, sum) : make_float2(-INFINITY, 0.0f), acc, sum);
     }
-    if constexpr (MODE == kAttnWeighed) {
-        if (dim == 0)
-            L.row_stats[s.number(L, r)] = any ? make_float2(top == -INFINITY ? 0.0f : top, __fdiv_rn(1.0f, exact)) : make_float2(0.0f, 0.0f);
-    }
+    if constexpr (MODE == kAttnWeighed)
+        if (dim == 0 && !L.fused) L.row_stats[s.number(L, r)] = row_stats(any, top, exact);
     if (any) {
         const float inv = __fdiv_rn(1.0f, sum);
         w.x = frag::pack_bf16(acc.x * inv, acc.y * inv);
@@ -224,9 +265,11 @@ __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b,
 
 // After a CTA has written its range's share of a tile (L.partial, L.stats):
 // the CTA that comes last joins the ranges, in their order, so that the result
-// does not depend on which one that is.  `flag`: a word of shared memory.
+// does not depend on which one that is.  `flag`: a word of shared memory; `fin`: the
+// rows' statistics there (kAttnWeighed).  Returns whether this CTA was the last.
 template <int D, int kRows, int kThreads, int MODE>
-__device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, int tile, int r0, int active, int tid, int *flag) {
+__device__ __forceinline__ bool join_ranges(const AttnLaunch &L, const Rows &s, int tile, int r0, int active, int tid, int *flag,
+                                            float2 *fin) {
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -235,7 +278,7 @@ __device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, 
         if (*flag) L.counters[tile] = 0u;   // ready for the next call
     }
     __syncthreads();
-    if (!*flag) return;
+    if (!*flag) return false;
     __threadfence();
     constexpr int kU = D / 4;   // units of four dimensions
     for (int i = tid; i < kRows * kU; i += kThreads) {
@@ -257,7 +300,12 @@ __device__ __forceinline__ void join_ranges(const AttnLaunch &L, const Rows &s, 
             if constexpr (MODE == kAttnWeighed) exact = fmaf(__ldcg(&L.sums[at + (size_t)x * kRows]), fac, exact);
         }
         store_out4<MODE>(L, s, r0 + r, D, 4 * u, acc, sum, top, exact);
+        if constexpr (MODE == kAttnWeighed) {
+            const Seen z = s.seen(L, r0 + r);
+            if (u == 0) fin[r] = row_stats(z.hi > z.lo, top, exact);
+        }
     }
+    return true;
 }
 
 }  // namespace cbs

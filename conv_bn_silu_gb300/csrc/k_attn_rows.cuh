@@ -29,8 +29,8 @@
 //
 // What the modes add (AttnMode): a group's prefix gives the rows' unnormalised
 // shares, the sequences' own keys are joined with them, and a weighed call also
-// writes every score and each row's maximum and sum, from which
-// k_attn_weights.cu has the weights of a key without reading it again.
+// writes every score, from which whoever knows the rows' maxima and sums at the end
+// has the weights of a key without reading it again.
 #pragma once
 
 #include "attn_common.cuh"
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     // kAttnWeighed: sums of the probabilities before they are rounded (in 8 bits s_l has those).
     constexpr bool kExact = MODE == kAttnWeighed;
     __shared__ float s_x[kExact ? kWarps : 1][kRows], s_statx[kExact ? kRows : 1];
+    __shared__ float2 s_fin[kExact ? kRows : 1];   // the rows' maxima and 1 / sums over all ranges
     __shared__ int s_flag;
     begin_attention<MODE>();
     ptx::griddep_launch_dependents();
@@ -467,6 +468,10 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         }
         if (active == 1) {
             store_out4<MODE>(L, rs, r0 + r, D, 4 * u, acc, sum, top, exact);
+            if constexpr (kExact) {
+                const Seen z = rs.seen(L, r0 + r);
+                if (u == 0) s_fin[r] = row_stats(z.hi > z.lo, top, exact);
+            }
         } else if (L.cluster) {   // (a unit's own place, which nobody else has read)
             *reinterpret_cast<float4 *>(&s_o[0][r][4 * u]) = acc;
             if (u == 0) s_stat[r] = make_float2(top, sum);
@@ -480,14 +485,44 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
                 if (u == 0) L.sums[at] = exact;
         }
     }
+    // A weighed call's keys [from, to): the rows' statistics are in s_fin.
+    const auto weigh = [&](int from, int to) {
+        __syncthreads();
+        for (int key = from + 4 * tid; key < to; key += 4 * kThreads) weigh_four(L, rs, b, key, to, [&](int r) { return s_fin[r]; });
+    };
+    const int end = min(len, L.len_pad);   // (of a weighed call)
+    if (kExact && L.fused && sp == 0 && tid == 0 && len > L.len_pad) atomicOr(c.status, kStatusBadIndex);
     if (!L.cluster) {
-        if (active > 1) join_ranges<D, kRows, kThreads, MODE>(L, rs, tile, r0, active, tid, &s_flag);
+        const bool mine = active == 1 || join_ranges<D, kRows, kThreads, MODE>(L, rs, tile, r0, active, tid, &s_flag, s_fin);
+        if constexpr (kExact)
+            if (L.fused && mine) weigh(0, end);
         return;
     }
     // The ranges of a cluster, in their order, from the CTAs' shared memory: each
     // CTA finishes some of the units.
     __syncthreads();
     cluster_sync();
+    if constexpr (kExact) {
+        if (L.fused && active > 1 && tid < R) {   // (one tile of rows)
+            const uint32_t at = ptx::smem_u32(&s_stat[tid]), x_at = ptx::smem_u32(&s_statx[tid]);
+            float2 st[kAttnClusterMost];
+            float sx[kAttnClusterMost], top = -INFINITY, exact = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x)
+                if (x < active) st[x] = ld_cluster2(at, x), sx[x] = ld_cluster1(x_at, x);
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x)
+                if (x < active) top = fmaxf(top, st[x].x);
+#pragma unroll
+            for (int x = 0; x < kAttnClusterMost; ++x) {
+                if (x >= active) break;
+                const float fac = share_factor(st[x].x, st[x].y, top);
+                if (!(st[x].x == -INFINITY && fac == 0.0f)) exact = fmaf(sx[x], fac, exact);
+            }
+            const Seen z = rs.seen(L, tid);
+            s_fin[tid] = row_stats(z.hi > z.lo, top, exact);
+        }
+    }
     if (active > 1) {
         for (int i = sp * kThreads + tid; i < kRows * kU; i += active * kThreads) {
             const int r = i / kU, u = i % kU;
@@ -511,12 +546,16 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
                 acc.x = fmaf(v[x].x, fac, acc.x); acc.y = fmaf(v[x].y, fac, acc.y);
                 acc.z = fmaf(v[x].z, fac, acc.z); acc.w = fmaf(v[x].w, fac, acc.w);
                 sum = fmaf(st[x].y, fac, sum);
-                if constexpr (kExact) exact = fmaf(ld_cluster1(ptx::smem_u32(&s_statx[r]), x), fac, exact);
+                if constexpr (kExact)   // (a few-row call's own weights have it already)
+                    if (!L.fused) exact = fmaf(ld_cluster1(ptx::smem_u32(&s_statx[r]), x), fac, exact);
             }
             store_out4<MODE>(L, rs, r0 + r, D, 4 * u, acc, sum, top, exact);
         }
     }
     __syncthreads();
+    if constexpr (kExact) {   // each range's CTA its own keys, the first and the last also what nobody sees
+        if (L.fused) weigh(sp == 0 ? 0 : lo16 + b0 * kBlock, sp == active - 1 ? end : min(end, lo16 + b1 * kBlock));
+    }
     cluster_sync();   // nobody's rows go while another CTA reads them
 }
 

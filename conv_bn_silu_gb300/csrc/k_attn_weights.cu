@@ -8,7 +8,8 @@
 // added atomically and equal calls give equal results.
 //
 // Few rows: the attention left its scores, 4 bytes a row and key where the key itself
-// has 64 to 256, and the first kernel sums them up.  Chunks would leave too many: the
+// has 64 to 256.  Where one tile holds a head's rows it sums them up itself, in the CTAs
+// that know the rows' sums; else the first kernel here does.  Chunks would leave too many: the
 // second kernel takes the first product again, S^T = K Q^T on tcgen05 with 128 keys as
 // the lanes of tensor memory.  A key tile stays where it is while the rows' tiles
 // pass, and a thread's sum over them never leaves its registers.  The exponentials
@@ -34,11 +35,6 @@ __device__ __forceinline__ Rows rows_again(const AttnLaunch &L, int b, int head)
     return s;
 }
 
-// A key's weight: what it was, and what came.
-__device__ __forceinline__ float weight_after(const AttnLaunch &L, const Rows &s, int key, float before, float came) {
-    return (key < s.base && L.decay != 0.0f ? L.decay * before : 0.0f) + came;
-}
-
 constexpr int kSumThreads = 128, kSumKeys = 4;   // keys of a thread
 
 __global__ void __launch_bounds__(kSumThreads) weights_of_scores_kernel(const AttnLaunch L) {
@@ -51,24 +47,7 @@ __global__ void __launch_bounds__(kSumThreads) weights_of_scores_kernel(const At
     if (rs.len > L.len_pad && threadIdx.x == 0) atomicOr(c.status, kStatusBadIndex);
     const int key = (blockIdx.x * kSumThreads + threadIdx.x) * kSumKeys, end = min(rs.len, L.len_pad);
     if (key >= end) return;
-    const float *scores = L.scores + (size_t)(b * c.kv_heads + head) * L.rows_pad * L.len_pad + key;
-    float sum[kSumKeys] = {};
-    for (int r = 0; r < rs.R; ++r) {
-        const Seen z = rs.seen(L, r);
-        if (z.hi <= key || z.lo >= key + kSumKeys) continue;
-        const float2 st = __ldg(&L.row_stats[rs.number(L, r)]);
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(scores + (size_t)r * L.len_pad));
-        const float s[kSumKeys] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < kSumKeys; ++i)
-            if (key + i >= z.lo && key + i < z.hi) sum[i] = fmaf(frag::ex2(s[i] - st.x), st.y, sum[i]);
-    }
-    const int p = page_of(c, b, key);   // (all of them: pages hold multiples of sixteen)
-    if (p < 0) return;
-    float *mass = L.mass + (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-#pragma unroll
-    for (int i = 0; i < kSumKeys; ++i)
-        if (key + i < end) mass[i] = weight_after(L, rs, key + i, mass[i], sum[i]);
+    weigh_four(L, rs, b, key, end, [&](int r) { return __ldg(&L.row_stats[rs.number(L, r)]); });
 }
 
 // ------------------------------------------------------------------- chunks
@@ -435,7 +414,7 @@ cbs_status launch_chunk_weights(const AttnLaunch &L, cudaStream_t s) {
 }  // namespace
 
 cbs_status launch_attn_weights(const AttnLaunch &L, cudaStream_t s) {
-    if (L.scores) {
+    if (L.scores) {   // (row tiles' shares of a key's weight)
         const int keys = kSumThreads * kSumKeys;
         return cuda_check(launch_kernel(weights_of_scores_kernel, dim3((L.len_pad + keys - 1) / keys, L.c.kv_heads, L.c.batch), kSumThreads, 0, s, L),
                           "weights launch");

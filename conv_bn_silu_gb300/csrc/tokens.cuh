@@ -134,7 +134,7 @@ struct AttnLaunch {
     // scores [batch][kv_heads][rows_pad][len_pad] of the few-row kernels.
     float2 *row_stats;
     float *sums, *scores, *mass;
-    int rows_pad, len_pad;
+    int rows_pad, len_pad, fused;   // fused: the few-row kernels sum the weights up themselves
     float decay;
 };
 // set_max_dyn_smem, once in a context: a call's host time is a small call's whole

@@ -467,8 +467,13 @@ cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c
     if (a.kernel != CBS_ATTN_CHUNK) L.scores = reinterpret_cast<float *>(at + w.scores);
     L.mass = mass;
     L.decay = decay;
+    // Few rows in one tile: the CTAs of a cluster weigh their own keys, and so does one
+    // CTA without ranges (one token over 1000 keys 10.8 -> 9.x us; 64 sequences of 300
+    // 26.7 -> 24.4).  Of ranges joined by the CTA that finishes last, that one would weigh
+    // all of them (32 sequences of up to 8192: 136 -> 159).
+    L.fused = L.scores && a.row_tiles == 1 && (L.cluster || a.split == 1);
     CBS_TRY(launch_attn_weighed(L, a.row_tile, (cudaStream_t)stream));
-    return launch_attn_weights(L, (cudaStream_t)stream);
+    return L.fused ? CBS_OK : launch_attn_weights(L, (cudaStream_t)stream);
 }
 
 cbs_status cbs_shared_plan(const cbs_shared_desc *d, cbs_shared_plan_t *out) {
