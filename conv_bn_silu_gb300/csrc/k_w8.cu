@@ -34,6 +34,7 @@ constexpr int kOut = 128;                    // outputs of a CTA: tensor memory'
 constexpr int kStageK = 128;                 // codes along k in a stage: a row of 128 bytes
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr int kShareMost = 8;                // shares of k: CTAs of a cluster
+constexpr int kPitch = kOut + 4;             // floats of a row of a share's sums
 
 // kN: input rows of a tile; kPair: CTAs that share it.
 template <int kN, int kPair>
@@ -41,17 +42,23 @@ struct W8Tile {
     static constexpr int kRows = kN / kPair;                 // input rows a CTA widens
     static constexpr int kW = kOut * 128, kRaw = kW + kRows * 128;
     static constexpr int kOp = kRows * 256;                  // a stage of B: two panels of 64
-    static constexpr int kStages = kN == 16 ? 5 : kN == 32 ? 4 : kN == 64 ? 3 : 4;
-    static constexpr int kOps = kN <= 64 ? 2 : 3;
+    static constexpr int kStages = kN == 64 ? 2 : 4;
+    static constexpr int kOps = kN <= 32 ? 2 : 3;
     // Warps that widen inputs, and the groups of them that take stages in turn: a
     // group then has two stages' time for its loads, stores and fence.
-    static constexpr int kWiden = kRows >= 128 ? 8 : kRows / 16, kTurns = kRows >= 128 ? 2 : 1;
+    static constexpr int kWiden = kRows >= 128 ? 8 : kRows / 16, kTurns = kRows >= 32 ? 2 : 1;
+    // A wait knows a barrier's turns apart only while it is less than two behind.  Loads
+    // land out of order, so whoever takes stages in turn has to see every turn of its
+    // slots: their number is a multiple of two (weights) and of kTurns.  A group's last
+    // stage waited for an MMA kTurns + kOps stages back, and MMAs end in order: with no
+    // more groups than places of B, that place's turn before the last one has ended.
+    static_assert(kStages % 2 == 0 && kStages % kTurns == 0 && kTurns <= kOps, "turns");
     static constexpr int kStoreWarps = kWiden >= 8 ? 16 : 8;   // at the end: each has 32 outputs of its part of the rows
     static constexpr int kWarpMma = 8 + kWiden, kWarpTma = kWarpMma + 1, kThreads = (kWarpTma + 1) * 32;
     static constexpr int kOpAt = kStages * kRaw, kBars = kOpAt + kOps * kOp;
     // Places of A in tensor memory, a stage each: from a place's MMA back to its next one
     // takes some 2500 cycles of hand-offs, so as many as fit.
-    static constexpr int kABufs = kN >= 128 ? 4 : 2, kACols = kStageK / 2;
+    static constexpr int kABufs = kN >= 128 ? 4 : 3, kACols = kStageK / 2;
     static constexpr int kTmem = kABufs * kACols + kN <= 256 ? 256 : 512;
     // raw_full[], raw_empty[], b_ready[], b_free[], peer[], a_ready[], a_free[], done;
     // TMEM address, flag; the input rows' scales
@@ -59,7 +66,7 @@ struct W8Tile {
     static constexpr int kScales = kBars + kNumBars * 8 + 16, kSmem = kScales + kN * 4;
     static_assert(kABufs * kACols + kN <= 512 && kScales % 8 == 0 && kRaw % 1024 == 0 && kOp % 1024 == 0, "tensor memory; operands at multiples of 1 KB");
     static_assert(kSmem <= kMaxDynSmem, "shared memory");
-    static_assert(kPair == 2 || kN * (kOut + 1) * 4 <= kBars, "a share's sums fit where the stages were");
+    static_assert(kPair == 2 || kN * kPitch * 4 <= kBars, "a share's sums fit where the stages were");
 };
 
 // Another CTA's barrier.  What this announces lies in the sender's own shared and
@@ -266,37 +273,45 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         // Sixteen codes a unit, eight units a row.  Lanes of a row's second 64 write
         // their upper half first: eight lanes are then in eight different sixteen-byte
         // banks.
-        constexpr int kLanes = C::kWiden / C::kTurns * 32, kPer = C::kRows * 8 / kLanes;
+        constexpr int kLanes = C::kWiden / C::kTurns * 32, kPer = C::kRows * 8 / kLanes, kOnce = kPer < 8 ? kPer : 8;
         const int turn = (tid - 256) / kLanes, t = (tid - 256) % kLanes, u = t & 7, row0 = t >> 3;
         const uint32_t second = u >> 2;
         for (int i = turn; i < ns; i += C::kTurns) {
             const int slot = i % C::kStages, op = i % C::kOps;
             bool ok = wait(raw_full(slot), (i / C::kStages) & 1);
             if (!__all_sync(~0u, ok)) break;
-            uint4 raw[kPer];
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int row = row0 + x * (kLanes / 8);
-                raw[x] = *reinterpret_cast<const uint4 *>(smem + slot * C::kRaw + C::kW + row * 128 + ((u ^ (row & 7)) << 4));
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(raw_empty(slot));
-            ok = wait(b_free(op), (i / C::kOps + 1) & 1) && !lost();
-            if (!__all_sync(~0u, ok)) break;
             unsigned char *const to = smem + C::kOpAt + op * C::kOp + (u >> 2) * C::kRows * 128;
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int row = row0 + x * (kLanes / 8);
-                uint32_t o[8];
-                frag::i8_halves(raw[x].x, o[0], o[1]);
-                frag::i8_halves(raw[x].y, o[2], o[3]);
-                frag::i8_halves(raw[x].z, o[4], o[5]);
-                frag::i8_halves(raw[x].w, o[6], o[7]);
-                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                const uint32_t at = row * 128 + ((((u & 3) * 2 + second) ^ (row & 7)) << 4);
-                *reinterpret_cast<uint4 *>(to + at) = second ? hi : lo;
-                *reinterpret_cast<uint4 *>(to + (at ^ 16)) = second ? lo : hi;
+            for (int pass = 0; pass < kPer / kOnce; ++pass) {
+                uint4 raw[kOnce];
+#pragma unroll
+                for (int x = 0; x < kOnce; ++x) {
+                    const int row = row0 + (pass * kOnce + x) * (kLanes / 8);
+                    raw[x] = *reinterpret_cast<const uint4 *>(smem + slot * C::kRaw + C::kW + row * 128 + ((u ^ (row & 7)) << 4));
+                }
+                if (pass == kPer / kOnce - 1) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(raw_empty(slot));
+                }
+                if (pass == 0) {
+                    ok = wait(b_free(op), (i / C::kOps + 1) & 1) && !lost();
+                    if (!__all_sync(~0u, ok)) break;
+                }
+#pragma unroll
+                for (int x = 0; x < kOnce; ++x) {
+                    const int row = row0 + (pass * kOnce + x) * (kLanes / 8);
+                    uint32_t o[8];
+                    frag::i8_halves(raw[x].x, o[0], o[1]);
+                    frag::i8_halves(raw[x].y, o[2], o[3]);
+                    frag::i8_halves(raw[x].z, o[4], o[5]);
+                    frag::i8_halves(raw[x].w, o[6], o[7]);
+                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                    const uint32_t at = row * 128 + ((((u & 3) * 2 + second) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(to + at) = second ? hi : lo;
+                    *reinterpret_cast<uint4 *>(to + (at ^ 16)) = second ? lo : hi;
+                }
             }
+            if (!__all_sync(~0u, ok)) break;
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(b_ready(op));
@@ -367,7 +382,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             for (int e = 0; e < kPart; ++e) {
                 const int m = m0 + col + e;
                 if (kPair == 1 && split > 1) {
-                    sum[(col + e) * (kOut + 1) + row] = __uint_as_float(v[e]);
+                    sum[(col + e) * kPitch + row] = __uint_as_float(v[e]);
                 } else if (m < L.rows && n < L.n) {
                     float y = __uint_as_float(v[e]) * (xs[col + e] * ws) + bias;
                     if (L.act == CBS_ACT_SILU) y = silu(y);
@@ -383,17 +398,39 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     else __syncthreads();
     if (warp == C::kWarpMma) T::dealloc(tmem, C::kTmem);
     if (kPair > 1 || split == 1) return;
+    // Four outputs of a row at a time, every share's on their way together.
     const int rows = min(kN, L.rows - m0);
-    for (int i = tid + share * C::kThreads; i < kOut * rows; i += C::kThreads * split) {
-        const int m = i / kOut, nn = i % kOut, n = n0 + nn;
+    for (int i = tid + share * C::kThreads; i < kOut / 4 * rows; i += C::kThreads * split) {
+        const int m = i / (kOut / 4), nn = i % (kOut / 4) * 4, n = n0 + nn;
         if (n >= L.n) continue;
-        float y = 0.0f;
-        for (int p = 0; p < split; ++p) y += ld_cluster1(sbase + (m * (kOut + 1) + nn) * 4, p);
-        y = y * (L.x_scale[m0 + m] * L.w_scale[n]) + (L.bias ? L.bias[n] : 0.0f);
-        if (L.act == CBS_ACT_SILU) y = silu(y);
+        const uint32_t from = sbase + (m * kPitch + nn) * 4;
+        float4 v[kShareMost];
+#pragma unroll
+        for (int p = 0; p < kShareMost; ++p)
+            if (p < split) v[p] = ld_cluster4(from, p);
+        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+        for (int p = 1; p < kShareMost; ++p)
+            if (p < split) y[0] += v[p].x, y[1] += v[p].y, y[2] += v[p].z, y[3] += v[p].w;
+        const float x_scale = xs[m];
         const size_t at = (size_t)(m0 + m) * L.n + n;
-        if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at] = __float2bfloat16_rn(y);
-        else static_cast<float *>(L.y)[at] = y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (n + e >= L.n) break;
+            y[e] = y[e] * (x_scale * L.w_scale[n + e]) + (L.bias ? L.bias[n + e] : 0.0f);
+            if (L.act == CBS_ACT_SILU) y[e] = silu(y[e]);
+        }
+        if (L.n % 4 == 0) {
+            if (L.out_bf16) *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(L.y) + at) = make_uint2(frag::pack_bf16(y[0], y[1]), frag::pack_bf16(y[2], y[3]));
+            else *reinterpret_cast<float4 *>(static_cast<float *>(L.y) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (n + e >= L.n) break;
+                if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at + e] = __float2bfloat16_rn(y[e]);
+                else static_cast<float *>(L.y)[at + e] = y[e];
+            }
+        }
     }
     cluster_sync();   // nobody's sums go while another CTA reads them
 }
@@ -465,12 +502,13 @@ __global__ void quantize_w8_kernel(const float *__restrict__ w, int n, int k, in
 // sizes of 256 x 1024 to 16384 x 8192, 1 to 6400 rows, every tile with 1 to 8 shares):
 // a CTA's start and end and each of its stages, alone on its SM and, for the tiles of
 // which two fit, for two side by side; and a share's part of the join.  What it takes
-// is 3% slower than the best on average and 20% at worst but for one (256 x 1024, 1600
-// rows: 9.5 us for 7.0).
+// is 0.8% slower than the best on average and 13% at worst (256 x 1024, 1600 rows: 7.2
+// us for 6.4).
 struct W8Cost { int rows, alone, stage, two, stage2, share; };
-constexpr W8Cost kCosts[] = {{16, 180, 47, 350, 61, 13}, {32, 200, 47, 380, 68, 28}, {64, 270, 53, 510, 79, 34},
-                             {128, 540, 49, 0, 0, 56}, {256, 560, 56, 0, 0, 0}};
-
+constexpr W8Cost kCosts[] = {{16, 134, 47, 140, 71, 15}, {32, 168, 39, 188, 67, 20}, {64, 208, 53, 241, 88, 16},
+                             {128, 410, 49, 0, 0, 12}, {256, 606, 56, 0, 0, 0}};
+// Of 152 SMs with a CTA each, that many clusters of 1, 2, 4 and 8 run at once.
+constexpr int kAtOnce[] = {152, 76, 36, 15};
 //
 // Few rows go to k_w8_few.cu: its time and this file's, one row: 1001 x 2064 4.0 and 5.6
 // us, 4096 x 4096 5.1 and 8.1, 6144 x 4096 6.6 and 9.1, 8192 x 8192 14.6 and 15.9, 16384 x
@@ -488,14 +526,16 @@ cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
     int rows = 0, split = 1;
     for (const W8Cost &c : kCosts) {
         if (rows && c.rows >= 2 * L.rows) break;   // (half of a larger tile would be empty)
-        for (int x = 1; x <= (c.rows == 256 ? 1 : kShareMost) && (x == 1 || 2 * x <= stages); x *= 2) {
-            const long long each = (stages + x - 1) / x, row_tiles = (L.rows + c.rows - 1) / c.rows;
+        const long long row_tiles = (L.rows + c.rows - 1) / c.rows;
+        for (int i = 0; i < (c.rows == 256 ? 1 : 4) && (i == 0 || 2 << i <= stages); ++i) {
+            const int x = 1 << i;
+            const long long each = (stages + x - 1) / x;
             long long cost;
             if (c.rows == 256) {   // pairs of CTAs
                 const long long pairs = std::max(sms / 2, 1ll), tiles = (L.n + 2 * kOut - 1) / (2 * kOut) * row_tiles;
                 cost = (tiles + pairs - 1) / pairs * (c.alone + each * c.stage);
             } else {
-                const long long per = ((L.n + kOut - 1) / kOut * row_tiles * x + sms - 1) / sms;
+                const long long at_once = std::max(kAtOnce[i] * sms / 152, 1ll), per = ((L.n + kOut - 1) / kOut * row_tiles + at_once - 1) / at_once;
                 cost = c.two ? per / 2 * (c.two + each * c.stage2) + per % 2 * (c.alone + each * c.stage) : per * (c.alone + each * c.stage);
                 if (x > 1) cost += x * c.share;
             }
