@@ -161,22 +161,33 @@ template <typename Stats>
 __device__ __forceinline__ void weigh_four(const AttnLaunch &L, const Rows &s, int b, int key, int end, Stats stats_of) {
     const CacheArgs &c = L.c;
     const float *scores = L.scores + (size_t)(b * c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
-    float sum[4] = {};
-    for (int r = 0; r < s.R; ++r) {
-        const Seen z = s.seen(L, r);
-        if (z.hi <= key || z.lo >= key + 4) continue;
-        const float2 st = stats_of(r);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(scores + (size_t)r * L.len_pad));
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (key + i >= z.lo && key + i < z.hi) sum[i] = fmaf(frag::ex2(x[i] - st.x), st.y, sum[i]);
-    }
     const int p = page_of(c, b, key);   // (all of them: pages hold multiples of sixteen)
     if (p < 0) return;
     float *mass = L.mass + (((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
     float4 before = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (L.decay != 0.0f) before = *reinterpret_cast<const float4 *>(mass);
+    float sum[4] = {};
+    constexpr int kOnce = 4;   // rows on their way together
+    for (int r0 = 0; r0 < s.R; r0 += kOnce) {
+        float4 v[kOnce];
+        float2 st[kOnce];
+        Seen z[kOnce];
+#pragma unroll
+        for (int x = 0; x < kOnce; ++x) {
+            z[x] = r0 + x < s.R ? s.seen(L, r0 + x) : Seen{0, 0};
+            if (z[x].hi <= key || z[x].lo >= key + 4) continue;
+            st[x] = stats_of(r0 + x);
+            v[x] = __ldcg(reinterpret_cast<const float4 *>(scores + (size_t)(r0 + x) * L.len_pad));
+        }
+#pragma unroll
+        for (int x = 0; x < kOnce; ++x) {
+            if (z[x].hi <= key || z[x].lo >= key + 4) continue;
+            const float y[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key + i >= z[x].lo && key + i < z[x].hi) sum[i] = fmaf(frag::ex2(y[i] - st[x].x), st[x].y, sum[i]);
+        }
+    }
     const float4 after = make_float4(weight_after(L, s, key, before.x, sum[0]), weight_after(L, s, key + 1, before.y, sum[1]),
                                      weight_after(L, s, key + 2, before.z, sum[2]), weight_after(L, s, key + 3, before.w, sum[3]));
     if (key + 4 <= end) {

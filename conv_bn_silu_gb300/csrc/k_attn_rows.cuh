@@ -222,6 +222,15 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         for (int i = 0; i < D * (I8 ? 1 : 2); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
     };
 
+    float *scores[kExact ? NR : 1][2];   // of this lane's rows
+    if constexpr (kExact) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                scores[n][i] = L.scores + ((size_t)(b * c.kv_heads + head) * L.rows_pad + r0 + n * 8 + 2 * j + i) * L.len_pad;
+    }
+
     F f;
     int blk = b0 + warp;
     unsigned live, live_next;
@@ -297,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = r0 + n * 8 + 2 * j + (i & 1), key = pos + g + 8 * (i >> 1);
-                    if (r < R && key < L.len_pad)
-                        L.scores[((size_t)(b * c.kv_heads + head) * L.rows_pad + r) * L.len_pad + key] = s[n][i];
+                    if (r < R && key < L.len_pad) scores[n][i & 1][key] = s[n][i];
                 }
         }
         // ---- running maximum
