@@ -13,6 +13,12 @@ One layer, for a prefix as for one new token:
     h, y8   = rmsnorm(h + out(a))
     delta   = down(silu(up(y8)))
 
+`AnswerHead` gives several answers about each image: the cells go through 8-bit
+products, a row's weight for the others is added up while they attend to one another,
+and the heaviest of them stay as the one prefix that all of an image's answers share.
+
+    python -m conv_bn_silu_gb300.token_head --answers 6 [--keep 100]
+
 The weights are random: there is nothing to learn here, only to run.  PyTorch
 looks up embeddings, picks the largest logit and holds the buffers; a step of
 one token each is captured in a CUDA graph, whose launches all read the same
@@ -25,7 +31,8 @@ import argparse
 import torch
 
 from . import _binding as B
-from .tokens import LinearW4, PagedAttention, PagedCache, dequantize_rows, rmsnorm
+from .tokens import (LinearW4, LinearW8, PagedAttention, PagedCache, SharedPrefixAttention, WeighedAttention, dequantize_rows,
+                     rmsnorm)
 
 EPS = 1e-5
 
@@ -148,21 +155,137 @@ class TokenHead:
         return self.caches[layer].read(self.seq_lens, self.page_table, self.max_len)
 
 
+class AnswerLayer:
+    """As Layer; products whose inputs are 8-bit rows have 8-bit weights, for a
+    prefix's thousands of rows as for an answer's token."""
+
+    def __init__(self, width, heads, kv_heads, head_dim, hidden, weights):
+        q_width, kv_width = heads * head_dim, kv_heads * head_dim
+        self.norm1, self.norm2 = weights.norm(width), weights.norm(width)
+        self.qkv = LinearW8.quantize(weights.normal(q_width + 2 * kv_width, width) * width ** -0.5)
+        self.out = weights.linear(width, q_width)
+        self.up = LinearW8.quantize(weights.normal(hidden, width) * width ** -0.5, activation=B.CBS_ACT_SILU)
+        self.down = weights.linear(width, hidden)
+
+
+class AnswerHead:
+    """`answers` sequences of up to max_answer tokens about each of `images`, over
+    the `keep` cells of the image's prefix that the others looked at most (each
+    key head's own choice)."""
+
+    def __init__(self, images: int, answers: int, cells: int = 400, keep: int = 100, width: int = 256, max_answer: int = 64,
+                 layers: int = 2, heads: int = 8, kv_heads: int = 2, head_dim: int = 64, hidden: int = 1024, vocabulary: int = 512,
+                 page: int = 16, seed: int = 0, device="cuda"):
+        if images < 1 or answers < 1 or cells < 1 or max_answer < 1 or not 1 <= keep <= cells:
+            raise ValueError(f"{answers} answers of {max_answer} about {images} images of {cells} cells, {keep} kept")
+        weights = _Weights(seed, device)
+        self.images, self.answers, self.cells, self.keep, self.max_answer = images, answers, cells, keep, max_answer
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.layers = [AnswerLayer(width, heads, kv_heads, head_dim, hidden, weights) for _ in range(layers)]
+        self.norm, self.logits_of = weights.norm(width), LinearW8.quantize(weights.normal(vocabulary, width) * width ** -0.5)
+        self.embedding = weights.normal(vocabulary, width).to(torch.bfloat16)
+        # Pages: the images' cells, what of them stays, the answers' own tokens.
+        batch = images * answers
+        counts = [(images, -(-cells // page)), (images, -(-keep // page)), (batch, -(-max_answer // page))]
+        tables, first = [], 0
+        for rows, pages in counts:
+            tables.append(torch.arange(first, first + rows * pages, dtype=torch.int32, device=device).view(rows, pages))
+            first += rows * pages
+        self.cell_table, self.prefix_table, self.page_table = tables
+        int32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)   # noqa: E731
+        self.cell_lens = int32(images) + cells
+        self.prefix_lens, self.seq_lens = int32(images) + keep, int32(batch)
+        self.cell_starts = torch.arange(0, images * cells + 1, cells, dtype=torch.int32, device=device)
+        self.starts = torch.arange(batch + 1, dtype=torch.int32, device=device)
+        self.group_start = torch.arange(0, batch + 1, answers, dtype=torch.int32, device=device)
+        self.caches = [PagedCache.empty(first, kv_heads, page, head_dim, device=device) for _ in self.layers]
+        self.mass = torch.zeros((first, kv_heads, page), device=device)
+        self.prefix = [WeighedAttention(c, images, cells, cells, heads, causal=False) for c in self.caches]
+        self.single = [SharedPrefixAttention(c, batch, images, 1, max_answer, keep, heads, max_group_new=answers) for c in self.caches]
+        self.kept = [None] * layers
+        self.token = torch.zeros(batch, dtype=torch.int64, device=device)
+        self.graph = None
+
+    def _run(self, h, attend):
+        delta = None
+        for i, layer in enumerate(self.layers):
+            y, scale, h = rmsnorm(h, layer.norm1, EPS, residual=delta, int8=True)
+            qkv = layer.qkv(y, scale).view(-1, self.heads + 2 * self.kv_heads, self.head_dim)
+            a = attend(i, *qkv.split((self.heads, self.kv_heads, self.kv_heads), dim=1))
+            y, scale, h = rmsnorm(h, layer.norm2, EPS, residual=layer.out(a.flatten(1)), int8=True)
+            delta = layer.down(layer.up(y, scale))
+        return h, delta
+
+    def start(self, cells: torch.Tensor):
+        """The images' cells (bfloat16 [images, ..., width]) into the caches, and
+        what stays of them into the prefixes."""
+        h = cells.reshape(-1, cells.shape[-1])
+        if h.shape[0] != self.images * self.cells:
+            raise ValueError(f"{h.shape[0]} cells for {self.images} images of {self.cells}")
+
+        def attend(i, q, k, v):
+            cache = self.caches[i]
+            cache.write(k, v, self.cell_starts, self.cell_lens, self.cell_table)
+            a = self.prefix[i](q, self.cell_starts, self.cell_lens, self.cell_table, self.mass, decay=0.0)
+            self.kept[i], _ = cache.evict(self.mass, self.cell_lens, self.cell_table, self.prefix_table, self.keep)
+            return a
+        self._run(h, attend)
+        self.seq_lens.zero_()
+
+    def step(self, token: torch.Tensor) -> torch.Tensor:
+        """One token (int64 [images * answers]) of each answer; the logits that
+        follow it."""
+        self.seq_lens += 1
+
+        def attend(i, q, k, v):
+            self.caches[i].write(k, v, self.starts, self.seq_lens, self.page_table)
+            return self.single[i](q, self.starts, self.seq_lens, self.page_table, self.group_start, self.prefix_lens, self.prefix_table)
+        h, delta = self._run(self.embedding[token], attend)
+        y, scale, _ = rmsnorm(h, self.norm, EPS, residual=delta, int8=True)
+        return self.logits_of(y, scale, dtype=torch.float32)
+
+    def _advance(self):
+        self.token.copy_(self.step(self.token).argmax(1))
+
+    def answer(self, cells: torch.Tensor, first: torch.Tensor, tokens: int) -> torch.Tensor:
+        """The `tokens` tokens that follow each answer's first one (int64 [images,
+        answers], what it is asked), int64 [images, answers, tokens]."""
+        if tokens < 1 or tokens > self.max_answer:
+            raise ValueError(f"{tokens} tokens: at most {self.max_answer}")
+        self.start(cells)
+        if self.graph is None:
+            self._advance()   # (everything a launch needs is set up before a capture)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                self._advance()
+            self.graph = graph
+            self.seq_lens.zero_()
+        self.token.copy_(first.reshape(-1))
+        out = torch.empty((self.images * self.answers, tokens), dtype=torch.int64, device=self.token.device)
+        for i in range(tokens):
+            self.graph.replay()
+            out[:, i] = self.token
+        return out.view(self.images, self.answers, tokens)
+
+
 def main():
     from .chain import Chain
     parser = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     parser.add_argument("--images", type=int, default=4)
     parser.add_argument("--tokens", type=int, default=32)
+    parser.add_argument("--answers", type=int, default=0, help="answers about each image (0: one, over the whole prefix)")
+    parser.add_argument("--keep", type=int, default=100, help="cells of an image that its answers see")
     args = parser.parse_args()
     chain = Chain("bf16", args.images)
     frame = torch.randn((args.images, 3, 640, 640), device="cuda")
-    head = TokenHead(args.images)
+    head = AnswerHead(args.images, args.answers, keep=args.keep, max_answer=args.tokens) if args.answers else TokenHead(args.images)
+    first = torch.arange(args.images * args.answers, device="cuda").view(args.images, args.answers) if args.answers else None
     start, seen, done = (torch.cuda.Event(enable_timing=True) for _ in range(3))
     for _ in range(3):
         start.record()
         cells = chain.run(frame)[-1]   # [images, 20, 20, 256]
         seen.record()
-        answer = head.answer(cells, args.tokens)
+        answer = head.answer(cells, first % 512, args.tokens).flatten(0, 1) if args.answers else head.answer(cells, args.tokens)
         done.record()
     torch.cuda.synchronize()
     status = B.cbs_read_device_status(True, torch.cuda.current_stream().cuda_stream)
