@@ -155,20 +155,15 @@ __device__ __forceinline__ float weight_after(const AttnLaunch &L, const Rows &s
     return (key < s.base && L.decay != 0.0f ? L.decay * before : 0.0f) + came;
 }
 
-// The weights of the four keys from `key` on (a multiple of four) that lie before
-// `end`: of all the head's rows, from the scores that the attention left.
+// What the four keys from `key` on (a multiple of four) receive from rows first,
+// first + 1, ... four at a time, every `step` after them, from the scores that the
+// attention left.
 template <typename Stats>
-__device__ __forceinline__ void weigh_four(const AttnLaunch &L, const Rows &s, int b, int key, int end, Stats stats_of) {
-    const CacheArgs &c = L.c;
-    const float *scores = L.scores + (size_t)(b * c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
-    const int p = page_of(c, b, key);   // (all of them: pages hold multiples of sixteen)
-    if (p < 0) return;
-    float *mass = L.mass + (((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
-    float4 before = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (L.decay != 0.0f) before = *reinterpret_cast<const float4 *>(mass);
+__device__ __forceinline__ float4 weigh_four(const AttnLaunch &L, const Rows &s, int b, int key, int first, int step, Stats stats_of) {
+    const float *scores = L.scores + (size_t)(b * L.c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
     float sum[4] = {};
     constexpr int kOnce = 4;   // rows on their way together
-    for (int r0 = 0; r0 < s.R; r0 += kOnce) {
+    for (int r0 = first; r0 < s.R; r0 += step) {
         float4 v[kOnce];
         float2 st[kOnce];
         Seen z[kOnce];
@@ -188,8 +183,20 @@ __device__ __forceinline__ void weigh_four(const AttnLaunch &L, const Rows &s, i
                 if (key + i >= z[x].lo && key + i < z[x].hi) sum[i] = fmaf(frag::ex2(y[i] - st[x].x), st[x].y, sum[i]);
         }
     }
-    const float4 after = make_float4(weight_after(L, s, key, before.x, sum[0]), weight_after(L, s, key + 1, before.y, sum[1]),
-                                     weight_after(L, s, key + 2, before.z, sum[2]), weight_after(L, s, key + 3, before.w, sum[3]));
+    return make_float4(sum[0], sum[1], sum[2], sum[3]);
+}
+
+// What they weigh then, those before `end`.  (All four are on one page: pages hold
+// multiples of sixteen.)
+__device__ __forceinline__ void store_four(const AttnLaunch &L, const Rows &s, int b, int key, int end, float4 came) {
+    const CacheArgs &c = L.c;
+    const int p = page_of(c, b, key);
+    if (p < 0) return;
+    float *mass = L.mass + (((size_t)p * c.kv_heads + s.head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
+    float4 before = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (L.decay != 0.0f) before = *reinterpret_cast<const float4 *>(mass);
+    const float4 after = make_float4(weight_after(L, s, key, before.x, came.x), weight_after(L, s, key + 1, before.y, came.y),
+                                     weight_after(L, s, key + 2, before.z, came.z), weight_after(L, s, key + 3, before.w, came.w));
     if (key + 4 <= end) {
         *reinterpret_cast<float4 *>(mass) = after;
     } else {

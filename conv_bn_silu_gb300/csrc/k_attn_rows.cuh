@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
     // A weighed call's keys [from, to): the rows' statistics are in s_fin.
     const auto weigh = [&](int from, int to) {
         __syncthreads();
-        for (int key = from + 4 * tid; key < to; key += 4 * kThreads) weigh_four(L, rs, b, key, to, [&](int r) { return s_fin[r]; });
+        for (int key = from + 4 * tid; key < to; key += 4 * kThreads)
+            store_four(L, rs, b, key, to, weigh_four(L, rs, b, key, 0, 4, [&](int r) { return s_fin[r]; }));
     };
     const int end = min(len, L.len_pad);   // (of a weighed call)
     if (kExact && L.fused && sp == 0 && tid == 0 && len > L.len_pad) atomicOr(c.status, kStatusBadIndex);

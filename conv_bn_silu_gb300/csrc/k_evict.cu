@@ -34,13 +34,6 @@ __device__ __forceinline__ int2 ld_cluster_pair(const int *p, uint32_t rank) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ int ld_cluster_int(const int *p, uint32_t rank) {
-    uint32_t a;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
 
 // Sum of a count over the threads before this one; one barrier.  `warps` is written
 // anew by the next call but one.
@@ -84,11 +77,12 @@ __device__ __forceinline__ Pair scan(Pair v, Pair &total, Pair *warps) {
 
 __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunch L) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // this CTA's positions, at most L.run
-    __shared__ int s_hist[3][kBins];
+    __shared__ __align__(8) int s_hist[3][kBins];
     __shared__ Pair s_warps[kThreads / 32];
     __shared__ int s_totals[2][kThreads / 32];
     __shared__ int s_found[3][2];   // a pass's digit, and how many are to be taken of those that have it
-    __shared__ int s_counts[2];     // heavier than the threshold, equal to it
+    __shared__ __align__(8) int s_counts[2];   // heavier than the threshold, equal to it
+    __shared__ int2 s_all[kMostCtas];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const CacheArgs &c = L.c;
@@ -166,10 +160,11 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     if (ctas > 1) {
         if (tid == 0) s_counts[0] = total.a, s_counts[1] = total.b;
         meet();
+        if (tid < ctas) s_all[tid] = ld_cluster_pair(s_counts, tid);
+        __syncthreads();
         for (int r = 0; r < rank; ++r) {
-            const int h = ld_cluster_int(&s_counts[0], r), e = ld_cluster_int(&s_counts[1], r);
-            place += h + max(0, min(e, left - ties));
-            ties += e;
+            place += s_all[r].x + max(0, min(s_all[r].y, left - ties));
+            ties += s_all[r].y;
         }
     }
     int seen = ties + before.b;   // equal ones before this thread's
@@ -237,7 +232,9 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
 template <int ROW>
 cudaError_t launch_move(const EvictLaunch &L, cudaStream_t s) {
     constexpr int kRows = kMoveThreads / (ROW / 16) * kSteps;
-    return launch_kernel(evict_move_kernel<ROW>, dim3((L.keep + kRows - 1) / kRows, L.c.kv_heads, L.c.batch), kMoveThreads, 0, s, L);
+    if (L.c.max_pages == 0) return cudaSuccess;   // nothing held, nothing moves
+    const long long held = (long long)L.c.max_pages << L.c.page_shift, rows = L.keep < held ? L.keep : held;
+    return launch_kernel(evict_move_kernel<ROW>, dim3((unsigned)((rows + kRows - 1) / kRows), L.c.kv_heads, L.c.batch), kMoveThreads, 0, s, L);
 }
 
 }  // namespace

@@ -250,85 +250,8 @@ cbs_status attn_call(const cbs_attn_plan_t &p, const cbs_cache *c, const cbs_seq
     return CBS_OK;
 }
 
-}  // namespace
-}  // namespace cbs
-
-using namespace cbs;
-
-extern "C" {
-
-cbs_status cbs_cache_write(const cbs_cache *c, const cbs_sequences *s, const void *k, long long k_stride,
-                           const void *v, long long v_stride, int in_prec, void *stream) {
-    CacheArgs a;
-    CBS_TRY(cache_args(c, s, true, &a));
-    CBS_TRY(float_type(in_prec, "keys and values"));
-    CBS_TRY(token_stride(k_stride, (long long)c->kv_heads * c->head_dim, "k_stride"));
-    CBS_TRY(token_stride(v_stride, (long long)c->kv_heads * c->head_dim, "v_stride"));
-    if (s->batch == 0 || s->total == 0) return CBS_OK;
-    CBS_TRY(need(k, "k"));
-    CBS_TRY(need(v, "v"));
-    CBS_TRY(status_word(&a));
-    return cuda_check(launch_cache_write(a, k, k_stride, v, v_stride, in_prec == CBS_BF16, (cudaStream_t)stream),
-                      "cache write launch");
-}
-
-cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_len, void *k_out, void *v_out,
-                          int out_prec, void *stream) {
-    CacheArgs a;
-    CBS_TRY(cache_args(c, s, false, &a));
-    CBS_TRY(float_type(out_prec, "output"));
-    if (max_len < 0) return fail(CBS_ERR_INVALID_ARG, "max_len %d", max_len);
-    if (s->batch > kGridMax || c->kv_heads > kGridMax)
-        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
-    if (s->batch == 0 || max_len == 0) return CBS_OK;
-    CBS_TRY(need(k_out, "k_out"));
-    CBS_TRY(need(v_out, "v_out"));
-    CBS_TRY(status_word(&a));
-    return cuda_check(launch_cache_read(a, max_len, k_out, v_out, out_prec == CBS_BF16, (cudaStream_t)stream),
-                      "cache read launch");
-}
-
-cbs_status cbs_cache_evict(const cbs_cache *c, const cbs_sequences *s, float *mass, const int32_t *new_table,
-                           int new_max_pages, int keep, int recent, int32_t *kept, int32_t *new_lens, void *stream) {
-    EvictLaunch L;
-    std::memset(&L, 0, sizeof(L));
-    CBS_TRY(cache_args(c, s, false, &L.c));
-    if (keep < 1 || recent < 0 || recent > keep) return fail(CBS_ERR_INVALID_ARG, "keep %d, recent %d of them", keep, recent);
-    if (new_max_pages < 0) return fail(CBS_ERR_INVALID_ARG, "new_max_pages %d", new_max_pages);
-    const long long held = (long long)s->max_pages * c->page_size;
-    if ((long long)new_max_pages * c->page_size < std::min<long long>(keep, held))
-        return fail(CBS_ERR_INVALID_ARG, "%d new pages of %d do not hold %lld positions", new_max_pages, c->page_size,
-                    std::min<long long>(keep, held));
-    if (held > kEvictMost) return fail(CBS_ERR_UNSUPPORTED, "tables of %lld positions: at most %lld", held, kEvictMost);
-    if (s->batch > kGridMax || c->kv_heads > kGridMax)
-        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
-    if (s->batch == 0) return CBS_OK;
-    CBS_TRY(need(mass, "mass"));
-    CBS_TRY(need(kept, "kept"));
-    CBS_TRY(need(new_lens, "new_lens"));
-    if (!new_table && new_max_pages > 0) return fail(CBS_ERR_INVALID_ARG, "new_table is NULL");
-    if (reinterpret_cast<uintptr_t>(new_table) & 3u) return fail(CBS_ERR_MISALIGNED, "new_table is not 4-byte aligned");
-    // What one part of the call writes, others still read.
-    const size_t rows = (size_t)c->num_pages * c->kv_heads * c->page_size, row = (size_t)c->head_dim * (c->prec == CBS_INT8 ? 1 : 2);
-    const size_t kept_bytes = (size_t)s->batch * c->kv_heads * keep * 4, lens_bytes = (size_t)s->batch * 4;
-    const struct { const void *p; size_t bytes; const char *what; } parts[] = {
-        {c->k, rows * row, "k"}, {c->v, rows * row, "v"}, {c->k_scale, rows * 4, "k_scale"}, {c->v_scale, rows * 4, "v_scale"},
-        {mass, rows * 4, "mass"}, {s->seq_lens, lens_bytes, "seq_lens"}, {s->page_table, (size_t)s->batch * s->max_pages * 4, "page_table"},
-        {new_table, (size_t)s->batch * new_max_pages * 4, "new_table"}, {new_lens, lens_bytes, "new_lens"}, {kept, kept_bytes, "kept"}};
-    constexpr int kParts = sizeof(parts) / sizeof(parts[0]);
-    for (int out = 4; out < kParts; ++out) {
-        if (out > 4 && out < 8) continue;   // inputs
-        for (int other = 0; other < out; ++other)
-            if (overlap(parts[out].p, parts[out].bytes, parts[other].p, parts[other].bytes))
-                return fail(CBS_ERR_INVALID_ARG, "%s lies on %s", parts[out].what, parts[other].what);
-    }
-    CBS_TRY(status_word(&L.c));
-    L.mass = mass; L.new_table = new_table; L.new_max_pages = new_max_pages;
-    L.keep = keep; L.recent = recent; L.kept = kept; L.new_lens = new_lens;
-    return cuda_check(launch_evict(L, (cudaStream_t)stream), "eviction launch");
-}
-
-cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
+// few: 1 or 0 for the few-row kernels or the chunk kernel, -1 for what the rows say.
+cbs_status attn_plan(const cbs_attn_desc *d, int few, cbs_attn_plan_t *out) {
     if (!d || !out) return fail(CBS_ERR_INVALID_ARG, "%s is NULL", d ? "out" : "desc");
     if (d->batch < 0 || d->max_new < 0 || d->max_len < 0 || d->heads < 1 || d->window < 0 || d->force_split < 0 ||
         d->num_sms < 0)
@@ -348,7 +271,7 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     p.desc = *d;
     const long long rows = (long long)d->max_new * (d->heads / d->kv_heads);
     const int rows_most = d->cache_prec == CBS_INT8 ? kAttnRowsMostInt8 : kAttnRowsMost;
-    p.kernel = d->force_kernel >= 0 ? d->force_kernel : rows > rows_most ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
+    p.kernel = d->force_kernel >= 0 ? d->force_kernel : (few < 0 ? rows > rows_most : !few) ? CBS_ATTN_CHUNK : CBS_ATTN_ROWS;
     const bool chunk = p.kernel == CBS_ATTN_CHUNK;
     // (Tiles of 16 rows in 8 bits alone: a bf16 cache's call of more than eight takes
     // the chunk kernel, unless told otherwise.)
@@ -404,6 +327,131 @@ cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) {
     return CBS_OK;
 }
 
+// What a plan's call takes, in nanoseconds: a few-row tile's thousand keys by head
+// dimension and type, or the chunk kernel's tiles.
+long long attn_ns(const cbs_attn_plan_t &p, int sms) {
+    const cbs_attn_desc &d = p.desc;
+    const long long base = (long long)std::max(d.batch, 1) * d.kv_heads * p.row_tiles;
+    if (p.kernel == CBS_ATTN_CHUNK) return chunk_ns(d, base, p.split, sms);
+    const int thousand = d.cache_prec == CBS_INT8 ? (d.head_dim == 64 ? 50 : 80) : d.head_dim == 64 ? 40 : 75;
+    return 4500 + base * d.max_len / 1000 * thousand;
+}
+
+// The faster kernel for a part of a call whose rows are more than the few-row
+// kernels' own: short sequences do not repay a chunk's start.  (`more`: what follows
+// the few-row kernel less what follows the chunk kernel.)  Head dimension 64, bf16, few
+// rows and chunks: 64 rows of 400 keys, two heads 5.2 and 9.2 us, 64 heads 11.4 and 9.5;
+// 8 bits, 64 rows of 400 keys, 320 heads 30 and 43, of 1500 99 and 88.
+cbs_status attn_plan_by_time(const cbs_attn_desc *d, long long (*more)(const cbs_attn_plan_t &few, const cbs_attn_plan_t &chunk, int sms),
+                             cbs_attn_plan_t *out) {
+    CBS_TRY(attn_plan(d, -1, out));
+    if (d->force_kernel >= 0) return CBS_OK;
+    const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
+    // Of more than eight rows the many ranges that a few-row kernel joins through the
+    // workspace take longer than eight in a cluster: 16 rows of 6000 keys, two heads of
+    // 128 in 8 bits 47 and 14 us, in bf16 21 and 15.
+    const auto in_clusters = [&](cbs_attn_plan_t *p) {
+        const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p->row_tiles;
+        if (p->kernel != CBS_ATTN_ROWS || p->split <= kAttnClusterMost || (long long)d->max_new * (d->heads / d->kv_heads) <= 8 ||
+            d->max_len > 8192 || base * kAttnClusterMost > 3ll * sms)
+            return;
+        p->kernel = CBS_ATTN_CLUSTER;
+        p->split = kAttnClusterMost;
+        p->grid_ctas = (int)(base * p->split);
+        p->workspace_bytes = 0;
+    };
+    if (out->kernel != CBS_ATTN_CHUNK) {
+        in_clusters(out);
+        return CBS_OK;
+    }
+    cbs_attn_plan_t few;
+    if (attn_plan(d, 1, &few) != CBS_OK) return CBS_OK;   // (too many row tiles)
+    in_clusters(&few);
+    if (attn_ns(few, sms) + (more ? more(few, *out, sms) : 0) < attn_ns(*out, sms)) *out = few;
+    return CBS_OK;
+}
+
+}  // namespace
+}  // namespace cbs
+
+using namespace cbs;
+
+extern "C" {
+
+cbs_status cbs_cache_write(const cbs_cache *c, const cbs_sequences *s, const void *k, long long k_stride,
+                           const void *v, long long v_stride, int in_prec, void *stream) {
+    CacheArgs a;
+    CBS_TRY(cache_args(c, s, true, &a));
+    CBS_TRY(float_type(in_prec, "keys and values"));
+    CBS_TRY(token_stride(k_stride, (long long)c->kv_heads * c->head_dim, "k_stride"));
+    CBS_TRY(token_stride(v_stride, (long long)c->kv_heads * c->head_dim, "v_stride"));
+    if (s->batch == 0 || s->total == 0) return CBS_OK;
+    CBS_TRY(need(k, "k"));
+    CBS_TRY(need(v, "v"));
+    CBS_TRY(status_word(&a));
+    return cuda_check(launch_cache_write(a, k, k_stride, v, v_stride, in_prec == CBS_BF16, (cudaStream_t)stream),
+                      "cache write launch");
+}
+
+cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, int max_len, void *k_out, void *v_out,
+                          int out_prec, void *stream) {
+    CacheArgs a;
+    CBS_TRY(cache_args(c, s, false, &a));
+    CBS_TRY(float_type(out_prec, "output"));
+    if (max_len < 0) return fail(CBS_ERR_INVALID_ARG, "max_len %d", max_len);
+    if (s->batch > kGridMax || c->kv_heads > kGridMax)
+        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
+    if (s->batch == 0 || max_len == 0) return CBS_OK;
+    CBS_TRY(need(k_out, "k_out"));
+    CBS_TRY(need(v_out, "v_out"));
+    CBS_TRY(status_word(&a));
+    return cuda_check(launch_cache_read(a, max_len, k_out, v_out, out_prec == CBS_BF16, (cudaStream_t)stream),
+                      "cache read launch");
+}
+
+cbs_status cbs_cache_evict(const cbs_cache *c, const cbs_sequences *s, float *mass, const int32_t *new_table,
+                           int new_max_pages, int keep, int recent, int32_t *kept, int32_t *new_lens, void *stream) {
+    EvictLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    CBS_TRY(cache_args(c, s, false, &L.c));
+    if (keep < 1 || recent < 0 || recent > keep) return fail(CBS_ERR_INVALID_ARG, "keep %d, recent %d of them", keep, recent);
+    if (keep > 1 << 30) return fail(CBS_ERR_UNSUPPORTED, "keep %d: at most 2^30", keep);
+    if (new_max_pages < 0) return fail(CBS_ERR_INVALID_ARG, "new_max_pages %d", new_max_pages);
+    const long long held = (long long)s->max_pages * c->page_size;
+    if ((long long)new_max_pages * c->page_size < std::min<long long>(keep, held))
+        return fail(CBS_ERR_INVALID_ARG, "%d new pages of %d do not hold %lld positions", new_max_pages, c->page_size,
+                    std::min<long long>(keep, held));
+    if (held > kEvictMost) return fail(CBS_ERR_UNSUPPORTED, "tables of %lld positions: at most %lld", held, kEvictMost);
+    if (s->batch > kGridMax || c->kv_heads > kGridMax)
+        return fail(CBS_ERR_UNSUPPORTED, "%d sequences, %d heads: at most %d", s->batch, c->kv_heads, kGridMax);
+    if (s->batch == 0) return CBS_OK;
+    CBS_TRY(need(mass, "mass"));
+    CBS_TRY(need(kept, "kept"));
+    CBS_TRY(need(new_lens, "new_lens"));
+    if (!new_table && new_max_pages > 0) return fail(CBS_ERR_INVALID_ARG, "new_table is NULL");
+    if (reinterpret_cast<uintptr_t>(new_table) & 3u) return fail(CBS_ERR_MISALIGNED, "new_table is not 4-byte aligned");
+    // What one part of the call writes, others still read.
+    const size_t rows = (size_t)c->num_pages * c->kv_heads * c->page_size, row = (size_t)c->head_dim * (c->prec == CBS_INT8 ? 1 : 2);
+    const size_t kept_bytes = (size_t)s->batch * c->kv_heads * keep * 4, lens_bytes = (size_t)s->batch * 4;
+    const struct { const void *p; size_t bytes; const char *what; } parts[] = {
+        {c->k, rows * row, "k"}, {c->v, rows * row, "v"}, {c->k_scale, rows * 4, "k_scale"}, {c->v_scale, rows * 4, "v_scale"},
+        {mass, rows * 4, "mass"}, {s->seq_lens, lens_bytes, "seq_lens"}, {s->page_table, (size_t)s->batch * s->max_pages * 4, "page_table"},
+        {new_table, (size_t)s->batch * new_max_pages * 4, "new_table"}, {new_lens, lens_bytes, "new_lens"}, {kept, kept_bytes, "kept"}};
+    constexpr int kParts = sizeof(parts) / sizeof(parts[0]);
+    for (int out = 4; out < kParts; ++out) {
+        if (out > 4 && out < 8) continue;   // inputs
+        for (int other = 0; other < out; ++other)
+            if (overlap(parts[out].p, parts[out].bytes, parts[other].p, parts[other].bytes))
+                return fail(CBS_ERR_INVALID_ARG, "%s lies on %s", parts[out].what, parts[other].what);
+    }
+    CBS_TRY(status_word(&L.c));
+    L.mass = mass; L.new_table = new_table; L.new_max_pages = new_max_pages;
+    L.keep = keep; L.recent = recent; L.kept = kept; L.new_lens = new_lens;
+    return cuda_check(launch_evict(L, (cudaStream_t)stream), "eviction launch");
+}
+
+cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out) { return attn_plan(d, -1, out); }
+
 cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache *c, const cbs_sequences *s, const void *q,
                                long long q_stride, float scale, void *out, long long out_stride, void *workspace,
                                size_t workspace_bytes, void *stream) {
@@ -425,7 +473,14 @@ cbs_status cbs_weighed_plan(const cbs_attn_desc *d, cbs_weighed_plan_t *out) {
     std::memset(&p, 0, sizeof(p));
     p.size = sizeof(p);
     p.abi_version = CBS_ABI_VERSION;
-    CBS_TRY(cbs_attn_plan(d, &p.attention));
+    // What comes after the attention: scores summed up, 5 us and some more with their
+    // number, or the chunk's keys again, 5.5 us a round of them and 0.8 a tile of rows.
+    CBS_TRY(attn_plan_by_time(d, [](const cbs_attn_plan_t &few, const cbs_attn_plan_t &chunk, int sms) -> long long {
+        const cbs_attn_desc &d = few.desc;
+        const long long rows = (long long)d.max_new * (d.heads / d.kv_heads), heads = (long long)d.batch * d.kv_heads;
+        const long long ctas = heads * chunk_key_tiles(d.max_len), rounds = (ctas + 2 * sms - 1) / (2 * sms);
+        return 5000 + heads * rows * d.max_len / 250 - rounds * (5500 + (rows + 127) / 128 * 800);
+    }, &p.attention));
     if ((d->max_len + 15ll) / 16 * 16 > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "max_len %d", d->max_len);
     p.workspace_bytes = weighed_parts(p.attention).all;
     *out = p;
@@ -486,9 +541,9 @@ cbs_status cbs_shared_plan(const cbs_shared_desc *d, cbs_shared_plan_t *out) {
     p.abi_version = CBS_ABI_VERSION;
     p.desc = *d;
     cbs_attn_desc part = {d->batch, d->max_new, d->max_len, d->heads, d->kv_heads, d->head_dim, d->cache_prec, 1, 0, d->num_sms, -1, 0};
-    CBS_TRY(cbs_attn_plan(&part, &p.own));
+    CBS_TRY(attn_plan_by_time(&part, nullptr, &p.own));
     part.batch = d->groups; part.max_new = d->max_group_new; part.max_len = d->max_prefix; part.causal = 0;
-    CBS_TRY(cbs_attn_plan(&part, &p.prefix));
+    CBS_TRY(attn_plan_by_time(&part, nullptr, &p.prefix));
     const long long total = std::min((long long)d->batch * d->max_new, (long long)d->groups * d->max_group_new);
     if (total > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "%lld new tokens", total);
     p.max_total = (int)total;

@@ -518,7 +518,7 @@ CBS_API cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, in
  *   new_lens: [batch], min(keep, length).  kept and new_lens are outputs (16-byte
  *     aligned) and on none of the inputs.
  * new_start is not read and may be NULL.  max_pages * page_size is at most
- * 393216.  Equal calls give equal results.
+ * 393216, keep 2^30.  Equal calls give equal results.
  */
 CBS_API cbs_status cbs_cache_evict(const cbs_cache *c, const cbs_sequences *s, float *mass, const int32_t *new_table,
                                    int new_max_pages, int keep, int recent, int32_t *kept, int32_t *new_lens,
@@ -590,7 +590,7 @@ CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache
  * sequences' pages are left as they are.
  *   mass: float [num_pages][kv_heads][page_size].  No page may belong to two of
  *     the call's sequences (they would overwrite each other's weights).
- *   decay: finite.  out: as cbs_paged_attention's, the same bits.
+ *   decay: finite.  out: as cbs_paged_attention's.
  * A sequence longer than the plan's max_len is reported, and its positions past
  * that (rounded up to 16) get no weight.  total is at most batch * max_new.  Sums
  * are in 32 bits; equal calls give equal results.  workspace: workspace_bytes, of

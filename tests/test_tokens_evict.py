@@ -142,12 +142,27 @@ def test_captured_and_other_streams():
         assert all(torch.equal(a, b) for a, b in zip(first, got))
 
 
+@pytest.mark.gpu
+def test_nothing_held():
+    """Tables without pages: no position stays, and none is looked for."""
+    from conv_bn_silu_gb300 import tokens
+    cache = tokens.PagedCache.empty(3, 2, 16, 64)
+    mass = torch.zeros((3, 2, 16), device="cuda")
+    i32 = lambda *shape: torch.zeros(shape, dtype=I32, device="cuda")
+    kept, after = cache.evict(mass, i32(2), i32(2, 0), i32(2, 0), 5, 1)
+    assert (kept == -1).all() and not after.any()
+    kept, after = cache.evict(mass, i32(0), i32(0, 4), i32(0, 4), 5, 1)
+    assert kept.shape == (0, 2, 5) and after.shape == (0,)
+    assert B.cbs_read_device_status(True, torch.cuda.current_stream().cuda_stream) == B.CBS_OK
+
+
 def test_refusals(cuda_lib):
     K = 1 << 30   # addresses that are checked for alignment and overlap only
     def call(c=None, s=None, mass=2 * K, table=3 * K, pages=4, keep=8, recent=2, kept=4 * K, lens=5 * K):
         B.cbs_cache_evict(c or c_cache(k=6 * K, v=7 * K, k_scale=8 * K, v_scale=9 * K), s or seqs(new_start=None, seq_lens=10 * K, page_table=11 * K),
                           mass, table, pages, keep, recent, kept, lens, None)
     refused(I, lambda: call(keep=0))
+    refused(U, lambda: call(keep=(1 << 30) + 1, pages=64))
     refused(I, lambda: call(recent=-1))
     refused(I, lambda: call(recent=9))
     refused(I, lambda: call(pages=0))

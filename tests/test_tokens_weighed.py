@@ -84,7 +84,10 @@ def run_case(lens, new, heads, kv, d, page, int8, causal=True, window=0, scale=N
             before[paged["table"][b, pos // page], :, pos % page] = math.nan
     mass = before.cuda()
     out = attn(*args, mass, decay=decay)
-    assert torch.equal(out.view(torch.int16), plain(*args).view(torch.int16))   # the same attention, to the bit
+    if attn.plan.attention.kernel == plain.plan.kernel:
+        assert torch.equal(out.view(torch.int16), plain(*args).view(torch.int16))   # the same attention, to the bit
+    ref, mag = refs.attention(q, paged, starts, lens, page, causal, window, scale or d ** -0.5)
+    assert ((out.double().cpu() - ref).abs() <= refs.attention_bound(ref, mag)).all()
     again = before.cuda()
     attn(*args, again, decay=decay, out=torch.empty_like(out))
     assert torch.equal(mass.view(I32), again.view(I32))
@@ -134,6 +137,16 @@ def test_ranges(split, int8):
 @pytest.mark.parametrize("decay", [0.0, 1.0, -0.25])
 def test_chunks(heads, kv, d, page, int8, decay):
     run_case([300, 77, 5, 260], [100, 77, 1, 0], heads, kv, d, page, int8, decay=decay, padding=4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("kernel", [B.CBS_ATTN_ROWS, B.CBS_ATTN_CLUSTER, CHUNK])
+@pytest.mark.parametrize("heads,kv,new", [(8, 2, [5, 1, 0]), (6, 1, [40, 33, 7]), (64, 1, [3, 2, 1]), (40, 8, [9, 1, 1])])
+def test_every_kernel(heads, kv, new, kernel, int8):
+    """More rows than a few-row tile, by either kernel: their scores are summed up by
+    warps side by side."""
+    run_case([90, 33, 400], new, heads, kv, 64, 16, int8, kernel=kernel, decay=0.5)
 
 
 @pytest.mark.gpu
