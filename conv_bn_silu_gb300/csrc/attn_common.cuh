@@ -160,7 +160,7 @@ __device__ __forceinline__ float weight_after(const AttnLaunch &L, const Rows &s
 // attention left.
 template <typename Stats>
 __device__ __forceinline__ float4 weigh_four(const AttnLaunch &L, const Rows &s, int b, int key, int first, int step, Stats stats_of) {
-    const float *scores = L.scores + (size_t)(b * L.c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
+    const float *scores = L.scores + ((size_t)b * L.c.kv_heads + s.head) * L.rows_pad * L.len_pad + key;
     float sum[4] = {};
     constexpr int kOnce = 4;   // rows on their way together
     for (int r0 = first; r0 < s.R; r0 += step) {

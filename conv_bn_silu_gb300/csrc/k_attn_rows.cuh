@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                scores[n][i] = L.scores + ((size_t)(b * c.kv_heads + head) * L.rows_pad + r0 + n * 8 + 2 * j + i) * L.len_pad;
+                scores[n][i] = L.scores + (((size_t)b * c.kv_heads + head) * L.rows_pad + r0 + n * 8 + 2 * j + i) * L.len_pad;
     }
 
     F f;

@@ -516,6 +516,7 @@ constexpr int kAtOnce[] = {152, 76, 36, 15};
 // x 256 14 and 9.0.
 constexpr long long kFewMost8 = 96ll << 20, kFewMost16 = 28ll << 20;
 constexpr int kFewMostOutputs16 = 16384;
+constexpr long long kGridMost = 65535;   // row tiles of a launch
 
 cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
     const long long weights = (long long)L.n * L.k;
@@ -526,7 +527,8 @@ cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
     int rows = 0, split = 1;
     for (const W8Cost &c : kCosts) {
         if (rows && c.rows >= 2 * L.rows) break;   // (half of a larger tile would be empty)
-        const long long row_tiles = (L.rows + c.rows - 1) / c.rows;
+        const long long row_tiles = ((long long)L.rows + c.rows - 1) / c.rows;
+        if (row_tiles > kGridMost) continue;
         for (int i = 0; i < (c.rows == 256 ? 1 : 4) && (i == 0 || 2 << i <= stages); ++i) {
             const int x = 1 << i;
             const long long each = (stages + x - 1) / x;

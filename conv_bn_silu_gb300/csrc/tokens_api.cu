@@ -175,7 +175,7 @@ WeighedParts weighed_parts(const cbs_attn_plan_t &p) {
     const cbs_attn_desc &d = p.desc;
     WeighedParts w;
     w.rows_pad = (int)((long long)d.max_new * (d.heads / d.kv_heads));
-    w.len_pad = (int)((d.max_len + 15ll) / 16 * 16);
+    w.len_pad = (int)(std::max(d.max_len + 15ll, 16ll) / 16 * 16);
     w.row_stats = round256(p.workspace_bytes);
     w.sums = w.row_stats + round256((size_t)d.batch * d.max_new * d.heads * 8);
     w.scores = w.sums + (p.workspace_bytes ? round256(attn_stat_rows(p) * 4) : 0);
@@ -523,8 +523,8 @@ cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c
     L.mass = mass;
     L.decay = decay;
     // Few rows in one tile: the CTAs of a cluster weigh their own keys, and so does one
-    // CTA without ranges (one token over 1000 keys 10.8 -> 9.x us; 64 sequences of 300
-    // 26.7 -> 24.4).  Of ranges joined by the CTA that finishes last, that one would weigh
+    // CTA without ranges (one token over 1000 keys 10.8 -> 8.6 us; 64 sequences of 300
+    // 26.7 -> 23.4).  Of ranges joined by the CTA that finishes last, that one would weigh
     // all of them (32 sequences of up to 8192: 136 -> 159).
     L.fused = L.scores && a.row_tiles == 1 && (L.cluster || a.split == 1);
     CBS_TRY(launch_attn_weighed(L, a.row_tile, (cudaStream_t)stream));
@@ -704,6 +704,7 @@ cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed
 static cbs_status w8_shape(int n, int k) {
     if (n < 1 || k < 1) return fail(CBS_ERR_INVALID_ARG, "bad weight shape (%d x %d)", n, k);
     if (k % 16) return fail(CBS_ERR_UNSUPPORTED, "k = %d is not a multiple of 16", k);
+    if (n > 1 << 30 || k > 1 << 30) return fail(CBS_ERR_UNSUPPORTED, "weights of %d x %d: at most 2^30 a side", n, k);
     return CBS_OK;
 }
 

@@ -701,9 +701,9 @@ CBS_API cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void
  * channel:
  *   y[m,n] = act( x_scale[m] w_scale[n] sum_k x[m,k] w[n,k] + bias[n] )
  * x: int8 [rows][k], x_scale float[rows] (cbs_rmsnorm's rows).  w: int8 [n][k],
- * w_scale float[n].  k a multiple of 16.  bias: float[n] or NULL.  y: [rows][n],
+ * w_scale float[n].  k a multiple of 16, n and k at most 2^30.  bias: float[n] or NULL.  y: [rows][n],
  * out_prec CBS_FP32 or CBS_BF16.  activation: cbs_activation.  The sums are exact
- * where they and their parts stay below 2^24 (any codes up to k = 1024; codes of
+ * where they and their parts stay below 2^24 (any codes up to k = 1008; codes of
  * ordinary rows far beyond), and rounded to 24 bits past that.  For one row as for
  * thousands.
  */

@@ -64,7 +64,7 @@ def test_sizes(rows, n, k):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,n,k", [(1, 6144, 4096), (16, 4096, 14336), (40, 256, 16384), (100, 512, 8192), (1600, 1536, 512),
-                                      (3000, 2048, 4096), (1, 70000, 256), (70000, 64, 32)])
+                                      (3000, 2048, 4096), (1, 70000, 256), (70000, 64, 32), (5000000, 3, 16)])
 def test_larger(rows, n, k):
     """Shares of k, rings gone round many times, many tiles."""
     run_case(rows, n, k, dtype=torch.bfloat16)
@@ -147,6 +147,8 @@ def test_refusals(cuda_lib):
     refused(I, lambda: call(n=0))
     refused(I, lambda: call(rows=-1))
     refused(U, lambda: call(rows=1 << 25))
+    refused(U, lambda: call(n=(1 << 30) + 1))
+    refused(U, lambda: call(k=(1 << 30) + 16))
     refused(I, lambda: call(act=5))
     refused(I, lambda: call(x=None))
     refused(I, lambda: call(xs=None))
