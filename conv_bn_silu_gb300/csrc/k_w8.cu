@@ -11,42 +11,33 @@
 // weights and store them to tensor memory as the MMA's A operand; other warps widen
 // the inputs into the swizzled rows of B.  Shared memory's bandwidth bounds it: a
 // byte is written by TMA, read by a thread, and B's twofold written and read again.
-// So the wide form pairs two CTAs (cta_group::2): each keeps the widened half of the
-// 256 input rows, the pair's MMA reads both, and what a CTA moves for a product of
-// 256 x 256 is half of what it would alone.
+// So many rows go to k_w8_pair.cu, where two CTAs share a tile.
 //
 // For few rows the weights' bytes bound it.  Shares of k are then CTAs of a cluster,
 // which add their sums in order through distributed shared memory.
 #include <algorithm>
 
-#include <cuda_bf16.h>
-
-#include "mma_frag.cuh"
-#include "tc_ptx.cuh"
-#include "tc_warp.cuh"
-#include "tokens.cuh"
+#include "w8.cuh"
 
 namespace cbs {
 
+using namespace w8;
+
 namespace {
 
-constexpr int kOut = 128;                    // outputs of a CTA: tensor memory's lanes
-constexpr int kStageK = 128;                 // codes along k in a stage: a row of 128 bytes
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr int kShareMost = 8;                // shares of k: CTAs of a cluster
 constexpr int kPitch = kOut + 4;             // floats of a row of a share's sums
 
-// kN: input rows of a tile; kPair: CTAs that share it.
-template <int kN, int kPair>
+// kN: input rows of a tile.
+template <int kN>
 struct W8Tile {
-    static constexpr int kRows = kN / kPair;                 // input rows a CTA widens
-    static constexpr int kW = kOut * 128, kRaw = kW + kRows * 128;
-    static constexpr int kOp = kRows * 256;                  // a stage of B: two panels of 64
+    static constexpr int kW = kOut * 128, kRaw = kW + kN * 128;
+    static constexpr int kOp = kN * 256;                  // a stage of B: two panels of 64
     static constexpr int kStages = kN == 64 ? 2 : 4;
     static constexpr int kOps = kN <= 32 ? 2 : 3;
     // Warps that widen inputs, and the groups of them that take stages in turn: a
     // group then has two stages' time for its loads, stores and fence.
-    static constexpr int kWiden = kRows >= 128 ? 8 : kRows / 16, kTurns = kRows >= 32 ? 2 : 1;
+    static constexpr int kWiden = kN >= 128 ? 8 : kN / 16, kTurns = kN >= 32 ? 2 : 1;
     // A wait knows a barrier's turns apart only while it is less than two behind.  Loads
     // land out of order, so whoever takes stages in turn has to see every turn of its
     // slots: their number is a multiple of two (weights) and of kTurns.  A group's last
@@ -60,93 +51,24 @@ struct W8Tile {
     // takes some 2500 cycles of hand-offs, so as many as fit.
     static constexpr int kABufs = kN >= 128 ? 4 : 3, kACols = kStageK / 2;
     static constexpr int kTmem = kABufs * kACols + kN <= 256 ? 256 : 512;
-    // raw_full[], raw_empty[], b_ready[], b_free[], peer[], a_ready[], a_free[], done;
+    // raw_full[], raw_empty[], b_ready[], b_free[], a_ready[], a_free[], done;
     // TMEM address, flag; the input rows' scales
-    static constexpr int kNumBars = 2 * kStages + 3 * kOps + 2 * kABufs + 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kOps + 2 * kABufs + 1;
     static constexpr int kScales = kBars + kNumBars * 8 + 16, kSmem = kScales + kN * 4;
     static_assert(kABufs * kACols + kN <= 512 && kScales % 8 == 0 && kRaw % 1024 == 0 && kOp % 1024 == 0, "tensor memory; operands at multiples of 1 KB");
     static_assert(kSmem <= kMaxDynSmem, "shared memory");
-    static_assert(kPair == 2 || kN * kPitch * 4 <= kBars, "a share's sums fit where the stages were");
+    static_assert(kN * kPitch * 4 <= kBars, "a share's sums fit where the stages were");
 };
 
-// Another CTA's barrier.  What this announces lies in the sender's own shared and
-// tensor memory, where its writers' fences have made it visible to the MMA's reads
-// before they arrived here; no thread of the other CTA reads it.  So nothing is
-// released in the cluster's scope, which took the sender some 1700 cycles a stage (256
-// rows of 8192 x 8192: 62.6 us, and 43.7 without).
-__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(bar), "r"(rank));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
-}
-// As mbar_wait_bounded, for the arrival of the pair's other CTA.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(1000u)
-            : "memory");
-        if (ok) return true;
-        const uint64_t t = ptx::globaltimer();
-        if (t0 == 0) t0 = t;
-        else if (t - t0 > limit_ns) return false;
-    }
-}
-// The instructions whose form names the number of CTAs (one kernel uses one form).
-template <int kPair>
-struct Tc {
-    static __device__ __forceinline__ void alloc(uint32_t at, uint32_t cols) {
-        if constexpr (kPair == 1) {
-            ptx::tmem_alloc(at, cols);
-            ptx::tmem_relinquish();
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(at), "r"(cols) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-        }
-    }
-    static __device__ __forceinline__ void dealloc(uint32_t t, uint32_t cols) {
-        if constexpr (kPair == 1) ptx::tmem_dealloc(t, cols);
-        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
-    }
-    static __device__ __forceinline__ void mma(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-        if constexpr (kPair == 1) {
-            mma_ts(lead, d, a, b, idesc, accumulate);
-        } else {
-            asm volatile(
-                "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-                "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-                : "memory");
-        }
-    }
-    // Arrives on `bar` of every CTA of the tile.
-    static __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
-        if constexpr (kPair == 1) {
-            mma_commit(lead, bar);
-        } else {
-            asm volatile(
-                "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-                "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(bar),
-                "r"(lead), "h"((uint16_t)3)
-                : "memory");
-        }
-    }
-};
-
-template <int kN, int kPair>
-__global__ void __launch_bounds__(W8Tile<kN, kPair>::kThreads, W8Tile<kN, kPair>::kSmem <= 113 * 1024 ? 2 : 1)
+template <int kN>
+__global__ void __launch_bounds__(W8Tile<kN>::kThreads, W8Tile<kN>::kSmem <= 113 * 1024 ? 2 : 1)
 w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const W8Launch L, int split) {
-    using C = W8Tile<kN, kPair>;
-    using T = Tc<kPair>;
+    using C = W8Tile<kN>;
     extern __shared__ __align__(1024) unsigned char smem[];   // the only shared memory: starts at a multiple of 1 KB
     const uint32_t sbase = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kPair > 1 || split > 1 ? (int)cluster_rank() : 0;
-    const int share = kPair > 1 ? 0 : rank;                  // of k
-    const int n0 = (kPair > 1 ? blockIdx.x : blockIdx.x / split) * kOut, m0 = blockIdx.y * kN;
+    const int share = split > 1 ? (int)cluster_rank() : 0;   // of k
+    const int n0 = (blockIdx.x / split) * kOut, m0 = blockIdx.y * kN;
     const int stages = (L.k + kStageK - 1) / kStageK;
     const int st0 = (int)((long long)stages * share / split), ns = (int)((long long)stages * (share + 1) / split) - st0;
     const auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
@@ -154,10 +76,9 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     const auto raw_empty = [&](int s) { return bar(C::kStages + s); };
     const auto b_ready = [&](int s) { return bar(2 * C::kStages + s); };
     const auto b_free = [&](int s) { return bar(2 * C::kStages + C::kOps + s); };
-    const auto peer = [&](int s) { return bar(2 * C::kStages + 2 * C::kOps + s); };   // the other CTA's operands are ready
-    const auto a_ready = [&](int w) { return bar(2 * C::kStages + 3 * C::kOps + w); };
-    const auto a_free = [&](int w) { return bar(2 * C::kStages + 3 * C::kOps + C::kABufs + w); };
-    const uint32_t done = bar(2 * C::kStages + 3 * C::kOps + 2 * C::kABufs);
+    const auto a_ready = [&](int w) { return bar(2 * C::kStages + 2 * C::kOps + w); };
+    const auto a_free = [&](int w) { return bar(2 * C::kStages + 2 * C::kOps + C::kABufs + w); };
+    const uint32_t done = bar(2 * C::kStages + 2 * C::kOps + 2 * C::kABufs);
     volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(smem + C::kBars + 8 * C::kNumBars);
     // words[0]: TMEM address; [1]: a wait ran out
 
@@ -169,7 +90,6 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         for (int s = 0; s < C::kOps; ++s) {
             ptx::mbar_init(b_ready(s), C::kWiden / C::kTurns);
             ptx::mbar_init(b_free(s), 1);
-            ptx::mbar_init(peer(s), 1);
         }
         for (int w = 0; w < C::kABufs; ++w) {
             ptx::mbar_init(a_ready(w), 4);
@@ -179,11 +99,13 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         ptx::fence_mbar_init();
         words[1] = 0;
     }
-    if (warp == C::kWarpMma) T::alloc(sbase + C::kBars + 8 * C::kNumBars, C::kTmem);
+    if (warp == C::kWarpMma) {
+        ptx::tmem_alloc(sbase + C::kBars + 8 * C::kNumBars, C::kTmem);
+        ptx::tmem_relinquish();
+    }
     if (warp == C::kWarpTma && lane < 2) ptx::prefetch_tmap(lane ? &tm_x : &tm_w);
     ptx::tc_fence_before();
-    if (kPair > 1) cluster_sync();   // both CTAs' barriers are ready for each other's arrivals
-    else __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -210,57 +132,36 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 
     if (warp == C::kWarpMma) {
         // ------------------------------------------------------- MMA issue
-        if (kPair == 1 || rank == 0) {
-            constexpr uint32_t idesc = (1u << 4) | ((kN >> 3) << 17) | ((kOut * kPair >> 4) << 24);   // f16 operands
-            const uint32_t lead = elect_one();
-            const uint64_t d_b = ptx::smem_desc(sbase + C::kOpAt, 16, 1024, 2);
-            int op = 0;
-            uint32_t op_parity = 0;
-            for (int i = 0; i < ns; ++i) {
-                bool ok = wait(a_ready(i % C::kABufs), (i / C::kABufs) & 1) && wait(b_ready(op), op_parity);
-                if (kPair > 1 && ok && !wait_cluster(peer(op), op_parity, kWaitNs)) {
-                    ok = false;
-                    words[1] = 1;
-                    atomicOr(L.status, kStatusTimeout);
-                }
-                ok = ok && !lost();
-                if (!__all_sync(~0u, ok)) break;
-                ptx::tc_fence_after();
-                const uint64_t b = d_b + (uint32_t)(op * C::kOp) / 16;
+        constexpr uint32_t idesc = (1u << 4) | ((kN >> 3) << 17) | ((kOut >> 4) << 24);   // f16 operands
+        const uint32_t lead = elect_one();
+        const uint64_t d_b = ptx::smem_desc(sbase + C::kOpAt, 16, 1024, 2);
+        int op = 0;
+        uint32_t op_parity = 0;
+        for (int i = 0; i < ns; ++i) {
+            const bool ok = wait(a_ready(i % C::kABufs), (i / C::kABufs) & 1) && wait(b_ready(op), op_parity) && !lost();
+            if (!__all_sync(~0u, ok)) break;
+            ptx::tc_fence_after();
+            const uint64_t b = d_b + (uint32_t)(op * C::kOp) / 16;
 #pragma unroll
-                for (int x = 0; x < kStageK / 16; ++x)
-                    T::mma(lead, t_d, t_a(i % C::kABufs) + 8 * x, b + (uint32_t)((x >> 2) * C::kRows * 8 + (x & 3) * 2), idesc, i > 0 || x > 0);
-                T::commit(lead, a_free(i % C::kABufs));
-                T::commit(lead, b_free(op));
-                if (++op == C::kOps) op = 0, op_parity ^= 1;
-            }
-            __syncwarp();
-            T::commit(lead, done);   // all that was issued, however the loop ended
-        } else {
-            // The other CTA's operands are announced once a stage.
-            int op = 0;
-            uint32_t op_parity = 0;
-            for (int i = 0; i < ns; ++i) {
-                const bool ok = wait(a_ready(i % C::kABufs), (i / C::kABufs) & 1) && wait(b_ready(op), op_parity) && !lost();
-                if (!__all_sync(~0u, ok)) break;
-                ptx::tc_fence_after();
-                ptx::tc_fence_before();
-                if (lane == 0) arrive_at(peer(op), 0);
-                if (++op == C::kOps) op = 0, op_parity ^= 1;
-            }
+            for (int x = 0; x < kStageK / 16; ++x)
+                mma_ts(lead, t_d, t_a(i % C::kABufs) + 8 * x, b + (uint32_t)((x >> 2) * kN * 8 + (x & 3) * 2), idesc, i > 0 || x > 0);
+            mma_commit(lead, a_free(i % C::kABufs));
+            mma_commit(lead, b_free(op));
+            if (++op == C::kOps) op = 0, op_parity ^= 1;
         }
+        __syncwarp();
+        mma_commit(lead, done);   // all that was issued, however the loop ended
     } else if (warp == C::kWarpTma) {
         // ------------------------------------------------------- TMA
         if (lane == 0) {
             int slot = 0, count = 0;
             uint32_t parity = 1;
-            const int row = m0 + (kPair > 1 ? rank * C::kRows : 0);
             for (int i = 0; i < ns; ++i) {
                 if (!wait(raw_empty(slot), parity) || lost()) break;
                 const uint32_t at = sbase + slot * C::kRaw;
                 ptx::mbar_arrive_expect_tx(raw_full(slot), C::kRaw);
                 ptx::tma_load_2d(at, &tm_w, raw_full(slot), (st0 + i) * kStageK, n0);
-                ptx::tma_load_2d(at + C::kW, &tm_x, raw_full(slot), (st0 + i) * kStageK, row);
+                ptx::tma_load_2d(at + C::kW, &tm_x, raw_full(slot), (st0 + i) * kStageK, m0);
                 ++count;
                 if (++slot == C::kStages) slot = 0, parity ^= 1;
             }
@@ -270,17 +171,14 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         }
     } else if (warp >= 8) {
         // ------------------------------------------------------- inputs
-        // Sixteen codes a unit, eight units a row.  Lanes of a row's second 64 write
-        // their upper half first: eight lanes are then in eight different sixteen-byte
-        // banks.
-        constexpr int kLanes = C::kWiden / C::kTurns * 32, kPer = C::kRows * 8 / kLanes, kOnce = kPer < 8 ? kPer : 8;
+        // Sixteen codes a unit, eight units a row.
+        constexpr int kLanes = C::kWiden / C::kTurns * 32, kPer = kN * 8 / kLanes, kOnce = kPer < 8 ? kPer : 8;
         const int turn = (tid - 256) / kLanes, t = (tid - 256) % kLanes, u = t & 7, row0 = t >> 3;
-        const uint32_t second = u >> 2;
         for (int i = turn; i < ns; i += C::kTurns) {
             const int slot = i % C::kStages, op = i % C::kOps;
             bool ok = wait(raw_full(slot), (i / C::kStages) & 1);
             if (!__all_sync(~0u, ok)) break;
-            unsigned char *const to = smem + C::kOpAt + op * C::kOp + (u >> 2) * C::kRows * 128;
+            unsigned char *const to = smem + C::kOpAt + op * C::kOp + (u >> 2) * kN * 128;
 #pragma unroll
             for (int pass = 0; pass < kPer / kOnce; ++pass) {
                 uint4 raw[kOnce];
@@ -300,15 +198,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
                 for (int x = 0; x < kOnce; ++x) {
                     const int row = row0 + (pass * kOnce + x) * (kLanes / 8);
-                    uint32_t o[8];
-                    frag::i8_halves(raw[x].x, o[0], o[1]);
-                    frag::i8_halves(raw[x].y, o[2], o[3]);
-                    frag::i8_halves(raw[x].z, o[4], o[5]);
-                    frag::i8_halves(raw[x].w, o[6], o[7]);
-                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                    const uint32_t at = row * 128 + ((((u & 3) * 2 + second) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(to + at) = second ? hi : lo;
-                    *reinterpret_cast<uint4 *>(to + (at ^ 16)) = second ? lo : hi;
+                    widen_input(to, row, u, raw[x]);
                 }
             }
             if (!__all_sync(~0u, ok)) break;
@@ -328,14 +218,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t a[32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(from + (((4 * h + q) ^ (row & 7)) << 4));
-                    frag::i8_halves(w.x, a[8 * q], a[8 * q + 1]);
-                    frag::i8_halves(w.y, a[8 * q + 2], a[8 * q + 3]);
-                    frag::i8_halves(w.z, a[8 * q + 4], a[8 * q + 5]);
-                    frag::i8_halves(w.w, a[8 * q + 6], a[8 * q + 7]);
-                }
+                widen_weights(from, row, h, a);
                 if (h == 0) {
                     ok = wait(a_free(buf), (i / C::kABufs + 1) & 1) && !lost();
                     if (!__all_sync(~0u, ok)) break;
@@ -378,26 +261,19 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
                 for (int e = 0; e < kPart; ++e) v[e] = 0;
             }
+            if (split > 1) {
 #pragma unroll
-            for (int e = 0; e < kPart; ++e) {
-                const int m = m0 + col + e;
-                if (kPair == 1 && split > 1) {
-                    sum[(col + e) * kPitch + row] = __uint_as_float(v[e]);
-                } else if (m < L.rows && n < L.n) {
-                    float y = __uint_as_float(v[e]) * (xs[col + e] * ws) + bias;
-                    if (L.act == CBS_ACT_SILU) y = silu(y);
-                    const size_t at = (size_t)m * L.n + n;
-                    if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at] = __float2bfloat16_rn(y);
-                    else static_cast<float *>(L.y)[at] = y;
-                }
+                for (int e = 0; e < kPart; ++e) sum[(col + e) * kPitch + row] = __uint_as_float(v[e]);
+            } else if (n < L.n) {
+                store_rows(L, m0 + col, n, v, xs + col, ws, bias);
             }
         }
     }
     ptx::tc_fence_before();
-    if (kPair > 1 || split > 1) cluster_sync();
+    if (split > 1) cluster_sync();
     else __syncthreads();
-    if (warp == C::kWarpMma) T::dealloc(tmem, C::kTmem);
-    if (kPair > 1 || split == 1) return;
+    if (warp == C::kWarpMma) ptx::tmem_dealloc(tmem, C::kTmem);
+    if (split == 1) return;
     // Four outputs of a row at a time, every share's on their way together.
     const int rows = min(kN, L.rows - m0);
     for (int i = tid + share * C::kThreads; i < kOut / 4 * rows; i += C::kThreads * split) {
@@ -435,35 +311,25 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     cluster_sync();   // nobody's sums go while another CTA reads them
 }
 
-template <int kN, int kPair>
+template <int kN>
 cbs_status launch_w8_one(const W8Launch &L, int split, cudaStream_t s) {
-    using C = W8Tile<kN, kPair>;
-    EncodeTiledFn fn = encode_tiled();
-    if (!fn) return fail(CBS_ERR_CUDA, "cannot resolve cuTensorMapEncodeTiled from the driver");
+    using C = W8Tile<kN>;
     alignas(64) CUtensorMap tw, tx;
-    const auto map = [&](CUtensorMap *tm, const void *p, int rows, int box_rows) {
-        const cuuint64_t dims[2] = {(cuuint64_t)L.k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)L.k};
-        const cuuint32_t box[2] = {(cuuint32_t)kStageK, (cuuint32_t)box_rows}, es[2] = {1u, 1u};
-        return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    CUresult r = map(&tw, L.w, L.n, kOut);
-    if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (weights) failed (%d)", (int)r);
-    r = map(&tx, L.x, L.rows, C::kRows);
-    if (r != CUDA_SUCCESS) return fail(CBS_ERR_CUDA, "cuTensorMapEncodeTiled (inputs) failed (%d)", (int)r);
-    const int tiles = (L.n + kOut * kPair - 1) / (kOut * kPair), row_tiles = (L.rows + kN - 1) / kN;
-    auto kern = w8_kernel<kN, kPair>;
+    CBS_TRY(codes_map(&tw, L.w, L.k, L.n, kOut));
+    CBS_TRY(codes_map(&tx, L.x, L.k, L.rows, kN));
+    const int tiles = (L.n + kOut - 1) / kOut, row_tiles = (L.rows + kN - 1) / kN;
+    auto kern = w8_kernel<kN>;
     static ContextOfDevice set;
     cudaError_t e = set_max_dyn_smem_once(kern, C::kSmem, set);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(tiles * split * kPair, row_tiles);
+        cfg.gridDim = dim3(tiles * split, row_tiles);
         cfg.blockDim = dim3(C::kThreads);
         cfg.dynamicSmemBytes = C::kSmem;
         cfg.stream = s;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = split * kPair;
+        attr[0].val.clusterDim.x = split;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -506,7 +372,8 @@ __global__ void quantize_w8_kernel(const float *__restrict__ w, int n, int k, in
 // us for 6.4).
 struct W8Cost { int rows, alone, stage, two, stage2, share; };
 constexpr W8Cost kCosts[] = {{16, 134, 47, 140, 71, 15}, {32, 168, 39, 188, 67, 20}, {64, 208, 53, 241, 88, 16},
-                             {128, 410, 49, 0, 0, 12}, {256, 606, 56, 0, 0, 0}};
+                             {128, 410, 49, 0, 0, 12}, {256, 450, 56, 0, 0, 0}};
+constexpr int kPairTile = 150;   // a tile of 256 more: what a pair's next one waits for
 // Of 152 SMs with a CTA each, that many clusters of 1, 2, 4 and 8 run at once.
 constexpr int kAtOnce[] = {152, 76, 36, 15};
 //
@@ -535,7 +402,7 @@ cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
             long long cost;
             if (c.rows == 256) {   // pairs of CTAs
                 const long long pairs = std::max(sms / 2, 1ll), tiles = (L.n + 2 * kOut - 1) / (2 * kOut) * row_tiles;
-                cost = (tiles + pairs - 1) / pairs * (c.alone + each * c.stage);
+                cost = c.alone + (tiles + pairs - 1) / pairs * (kPairTile + each * c.stage);
             } else {
                 const long long at_once = std::max(kAtOnce[i] * sms / 152, 1ll), per = ((L.n + kOut - 1) / kOut * row_tiles + at_once - 1) / at_once;
                 cost = c.two ? per / 2 * (c.two + each * c.stage2) + per % 2 * (c.alone + each * c.stage) : per * (c.alone + each * c.stage);
@@ -545,11 +412,11 @@ cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
         }
     }
     switch (rows) {
-    case 16: return launch_w8_one<16, 1>(L, split, s);
-    case 32: return launch_w8_one<32, 1>(L, split, s);
-    case 64: return launch_w8_one<64, 1>(L, split, s);
-    case 128: return launch_w8_one<128, 1>(L, split, s);
-    default: return launch_w8_one<256, 2>(L, 1, s);
+    case 16: return launch_w8_one<16>(L, split, s);
+    case 32: return launch_w8_one<32>(L, split, s);
+    case 64: return launch_w8_one<64>(L, split, s);
+    case 128: return launch_w8_one<128>(L, split, s);
+    default: return launch_w8_pair(L, s);
     }
 }
 

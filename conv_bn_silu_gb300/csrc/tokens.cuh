@@ -108,6 +108,7 @@ struct W8Launch {
     int rows, n, k, out_bf16, act;
 };
 cbs_status launch_w8(const W8Launch &L, cudaStream_t s);
+cbs_status launch_w8_pair(const W8Launch &L, cudaStream_t s);    // tiles of 256 rows
 cudaError_t launch_w8_few(const W8Launch &L, cudaStream_t s);   // up to sixteen rows
 cudaError_t launch_quantize_w8(const float *w, int n, int k, int8_t *codes, float *scales, cudaStream_t s);
 
