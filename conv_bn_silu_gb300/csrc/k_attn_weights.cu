@@ -12,8 +12,11 @@
 // that know the rows' sums; else the first kernel here does.  Chunks would leave too many: the
 // second kernel takes the first product again, S^T = K Q^T on tcgen05 with 128 keys as
 // the lanes of tensor memory.  A key tile stays where it is while the rows' tiles
-// pass, and a thread's sum over them never leaves its registers.  The exponentials
-// bound it: one a score, sixteen a clock and SM.
+// pass, and a thread's sum over them never leaves its registers.  The exponentials,
+// one a score and sixteen a clock and SM, bound it from below: 1024 tokens over 16384
+// keys, 32 heads, 107 us of them; it takes 155, for a buffer of scores goes from hand to
+// hand in some 3000 cycles.  (32 streams of one token, 8192 keys, 8 bits: the first
+// kernel 15 us after an attention of 125.)
 #include "attn_common.cuh"
 #include "tc_ptx.cuh"
 #include "tc_warp.cuh"

@@ -9,6 +9,9 @@
 // distributed shared memory), and one scan over (heavier, equal) counts gives
 // every position that stays its place, equal weights by position.  The second
 // copies rows, sixteen bytes a thread: reading and writing them once bounds it.
+//
+// Measured, 16 sequences of up to 8192 positions, 4096 kept, 8 heads of 128: bf16 105 us;
+// 8 bits 64 us, of which the choice takes 17 and the rows 47 (4.8 TB/s).
 #include "tc_ptx.cuh"
 #include "tc_warp.cuh"
 #include "tokens.cuh"

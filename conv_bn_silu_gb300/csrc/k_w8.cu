@@ -15,6 +15,9 @@
 //
 // For few rows the weights' bytes bound it.  Shares of k are then CTAs of a cluster,
 // which add their sums in order through distributed shared memory.
+//
+// Measured with the weights in turn (not in L2), 16384 x 8192: 32 rows 28 us, 4.8 TB/s;
+// 128 rows 37 us, 0.94 PFLOP/s.  1001 x 2064, 400 rows 9.7 us: starts and ends.
 #include <algorithm>
 
 #include "w8.cuh"
@@ -367,13 +370,14 @@ __global__ void quantize_w8_kernel(const float *__restrict__ w, int n, int k, in
 // The tile and the shares of k, by what was measured (hundredths of a microsecond; 60
 // sizes of 256 x 1024 to 16384 x 8192, 1 to 6400 rows, every tile with 1 to 8 shares):
 // a CTA's start and end and each of its stages, alone on its SM and, for the tiles of
-// which two fit, for two side by side; and a share's part of the join.  What it takes
-// is 0.8% slower than the best on average and 13% at worst (256 x 1024, 1600 rows: 7.2
-// us for 6.4).
+// which two fit, for two side by side; and the join of shares.  What it takes is 0.8%
+// slower than the best on average and 19% at worst (1024 x 256, 6400 rows: 14.9 us for
+// 12.6).
 struct W8Cost { int rows, alone, stage, two, stage2, share; };
-constexpr W8Cost kCosts[] = {{16, 134, 47, 140, 71, 15}, {32, 168, 39, 188, 67, 20}, {64, 208, 53, 241, 88, 16},
-                             {128, 410, 49, 0, 0, 12}, {256, 450, 56, 0, 0, 0}};
-constexpr int kPairTile = 150;   // a tile of 256 more: what a pair's next one waits for
+constexpr W8Cost kCosts[] = {{16, 88, 45, 72, 68, 0}, {32, 128, 36, 128, 65, 0}, {64, 130, 51, 173, 84, 0},
+                             {128, 227, 49, 0, 0, 22}, {256, 142, 55, 0, 0, 0}};
+constexpr int kJoin = 146;
+constexpr int kPairTile = 373;   // of a tile of 256, beside its stages: where the next one's begin late
 // Of 152 SMs with a CTA each, that many clusters of 1, 2, 4 and 8 run at once.
 constexpr int kAtOnce[] = {152, 76, 36, 15};
 //
@@ -405,8 +409,8 @@ cbs_status launch_w8(const W8Launch &L, cudaStream_t s) {
                 cost = c.alone + (tiles + pairs - 1) / pairs * (kPairTile + each * c.stage);
             } else {
                 const long long at_once = std::max(kAtOnce[i] * sms / 152, 1ll), per = ((L.n + kOut - 1) / kOut * row_tiles + at_once - 1) / at_once;
-                cost = c.two ? per / 2 * (c.two + each * c.stage2) + per % 2 * (c.alone + each * c.stage) : per * (c.alone + each * c.stage);
-                if (x > 1) cost += x * c.share;
+                const long long join = x > 1 ? kJoin + x * c.share : 0;
+                cost = c.two ? per / 2 * (c.two + each * c.stage2 + join) + per % 2 * (c.alone + each * c.stage + join) : per * (c.alone + each * c.stage + join);
             }
             if (!rows || cost < best) best = cost, rows = c.rows, split = x;
         }

@@ -6,6 +6,9 @@
 // lane's share of an output is sixteen consecutive codes, loaded at once; both sides
 // widen exactly to f16.  No shared memory, barrier or hand-off before the end, where
 // the warps' sums meet in order: whole numbers, exact below 2^24 in any order.
+//
+// Measured, one row: 6144 x 4096 6.6 us, 3.8 TB/s; 16384 x 8192 26.5 us, 5.1 TB/s; 60% of the
+// issue slots.
 #include <cuda_bf16.h>
 
 #include "mma_frag.cuh"

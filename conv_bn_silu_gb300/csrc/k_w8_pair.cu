@@ -6,6 +6,9 @@
 // Persistent: a pair takes tiles in turn.  The loads and the widening run on into the
 // next tile, whose first MMA waits only until warps of their own have read the last
 // one's sums; a CTA's start (tensor memory, barriers, the first loads) is paid once.
+//
+// Measured: 8192 rows of 8192 x 8192 549 us, 2.0 PFLOP/s; 1024 rows 82 us, 1.67; 2048 rows
+// of 4096 x 8192 with the tensor pipe 84% active and 55% of the issue slots (widening).
 #include <algorithm>
 
 #include "w8.cuh"
