@@ -7,7 +7,8 @@
 // A key/value head's G query heads and the chunk's tokens make the rows of one
 // product (row = t G + g), so K and V are read once for all of them.  HBM (or
 // L2) bandwidth bounds it: each CTA takes 8 or 16 rows and a range of keys, its
-// warps blocks of 16 keys in turn, straight from global memory to registers.
+// warps blocks of 16 keys in turn, in bf16 straight from global memory to registers,
+// in 8 bits through a ring of three blocks a warp in shared memory.
 // The products are S^T = K Q^T and O^T = V^T P^T: keys, then head dimensions,
 // fill the 16 rows of the MMA and the few query rows its 8 columns, so no lane
 // of a single-token call's MMA is spent on rows that do not exist twice over.
@@ -17,10 +18,11 @@
 //
 // One token of 32 heads, 8 key heads of 128: 1000 keys 5.6 us (latency: 8 ranges in
 // clusters; 6.8 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
-// and 208 us in 8 bits, 4.0 TB/s (225 with keys widened to bf16).  In 8 bits neither
-// memory (half its rate) nor the issue slots (46%) are full: warps wait for their
-// loads, twelve of them an SM with a block of 16 keys each, half the bytes in
-// flight of bf16.
+// and 155 us in 8 bits, 5.4 TB/s.  (With 8 bits in registers too, 205 us: twelve warps an
+// SM waited for a block of 16 keys each, half the bytes in flight of bf16.  The ring
+// has two blocks on their way beside the one at hand, and sixteen warps.  16 sequences
+// of 4000, 32 rows: 98 -> 73; head dimension 64, 64 of 8000: 126 -> 97; one of 1000: 6.2 ->
+// 5.9.)
 //
 // Up to eight ranges of keys are the CTAs of a cluster, which join them from each
 // other's shared memory; more are joined through the workspace by the CTA that
@@ -98,15 +100,84 @@ struct KvFrag {
     }
 };
 
-// CTAs an SM: what fits without spilled registers (head dimension 64 at five in
-// place of three: 64 x 8000 keys 202 -> 150 us in 8 bits, 185 -> 163 in bf16;
-// 128 at four in place of three, 8 x 8000 keys: 44 -> 53 in 8 bits, 51 -> 69).
+// 8 bits: a warp's ring of blocks in shared memory, filled by its lanes' asynchronous
+// copies.  A block's 16 rows of K, of V, then the scales of both; 16-byte units are
+// permuted within 128 bytes, so that V's reads of eight lanes meet all banks.
+template <int D>
+struct KvRing {
+    static constexpr int kStages = 3, kRows = kBlock * D, kStage = 2 * kRows + 128, kWarp = kStages * kStage;
+    int put[2], k_at, v_at[2];   // of a lane
+    __device__ __forceinline__ explicit KvRing(int lane) {
+        const int g = lane >> 2, j = lane & 3;
+        if constexpr (D == 128) {
+            put[0] = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) * 16);
+            put[1] = put[0] ^ 64;
+            k_at = g * 128 + ((j ^ g) * 16);
+            v_at[0] = 2 * j * 128 + ((g ^ (2 * j)) * 16);
+            v_at[1] = (2 * j + 1) * 128 + ((g ^ (2 * j + 1)) * 16);
+        } else {
+            put[0] = put[1] = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) * 16);
+            k_at = g * 64 + ((j ^ (g >> 1)) * 16);
+            v_at[0] = 2 * j * 64 + (((g >> 1) ^ j) * 16) + (g & 1) * 8;
+            v_at[1] = v_at[0] + 64;
+        }
+    }
+    // A block whose first row is row0, all of it (a block lies within a page).
+    __device__ __forceinline__ void copy(const CacheArgs &c, size_t row0, uint32_t to, int lane) const {
+        const char *k = static_cast<const char *>(c.k) + row0 * D + lane * 16, *v = static_cast<const char *>(c.v) + row0 * D + lane * 16;
+#pragma unroll
+        for (int i = 0; i < kRows / 512; ++i) {
+            ptx::cp_async_16(to + i * 512 + put[i & 1], k + i * 512, 16);
+            ptx::cp_async_16(to + kRows + i * 512 + put[i & 1], v + i * 512, 16);
+        }
+        const float *sc = (lane < 16 ? c.k_scale : c.v_scale) + row0 + (lane & 15);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 2 * kRows + lane * 4), "l"(sc) : "memory");
+    }
+    __device__ __forceinline__ void read_k(KvFrag<D, true> &f, const unsigned char *at, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int q = 0; q < KvFrag<D, true>::kKC; ++q)
+                f.k[i][q] = *reinterpret_cast<const uint4 *>(at + i * 8 * D + (k_at ^ (q * 64)));
+            f.ks[i] = *reinterpret_cast<const float *>(at + 2 * kRows + ((lane >> 2) + 8 * i) * 4);
+        }
+    }
+    __device__ __forceinline__ void read_v(KvFrag<D, true> &f, const unsigned char *at, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned char *p = at + kRows + (i >> 1) * 8 * D + v_at[i & 1];
+            if constexpr (D == 64) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(p);
+                f.v[i][0] = w.x; f.v[i][1] = w.y;
+            } else {
+                const uint4 w = *reinterpret_cast<const uint4 *>(p);
+                f.v[i][0] = w.x; f.v[i][1] = w.y; f.v[i][2] = w.z; f.v[i][3] = w.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f.vs[i] = *reinterpret_cast<const float *>(at + 2 * kRows + 64 + ((lane >> 2) + 8 * i) * 4);
+    }
+};
+
+// CTAs an SM: what fits without spilled registers (bf16: head dimension 64 at five in
+// place of three, 64 x 8000 keys: 185 -> 163 us; 128 at four in place of three, 8 x 8000
+// keys: 51 -> 69.  8 bits: 128 at four in place of three, 64 x 1000 keys 30.5 -> 28.9, 16 x
+// 4000 34.0 -> 35.0, and with two tiles of rows at three in place of two 84 -> 73; 64 at
+// six in place of five, 64 x 8000 keys: 97 -> 104).
+constexpr int rows_ctas(int d, bool i8, int nr) { return d == 64 ? (nr == 2 ? 4 : 5) : i8 ? (nr == 2 ? 3 : 4) : nr == 2 ? 2 : 3; }
 template <int D, bool I8, int NR, int MODE>
-__global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR == 2 ? 4 : 5)) attn_rows_kernel(const AttnLaunch L) {
+__global__ void __launch_bounds__(kThreads, rows_ctas(D, I8, NR)) attn_rows_kernel(const AttnLaunch L) {
     constexpr int kRows = 8 * NR;
     constexpr int kMT = D / 16;              // 16-dimension tiles of O^T
     using F = KvFrag<D, I8>;
-    __shared__ __align__(16) float s_o[kWarps][kRows][D + 4];
+    // The warps' shares at the end; in 8 bits each where the warp's ring was.
+    using Ring = KvRing<D>;
+    constexpr int kPitch = D + 4, kShare = I8 ? Ring::kWarp / 4 : kRows * kPitch;
+    static_assert(kShare >= kRows * kPitch, "a share fits where the ring was");
+    __shared__ __align__(16) float s_bf16[I8 ? 4 : kWarps * kShare];
+    extern __shared__ __align__(128) unsigned char s_ring[];
+    float *const s_o = I8 ? reinterpret_cast<float *>(s_ring) : s_bf16;
+    const auto share = [&](int w, int r, int dim) { return s_o + w * kShare + r * kPitch + dim; };
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     __shared__ float2 s_stat[kRows];   // a range's (maximum, sum), for the other CTAs of a cluster
     // kAttnWeighed: sums of the probabilities before they are rounded (in 8 bits s_l has those).
@@ -233,13 +304,45 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 
     F f;
     int blk = b0 + warp;
-    unsigned live, live_next;
-    size_t row = place_of(blk, live), row_next = place_of(blk + kWarps, live_next);
-    f.load_k(c, row, lane, live);
-    f.load_v(c, row, lane, live);
+    unsigned live, live_next;   // of the block at hand, of the next one to load
+    size_t row, row_next;
+    // 8 bits: blocks on their way, the next one's first.
+    constexpr int kAhead = Ring::kStages - 1;
+    const Ring ring(lane);
+    const unsigned char *const ring_at = s_ring + warp * Ring::kWarp;
+    const uint32_t ring_to = ptx::smem_u32(ring_at);
+    unsigned coming[kAhead];
+    int stage = 0;   // bytes
+    if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            row = place_of(blk + i * kWarps, coming[i]);
+            if (coming[i]) ring.copy(c, row, ring_to + i * Ring::kStage, lane);
+            ptx::cp_async_commit();
+        }
+        row_next = place_of(blk + kAhead * kWarps, live_next);
+    } else {
+        row = place_of(blk, live);
+        row_next = place_of(blk + kWarps, live_next);
+        f.load_k(c, row, lane, live);
+        f.load_v(c, row, lane, live);
+    }
     bool poison = false;
     while (blk < b1) {
         const int pos = lo16 + blk * kBlock;
+        if constexpr (I8) {
+            // This block has arrived, and every lane is done with the one before.
+            ptx::cp_async_wait<kAhead - 1>();
+            __syncwarp();
+            if (live_next) ring.copy(c, row_next, ring_to + (stage ? stage - Ring::kStage : kAhead * Ring::kStage), lane);
+            ptx::cp_async_commit();
+            live = coming[0];
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) coming[i] = coming[i + 1];
+            coming[kAhead - 1] = live_next;
+            row_next = place_of(blk + (kAhead + 1) * kWarps, live_next);
+            ring.read_k(f, ring_at + stage, lane);
+        }
         // ---- S^T = K Q^T
         float s[NR][4];
 #pragma unroll
@@ -271,11 +374,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         const float ks0 = I8 ? f.ks[0] * L.scale_log2 : L.scale_log2, ks1 = I8 ? f.ks[1] * L.scale_log2 : L.scale_log2;
         // The next block's keys, while this one's scores become probabilities.
         const int next = blk + kWarps;
-        row = row_next;
-        live = live_next;
-        f.load_k(c, row, lane, live);
-        row_next = place_of(next + kWarps, live_next);
-        prefetch(row_next, live_next);
+        if constexpr (!I8) {
+            row = row_next;
+            live = live_next;
+            f.load_k(c, row, lane, live);
+            row_next = place_of(next + kWarps, live_next);
+            prefetch(row_next, live_next);
+        }
 
         // ---- scores, in base 2; keys a row does not see become -inf
         const bool partial = now != 0xffffu || pos < all_lo || pos + kBlock > all_hi;
@@ -309,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
                     if (r < R && key < L.len_pad) scores[n][i & 1][key] = s[n][i];
                 }
         }
+        if constexpr (I8) ring.read_v(f, ring_at + stage, lane);
         // ---- running maximum
         float top[NR][2];
         bool grow = false;
@@ -399,10 +505,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
                 for (int n = 0; n < NR; ++n) frag::mma(o[n][w], a0, a1, a2, a3, p0[n], p1[n]);
             }
         }
-        f.load_v(c, row, lane, live);
+        if constexpr (I8) stage = stage == kAhead * Ring::kStage ? 0 : stage + Ring::kStage;
+        else f.load_v(c, row, lane, live);
         blk = next;
     }
     if (poison) s_flag = 1;
+    if constexpr (I8) __syncwarp();   // the ring's place becomes the share's
 
     // ---- the warps' shares, joined in shared memory
 #pragma unroll
@@ -429,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
 #pragma unroll
             for (int d = 0; d < kMT; ++d) {
                 const int dim = I8 ? g * (D / 8) + 2 * d : (d >> 2) * 64 + g * 8 + 2 * (d & 3);
-                s_o[warp][r][dim] = o[n][d][i];
-                s_o[warp][r][dim + 1] = o[n][d][2 + i];
+                share(warp, r, dim)[0] = o[n][d][i];
+                share(warp, r, dim)[1] = o[n][d][2 + i];
             }
         }
     __syncthreads();
@@ -443,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
             float acc[kE], mm, ll;
             slow_row<D, false>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s_o[0][r][lane * kE + e] = acc[e];
+            for (int e = 0; e < kE; ++e) *share(0, r, lane * kE + e) = acc[e];
             if (lane < kWarps) {
                 s_m[lane][r] = lane == 0 ? mm : -INFINITY;
                 s_l[lane][r] = lane == 0 ? ll : 0.0f;
@@ -468,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         for (int w = 0; w < kWarps; ++w) {
             const float fac = share_factor(s_m[w][r], s_l[w][r], top);
             if (s_m[w][r] == -INFINITY && fac == 0.0f) continue;
-            const float4 v = *reinterpret_cast<const float4 *>(&s_o[w][r][4 * u]);
+            const float4 v = *reinterpret_cast<const float4 *>(share(w, r, 4 * u));
             acc.x = fmaf(v.x, fac, acc.x); acc.y = fmaf(v.y, fac, acc.y);
             acc.z = fmaf(v.z, fac, acc.z); acc.w = fmaf(v.w, fac, acc.w);
             sum = fmaf(s_l[w][r], fac, sum);
@@ -481,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
                 if (u == 0) s_fin[r] = row_stats(z.hi > z.lo, top, exact);
             }
         } else if (L.cluster) {   // (a unit's own place, which nobody else has read)
-            *reinterpret_cast<float4 *>(&s_o[0][r][4 * u]) = acc;
+            *reinterpret_cast<float4 *>(share(0, r, 4 * u)) = acc;
             if (u == 0) s_stat[r] = make_float2(top, sum);
             if constexpr (kExact)
                 if (u == 0) s_statx[r] = exact;
@@ -536,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? (NR == 2 ? 2 : 3) : (NR =
         for (int i = sp * kThreads + tid; i < kRows * kU; i += active * kThreads) {
             const int r = i / kU, u = i % kU;
             if (r0 + r >= R) break;
-            const uint32_t o_at = ptx::smem_u32(&s_o[0][r][4 * u]), s_at = ptx::smem_u32(&s_stat[r]);
+            const uint32_t o_at = ptx::smem_u32(share(0, r, 4 * u)), s_at = ptx::smem_u32(&s_stat[r]);
             float2 st[kAttnClusterMost];
             float4 v[kAttnClusterMost];
             float top = -INFINITY, sum = 0.0f, exact = 0.0f;
@@ -582,8 +690,14 @@ cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.cluster ? 2 : 1;
-    if constexpr (I8)
+    if constexpr (I8) {
+        cfg.dynamicSmemBytes = kWarps * KvRing<D>::kWarp;
+        static ContextOfDevice set1, set2;
+        cudaError_t e = row_tile == 16 ? set_max_dyn_smem_once(attn_rows_kernel<D, I8, 2, MODE>, (int)cfg.dynamicSmemBytes, set2)
+                                       : set_max_dyn_smem_once(attn_rows_kernel<D, I8, 1, MODE>, (int)cfg.dynamicSmemBytes, set1);
+        if (e != cudaSuccess) return e;
         if (row_tile == 16) return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 2, MODE>, L);
+    }
     return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 1, MODE>, L);
 }
 

@@ -104,8 +104,8 @@ constexpr int kGridMax = 65535;
 // 16, 32, 64 rows: bf16 (tiles of 8 rows), one sequence of 4000 keys 11/13, 13/13,
 // 18/14, 24/14; 16 of 4000 53/56, 82/56, 134/56, 238/57; 64 of 1000 59/79, 78/80,
 // 127/82, 226/85.  8 bits (tiles of 16 from 16 rows on; the chunk kernel widens every
-// code first): 11/19, 11/19, 14/19, 17/20; 46/119, 54/120, 100/120, 165/119; 50/126,
-// 51/127, 94/126, 160/127.
+// code first): 10/20, 12/20, 15/20, 18/20; 35/121, 47/121, 77/121, 133/121; 32/127,
+// 42/126, 66/127, 124/127.
 constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
 // Of 152 SMs with one CTA each, that many clusters of x of the chunk kernel's CTAs run at once.
@@ -328,20 +328,23 @@ cbs_status attn_plan(const cbs_attn_desc *d, int few, cbs_attn_plan_t *out) {
 }
 
 // What a plan's call takes, in nanoseconds: a few-row tile's thousand keys by head
-// dimension and type, or the chunk kernel's tiles.
+// dimension and type (in 8 bits a tile's start and end are worth 160 more), or the chunk
+// kernel's tiles.
 long long attn_ns(const cbs_attn_plan_t &p, int sms) {
     const cbs_attn_desc &d = p.desc;
     const long long base = (long long)std::max(d.batch, 1) * d.kv_heads * p.row_tiles;
     if (p.kernel == CBS_ATTN_CHUNK) return chunk_ns(d, base, p.split, sms);
-    const int thousand = d.cache_prec == CBS_INT8 ? (d.head_dim == 64 ? 50 : 80) : d.head_dim == 64 ? 40 : 75;
-    return 4500 + base * d.max_len / 1000 * thousand;
+    const bool int8 = d.cache_prec == CBS_INT8;
+    const int thousand = int8 ? (d.head_dim == 64 ? 28 : 47) : d.head_dim == 64 ? 40 : 75;
+    return 4500 + base * (d.max_len + (int8 ? 160 : 0)) / 1000 * thousand;
 }
 
 // The faster kernel for a part of a call whose rows are more than the few-row
 // kernels' own: short sequences do not repay a chunk's start.  (`more`: what follows
 // the few-row kernel less what follows the chunk kernel.)  Head dimension 64, bf16, few
 // rows and chunks: 64 rows of 400 keys, two heads 5.2 and 9.2 us, 64 heads 11.4 and 9.5;
-// 8 bits, 64 rows of 400 keys, 320 heads 30 and 43, of 1500 99 and 88.
+// 8 bits, 64 rows of 200 keys, 512 heads 23 and 42, of 1000 62 and 81, and 128 rows 113
+// and 82.
 cbs_status attn_plan_by_time(const cbs_attn_desc *d, long long (*more)(const cbs_attn_plan_t &few, const cbs_attn_plan_t &chunk, int sms),
                              cbs_attn_plan_t *out) {
     CBS_TRY(attn_plan(d, -1, out));
@@ -479,7 +482,7 @@ cbs_status cbs_weighed_plan(const cbs_attn_desc *d, cbs_weighed_plan_t *out) {
         const cbs_attn_desc &d = few.desc;
         const long long rows = (long long)d.max_new * (d.heads / d.kv_heads), heads = (long long)d.batch * d.kv_heads;
         const long long ctas = heads * chunk_key_tiles(d.max_len), rounds = (ctas + 2 * sms - 1) / (2 * sms);
-        return 5000 + heads * rows * d.max_len / 250 - rounds * (5500 + (rows + 127) / 128 * 800);
+        return 5000 + heads * rows * d.max_len / 700 - rounds * (5500 + (rows + 127) / 128 * 800);
     }, &p.attention));
     if ((d->max_len + 15ll) / 16 * 16 > INT_MAX) return fail(CBS_ERR_UNSUPPORTED, "max_len %d", d->max_len);
     p.workspace_bytes = weighed_parts(p.attention).all;
