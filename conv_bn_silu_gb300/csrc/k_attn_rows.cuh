@@ -159,14 +159,8 @@ struct KvRing {
     }
 };
 
-// CTAs an SM: what fits without spilled registers (bf16: head dimension 64 at five in
-// place of three, 64 x 8000 keys: 185 -> 163 us; 128 at four in place of three, 8 x 8000
-// keys: 51 -> 69.  8 bits: 128 at four in place of three, 64 x 1000 keys 30.5 -> 28.9, 16 x
-// 4000 34.0 -> 35.0, and with two tiles of rows at three in place of two 84 -> 73; 64 at
-// six in place of five, 64 x 8000 keys: 97 -> 104).
-constexpr int rows_ctas(int d, bool i8, int nr) { return d == 64 ? (nr == 2 ? 4 : 5) : i8 ? (nr == 2 ? 3 : 4) : nr == 2 ? 2 : 3; }
 template <int D, bool I8, int NR, int MODE>
-__global__ void __launch_bounds__(kThreads, rows_ctas(D, I8, NR)) attn_rows_kernel(const AttnLaunch L) {
+__global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_rows_kernel(const AttnLaunch L) {
     constexpr int kRows = 8 * NR;
     constexpr int kMT = D / 16;              // 16-dimension tiles of O^T
     using F = KvFrag<D, I8>;

@@ -5,13 +5,15 @@
 // Two kernels.  The first chooses: a cluster takes a (sequence, head), each of
 // its CTAs a run of the positions, whose weights become whole numbers of the same
 // order in shared memory.  A radix selection finds the lightest weight that stays
-// (11, 11 and 10 bits, from the top; the CTAs add their histograms up through
-// distributed shared memory), and one scan over (heavier, equal) counts gives
+// (11, 11 and 10 bits, from the top; the CTAs' histograms meet through distributed
+// shared memory, groups of 64 bins first), and one scan over (heavier, equal) counts gives
 // every position that stays its place, equal weights by position.  The second
 // copies rows, sixteen bytes a thread: reading and writing them once bounds it.
 //
-// Measured, 16 sequences of up to 8192 positions, 4096 kept, 8 heads of 128: bf16 105 us;
-// 8 bits 64 us, of which the choice takes 17 and the rows 47 (4.8 TB/s).
+// Measured, 16 sequences of up to 8192 positions, 4096 kept, 8 heads of 128: bf16 98 us;
+// 8 bits 58 us.  One of 65001, 4001 kept, 4 heads of 64: 19 us.
+#include <type_traits>
+
 #include "tc_ptx.cuh"
 #include "tc_warp.cuh"
 #include "tokens.cuh"
@@ -30,6 +32,13 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
+__device__ __forceinline__ int ld_cluster_int(const int *p, uint32_t rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ int2 ld_cluster_pair(const int *p, uint32_t rank) {
     uint32_t a;
     int2 v;
@@ -38,41 +47,25 @@ __device__ __forceinline__ int2 ld_cluster_pair(const int *p, uint32_t rank) {
     return v;
 }
 
-// Sum of a count over the threads before this one; one barrier.  `warps` is written
-// anew by the next call but one.
-__device__ __forceinline__ int scan(int v, int *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const auto inclusive = [&](int s) {
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int inclusive(int s) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(~0u, s, o);
-            if (lane >= o) s += a;
-        }
-        return s;
-    };
-    const int s = inclusive(v);
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    const int before = __shfl_sync(~0u, inclusive(warps[lane]), warp ? warp - 1 : 0);
-    return s - v + (warp ? before : 0);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(~0u, s, o);
+        if (lane >= o) s += a;
+    }
+    return s;
 }
 
-// The same of a pair of counts, and over all threads.
+// Sums of a pair of counts over the threads before this one and over all; one barrier.
 struct Pair { int a, b; };
 __device__ __forceinline__ Pair scan(Pair v, Pair &total, Pair *warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const auto inclusive = [&](Pair s) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(~0u, s.a, o), b = __shfl_up_sync(~0u, s.b, o);
-            if (lane >= o) s.a += a, s.b += b;
-        }
-        return s;
-    };
-    const Pair s = inclusive(v);
+    const Pair s = {inclusive(v.a), inclusive(v.b)};
     if (lane == 31) warps[warp] = s;
     __syncthreads();
-    const Pair w = inclusive(warps[lane]);
+    const Pair w = {inclusive(warps[lane].a), inclusive(warps[lane].b)};
     total = Pair{__shfl_sync(~0u, w.a, 31), __shfl_sync(~0u, w.b, 31)};
     const int from = warp ? warp - 1 : 0, a = __shfl_sync(~0u, w.a, from), b = __shfl_sync(~0u, w.b, from);
     return Pair{s.a - v.a + (warp ? a : 0), s.b - v.b + (warp ? b : 0)};
@@ -82,14 +75,14 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     extern __shared__ __align__(16) uint32_t s_keys[];   // this CTA's positions, at most L.run
     __shared__ __align__(8) int s_hist[3][kBins];
     __shared__ Pair s_warps[kThreads / 32];
-    __shared__ int s_totals[2][kThreads / 32];
+    __shared__ int s_groups[3][kThreads / 32];   // sums of 64 bins
     __shared__ int s_found[3][2];   // a pass's digit, and how many are to be taken of those that have it
     __shared__ __align__(8) int s_counts[2];   // heavier than the threshold, equal to it
     __shared__ int2 s_all[kMostCtas];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const CacheArgs &c = L.c;
-    const int tid = threadIdx.x, ctas = L.ctas, rank = ctas > 1 ? (int)cluster_rank() : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = L.ctas, rank = ctas > 1 ? (int)cluster_rank() : 0;
     const int head = blockIdx.y, b = blockIdx.z;
     const auto meet = [&] {
         if (ctas > 1) cluster_sync();
@@ -106,12 +99,41 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     const int shift = c.page_shift, slots = 1 << shift;
     for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
     if (tid < 6) s_found[0][tid] = 0;
-#pragma unroll 4
-    for (int i = tid; i < m; i += kThreads) {
-        const int pos = p0 + i, p = page_of(c, b, pos);
-        // (A page outside the pool: reported; its positions go first.)
-        s_keys[i] = p < 0 ? 0u : ordered(L.mass[(((size_t)p * c.kv_heads + head) << shift) + (pos & (slots - 1))]);
-    }
+    __syncthreads();
+    // Pages first, then weights, eight of each on their way at once (two where that is
+    // all): what is wrong is reported behind them.  (A page outside the pool: its
+    // positions go first.)  65001 positions of 4 heads 24.4 -> 18.9 us, with the groups below.
+    bool bad = false;
+    const auto load = [&](auto loads) {
+        constexpr int kLoads = decltype(loads)::value;
+        for (int i = tid; i < m; i += kLoads * kThreads) {
+            int page[kLoads];
+            float w[kLoads];
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const int at = i + x * kThreads, slot = (p0 + at) >> shift;
+                page[x] = at < m && slot < c.max_pages ? c.page_table[(size_t)b * c.max_pages + slot] : -1;
+            }
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const int pos = p0 + i + x * kThreads;
+                w[x] = (unsigned)page[x] < (unsigned)c.num_pages ? L.mass[(((size_t)page[x] * c.kv_heads + head) << shift) + (pos & (slots - 1))] : 0.0f;
+            }
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const int at = i + x * kThreads;
+                if (at >= m) break;
+                const bool in = (unsigned)page[x] < (unsigned)c.num_pages;
+                const uint32_t key = in ? ordered(w[x]) : 0u;
+                bad |= !in;
+                s_keys[at] = key;
+                atomicAdd(&s_hist[0][key >> 21], 1);
+            }
+        }
+    };
+    if (m <= 2 * kThreads) load(std::integral_constant<int, 2>{});
+    else load(std::integral_constant<int, 8>{});
+    if (bad) atomicOr(c.status, kStatusBadIndex);
     __syncthreads();
     uint32_t prefix = 0, mask = 0;   // the threshold's digits so far
     int left = take;                 // how many stay of those that share them
@@ -122,28 +144,40 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
             const int shift_to = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t digits = pass == 2 ? 1023u : 2047u;
             int *const hist = s_hist[pass];
-            for (int i = tid; i < m; i += kThreads) {
-                const uint32_t k = s_keys[i];
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift_to) & digits], 1);
+            if (pass) {
+                for (int i = tid; i < m; i += kThreads) {
+                    const uint32_t k = s_keys[i];
+                    if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift_to) & digits], 1);
+                }
+                __syncthreads();
             }
+            const int2 own = *reinterpret_cast<const int2 *>(&hist[2 * tid]);
+            const int sum = __reduce_add_sync(~0u, own.x + own.y);
+            if (lane == 0) s_groups[pass][warp] = sum;
             meet();
-            // Bins from the top: thread t has bins 2047 - 2t and 2046 - 2t, of all CTAs.
-            const int top = kBins - 1 - 2 * tid;
-            int x = 0, y = 0;
-            if (ctas == 1) {
-                x = hist[top], y = hist[top - 1];
-            } else {
-                int2 v[kMostCtas];
+            // From the top, of all CTAs: the group of 64 bins, then the bin.  (All bins of
+            // all CTAs read by all threads took 4500 cycles.)
+            if (warp == 0) {
+                int x = 0;
 #pragma unroll
                 for (int r = 0; r < kMostCtas; ++r)
-                    if (r < ctas) v[r] = ld_cluster_pair(&hist[top - 1], r);
+                    if (r < ctas) x += ctas == 1 ? s_groups[pass][31 - lane] : ld_cluster_int(&s_groups[pass][31 - lane], r);
+                const int before = inclusive(x) - x;
+                const unsigned hit = __ballot_sync(~0u, before < left && left <= before + x);
+                if (hit) {
+                    const int at = __ffs(hit) - 1, rest = left - __shfl_sync(~0u, before, at), bin = (31 - at) * 64 + 62 - 2 * lane;
+                    int2 v = {0, 0};
 #pragma unroll
-                for (int r = 0; r < kMostCtas; ++r)
-                    if (r < ctas) x += v[r].y, y += v[r].x;
+                    for (int r = 0; r < kMostCtas; ++r) {
+                        if (r >= ctas) break;
+                        const int2 o = ctas == 1 ? *reinterpret_cast<const int2 *>(&hist[bin]) : ld_cluster_pair(&hist[bin], r);
+                        v.x += o.x, v.y += o.y;
+                    }
+                    const int above = inclusive(v.x + v.y) - (v.x + v.y);
+                    if (above < rest && rest <= above + v.y) s_found[pass][0] = bin + 1, s_found[pass][1] = rest - above;
+                    else if (above + v.y < rest && rest <= above + v.y + v.x) s_found[pass][0] = bin, s_found[pass][1] = rest - above - v.y;
+                }
             }
-            const int before = scan(x + y, s_totals[pass & 1]);
-            if (before < left && left <= before + x) s_found[pass][0] = top, s_found[pass][1] = left - before;
-            else if (before + x < left && left <= before + x + y) s_found[pass][0] = top - 1, s_found[pass][1] = left - before - x;
             __syncthreads();
             prefix |= (uint32_t)s_found[pass][0] << shift_to;
             mask |= digits << shift_to;
@@ -185,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
 // Rows of K and V by the list, and what goes with them.  D * element bytes / 16
 // threads a row, kSteps rows of each thread on their way at a time: fewer a thread and
 // more CTAs hide the list's and the tables' loads better (16 sequences of 8192 to 4096
-// in bf16: four rows 124 us, two 115; in 8 bits 78 and 74, 4.9 TB/s with the choice).
+// in bf16: four rows 105 us, two 98; in 8 bits 63 and 58).
 constexpr int kMoveThreads = 256, kSteps = 2;
 
 template <int ROW>   // bytes of a row
@@ -201,18 +235,31 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
     size_t to[kSteps];
     float more[3][kSteps];   // weight and scales
     unsigned on = 0;
+    // Places, pages, rows: each step's on their way at once.  What is wrong is reported
+    // behind them.
+    int pos[kSteps], page[kSteps], new_page[kSteps];
+    bool bad = false;
 #pragma unroll
     for (int x = 0; x < kSteps; ++x) {
         const int r = r0 + x * kRows;
-        const int pos = r < L.keep ? kept[r] : -1;
-        if (pos < 0) continue;
-        const int p = page_of(c, b, pos);
-        const int slot = r >> c.page_shift, np = slot < L.new_max_pages ? L.new_table[(size_t)b * L.new_max_pages + slot] : -1;
-        if ((unsigned)np >= (unsigned)c.num_pages) atomicOr(c.status, kStatusBadIndex);
-        if (p < 0 || (unsigned)np >= (unsigned)c.num_pages) continue;
+        pos[x] = r < L.keep ? kept[r] : -1;
+    }
+#pragma unroll
+    for (int x = 0; x < kSteps; ++x) {
+        const int slot = pos[x] >> c.page_shift, new_slot = (r0 + x * kRows) >> c.page_shift;
+        page[x] = pos[x] >= 0 && slot < c.max_pages ? c.page_table[(size_t)b * c.max_pages + slot] : -1;
+        new_page[x] = pos[x] >= 0 && new_slot < L.new_max_pages ? L.new_table[(size_t)b * L.new_max_pages + new_slot] : -1;
+    }
+#pragma unroll
+    for (int x = 0; x < kSteps; ++x) {
+        if (pos[x] < 0) continue;
+        if ((unsigned)page[x] >= (unsigned)c.num_pages || (unsigned)new_page[x] >= (unsigned)c.num_pages) {
+            bad = true;
+            continue;
+        }
         on |= 1u << x;
-        const size_t from = (((size_t)p * c.kv_heads + head) << c.page_shift) + (pos & (slots - 1));
-        to[x] = (((size_t)np * c.kv_heads + head) << c.page_shift) + (r & (slots - 1));
+        const size_t from = (((size_t)page[x] * c.kv_heads + head) << c.page_shift) + (pos[x] & (slots - 1));
+        to[x] = (((size_t)new_page[x] * c.kv_heads + head) << c.page_shift) + ((r0 + x * kRows) & (slots - 1));
         w[0][x] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const char *>(c.k) + from * ROW) + u);
         w[1][x] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const char *>(c.v) + from * ROW) + u);
         if (u == 0) {
@@ -220,6 +267,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const Evict
             if (c.int8) more[1][x] = c.k_scale[from], more[2][x] = c.v_scale[from];
         }
     }
+    if (bad) atomicOr(c.status, kStatusBadIndex);
 #pragma unroll
     for (int x = 0; x < kSteps; ++x) {
         if (!((on >> x) & 1)) continue;
@@ -245,7 +293,8 @@ cudaError_t launch_move(const EvictLaunch &L, cudaStream_t s) {
 cudaError_t launch_evict(EvictLaunch L, cudaStream_t s) {
     // Positions a CTA may meet: what the table can hold, in as few CTAs as hold it, or
     // more while each still has kRunLeast and every one an SM.  1, 2, 4 and 8 CTAs: 8
-    // heads of 16000 39, 34, 28, 34 us; 128 heads of 8192 (16 sequences, 8 bits) 74, 84.
+    // heads of 16000 39, 34, 28, 34 us (the latter two 25.0 and 25.4 with the loads side by
+    // side), 8 heads of 4000 2 and 4 CTAs 21.1, 22.8; 128 heads of 8192, 1 and 2, 74, 84.
     const long long most = (long long)L.c.max_pages << L.c.page_shift, heads = (long long)L.c.kv_heads * L.c.batch;
     const auto each = [&](int ctas) { return (most + ctas - 1) / ctas; };
     L.ctas = 1;

@@ -602,7 +602,7 @@ cbs_status cbs_shared_attention(const cbs_shared_plan_t *p, const cbs_cache *c, 
     const bool chunk = p->prefix.kernel == CBS_ATTN_CHUNK;
     const int sms = p->desc.num_sms > 0 ? p->desc.num_sms : kDefaultNumSMs;
     const long long taken = chunk ? std::min<long long>(sms, prefix_base * pre.split) : 0;
-    const int per_sm = p->own.kernel == CBS_ATTN_CHUNK ? 1 : p->desc.head_dim == 64 ? 5 : 3;
+    const int per_sm = p->own.kernel == CBS_ATTN_CHUNK ? 1 : attn_rows_ctas(p->desc.head_dim, p->desc.cache_prec == CBS_INT8, p->own.row_tile);
     if (p->own.grid_ctas <= (sms - taken) * per_sm) return launch_attn_own(own, p->own.row_tile, (cudaStream_t)stream);
     own.share_stats = reinterpret_cast<float2 *>(at + parts.own_stats);
     own.share = reinterpret_cast<float *>(at + parts.own_share);
