@@ -11,7 +11,7 @@
 // copies rows, sixteen bytes a thread: reading and writing them once bounds it.
 //
 // Measured, 16 sequences of up to 8192 positions, 4096 kept, 8 heads of 128: bf16 98 us;
-// 8 bits 58 us.  One of 65001, 4001 kept, 4 heads of 64: 19 us.
+// 8 bits 58 us.  One of 65001, 4001 kept, 4 heads of 64: 17 us.
 #include <type_traits>
 
 #include "tc_ptx.cuh"
@@ -58,18 +58,7 @@ __device__ __forceinline__ int inclusive(int s) {
     return s;
 }
 
-// Sums of a pair of counts over the threads before this one and over all; one barrier.
 struct Pair { int a, b; };
-__device__ __forceinline__ Pair scan(Pair v, Pair &total, Pair *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Pair s = {inclusive(v.a), inclusive(v.b)};
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    const Pair w = {inclusive(warps[lane].a), inclusive(warps[lane].b)};
-    total = Pair{__shfl_sync(~0u, w.a, 31), __shfl_sync(~0u, w.b, 31)};
-    const int from = warp ? warp - 1 : 0, a = __shfl_sync(~0u, w.a, from), b = __shfl_sync(~0u, w.b, from);
-    return Pair{s.a - v.a + (warp ? a : 0), s.b - v.b + (warp ? b : 0)};
-}
 
 __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunch L) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // this CTA's positions, at most L.run
@@ -93,8 +82,7 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     int *const kept = L.kept + ((size_t)b * c.kv_heads + head) * L.keep;
     if (rank == 0 && head == 0 && tid == 0) L.new_lens[b] = after;
 
-    // This CTA's positions [p0, p0 + m), and each thread's run of them.  (Runs of odd
-    // length: 32 lanes of a scan are in 32 banks.)
+    // This CTA's positions [p0, p0 + m).
     const int share = (others + ctas - 1) / ctas, p0 = min(others, rank * share), m = min(others - p0, share);
     const int shift = c.page_shift, slots = 1 << shift;
     for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
@@ -102,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     __syncthreads();
     // Pages first, then weights, eight of each on their way at once (two where that is
     // all): what is wrong is reported behind them.  (A page outside the pool: its
-    // positions go first.)  65001 positions of 4 heads 24.4 -> 18.9 us, with the groups below.
+    // positions go first.)  65001 positions of 4 heads 24.4 -> 16.9 us, with the groups below.
     bool bad = false;
     const auto load = [&](auto loads) {
         constexpr int kLoads = decltype(loads)::value;
@@ -156,22 +144,30 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
             if (lane == 0) s_groups[pass][warp] = sum;
             meet();
             // From the top, of all CTAs: the group of 64 bins, then the bin.  (All bins of
-            // all CTAs read by all threads took 4500 cycles.)
+            // all CTAs read by all threads took 4500 cycles.)  The loads have no branches
+            // between them: the CTAs' answers come together.
             if (warp == 0) {
-                int x = 0;
+                int x = s_groups[pass][31 - lane];
+                if (ctas > 1) {
+                    int o[kMostCtas];
 #pragma unroll
-                for (int r = 0; r < kMostCtas; ++r)
-                    if (r < ctas) x += ctas == 1 ? s_groups[pass][31 - lane] : ld_cluster_int(&s_groups[pass][31 - lane], r);
+                    for (int r = 0; r < kMostCtas; ++r) o[r] = ld_cluster_int(&s_groups[pass][31 - lane], min(r, ctas - 1));
+                    x = 0;
+#pragma unroll
+                    for (int r = 0; r < kMostCtas; ++r) x += r < ctas ? o[r] : 0;
+                }
                 const int before = inclusive(x) - x;
                 const unsigned hit = __ballot_sync(~0u, before < left && left <= before + x);
                 if (hit) {
                     const int at = __ffs(hit) - 1, rest = left - __shfl_sync(~0u, before, at), bin = (31 - at) * 64 + 62 - 2 * lane;
-                    int2 v = {0, 0};
+                    int2 v = *reinterpret_cast<const int2 *>(&hist[bin]);
+                    if (ctas > 1) {
+                        int2 o[kMostCtas];
 #pragma unroll
-                    for (int r = 0; r < kMostCtas; ++r) {
-                        if (r >= ctas) break;
-                        const int2 o = ctas == 1 ? *reinterpret_cast<const int2 *>(&hist[bin]) : ld_cluster_pair(&hist[bin], r);
-                        v.x += o.x, v.y += o.y;
+                        for (int r = 0; r < kMostCtas; ++r) o[r] = ld_cluster_pair(&hist[bin], min(r, ctas - 1));
+                        v = {0, 0};
+#pragma unroll
+                        for (int r = 0; r < kMostCtas; ++r) v.x += r < ctas ? o[r].x : 0, v.y += r < ctas ? o[r].y : 0;
                     }
                     const int above = inclusive(v.x + v.y) - (v.x + v.y);
                     if (above < rest && rest <= above + v.y) s_found[pass][0] = bin + 1, s_found[pass][1] = rest - above;
@@ -187,12 +183,21 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
     // Everything stays, or nothing but the recent ones, or those above `prefix` and
     // the first `left` that equal it.
     const bool all_stay = take >= others;
-    const int run = ((m + kThreads - 1) / kThreads) | 1, i0 = min(m, tid * run), i1 = min(m, i0 + run);
     const auto heavier = [&](uint32_t k) { return all_stay || (take > 0 && k > prefix); };
     const auto equal = [&](uint32_t k) { return !all_stay && take > 0 && k == prefix; };
-    Pair mine = {0, 0}, total;
-    for (int i = i0; i < i1; ++i) mine.a += heavier(s_keys[i]), mine.b += equal(s_keys[i]);
-    Pair before = scan(mine, total, s_warps);
+    // A warp takes a run of the positions, 32 at a time.
+    const int run = (m + kThreads - 1) / kThreads * 32, i0 = min(m, warp * run), i1 = min(m, i0 + run);
+    Pair mine = {0, 0};
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t k = i + lane < i1 ? s_keys[i + lane] : 0u;
+        mine.a += __popc(__ballot_sync(~0u, i + lane < i1 && heavier(k)));
+        mine.b += __popc(__ballot_sync(~0u, i + lane < i1 && equal(k)));
+    }
+    if (lane == 0) s_warps[warp] = mine;
+    __syncthreads();
+    const Pair upto = {inclusive(s_warps[lane].a), inclusive(s_warps[lane].b)};
+    const Pair total = {__shfl_sync(~0u, upto.a, 31), __shfl_sync(~0u, upto.b, 31)};
+    const Pair before = {__shfl_sync(~0u, upto.a, warp) - mine.a, __shfl_sync(~0u, upto.b, warp) - mine.b};
     int place = 0, ties = 0;   // before this CTA: stayed, equal
     if (ctas > 1) {
         if (tid == 0) s_counts[0] = total.a, s_counts[1] = total.b;
@@ -204,13 +209,20 @@ __global__ void __launch_bounds__(kThreads) evict_choose_kernel(const EvictLaunc
             ties += s_all[r].y;
         }
     }
-    int seen = ties + before.b;   // equal ones before this thread's
+    int seen = ties + before.b;   // equal ones before this warp's
     place += before.a + min(max(left - ties, 0), before.b);
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = s_keys[i];
-        const bool e = equal(k);
-        if ((heavier(k) || (e && seen < left)) && place < L.keep) kept[place++] = p0 + i;
-        seen += e;
+    const unsigned below = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += 32) {
+        const bool in = i + lane < i1;
+        const uint32_t k = in ? s_keys[i + lane] : 0u;
+        const bool e = in && equal(k);
+        const unsigned equals = __ballot_sync(~0u, e);
+        const bool stays = (in && heavier(k)) || (e && seen + __popc(equals & below) < left);
+        const unsigned staying = __ballot_sync(~0u, stays);
+        const int at = place + __popc(staying & below);
+        if (stays && at < L.keep) kept[at] = p0 + i + lane;
+        place += __popc(staying);
+        seen += __popc(equals);
     }
     for (int i = rank * kThreads + tid; i < L.keep - take; i += ctas * kThreads) kept[take + i] = i < recent ? others + i : -1;
     if (ctas > 1) cluster_sync();   // nobody's counts go while another CTA reads them
