@@ -17,7 +17,7 @@
 // which add their sums in order through distributed shared memory.
 //
 // Measured with the weights in turn (not in L2), 16384 x 8192: 32 rows 28 us, 4.8 TB/s;
-// 128 rows 37 us, 0.94 PFLOP/s.  1001 x 2064, 400 rows 9.7 us: starts and ends.
+// 64 rows 34 us; 128 rows 37 us, 0.94 PFLOP/s.  1001 x 2064, 400 rows 9.7 us: starts and ends.
 #include <algorithm>
 
 #include "w8.cuh"
@@ -36,7 +36,9 @@ template <int kN>
 struct W8Tile {
     static constexpr int kW = kOut * 128, kRaw = kW + kN * 128;
     static constexpr int kOp = kN * 256;                  // a stage of B: two panels of 64
-    static constexpr int kStages = kN == 64 ? 2 : 4;
+    // (64 rows with two stages let two CTAs on an SM, which waited for their loads: 64 rows
+    // of 16384 x 8192 38.7 us, with four 33.3; of 6144 x 4096 12.0 and 12.3.)
+    static constexpr int kStages = 4;
     static constexpr int kOps = kN <= 32 ? 2 : 3;
     // Warps that widen inputs, and the groups of them that take stages in turn: a
     // group then has two stages' time for its loads, stores and fence.
@@ -370,11 +372,11 @@ __global__ void quantize_w8_kernel(const float *__restrict__ w, int n, int k, in
 // The tile and the shares of k, by what was measured (hundredths of a microsecond; 60
 // sizes of 256 x 1024 to 16384 x 8192, 1 to 6400 rows, every tile with 1 to 8 shares):
 // a CTA's start and end and each of its stages, alone on its SM and, for the tiles of
-// which two fit, for two side by side; and the join of shares.  What it takes is 0.8%
+// which two fit, for two side by side; and the join of shares.  What it takes is 1%
 // slower than the best on average and 19% at worst (1024 x 256, 6400 rows: 14.9 us for
 // 12.6).
 struct W8Cost { int rows, alone, stage, two, stage2, share; };
-constexpr W8Cost kCosts[] = {{16, 88, 45, 72, 68, 0}, {32, 128, 36, 128, 65, 0}, {64, 130, 51, 173, 84, 0},
+constexpr W8Cost kCosts[] = {{16, 88, 45, 72, 68, 0}, {32, 128, 36, 128, 65, 0}, {64, 155, 46, 0, 0, 5},
                              {128, 227, 49, 0, 0, 22}, {256, 142, 55, 0, 0, 0}};
 constexpr int kJoin = 146;
 constexpr int kPairTile = 373;   // of a tile of 256, beside its stages: where the next one's begin late
