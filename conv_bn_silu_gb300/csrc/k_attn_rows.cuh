@@ -7,8 +7,8 @@
 // A key/value head's G query heads and the chunk's tokens make the rows of one
 // product (row = t G + g), so K and V are read once for all of them.  HBM (or
 // L2) bandwidth bounds it: each CTA takes 8 or 16 rows and a range of keys, its
-// warps blocks of 16 keys in turn, in bf16 straight from global memory to registers,
-// in 8 bits through a ring of three blocks a warp in shared memory.
+// warps blocks of 16 keys in turn, rows of 256 bytes straight from global memory to
+// registers, shorter ones through a ring of three blocks a warp in shared memory.
 // The products are S^T = K Q^T and O^T = V^T P^T: keys, then head dimensions,
 // fill the 16 rows of the MMA and the few query rows its 8 columns, so no lane
 // of a single-token call's MMA is spent on rows that do not exist twice over.
@@ -21,8 +21,8 @@
 // and 155 us in 8 bits, 5.4 TB/s.  (With 8 bits in registers too, 205 us: twelve warps an
 // SM waited for a block of 16 keys each, half the bytes in flight of bf16.  The ring
 // has two blocks on their way beside the one at hand, and sixteen warps.  16 sequences
-// of 4000, 32 rows: 98 -> 73; head dimension 64, 64 of 8000: 126 -> 97; one of 1000: 6.2 ->
-// 5.9.)
+// of 4000, 32 rows: 98 -> 73; head dimension 64, 64 of 8000: 126 -> 97, in bf16 128 -> 122,
+// 64 of 1000 24.0 -> 19.5; one of 1000: 6.2 -> 5.9.)
 //
 // Up to eight ranges of keys are the CTAs of a cluster, which join them from each
 // other's shared memory; more are joined through the workspace by the CTA that
@@ -100,16 +100,19 @@ struct KvFrag {
     }
 };
 
-// 8 bits: a warp's ring of blocks in shared memory, filled by its lanes' asynchronous
-// copies.  A block's 16 rows of K, of V, then the scales of both; 16-byte units are
-// permuted within 128 bytes, so that V's reads of eight lanes meet all banks.
-template <int D>
+// Rows of 64 or 128 bytes: a warp's ring of blocks in shared memory, filled by its
+// lanes' asynchronous copies.  A block's 16 rows of K, of V, then the scales of both;
+// 16-byte units are permuted within 128 bytes, so that V's reads of eight lanes meet
+// all banks.
+template <int D, bool I8>
 struct KvRing {
-    static constexpr int kStages = 3, kRows = kBlock * D, kStage = 2 * kRows + 128, kWarp = kStages * kStage;
+    static constexpr bool kOn = I8 || D == 64;
+    static constexpr int kRow = D * (I8 ? 1 : 2), kStages = 3, kRows = kBlock * kRow, kStage = 2 * kRows + (I8 ? 128 : 0), kWarp = kStages * kStage;
+    using F = KvFrag<D, I8>;
     int put[2], k_at, v_at[2];   // of a lane
     __device__ __forceinline__ explicit KvRing(int lane) {
         const int g = lane >> 2, j = lane & 3;
-        if constexpr (D == 128) {
+        if constexpr (kRow == 128) {
             put[0] = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) * 16);
             put[1] = put[0] ^ 64;
             k_at = g * 128 + ((j ^ g) * 16);
@@ -122,31 +125,35 @@ struct KvRing {
             v_at[1] = v_at[0] + 64;
         }
     }
-    // A block whose first row is row0, all of it (a block lies within a page).
-    __device__ __forceinline__ void copy(const CacheArgs &c, size_t row0, uint32_t to, int lane) const {
-        const char *k = static_cast<const char *>(c.k) + row0 * D + lane * 16, *v = static_cast<const char *>(c.v) + row0 * D + lane * 16;
+    // A block whose first row is row0 (a block lies within a page): in 8 bits all of it,
+    // whose codes are numbers whatever they are; in bf16 what is not live is zeros.
+    __device__ __forceinline__ void copy(const CacheArgs &c, size_t row0, unsigned live, uint32_t to, int lane) const {
+        const char *k = static_cast<const char *>(c.k) + row0 * kRow + lane * 16, *v = static_cast<const char *>(c.v) + row0 * kRow + lane * 16;
 #pragma unroll
         for (int i = 0; i < kRows / 512; ++i) {
-            ptx::cp_async_16(to + i * 512 + put[i & 1], k + i * 512, 16);
-            ptx::cp_async_16(to + kRows + i * 512 + put[i & 1], v + i * 512, 16);
+            const uint32_t bytes = I8 || (live >> (i * (512 / kRow) + lane / (kRow / 16)) & 1) ? 16 : 0;
+            ptx::cp_async_16(to + i * 512 + put[i & 1], k + i * 512, bytes);
+            ptx::cp_async_16(to + kRows + i * 512 + put[i & 1], v + i * 512, bytes);
         }
-        const float *sc = (lane < 16 ? c.k_scale : c.v_scale) + row0 + (lane & 15);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 2 * kRows + lane * 4), "l"(sc) : "memory");
+        if constexpr (I8) {
+            const float *sc = (lane < 16 ? c.k_scale : c.v_scale) + row0 + (lane & 15);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 2 * kRows + lane * 4), "l"(sc) : "memory");
+        }
     }
-    __device__ __forceinline__ void read_k(KvFrag<D, true> &f, const unsigned char *at, int lane) const {
+    __device__ __forceinline__ void read_k(F &f, const unsigned char *at, int lane) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int q = 0; q < KvFrag<D, true>::kKC; ++q)
-                f.k[i][q] = *reinterpret_cast<const uint4 *>(at + i * 8 * D + (k_at ^ (q * 64)));
-            f.ks[i] = *reinterpret_cast<const float *>(at + 2 * kRows + ((lane >> 2) + 8 * i) * 4);
+            for (int q = 0; q < F::kKC; ++q)
+                f.k[i][q] = *reinterpret_cast<const uint4 *>(at + i * 8 * kRow + (k_at ^ (q * 64)));
+            if constexpr (I8) f.ks[i] = *reinterpret_cast<const float *>(at + 2 * kRows + ((lane >> 2) + 8 * i) * 4);
         }
     }
-    __device__ __forceinline__ void read_v(KvFrag<D, true> &f, const unsigned char *at, int lane) const {
+    __device__ __forceinline__ void read_v(F &f, const unsigned char *at, int lane) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned char *p = at + kRows + (i >> 1) * 8 * D + v_at[i & 1];
-            if constexpr (D == 64) {
+            const unsigned char *p = at + kRows + (i >> 1) * 8 * kRow + v_at[i & 1];
+            if constexpr (kRow == 64) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(p);
                 f.v[i][0] = w.x; f.v[i][1] = w.y;
             } else {
@@ -155,7 +162,7 @@ struct KvRing {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) f.vs[i] = *reinterpret_cast<const float *>(at + 2 * kRows + 64 + ((lane >> 2) + 8 * i) * 4);
+        for (int i = 0; i < (I8 ? 2 : 0); ++i) f.vs[i] = *reinterpret_cast<const float *>(at + 2 * kRows + 64 + ((lane >> 2) + 8 * i) * 4);
     }
 };
 
@@ -164,13 +171,13 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
     constexpr int kRows = 8 * NR;
     constexpr int kMT = D / 16;              // 16-dimension tiles of O^T
     using F = KvFrag<D, I8>;
-    // The warps' shares at the end; in 8 bits each where the warp's ring was.
-    using Ring = KvRing<D>;
-    constexpr int kPitch = D + 4, kShare = I8 ? Ring::kWarp / 4 : kRows * kPitch;
+    // The warps' shares at the end, each where the warp's ring was if there is one.
+    using Ring = KvRing<D, I8>;
+    constexpr int kPitch = D + 4, kShare = Ring::kOn ? Ring::kWarp / 4 : kRows * kPitch;
     static_assert(kShare >= kRows * kPitch, "a share fits where the ring was");
-    __shared__ __align__(16) float s_bf16[I8 ? 4 : kWarps * kShare];
+    __shared__ __align__(16) float s_wide[Ring::kOn ? 4 : kWarps * kShare];
     extern __shared__ __align__(128) unsigned char s_ring[];
-    float *const s_o = I8 ? reinterpret_cast<float *>(s_ring) : s_bf16;
+    float *const s_o = Ring::kOn ? reinterpret_cast<float *>(s_ring) : s_wide;
     const auto share = [&](int w, int r, int dim) { return s_o + w * kShare + r * kPitch + dim; };
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     __shared__ float2 s_stat[kRows];   // a range's (maximum, sum), for the other CTAs of a cluster
@@ -300,18 +307,18 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
     int blk = b0 + warp;
     unsigned live, live_next;   // of the block at hand, of the next one to load
     size_t row, row_next;
-    // 8 bits: blocks on their way, the next one's first.
+    // With a ring: blocks on their way, the next one's first.
     constexpr int kAhead = Ring::kStages - 1;
     const Ring ring(lane);
     const unsigned char *const ring_at = s_ring + warp * Ring::kWarp;
     const uint32_t ring_to = ptx::smem_u32(ring_at);
     unsigned coming[kAhead];
     int stage = 0;   // bytes
-    if constexpr (I8) {
+    if constexpr (Ring::kOn) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             row = place_of(blk + i * kWarps, coming[i]);
-            if (coming[i]) ring.copy(c, row, ring_to + i * Ring::kStage, lane);
+            if (I8 ? coming[i] != 0 : blk + i * kWarps < b1) ring.copy(c, row, coming[i], ring_to + i * Ring::kStage, lane);
             ptx::cp_async_commit();
         }
         row_next = place_of(blk + kAhead * kWarps, live_next);
@@ -324,11 +331,12 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
     bool poison = false;
     while (blk < b1) {
         const int pos = lo16 + blk * kBlock;
-        if constexpr (I8) {
+        if constexpr (Ring::kOn) {
             // This block has arrived, and every lane is done with the one before.
             ptx::cp_async_wait<kAhead - 1>();
             __syncwarp();
-            if (live_next) ring.copy(c, row_next, ring_to + (stage ? stage - Ring::kStage : kAhead * Ring::kStage), lane);
+            if (I8 ? live_next != 0 : blk + kAhead * kWarps < b1)
+                ring.copy(c, row_next, live_next, ring_to + (stage ? stage - Ring::kStage : kAhead * Ring::kStage), lane);
             ptx::cp_async_commit();
             live = coming[0];
 #pragma unroll
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
         const float ks0 = I8 ? f.ks[0] * L.scale_log2 : L.scale_log2, ks1 = I8 ? f.ks[1] * L.scale_log2 : L.scale_log2;
         // The next block's keys, while this one's scores become probabilities.
         const int next = blk + kWarps;
-        if constexpr (!I8) {
+        if constexpr (!Ring::kOn) {
             row = row_next;
             live = live_next;
             f.load_k(c, row, lane, live);
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
                     if (r < R && key < L.len_pad) scores[n][i & 1][key] = s[n][i];
                 }
         }
-        if constexpr (I8) ring.read_v(f, ring_at + stage, lane);
+        if constexpr (Ring::kOn) ring.read_v(f, ring_at + stage, lane);
         // ---- running maximum
         float top[NR][2];
         bool grow = false;
@@ -499,12 +507,12 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
                 for (int n = 0; n < NR; ++n) frag::mma(o[n][w], a0, a1, a2, a3, p0[n], p1[n]);
             }
         }
-        if constexpr (I8) stage = stage == kAhead * Ring::kStage ? 0 : stage + Ring::kStage;
+        if constexpr (Ring::kOn) stage = stage == kAhead * Ring::kStage ? 0 : stage + Ring::kStage;
         else f.load_v(c, row, lane, live);
         blk = next;
     }
     if (poison) s_flag = 1;
-    if constexpr (I8) __syncwarp();   // the ring's place becomes the share's
+    if constexpr (Ring::kOn) __syncwarp();   // the ring's place becomes the share's
 
     // ---- the warps' shares, joined in shared memory
 #pragma unroll
@@ -684,15 +692,18 @@ cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.cluster ? 2 : 1;
-    if constexpr (I8) {
-        cfg.dynamicSmemBytes = kWarps * KvRing<D>::kWarp;
-        static ContextOfDevice set1, set2;
-        cudaError_t e = row_tile == 16 ? set_max_dyn_smem_once(attn_rows_kernel<D, I8, 2, MODE>, (int)cfg.dynamicSmemBytes, set2)
-                                       : set_max_dyn_smem_once(attn_rows_kernel<D, I8, 1, MODE>, (int)cfg.dynamicSmemBytes, set1);
-        if (e != cudaSuccess) return e;
-        if (row_tile == 16) return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 2, MODE>, L);
-    }
-    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, I8, 1, MODE>, L);
+    const auto launch = [&](auto kern, ContextOfDevice &set) {
+        if constexpr (KvRing<D, I8>::kOn) {
+            cfg.dynamicSmemBytes = kWarps * KvRing<D, I8>::kWarp;
+            const cudaError_t e = set_max_dyn_smem_once(kern, (int)cfg.dynamicSmemBytes, set);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaLaunchKernelEx(&cfg, kern, L);
+    };
+    static ContextOfDevice set1, set2;
+    if constexpr (I8)
+        if (row_tile == 16) return launch(attn_rows_kernel<D, I8, 2, MODE>, set2);
+    return launch(attn_rows_kernel<D, I8, 1, MODE>, set1);
 }
 
 template <int MODE>
