@@ -7,8 +7,8 @@
 // A key/value head's G query heads and the chunk's tokens make the rows of one
 // product (row = t G + g), so K and V are read once for all of them.  HBM (or
 // L2) bandwidth bounds it: each CTA takes 8 or 16 rows and a range of keys, its
-// warps blocks of 16 keys in turn, rows of 256 bytes straight from global memory to
-// registers, shorter ones through a ring of three blocks a warp in shared memory.
+// warps blocks of 16 keys in turn, through a ring of three blocks a warp in shared
+// memory.
 // The products are S^T = K Q^T and O^T = V^T P^T: keys, then head dimensions,
 // fill the 16 rows of the MMA and the few query rows its 8 columns, so no lane
 // of a single-token call's MMA is spent on rows that do not exist twice over.
@@ -16,13 +16,11 @@
 // consecutive elements, and 8-bit codes are widened exactly in registers, keys to
 // f16 and values to bf16 (their scales multiply the scores and the probabilities).
 //
-// One token of 32 heads, 8 key heads of 128: 1000 keys 5.6 us (latency: 8 ranges in
-// clusters; 6.8 us through the workspace); 64 sequences of up to 8192 keys 250 us in bf16, 6.5 TB/s,
-// and 155 us in 8 bits, 5.4 TB/s.  (With 8 bits in registers too, 205 us: twelve warps an
-// SM waited for a block of 16 keys each, half the bytes in flight of bf16.  The ring
-// has two blocks on their way beside the one at hand, and sixteen warps.  16 sequences
-// of 4000, 32 rows: 98 -> 73; head dimension 64, 64 of 8000: 126 -> 97, in bf16 128 -> 122,
-// 64 of 1000 24.0 -> 19.5; one of 1000: 6.2 -> 5.9.)
+// One token of 32 heads, 8 key heads of 128: 1000 keys 5.3 us on the GPU (latency: 8
+// ranges in clusters); 64 sequences of 4000 to 8000 keys 226 us in bf16, of up to 8192 155
+// us in 8 bits, 5.4 TB/s.  With the next block in registers in place of the ring: 239 and
+// 205; 64 of 1000 45 us in bf16, now 34, in 8 bits 40 and 29; one of 4000 in bf16 9.7
+// and 7.7; heads of 64 in bf16, 64 of 1000, 24.0 and 19.5.
 //
 // Up to eight ranges of keys are the CTAs of a cluster, which join them from each
 // other's shared memory; more are joined through the workspace by the CTA that
@@ -61,65 +59,33 @@ struct KvFrag {
     uint4 k[2][kKC];
     uint32_t v[4][kVW];
     float ks[2], vs[2];
-
-    __device__ __forceinline__ void load_k(const CacheArgs &c, size_t row0, int lane, unsigned live) {
-        const int g = lane >> 2, j = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool on = (live >> (g + 8 * i)) & 1;
-            const char *p = static_cast<const char *>(c.k) + (row0 + g + 8 * i) * (size_t)(D * (I8 ? 1 : 2)) + j * 16;
-#pragma unroll
-            for (int q = 0; q < kKC; ++q)
-                k[i][q] = on ? __ldg(reinterpret_cast<const uint4 *>(p + q * 64)) : make_uint4(0, 0, 0, 0);
-            if (I8) ks[i] = on ? __ldg(c.k_scale + row0 + g + 8 * i) : 0.0f;
-        }
-    }
-    __device__ __forceinline__ void load_v(const CacheArgs &c, size_t row0, int lane, unsigned live) {
-        const int g = lane >> 2, j = lane & 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = 2 * j + (i & 1) + 8 * (i >> 1);
-            const bool on = (live >> key) & 1;
-            const char *p = static_cast<const char *>(c.v) + (row0 + key) * (size_t)(D * (I8 ? 1 : 2));
-            if constexpr (I8 && D == 64) {
-                const uint2 w = on ? __ldg(reinterpret_cast<const uint2 *>(p + g * 8)) : make_uint2(0, 0);
-                v[i][0] = w.x; v[i][1] = w.y;
-            } else {
-#pragma unroll
-                for (int q = 0; q < kVW / 4; ++q) {
-                    const uint4 w = on ? __ldg(reinterpret_cast<const uint4 *>(p + g * 16 + q * 128)) : make_uint4(0, 0, 0, 0);
-                    v[i][4 * q] = w.x; v[i][4 * q + 1] = w.y; v[i][4 * q + 2] = w.z; v[i][4 * q + 3] = w.w;
-                }
-            }
-        }
-        if (I8) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                vs[i] = (live >> (g + 8 * i)) & 1 ? __ldg(c.v_scale + row0 + g + 8 * i) : 0.0f;
-        }
-    }
 };
 
-// Rows of 64 or 128 bytes: a warp's ring of blocks in shared memory, filled by its
-// lanes' asynchronous copies.  A block's 16 rows of K, of V, then the scales of both;
-// 16-byte units are permuted within 128 bytes, so that V's reads of eight lanes meet
-// all banks.
+// A warp's ring of blocks in shared memory, filled by its lanes' asynchronous copies.  A
+// block's 16 rows of K, of V, then the scales of both; rows of 256 bytes as two panels
+// of 128; 16-byte units are permuted within 128 bytes, so that V's reads of eight lanes
+// meet all banks.
 template <int D, bool I8>
 struct KvRing {
-    static constexpr bool kOn = I8 || D == 64;
     static constexpr int kRow = D * (I8 ? 1 : 2), kStages = 3, kRows = kBlock * kRow, kStage = 2 * kRows + (I8 ? 128 : 0), kWarp = kStages * kStage;
+    static constexpr int kPart = kRow == 256 ? 128 : kRow, kPanel = kBlock * 128;   // of a row; of a block
     using F = KvFrag<D, I8>;
-    int put[2], k_at, v_at[2];   // of a lane
+    int put[4], k_at, v_at[2];   // of a lane
     __device__ __forceinline__ explicit KvRing(int lane) {
         const int g = lane >> 2, j = lane & 3;
-        if constexpr (kRow == 128) {
-            put[0] = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) * 16);
-            put[1] = put[0] ^ 64;
+        if constexpr (kRow == 256) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) put[i] = ((lane >> 3) & 1) * kPanel + (lane >> 4) * 128 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) * 16);
+        } else if constexpr (kRow == 128) {
+            put[0] = put[2] = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) * 16);
+            put[1] = put[3] = put[0] ^ 64;
+        }
+        if constexpr (kRow >= 128) {
             k_at = g * 128 + ((j ^ g) * 16);
             v_at[0] = 2 * j * 128 + ((g ^ (2 * j)) * 16);
             v_at[1] = (2 * j + 1) * 128 + ((g ^ (2 * j + 1)) * 16);
         } else {
-            put[0] = put[1] = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) * 16);
+            put[0] = put[1] = put[2] = put[3] = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) * 16);
             k_at = g * 64 + ((j ^ (g >> 1)) * 16);
             v_at[0] = 2 * j * 64 + (((g >> 1) ^ j) * 16) + (g & 1) * 8;
             v_at[1] = v_at[0] + 64;
@@ -132,8 +98,8 @@ struct KvRing {
 #pragma unroll
         for (int i = 0; i < kRows / 512; ++i) {
             const uint32_t bytes = I8 || (live >> (i * (512 / kRow) + lane / (kRow / 16)) & 1) ? 16 : 0;
-            ptx::cp_async_16(to + i * 512 + put[i & 1], k + i * 512, bytes);
-            ptx::cp_async_16(to + kRows + i * 512 + put[i & 1], v + i * 512, bytes);
+            ptx::cp_async_16(to + i * (512 * kPart / kRow) + put[i & 3], k + i * 512, bytes);
+            ptx::cp_async_16(to + kRows + i * (512 * kPart / kRow) + put[i & 3], v + i * 512, bytes);
         }
         if constexpr (I8) {
             const float *sc = (lane < 16 ? c.k_scale : c.v_scale) + row0 + (lane & 15);
@@ -145,20 +111,23 @@ struct KvRing {
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int q = 0; q < F::kKC; ++q)
-                f.k[i][q] = *reinterpret_cast<const uint4 *>(at + i * 8 * kRow + (k_at ^ (q * 64)));
+                f.k[i][q] = *reinterpret_cast<const uint4 *>(at + i * 8 * kPart + (q >> 1) * kPanel + (k_at ^ ((q & 1) * 64)));
             if constexpr (I8) f.ks[i] = *reinterpret_cast<const float *>(at + 2 * kRows + ((lane >> 2) + 8 * i) * 4);
         }
     }
     __device__ __forceinline__ void read_v(F &f, const unsigned char *at, int lane) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned char *p = at + kRows + (i >> 1) * 8 * kRow + v_at[i & 1];
+            const unsigned char *p = at + kRows + (i >> 1) * 8 * kPart + v_at[i & 1];
             if constexpr (kRow == 64) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(p);
                 f.v[i][0] = w.x; f.v[i][1] = w.y;
             } else {
-                const uint4 w = *reinterpret_cast<const uint4 *>(p);
-                f.v[i][0] = w.x; f.v[i][1] = w.y; f.v[i][2] = w.z; f.v[i][3] = w.w;
+#pragma unroll
+                for (int q = 0; q < F::kVW / 4; ++q) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(p + q * kPanel);
+                    f.v[i][4 * q] = w.x; f.v[i][4 * q + 1] = w.y; f.v[i][4 * q + 2] = w.z; f.v[i][4 * q + 3] = w.w;
+                }
             }
         }
 #pragma unroll
@@ -171,13 +140,12 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
     constexpr int kRows = 8 * NR;
     constexpr int kMT = D / 16;              // 16-dimension tiles of O^T
     using F = KvFrag<D, I8>;
-    // The warps' shares at the end, each where the warp's ring was if there is one.
+    // The warps' shares at the end, each where the warp's ring was.
     using Ring = KvRing<D, I8>;
-    constexpr int kPitch = D + 4, kShare = Ring::kOn ? Ring::kWarp / 4 : kRows * kPitch;
+    constexpr int kPitch = D + 4, kShare = Ring::kWarp / 4;
     static_assert(kShare >= kRows * kPitch, "a share fits where the ring was");
-    __shared__ __align__(16) float s_wide[Ring::kOn ? 4 : kWarps * kShare];
     extern __shared__ __align__(128) unsigned char s_ring[];
-    float *const s_o = Ring::kOn ? reinterpret_cast<float *>(s_ring) : s_wide;
+    float *const s_o = reinterpret_cast<float *>(s_ring);
     const auto share = [&](int w, int r, int dim) { return s_o + w * kShare + r * kPitch + dim; };
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     __shared__ float2 s_stat[kRows];   // a range's (maximum, sum), for the other CTAs of a cluster
@@ -282,18 +250,6 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
         return (((size_t)p * c.kv_heads + head) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
     };
 
-    // The block after the next one to the L2 cache, a lane a key's row of K or V: a
-    // block of a warp's own is all that its registers hold ahead (64 sequences of up
-    // to 8192 keys: 281 -> 250 us in bf16, 237 -> 226 in 8 bits, when keys were still
-    // widened to bf16).
-    const char *const ahead = static_cast<const char *>(lane < kBlock ? c.k : c.v) + (size_t)(lane & (kBlock - 1)) * (D * (I8 ? 1 : 2));
-    const auto prefetch = [&](size_t row0, unsigned on) {
-        if (!((on >> (lane & (kBlock - 1))) & 1)) return;
-        const char *p = ahead + row0 * (D * (I8 ? 1 : 2));
-#pragma unroll
-        for (int i = 0; i < D * (I8 ? 1 : 2); i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-    };
-
     float *scores[kExact ? NR : 1][2];   // of this lane's rows
     if constexpr (kExact) {
 #pragma unroll
@@ -305,46 +261,35 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
 
     F f;
     int blk = b0 + warp;
-    unsigned live, live_next;   // of the block at hand, of the next one to load
-    size_t row, row_next;
-    // With a ring: blocks on their way, the next one's first.
+    unsigned live_next;   // of the next block to load; `coming`: of those on their way, the first one's first
     constexpr int kAhead = Ring::kStages - 1;
     const Ring ring(lane);
     const unsigned char *const ring_at = s_ring + warp * Ring::kWarp;
     const uint32_t ring_to = ptx::smem_u32(ring_at);
     unsigned coming[kAhead];
     int stage = 0;   // bytes
-    if constexpr (Ring::kOn) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            row = place_of(blk + i * kWarps, coming[i]);
-            if (I8 ? coming[i] != 0 : blk + i * kWarps < b1) ring.copy(c, row, coming[i], ring_to + i * Ring::kStage, lane);
-            ptx::cp_async_commit();
-        }
-        row_next = place_of(blk + kAhead * kWarps, live_next);
-    } else {
-        row = place_of(blk, live);
-        row_next = place_of(blk + kWarps, live_next);
-        f.load_k(c, row, lane, live);
-        f.load_v(c, row, lane, live);
+    for (int i = 0; i < kAhead; ++i) {
+        const size_t row = place_of(blk + i * kWarps, coming[i]);
+        if (I8 ? coming[i] != 0 : blk + i * kWarps < b1) ring.copy(c, row, coming[i], ring_to + i * Ring::kStage, lane);
+        ptx::cp_async_commit();
     }
+    size_t row_next = place_of(blk + kAhead * kWarps, live_next);
     bool poison = false;
     while (blk < b1) {
         const int pos = lo16 + blk * kBlock;
-        if constexpr (Ring::kOn) {
-            // This block has arrived, and every lane is done with the one before.
-            ptx::cp_async_wait<kAhead - 1>();
-            __syncwarp();
-            if (I8 ? live_next != 0 : blk + kAhead * kWarps < b1)
-                ring.copy(c, row_next, live_next, ring_to + (stage ? stage - Ring::kStage : kAhead * Ring::kStage), lane);
-            ptx::cp_async_commit();
-            live = coming[0];
+        // This block has arrived, and every lane is done with the one before.
+        ptx::cp_async_wait<kAhead - 1>();
+        __syncwarp();
+        if (I8 ? live_next != 0 : blk + kAhead * kWarps < b1)
+            ring.copy(c, row_next, live_next, ring_to + (stage ? stage - Ring::kStage : kAhead * Ring::kStage), lane);
+        ptx::cp_async_commit();
+        const unsigned now = coming[0];
 #pragma unroll
-            for (int i = 0; i + 1 < kAhead; ++i) coming[i] = coming[i + 1];
-            coming[kAhead - 1] = live_next;
-            row_next = place_of(blk + (kAhead + 1) * kWarps, live_next);
-            ring.read_k(f, ring_at + stage, lane);
-        }
+        for (int i = 0; i + 1 < kAhead; ++i) coming[i] = coming[i + 1];
+        coming[kAhead - 1] = live_next;
+        row_next = place_of(blk + (kAhead + 1) * kWarps, live_next);
+        ring.read_k(f, ring_at + stage, lane);
         // ---- S^T = K Q^T
         float s[NR][4];
 #pragma unroll
@@ -372,17 +317,7 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
                                   q[n][u * 4 + 2 * h + 1]);
             }
         }
-        const unsigned now = live;
         const float ks0 = I8 ? f.ks[0] * L.scale_log2 : L.scale_log2, ks1 = I8 ? f.ks[1] * L.scale_log2 : L.scale_log2;
-        // The next block's keys, while this one's scores become probabilities.
-        const int next = blk + kWarps;
-        if constexpr (!Ring::kOn) {
-            row = row_next;
-            live = live_next;
-            f.load_k(c, row, lane, live);
-            row_next = place_of(next + kWarps, live_next);
-            prefetch(row_next, live_next);
-        }
 
         // ---- scores, in base 2; keys a row does not see become -inf
         const bool partial = now != 0xffffu || pos < all_lo || pos + kBlock > all_hi;
@@ -416,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
                     if (r < R && key < L.len_pad) scores[n][i & 1][key] = s[n][i];
                 }
         }
-        if constexpr (Ring::kOn) ring.read_v(f, ring_at + stage, lane);
+        ring.read_v(f, ring_at + stage, lane);
         // ---- running maximum
         float top[NR][2];
         bool grow = false;
@@ -507,12 +442,11 @@ __global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_
                 for (int n = 0; n < NR; ++n) frag::mma(o[n][w], a0, a1, a2, a3, p0[n], p1[n]);
             }
         }
-        if constexpr (Ring::kOn) stage = stage == kAhead * Ring::kStage ? 0 : stage + Ring::kStage;
-        else f.load_v(c, row, lane, live);
-        blk = next;
+        stage = stage == kAhead * Ring::kStage ? 0 : stage + Ring::kStage;
+        blk += kWarps;
     }
     if (poison) s_flag = 1;
-    if constexpr (Ring::kOn) __syncwarp();   // the ring's place becomes the share's
+    __syncwarp();   // the ring's place becomes the share's
 
     // ---- the warps' shares, joined in shared memory
 #pragma unroll
@@ -692,13 +626,10 @@ cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.cluster ? 2 : 1;
+    cfg.dynamicSmemBytes = kWarps * KvRing<D, I8>::kWarp;
     const auto launch = [&](auto kern, ContextOfDevice &set) {
-        if constexpr (KvRing<D, I8>::kOn) {
-            cfg.dynamicSmemBytes = kWarps * KvRing<D, I8>::kWarp;
-            const cudaError_t e = set_max_dyn_smem_once(kern, (int)cfg.dynamicSmemBytes, set);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaLaunchKernelEx(&cfg, kern, L);
+        const cudaError_t e = set_max_dyn_smem_once(kern, (int)cfg.dynamicSmemBytes, set);
+        return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, L);
     };
     static ContextOfDevice set1, set2;
     if constexpr (I8)

@@ -152,13 +152,12 @@ cudaError_t set_max_dyn_smem_once(F *kern, int bytes, ContextOfDevice &done) {
     return e;
 }
 
-// The few-row kernels' CTAs an SM: what fits without spilled registers.  bf16: head
-// dimension 64 as many as rings fit; 128 at four in place of three, 8 x 8000 keys: 51 -> 69
-// us.  8 bits: 128 at four in place of three, 64 x
-// 1000 keys 30.5 -> 28.9, 16 x 4000 34.0 -> 35.0, and with tiles of 16 rows at three in place
-// of two 84 -> 73; 64 at six in place of five, 64 x 8000 keys: 97 -> 104.
+// The few-row kernels' CTAs an SM: as many as rings and registers fit.  (8 bits, heads of
+// 128 at four in place of three, 64 x 1000 keys 30.5 -> 28.9 us, 16 x 4000 34.0 -> 35.0, and
+// with tiles of 16 rows at three in place of two 84 -> 73; 64 at six in place of five, 64
+// x 8000 keys: 97 -> 104.)
 constexpr int attn_rows_ctas(int d, bool int8, int row_tile) {
-    return d == 64 ? (int8 && row_tile == 8 ? 5 : 4) : int8 ? (row_tile == 16 ? 3 : 4) : row_tile == 16 ? 2 : 3;
+    return d == 64 ? (int8 && row_tile == 8 ? 5 : 4) : int8 ? (row_tile == 16 ? 3 : 4) : 2;
 }
 cudaError_t launch_attn_rows(const AttnLaunch &L, int row_tile, cudaStream_t s);
 // Tensor-core kernel: tiles of kAttnChunkRows rows.

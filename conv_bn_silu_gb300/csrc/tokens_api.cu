@@ -143,15 +143,16 @@ long long chunk_ns(const cbs_attn_desc &d, long long base, int x, int sms) {
 
 // Ranges of a shared prefix, whose CTAs run beside those of the sequences' own part and
 // keep their SMs from it: the least of the two parts' end.  The own part takes its bytes at
-// 4.4 TB/s (few rows; sequences three quarters of the longest on average) or its tiles'
+// 5.8 TB/s (few rows; sequences three quarters of the longest on average) or its tiles'
 // time; beside it a prefix's takes a fifth longer.  64 streams over a prefix of 8192
 // (bf16, own part of up to 1000 keys 45 us alone), 1, 2, 3, 4 and 8 ranges (8 to 64 CTAs,
-// alone 107, 62, 47, 37, 27 us): 121, 73, 57, 52, 57 us.
+// alone 107, 62, 47, 37, 27 us): 121, 73, 57, 52, 57 us; with the own part at 36 us alone
+// 51 with four and 47.6 with five.
 int prefix_split(const cbs_shared_plan_t &p, long long base, int sms) {
     const cbs_attn_desc &d = p.prefix.desc, &o = p.own.desc;
     const long long bytes = (long long)o.batch * o.max_len * 3 / 4 * d.kv_heads * d.head_dim * (d.cache_prec == CBS_INT8 ? 2 : 4);
     const long long own = p.own.kernel == CBS_ATTN_CHUNK ? chunk_ns(o, (long long)o.batch * o.kv_heads * p.own.row_tiles, p.own.split, sms)
-                                                         : bytes / 4400;
+                                                         : bytes / 5800;
     long long best = 0;
     int split = 1;
     for (int x = 1; x <= std::min(chunk_key_tiles(d.max_len), kAttnChunkSplitMost); ++x) {
@@ -335,7 +336,7 @@ long long attn_ns(const cbs_attn_plan_t &p, int sms) {
     const long long base = (long long)std::max(d.batch, 1) * d.kv_heads * p.row_tiles;
     if (p.kernel == CBS_ATTN_CHUNK) return chunk_ns(d, base, p.split, sms);
     const bool int8 = d.cache_prec == CBS_INT8;
-    const int thousand = int8 ? (d.head_dim == 64 ? 28 : 47) : d.head_dim == 64 ? 40 : 75;
+    const int thousand = int8 ? (d.head_dim == 64 ? 28 : 47) : d.head_dim == 64 ? 31 : 62;
     return 4500 + base * (d.max_len + (int8 ? 160 : 0)) / 1000 * thousand;
 }
 
