@@ -7,8 +7,8 @@
 // A key/value head's G query heads and the chunk's tokens make the rows of one
 // product (row = t G + g), so K and V are read once for all of them.  HBM (or
 // L2) bandwidth bounds it: each CTA takes 8 or 16 rows and a range of keys, its
-// warps blocks of 16 keys in turn, through a ring of three blocks a warp in shared
-// memory.
+// warps blocks of 16 keys in turn, through a ring of three blocks a warp (or two:
+// takes_second) in shared memory.
 // The products are S^T = K Q^T and O^T = V^T P^T: keys, then head dimensions,
 // fill the 16 rows of the MMA and the few query rows its 8 columns, so no lane
 // of a single-token call's MMA is spent on rows that do not exist twice over.
@@ -33,6 +33,8 @@
 // has the weights of a key without reading it again.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "mma_frag.cuh"
 #include "tc_ptx.cuh"
@@ -47,6 +49,29 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps, kBlock = 16;   // keys a warp 
 
 __device__ __forceinline__ bool not_finite_pair(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// CTAs an SM and blocks of a warp's ring.  The first form has three blocks and as many
+// CTAs as then fit (attn_rows_ctas); the second one, where there is one, these.
+constexpr int kRingStages = 3;
+struct Fit { int ctas, stages; };
+template <int D, bool I8, int NR>
+constexpr Fit kSecond = I8 ? (D == 64 ? Fit{0, 0} : Fit{NR == 1 ? 3 : 2, 3}) : D == 128 ? Fit{3, 2} : Fit{5, 2};
+
+// Which form a call takes (the results are the same).  bf16: one CTA more an SM, where that
+// saves a round of them.  One token of 32 heads, 8 key heads, first / second form in us: heads
+// of 128, 48 sequences (384 CTAs, two rounds and one) of 30 keys 5.9/3.8, of 500 18.3/15.4, 80
+// (640, three and two) 8.3/6.3 and 33.5/30.5, but 64 (512, two and two) of 500 25.4/28.4; heads
+// of 64, 80 of 30 and 500 (two and one) 5.2/3.7 and 14.1/10.9.  8 bits, heads of 128: one CTA
+// fewer with more registers, where both have one round of them and that many an SM: 48 of 500
+// 16.4/13.3, but 32 10.9/13.0 and 64 16.7/18.4; tiles of 16 rows, four tokens a sequence, 30
+// (240 CTAs) of 1000 28.8/21.1.
+template <int D, bool I8, int NR>
+bool takes_second(long long ctas) {
+    const long long sms = current_device_sms();
+    if (I8) return ctas <= kSecond<D, I8, NR>.ctas * sms && (NR == 2 || ctas > 2 * sms);
+    const auto rounds = [&](int per_sm) { return (ctas + per_sm * sms - 1) / (per_sm * sms); };
+    return rounds(kSecond<D, I8, NR>.ctas) < rounds(attn_rows_ctas(D, I8, 8));
 }
 
 template <int D, bool I8>
@@ -65,9 +90,9 @@ struct KvFrag {
 // block's 16 rows of K, of V, then the scales of both; rows of 256 bytes as two panels
 // of 128; 16-byte units are permuted within 128 bytes, so that V's reads of eight lanes
 // meet all banks.
-template <int D, bool I8>
+template <int D, bool I8, int STAGES>
 struct KvRing {
-    static constexpr int kRow = D * (I8 ? 1 : 2), kStages = 3, kRows = kBlock * kRow, kStage = 2 * kRows + (I8 ? 128 : 0), kWarp = kStages * kStage;
+    static constexpr int kRow = D * (I8 ? 1 : 2), kStages = STAGES, kRows = kBlock * kRow, kStage = 2 * kRows + (I8 ? 128 : 0), kWarp = kStages * kStage;
     static constexpr int kPart = kRow == 256 ? 128 : kRow, kPanel = kBlock * 128;   // of a row; of a block
     using F = KvFrag<D, I8>;
     int put[4], k_at, v_at[2];   // of a lane
@@ -135,13 +160,13 @@ struct KvRing {
     }
 };
 
-template <int D, bool I8, int NR, int MODE>
-__global__ void __launch_bounds__(kThreads, attn_rows_ctas(D, I8, 8 * NR)) attn_rows_kernel(const AttnLaunch L) {
+template <int D, bool I8, int NR, int MODE, bool SECOND>
+__global__ void __launch_bounds__(kThreads, SECOND ? kSecond<D, I8, NR>.ctas : attn_rows_ctas(D, I8, 8 * NR)) attn_rows_kernel(const AttnLaunch L) {
     constexpr int kRows = 8 * NR;
     constexpr int kMT = D / 16;              // 16-dimension tiles of O^T
     using F = KvFrag<D, I8>;
     // The warps' shares at the end, each where the warp's ring was.
-    using Ring = KvRing<D, I8>;
+    using Ring = KvRing<D, I8, SECOND ? kSecond<D, I8, NR>.stages : kRingStages>;
     constexpr int kPitch = D + 4, kShare = Ring::kWarp / 4;
     static_assert(kShare >= kRows * kPitch, "a share fits where the ring was");
     extern __shared__ __align__(128) unsigned char s_ring[];
@@ -626,15 +651,23 @@ cudaError_t launch_rows(const AttnLaunch &L, int row_tile, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.cluster ? 2 : 1;
-    cfg.dynamicSmemBytes = kWarps * KvRing<D, I8>::kWarp;
-    const auto launch = [&](auto kern, ContextOfDevice &set) {
-        const cudaError_t e = set_max_dyn_smem_once(kern, (int)cfg.dynamicSmemBytes, set);
+    const auto launch = [&](auto kern, int smem, ContextOfDevice &set) {
+        cfg.dynamicSmemBytes = smem;
+        const cudaError_t e = set_max_dyn_smem_once(kern, smem, set);
         return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, L);
     };
-    static ContextOfDevice set1, set2;
+    const auto either = [&](auto tiles) {
+        constexpr int NR = decltype(tiles)::value;
+        constexpr Fit second = kSecond<D, I8, NR>;
+        static ContextOfDevice set1, set2;
+        if constexpr (MODE == kAttnPlain && second.ctas > 0)
+            if (takes_second<D, I8, NR>((long long)cfg.gridDim.x * cfg.gridDim.y * cfg.gridDim.z))
+                return launch(attn_rows_kernel<D, I8, NR, MODE, true>, kWarps * KvRing<D, I8, second.stages>::kWarp, set2);
+        return launch(attn_rows_kernel<D, I8, NR, MODE, false>, kWarps * KvRing<D, I8, kRingStages>::kWarp, set1);
+    };
     if constexpr (I8)
-        if (row_tile == 16) return launch(attn_rows_kernel<D, I8, 2, MODE>, set2);
-    return launch(attn_rows_kernel<D, I8, 1, MODE>, set1);
+        if (row_tile == 16) return either(std::integral_constant<int, 2>{});
+    return either(std::integral_constant<int, 1>{});
 }
 
 template <int MODE>
