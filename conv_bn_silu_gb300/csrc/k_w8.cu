@@ -270,7 +270,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
                 for (int e = 0; e < kPart; ++e) sum[(col + e) * kPitch + row] = __uint_as_float(v[e]);
             } else if (n < L.n) {
-                store_rows(L, m0 + col, n, v, xs + col, ws, bias);
+                store_rows(L, m0 + col, n, v, xs + col, Channel(ws, bias));
             }
         }
     }
@@ -298,7 +298,7 @@ w8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (n + e >= L.n) break;
-            y[e] = y[e] * (x_scale * L.w_scale[n + e]) + (L.bias ? L.bias[n + e] : 0.0f);
+            y[e] = Channel(L.w_scale[n + e], L.bias ? L.bias[n + e] : 0.0f)(y[e], x_scale);
             if (L.act == CBS_ACT_SILU) y[e] = silu(y[e]);
         }
         if (L.n % 4 == 0) {

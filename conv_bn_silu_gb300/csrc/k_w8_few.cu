@@ -14,6 +14,7 @@
 #include "mma_frag.cuh"
 #include "tc_ptx.cuh"
 #include "tokens.cuh"
+#include "w8.cuh"
 
 namespace cbs {
 
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) w8_few_kernel(const W8Launch 
         if (m >= L.rows || n >= L.n) continue;
         float y = 0.0f;
         for (int w = o / 16 * wk; w < (o / 16 + 1) * wk; ++w) y += s_sum[w][r][o % 16];
-        y = y * (L.x_scale[m] * L.w_scale[n]) + (L.bias ? L.bias[n] : 0.0f);
+        y = w8::Channel(L.w_scale[n], L.bias ? L.bias[n] : 0.0f)(y, L.x_scale[m]);
         if (L.act == CBS_ACT_SILU) y = silu(y);
         const size_t at = (size_t)m * L.n + n;
         if (L.out_bf16) static_cast<__nv_bfloat16 *>(L.y)[at] = __float2bfloat16_rn(y);

@@ -225,7 +225,7 @@ w8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             const int n = tile.n0 + row;
             float *const xs = reinterpret_cast<float *>(smem + kScales) + (it & 1) * kTileRows;
             xs[t] = tile.m0 + t < L.rows ? L.x_scale[tile.m0 + t] : 0.0f;
-            const float ws = n < L.n ? L.w_scale[n] : 0.0f, bias = n < L.n && L.bias ? L.bias[n] : 0.0f;
+            const Channel channel(n < L.n ? L.w_scale[n] : 0.0f, n < L.n && L.bias ? L.bias[n] : 0.0f);
             const bool ok = wait(d_full, it & 1) && !lost();
             if (ptx::bar_red_or(1, kStoreWarps * 32, !ok)) break;   // (together, whatever ran out; and the scales are there)
             ptx::tc_fence_after();
@@ -242,7 +242,7 @@ w8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(d_free);
                 }
-                if (n < L.n) store_rows(L, tile.m0 + col, n, v, xs + col, ws, bias);
+                if (n < L.n) store_rows(L, tile.m0 + col, n, v, xs + col, channel);
             }
         }
     } else if (warp >= 8) {

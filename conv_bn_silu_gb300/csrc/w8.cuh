@@ -45,14 +45,27 @@ __device__ __forceinline__ void widen_weights(const unsigned char *from, int row
     }
 }
 
+// sum x_scale w_scale + bias, as (sum first) x_scale last + bias.  The scales' product may
+// leave the float range where the result does not, so the sum, a whole number, is multiplied
+// with one at a time: it only makes a scale larger, and one up to 1 leaves it in range; of a
+// larger w_scale first, x_scale's turn comes before, and what then leaves the range would
+// have.  (2048 rows of 8192 x 256 21.5 us with the scales' product, now 22.0; with the smaller
+// of both first, by comparisons for every sum, 23.8.)
+struct Channel {
+    float first, last, bias;
+    __device__ __forceinline__ Channel(float w_scale, float bias)
+        : first(fabsf(w_scale) <= 1.0f ? w_scale : 1.0f), last(fabsf(w_scale) <= 1.0f ? 1.0f : w_scale), bias(bias) {}   // (a NaN is last)
+    __device__ __forceinline__ float operator()(float sum, float x_scale) const { return fmaf(sum * first * x_scale, last, bias); }
+};
+
 // One output of input rows m, m + 1, ...: sums, as they come from tensor memory, to
 // y + (m * n + its number).  `scales`: those rows', `left`: how many there are.
 template <bool BF16, bool SILU, int COUNT>
-__device__ __forceinline__ void store_rows(void *y, size_t at, int pitch, const uint32_t (&sums)[COUNT], const float *scales, float scale,
-                                           float bias, int left) {
+__device__ __forceinline__ void store_rows(void *y, size_t at, int pitch, const uint32_t (&sums)[COUNT], const float *scales,
+                                           const Channel &channel, int left) {
 #pragma unroll
     for (int e = 0; e < COUNT; ++e) {
-        float v = __uint_as_float(sums[e]) * (scales[e] * scale) + bias;
+        float v = channel(__uint_as_float(sums[e]), scales[e]);
         if (SILU) v = silu(v);
         if (e < left) {
             if (BF16) static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
@@ -62,16 +75,16 @@ __device__ __forceinline__ void store_rows(void *y, size_t at, int pitch, const 
     }
 }
 template <int COUNT>
-__device__ __forceinline__ void store_rows(const W8Launch &L, int m, int n, const uint32_t (&sums)[COUNT], const float *scales, float scale,
-                                           float bias) {
+__device__ __forceinline__ void store_rows(const W8Launch &L, int m, int n, const uint32_t (&sums)[COUNT], const float *scales,
+                                           const Channel &channel) {
     const size_t at = (size_t)m * L.n + n;
     const int left = L.rows - m;
     if (L.act == CBS_ACT_SILU) {
-        if (L.out_bf16) store_rows<true, true>(L.y, at, L.n, sums, scales, scale, bias, left);
-        else store_rows<false, true>(L.y, at, L.n, sums, scales, scale, bias, left);
+        if (L.out_bf16) store_rows<true, true>(L.y, at, L.n, sums, scales, channel, left);
+        else store_rows<false, true>(L.y, at, L.n, sums, scales, channel, left);
     } else {
-        if (L.out_bf16) store_rows<true, false>(L.y, at, L.n, sums, scales, scale, bias, left);
-        else store_rows<false, false>(L.y, at, L.n, sums, scales, scale, bias, left);
+        if (L.out_bf16) store_rows<true, false>(L.y, at, L.n, sums, scales, channel, left);
+        else store_rows<false, false>(L.y, at, L.n, sums, scales, channel, left);
     }
 }
 
