@@ -5,7 +5,8 @@
 // Y^T = W X^T on tcgen05: 128 outputs of a CTA are the lanes of tensor memory, its
 // input rows the product's columns.  Codes are widened to f16, which holds them
 // exactly, and sums of products are kept in 32 bits: whole numbers, exact below
-// 2^24.  (The card's 8-bit integer tensor rate is far below its f16 one.)
+// 2^24, past which each of an MMA's additions (sixteen products) rounds or cuts after 23
+// bits.  (The card's 8-bit integer tensor rate is far below its f16 one.)
 //
 // TMA brings the codes, one byte each.  Two warpgroups in turn widen a stage's
 // weights and store them to tensor memory as the MMA's A operand; other warps widen

@@ -708,7 +708,9 @@ cbs_status cbs_quantize_w4(const float *w, int n, int k, int group, void *packed
 static cbs_status w8_shape(int n, int k) {
     if (n < 1 || k < 1) return fail(CBS_ERR_INVALID_ARG, "bad weight shape (%d x %d)", n, k);
     if (k % 16) return fail(CBS_ERR_UNSUPPORTED, "k = %d is not a multiple of 16", k);
-    if (n > 1 << 30 || k > 1 << 30) return fail(CBS_ERR_UNSUPPORTED, "weights of %d x %d: at most 2^30 a side", n, k);
+    if (n > 1 << 30) return fail(CBS_ERR_UNSUPPORTED, "%d outputs: at most 2^30", n);
+    // (Past this the additions' errors, k / 16 of 2^-23, are over 2^-11 of what is added up.)
+    if (k > 1 << 16) return fail(CBS_ERR_UNSUPPORTED, "k = %d: at most 65536", k);
     return CBS_OK;
 }
 

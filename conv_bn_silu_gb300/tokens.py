@@ -137,8 +137,8 @@ class LinearW4:
 
 
 class LinearW8:
-    """A layer of 8-bit weights [n, k], a float scale for each output: y = act(x_scale
-    w_scale (x W^T) + bias), for one row of codes as for thousands."""
+    """A layer of 8-bit weights [n, k] (k at most 65536), a float scale for each output:
+    y = act(x_scale w_scale (x W^T) + bias), for one row of codes as for thousands."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
                  activation: int = B.CBS_ACT_IDENTITY):

@@ -1,10 +1,11 @@
 """8-bit products at the edges of their contract: scales whose product leaves the
-float range."""
+float range, and the longest contraction."""
 import pytest
 import torch
 
 from conv_bn_silu_gb300 import _binding as B
-from tests.test_tokens_w8 import inputs
+from tests.test_tokens_refusals import U, refused
+from tests.test_tokens_w8 import inputs, run_case
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -45,3 +46,23 @@ def test_rows_of_zeros_have_no_size(rows, n, k):
     x[0] = 0
     got = tokens.LinearW8(w.cuda(), (ws * 0 + 1e30).cuda(), bias.cuda())(x.cuda(), (xs * 0 + 1e30).cuda(), dtype=torch.float32)
     assert torch.equal(got[0].cpu(), bias)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,n", [(1, 300), (12, 300), (20, 140), (100, 300), (300, 1000)])
+def test_longest(rows, n):
+    """Sums of one sign as far as they go: 65536 products of 2^14, each sixteen of
+    them an addition that is off by 2^-23 of the sum so far at most."""
+    k = 65536
+    full = lambda x, w: (torch.full_like(x, -128), torch.full_like(w, -128))
+    run_case(rows, n, k, codes=full, sums=(k / 16 + 16) * 2.0 ** -23)
+    run_case(rows, n, k, seed=1, sums=(k / 16 + 16) * 2.0 ** -23)
+
+
+def test_longer_is_refused(cuda_lib):
+    """Past k = 65536 the bound of the sums' error, k / 16 additions of 2^-23, is more
+    than 2^-11 of what they add up."""
+    K = 1 << 30
+    for k in (65536 + 16, 1 << 20, 1 << 30):
+        refused(U, B.cbs_linear_w8, K, 2 * K, 3 * K, 4 * K, None, 5 * K, B.CBS_BF16, 2, 8, k, B.CBS_ACT_IDENTITY, None)
+        refused(U, B.cbs_quantize_w8, K, 8, k, 2 * K, 3 * K, None)
