@@ -356,7 +356,7 @@ cbs_status attn_plan_by_time(const cbs_attn_desc *d, long long (*more)(const cbs
     // 128 in 8 bits 47 and 14 us, in bf16 21 and 15.
     const auto in_clusters = [&](cbs_attn_plan_t *p) {
         const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p->row_tiles;
-        if (p->kernel != CBS_ATTN_ROWS || p->split <= kAttnClusterMost || (long long)d->max_new * (d->heads / d->kv_heads) <= 8 ||
+        if (d->force_split || p->kernel != CBS_ATTN_ROWS || p->split <= kAttnClusterMost || (long long)d->max_new * (d->heads / d->kv_heads) <= 8 ||
             d->max_len > 8192 || base * kAttnClusterMost > 3ll * sms)
             return;
         p->kernel = CBS_ATTN_CLUSTER;
