@@ -105,6 +105,18 @@ __device__ __noinline__ float slow_score(const AttnLaunch &L, const Rows &s, int
     return __fmul_rn(dot, I8 ? L.c.k_scale[row] * L.scale_log2 : L.scale_log2);
 }
 
+// Whether a row of the keys' operand holds an infinity or a NaN.
+template <int D>
+__device__ __noinline__ bool odd_key(const unsigned char *keys, int row) {
+    const auto not_finite = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+    bool odd = false;
+    for (int u = 0; u < D / 8; ++u) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(keys + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+        odd |= not_finite(w.x) || not_finite(w.y) || not_finite(w.z) || not_finite(w.w);
+    }
+    return odd;
+}
+
 __device__ __forceinline__ bool far_row(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2) {
@@ -258,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __g
             *reinterpret_cast<uint4 *>(smem + (u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
         }
     }
-    // Rows that no box brings: zeros, whose exponentials then count for nothing.
+    // Rows that no box brings: zeros, whose exponentials then count for nothing (but with
+    // a key that is not finite: its summing warp leaves them out).
     const int boxed = rt.heads * rt.tokens, rest = (kRowTile - boxed) * 8;
     for (int i = tid; i < kBufs * (D / 64) * rest; i += kThreads)
         *reinterpret_cast<uint4 *>(smem + C::kQ + (i / rest) * (kKeys * 128) + boxed * 128 + i % rest * 16) = make_uint4(0, 0, 0, 0);
@@ -357,6 +370,10 @@ __global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __g
         const int p = key < end ? page_of(c, b, key) : -1;
         const size_t at = p < 0 ? 0 : (((size_t)p * c.kv_heads + head) << c.page_shift) + (key & ((1 << c.page_shift) - 1));
         const float scale = I8 ? (p < 0 ? 0.0f : c.k_scale[at] * L.scale_log2) : L.scale_log2;
+        // A box's tokens, where all of its rows may count (-1: rows that no box brings are left
+        // out, beside a key that is not finite).
+        int box_tokens = rt.tokens;
+        if (rest > 0 && __any_sync(~0u, I8 ? !(fabsf(scale) < INFINITY) : odd_key<D>(smem, key - key0))) box_tokens = -1;
         F2 sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
         float slow = 0.0f;
         for (int i = wg; i < tiles; i += kBufs) {
@@ -366,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __g
             ptx::tc_fence_after();
             const float *stat = reinterpret_cast<const float *>(smem + C::kStats + wg * C::kStat);
             // Every row of the box is the sequence's, and sees every key.
-            const bool whole = t.tokens == rt.tokens && seen_by(rs.base + t.token + t.tokens - 1, rs.len, L.causal, L.window).lo <= key0 &&
+            const bool whole = t.tokens == box_tokens && seen_by(rs.base + t.token + t.tokens - 1, rs.len, L.causal, L.window).lo <= key0 &&
                                seen_by(rs.base + t.token, rs.len, L.causal, L.window).hi >= end;
             const uint32_t taddr = tmem + (uint32_t)(wg * kRowTile) + lanes;
             if (whole) tile_sum<false>(taddr, stat, scale, key, sums);

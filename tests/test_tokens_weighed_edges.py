@@ -1,14 +1,86 @@
-"""Weighed attention at the edges of its contract: plans of a given split."""
+"""Weighed attention at the edges of its contract: keys that are not finite,
+plans of a given split."""
+import math
+
 import pytest
+import torch
 
 from conv_bn_silu_gb300 import _binding as B
+from tests import token_refs as refs
 from tests.test_tokens_refusals import desc
+from tests.test_tokens_weighed import received
+
+I32 = torch.int32
+KERNELS = [B.CBS_ATTN_ROWS, B.CBS_ATTN_CLUSTER, B.CBS_ATTN_CHUNK]
 
 
 @pytest.fixture(scope="module", autouse=True)
 def token_calls(cuda_lib):
     from conv_bn_silu_gb300 import build
     build.build_tokens()
+
+
+def weights(paged, q, lens, new, heads, scale, **plan):
+    """(out, what each sequence's positions received: [kv, length])."""
+    from conv_bn_silu_gb300 import tokens
+    page = paged["k"].shape[2]
+    starts = [sum(new[:i]) for i in range(len(new) + 1)]
+    dev = {n: None if t is None else t.cuda() for n, t in paged.items()}
+    cache = tokens.PagedCache(dev["k"], dev["v"], dev["k_scale"], dev["v_scale"])
+    mass = torch.zeros(paged["k"].shape[:3], device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=I32, device="cuda")
+    attn = tokens.WeighedAttention(cache, len(lens), max(new), max(lens), heads, scale=scale, **plan)
+    out = attn(q.cuda(), i32(starts), i32(lens), dev["table"], mass)
+    assert B.cbs_read_device_status(True, torch.cuda.current_stream().cuda_stream) == B.CBS_OK
+    mass, got = mass.cpu().double(), []
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        got.append(mass[paged["table"][b].long()[pos // page], :, pos % page].T)
+    return out, got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(3, 1), (5, 1), (7, 1), (8, 2), (130, 1)])
+def test_a_key_that_nobody_can_reach(heads, kv, d, kernel):
+    """A key of minus infinity where every query is positive: scores of minus infinity, and
+    no weight, for its position; the others as if it were not there."""
+    lens, new, at = [400], [130], 20   # (every new token sees the first 270 positions)
+    paged = refs.make_paged(lens, kv, d, 16, False, 3, junk=False)
+    page, slot = paged["table"][0, at // 16], at % 16
+    paged["k"][page, :, slot, 5] = -math.inf
+    q = torch.randn((130, heads, d), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    out, (got,) = weights(paged, q, lens, new, heads, None, force_kernel=kernel)
+    assert got.isfinite().all() and (got[:, at] == 0).all() and out.isfinite().all()
+    # what the others receive: the same with a key so far below that nothing reaches it
+    paged["k"][page, :, slot] = 0
+    paged["k"][page, :, slot, 5] = -3e4
+    rec, far = received(q, paged, [0, 130], lens, 16, True, 0, d ** -0.5)[0]
+    assert (rec[:, at] < 1e-30).all()
+    others = torch.arange(400) != at
+    # (that key's own error counts for nothing in the rows' sums, however large its products)
+    far = torch.minimum(far, rec * 2.0 ** -8 + 1e-6)
+    assert ((got - rec).abs() <= far + 2.0 ** -23 * rec + 1e-30)[:, others].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("heads,kv", [(3, 1), (8, 2)])
+def test_a_key_of_infinite_scale(heads, kv, kernel):
+    """The same in 8 bits: a key whose scale is infinite, far below every query."""
+    lens, new, at = [400], [130], 20
+    paged = refs.make_paged(lens, kv, 64, 16, True, 3, junk=False)
+    page, slot = paged["table"][0, at // 16], at % 16
+    paged["k_scale"][page, :, slot], paged["k"][page, :, slot] = math.inf, 0
+    paged["k"][page, :, slot, 5] = -100
+    q = torch.randn((130, heads, 64), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    out, (got,) = weights(paged, q, lens, new, heads, None, force_kernel=kernel)
+    assert got.isfinite().all() and (got[:, at] == 0).all() and out.isfinite().all()
+    # (what a row gives adds up to one, within n + R + 64 roundings of 2^-23 and the exponentials' 2^-20)
+    assert ((got.sum(1) / (130 * heads // kv) - 1).abs() <= (400 + 130 * heads + 64) * 2.0 ** -23 + 2.0 ** -20).all()
 
 
 def test_a_given_split_stays(cuda_lib):
