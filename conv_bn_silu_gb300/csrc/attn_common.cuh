@@ -239,8 +239,9 @@ __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, i
 // A row by itself over keys [k0, k1): what the kernels fall back to when a block
 // that some rows must not see in full holds a value that is not finite (0 x inf
 // would reach them; a bf16 cache), or when scores are too large for the fast
-// pass.  A warp; lane holds D / 32 dimensions.
-template <int D, bool I8>
+// pass.  A warp; lane holds D / 32 dimensions.  KEEP: its scores, which are summed up in
+// another order than the fast pass does, to L.scores.
+template <int D, bool I8, bool KEEP = false>
 __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b, int r, int k0, int k1, int lane,
                                       float (&acc)[D / 32], float &mm, float &ll) {
     constexpr int kE = D / 32;
@@ -270,6 +271,8 @@ __device__ __noinline__ void slow_row(const AttnLaunch &L, const Rows &s, int b,
 #pragma unroll
         for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(~0u, dot, x);
         dot = __fmul_rn(dot, I8 ? c.k_scale[row] * L.scale_log2 : L.scale_log2);   // rounded, as the maximum is
+        if (KEEP && lane == 0 && key < L.len_pad)
+            L.scores[(((size_t)b * c.kv_heads + s.head) * L.rows_pad + r) * L.len_pad + key] = dot;
         const float nm = fmaxf(mm, dot);
         const float use = nm == -INFINITY ? 0.0f : nm;
         const float fac = mm == -INFINITY ? 0.0f : frag::ex2(mm - use), pr = frag::ex2(dot - use);

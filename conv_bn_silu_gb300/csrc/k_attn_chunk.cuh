@@ -727,11 +727,24 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         float2 *const stats = reinterpret_cast<float2 *>(sgen + C::kQ + C::kJoinStats);
         if (words[2]) {
             constexpr int kE = D / 32;
+            float lx_row = 0.0f;
+            if constexpr (kExact) {
+                share[part * kRows + h * kHalf + hr] = lx;
+                ptx::bar_red_or(pair_bar, 64, false);
+                lx_row = lx + share[(part ^ 1) * kRows + h * kHalf + hr];
+            }
             for (int x = part; x < 32; x += 2) {
                 const int row = r - lane + x;
                 if (row >= rs.R) break;
                 float acc[kE], mm, ll;
                 slow_row<D, I8>(L, rs, b, row, key0, key0 + n * kTile, lane, acc, mm, ll);
+                // What the weights are divided by is of the scores that they are taken from:
+                // this pass's own but for far rows (k_attn_weights.cu).
+                float exact = ll;
+                if constexpr (kExact) {
+                    const float m_row = __shfl_sync(~0u, m, x), sum_row = __shfl_sync(~0u, lx_row, x);
+                    if (mm != -INFINITY && !is_far(m_row)) exact = sum_row * frag::ex2(m_row - mm);
+                }
                 if (!join) {
                     const Seen z = rs.seen(L, row);
                     const float inv = __fdiv_rn(1.0f, ll);
@@ -746,7 +759,7 @@ attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     if (lane == 0) {
                         stats[row - r0] = make_float2(mm, ll);
-                        if constexpr (kExact) reinterpret_cast<float *>(sgen + C::kQ + C::kJoinSums)[row - r0] = ll;
+                        if constexpr (kExact) reinterpret_cast<float *>(sgen + C::kQ + C::kJoinSums)[row - r0] = exact;
                     }
                 }
             }

@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, SECOND ? kSecond<D, I8, NR>.ctas : a
         constexpr int kE = D / 32;   // dimensions a lane
         for (int r = warp; r < kRows && r0 + r < R; r += kWarps) {
             float acc[kE], mm, ll;
-            slow_row<D, false>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
+            slow_row<D, false, kExact>(L, rs, b, r0 + r, lo16 + b0 * kBlock, lo16 + b1 * kBlock, lane, acc, mm, ll);
 #pragma unroll
             for (int e = 0; e < kE; ++e) *share(0, r, lane * kE + e) = acc[e];
             if (lane < kWarps) {

@@ -1,5 +1,5 @@
-"""Weighed attention at the edges of its contract: keys that are not finite,
-plans of a given split."""
+"""Weighed attention at the edges of its contract: keys and values that are not
+finite, rows far from zero, plans of a given split."""
 import math
 
 import pytest
@@ -81,6 +81,28 @@ def test_a_key_of_infinite_scale(heads, kv, kernel):
     assert got.isfinite().all() and (got[:, at] == 0).all() and out.isfinite().all()
     # (what a row gives adds up to one, within n + R + 64 roundings of 2^-23 and the exponentials' 2^-20)
     assert ((got.sum(1) / (130 * heads // kv) - 1).abs() <= (400 + 130 * heads + 64) * 2.0 ** -23 + 2.0 ** -20).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("split", [0, 1, 3])
+@pytest.mark.parametrize("size", [30.0, 1e18])
+def test_far_rows_beside_values_that_are_not_finite(size, split, kernel):
+    """As rows far from zero, with a NaN among the values of the last position: it sends
+    the rows of a tile that may not see it on a way of their own, whose scores are summed
+    up in another order.  A position still has a row's whole weight or none of it: what a row
+    gives is taken from the same scores as what it is divided by."""
+    lens, new, heads = [70, 130], [2, 2], 4
+    paged = refs.make_paged(lens, 2, 64, 16, False, 9, junk=False)
+    for b, n in enumerate(lens):
+        paged["v"][paged["table"][b, (n - 1) // 16], :, (n - 1) % 16, 7] = math.nan
+    q = torch.randn((4, heads, 64), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16) * size
+    _, got = weights(paged, q, lens, new, heads, 100.0, force_kernel=kernel, force_split=split)
+    for b, (rec, _) in enumerate(received(q, paged, [0, 2, 4], lens, 16, True, 0, 100.0)):
+        assert got[b].isfinite().all(), b
+        # whole numbers: no two of these keys' scores are within 2^-20 of one another
+        assert torch.equal(rec.round(), got[b].round()), b
+        assert (got[b] - got[b].round()).abs().max() <= 1e-3
 
 
 def test_a_given_split_stays(cuda_lib):
