@@ -512,7 +512,8 @@ cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c
     const struct { const void *p; size_t bytes; const char *what; } others[] = {
         {c->k, rows * row, "k"}, {c->v, rows * row, "v"}, {c->k_scale, rows * 4, "k_scale"}, {c->v_scale, rows * 4, "v_scale"},
         {q, (size_t)((s->total - 1) * q_stride + width) * 2, "q"}, {out, (size_t)((s->total - 1) * out_stride + width) * 2, "out"},
-        {workspace, p->workspace_bytes, "workspace"}};
+        {workspace, p->workspace_bytes, "workspace"}, {s->new_start, ((size_t)s->batch + 1) * 4, "new_start"},
+        {s->seq_lens, (size_t)s->batch * 4, "seq_lens"}, {s->page_table, (size_t)s->batch * s->max_pages * 4, "page_table"}};
     for (const auto &o : others)
         if (overlap(mass, rows * 4, o.p, o.bytes)) return fail(CBS_ERR_INVALID_ARG, "mass lies on %s", o.what);
     CBS_TRY(status_word(&L.c));

@@ -7,7 +7,7 @@ import torch
 
 from conv_bn_silu_gb300 import _binding as B
 from tests import token_refs as refs
-from tests.test_tokens_refusals import desc
+from tests.test_tokens_refusals import I, cache as c_cache, desc, refused, seqs
 from tests.test_tokens_weighed import received
 
 I32 = torch.int32
@@ -112,3 +112,12 @@ def test_a_given_split_stays(cuda_lib):
         assert (plan.attention.kernel, plan.attention.split) == (B.CBS_ATTN_ROWS, 20), kw
     plan = B.cbs_weighed_plan(desc(batch=1, max_len=8000, heads=8))
     assert (plan.attention.kernel, plan.attention.split) == (B.CBS_ATTN_CLUSTER, 8)
+
+
+def test_weights_on_what_the_call_reads(cuda_lib):
+    plan = B.cbs_weighed_plan(desc())
+    K = 1 << 30
+    c = c_cache(k=5 * K, v=6 * K, k_scale=7 * K, v_scale=8 * K)
+    s = seqs(new_start=9 * K, seq_lens=10 * K, page_table=11 * K)
+    for at in (9 * K, 10 * K, 11 * K, 9 * K - 16):   # new_start, seq_lens, page_table, and across one's start
+        refused(I, B.cbs_weighed_attention, plan, c, s, K, 256, 0.1, 2 * K, 256, at, 1.0, 4 * K, plan.workspace_bytes, None)
