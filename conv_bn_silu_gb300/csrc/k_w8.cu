@@ -48,7 +48,8 @@ struct W8Tile {
     // land out of order, so whoever takes stages in turn has to see every turn of its
     // slots: their number is a multiple of two (weights) and of kTurns.  A group's last
     // stage waited for an MMA kTurns + kOps stages back, and MMAs end in order: with no
-    // more groups than places of B, that place's turn before the last one has ended.
+    // more groups than places of B, that place's turn before the last one has ended.  So
+    // too the two groups of weights and the places of A.
     static_assert(kStages % 2 == 0 && kStages % kTurns == 0 && kTurns <= kOps, "turns");
     static constexpr int kStoreWarps = kWiden >= 8 ? 16 : 8;   // at the end: each has 32 outputs of its part of the rows
     static constexpr int kWarpMma = 8 + kWiden, kWarpTma = kWarpMma + 1, kThreads = (kWarpTma + 1) * 32;
@@ -56,6 +57,7 @@ struct W8Tile {
     // Places of A in tensor memory, a stage each: from a place's MMA back to its next one
     // takes some 2500 cycles of hand-offs, so as many as fit.
     static constexpr int kABufs = kN >= 128 ? 4 : 3, kACols = kStageK / 2;
+    static_assert(2 <= kABufs, "turns");
     static constexpr int kTmem = kABufs * kACols + kN <= 256 ? 256 : 512;
     // raw_full[], raw_empty[], b_ready[], b_free[], a_ready[], a_free[], done;
     // TMEM address, flag; the input rows' scales

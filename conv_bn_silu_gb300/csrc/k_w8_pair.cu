@@ -24,7 +24,7 @@ constexpr int kW = kOut * 128, kRaw = kW + kRows * 128;   // a stage's codes: we
 constexpr int kOp = kRows * 256;                          // a stage of B: two panels of 64
 constexpr int kStages = 4, kOps = 3, kABufs = 4, kACols = kStageK / 2;
 constexpr int kTurns = 2;   // groups of warps that take stages in turn, of weights and of inputs (as in k_w8.cu)
-static_assert(kStages % kTurns == 0 && kTurns <= kOps, "turns");
+static_assert(kStages % kTurns == 0 && kTurns <= kOps && kTurns <= kABufs, "turns");
 static_assert(kABufs * kACols + kTileRows == 512, "tensor memory");
 constexpr int kStoreWarps = 8, kWarpStore = 16, kWarpMma = kWarpStore + kStoreWarps, kWarpTma = kWarpMma + 1;
 constexpr int kThreads = (kWarpTma + 1) * 32;
