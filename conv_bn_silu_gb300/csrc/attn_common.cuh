@@ -27,7 +27,10 @@ enum AttnMode {
 // prefixes' part, the kernel before it, still runs.  All that it reads and writes but
 // the shares is older: it is launched once every CTA of the prefixes' part has let it,
 // which they do after their own wait for the kernels before.  The fence drops what this
-// SM's L1 held until then.
+// SM's L1 held until then.  (A kernel's own griddepcontrol.wait is all that the programming
+// model names as making older writes visible.  That the fence does it here rests on the
+// chip: those kernels have ended, so their writes are in L2, and loads after the fence come
+// from there.  With the wait at the start the two parts would not overlap.)
 constexpr bool runs_beside(int mode) { return mode == kAttnOwn || mode == kAttnBeside; }
 template <int MODE>
 __device__ __forceinline__ void begin_attention() {

@@ -16,7 +16,7 @@
 // one a score and sixteen a clock and SM, bound it from below: 1024 tokens over 16384
 // keys, 32 heads, 107 us of them; it takes 155, for a buffer of scores goes from hand to
 // hand in some 3000 cycles.  (32 streams of one token, 8192 keys, 8 bits: the first
-// kernel 15 us after an attention of 125.)
+// kernel 15 us after an attention of 98.)
 #include "attn_common.cuh"
 #include "tc_ptx.cuh"
 #include "tc_warp.cuh"

@@ -7,8 +7,8 @@
 // widen exactly to f16.  No shared memory, barrier or hand-off before the end, where
 // the warps' sums meet in order: whole numbers, exact below 2^24 in any order.
 //
-// Measured, one row: 6144 x 4096 6.6 us, 3.8 TB/s; 16384 x 8192 26.5 us, 5.1 TB/s; 60% of the
-// issue slots.
+// Measured, one row: 6144 x 4096 6.6 us, 3.8 TB/s; 8192 x 8192 14.6 us, 4.6 TB/s; 60% of the
+// issue slots.  (Of more than 96 MB of weights k_w8.cu takes over.)
 #include <cuda_bf16.h>
 
 #include "mma_frag.cuh"
@@ -116,7 +116,8 @@ cudaError_t launch_w8_few(const W8Launch &L, cudaStream_t s) {
     // What is in flight is about as much with two CTAs an SM, four steps ahead, as with
     // three or four, two ahead; so as many as take the grid in one round, or four.  Two,
     // three and four, one row: 4096 x 4096 (256 CTAs) 5.1, 5.9, 6.2 us; 6144 x 4096 (384)
-    // 8.4, 6.6, 8.2; 8192 x 8192 (512) 15.7, 19.1, 14.6; 16384 x 8192 (1024) 28.8, 30.0, 27.2.
+    // 8.4, 6.6, 8.2; 8192 x 8192 (512) 15.7, 19.1, 14.6; and, past what is sent here, 16384 x
+    // 8192 (1024) 28.8, 30.0, 27.2.
     const int sms = current_device_sms();
     if (grid <= 2 * sms) return launch_kernel(w8_few_kernel<1, 2, 4>, grid, kThreads, 0, s, L, wk);
     if (grid <= 3 * sms) return launch_kernel(w8_few_kernel<1, 3, 2>, grid, kThreads, 0, s, L, wk);

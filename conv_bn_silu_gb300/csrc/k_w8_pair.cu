@@ -7,8 +7,9 @@
 // next tile, whose first MMA waits only until warps of their own have read the last
 // one's sums; a CTA's start (tensor memory, barriers, the first loads) is paid once.
 //
-// Measured: 8192 rows of 8192 x 8192 549 us, 2.0 PFLOP/s; 1024 rows 82 us, 1.67; 2048 rows
-// of 4096 x 8192 with the tensor pipe 84% active and 55% of the issue slots (widening).
+// Measured: 8192 rows of 8192 x 8192 549 us, 2.0 PFLOP/s, and 611 us, 1.80, with the card warm
+// from the calls before; 1024 rows 82 us, 1.67; 2048 rows of 4096 x 8192 80 us, with the tensor
+// pipe 84% active and 55% of the issue slots (widening).
 #include <algorithm>
 
 #include "w8.cuh"

@@ -100,12 +100,12 @@ bool rows_overlap(const void *a, long long a_stride, const void *b, long long b_
 constexpr int kGridMax = 65535;
 
 // Most rows of a key head for the few-row kernel.  32 heads, 8 key heads of 128,
-// few-row (the better of its two ways to join ranges) / chunk kernel in us, for 8,
-// 16, 32, 64 rows: bf16 (tiles of 8 rows), one sequence of 4000 keys 11/13, 13/13,
-// 18/14, 24/14; 16 of 4000 53/56, 82/56, 134/56, 238/57; 64 of 1000 59/79, 78/80,
-// 127/82, 226/85.  8 bits (tiles of 16 from 16 rows on; the chunk kernel widens every
-// code first): 10/20, 12/20, 15/20, 18/20; 35/121, 47/121, 77/121, 133/121; 32/127,
-// 42/126, 66/127, 124/127.
+// few-row (the better of its two ways to join ranges) / chunk kernel in us on the GPU, for
+// 8, 16, 32, 64 rows: bf16 (tiles of 8 rows), one sequence of 4000 keys 9.1/14, 10/14,
+// 14/15, 16/15; 16 of 4000 47/58, 64/58, 94/58, 158/58; 64 of 1000 45/83, 60/84, 87/84,
+// 153/86 (so sixteen rows would be faster in two of three).  8 bits (tiles of 16 from 16
+// rows on; the chunk kernel widens every code first): 9.8/19, 11/19, 14/19, 17/20; 35/120,
+// 49/120, 77/120, 135/120; 33/126, 45/127, 69/127, 126/127.
 constexpr int kAttnRowsMost = 8, kAttnRowsMostInt8 = 32;
 
 // Of 152 SMs with one CTA each, that many clusters of x of the chunk kernel's CTAs run at once.
@@ -293,22 +293,24 @@ cbs_status attn_plan(const cbs_attn_desc *d, int few, cbs_attn_plan_t *out) {
         p.split = chunk_split(base, keys, sms);
     } else {
         // At least a CTA for each SM if that leaves a range 64 keys, and up to
-        // twelve if it leaves 640.  Tokens of 32 heads, 8 key heads, 1, 2, 4, ... 32
-        // ranges: one sequence of 1000 keys 16, 12, 8.1, 6.8, 6.8, 9.8 us; one of 8192
-        // 112, 59, 32, 19, 13, 14; 8 of 8192 140, 76, 55, 63, 57, 61 (12 ranges 52); 32
-        // of 1024 29, 37, 34, 37, 51, 88.  8 bits: one of 1000 15, 11, 7.8, 6.8, 7.1, 10;
-        // one of 8192 99, 54, 29, 18, 12, 15; 32 of 8192 194, 178, 146, 137, 150, 180.
+        // twelve if it leaves 640.  Tokens of 32 heads, 8 key heads of 128, 1, 2, 4, 8, 12, 16
+        // and 32 ranges joined through the workspace, us on the GPU: one sequence of 1000 keys
+        // 12, 9.6, 6.9, 6.5, 7.7, 7.1, 10; one of 8192 79, 44, 24, 15, 12, 11, 14; 8 of 8192 89,
+        // 52, 45, 49, 50, 54, 59; 32 of 1024 24, 30, 31, 35, 43, 50, 86.  8 bits: one of 1000 14,
+        // 11, 7.7, 7.1, 8.2, 8.0, 12; one of 8192 92, 50, 27, 17, 14, 13, 14; 32 of 8192 135, 116,
+        // 103, 107, 111, 115, 136.
         const long long few = std::min((sms + base - 1) / base, ((long long)keys + 63) / 64);
         const long long many = std::min((sms * 12ll + base - 1) / base, (long long)keys / 640);
         p.split = (int)std::max(1ll, std::max(few, many));
         // Up to eight ranges join in a cluster where it does not keep CTAs waiting (three
-        // an SM; more are made eight if that leaves a range 512 keys at most, and five to
-        // seven four).  Through the workspace / in a cluster: one token over 1000 keys, 8
-        // ranges 6.8/5.7 us (16 ranges 6.8 through the workspace), over 4000 12.0/10.9 (19
-        // ranges 10.1), two tokens over 1000 8.1/5.9; four sequences of 1000, 4 ranges
-        // 8.3/7.3, 5 ranges 9.2/8.5; 16 of 1000, 2 ranges 16.8/15.5; 8 of 8000, 8 ranges
-        // 62/60; 32 of 8000, 8 ranges 168/187.  8 bits: 6.9/5.7 (7.1), 11.4/10.2 (10.0),
-        // 8.3/5.9; 8.0/7.0, 9.2/8.6; 16.5/15.2; 52/53; 135/159.
+        // an SM, which calls of one token take in one round by one form of the kernel or the
+        // other; more are made eight if that leaves a range 512 keys at most, and five to seven
+        // four).  Through the workspace / in a cluster: one token over 1000 keys, 8 ranges
+        // 6.4/5.1 us (16 ranges 7.1 through the workspace), over 4000 10.0/8.9 (19 ranges 9.5),
+        // two tokens over 1000 8.0/5.2; four sequences of 1000, 4 ranges 7.0/6.1, 5 ranges
+        // 8.2/7.0; 16 of 1000, 2 ranges 11.6/10.2; 8 of 8000, 8 ranges 48/47; 32 of 8000, 8 ranges
+        // 162/183.  8 bits: 7.0/5.3 (8.1), 11.3/9.5 (9.8), 8.6/5.5; 7.6/6.5, 8.7/8.0; 13.0/11.5;
+        // 36/34; 105/107.
         const int most = std::min(p.split, kAttnClusterMost), x = most > 4 && most < 8 ? 4 : most;
         const bool fits = p.split <= kAttnClusterMost || keys <= 512 * kAttnClusterMost;
         if (d->force_kernel == CBS_ATTN_CLUSTER || (d->force_kernel < 0 && fits && base * x <= 3ll * sms)) {
@@ -343,9 +345,9 @@ long long attn_ns(const cbs_attn_plan_t &p, int sms) {
 // The faster kernel for a part of a call whose rows are more than the few-row
 // kernels' own: short sequences do not repay a chunk's start.  (`more`: what follows
 // the few-row kernel less what follows the chunk kernel.)  Head dimension 64, bf16, few
-// rows and chunks: 64 rows of 400 keys, two heads 5.2 and 9.2 us, 64 heads 11.4 and 9.5;
-// 8 bits, 64 rows of 200 keys, 512 heads 23 and 42, of 1000 62 and 81, and 128 rows 113
-// and 82.
+// rows and chunks: 64 rows of 400 keys, two heads 4.3 and 9.2 us, 64 heads 8.0 and 9.4;
+// 8 bits, 512 heads, 64 rows of 200 keys 25 and 43, of 1000 76 and 93, and 128 rows of 1000
+// 141 and 95.
 cbs_status attn_plan_by_time(const cbs_attn_desc *d, long long (*more)(const cbs_attn_plan_t &few, const cbs_attn_plan_t &chunk, int sms),
                              cbs_attn_plan_t *out) {
     CBS_TRY(attn_plan(d, -1, out));
@@ -353,7 +355,7 @@ cbs_status attn_plan_by_time(const cbs_attn_desc *d, long long (*more)(const cbs
     const int sms = d->num_sms > 0 ? d->num_sms : kDefaultNumSMs;
     // Of more than eight rows the many ranges that a few-row kernel joins through the
     // workspace take longer than eight in a cluster: 16 rows of 6000 keys, two heads of
-    // 128 in 8 bits 47 and 14 us, in bf16 21 and 15.
+    // 128 in 8 bits 56 and 14 us, in bf16 19 and 11.  (Given ranges stay as they are.)
     const auto in_clusters = [&](cbs_attn_plan_t *p) {
         const long long base = (long long)std::max(d->batch, 1) * d->kv_heads * p->row_tiles;
         if (d->force_split || p->kernel != CBS_ATTN_ROWS || p->split <= kAttnClusterMost || (long long)d->max_new * (d->heads / d->kv_heads) <= 8 ||
@@ -528,9 +530,10 @@ cbs_status cbs_weighed_attention(const cbs_weighed_plan_t *p, const cbs_cache *c
     L.mass = mass;
     L.decay = decay;
     // Few rows in one tile: the CTAs of a cluster weigh their own keys, and so does one
-    // CTA without ranges (one token over 1000 keys 10.8 -> 8.6 us; 64 sequences of 300
-    // 26.7 -> 23.4).  Of ranges joined by the CTA that finishes last, that one would weigh
-    // all of them (32 sequences of up to 8192: 136 -> 159).
+    // CTA without ranges (on the GPU, by the kernel after them / by themselves: one token over
+    // 1000 keys 9.3/7.8 us; 64 sequences of 300 17.8/16.6).  Of ranges joined by the CTA that
+    // finishes last, that one would weigh all of them (32 sequences of up to 8192, 8 bits:
+    // 107/121).
     L.fused = L.scores && a.row_tiles == 1 && (L.cluster || a.split == 1);
     CBS_TRY(launch_attn_weighed(L, a.row_tile, (cudaStream_t)stream));
     return L.fused ? CBS_OK : launch_attn_weights(L, (cudaStream_t)stream);

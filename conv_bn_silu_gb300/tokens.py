@@ -224,7 +224,7 @@ class PagedCache:
               recent: int = 0):
         """The last `recent` positions of each sequence and the heaviest others,
         `keep` in all, in order to the pages of new_table (int32 [batch, pages],
-        none of them the sequences' own); each key head chooses by itself.  mass:
+        none of them the sequences' own, none twice: not checked); each key head chooses by itself.  mass:
         float32 [num_pages, kv_heads, page_size] (WeighedAttention adds it up), which
         moves along.  Returns the old positions (int32 [batch, kv_heads, keep], -1
         past them) and the new lengths."""

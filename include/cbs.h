@@ -511,8 +511,9 @@ CBS_API cbs_status cbs_cache_read(const cbs_cache *c, const cbs_sequences *s, in
  * order, to positions 0, 1, ... of new pages: keys, values, scales and weights.
  *   mass: float [num_pages][kv_heads][page_size];
  *   new_table: [batch][new_max_pages], pages that none of the call's sequences
- *     holds (the old ones are left as they are, and free after the call unless
- *     others share them); 0 <= recent <= keep, and the pages hold
+ *     holds and that stand there once (which is not checked: what two positions are
+ *     copied to, or one from after that, holds either).  The old ones are left as they
+ *     are, and free after the call unless others share them; 0 <= recent <= keep, and the pages hold
  *     min(keep, max_pages * page_size) positions (more is refused);
  *   kept: [batch][kv_heads][keep], the old position of each new one, -1 past them;
  *   new_lens: [batch], min(keep, length).  kept and new_lens are outputs (16-byte
@@ -539,7 +540,7 @@ typedef struct cbs_attn_desc {
 } cbs_attn_desc;
 
 typedef enum cbs_attn_kernel {
-    CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 (token, head) rows, or 16 over 8 bits, keys straight to registers */
+    CBS_ATTN_ROWS = 0,  /* few query rows: tiles of 8 (token, head) rows, or 16 over 8 bits, on mma.sync */
     CBS_ATTN_CHUNK = 1, /* many: tiles of 256 rows on tcgen05, scores and output in tensor memory */
     CBS_ATTN_CLUSTER = 2 /* as CBS_ATTN_ROWS, with up to 8 ranges of keys joined in a cluster and no workspace */
 } cbs_attn_kernel;
@@ -569,6 +570,10 @@ CBS_API cbs_status cbs_attn_plan(const cbs_attn_desc *d, cbs_attn_plan_t *out);
  * it, whatever they hold (a NaN or infinity included).
  * CBS_INT8: a score is the sum of q times the codes, times the key's scale; that
  * sum has to stay in float's range too (|q| below 2^112 does).
+ * Scores, maxima and sums are in 32 bits.  The probabilities are rounded to bfloat16
+ * (over CBS_INT8 with the values' scales in them) for their product with the values,
+ * which moves an output by up to 2^-8 of sum_j p_j |v_j| / sum_j p_j beside its own
+ * rounding; so too where prefixes are shared and positions weighed.
  * q, out: bfloat16 [total][heads][head_dim] with q_stride, out_stride elements
  * between tokens (multiples of 8).  scale: finite.  workspace (plan's
  * workspace_bytes, which may be 0): zeroed once with cbs_workspace_init; not
@@ -590,7 +595,8 @@ CBS_API cbs_status cbs_paged_attention(const cbs_attn_plan_t *p, const cbs_cache
  * sequences' pages are left as they are.
  *   mass: float [num_pages][kv_heads][page_size].  No page may belong to two of
  *     the call's sequences (they would overwrite each other's weights).
- *   decay: finite.  out: as cbs_paged_attention's.
+ *   decay: finite.  out: as cbs_paged_attention's.  (The weights are of the
+ *     probabilities in 32 bits.)
  * A sequence longer than the plan's max_len is reported, and its positions past
  * that (rounded up to 16) get no weight.  total is at most batch * max_new.  Sums
  * are in 32 bits; equal calls give equal results.  workspace: workspace_bytes, of
