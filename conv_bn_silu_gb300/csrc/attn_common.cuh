@@ -239,6 +239,40 @@ __device__ __forceinline__ void store_out4(const AttnLaunch &L, const Rows &s, i
     *reinterpret_cast<uint2 *>(s.out(L, r, D) + dim) = w;
 }
 
+// Pairs of floats in one register pair (two lanes of one instruction).
+struct F2 { unsigned long long v; };
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+
+// Beyond 2^22 a float's last place is more than a quarter: a score's product with
+// the scale, which the chunk kernels' passes do not round, may then lie far from the
+// reference, which is rounded (from 2^31 on by 2^128 and more).  Such rows, seldom met,
+// go the slow path.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
+
 // A row by itself over keys [k0, k1): what the kernels fall back to when a block
 // that some rows must not see in full holds a value that is not finite (0 x inf
 // would reach them; a bf16 cache), or when scores are too large for the fast

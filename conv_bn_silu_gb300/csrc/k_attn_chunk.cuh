@@ -103,34 +103,6 @@ __device__ __forceinline__ Span span_of(const AttnLaunch &L, const Rows &s, int 
     return Span{a.lo, b.hi, b.lo, a.hi};
 }
 
-// Pairs of floats in one register pair (two lanes of one instruction).
-struct F2 { unsigned long long v; };
-__device__ __forceinline__ F2 pair(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-
 // A thread's pass over its kCols of a row's scores: t = s * scale - ref (ks: a scale a key,
 // for 8-bit keys), p = 2^t (times vs, for 8-bit values) as bf16 pairs, the
 // largest t and, in 8 bits, the sum of 2^t (p has the value's scale in it; in
@@ -215,12 +187,6 @@ __device__ __forceinline__ float tile_top(uint32_t taddr, float scale, const flo
     }
     return fmaxf(tops[0], tops[1]);
 }
-
-// Beyond 2^22 a float's last place is more than a quarter: a score's product with
-// the scale, which tile_pass does not round, may then lie far from the reference,
-// which is rounded (from 2^31 on by 2^128 and more).  Such rows, seldom met, go
-// the slow path.
-__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
 
 template <int D, bool I8, int MODE>
 __global__ void __launch_bounds__(Chunk<D, I8>::kThreads, 1)

@@ -117,8 +117,6 @@ __device__ __noinline__ bool odd_key(const unsigned char *keys, int row) {
     return odd;
 }
 
-__device__ __forceinline__ bool far_row(float m) { return fabsf(m) > 4194304.0f && fabsf(m) < INFINITY; }
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
@@ -129,23 +127,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint
 // A thread's sum over a tile's rows: scores, as they come from tensor memory, to
 // exponentials times what belongs to each row.  Two lanes of an instruction at a time,
 // and the next sixteen scores on their way.
-struct F2 { unsigned long long v; };
-__device__ __forceinline__ F2 pair(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // MASK: rows that do not see `key` are left out.
 template <bool MASK>
 __device__ __forceinline__ void tile_sum(uint32_t taddr, const float *stat, float scale, int key, F2 (&sums)[2]) {
@@ -351,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __g
             next = statistics(row_next);
             const bool ok = wait(s_free(s), (i / kBufs + 1) & 1) && !lost();
             // A far row: by itself, from its own loads; here every exponential of it is zero.
-            const bool far = far_row(st.x), any_far = ptx::bar_red_or(1, kStatWarps * 32, far);
+            const bool far = is_far(st.x), any_far = ptx::bar_red_or(1, kStatWarps * 32, far);
             if (ptx::bar_red_or(1, kStatWarps * 32, !ok)) break;   // (together, whatever ran out)
             float *const stat = reinterpret_cast<float *>(smem + C::kStats + s * C::kStat);
             const Seen z = r >= 0 ? rs.seen(L, r) : Seen{0, 0};
@@ -396,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_of_chunk_kernel(const __g
                 for (int x = 0; x < t.tokens * rt.heads; ++x) {
                     const int r = (t.token + x / rt.heads) * L.group + t.head + x % rt.heads;
                     const float2 st = __ldg(&L.row_stats[rs.number(L, r)]);
-                    if (!far_row(st.x)) continue;
+                    if (!is_far(st.x)) continue;
                     const Seen z = rs.seen(L, r);
                     for (int y = 0; y < 32; ++y) {
                         const int k = __shfl_sync(~0u, key, y), kp = __shfl_sync(~0u, p, y);
