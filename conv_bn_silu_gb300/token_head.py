@@ -252,6 +252,8 @@ class AnswerHead:
         answers], what it is asked), int64 [images, answers, tokens]."""
         if tokens < 1 or tokens > self.max_answer:
             raise ValueError(f"{tokens} tokens: at most {self.max_answer}")
+        if first.numel() != self.images * self.answers:
+            raise ValueError(f"{first.numel()} first tokens for {self.images} images of {self.answers} answers")
         self.start(cells)
         if self.graph is None:
             self._advance()   # (everything a launch needs is set up before a capture)
